@@ -18,6 +18,7 @@ from . import build_lib
 MOE_ROUTE_SORT_NOALLOC_SCRATCH_BYTES = 512 * 1024
 MOE_F32, MOE_BF16 = 0, 1
 MOE_ACT_ROW_MAJOR, MOE_ACT_K8_INTERLEAVED, MOE_ACT_K8_TOKEN_ORDER = 0, 1, 2
+MOE_FP4_MX, MOE_FP4_NV = 0, 1
 
 SYMBOLS = (
     "moe_status_string", "moe_workspace_bytes", "moe_clear_status", "moe_read_status",
@@ -26,7 +27,9 @@ SYMBOLS = (
     "moe_route_sort_noalloc", "moe_nvfp4_cast_workspace_bytes", "moe_mxfp4_to_nvfp4",
     "moe_nvfp4_grouped_gemm", "moe_mxfp4_grouped_gemm_swiglu", "moe_mxfp4_grouped_gemm_block",
     "moe_mxfp4_grouped_gemm_swiglu_gather", "moe_mxfp4_grouped_gemm_scatter", "moe_combine_slots",
-    "moe_act_interleave_k8", "moe_set_gemm_pairing",
+    "moe_act_interleave_k8", "moe_set_gemm_pairing", "moe_topk_gate", "moe_topk_gate_backward",
+    "moe_fp4_quantize", "moe_fp4_grouped_gemm", "moe_fp4_grouped_gemm_swiglu",
+    "moe_layer_forward_fp4", "moe_combine_backward", "moe_gather_backward",
 )
 
 _lock = threading.Lock()
@@ -85,6 +88,19 @@ def load(path: str | None = None):
                 "moe_mxfp4_to_nvfp4": ([P, I32, I32, I32, P, P, P, P, SZ, P], C.c_int),
                 "moe_nvfp4_grouped_gemm": ([P, C.c_int, I64, I32, P, P, P, P, I32, I32, P, C.c_int,
                                             P, SZ, P], C.c_int),
+                "moe_topk_gate": ([P, C.c_int, I64, I32, I32, I32, I32, P, P, P], C.c_int),
+                "moe_topk_gate_backward": ([P, C.c_int, I64, I32, I32, I32, I32, P, P, P, P], C.c_int),
+                "moe_fp4_quantize": ([P, C.c_int, I64, I64, I32, P, I32, I64, C.c_int, P, P, P, P,
+                                      C.c_int, P, SZ, P], C.c_int),
+                "moe_fp4_grouped_gemm": ([P, P, P, I64, I32, P, P, P, C.c_int, P, I32, I32, P, C.c_int,
+                                          P, SZ, P], C.c_int),
+                "moe_fp4_grouped_gemm_swiglu": ([P, P, P, I64, I32, P, P, P, C.c_int, P, I32, I32, P, P,
+                                                 P, P, SZ, P], C.c_int),
+                "moe_layer_forward_fp4": ([P, P, P, I32, I32, I32, I32, I32, C.c_int] + [P] * 18 +
+                                          [P, SZ, P], C.c_int),
+                "moe_combine_backward": ([P, C.c_int, P, C.c_int, P, P, I32, I32, I32, P, C.c_int, P, P],
+                                         C.c_int),
+                "moe_gather_backward": ([P, C.c_int, P, I32, I32, I32, P, C.c_int, P], C.c_int),
             }
             for name, (args, res) in sig.items():
                 f = getattr(lib, name)
@@ -443,6 +459,276 @@ def mxfp4_to_nvfp4(scales: torch.Tensor, out=None, workspace: torch.Tensor | Non
                                    _ptr(workspace), workspace.numel(), _stream(stream))
     _check(rc, "moe_mxfp4_to_nvfp4")
     return out
+
+
+# ------------------------------------------- router gate, 4-bit path, gradients
+
+def _need(name: str, t: torch.Tensor, shape, *dtypes):
+    """The library takes raw pointers: a tensor it would misread is refused here."""
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: not contiguous")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: not a CUDA tensor")
+
+
+def _rows_of(name: str, t: torch.Tensor) -> int:
+    """Row stride, in elements, of a 2-D tensor whose rows are contiguous."""
+    if t.dim() != 2 or t.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"{name}: a 2-D float32 or bfloat16 tensor is needed")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: not a CUDA tensor")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: rows are not contiguous")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def topk_gate(logits: torch.Tensor, k: int, renorm: bool = False, out=None, stream=None):
+    """Router gate: logits [T, E] (f32 or bf16, any row stride) -> (ids int32 [T, k],
+    weights f32 [T, k]): the k largest, ties to the lower expert, and softmax over all
+    E (renorm: over the chosen k) at them."""
+    stride = _rows_of("logits", logits)
+    T, E = logits.shape
+    if out is None:
+        out = (torch.empty((T, k), dtype=torch.int32, device=logits.device),
+               torch.empty((T, k), dtype=torch.float32, device=logits.device))
+    ids, w = out
+    _need("ids", ids, (T, k), torch.int32)
+    _need("weights", w, (T, k), torch.float32)
+    rc = load().moe_topk_gate(_ptr(logits), _dtype_code(logits.dtype), stride, T, E, int(k),
+                              int(bool(renorm)), _ptr(ids), _ptr(w), _stream(stream))
+    _check(rc, "moe_topk_gate")
+    return out
+
+
+def topk_gate_backward(logits: torch.Tensor, ids: torch.Tensor, dw: torch.Tensor, renorm: bool = False,
+                       out: torch.Tensor | None = None, stream=None):
+    """Gradient of topk_gate's weights: dw f32 [T, k] -> dlogits [T, E] of the logits' type."""
+    stride = _rows_of("logits", logits)
+    T, E = logits.shape
+    k = ids.shape[1] if ids.dim() == 2 else 0
+    _need("ids", ids, (T, k), torch.int32)
+    _need("dw", dw, (T, k), torch.float32)
+    if out is None:
+        out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    _need("dlogits", out, (T, E), logits.dtype)
+    rc = load().moe_topk_gate_backward(_ptr(logits), _dtype_code(logits.dtype), stride, T, E, k,
+                                       int(bool(renorm)), _ptr(ids), _ptr(dw), _ptr(out), _stream(stream))
+    _check(rc, "moe_topk_gate_backward")
+    return out
+
+
+def _fp4_block(fmt: int) -> int:
+    if fmt not in (MOE_FP4_MX, MOE_FP4_NV):
+        raise ValueError(f"unknown 4-bit format {fmt}")
+    return 32 if fmt == MOE_FP4_MX else 16
+
+
+def _tensor_scale(name: str, t, n: int, fmt: int):
+    if fmt == MOE_FP4_NV:
+        if t is None:
+            raise ValueError(f"{name} is needed for NVFP4")
+        _need(name, t, (n,), torch.float32)
+        return _ptr(t)
+    return None
+
+
+def fp4_quantize(x: torch.Tensor, fmt: int, row_index: torch.Tensor | None = None, index_div: int = 1,
+                 tensor_scale: torch.Tensor | None = None, out=None, values: torch.Tensor | None = None,
+                 workspace: torch.Tensor | None = None, stream=None):
+    """x [x_rows, K] (f32 or bf16, any row stride) -> (codes uint8 [rows, K/2], scales uint8
+    [rows, K/32 or K/16]).  With row_index int32 [rows] row r holds x[row_index[r] // index_div].
+    tensor_scale f32 [1] (NVFP4).  values (f32 or bf16 [rows, K]) receives what the codes
+    stand for."""
+    stride = _rows_of("x", x)
+    block = _fp4_block(fmt)
+    x_rows, K = x.shape
+    rows = x_rows if row_index is None else row_index.numel()
+    if row_index is not None:
+        _need("row_index", row_index, (rows,), torch.int32)
+    if out is None:
+        out = (torch.empty((rows, K // 2), dtype=torch.uint8, device=x.device),
+               torch.empty((rows, K // block), dtype=torch.uint8, device=x.device))
+    codes, scales = out
+    _need("codes", codes, (rows, K // 2), torch.uint8)
+    _need("scales", scales, (rows, K // block), torch.uint8)
+    vdt = MOE_F32
+    if values is not None:
+        _need("values", values, (rows, K), torch.float32, torch.bfloat16)
+        vdt = _dtype_code(values.dtype)
+    if workspace is None:
+        workspace = make_workspace(0, 1, 1, x.device, stream)
+    rc = load().moe_fp4_quantize(_ptr(x), _dtype_code(x.dtype), x_rows, stride, K, _ptr(row_index),
+                                 int(index_div), rows, fmt,
+                                 _tensor_scale("tensor_scale", tensor_scale, 1, fmt), _ptr(codes),
+                                 _ptr(scales), _ptr(values), vdt, _ptr(workspace), workspace.numel(),
+                                 _stream(stream))
+    _check(rc, "moe_fp4_quantize")
+    return out
+
+
+def _fp4_operands(act_codes, act_scales, codes, scales, group_sizes, fmt):
+    block = _fp4_block(fmt)
+    rows, half = act_codes.shape
+    E, N, _ = codes.shape
+    K = 2 * half
+    _need("act_codes", act_codes, (rows, half), torch.uint8)
+    _need("act_scales", act_scales, (rows, K // block), torch.uint8)
+    _need("codes", codes, (E, N, half), torch.uint8)
+    _need("scales", scales, (E, N, K // block), torch.uint8)
+    _need("group_sizes", group_sizes, (E,), torch.int32)
+    return rows, K, E, N, block
+
+
+def fp4_grouped_gemm(act_codes: torch.Tensor, act_scales: torch.Tensor, codes: torch.Tensor,
+                     scales: torch.Tensor, group_sizes: torch.Tensor, fmt: int,
+                     act_scale_2: torch.Tensor | None = None,
+                     weight_scale_2: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                     out_dtype=torch.float32, workspace: torch.Tensor | None = None, stream=None):
+    """4-bit activations (fp4_quantize) by 4-bit weights uint8 [E, N, K/2] with scales
+    [E, N, K/32 or K/16] over row bands group_sizes int32 [E] -> out [rows, N] (f32 or bf16).
+    NVFP4: act_scale_2 f32 [1] and weight_scale_2 f32 [E]."""
+    rows, K, E, N, _ = _fp4_operands(act_codes, act_scales, codes, scales, group_sizes, fmt)
+    if out is None:
+        out = torch.empty((rows, N), dtype=out_dtype, device=act_codes.device)
+    _need("out", out, (rows, N), torch.float32, torch.bfloat16)
+    if workspace is None:
+        workspace = make_workspace(0, 1, 1, act_codes.device, stream)
+    rc = load().moe_fp4_grouped_gemm(_ptr(act_codes), _ptr(act_scales),
+                                     _tensor_scale("act_scale_2", act_scale_2, 1, fmt), rows, K,
+                                     _ptr(codes), _ptr(scales),
+                                     _tensor_scale("weight_scale_2", weight_scale_2, E, fmt), fmt,
+                                     _ptr(group_sizes), E, N, _ptr(out), _dtype_code(out.dtype),
+                                     _ptr(workspace), workspace.numel(), _stream(stream))
+    _check(rc, "moe_fp4_grouped_gemm")
+    return out
+
+
+def fp4_grouped_gemm_swiglu(act_codes: torch.Tensor, act_scales: torch.Tensor, codes: torch.Tensor,
+                            scales: torch.Tensor, group_sizes: torch.Tensor, fmt: int,
+                            act_scale_2: torch.Tensor | None = None,
+                            weight_scale_2: torch.Tensor | None = None,
+                            h_scale_2: torch.Tensor | None = None, out=None,
+                            workspace: torch.Tensor | None = None, stream=None):
+    """The w13 product (codes [E, 2I, K/2], gate rows first) with SwiGLU and the
+    quantisation of h in its epilogue -> (h_codes uint8 [rows, I/2], h_scales uint8
+    [rows, I/32 or I/16])."""
+    rows, K, E, N, block = _fp4_operands(act_codes, act_scales, codes, scales, group_sizes, fmt)
+    if N % 2:
+        raise ValueError("codes: an odd number of gate and up rows")
+    I = N // 2
+    if out is None:
+        out = (torch.empty((rows, I // 2), dtype=torch.uint8, device=act_codes.device),
+               torch.empty((rows, I // block), dtype=torch.uint8, device=act_codes.device))
+    h_codes, h_scales = out
+    _need("h_codes", h_codes, (rows, I // 2), torch.uint8)
+    _need("h_scales", h_scales, (rows, I // block), torch.uint8)
+    if workspace is None:
+        workspace = make_workspace(0, 1, 1, act_codes.device, stream)
+    rc = load().moe_fp4_grouped_gemm_swiglu(
+        _ptr(act_codes), _ptr(act_scales), _tensor_scale("act_scale_2", act_scale_2, 1, fmt), rows, K,
+        _ptr(codes), _ptr(scales), _tensor_scale("weight_scale_2", weight_scale_2, E, fmt), fmt,
+        _ptr(group_sizes), E, I, _tensor_scale("h_scale_2", h_scale_2, 1, fmt), _ptr(h_codes),
+        _ptr(h_scales), _ptr(workspace), workspace.numel(), _stream(stream))
+    _check(rc, "moe_fp4_grouped_gemm_swiglu")
+    return out
+
+
+def combine_backward(dout: torch.Tensor, y: torch.Tensor, slot_to_row: torch.Tensor,
+                     topk_w: torch.Tensor, out=None, dy_dtype=None, stream=None):
+    """Gradient of combine: dout [T, N], y [T*k, N] (f32 or bf16 each) -> (dy [T*k, N] of
+    dy_dtype (default: dout's), dw f32 [T, k])."""
+    T, k = topk_w.shape
+    N = dout.shape[-1]
+    _need("dout", dout, (T, N), torch.float32, torch.bfloat16)
+    _need("y", y, (T * k, N), torch.float32, torch.bfloat16)
+    _need("slot_to_row", slot_to_row, (T * k,), torch.int32)
+    _need("topk_w", topk_w, (T, k), torch.float32)
+    if out is None:
+        out = (torch.empty((T * k, N), dtype=dy_dtype or dout.dtype, device=dout.device),
+               torch.empty((T, k), dtype=torch.float32, device=dout.device))
+    dy, dw = out
+    _need("dy", dy, (T * k, N), torch.float32, torch.bfloat16)
+    _need("dw", dw, (T, k), torch.float32)
+    rc = load().moe_combine_backward(_ptr(dout), _dtype_code(dout.dtype), _ptr(y), _dtype_code(y.dtype),
+                                     _ptr(slot_to_row), _ptr(topk_w), T, k, N, _ptr(dy),
+                                     _dtype_code(dy.dtype), _ptr(dw), _stream(stream))
+    _check(rc, "moe_combine_backward")
+    return out
+
+
+def gather_backward(dx_sorted: torch.Tensor, slot_to_row: torch.Tensor, k: int,
+                    out: torch.Tensor | None = None, stream=None):
+    """Gradient of route_sort's gather: dx_sorted [T*k, hidden] (f32 or bf16) -> dx [T, hidden]."""
+    rows, hidden = dx_sorted.shape
+    if k < 1 or rows % k:
+        raise ValueError("dx_sorted: rows are not a multiple of k")
+    T = rows // k
+    _need("dx_sorted", dx_sorted, (rows, hidden), torch.float32, torch.bfloat16)
+    _need("slot_to_row", slot_to_row, (rows,), torch.int32)
+    if out is None:
+        out = torch.empty((T, hidden), dtype=dx_sorted.dtype, device=dx_sorted.device)
+    _need("dx", out, (T, hidden), torch.float32, torch.bfloat16)
+    rc = load().moe_gather_backward(_ptr(dx_sorted), _dtype_code(dx_sorted.dtype), _ptr(slot_to_row), T,
+                                    int(k), hidden, _ptr(out), _dtype_code(out.dtype), _stream(stream))
+    _check(rc, "moe_gather_backward")
+    return out
+
+
+class LayerBuffersFp4:
+    """Caller-owned intermediates of one 4-bit layer pass (allocated once, reused)."""
+
+    def __init__(self, T: int, k: int, E: int, hidden: int, inter: int, fmt: int, device="cuda"):
+        rows, block = T * k, _fp4_block(fmt)
+        i32 = dict(dtype=torch.int32, device=device)
+        u8 = dict(dtype=torch.uint8, device=device)
+        self.fmt = fmt
+        self.group_sizes = torch.empty(E, **i32)
+        self.group_offsets = torch.empty(E + 1, **i32)
+        self.sorted_slot = torch.empty(rows, **i32)
+        self.slot_to_row = torch.empty(rows, **i32)
+        self.x_codes = torch.empty((rows, hidden // 2), **u8)
+        self.x_scales = torch.empty((rows, hidden // block), **u8)
+        self.h_codes = torch.empty((rows, inter // 2), **u8)
+        self.h_scales = torch.empty((rows, inter // block), **u8)
+        self.y2 = torch.empty((rows, hidden), dtype=torch.float32, device=device)
+        self.out = torch.empty((T, hidden), dtype=torch.float32, device=device)
+        self.workspace = make_workspace(T, k, E, device)
+
+
+def layer_forward_fp4(x, topk_ids, topk_w, w13, w2, buffers: LayerBuffersFp4, x_scale_2=None,
+                      h_scale_2=None, stream=None):
+    """The routed-expert layer with 4-bit activations and weights.  w13 and w2 are (codes,
+    scales, weight_scale_2 or None); x bf16 [T, hidden]; -> buffers.out f32 [T, hidden]."""
+    b, fmt = buffers, buffers.fmt
+    block = _fp4_block(fmt)
+    (c13, s13, g13), (c2, s2, g2) = w13, w2
+    T, k = topk_ids.shape
+    E, two_i, half = c13.shape
+    hidden, inter = 2 * half, two_i // 2
+    _need("x", x, (T, hidden), torch.bfloat16)
+    _need("topk_ids", topk_ids, (T, k), torch.int32)
+    _need("topk_w", topk_w, (T, k), torch.float32)
+    _need("w13 codes", c13, (E, 2 * inter, hidden // 2), torch.uint8)
+    _need("w13 scales", s13, (E, 2 * inter, hidden // block), torch.uint8)
+    _need("w2 codes", c2, (E, hidden, inter // 2), torch.uint8)
+    _need("w2 scales", s2, (E, hidden, inter // block), torch.uint8)
+    _need("buffers.x_codes", b.x_codes, (T * k, hidden // 2), torch.uint8)
+    _need("buffers.h_codes", b.h_codes, (T * k, inter // 2), torch.uint8)
+    _need("buffers.group_sizes", b.group_sizes, (E,), torch.int32)
+    rc = load().moe_layer_forward_fp4(
+        _ptr(x), _ptr(topk_ids), _ptr(topk_w), T, k, E, hidden, inter, fmt, _ptr(c13), _ptr(s13),
+        _tensor_scale("w13 weight_scale_2", g13, E, fmt), _ptr(c2), _ptr(s2),
+        _tensor_scale("w2 weight_scale_2", g2, E, fmt), _tensor_scale("x_scale_2", x_scale_2, 1, fmt),
+        _tensor_scale("h_scale_2", h_scale_2, 1, fmt), _ptr(b.out), _ptr(b.group_sizes),
+        _ptr(b.group_offsets), _ptr(b.sorted_slot), _ptr(b.slot_to_row), _ptr(b.x_codes),
+        _ptr(b.x_scales), _ptr(b.h_codes), _ptr(b.h_scales), _ptr(b.y2), _ptr(b.workspace),
+        b.workspace.numel(), _stream(stream))
+    _check(rc, "moe_layer_forward_fp4")
+    return b.out
 
 
 def debug_bounded_wait(limit_ns: int, workspace: torch.Tensor, stream=None):

@@ -82,6 +82,54 @@ moe_status check_route_args(const int32_t *ids, int32_t T, int32_t k, int32_t E,
     return MOE_OK;
 }
 
+bool known_dtype(int d) { return d == MOE_F32 || d == MOE_BF16; }
+
+moe_status check_fp4_gemm_args(const uint8_t *act_codes, const uint8_t *act_scales, const float *act_scale_2,
+                               int64_t rows, int32_t K, const uint8_t *codes, const uint8_t *scales,
+                               const float *weight_scale_2, int format, const int32_t *group_sizes, int32_t E,
+                               int64_t N, const void *workspace, size_t workspace_bytes) {
+    if (format != MOE_FP4_MX && format != MOE_FP4_NV) return MOE_ERR_INVALID_ARG;
+    if (rows < 0 || rows > INT32_MAX || K <= 0 || K % 32 != 0 || N <= 0 || E <= 0 || E > kMaxE)
+        return MOE_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(E) * N > INT32_MAX) return MOE_ERR_INVALID_ARG;
+    if (!codes || !scales || !group_sizes || !workspace || workspace_bytes < kStatusBytes)
+        return MOE_ERR_INVALID_ARG;
+    if (rows > 0 && (!act_codes || !act_scales)) return MOE_ERR_INVALID_ARG;
+    if (!aligned(act_codes, 16) || !aligned(codes, 16) || !aligned(workspace, 16)) return MOE_ERR_INVALID_ARG;
+    if (format == MOE_FP4_NV && (!act_scale_2 || !weight_scale_2 || !aligned(act_scale_2, 4) ||
+                                 !aligned(weight_scale_2, 4)))
+        return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
+moe::Fp4Gemm fp4_gemm(const uint8_t *act_codes, const uint8_t *act_scales, const float *act_scale_2, int64_t rows,
+                      int32_t K, const uint8_t *codes, const uint8_t *scales, const float *weight_scale_2,
+                      const int32_t *group_sizes, int32_t E, int32_t N, void *workspace) {
+    moe::Fp4Gemm g = {};
+    g.a_codes = act_codes;
+    g.a_scales = act_scales;
+    g.a_scale_2 = act_scale_2;
+    g.w_codes = codes;
+    g.w_scales = scales;
+    g.w_scale_2 = weight_scale_2;
+    g.group_sizes = group_sizes;
+    g.rows = static_cast<int>(rows);
+    g.K = K;
+    g.E = E;
+    g.N = N;
+    g.status = status_word(workspace);
+    g.wait_limit_ns = kWaitLimitNs;
+    return g;
+}
+
+moe_status check_gate_args(const void *logits, int dtype, int64_t stride, int32_t T, int32_t E, int32_t k) {
+    if (T < 0 || E <= 0 || E > kMaxE || k <= 0 || k > E || !known_dtype(dtype) || stride < 0)
+        return MOE_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(T) * k > INT32_MAX) return MOE_ERR_INVALID_ARG;
+    if (T > 0 && (!logits || !aligned(logits, dtype == MOE_F32 ? 4 : 2))) return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -464,6 +512,193 @@ moe_status moe_mxfp4_to_nvfp4(const uint8_t *scales, int32_t E, int32_t N, int32
         reinterpret_cast<int *>(static_cast<uint8_t *>(workspace) + kStatusBytes),
         status_word(workspace), kWaitLimitNs, static_cast<cudaStream_t>(stream), sms, &launches);
     g_last_launches = launches;
+    return st;
+}
+
+moe_status moe_topk_gate(const void *logits, moe_dtype dtype, int64_t stride, int32_t T, int32_t E,
+                         int32_t k, int32_t renorm, int32_t *topk_ids, float *topk_w, void *stream) {
+    moe_status st = check_gate_args(logits, dtype, stride, T, E, k);
+    if (st != MOE_OK) return st;
+    if (T > 0 && (!topk_ids || !topk_w)) return MOE_ERR_INVALID_ARG;
+    int sms = 0;
+    if ((st = current_device(&sms)) != MOE_OK) return st;
+    moe::Gate g = {logits, dtype == MOE_BF16, stride, T, E, k, renorm != 0, topk_ids, topk_w, nullptr, nullptr};
+    st = moe::launch_topk_gate(g, false, static_cast<cudaStream_t>(stream));
+    g_last_launches = T > 0 ? 1 : 0;
+    return st;
+}
+
+moe_status moe_topk_gate_backward(const void *logits, moe_dtype dtype, int64_t stride, int32_t T,
+                                  int32_t E, int32_t k, int32_t renorm, const int32_t *topk_ids,
+                                  const float *topk_dw, void *dlogits, void *stream) {
+    moe_status st = check_gate_args(logits, dtype, stride, T, E, k);
+    if (st != MOE_OK) return st;
+    if (T > 0 && (!topk_ids || !topk_dw || !dlogits || !aligned(dlogits, dtype == MOE_F32 ? 4 : 2)))
+        return MOE_ERR_INVALID_ARG;
+    int sms = 0;
+    if ((st = current_device(&sms)) != MOE_OK) return st;
+    moe::Gate g = {logits, dtype == MOE_BF16, stride, T, E, k, renorm != 0,
+                   const_cast<int32_t *>(topk_ids), nullptr, topk_dw, dlogits};
+    st = moe::launch_topk_gate(g, true, static_cast<cudaStream_t>(stream));
+    g_last_launches = T > 0 ? 1 : 0;
+    return st;
+}
+
+moe_status moe_fp4_quantize(const void *x, moe_dtype dtype, int64_t x_rows, int64_t x_stride, int32_t K,
+                            const int32_t *row_index, int32_t index_div, int64_t rows,
+                            moe_fp4_format format, const float *tensor_scale, uint8_t *codes,
+                            uint8_t *scales, void *values, moe_dtype values_dtype, void *workspace,
+                            size_t workspace_bytes, void *stream) {
+    if (!known_dtype(dtype) || (format != MOE_FP4_MX && format != MOE_FP4_NV) || K <= 0 || K % 32 != 0 ||
+        x_rows < 0 || x_rows > INT32_MAX || x_stride < 0 || rows < 0 || rows > INT32_MAX || index_div < 1)
+        return MOE_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < kStatusBytes || !aligned(workspace, 16)) return MOE_ERR_INVALID_ARG;
+    if (values && (!known_dtype(values_dtype) || !aligned(values, 16))) return MOE_ERR_INVALID_ARG;
+    if (format == MOE_FP4_NV && (!tensor_scale || !aligned(tensor_scale, 4))) return MOE_ERR_INVALID_ARG;
+    if (rows > 0 && (!codes || !scales || !aligned(codes, 16))) return MOE_ERR_INVALID_ARG;
+    if (rows > 0 && x_rows > 0 && (!x || !aligned(x, dtype == MOE_F32 ? 4 : 2))) return MOE_ERR_INVALID_ARG;
+    if (!row_index && rows > x_rows) return MOE_ERR_INVALID_ARG;
+    int sms = 0;
+    moe_status st = current_device(&sms);
+    if (st != MOE_OK) return st;
+    moe::Fp4Quant q = {x, dtype == MOE_BF16, x_rows, x_stride, K, row_index, index_div, rows,
+                       format == MOE_FP4_NV, tensor_scale, codes, scales, values,
+                       values_dtype == MOE_BF16, status_word(workspace)};
+    st = moe::launch_fp4_quantize(q, static_cast<cudaStream_t>(stream), sms);
+    g_last_launches = rows > 0 ? 1 : 0;
+    return st;
+}
+
+moe_status moe_fp4_grouped_gemm(const uint8_t *act_codes, const uint8_t *act_scales,
+                                const float *act_scale_2, int64_t rows, int32_t K, const uint8_t *codes,
+                                const uint8_t *scales, const float *weight_scale_2,
+                                moe_fp4_format format, const int32_t *group_sizes, int32_t E, int32_t N,
+                                void *out, moe_dtype out_dtype, void *workspace, size_t workspace_bytes,
+                                void *stream) {
+    moe_status st = check_fp4_gemm_args(act_codes, act_scales, act_scale_2, rows, K, codes, scales,
+                                        weight_scale_2, format, group_sizes, E, N, workspace, workspace_bytes);
+    if (st != MOE_OK) return st;
+    if (!known_dtype(out_dtype) || (rows > 0 && !out) || !aligned(out, out_dtype == MOE_F32 ? 4 : 2))
+        return MOE_ERR_INVALID_ARG;
+    int sms = 0;
+    if ((st = current_device(&sms)) != MOE_OK) return st;
+    moe::Fp4Gemm g = fp4_gemm(act_codes, act_scales, act_scale_2, rows, K, codes, scales, weight_scale_2,
+                              group_sizes, E, N, workspace);
+    g.out = out;
+    g.out_bf16 = out_dtype == MOE_BF16;
+    st = moe::launch_fp4_gemm(g, format == MOE_FP4_NV, false, static_cast<cudaStream_t>(stream), sms);
+    g_last_launches = rows > 0 ? 1 : 0;
+    return st;
+}
+
+moe_status moe_fp4_grouped_gemm_swiglu(const uint8_t *act_codes, const uint8_t *act_scales,
+                                       const float *act_scale_2, int64_t rows, int32_t K,
+                                       const uint8_t *codes, const uint8_t *scales,
+                                       const float *weight_scale_2, moe_fp4_format format,
+                                       const int32_t *group_sizes, int32_t E, int32_t I,
+                                       const float *h_scale_2, uint8_t *h_codes, uint8_t *h_scales,
+                                       void *workspace, size_t workspace_bytes, void *stream) {
+    if (I <= 0 || I % 32 != 0) return MOE_ERR_INVALID_ARG;
+    moe_status st = check_fp4_gemm_args(act_codes, act_scales, act_scale_2, rows, K, codes, scales,
+                                        weight_scale_2, format, group_sizes, E, 2 * static_cast<int64_t>(I),
+                                        workspace, workspace_bytes);
+    if (st != MOE_OK) return st;
+    if (rows > 0 && (!h_codes || !h_scales || !aligned(h_codes, 16))) return MOE_ERR_INVALID_ARG;
+    if (format == MOE_FP4_NV && (!h_scale_2 || !aligned(h_scale_2, 4))) return MOE_ERR_INVALID_ARG;
+    int sms = 0;
+    if ((st = current_device(&sms)) != MOE_OK) return st;
+    moe::Fp4Gemm g = fp4_gemm(act_codes, act_scales, act_scale_2, rows, K, codes, scales, weight_scale_2,
+                              group_sizes, E, 2 * I, workspace);
+    g.out = h_codes;
+    g.out_scales = h_scales;
+    g.h_scale_2 = h_scale_2;
+    st = moe::launch_fp4_gemm(g, format == MOE_FP4_NV, true, static_cast<cudaStream_t>(stream), sms);
+    g_last_launches = rows > 0 ? 1 : 0;
+    return st;
+}
+
+moe_status moe_layer_forward_fp4(
+    const uint16_t *x, const int32_t *topk_ids, const float *topk_w, int32_t T, int32_t k, int32_t E,
+    int32_t hidden, int32_t inter, moe_fp4_format format, const uint8_t *w13_codes,
+    const uint8_t *w13_scales, const float *w13_scale_2, const uint8_t *w2_codes, const uint8_t *w2_scales,
+    const float *w2_scale_2, const float *x_scale_2, const float *h_scale_2, float *out,
+    int32_t *group_sizes, int32_t *group_offsets, int32_t *sorted_slot, int32_t *slot_to_row,
+    uint8_t *x_codes, uint8_t *x_scales, uint8_t *h_codes, uint8_t *h_scales, float *y2, void *workspace,
+    size_t workspace_bytes, void *stream) {
+    // Every check of every stage first: a call that fails enqueues nothing.
+    if (hidden <= 0 || hidden % 32 || inter <= 0 || inter % 32) return MOE_ERR_INVALID_ARG;
+    moe_status st = check_route_args(topk_ids, T, k, E, group_sizes, group_offsets, sorted_slot, slot_to_row,
+                                     nullptr, 0, nullptr, MOE_ACT_ROW_MAJOR, workspace, workspace_bytes);
+    if (st != MOE_OK) return st;
+    const int64_t rows = static_cast<int64_t>(T) * k;
+    if ((st = check_fp4_gemm_args(x_codes, x_scales, x_scale_2, rows, hidden, w13_codes, w13_scales, w13_scale_2,
+                                  format, group_sizes, E, 2 * static_cast<int64_t>(inter), workspace,
+                                  workspace_bytes)) != MOE_OK ||
+        (st = check_fp4_gemm_args(h_codes, h_scales, h_scale_2, rows, inter, w2_codes, w2_scales, w2_scale_2,
+                                  format, group_sizes, E, hidden, workspace, workspace_bytes)) != MOE_OK)
+        return st;
+    if (T > 0 && (!x || !topk_w || !y2 || !out || !aligned(x, 2) || !aligned(y2, 16) || !aligned(out, 16)))
+        return MOE_ERR_INVALID_ARG;
+    int sms = 0;
+    if ((st = current_device(&sms)) != MOE_OK) return st;
+    const bool nv = format == MOE_FP4_NV;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int launches = 0;
+    st = moe::launch_route_sort(topk_ids, T, k, E, group_sizes, group_offsets, sorted_slot, slot_to_row, nullptr, 0,
+                                nullptr, 0, static_cast<uint8_t *>(workspace) + kStatusBytes,
+                                status_word(workspace), s, &launches);
+    if (st == MOE_OK && rows > 0) {
+        moe::Fp4Quant q = {x, 1, T, hidden, hidden, sorted_slot, k, rows, nv, x_scale_2, x_codes, x_scales,
+                           nullptr, 0, status_word(workspace)};
+        moe::Fp4Gemm g13 = fp4_gemm(x_codes, x_scales, x_scale_2, rows, hidden, w13_codes, w13_scales, w13_scale_2,
+                                    group_sizes, E, 2 * inter, workspace);
+        g13.out = h_codes;
+        g13.out_scales = h_scales;
+        g13.h_scale_2 = h_scale_2;
+        moe::Fp4Gemm g2 = fp4_gemm(h_codes, h_scales, h_scale_2, rows, inter, w2_codes, w2_scales, w2_scale_2,
+                                   group_sizes, E, hidden, workspace);
+        g2.out = y2;
+        if ((st = moe::launch_fp4_quantize(q, s, sms)) == MOE_OK) ++launches;
+        if (st == MOE_OK && (st = moe::launch_fp4_gemm(g13, nv, true, s, sms)) == MOE_OK) ++launches;
+        if (st == MOE_OK && (st = moe::launch_fp4_gemm(g2, nv, false, s, sms)) == MOE_OK) ++launches;
+        if (st == MOE_OK && (st = moe::launch_combine(y2, slot_to_row, topk_w, T, k, hidden, out, 0, s, sms)) == MOE_OK)
+            ++launches;
+    }
+    g_last_launches = launches;
+    return st;
+}
+
+moe_status moe_combine_backward(const void *dout, moe_dtype dout_dtype, const void *y, moe_dtype y_dtype,
+                                const int32_t *slot_to_row, const float *topk_w, int32_t T, int32_t k,
+                                int32_t N, void *dy, moe_dtype dy_dtype, float *topk_dw, void *stream) {
+    if (T < 0 || k <= 0 || N <= 0 || static_cast<int64_t>(T) * k > INT32_MAX) return MOE_ERR_INVALID_ARG;
+    if (!known_dtype(dout_dtype) || !known_dtype(y_dtype) || !known_dtype(dy_dtype)) return MOE_ERR_INVALID_ARG;
+    if (T > 0 && (!dout || !slot_to_row || !topk_w || (topk_dw && !y) || (!dy && !topk_dw))) return MOE_ERR_INVALID_ARG;
+    if (!aligned(dout, 16) || !aligned(y, 16) || !aligned(dy, 16)) return MOE_ERR_INVALID_ARG;
+    int sms = 0;
+    moe_status st = current_device(&sms);
+    if (st != MOE_OK) return st;
+    moe::CombineGrad c = {dout, y, dout_dtype == MOE_BF16, y_dtype == MOE_BF16, dy_dtype == MOE_BF16,
+                          slot_to_row, topk_w, T, k, N, dy, topk_dw};
+    st = moe::launch_combine_backward(c, static_cast<cudaStream_t>(stream), sms);
+    g_last_launches = T > 0 ? 1 : 0;
+    return st;
+}
+
+moe_status moe_gather_backward(const void *dx_sorted, moe_dtype in_dtype, const int32_t *slot_to_row,
+                               int32_t T, int32_t k, int32_t hidden, void *dx, moe_dtype out_dtype,
+                               void *stream) {
+    if (T < 0 || k <= 0 || hidden <= 0 || static_cast<int64_t>(T) * k > INT32_MAX || !known_dtype(in_dtype) ||
+        !known_dtype(out_dtype))
+        return MOE_ERR_INVALID_ARG;
+    if (T > 0 && (!dx_sorted || !slot_to_row || !dx || !aligned(dx_sorted, 16) || !aligned(dx, 16)))
+        return MOE_ERR_INVALID_ARG;
+    int sms = 0;
+    moe_status st = current_device(&sms);
+    if (st != MOE_OK) return st;
+    st = moe::launch_gather_backward(dx_sorted, in_dtype == MOE_BF16, slot_to_row, T, k, hidden, dx,
+                                     out_dtype == MOE_BF16, static_cast<cudaStream_t>(stream), sms);
+    g_last_launches = T > 0 ? 1 : 0;
     return st;
 }
 

@@ -95,4 +95,66 @@ moe_status launch_combine(const float *y, const int32_t *s2r, const float *w, in
                           void *out, int out_bf16, cudaStream_t stream, int num_sms,
                           int slot_order = 0);
 
+// Grouped product of 4-bit activations and 4-bit weights.  swiglu: N = 2 * I weight
+// rows ([gate | up]), `out` = h codes [rows, I / 2] with `out_scales`.
+struct Fp4Gemm {
+    const uint8_t *a_codes, *a_scales, *w_codes, *w_scales;
+    const float *a_scale_2, *w_scale_2, *h_scale_2;   // NVFP4 only
+    const int32_t *group_sizes;
+    int rows, K, E, N;
+    void *out;
+    uint8_t *out_scales;
+    int out_bf16;
+    int *status;
+    uint64_t wait_limit_ns;
+};
+moe_status launch_fp4_gemm(const Fp4Gemm &g, bool nv, bool swiglu, cudaStream_t stream, int num_sms);
+
+// Rows of x (row r, or row row_index[r] / index_div) to 4-bit codes and block
+// scales; `values` (optional) receives what they stand for.
+struct Fp4Quant {
+    const void *x;
+    int in_bf16;
+    int64_t x_rows, x_stride;
+    int K;
+    const int32_t *row_index;
+    int index_div;
+    int64_t rows;
+    bool nv;
+    const float *tensor_scale;
+    uint8_t *codes, *scales;
+    void *values;
+    int values_bf16;
+    int *status;
+};
+moe_status launch_fp4_quantize(const Fp4Quant &q, cudaStream_t stream, int num_sms);
+
+// Gradient of the combine: dy and dw (either may be null).
+struct CombineGrad {
+    const void *dout, *y;
+    int dout_bf16, y_bf16, dy_bf16;
+    const int32_t *s2r;
+    const float *w;
+    int T, k, N;
+    void *dy;
+    float *dw;
+};
+moe_status launch_combine_backward(const CombineGrad &c, cudaStream_t stream, int num_sms);
+
+moe_status launch_gather_backward(const void *dxs, int in_bf16, const int32_t *s2r, int T, int k, int N, void *dx,
+                                  int out_bf16, cudaStream_t stream, int num_sms);
+
+// Router gate (ids, weights written) and its gradient (ids, dw read, dlogits written).
+struct Gate {
+    const void *logits;
+    int bf16;
+    int64_t stride;
+    int T, E, k, renorm;
+    int32_t *ids;
+    float *weights;
+    const float *dw;
+    void *dlogits;
+};
+moe_status launch_topk_gate(const Gate &g, bool backward, cudaStream_t stream);
+
 }  // namespace moe

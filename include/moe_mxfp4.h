@@ -523,6 +523,198 @@ MOE_API moe_status moe_mxfp4_to_nvfp4(const uint8_t *scales, int32_t E, int32_t 
                                       uint64_t *out_of_range, void *workspace,
                                       size_t workspace_bytes, void *stream);
 
+/* 4-bit formats of both operands of the W4A4 product: e2m1 codes, two a byte
+ * (element 2j in bits 0-3), under block scales along K.
+ *  MOE_FP4_MX  one E8M0 byte (2^(byte - 127)) per 32 elements.
+ *  MOE_FP4_NV  one E4M3 byte per 16 elements, times an f32 tensor scale. */
+typedef enum { MOE_FP4_MX = 0, MOE_FP4_NV = 1 } moe_fp4_format;
+
+/*
+ * moe_topk_gate — router gate: the k largest logits of every token, and their
+ * softmax weights.
+ *
+ *   topk_ids[t, :] = the k largest of logits[t, :] in descending order; equal
+ *                    logits by ascending expert (-0 equals +0; a NaN ranks with
+ *                    -inf)
+ *   topk_w[t, j]   = exp(l_j - m) / sum, the sum over all E logits (renorm = 0)
+ *                    or over the k chosen ones (renorm = 1)
+ * in f32.  -inf masks an expert: it adds nothing to a sum, and is chosen (with
+ * weight 0) only when fewer than k others are left.  A row whose logits are all
+ * -inf gets weights 0.  A NaN makes the weights of every sum it enters NaN; the
+ * ids stay valid.
+ *
+ *  logits   device [T, E] f32 or bf16, row t at logits + t * stride elements.
+ *  E, k     1..1024 experts, k in 1..E.
+ *  topk_ids device int32 [T, k] out; topk_w device f32 [T, k] out.
+ */
+MOE_API moe_status moe_topk_gate(const void *logits, moe_dtype dtype, int64_t stride, int32_t T,
+                                 int32_t E, int32_t k, int32_t renorm, int32_t *topk_ids,
+                                 float *topk_w, void *stream);
+
+/*
+ * moe_topk_gate_backward — gradient of moe_topk_gate's weights with respect to
+ * the logits.  With p the softmax that the weights were taken from and dot =
+ * sum_j p_j dw_j over the chosen experts:
+ *   renorm = 0:  dlogits[t, e] = p_e * (dw_e - dot), dw_e = 0 where not chosen
+ *   renorm = 1:  the same over the chosen experts alone, 0 elsewhere.
+ * The softmax is recomputed from the logits.  An id outside [0, E) adds nothing.
+ *
+ *  topk_ids device int32 [T, k]; topk_dw device f32 [T, k].
+ *  dlogits  device [T, E] out, contiguous, of the logits' type.
+ */
+MOE_API moe_status moe_topk_gate_backward(const void *logits, moe_dtype dtype, int64_t stride,
+                                          int32_t T, int32_t E, int32_t k, int32_t renorm,
+                                          const int32_t *topk_ids, const float *topk_dw,
+                                          void *dlogits, void *stream);
+
+/*
+ * moe_fp4_quantize — activation rows to 4-bit codes and block scales, with the
+ * routing permutation in the load:
+ *
+ *   row r of the result holds x[row_index[r] / index_div, :]  (row_index NULL: x[r, :])
+ *
+ *  MOE_FP4_MX: for each 32 elements with largest magnitude a: scale byte =
+ *    clamp(floor(log2 a) - 2 + 127, 0, 252), code = e2m1(x / 2^(byte - 127)),
+ *    nearest, ties to the even mantissa, saturating at 6.
+ *  MOE_FP4_NV: for each 16 elements: scale byte s = e4m3(min(a / (6 g), 448))
+ *    with g = *tensor_scale, code = e2m1(x * (1 / (s g))), both nearest, ties to
+ *    even, in f32.  A block whose s is 0 (or 1 / (s g) not finite) has zero codes.
+ * A block that holds an infinity or a NaN gets zero codes and the scale byte
+ * that stands for NaN (255; 0x7F), which the products report.  -0 is stored as
+ * +0.
+ *
+ *  x            device f32 or bf16, x_rows rows of K elements, row i at x + i *
+ *               x_stride elements (x_stride >= 0).  16-byte aligned rows load as
+ *               vectors; any other alignment of the element type is taken.
+ *  K            row length, a multiple of 32.
+ *  row_index    device int32 [rows], or NULL; index_div >= 1.  With sorted_slot
+ *               and index_div = top_k, the gather of moe_route_sort.  An entry
+ *               whose row lies outside [0, x_rows) sets MOE_ERR_DATA and its row
+ *               becomes zeros.  With NULL, rows <= x_rows.
+ *  tensor_scale device f32 [1], positive and finite (MOE_FP4_NV; ignored for
+ *               MOE_FP4_MX).  Another value sets MOE_ERR_DATA.
+ *  codes        device uint8 [rows, K/2] out, 16-byte aligned.
+ *  scales       device uint8 [rows, K/32] or [rows, K/16] out.
+ *  values       device [rows, K] out or NULL, 16-byte aligned: the numbers the
+ *               codes stand for (bf16 holds them exactly for MOE_FP4_MX).
+ *  workspace    device, >= 256 bytes, 16-byte aligned (status word).
+ */
+MOE_API moe_status moe_fp4_quantize(const void *x, moe_dtype dtype, int64_t x_rows, int64_t x_stride,
+                                    int32_t K, const int32_t *row_index, int32_t index_div,
+                                    int64_t rows, moe_fp4_format format, const float *tensor_scale,
+                                    uint8_t *codes, uint8_t *scales, void *values,
+                                    moe_dtype values_dtype, void *workspace, size_t workspace_bytes,
+                                    void *stream);
+
+/*
+ * moe_fp4_grouped_gemm — grouped matmul with both operands in 4 bits (W4A4):
+ *
+ *   out[r, n] = sum_k a[r, k] * w[e, n, k]   for every row r of band e
+ *
+ * with a and w the values of codes and scales (for MOE_FP4_NV times
+ * act_scale_2[0] * weight_scale_2[e], applied once to the f32 sum).  The
+ * tensor core multiplies the codes and applies the scales (block-scaled MMA);
+ * products are exact and sums are kept in f32.
+ *
+ *  act_codes    device uint8 [rows, K/2], act_scales [rows, K/32] or [rows, K/16]
+ *               (moe_fp4_quantize).
+ *  codes        device uint8 [E, N, K/2], scales [E, N, K/32] or [E, N, K/16]: the
+ *               weights of moe_mxfp4_grouped_gemm / moe_nvfp4_grouped_gemm.
+ *  K            a multiple of 32.  Both code buffers 16-byte aligned.
+ *  act_scale_2, weight_scale_2   device f32 [1] and [E] (MOE_FP4_NV; ignored for
+ *               MOE_FP4_MX).
+ *  Other arguments as for moe_mxfp4_grouped_gemm.
+ * A scale byte that stands for NaN (255; 0x7F), and for MOE_FP4_NV a negative
+ * scale (the MMA's scales are unsigned), sets MOE_ERR_DATA; the outputs of its
+ * row or column are then unspecified.  One kernel launch.
+ */
+MOE_API moe_status moe_fp4_grouped_gemm(const uint8_t *act_codes, const uint8_t *act_scales,
+                                        const float *act_scale_2, int64_t rows, int32_t K,
+                                        const uint8_t *codes, const uint8_t *scales,
+                                        const float *weight_scale_2, moe_fp4_format format,
+                                        const int32_t *group_sizes, int32_t E, int32_t N, void *out,
+                                        moe_dtype out_dtype, void *workspace,
+                                        size_t workspace_bytes, void *stream);
+
+/*
+ * moe_fp4_grouped_gemm_swiglu — the w13 product with both operands in 4 bits,
+ * SwiGLU and the requantisation of h in its epilogue:
+ *
+ *   y = moe_fp4_grouped_gemm over 2 I weight rows ([0, I) gate, [I, 2I) up), in f32
+ *   h = silu(y[r, i]) * y[r, I + i] in f32, quantised as moe_fp4_quantize does it
+ * so neither y nor h is stored in 16 or 32 bits and h_codes / h_scales feed the
+ * w2 product.
+ *
+ *  I            columns of h, a multiple of 32.
+ *  h_scale_2    device f32 [1]: tensor scale of h (MOE_FP4_NV; ignored for
+ *               MOE_FP4_MX); not positive and finite sets MOE_ERR_DATA.
+ *  h_codes      device uint8 [rows, I/2] out, 16-byte aligned; h_scales [rows,
+ *               I/32] or [rows, I/16] out.
+ */
+MOE_API moe_status moe_fp4_grouped_gemm_swiglu(const uint8_t *act_codes, const uint8_t *act_scales,
+                                               const float *act_scale_2, int64_t rows, int32_t K,
+                                               const uint8_t *codes, const uint8_t *scales,
+                                               const float *weight_scale_2, moe_fp4_format format,
+                                               const int32_t *group_sizes, int32_t E, int32_t I,
+                                               const float *h_scale_2, uint8_t *h_codes,
+                                               uint8_t *h_scales, void *workspace,
+                                               size_t workspace_bytes, void *stream);
+
+/*
+ * moe_layer_forward_fp4 — moe_layer_forward with 4-bit activations: route sort ->
+ * moe_fp4_quantize (gathering) -> moe_fp4_grouped_gemm_swiglu ->
+ * moe_fp4_grouped_gemm -> moe_combine, all on `stream`.
+ *
+ *  x_scale_2, h_scale_2, w13_scale_2, w2_scale_2   tensor scales (MOE_FP4_NV).
+ *  Caller-owned intermediates: x_codes [T*k, hidden/2], x_scales, h_codes [T*k,
+ *  inter/2], h_scales, y2 f32 [T*k, hidden]; others as for moe_layer_forward.
+ */
+MOE_API moe_status moe_layer_forward_fp4(
+    const uint16_t *x, const int32_t *topk_ids, const float *topk_w, int32_t T, int32_t k, int32_t E,
+    int32_t hidden, int32_t inter, moe_fp4_format format, const uint8_t *w13_codes,
+    const uint8_t *w13_scales, const float *w13_scale_2, const uint8_t *w2_codes,
+    const uint8_t *w2_scales, const float *w2_scale_2, const float *x_scale_2,
+    const float *h_scale_2, float *out, int32_t *group_sizes, int32_t *group_offsets,
+    int32_t *sorted_slot, int32_t *slot_to_row, uint8_t *x_codes, uint8_t *x_scales,
+    uint8_t *h_codes, uint8_t *h_scales, float *y2, void *workspace, size_t workspace_bytes,
+    void *stream);
+
+/*
+ * moe_combine_backward — gradient of moe_combine (out[t] = sum_j topk_w[t, j] *
+ * y[slot_to_row[t*k + j]]):
+ *
+ *   dy[slot_to_row[t*k + j], n] = topk_w[t, j] * dout[t, n]
+ *   topk_dw[t, j]               = sum_n dout[t, n] * y[slot_to_row[t*k + j], n]
+ * in f32, one writer per element and a fixed order of every sum (no atomics:
+ * results repeat bit for bit).  A slot whose slot_to_row entry lies outside [0,
+ * T*k) has topk_dw 0 and writes no row; rows of dy that no slot names are not
+ * written.
+ *
+ *  dout         device [T, N]; y device [T*k, N]; dy device [T*k, N] out: f32 or
+ *               bf16 each, 16-byte aligned.
+ *  dy, topk_dw  either may be NULL (not computed); y may be NULL without topk_dw.
+ *  slot_to_row, topk_w   as for moe_combine.
+ */
+MOE_API moe_status moe_combine_backward(const void *dout, moe_dtype dout_dtype, const void *y,
+                                        moe_dtype y_dtype, const int32_t *slot_to_row,
+                                        const float *topk_w, int32_t T, int32_t k, int32_t N,
+                                        void *dy, moe_dtype dy_dtype, float *topk_dw, void *stream);
+
+/*
+ * moe_gather_backward — gradient of the sort's gather (x_sorted[slot_to_row[t*k +
+ * j]] = x[t]):
+ *
+ *   dx[t, n] = sum_j dx_sorted[slot_to_row[t*k + j], n]
+ * summed in f32 in ascending j.  A slot whose entry lies outside [0, T*k) adds
+ * nothing.
+ *
+ *  dx_sorted    device [T*k, hidden]; dx device [T, hidden] out: f32 or bf16 each,
+ *               16-byte aligned.
+ */
+MOE_API moe_status moe_gather_backward(const void *dx_sorted, moe_dtype in_dtype,
+                                       const int32_t *slot_to_row, int32_t T, int32_t k,
+                                       int32_t hidden, void *dx, moe_dtype out_dtype, void *stream);
+
 /*
  * moe_debug_bounded_wait — failure-detection self-test.  Launches one block
  * that waits on a shared-memory barrier nothing will ever complete, using the
