@@ -46,14 +46,17 @@
 namespace moe {
 namespace fp4 {
 
-constexpr int kThreads = 256;
-constexpr int kProducerWarp = 0, kIssuerWarp = 1, kWScaleWarp = 2, kAScaleWarp = 3;   // 4..7: epilogue
+constexpr int kProducerWarp = 0, kIssuerWarp = 1;
+constexpr int kLoaders = 4;                    // scale-loader warps an operand, on stages in turn
+constexpr int kWScaleWarp = 2, kAScaleWarp = kWScaleWarp + kLoaders;
+constexpr int kEpilogueWarp = kAScaleWarp + kLoaders;
+constexpr int kThreads = 32 * (kEpilogueWarp + 4);
 constexpr int kMaxE = 1024;
 constexpr int kTileN = 128;                    // weight rows a tile (MMA M)
 constexpr int kStageBytesRow = 128;            // 256 k
 constexpr int kStageK = 256;
 constexpr int kMaxStages = 12;
-constexpr int kPrefetch = 4;                   // stages of scale bytes in registers
+constexpr int kPrefetch = 2;                   // stages of scale bytes a loader holds in registers
 constexpr int kAccCols = 192;                  // columns of one accumulator buffer
 constexpr int kSfCol0 = 2 * kAccCols;          // scale atoms, two sets of 64 columns
 constexpr int kSfSetCols = 64;
@@ -179,11 +182,8 @@ __device__ __forceinline__ Item decode_item(int j, const int *roff, const int *i
 // Position in the stage ring.
 struct Ring {
     uint32_t slot = 0, phase = 0;
-    __device__ __forceinline__ void next(uint32_t n) {
-        if (++slot == n) {
-            slot = 0;
-            phase ^= 1u;
-        }
+    __device__ __forceinline__ void next(uint32_t n, uint32_t by = 1) {
+        for (slot += by; slot >= n; slot -= n) phase ^= 1u;
     }
 };
 
@@ -199,10 +199,10 @@ struct Cursor {
         if (j < total) it = decode_item<kMost>(j, roff, ioff, E, n_tiles);
     }
     __device__ __forceinline__ void next(int total, int k_stages, const int *roff, const int *ioff, int E,
-                                         int n_tiles) {
-        if (++ks < k_stages) return;
-        ks = 0;
-        j += gridDim.x;
+                                         int n_tiles, int by = 1) {
+        ks += by;
+        if (ks < k_stages) return;
+        for (; ks >= k_stages; ks -= k_stages) j += gridDim.x;
         if (j < total) it = decode_item<kMost>(j, roff, ioff, E, n_tiles);
     }
 };
@@ -243,55 +243,47 @@ __device__ __forceinline__ bool bad_word(uint32_t w) {
     else return __vcmpeq4(w, 0xFFFFFFFFu) != 0;
 }
 
-// Body of a scale-loader warp.  kWeights: the weight tiles' scales (4 MT rows
+// Body of scale-loader warp `part` of `parts`, which takes every parts-th stage.
+// parts <= n_stages: a loader that waits for the slot of stage s has seen stage s -
+// parts - n_stages consumed, so the slot's barrier is at most one phase behind and
+// its parity is unambiguous.  kWeights: the weight tiles' scales (4 MT rows
 // a lane), else the tokens' (AR rows a lane).
 template <bool kNv, bool kSwiglu, bool kWeights>
 __device__ __forceinline__ void load_scales(const Params &p, uint8_t *sf_ring, uint32_t n_stages, int total,
                                             const int *roff, const int *ioff, uint64_t *sf_full,
-                                            uint64_t *empty, volatile int *abort_flag) {
+                                            uint64_t *empty, volatile int *abort_flag, int part, int parts) {
     using S = Shape<kNv, kSwiglu>;
     constexpr int R = kWeights ? 4 * S::MT : S::AR;
     constexpr int W = S::W;
     const int lane = threadIdx.x & 31;
     const int k_stages = (p.K + kStageK - 1) / kStageK;
     const int vec = kWeights ? p.w_vec : p.a_vec;
-    uint32_t buf[kPrefetch][R][W];
+    uint32_t buf[kPrefetch][R][W] = {};
     bool bad = false;
     Cursor<S::NT> ld, st;
     ld.start(total, roff, ioff, p.E, p.n_tiles);
+    if (part) ld.next(total, k_stages, roff, ioff, p.E, p.n_tiles, part);
     st = ld;
 
     auto fetch = [&](uint32_t (&b)[R][W]) {
         const int first = ld.ks * 4 * W;
 #pragma unroll
         for (int q = 0; q < R; ++q) {
+            // Rows past the tile's or the chunk's end read its last row again
+            // (their sums are never stored): nothing here waits for the load.
             int64_t row;
-            bool counts;
             if constexpr (kWeights) {
-                // Row of weight tile q / 4; rows past the tile's end are clamped
-                // into the tensor (their sums are never stored).
                 const int cols = kSwiglu ? p.I : p.N;
-                const int n = ld.it.n0 + lane + 32 * (q & 3);
-                counts = n < cols;
-                row = static_cast<int64_t>(ld.it.e) * p.N + (q >= 4 ? p.I : 0) + (counts ? n : cols - 1);
+                row = static_cast<int64_t>(ld.it.e) * p.N + (q >= 4 ? p.I : 0) +
+                      min(ld.it.n0 + lane + 32 * (q & 3), cols - 1);
             } else {
-                const int t = lane + 32 * q;
-                counts = t < ld.it.nvalid;
-                row = ld.it.row0 + (counts ? t : 0);
-            }
-            if (!kWeights && 32 * q >= ld.it.nt) {
-#pragma unroll
-                for (int i = 0; i < W; ++i) b[q][i] = 0;
-                continue;
+                if (32 * q >= ld.it.nt) continue;
+                row = ld.it.row0 + min(lane + 32 * q, ld.it.nvalid - 1);
             }
             load_words<W>((kWeights ? p.w_scales : p.a_scales) + row * p.scale_row, first, p.scale_row, vec,
                           b[q]);
-            if (!counts) {
-#pragma unroll
-                for (int i = 0; i < W; ++i) b[q][i] = 0;
-            }
         }
-        ld.next(total, k_stages, roff, ioff, p.E, p.n_tiles);
+        ld.next(total, k_stages, roff, ioff, p.E, p.n_tiles, parts);
     };
 
 #pragma unroll
@@ -299,6 +291,7 @@ __device__ __forceinline__ void load_scales(const Params &p, uint8_t *sf_ring, u
         if (ld.valid(total)) fetch(buf[d]);
 
     Ring r;
+    if (part) r.next(n_stages, part);
     bool ok = true;
     while (ok && st.valid(total)) {
 #pragma unroll
@@ -308,9 +301,11 @@ __device__ __forceinline__ void load_scales(const Params &p, uint8_t *sf_ring, u
             if (!ok) break;
             uint8_t *dst = sf_ring + r.slot * S::kSfBytes + (kWeights ? 0 : S::kSfaBytes) + lane * 16;
 #pragma unroll
-            for (int q = 0; q < R; ++q)
+            for (int q = 0; q < R; ++q) {
+                if (!kWeights && 32 * q >= st.it.nt) continue;
 #pragma unroll
                 for (int i = 0; i < W; ++i) bad |= bad_word<kNv>(buf[d][q][i]);
+            }
             constexpr int ATOMS = (R + 3) / 4;
 #pragma unroll
             for (int a = 0; a < ATOMS; ++a)
@@ -329,8 +324,8 @@ __device__ __forceinline__ void load_scales(const Params &p, uint8_t *sf_ring, u
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) mbar_arrive(&sf_full[r.slot]);
-            r.next(n_stages);
-            st.next(total, k_stages, roff, ioff, p.E, p.n_tiles);
+            r.next(n_stages, parts);
+            st.next(total, k_stages, roff, ioff, p.E, p.n_tiles, parts);
             if (ld.valid(total)) fetch(buf[d]);
         }
     }
@@ -546,107 +541,120 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t lim = p.wait_limit_ns;
 
     if (warp == kProducerWarp) {
-        if (lane == 0) {
+        const bool leader = elect_one();
+        if (leader) {
             tma_prefetch_map(&tm_w);
             tma_prefetch_map(&tm_a64);
             tma_prefetch_map(&tm_a16);
-            Cursor<S::NT> c;
-            c.start(total, roff, ioff, E, p.n_tiles);
-            Ring r;
-            uint32_t issued = 0;
-            bool ok = true;
-            while (c.valid(total)) {
-                ok = wait_bounded(&empty[r.slot], r.phase ^ 1u, abort_flag, p.status, lim);
+        }
+        const uint32_t a_base = smem_u32(smem), b_base = smem_u32(b_ring);
+        Ring r;
+        uint32_t issued = 0;
+        bool ok = true;
+        for (int j = blockIdx.x; ok && j < total; j += gridDim.x) {
+            const Item it = decode_item<S::NT>(j, roff, ioff, E, p.n_tiles);
+            // Token rows in 64-row boxes; a last part of at most 32 rows in 16-row
+            // boxes (rows past the chunk belong to the next one; their columns are
+            // not stored).
+            const int part = it.nt & 63;
+            const int n64 = (it.nt >> 6) + (part > 32), n16 = part > 32 ? 0 : part >> 4;
+            const uint32_t bytes = S::kABytes + (n64 * 64 + n16 * 16) * kStageBytesRow;
+            const int wrow = it.e * p.N + it.n0;
+            for (int ks = 0; ks < k_stages; ++ks) {
+                ok = warp_wait_bounded(&empty[r.slot], r.phase ^ 1u, abort_flag, p.status, lim);
                 if (!ok) break;
-                const uint32_t a_dst = smem_u32(smem + r.slot * S::kABytes);
-                const uint32_t b_dst = smem_u32(b_ring + r.slot * b_bytes);
-                // Token rows in 64-row boxes; a last part of at most 32 rows in
-                // 16-row boxes (rows past the chunk belong to the next one; their
-                // columns are not stored).
-                const int nt = c.it.nt;
-                const int part = nt & 63;
-                const int n64 = (nt >> 6) + (part > 32), n16 = part > 32 ? 0 : part >> 4;
-                mbar_arrive_expect_tx(&full[r.slot], S::kABytes + (n64 * 64 + n16 * 16) * kStageBytesRow);
-                const int x = c.ks * kStageBytesRow;
-                const int wrow = c.it.e * p.N + c.it.n0;
-                tma_load_2d(a_dst, &tm_w, x, wrow, &full[r.slot]);
-                if constexpr (kSwiglu)
-                    tma_load_2d(a_dst + kTileN * kStageBytesRow, &tm_w, x, wrow + p.I, &full[r.slot]);
-                for (int i = 0; i < n64; ++i)
-                    tma_load_2d(b_dst + i * 64 * kStageBytesRow, &tm_a64, x, c.it.row0 + i * 64, &full[r.slot]);
-                for (int i = 0; i < n16; ++i)
-                    tma_load_2d(b_dst + (n64 * 64 + i * 16) * kStageBytesRow, &tm_a16, x,
-                                c.it.row0 + n64 * 64 + i * 16, &full[r.slot]);
+                uint64_t *bar = &full[r.slot];
+                const uint32_t a_dst = a_base + r.slot * S::kABytes, b_dst = b_base + r.slot * b_bytes;
+                const int x = ks * kStageBytesRow;
+                if (leader) {
+                    mbar_arrive_expect_tx(bar, bytes);
+                    tma_load_2d(a_dst, &tm_w, x, wrow, bar);
+                    if constexpr (kSwiglu) tma_load_2d(a_dst + kTileN * kStageBytesRow, &tm_w, x, wrow + p.I, bar);
+                    for (int i = 0; i < n64; ++i)
+                        tma_load_2d(b_dst + i * 64 * kStageBytesRow, &tm_a64, x, it.row0 + i * 64, bar);
+                    for (int i = 0; i < n16; ++i)
+                        tma_load_2d(b_dst + (n64 * 64 + i * 16) * kStageBytesRow, &tm_a16, x,
+                                    it.row0 + n64 * 64 + i * 16, bar);
+                }
+                __syncwarp();
                 ++issued;
                 r.next(n_stages);
-                c.next(total, k_stages, roff, ioff, E, p.n_tiles);
             }
-            if (!ok) {   // drain: every issued copy must land before the CTA exits
-                for (uint32_t i = issued > n_stages ? issued - n_stages : 0; i < issued; ++i)
-                    wait_bounded(&full[i % n_stages], (i / n_stages) & 1u, nullptr, p.status, lim);
-            }
+        }
+        if (!ok && lane == 0) {   // drain: every issued copy must land before the CTA exits
+            for (uint32_t i = issued > n_stages ? issued - n_stages : 0; i < issued; ++i)
+                wait_bounded(&full[i % n_stages], (i / n_stages) & 1u, nullptr, p.status, lim);
         }
     } else if (warp == kIssuerWarp) {
-        if (lane == 0) {
-            Cursor<S::NT> c;
-            c.start(total, roff, ioff, E, p.n_tiles);
-            Ring r;
-            uint32_t buf = 0, acc_phase = 1, set = 0;
-            bool ok = true;
-            while (ok && c.valid(total)) {
-                if (c.ks == 0) {
-                    ok = wait_bounded(&acc_empty[buf], acc_phase, abort_flag, p.status, lim);
-                    if (!ok) break;
-                }
-                ok = wait_bounded(&full[r.slot], r.phase, abort_flag, p.status, lim) &&
-                     wait_bounded(&sf_full[r.slot], r.phase, abort_flag, p.status, lim);
+        // The whole warp runs the loop, so that addresses and descriptors stay in
+        // the warp-uniform registers the tcgen05 instructions take; one elected
+        // lane (always the same) issues.  A single-lane loop issued a stage in
+        // 1,600 cycles, four times what its MMAs take.
+        const bool leader = elect_one();
+        const uint32_t a_base = smem_u32(smem), b_base = smem_u32(b_ring), sf_base = smem_u32(sf_ring);
+        const int last_steps = (p.K - (k_stages - 1) * kStageK + 63) >> 6;
+        Ring r;
+        uint32_t buf = 0, acc_phase = 1, set = 0;
+        bool ok = true;
+        for (int j = blockIdx.x; ok && j < total; j += gridDim.x) {
+            const Item it = decode_item<S::NT>(j, roff, ioff, E, p.n_tiles);
+            const uint32_t id0 = idesc_fp4<kNv>(it.nt, 0), id2 = idesc_fp4<kNv>(it.nt, kNv ? 0 : 2);
+            const bool two = S::NA == 2 && it.nt > 128;
+            const uint32_t d = tmem + buf * kAccCols;
+            ok = warp_wait_bounded(&acc_empty[buf], acc_phase, abort_flag, p.status, lim);
+            for (int ks = 0; ok && ks < k_stages; ++ks) {
+                ok = warp_wait_bounded(&full[r.slot], r.phase, abort_flag, p.status, lim) &&
+                     warp_wait_bounded(&sf_full[r.slot], r.phase, abort_flag, p.status, lim);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t sf_s = smem_u32(sf_ring + r.slot * S::kSfBytes);
+                const uint32_t sf_s = sf_base + r.slot * S::kSfBytes;
                 const uint32_t sfa = tmem + kSfCol0 + set * kSfSetCols;
                 const uint32_t sfb = sfa + S::MT * S::W * 4;
+                const uint64_t a_desc = smem_desc_sw128(a_base + r.slot * S::kABytes);
+                const uint64_t b_desc = smem_desc_sw128(b_base + r.slot * b_bytes);
+                const int steps = ks == k_stages - 1 ? last_steps : 4;
+                if (leader) {
 #pragma unroll
-                for (int i = 0; i < S::MT * S::W; ++i) copy_atom(sfa + 4 * i, sf_s + i * kAtomBytes);
+                    for (int i = 0; i < S::MT * S::W; ++i) copy_atom(sfa + 4 * i, sf_s + i * kAtomBytes);
 #pragma unroll
-                for (int i = 0; i < S::W; ++i)
+                    for (int i = 0; i < S::W * S::NA; ++i)
+                        if (i % S::NA == 0 || two)
+                            copy_atom(sfb + 4 * i, sf_s + S::kSfaBytes + i * kAtomBytes);
 #pragma unroll
-                    for (int a = 0; a < S::NA; ++a)
-                        if (a == 0 || c.it.nt > 128)
-                            copy_atom(sfb + 4 * (i * S::NA + a),
-                                      sf_s + S::kSfaBytes + (i * S::NA + a) * kAtomBytes);
-                const uint64_t a_desc = smem_desc_sw128(smem_u32(smem + r.slot * S::kABytes));
-                const uint64_t b_desc = smem_desc_sw128(smem_u32(b_ring + r.slot * b_bytes));
-                const uint32_t d = tmem + buf * kAccCols;
-                const int steps = min(4, (p.K - c.ks * kStageK + 63) >> 6);
-                for (int j = 0; j < steps; ++j) {
-                    const int word = kNv ? j : j >> 1;
-                    const uint32_t id = idesc_fp4<kNv>(c.it.nt, kNv ? 0u : 2u * (j & 1));
-                    // 64 k are 32 bytes of the swizzled row: 2 in descriptor units
+                    for (int t = 0; t < 4; ++t) {
+                        if (t >= steps) break;
+                        const int word = kNv ? t : t >> 1;
+                        // 64 k are 32 bytes of the swizzled row: 2 in descriptor units
 #pragma unroll
-                    for (int m = 0; m < S::MT; ++m)
-                        mma_fp4<kNv>(d + m * S::kAccStep,
-                                     a_desc + 2 * j + m * (kTileN * kStageBytesRow >> 4), b_desc + 2 * j, id,
-                                     sfa + 4 * (m * S::W + word), sfb + 4 * word * S::NA,
-                                     (c.ks | j) != 0);
+                        for (int m = 0; m < S::MT; ++m)
+                            mma_fp4<kNv>(d + m * S::kAccStep, a_desc + 2 * t + m * (kTileN * kStageBytesRow >> 4),
+                                         b_desc + 2 * t, t & 1 ? id2 : id0, sfa + 4 * (m * S::W + word),
+                                         sfb + 4 * word * S::NA, (ks | t) != 0);
+                    }
+                    mma_commit(&empty[r.slot]);
+                    if (ks == k_stages - 1) mma_commit(&acc_full[buf]);
                 }
-                mma_commit(&empty[r.slot]);
-                if (c.ks == k_stages - 1) {
-                    mma_commit(&acc_full[buf]);
-                    buf ^= 1u;
-                    if (buf == 0) acc_phase ^= 1u;
-                }
+                __syncwarp();
                 set ^= 1u;
                 r.next(n_stages);
-                c.next(total, k_stages, roff, ioff, E, p.n_tiles);
             }
-            // Every MMA and commit of this thread done before the CTA leaves.
-            mma_commit(final_bar);
-            wait_bounded(final_bar, 0, nullptr, p.status, lim);
+            buf ^= 1u;
+            if (buf == 0) acc_phase ^= 1u;
         }
-    } else if (warp == kWScaleWarp) {
-        load_scales<kNv, kSwiglu, true>(p, sf_ring, n_stages, total, roff, ioff, sf_full, empty, abort_flag);
-    } else if (warp == kAScaleWarp) {
-        load_scales<kNv, kSwiglu, false>(p, sf_ring, n_stages, total, roff, ioff, sf_full, empty, abort_flag);
+        // Every MMA and commit of the warp done before the CTA leaves.
+        if (leader) mma_commit(final_bar);
+        __syncwarp();
+        warp_wait_bounded(final_bar, 0, nullptr, p.status, lim);
+    } else if (warp < kAScaleWarp) {
+        const int parts = min(kLoaders, static_cast<int>(n_stages)), part = warp - kWScaleWarp;
+        if (part < parts)
+            load_scales<kNv, kSwiglu, true>(p, sf_ring, n_stages, total, roff, ioff, sf_full, empty, abort_flag, part,
+                                            parts);
+    } else if (warp < kEpilogueWarp) {
+        const int parts = min(kLoaders, static_cast<int>(n_stages)), part = warp - kAScaleWarp;
+        if (part < parts)
+            load_scales<kNv, kSwiglu, false>(p, sf_ring, n_stages, total, roff, ioff, sf_full, empty, abort_flag, part,
+                                             parts);
     } else {
         const int quarter = warp & 3;
         const float a2 = kNv ? __ldg(p.a_scale_2) : 1.0f;

@@ -259,7 +259,7 @@ def check_product(B, rng, fmt, sizes, K, N, out_dtype=torch.float32, wide=False,
 SIZES = [
     ([1], 32, 1), ([5], 64, 130), ([0, 3, 0], 96, 128), ([17, 1, 0, 40], 256, 129),
     ([16, 33, 65], 512, 384), ([129, 0, 193, 385], 288, 200), ([192, 191, 1], 1056, 260),
-    ([700], 768, 136), ([2] * 40 + [0] * 5 + [90], 512, 256), ([1], 8192, 256),
+    ([700], 768, 136), ([192, 400], 4096, 128), ([2] * 40 + [0] * 5 + [90], 512, 256), ([1], 8192, 256),
 ]
 
 
@@ -374,7 +374,7 @@ def swiglu_reference(a, w, I, s):
 
 @pytest.mark.parametrize("fmt", [MX, NV], ids=["mx", "nv"])
 @pytest.mark.parametrize("sizes,K,I", [([1], 32, 32), ([5, 0, 3], 96, 160), ([97, 16, 200], 512, 128),
-                                       ([33, 64], 1056, 416), ([2] * 30, 256, 256)])
+                                       ([33, 64], 1056, 416), ([2] * 30, 256, 256), ([96, 200], 4096, 64)])
 def test_swiglu_product_quantises_h(B, fmt, sizes, K, I):
     rng = np.random.default_rng(K + I + fmt)
     E, rows, blk = len(sizes), sum(sizes), BLOCK[fmt]
