@@ -89,9 +89,12 @@ moe_status check_fp4_gemm_args(const uint8_t *act_codes, const uint8_t *act_scal
                                const float *weight_scale_2, int format, const int32_t *group_sizes, int32_t E,
                                int64_t N, const void *workspace, size_t workspace_bytes) {
     if (format != MOE_FP4_MX && format != MOE_FP4_NV) return MOE_ERR_INVALID_ARG;
-    if (rows < 0 || rows > INT32_MAX || K <= 0 || K % 32 != 0 || N <= 0 || E <= 0 || E > kMaxE)
+    // A tile may start its loads up to 256 rows past the last row (they read as
+    // zeros): its coordinates stay 32-bit.
+    constexpr int64_t kMaxRows = INT32_MAX - 512;
+    if (rows < 0 || rows > kMaxRows || K <= 0 || K % 32 != 0 || N <= 0 || E <= 0 || E > kMaxE)
         return MOE_ERR_INVALID_ARG;
-    if (static_cast<int64_t>(E) * N > INT32_MAX) return MOE_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(E) * N > kMaxRows) return MOE_ERR_INVALID_ARG;
     if (!codes || !scales || !group_sizes || !workspace || workspace_bytes < kStatusBytes)
         return MOE_ERR_INVALID_ARG;
     if (rows > 0 && (!act_codes || !act_scales)) return MOE_ERR_INVALID_ARG;

@@ -13,13 +13,14 @@
 //    row wastes no weight traffic.
 //  * One K stage is 256 k: 128 bytes a row, the 128-byte swizzle TMA writes and
 //    the MMA reads; four MMAs of 64 k.
-//  * Block scales have to sit in tensor memory as 32-lane atoms (word of row m
-//    at lane m % 32, column m / 32; a word holds four consecutive scales).
-//    Two loader warps fetch the scale bytes row by row with a register prefetch
-//    of kPrefetch stages, write the atoms to shared memory (a 4 x 4 word
-//    transpose per lane, one 16-byte store), and the issuer copies them with
-//    tcgen05.cp in front of the stage's MMAs.  So scales keep the layout the
-//    rest of the library uses, and tokens may start at any row.
+//  * Block scales have to sit in tensor memory (word of row m at lane m % 32 of
+//    all four lane quarters, column m / 32; a word holds four consecutive
+//    scales).  Two warps copy the scale bytes row by row into a staging area
+//    (cp.async, several stages ahead), and four converter warps, one a lane
+//    quarter, read them back and write them with tcgen05.st.  So scales keep the
+//    layout the rest of the library uses, and tokens may start at any row.  The
+//    other way, atoms in shared memory and tcgen05.cp, cost the tensor pipe about
+//    66 cycles a copy: 600 (MXFP4) to 1,000 (NVFP4) cycles a stage, for 384 of MMA.
 //  * Accumulators are double-buffered (2 x 192 columns): the epilogue warps of
 //    one item run under the next item's MMAs.  A band's rows are cut into equal
 //    chunks of at most 192 (96 with SwiGLU) tokens, multiples of 16.
@@ -42,36 +43,45 @@
 #include "device_common.cuh"
 #include "fp4_common.cuh"
 #include "launch.h"
+#include "vec_io.cuh"
 
 namespace moe {
 namespace fp4 {
 
 constexpr int kProducerWarp = 0, kIssuerWarp = 1;
-constexpr int kLoaders = 4;                    // scale-loader warps an operand, on stages in turn
-constexpr int kWScaleWarp = 2, kAScaleWarp = kWScaleWarp + kLoaders;
-constexpr int kEpilogueWarp = kAScaleWarp + kLoaders;
+constexpr int kWCopyWarp = 2, kACopyWarp = 3;          // scale bytes of weights, of tokens
+constexpr int kConvertWarp = 4, kEpilogueWarp = 8;     // four warps each: one a lane quarter
 constexpr int kThreads = 32 * (kEpilogueWarp + 4);
 constexpr int kMaxE = 1024;
 constexpr int kTileN = 128;                    // weight rows a tile (MMA M)
 constexpr int kStageBytesRow = 128;            // 256 k
 constexpr int kStageK = 256;
 constexpr int kMaxStages = 12;
-constexpr int kPrefetch = 2;                   // stages of scale bytes a loader holds in registers
+constexpr int kDepth = 4;                      // scale groups in the staging area
 constexpr int kAccCols = 192;                  // columns of one accumulator buffer
-constexpr int kSfCol0 = 2 * kAccCols;          // scale atoms, two sets of 64 columns
-constexpr int kSfSetCols = 64;
+constexpr int kSfCol0 = 2 * kAccCols;          // scale columns after the accumulators
 constexpr int kTmemCols = 512;
-constexpr int kAtomBytes = 512;
 
-constexpr int kRingBytes = 208 * 1024;
-constexpr int kOffRow = kRingBytes;
+constexpr int kRingBytes = 192 * 1024;
+constexpr int kOffStaging = kRingBytes;        // scale bytes on their way to atoms
+constexpr int kStagingBytes = kDepth * 11 * 512;
+constexpr int kOffRow = kOffStaging + kStagingBytes;
 constexpr int kOffItem = kOffRow + (kMaxE + 1) * 4;
 constexpr int kOffBars = (kOffItem + (kMaxE + 1) * 4 + 7) & ~7;
-constexpr int kNumBars = 3 * kMaxStages + 4 + 1;
+constexpr int kNumBars = 2 * kMaxStages + 2 * 5 + 4 + 1 + 4 * kDepth;
 constexpr int kOffMisc = kOffBars + kNumBars * 8;
 constexpr int kSmemBytes = kOffMisc + 64 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
-static_assert(kSfCol0 + 2 * kSfSetCols <= kTmemCols, "tensor memory budget");
+
+// Scale columns of a stage, and the stages they are kept for: every shape here has 12
+// columns a scale word (384 rows of 32-row columns over both operands).
+template <bool kNv>
+struct ScaleCols {
+    static constexpr int W = kNv ? 4 : 2;                  // scale words a row and stage
+    static constexpr int kCols = 12 * W;
+    static constexpr int kSlots = (kTmemCols - kSfCol0) / kCols;   // 5 or 2
+};
+constexpr int kMaxSfSlots = 5;
 
 struct Params {
     const uint8_t *w_scales, *a_scales;
@@ -85,7 +95,7 @@ struct Params {
     int out_bf16;
     int n_tiles;
     int scale_row;           // scale bytes a row of K: K / 32 or K / 16
-    int w_vec, a_vec;        // a stage's scale bytes of a row load as one aligned vector
+    int w_vec, a_vec;        // scale bytes that load at once (see load_words)
     uint64_t wait_limit_ns;
 };
 
@@ -95,12 +105,10 @@ struct Shape {
     static constexpr int NT = kSwiglu ? 96 : 192;          // tokens an item, at most
     static constexpr int W = kNv ? 4 : 2;                  // scale words a row and stage
     static constexpr int NA = kSwiglu ? 1 : 2;             // token atoms of 128 rows
-    static constexpr int AR = NT / 32;                     // token rows a lane of the scale loader
+    static constexpr int AR = NT / 32;                     // token rows a lane of the scale copier
     static constexpr int kABytes = MT * kTileN * kStageBytesRow;
-    static constexpr int kSfaBytes = MT * W * kAtomBytes;
-    static constexpr int kSfBytes = kSfaBytes + NA * W * kAtomBytes;
     static constexpr int kAccStep = kSwiglu ? 96 : 0;      // columns from the gate to the up sums
-    static_assert(kSfBytes / kAtomBytes * 4 <= kSfSetCols, "scale columns of one stage");
+    static_assert(kDepth * (4 * MT + AR) * 512 <= kStagingBytes, "scale staging");
 };
 
 // ------------------------------------------------------- block-scaled MMA
@@ -135,14 +143,22 @@ __device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint
             : "memory");
 }
 
-// One 512-byte scale atom (32 rows of 16 bytes, contiguous) from shared memory
-// to 4 tensor-memory columns, the same 32 lanes for all four lane quarters.
-__device__ __forceinline__ void copy_atom(uint32_t taddr, uint32_t saddr) {
-    uint64_t d = (saddr & 0x3FFFFu) >> 4;
-    d |= static_cast<uint64_t>(16u >> 4) << 16;
-    d |= static_cast<uint64_t>(128u >> 4) << 32;   // 8-row groups 128 bytes apart, no swizzle
-    d |= 1ull << 46;
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+// ------------------------------------------------------------------ waits
+
+// The roles' loops share the SM's instruction caches: with every wait, item decode
+// and alignment case inlined, a third of all stalls were instruction fetches.  So
+// what a loop does not run every time is out of line.
+
+__device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *status,
+                                       uint64_t lim) {
+    return warp_wait_bounded(bar, parity, abort_flag, status, lim);
+}
+
+// warp_wait_bounded with its slow path out of line.
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *status,
+                                     uint64_t lim) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    return wait_slow(bar, parity, abort_flag, status, lim);
 }
 
 // ------------------------------------------------------------------ items
@@ -158,8 +174,8 @@ __device__ __forceinline__ int chunk_rows(int n, int most) {
     return ((n + nch - 1) / nch + 15) & ~15;
 }
 
-template <int kMost>
-__device__ __forceinline__ Item decode_item(int j, const int *roff, const int *ioff, int E, int n_tiles) {
+template <int kMost, int kTile>
+__device__ __noinline__ Item decode_item(int j, const int *roff, const int *ioff, int E, int n_tiles) {
     int lo = 0, hi = E - 1;   // last e with ioff[e] <= j (its band is non-empty)
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -171,7 +187,7 @@ __device__ __forceinline__ Item decode_item(int j, const int *roff, const int *i
     const int cr = chunk_rows(n, kMost);
     const int r = j - ioff[lo];
     const int ch = r / n_tiles;
-    it.n0 = (r - ch * n_tiles) * kTileN;
+    it.n0 = (r - ch * n_tiles) * kTile;
     const int t0 = ch * cr;
     it.nvalid = min(cr, n - t0);
     it.nt = (it.nvalid + 15) & ~15;
@@ -187,50 +203,38 @@ struct Ring {
     }
 };
 
-// Items of this CTA times stages, in order.
-template <int kMost>
-struct Cursor {
-    int j, ks;
-    Item it;
-    __device__ __forceinline__ bool valid(int total) const { return j < total; }
-    __device__ __forceinline__ void start(int total, const int *roff, const int *ioff, int E, int n_tiles) {
-        j = blockIdx.x;
-        ks = 0;
-        if (j < total) it = decode_item<kMost>(j, roff, ioff, E, n_tiles);
-    }
-    __device__ __forceinline__ void next(int total, int k_stages, const int *roff, const int *ioff, int E,
-                                         int n_tiles, int by = 1) {
-        ks += by;
-        if (ks < k_stages) return;
-        for (; ks >= k_stages; ks -= k_stages) j += gridDim.x;
-        if (j < total) it = decode_item<kMost>(j, roff, ioff, E, n_tiles);
-    }
-};
-
 // ---------------------------------------------------------- scale loaders
 
-// The W scale words of one row and stage: bytes [first, first + 4 W) of a row of
-// `scale_row` bytes, zeros past its end (2^-127 or 0: finite, times zero codes).
-template <int W>
-__device__ __forceinline__ void load_words(const uint8_t *row, int first, int scale_row, int vec,
-                                           uint32_t (&w)[W]) {
-    if (vec) {
-        if constexpr (W == 2) {
-            const uint2 v = __ldg(reinterpret_cast<const uint2 *>(row + first));
-            w[0] = v.x; w[1] = v.y;
-        } else {
-            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(row + first));
-            w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+// Copy of 16 scale bytes [at, at + 16) of one row into shared memory where rows do
+// not load as 16-byte vectors; zeros past the row's end (2^-127 or 0: finite, and
+// they meet zero codes).  `vec`: bytes that load at once (8, 4 or 1; it divides the
+// row and the base address); 8 and 4 are asynchronous.
+__device__ __noinline__ void copy_words(uint8_t *dst, const uint8_t *row, int at, int scale_row, int vec) {
+    const uint32_t sd = smem_u32(dst);
+    if (vec == 8) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const bool in = at + 8 * i < scale_row;
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(sd + 8 * i),
+                         "l"(in ? row + at + 8 * i : row), "r"(in ? 8 : 0)
+                         : "memory");
         }
-        return;
-    }
+    } else if (vec == 4) {
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
-        w[i] = 0;
+        for (int i = 0; i < 4; ++i) {
+            const bool in = at + 4 * i < scale_row;
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(sd + 4 * i),
+                         "l"(in ? row + at + 4 * i : row), "r"(in ? 4 : 0)
+                         : "memory");
+        }
+    } else {
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+            uint32_t w = 0;
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            const int k = first + 4 * i + b;
-            if (k < scale_row) w[i] |= static_cast<uint32_t>(__ldg(row + k)) << (8 * b);
+            for (int b = 0; b < 4; ++b)
+                if (at + 4 * i + b < scale_row) w |= static_cast<uint32_t>(__ldg(row + at + 4 * i + b)) << (8 * b);
+            *reinterpret_cast<uint32_t *>(dst + 4 * i) = w;
         }
     }
 }
@@ -238,95 +242,193 @@ __device__ __forceinline__ void load_words(const uint8_t *row, int first, int sc
 // A byte the format does not allow: E8M0 255; E4M3 NaN or a set sign bit (the
 // block-scaled MMA takes unsigned scales).
 template <bool kNv>
-__device__ __forceinline__ bool bad_word(uint32_t w) {
-    if constexpr (kNv) return ((w & 0x80808080u) | __vcmpeq4(w, 0x7F7F7F7Fu)) != 0;
-    else return __vcmpeq4(w, 0xFFFFFFFFu) != 0;
+__device__ __forceinline__ uint32_t bad_bits(uint32_t w) {
+    const uint32_t x = kNv ? w ^ 0x7F7F7F7Fu : ~w;               // a byte 0 where w has the NaN byte
+    const uint32_t zero = (x - 0x01010101u) & ~x & 0x80808080u;  // nonzero if and only if there is one
+    return kNv ? zero | (w & 0x80808080u) : zero;
 }
 
-// Body of scale-loader warp `part` of `parts`, which takes every parts-th stage.
-// parts <= n_stages: a loader that waits for the slot of stage s has seen stage s -
-// parts - n_stages consumed, so the slot's barrier is at most one phase behind and
-// its parity is unambiguous.  kWeights: the weight tiles' scales (4 MT rows
-// a lane), else the tokens' (AR rows a lane).
-template <bool kNv, bool kSwiglu, bool kWeights>
-__device__ __forceinline__ void load_scales(const Params &p, uint8_t *sf_ring, uint32_t n_stages, int total,
-                                            const int *roff, const int *ioff, uint64_t *sf_full,
-                                            uint64_t *empty, volatile int *abort_flag, int part, int parts) {
-    using S = Shape<kNv, kSwiglu>;
-    constexpr int R = kWeights ? 4 * S::MT : S::AR;
-    constexpr int W = S::W;
+// Staging of one operand's scale bytes: kDepth groups of 16 bytes a row (two stages
+// of MXFP4, one of NVFP4), R rows a lane (row lane + 32 q of the tile).
+struct Staging {
+    uint8_t *bytes;                   // kDepth * R * 512
+    uint64_t *full, *empty;           // one a group: copier -> converters -> copier
+};
+
+// What the scale warps need of their kernel.
+struct ScaleEnv {
+    const Params *p;
+    const int *roff, *ioff;
+    volatile int *abort_flag;
+    int first, step, total;           // the items: first, first + step, ... < total
+};
+
+// Copier warp.  The copies have a warp of their own so that nothing the converters
+// wait for or fence waits for copies of later stages.
+//
+// row(item, q): row of this lane, clamped to the tile's or the chunk's last row past
+// its end (those sums are never stored); groups of 32 rows from rows(item) on are
+// skipped.
+template <int R, int kMost, int kTile, class RowFn, class RowsFn>
+__device__ __forceinline__ void copy_scales(const ScaleEnv &v, const Staging &g, const uint8_t *base, int vec,
+                                            RowFn row, RowsFn rows) {
+    const Params &p = *v.p;
+    const int lane = threadIdx.x & 31;
+    const int pieces = (p.scale_row + 15) / 16;
+    Ring r;
+    bool ok = true;
+    for (int j = v.first; ok && j < v.total; j += v.step) {
+        const Item it = decode_item<kMost, kTile>(j, v.roff, v.ioff, p.E, p.n_tiles);
+        const int n = rows(it);
+        const uint8_t *src[R];
+#pragma unroll
+        for (int q = 0; q < R; ++q) src[q] = base + (q < n ? row(it, q) : 0) * p.scale_row;
+        for (int i = 0; i < pieces; ++i) {
+            ok = wait(&g.empty[r.slot], r.phase ^ 1u, v.abort_flag, p.status, p.wait_limit_ns);
+            if (!ok) break;
+            uint8_t *dst = g.bytes + r.slot * (R * 512) + lane * 16;
+            if (vec == 16) {
+                const uint32_t sd = smem_u32(dst);
+#pragma unroll
+                for (int q = 0; q < R; ++q)
+                    if (q < n)
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(sd + q * 512),
+                                     "l"(src[q] + i * 16)
+                                     : "memory");
+            } else {
+#pragma unroll 1
+                for (int q = 0; q < n; ++q)
+                    copy_words(dst + q * 512, base + row(it, q) * p.scale_row, i * 16, p.scale_row, vec);
+            }
+            if (vec == 1)
+                mbar_arrive(&g.full[r.slot]);
+            else
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(&g.full[r.slot]))
+                             : "memory");
+            __syncwarp();
+            r.next(kDepth);
+        }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");   // none in flight when the CTA leaves
+}
+
+// 4, 8, 16 or 32 consecutive columns of each lane's own tensor-memory lane.
+template <int C>
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&v)[C]) {
+    if constexpr (C == 32) {
+        tmem_st32(taddr, v);
+    } else if constexpr (C == 16) {
+        tmem_st16(taddr, v);
+    } else if constexpr (C == 8) {
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
+                     "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                     : "memory");
+    }
+}
+
+// One staged group of an operand in registers: scale word i of row lane + 32 q in
+// w[q][i].  Rows nothing was copied for (q with used(q) false) read as zeros.
+template <int R, class Used>
+__device__ __forceinline__ void read_group(const uint8_t *group, uint32_t (&w)[R][4], Used used) {
+    const uint8_t *mine = group + (threadIdx.x & 31) * 16;
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (used(q)) x = *reinterpret_cast<const uint4 *>(mine + q * 512);
+        w[q][0] = x.x; w[q][1] = x.y; w[q][2] = x.z; w[q][3] = x.w;
+    }
+}
+
+template <bool kNv, int R>
+__device__ __forceinline__ uint32_t bad_group(const uint32_t (&w)[R][4]) {
+    uint32_t bad = 0;
+#pragma unroll
+    for (int q = 0; q < R; ++q)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) bad |= bad_bits<kNv>(w[q][i]);
+    return bad;
+}
+
+// Scale columns of stage s of a group.  kByTile: (tile of 128 rows, word, column),
+// else (word, tile, column).
+template <bool kNv, int R, bool kByTile>
+__device__ __forceinline__ void store_columns(uint32_t taddr, const uint32_t (&w)[R][4], int s) {
+    constexpr int W = kNv ? 4 : 2, T = (R + 3) / 4, C = 4 * T * W;
+    uint32_t v[C];
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int q = 4 * t + c;
+                const uint32_t a = q < R ? w[q < R ? q : 0][i] : 0u;
+                const uint32_t b = !kNv && q < R ? w[q < R ? q : 0][!kNv ? 2 + i : i] : a;
+                v[(kByTile ? t * W + i : i * T + t) * 4 + c] = s ? b : a;
+            }
+    tmem_st<C>(taddr, v);
+}
+
+__device__ __forceinline__ void init_scale_bars(uint64_t *sf_full, uint64_t *sf_empty, uint64_t *raw_bars) {
+    for (int i = 0; i < kMaxSfSlots; ++i) {
+        mbar_init(&sf_full[i], 4);
+        mbar_init(&sf_empty[i], 1);
+    }
+    for (int d = 0; d < kDepth; ++d) {
+        mbar_init(&raw_bars[d], 32);                  // weights: the copier's lanes
+        mbar_init(&raw_bars[kDepth + d], 4);          // the converter warps
+        mbar_init(&raw_bars[2 * kDepth + d], 32);     // tokens
+        mbar_init(&raw_bars[3 * kDepth + d], 4);
+    }
+}
+
+// Converter warp: staged bytes of both operands -> scale columns in tensor memory,
+// ring of kSlots stages.  A: the MMA's A operand (kByTile), B: its B operand.
+template <bool kNv, int RA, int RB, int kMost, int kTile, class RowsA, class RowsB>
+__device__ __forceinline__ void convert_scales(const ScaleEnv &v, const Staging &a, const Staging &b, uint32_t sf_tmem,
+                                               uint64_t *sf_full, uint64_t *sf_empty, RowsA rows_a, RowsB rows_b) {
+    using C = ScaleCols<kNv>;
+    constexpr int G = 4 / C::W, kACols = 4 * ((RA + 3) / 4) * C::W;
+    static_assert(kACols + 4 * ((RB + 3) / 4) * C::W == C::kCols, "scale columns of a stage");
+    const Params &p = *v.p;
     const int lane = threadIdx.x & 31;
     const int k_stages = (p.K + kStageK - 1) / kStageK;
-    const int vec = kWeights ? p.w_vec : p.a_vec;
-    uint32_t buf[kPrefetch][R][W] = {};
-    bool bad = false;
-    Cursor<S::NT> ld, st;
-    ld.start(total, roff, ioff, p.E, p.n_tiles);
-    if (part) ld.next(total, k_stages, roff, ioff, p.E, p.n_tiles, part);
-    st = ld;
-
-    auto fetch = [&](uint32_t (&b)[R][W]) {
-        const int first = ld.ks * 4 * W;
-#pragma unroll
-        for (int q = 0; q < R; ++q) {
-            // Rows past the tile's or the chunk's end read its last row again
-            // (their sums are never stored): nothing here waits for the load.
-            int64_t row;
-            if constexpr (kWeights) {
-                const int cols = kSwiglu ? p.I : p.N;
-                row = static_cast<int64_t>(ld.it.e) * p.N + (q >= 4 ? p.I : 0) +
-                      min(ld.it.n0 + lane + 32 * (q & 3), cols - 1);
-            } else {
-                if (32 * q >= ld.it.nt) continue;
-                row = ld.it.row0 + min(lane + 32 * q, ld.it.nvalid - 1);
-            }
-            load_words<W>((kWeights ? p.w_scales : p.a_scales) + row * p.scale_row, first, p.scale_row, vec,
-                          b[q]);
-        }
-        ld.next(total, k_stages, roff, ioff, p.E, p.n_tiles, parts);
-    };
-
-#pragma unroll
-    for (int d = 0; d < kPrefetch; ++d)
-        if (ld.valid(total)) fetch(buf[d]);
-
-    Ring r;
-    if (part) r.next(n_stages, part);
+    uint32_t bad = 0;
     bool ok = true;
-    while (ok && st.valid(total)) {
-#pragma unroll
-        for (int d = 0; d < kPrefetch; ++d) {
-            if (!ok || !st.valid(total)) break;
-            ok = warp_wait_bounded(&empty[r.slot], r.phase ^ 1u, abort_flag, p.status, p.wait_limit_ns);
+    const bool checks = (threadIdx.x >> 5) == kConvertWarp;    // the four read the same bytes
+    Ring sf, raw;
+    for (int j = v.first; ok && j < v.total; j += v.step) {
+        const Item it = decode_item<kMost, kTile>(j, v.roff, v.ioff, p.E, p.n_tiles);
+        const int qa = rows_a(it), qb = rows_b(it);
+        for (int ks = 0; ok && ks < k_stages; ks += G) {
+            ok = wait(&a.full[raw.slot], raw.phase, v.abort_flag, p.status, p.wait_limit_ns) &&
+                 wait(&b.full[raw.slot], raw.phase, v.abort_flag, p.status, p.wait_limit_ns);
             if (!ok) break;
-            uint8_t *dst = sf_ring + r.slot * S::kSfBytes + (kWeights ? 0 : S::kSfaBytes) + lane * 16;
-#pragma unroll
-            for (int q = 0; q < R; ++q) {
-                if (!kWeights && 32 * q >= st.it.nt) continue;
-#pragma unroll
-                for (int i = 0; i < W; ++i) bad |= bad_word<kNv>(buf[d][q][i]);
-            }
-            constexpr int ATOMS = (R + 3) / 4;
-#pragma unroll
-            for (int a = 0; a < ATOMS; ++a)
-#pragma unroll
-                for (int i = 0; i < W; ++i) {
-                    uint4 v;
-                    v.x = buf[d][4 * a][i];
-                    v.y = 4 * a + 1 < R ? buf[d][4 * a + 1 < R ? 4 * a + 1 : 0][i] : 0u;
-                    v.z = 4 * a + 2 < R ? buf[d][4 * a + 2 < R ? 4 * a + 2 : 0][i] : 0u;
-                    v.w = 4 * a + 3 < R ? buf[d][4 * a + 3 < R ? 4 * a + 3 : 0][i] : 0u;
-                    // weights: atom (tile, word); tokens: atoms of one word adjacent
-                    const int atom = kWeights ? a * W + i : i * S::NA + a;
-                    *reinterpret_cast<uint4 *>(dst + atom * kAtomBytes) = v;
-                }
-            // The atoms are read by tcgen05.cp (the async proxy).
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            uint32_t wa[RA][4], wb[RB][4];
+            read_group(a.bytes + raw.slot * (RA * 512), wa, [&](int q) { return q < qa; });
+            read_group(b.bytes + raw.slot * (RB * 512), wb, [&](int q) { return q < qb; });
+            if (checks) bad |= bad_group<kNv>(wa) | bad_group<kNv>(wb);
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sf_full[r.slot]);
-            r.next(n_stages, parts);
-            st.next(total, k_stages, roff, ioff, p.E, p.n_tiles, parts);
-            if (ld.valid(total)) fetch(buf[d]);
+            if (lane == 0) {
+                mbar_arrive(&a.empty[raw.slot]);
+                mbar_arrive(&b.empty[raw.slot]);
+            }
+            raw.next(kDepth);
+#pragma unroll
+            for (int s = 0; s < G; ++s) {
+                if (!ok || ks + s >= k_stages) break;
+                ok = wait(&sf_empty[sf.slot], sf.phase ^ 1u, v.abort_flag, p.status, p.wait_limit_ns);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t at = sf_tmem + sf.slot * C::kCols;
+                store_columns<kNv, RA, true>(at, wa, s);
+                store_columns<kNv, RB, false>(at + kACols, wb, s);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sf_full[sf.slot]);
+                sf.next(C::kSlots);
+            }
         }
     }
     if (bad) set_status(p.status, MOE_ERR_DATA);
@@ -346,12 +448,12 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&v)[8]) {
 __device__ __forceinline__ void store_plain(const Params &p, const Item &it, uint32_t acc, int n, float scale,
                                             uint64_t *acc_empty) {
     const int lane = threadIdx.x & 31;
-    for (int c = 0; c < it.nt; c += 16) {
+    for (int c = 0; c < it.nvalid; c += 16) {
         uint32_t v[16];
         __syncwarp();
         tmem_ld16(acc + c, v);
         tmem_ld_wait();
-        if (c + 16 >= it.nt) {      // the sums are in registers: release the buffer
+        if (c + 16 >= it.nvalid) {      // the sums are in registers: release the buffer
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(acc_empty);
@@ -382,13 +484,13 @@ __device__ __forceinline__ void store_swiglu(const Params &p, const Item &it, ui
     const int lane = threadIdx.x & 31;
     const int t8 = lane & 7, q = lane >> 3;
     const float g6 = 6.0f * h_scale;
-    for (int c = 0; c < it.nt; c += 8) {
+    for (int c = 0; c < it.nvalid; c += 8) {
         uint32_t g[8], u[8];
         __syncwarp();
         tmem_ld8(acc + c, g);
         tmem_ld8(acc + Shape<kNv, true>::kAccStep + c, u);
         tmem_ld_wait();
-        if (c + 8 >= it.nt) {
+        if (c + 8 >= it.nvalid) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(acc_empty);
@@ -438,37 +540,14 @@ __device__ __forceinline__ void store_swiglu(const Params &p, const Item &it, ui
     }
 }
 
-// ------------------------------------------------------------------ kernel
-
-template <bool kNv, bool kSwiglu>
-__global__ void __launch_bounds__(kThreads, 1)
-    fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a64,
-                    const __grid_constant__ CUtensorMap tm_a16, const Params p) {
-    using S = Shape<kNv, kSwiglu>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    int *roff = reinterpret_cast<int *>(smem + kOffRow);
-    int *ioff = reinterpret_cast<int *>(smem + kOffItem);
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kOffBars);   // TMA -> issuer
-    uint64_t *sf_full = full + kMaxStages;                            // scale loaders -> issuer
-    uint64_t *empty = sf_full + kMaxStages;                           // MMA commit -> loaders
-    uint64_t *acc_full = empty + kMaxStages;                          // MMA commit -> epilogue
-    uint64_t *acc_empty = acc_full + 2;                               // epilogue -> issuer
-    uint64_t *final_bar = acc_empty + 2;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kOffMisc);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kOffMisc + 8);
-    int *bad_flag = reinterpret_cast<int *>(smem + kOffMisc + 16);
-    int *nt_slot = reinterpret_cast<int *>(smem + kOffMisc + 24);
-
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int E = p.E;
-
-    // Row and item offsets from the group sizes (64-bit sums: sizes that wrap 32
-    // bits are caught).
-    for (int e = tid; e < E; e += kThreads) roff[e] = __ldg(p.group_sizes + e);
-    if (tid == 0) *abort_flag = 0;
+// Row and item offsets from the group sizes (64-bit sums: sizes that wrap 32 bits
+// are caught), and the widest chunk.  False (recorded): the sizes do not add up.
+template <int kMost>
+__device__ __forceinline__ bool build_items(const Params &p, int *roff, int *ioff, int *bad_flag, int *nt_slot) {
+    const int tid = threadIdx.x, lane = tid & 31, E = p.E;
+    for (int e = tid; e < E; e += blockDim.x) roff[e] = __ldg(p.group_sizes + e);
     __syncthreads();
-    if (warp == 0) {
+    if (tid < 32) {
         long long rsum = 0, isum = 0;
         int most = 0;
         bool neg = false;
@@ -478,9 +557,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             neg |= n < 0;
             long long rows = n > 0 ? n : 0, items = 0;
             if (rows > 0) {
-                const int cr = chunk_rows(static_cast<int>(min(rows, static_cast<long long>(p.rows))), S::NT);
-                most = max(most, min(cr, S::NT));
-                items = ((rows + S::NT - 1) / S::NT) * p.n_tiles;
+                const int cr = chunk_rows(static_cast<int>(min(rows, static_cast<long long>(p.rows))), kMost);
+                most = max(most, min(cr, kMost));
+                items = ((rows + kMost - 1) / kMost) * p.n_tiles;
             }
             long long r = rows, i = items;
 #pragma unroll
@@ -507,7 +586,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     __syncthreads();
-    if (*bad_flag) return;
+    return !*bad_flag;
+}
+
+// ------------------------------------------------------------------ kernel
+
+template <bool kNv, bool kSwiglu>
+__global__ void __launch_bounds__(kThreads, 1)
+    fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a64,
+                    const __grid_constant__ CUtensorMap tm_a16, const Params p) {
+    using S = Shape<kNv, kSwiglu>;
+    using C = ScaleCols<kNv>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    int *roff = reinterpret_cast<int *>(smem + kOffRow);
+    int *ioff = reinterpret_cast<int *>(smem + kOffItem);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kOffBars);   // TMA -> issuer
+    uint64_t *empty = full + kMaxStages;                              // MMA commit -> TMA
+    uint64_t *sf_full = empty + kMaxStages;                           // scale converters -> issuer
+    uint64_t *sf_empty = sf_full + kMaxSfSlots;                       // MMA commit -> scale converters
+    uint64_t *acc_full = sf_empty + kMaxSfSlots;                        // MMA commit -> epilogue
+    uint64_t *acc_empty = acc_full + 2;                               // epilogue -> issuer
+    uint64_t *final_bar = acc_empty + 2;
+    uint64_t *raw_bars = final_bar + 1;                               // scale copiers <-> converters
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kOffMisc);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kOffMisc + 8);
+    int *bad_flag = reinterpret_cast<int *>(smem + kOffMisc + 16);
+    int *nt_slot = reinterpret_cast<int *>(smem + kOffMisc + 24);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int E = p.E;
+
+    if (tid == 0) *abort_flag = 0;
+    if (!build_items<S::NT>(p, roff, ioff, bad_flag, nt_slot)) return;
     const int total = ioff[E];
     if (static_cast<int>(blockIdx.x) >= total) return;
 
@@ -515,18 +626,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int nt_max = *nt_slot;
     const uint32_t b_rows = nt_max <= 32 ? nt_max : (nt_max + 63) & ~63;
     const uint32_t b_bytes = b_rows * kStageBytesRow;
-    const uint32_t n_stages = min(static_cast<uint32_t>(kMaxStages), kRingBytes / (S::kABytes + b_bytes + S::kSfBytes));
+    const uint32_t n_stages = min(static_cast<uint32_t>(kMaxStages), kRingBytes / (S::kABytes + b_bytes));
     uint8_t *b_ring = smem + n_stages * S::kABytes;
-    uint8_t *sf_ring = b_ring + n_stages * b_bytes;
     const int k_stages = (p.K + kStageK - 1) / kStageK;
 
     if (warp == kProducerWarp) tmem_alloc(tmem_slot, kTmemCols);
     if (tid == 0) {
         for (uint32_t s = 0; s < n_stages; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&sf_full[s], 2);
             mbar_init(&empty[s], 1);
         }
+        init_scale_bars(sf_full, sf_empty, raw_bars);
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
             mbar_init(&acc_empty[b], 4);
@@ -552,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t issued = 0;
         bool ok = true;
         for (int j = blockIdx.x; ok && j < total; j += gridDim.x) {
-            const Item it = decode_item<S::NT>(j, roff, ioff, E, p.n_tiles);
+            const Item it = decode_item<S::NT, kTileN>(j, roff, ioff, E, p.n_tiles);
             // Token rows in 64-row boxes; a last part of at most 32 rows in 16-row
             // boxes (rows past the chunk belong to the next one; their columns are
             // not stored).
@@ -561,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t bytes = S::kABytes + (n64 * 64 + n16 * 16) * kStageBytesRow;
             const int wrow = it.e * p.N + it.n0;
             for (int ks = 0; ks < k_stages; ++ks) {
-                ok = warp_wait_bounded(&empty[r.slot], r.phase ^ 1u, abort_flag, p.status, lim);
+                ok = wait(&empty[r.slot], r.phase ^ 1u, abort_flag, p.status, lim);
                 if (!ok) break;
                 uint64_t *bar = &full[r.slot];
                 const uint32_t a_dst = a_base + r.slot * S::kABytes, b_dst = b_base + r.slot * b_bytes;
@@ -591,35 +701,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         // lane (always the same) issues.  A single-lane loop issued a stage in
         // 1,600 cycles, four times what its MMAs take.
         const bool leader = elect_one();
-        const uint32_t a_base = smem_u32(smem), b_base = smem_u32(b_ring), sf_base = smem_u32(sf_ring);
+        const uint32_t a_base = smem_u32(smem), b_base = smem_u32(b_ring);
         const int last_steps = (p.K - (k_stages - 1) * kStageK + 63) >> 6;
-        Ring r;
-        uint32_t buf = 0, acc_phase = 1, set = 0;
+        Ring r, sf;
+        uint32_t buf = 0, acc_phase = 1;
         bool ok = true;
         for (int j = blockIdx.x; ok && j < total; j += gridDim.x) {
-            const Item it = decode_item<S::NT>(j, roff, ioff, E, p.n_tiles);
+            const Item it = decode_item<S::NT, kTileN>(j, roff, ioff, E, p.n_tiles);
             const uint32_t id0 = idesc_fp4<kNv>(it.nt, 0), id2 = idesc_fp4<kNv>(it.nt, kNv ? 0 : 2);
-            const bool two = S::NA == 2 && it.nt > 128;
             const uint32_t d = tmem + buf * kAccCols;
-            ok = warp_wait_bounded(&acc_empty[buf], acc_phase, abort_flag, p.status, lim);
+            ok = wait(&acc_empty[buf], acc_phase, abort_flag, p.status, lim);
             for (int ks = 0; ok && ks < k_stages; ++ks) {
-                ok = warp_wait_bounded(&full[r.slot], r.phase, abort_flag, p.status, lim) &&
-                     warp_wait_bounded(&sf_full[r.slot], r.phase, abort_flag, p.status, lim);
+                ok = wait(&full[r.slot], r.phase, abort_flag, p.status, lim) &&
+                     wait(&sf_full[sf.slot], sf.phase, abort_flag, p.status, lim);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t sf_s = sf_base + r.slot * S::kSfBytes;
-                const uint32_t sfa = tmem + kSfCol0 + set * kSfSetCols;
+                const uint32_t sfa = tmem + kSfCol0 + sf.slot * C::kCols;
                 const uint32_t sfb = sfa + S::MT * S::W * 4;
                 const uint64_t a_desc = smem_desc_sw128(a_base + r.slot * S::kABytes);
                 const uint64_t b_desc = smem_desc_sw128(b_base + r.slot * b_bytes);
                 const int steps = ks == k_stages - 1 ? last_steps : 4;
                 if (leader) {
-#pragma unroll
-                    for (int i = 0; i < S::MT * S::W; ++i) copy_atom(sfa + 4 * i, sf_s + i * kAtomBytes);
-#pragma unroll
-                    for (int i = 0; i < S::W * S::NA; ++i)
-                        if (i % S::NA == 0 || two)
-                            copy_atom(sfb + 4 * i, sf_s + S::kSfaBytes + i * kAtomBytes);
 #pragma unroll
                     for (int t = 0; t < 4; ++t) {
                         if (t >= steps) break;
@@ -632,11 +734,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                                          sfb + 4 * word * S::NA, (ks | t) != 0);
                     }
                     mma_commit(&empty[r.slot]);
+                    mma_commit(&sf_empty[sf.slot]);
                     if (ks == k_stages - 1) mma_commit(&acc_full[buf]);
                 }
                 __syncwarp();
-                set ^= 1u;
                 r.next(n_stages);
+                sf.next(C::kSlots);
             }
             buf ^= 1u;
             if (buf == 0) acc_phase ^= 1u;
@@ -644,17 +747,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Every MMA and commit of the warp done before the CTA leaves.
         if (leader) mma_commit(final_bar);
         __syncwarp();
-        warp_wait_bounded(final_bar, 0, nullptr, p.status, lim);
-    } else if (warp < kAScaleWarp) {
-        const int parts = min(kLoaders, static_cast<int>(n_stages)), part = warp - kWScaleWarp;
-        if (part < parts)
-            load_scales<kNv, kSwiglu, true>(p, sf_ring, n_stages, total, roff, ioff, sf_full, empty, abort_flag, part,
-                                            parts);
+        wait(final_bar, 0, nullptr, p.status, lim);
     } else if (warp < kEpilogueWarp) {
-        const int parts = min(kLoaders, static_cast<int>(n_stages)), part = warp - kAScaleWarp;
-        if (part < parts)
-            load_scales<kNv, kSwiglu, false>(p, sf_ring, n_stages, total, roff, ioff, sf_full, empty, abort_flag, part,
-                                             parts);
+        const ScaleEnv v = {&p, roff, ioff, abort_flag, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), total};
+        const Staging gw = {smem + kOffStaging, raw_bars, raw_bars + kDepth};
+        const Staging ga = {smem + kOffStaging + kDepth * 4 * S::MT * 512, raw_bars + 2 * kDepth, raw_bars + 3 * kDepth};
+        const auto all = [](const Item &) { return 4 * S::MT; };
+        const auto some = [](const Item &it) { return (it.nvalid + 31) >> 5; };
+        if (warp == kWCopyWarp) {
+            const int cols = kSwiglu ? p.I : p.N;
+            copy_scales<4 * S::MT, S::NT, kTileN>(
+                v, gw, p.w_scales, p.w_vec,
+                [&](const Item &it, int q) {
+                    return static_cast<int64_t>(it.e) * p.N + (q >= 4 ? p.I : 0) +
+                           min(it.n0 + lane + 32 * (q & 3), cols - 1);
+                },
+                all);
+        } else if (warp == kACopyWarp) {
+            copy_scales<S::AR, S::NT, kTileN>(
+                v, ga, p.a_scales, p.a_vec,
+                [&](const Item &it, int q) {
+                    return static_cast<int64_t>(it.row0 + min(lane + 32 * q, it.nvalid - 1));
+                },
+                some);
+        } else {
+            convert_scales<kNv, 4 * S::MT, S::AR, S::NT, kTileN>(
+                v, gw, ga, tmem + kSfCol0 + (static_cast<uint32_t>((warp & 3) * 32) << 16), sf_full, sf_empty, all, some);
+        }
     } else {
         const int quarter = warp & 3;
         const float a2 = kNv ? __ldg(p.a_scale_2) : 1.0f;
@@ -662,8 +781,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(h2 > 0.0f && h2 < __uint_as_float(kF32Inf)) && tid == kThreads - 1) set_status(p.status, MOE_ERR_DATA);
         uint32_t buf = 0, phase = 0;
         for (int j = blockIdx.x; j < total; j += gridDim.x) {
-            const Item it = decode_item<S::NT>(j, roff, ioff, E, p.n_tiles);
-            if (!warp_wait_bounded(&acc_full[buf], phase, abort_flag, p.status, lim)) break;
+            const Item it = decode_item<S::NT, kTileN>(j, roff, ioff, E, p.n_tiles);
+            if (!wait(&acc_full[buf], phase, abort_flag, p.status, lim)) break;
             tc_fence_after();
             const uint32_t acc = tmem + buf * kAccCols + (static_cast<uint32_t>(quarter * 32) << 16);
             const float scale = kNv ? __ldg(p.w_scale_2 + it.e) * a2 : 1.0f;
@@ -680,6 +799,469 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     if (warp == kProducerWarp) tmem_dealloc(tmem, kTmemCols);
+}
+
+// ------------------------------------------------- long bands: CTA pairs
+//
+// Bands of many rows are bound by what TMA brings into an SM (about 53 bytes a
+// cycle), not by the MMA.  So two CTAs of a cluster share an item (cta_group::2,
+// M = 256): 256 token rows, 128 a CTA, are now the A operand, and 192 weight rows
+// the B operand, of which each CTA loads half.  A 256-k stage is 28 KB a CTA, 541
+// cycles of copies for 384 cycles of MMA; one CTA with a 128 x 192 tile would copy
+// 40 KB for the same 384.
+//
+// With tokens as rows of D a thread holds one token's consecutive output columns:
+// an MX or NV block of h lies in one thread (no shuffles, no transpose), with the
+// gate sums in columns 0..95 and the up sums in 96..191 (CTA 0 loads the gate rows,
+// CTA 1 the up rows).  Plain outputs go through a 32 x 32 transpose in shared
+// memory to be stored in whole rows.
+//
+// The even CTA issues.  Token scales sit in the CTA of their rows, weight scales in
+// both (each SM scales its own half of D).  The odd CTA's issuer warp relays: once
+// its CTA's copies and scale atoms of a stage are there (it has waited for both: the
+// copies' transaction bytes, and the loaders' arrivals after their proxy fence) it
+// arrives on the even CTA's `ready` barrier; commits are multicast to both.  That
+// arrival is relaxed: what it reports is already in the odd SM's shared memory, and
+// a release at cluster scope took 1,650 cycles a stage.
+
+constexpr int kPairM = 256;                    // token rows of an item
+constexpr int kPairN = 192;                    // weight rows of an item
+constexpr int kPairStages = 6;
+constexpr int kPairABytes = 128 * kStageBytesRow;
+constexpr int kPairBBytes = kPairN / 2 * kStageBytesRow;
+constexpr int kPairRing = kPairStages * (kPairABytes + kPairBBytes);
+constexpr int kPairStaging = kDepth * (6 + 4) * 512;           // scale bytes on their way to atoms
+constexpr int kPatchRow = 36;                  // floats a row of a warp's 32 x 32 transpose
+constexpr int kPairOffStaging = kPairRing;
+constexpr int kPairOffPatch = kPairOffStaging + kPairStaging;
+constexpr int kPairOffRow = kPairOffPatch + 4 * 32 * kPatchRow * 4;
+constexpr int kPairOffItem = kPairOffRow + (kMaxE + 1) * 4;
+constexpr int kPairOffBars = (kPairOffItem + (kMaxE + 1) * 4 + 7) & ~7;
+constexpr int kPairOffMisc = kPairOffBars + (3 * kPairStages + 2 * kMaxSfSlots + 4 + 1 + 4 * kDepth) * 8;
+constexpr int kPairSmem = kPairOffMisc + 64 + 1024;
+static_assert(kPairSmem <= 232448, "shared memory budget (pairs)");
+
+template <bool kNv>
+__device__ __forceinline__ void mma_fp4_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                                             uint32_t sfb, uint32_t accumulate) {
+    if constexpr (kNv)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, "
+            "[%5], [%6], p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sfa),
+            "r"(sfb)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, "
+            "[%5], [%6], p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sfa),
+            "r"(sfb)
+            : "memory");
+}
+
+__device__ __forceinline__ bool try_wait_cluster(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// warp_wait_bounded with acquire at cluster scope.
+__device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *status,
+                                             uint64_t lim) {
+    if (__all_sync(0xffffffffu, try_wait_cluster(bar, parity))) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (;;) {
+        if (__all_sync(0xffffffffu, try_wait_cluster(bar, parity))) return true;
+        const bool late = globaltimer_ns() - t0 > lim;
+        if (__any_sync(0xffffffffu, late || *abort_flag)) {
+            if (late) {
+                *abort_flag = 1;
+                set_status(status, MOE_ERR_TIMEOUT);
+            }
+            return false;
+        }
+    }
+}
+
+// Token rows of CTA `rank` of an item: the chunk in two halves, the first a
+// multiple of 16.
+__device__ __forceinline__ void pair_rows(const Item &it, uint32_t rank, int *row0, int *valid) {
+    const int half = ((it.nvalid + 1) / 2 + 15) & ~15;
+    *row0 = it.row0 + (rank ? half : 0);
+    *valid = rank ? max(it.nvalid - half, 0) : min(half, it.nvalid);
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(taddr));
+}
+
+// Plain outputs of one warp: 32 token rows x 192 columns, 32 columns at a time
+// through the warp's transpose patch.  `vec`: rows of 16-byte vectors.
+__device__ __forceinline__ void pair_store_plain(const Params &p, uint32_t acc, int row0, int valid, int n0,
+                                                 int cols, float scale, float *patch, int vec, uint32_t empty_bar) {
+    const int lane = threadIdx.x & 31;
+    for (int c = 0; c < cols; c += 32) {
+        uint32_t v[32];
+        __syncwarp();
+        tmem_ld32(acc + c, v);
+        tmem_ld_wait();
+        if (c + 32 >= cols) {          // the last sums are in registers: release the buffer
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(empty_bar);
+        }
+        if (valid <= 0) continue;      // warp-uniform
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<float4 *>(patch + lane * kPatchRow + 4 * i) =
+                make_float4(__uint_as_float(v[4 * i]) * scale, __uint_as_float(v[4 * i + 1]) * scale,
+                            __uint_as_float(v[4 * i + 2]) * scale, __uint_as_float(v[4 * i + 3]) * scale);
+        __syncwarp();
+        const size_t base = static_cast<size_t>(row0) * p.N + n0 + c;
+        const int left = p.N - n0 - c;
+        if (!vec) {
+            if (lane < left)
+#pragma unroll 1
+                for (int r = 0; r < min(32, valid); ++r) {
+                    const float f = patch[r * kPatchRow + lane];
+                    const size_t off = base + static_cast<size_t>(r) * p.N + lane;
+                    if (p.out_bf16) reinterpret_cast<__nv_bfloat16 *>(p.out)[off] = __float2bfloat16_rn(f);
+                    else reinterpret_cast<float *>(p.out)[off] = f;
+                }
+        } else if (p.out_bf16) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = i * 8 + (lane >> 2), k = (lane & 3) * 8;
+                const float4 a = *reinterpret_cast<const float4 *>(patch + r * kPatchRow + k);
+                const float4 b = *reinterpret_cast<const float4 *>(patch + r * kPatchRow + k + 4);
+                if (r < valid && k < left) {
+                    const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+                    store_row<8>(reinterpret_cast<__nv_bfloat16 *>(p.out) + base + static_cast<size_t>(r) * p.N + k, f);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = i * 4 + (lane >> 3), k = (lane & 7) * 4;
+                const float4 a = *reinterpret_cast<const float4 *>(patch + r * kPatchRow + k);
+                if (r < valid && k < left)
+                    *reinterpret_cast<float4 *>(reinterpret_cast<float *>(p.out) + base +
+                                                static_cast<size_t>(r) * p.N + k) = a;
+            }
+        }
+    }
+}
+
+// SwiGLU of one warp: lane = token row; blocks of 32 h columns.
+template <bool kNv>
+__device__ __forceinline__ void pair_store_swiglu(const Params &p, uint32_t acc, int row0, int valid, int n0,
+                                                  float scale, float h_scale, uint32_t empty_bar) {
+    const int lane = threadIdx.x & 31;
+    const float g6 = 6.0f * h_scale;
+    for (int b = 0; b < kPairN / 2; b += 32) {
+        uint32_t g[32], u[32];
+        __syncwarp();
+        tmem_ld32(acc + b, g);
+        tmem_ld32(acc + kPairN / 2 + b, u);
+        tmem_ld_wait();
+        if (b + 32 >= kPairN / 2) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(empty_bar);
+        }
+        if (n0 + b >= p.I || lane >= valid) continue;      // I is a multiple of 32
+        const size_t row = static_cast<size_t>(row0 + lane);
+        float h[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            h[i] = silu_f32(__uint_as_float(g[i]) * scale) * (__uint_as_float(u[i]) * scale);
+        uint32_t w[4];
+        constexpr int kBlock = kNv ? 16 : 32;
+#pragma unroll
+        for (int k = 0; k < 32; k += kBlock) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < kBlock; ++i) m = max(m, __float_as_uint(h[k + i]) & 0x7FFFFFFFu);
+            uint32_t byte;
+            float inv;
+            bool nan;
+            if constexpr (kNv) {
+                byte = nv_scale_byte(m, g6);
+                inv = nv_inverse(byte, h_scale);
+                nan = byte == 0x7Fu;
+            } else {
+                byte = mx_scale_byte(m);
+                inv = mx_inverse(byte);
+                nan = byte == 255u;
+            }
+#pragma unroll
+            for (int i = 0; i < kBlock; i += 8) {
+                float q[8];
+#pragma unroll
+                for (int t = 0; t < 8; ++t) q[t] = nan ? 0.0f : h[k + i + t] * inv;
+                w[(k + i) / 8] = e2m1x8(q);
+            }
+            p.out_scales[row * (p.I / kBlock) + (n0 + b + k) / kBlock] = static_cast<uint8_t>(byte);
+        }
+        *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) + row * (p.I / 2) + (n0 + b) / 2) =
+            make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+template <bool kNv, bool kSwiglu>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a128,
+                         const __grid_constant__ CUtensorMap tm_a64, const __grid_constant__ CUtensorMap tm_a32,
+                         const Params p, int out_vec) {
+    using C = ScaleCols<kNv>;
+    constexpr int kTile = kSwiglu ? kPairN / 2 : kPairN;            // output columns of an item
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    float *patch = reinterpret_cast<float *>(smem + kPairOffPatch);
+    int *roff = reinterpret_cast<int *>(smem + kPairOffRow);
+    int *ioff = reinterpret_cast<int *>(smem + kPairOffItem);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kPairOffBars);   // TMA -> issuer / relay
+    uint64_t *ready = full + kPairStages;                                 // relay -> even CTA's issuer
+    uint64_t *empty = ready + kPairStages;                                // pair commit -> TMA of both
+    uint64_t *sf_full = empty + kPairStages;                              // scale converters -> issuer / relay
+    uint64_t *sf_empty = sf_full + kMaxSfSlots;                           // pair commit -> converters of both
+    uint64_t *acc_full = sf_empty + kMaxSfSlots;                           // pair commit -> epilogues of both
+    uint64_t *acc_empty = acc_full + 2;                                   // epilogues of both -> issuer
+    uint64_t *final_bar = acc_empty + 2;
+    uint64_t *raw_bars = final_bar + 1;                               // scale copiers <-> converters
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kPairOffMisc);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kPairOffMisc + 8);
+    int *bad_flag = reinterpret_cast<int *>(smem + kPairOffMisc + 16);
+    int *nt_slot = reinterpret_cast<int *>(smem + kPairOffMisc + 24);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int E = p.E;
+    const uint32_t rank = cluster_rank();
+    const int first = static_cast<int>(blockIdx.x >> 1), step = static_cast<int>(gridDim.x >> 1);
+
+    if (tid == 0) *abort_flag = 0;
+    // Both CTAs read the same sizes, so both return here or neither does.
+    if (!build_items<kPairM>(p, roff, ioff, bad_flag, nt_slot)) return;
+    const int total = ioff[E];
+    if (first >= total) return;
+    constexpr uint32_t n_stages = kPairStages;
+    const int k_stages = (p.K + kStageK - 1) / kStageK;
+    uint8_t *b_ring = smem + n_stages * kPairABytes;
+
+    if (warp == kProducerWarp) tmem_alloc_pair(tmem_slot, kTmemCols);
+    if (tid == 0) {
+        for (uint32_t s = 0; s < n_stages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&ready[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        init_scale_bars(sf_full, sf_empty, raw_bars);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&acc_full[b], 1);
+            mbar_init(&acc_empty[b], 8);
+        }
+        mbar_init(final_bar, 1);
+        mbar_fence_init();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();        // the peer's barriers exist before any remote arrival
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const uint64_t lim = p.wait_limit_ns;
+
+    if (warp == kProducerWarp) {
+        const bool leader = elect_one();
+        if (leader) {
+            tma_prefetch_map(&tm_w);
+            tma_prefetch_map(&tm_a128);
+            tma_prefetch_map(&tm_a64);
+            tma_prefetch_map(&tm_a32);
+        }
+        const uint32_t a_base = smem_u32(smem), b_base = smem_u32(b_ring);
+        Ring r;
+        uint32_t issued = 0;
+        bool ok = true;
+        for (int j = first; ok && j < total; j += step) {
+            const Item it = decode_item<kPairM, kTile>(j, roff, ioff, E, p.n_tiles);
+            int row0, valid;
+            pair_rows(it, rank, &row0, &valid);
+            // Token rows in one box of 128 or 64, or 64 + 32, or 32: a copy costs per
+            // request as well as per byte.
+            const int n64 = valid > 96 ? 2 : valid > 32 ? 1 : 0;
+            const int n32 = valid > 64 && valid <= 96 ? 1 : valid > 0 && valid <= 32 ? 1 : 0;
+            const uint32_t bytes = kPairBBytes + (n64 * 64 + n32 * 32) * kStageBytesRow;
+            // This CTA's half of the weight rows: gate or up, or 96 of 192.
+            const int wrow = it.e * p.N + it.n0 + (rank ? (kSwiglu ? p.I : kPairN / 2) : 0);
+            for (int ks = 0; ks < k_stages; ++ks) {
+                ok = wait(&empty[r.slot], r.phase ^ 1u, abort_flag, p.status, lim);
+                if (!ok) break;
+                uint64_t *bar = &full[r.slot];
+                const uint32_t a_dst = a_base + r.slot * kPairABytes;
+                const int x = ks * kStageBytesRow;
+                if (leader) {
+                    mbar_arrive_expect_tx(bar, bytes);
+                    tma_load_2d(b_base + r.slot * kPairBBytes, &tm_w, x, wrow, bar);
+                    if (n64 == 2) tma_load_2d(a_dst, &tm_a128, x, row0, bar);
+                    if (n64 == 1) tma_load_2d(a_dst, &tm_a64, x, row0, bar);
+                    if (n32) tma_load_2d(a_dst + n64 * 64 * kStageBytesRow, &tm_a32, x, row0 + n64 * 64, bar);
+                }
+                __syncwarp();
+                ++issued;
+                r.next(n_stages);
+            }
+        }
+        if (!ok && lane == 0) {   // drain: every issued copy must land before the CTA exits
+            for (uint32_t i = issued > n_stages ? issued - n_stages : 0; i < issued; ++i)
+                wait_bounded(&full[i % n_stages], (i / n_stages) & 1u, nullptr, p.status, lim);
+        }
+    } else if (warp == kIssuerWarp && rank == 1) {
+        const uint32_t peer_ready = cluster_addr(ready, 0);
+        Ring r, sf;
+        bool ok = true;
+        for (int j = first; ok && j < total; j += step)
+            for (int ks = 0; ok && ks < k_stages; ++ks) {
+                ok = wait(&full[r.slot], r.phase, abort_flag, p.status, lim) &&
+                     wait(&sf_full[sf.slot], sf.phase, abort_flag, p.status, lim);
+                if (ok && lane == 0) mbar_arrive_cluster(peer_ready + r.slot * 8);
+                __syncwarp();
+                r.next(n_stages);
+                sf.next(C::kSlots);
+            }
+    } else if (warp == kIssuerWarp) {
+        const bool leader = elect_one();
+        const uint32_t a_base = smem_u32(smem), b_base = smem_u32(b_ring);
+        const int last_steps = (p.K - (k_stages - 1) * kStageK + 63) >> 6;
+        // M = 256: the descriptor's M field (units of 16) is twice idesc_fp4's.
+        const uint32_t m256 = (128u >> 4) << 24;
+        const uint32_t id0 = idesc_fp4<kNv>(kPairN, 0) + m256, id2 = idesc_fp4<kNv>(kPairN, kNv ? 0 : 2) + m256;
+        Ring r, sf;
+        uint32_t buf = 0, acc_phase = 1;
+        bool ok = true;
+        for (int j = first; ok && j < total; j += step) {
+            const uint32_t d = tmem + buf * kAccCols;
+            ok = wait_cluster(&acc_empty[buf], acc_phase, abort_flag, p.status, lim);
+            for (int ks = 0; ok && ks < k_stages; ++ks) {
+                ok = wait(&full[r.slot], r.phase, abort_flag, p.status, lim) &&
+                     wait(&sf_full[sf.slot], sf.phase, abort_flag, p.status, lim) &&
+                     wait_cluster(&ready[r.slot], r.phase, abort_flag, p.status, lim);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t sfa = tmem + kSfCol0 + sf.slot * C::kCols;
+                const uint32_t sfb = sfa + C::W * 4;
+                const uint64_t a_desc = smem_desc_sw128(a_base + r.slot * kPairABytes);
+                const uint64_t b_desc = smem_desc_sw128(b_base + r.slot * kPairBBytes);
+                const int steps = ks == k_stages - 1 ? last_steps : 4;
+                if (leader) {
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        if (t >= steps) break;
+                        const int word = kNv ? t : t >> 1;
+                        mma_fp4_pair<kNv>(d, a_desc + 2 * t, b_desc + 2 * t, t & 1 ? id2 : id0, sfa + 4 * word,
+                                          sfb + 8 * word, (ks | t) != 0);
+                    }
+                    mma_commit_pair(&empty[r.slot], 3);
+                    mma_commit_pair(&sf_empty[sf.slot], 3);
+                    if (ks == k_stages - 1) mma_commit_pair(&acc_full[buf], 3);
+                }
+                __syncwarp();
+                r.next(n_stages);
+                sf.next(C::kSlots);
+            }
+            buf ^= 1u;
+            if (buf == 0) acc_phase ^= 1u;
+        }
+        if (leader) mma_commit_pair(final_bar, 1);
+        __syncwarp();
+        wait(final_bar, 0, nullptr, p.status, lim);
+    } else if (warp < kEpilogueWarp) {
+        const ScaleEnv v = {&p, roff, ioff, abort_flag, first, step, total};
+        const Staging gw = {smem + kPairOffStaging, raw_bars, raw_bars + kDepth};
+        const Staging ga = {smem + kPairOffStaging + kDepth * 6 * 512, raw_bars + 2 * kDepth, raw_bars + 3 * kDepth};
+        const auto all = [](const Item &) { return kPairN / 32; };
+        const auto some = [&](const Item &it) {
+            int row0, valid;
+            pair_rows(it, rank, &row0, &valid);
+            return (valid + 31) >> 5;
+        };
+        if (warp == kWCopyWarp) {
+            // All 192 weight rows, in the order of the MMA's columns.
+            const int cols = kSwiglu ? p.I : p.N;
+            copy_scales<kPairN / 32, kPairM, kTile>(
+                v, gw, p.w_scales, p.w_vec,
+                [&](const Item &it, int q) {
+                    const int n = kSwiglu ? (q >= 3 ? q - 3 : q) * 32 + lane : q * 32 + lane;
+                    return static_cast<int64_t>(it.e) * p.N + (kSwiglu && q >= 3 ? p.I : 0) +
+                           min(it.n0 + n, cols - 1);
+                },
+                all);
+        } else if (warp == kACopyWarp) {
+            copy_scales<4, kPairM, kTile>(
+                v, ga, p.a_scales, p.a_vec,
+                [&](const Item &it, int q) {
+                    int row0, valid;
+                    pair_rows(it, rank, &row0, &valid);
+                    return static_cast<int64_t>(row0 + min(lane + 32 * q, valid - 1));
+                },
+                some);
+        } else {
+            convert_scales<kNv, 4, kPairN / 32, kPairM, kTile>(
+                v, ga, gw, tmem + kSfCol0 + (static_cast<uint32_t>((warp & 3) * 32) << 16), sf_full, sf_empty, some, all);
+        }
+    } else {
+        const int quarter = warp & 3;
+        const float a2 = kNv ? __ldg(p.a_scale_2) : 1.0f;
+        const float h2 = kNv && kSwiglu ? __ldg(p.h_scale_2) : 1.0f;
+        if (!(h2 > 0.0f && h2 < __uint_as_float(kF32Inf)) && tid == kThreads - 1) set_status(p.status, MOE_ERR_DATA);
+        uint32_t buf = 0, phase = 0;
+        for (int j = first; j < total; j += step) {
+            const Item it = decode_item<kPairM, kTile>(j, roff, ioff, E, p.n_tiles);
+            int row0, valid;
+            pair_rows(it, rank, &row0, &valid);
+            if (!wait(&acc_full[buf], phase, abort_flag, p.status, lim)) break;
+            tc_fence_after();
+            const uint32_t acc = tmem + buf * kAccCols + (static_cast<uint32_t>(quarter * 32) << 16);
+            const float scale = kNv ? __ldg(p.w_scale_2 + it.e) * a2 : 1.0f;
+            const uint32_t bar = cluster_addr(&acc_empty[buf], 0);
+            if constexpr (kSwiglu)
+                pair_store_swiglu<kNv>(p, acc, row0 + quarter * 32, valid - quarter * 32, it.n0, scale, h2, bar);
+            else
+                pair_store_plain(p, acc, row0 + quarter * 32, valid - quarter * 32, it.n0,
+                                 min(kPairN, (p.N - it.n0 + 31) & ~31), scale, patch + quarter * 32 * kPatchRow,
+                                 out_vec, bar);
+            buf ^= 1u;
+            if (buf == 0) phase ^= 1u;
+        }
+    }
+    // Neither CTA frees its tensor memory or leaves while the pair's MMAs, commits
+    // or the peer's arrivals may still reach it.
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    if (warp == kProducerWarp) {
+        __syncwarp();
+        tmem_dealloc_pair(tmem, kTmemCols);
+    }
+    cluster_sync();
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -709,22 +1291,29 @@ bool encode_codes(CUtensorMap *map, const void *base, int64_t rows, int K, uint3
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Shared-memory attribute of a kernel, set once per device (the mask is the
+// caller's, one per kernel).
+bool set_smem(const void *kernel, int bytes, std::atomic<uint64_t> &mask) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+    if (bit && (mask.load(std::memory_order_acquire) & bit)) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+    mask.fetch_or(bit, std::memory_order_release);
+    return true;
+}
+
 template <bool kNv, bool kSwiglu>
 moe_status launch(const Fp4Gemm &g, cudaStream_t stream, int num_sms) {
-    CUtensorMap tm_w, tm_a64, tm_a16;
-    if (!encode_codes(&tm_w, g.w_codes, static_cast<int64_t>(g.E) * g.N, g.K, kTileN) ||
-        !encode_codes(&tm_a64, g.a_codes, g.rows, g.K, 64) || !encode_codes(&tm_a16, g.a_codes, g.rows, g.K, 16))
+    // Long bands (64 rows an expert on average) in CTA pairs; see DESIGN.
+    const bool pair = static_cast<int64_t>(g.rows) >= 64 * static_cast<int64_t>(g.E);
+    CUtensorMap tm_w, tm_a64, tm_a2, tm_a128;
+    if (!encode_codes(&tm_w, g.w_codes, static_cast<int64_t>(g.E) * g.N, g.K, pair ? kPairN / 2 : kTileN) ||
+        !encode_codes(&tm_a64, g.a_codes, g.rows, g.K, 64) ||
+        !encode_codes(&tm_a2, g.a_codes, g.rows, g.K, pair ? 32 : 16) ||
+        (pair && !encode_codes(&tm_a128, g.a_codes, g.rows, g.K, 128)))
         return MOE_ERR_CUDA;
-    static std::atomic<uint64_t> attr_dev_mask{0};   // devices whose attribute is set
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
-    const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
-    if (!(attr_dev_mask.load(std::memory_order_acquire) & bit) || !bit) {
-        if (cudaFuncSetAttribute(fp4_gemm_kernel<kNv, kSwiglu>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 kSmemBytes) != cudaSuccess)
-            return MOE_ERR_CUDA;
-        attr_dev_mask.fetch_or(bit, std::memory_order_release);
-    }
+    const int tile = pair ? (kSwiglu ? kPairN / 2 : kPairN) : kTileN;
     Params p;
     p.w_scales = g.w_scales;
     p.a_scales = g.a_scales;
@@ -741,14 +1330,27 @@ moe_status launch(const Fp4Gemm &g, cudaStream_t stream, int num_sms) {
     p.E = g.E;
     p.I = kSwiglu ? g.N / 2 : 0;
     p.out_bf16 = g.out_bf16;
-    p.n_tiles = ((kSwiglu ? g.N / 2 : g.N) + kTileN - 1) / kTileN;
+    p.n_tiles = ((kSwiglu ? g.N / 2 : g.N) + tile - 1) / tile;
     p.scale_row = g.K / (kNv ? 16 : 32);
-    const int vec_bytes = kNv ? 16 : 8;
-    const bool whole = g.K % kStageK == 0;
-    p.w_vec = whole && reinterpret_cast<uintptr_t>(g.w_scales) % vec_bytes == 0;
-    p.a_vec = whole && reinterpret_cast<uintptr_t>(g.a_scales) % vec_bytes == 0;
+    const auto vec = [&](const uint8_t *scales) {
+        const uintptr_t both = reinterpret_cast<uintptr_t>(scales) | static_cast<uintptr_t>(p.scale_row);
+        return both % 16 == 0 ? 16 : both % 8 == 0 ? 8 : both % 4 == 0 ? 4 : 1;
+    };
+    p.w_vec = vec(g.w_scales);
+    p.a_vec = vec(g.a_scales);
     p.wait_limit_ns = g.wait_limit_ns;
-    fp4_gemm_kernel<kNv, kSwiglu><<<num_sms, kThreads, kSmemBytes, stream>>>(tm_w, tm_a64, tm_a16, p);
+    if (pair) {
+        static std::atomic<uint64_t> mask{0};
+        const auto kernel = fp4_gemm_pair_kernel<kNv, kSwiglu>;
+        if (!set_smem(reinterpret_cast<const void *>(kernel), kPairSmem, mask)) return MOE_ERR_CUDA;
+        const int out_vec = reinterpret_cast<uintptr_t>(g.out) % 16 == 0 && g.N % (g.out_bf16 ? 8 : 4) == 0;
+        kernel<<<num_sms & ~1, kThreads, kPairSmem, stream>>>(tm_w, tm_a128, tm_a64, tm_a2, p, out_vec);
+    } else {
+        static std::atomic<uint64_t> mask{0};
+        const auto kernel = fp4_gemm_kernel<kNv, kSwiglu>;
+        if (!set_smem(reinterpret_cast<const void *>(kernel), kSmemBytes, mask)) return MOE_ERR_CUDA;
+        kernel<<<num_sms, kThreads, kSmemBytes, stream>>>(tm_w, tm_a64, tm_a2, p);
+    }
     return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
