@@ -50,7 +50,8 @@ namespace fp4 {
 
 constexpr int kProducerWarp = 0, kIssuerWarp = 1;
 constexpr int kWCopyWarp = 2, kACopyWarp = 3;          // scale bytes of weights, of tokens
-constexpr int kConvertWarp = 4, kEpilogueWarp = 8;     // four warps each: one a lane quarter
+constexpr int kSets = 2;                               // converter sets, on scale groups in turn
+constexpr int kConvertWarp = 4, kEpilogueWarp = kConvertWarp + 4 * kSets;   // four warps a set: one a lane quarter
 constexpr int kThreads = 32 * (kEpilogueWarp + 4);
 constexpr int kMaxE = 1024;
 constexpr int kTileN = 128;                    // weight rows a tile (MMA M)
@@ -68,7 +69,7 @@ constexpr int kStagingBytes = kDepth * 11 * 512;
 constexpr int kOffRow = kOffStaging + kStagingBytes;
 constexpr int kOffItem = kOffRow + (kMaxE + 1) * 4;
 constexpr int kOffBars = (kOffItem + (kMaxE + 1) * 4 + 7) & ~7;
-constexpr int kNumBars = 2 * kMaxStages + 2 * 5 + 4 + 1 + 4 * kDepth;
+constexpr int kNumBars = 2 * kMaxStages + 4 + 1 + 4 * kDepth;
 constexpr int kOffMisc = kOffBars + kNumBars * 8;
 constexpr int kSmemBytes = kOffMisc + 64 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
@@ -81,7 +82,6 @@ struct ScaleCols {
     static constexpr int kCols = 12 * W;
     static constexpr int kSlots = (kTmemCols - kSfCol0) / kCols;   // 5 or 2
 };
-constexpr int kMaxSfSlots = 5;
 
 struct Params {
     const uint8_t *w_scales, *a_scales;
@@ -369,11 +369,7 @@ __device__ __forceinline__ void store_columns(uint32_t taddr, const uint32_t (&w
     tmem_st<C>(taddr, v);
 }
 
-__device__ __forceinline__ void init_scale_bars(uint64_t *sf_full, uint64_t *sf_empty, uint64_t *raw_bars) {
-    for (int i = 0; i < kMaxSfSlots; ++i) {
-        mbar_init(&sf_full[i], 4);
-        mbar_init(&sf_empty[i], 1);
-    }
+__device__ __forceinline__ void init_scale_bars(uint64_t *raw_bars) {
     for (int d = 0; d < kDepth; ++d) {
         mbar_init(&raw_bars[d], 32);                  // weights: the copier's lanes
         mbar_init(&raw_bars[kDepth + d], 4);          // the converter warps
@@ -383,10 +379,17 @@ __device__ __forceinline__ void init_scale_bars(uint64_t *sf_full, uint64_t *sf_
 }
 
 // Converter warp: staged bytes of both operands -> scale columns in tensor memory,
-// ring of kSlots stages.  A: the MMA's A operand (kByTile), B: its B operand.
+// a ring of n_sf <= n_stages stages.  The warp arrives on the stage's `full` barrier,
+// the TMA's; the scale slot of stage s is free once the MMAs of stage s - n_sf are
+// done, which that stage's `empty` barrier tells.  The sets take groups in turn (two,
+// since one set's reads and stores were slower than a stage's MMAs); with kDepth
+// even and n_stages >= 3 > G no barrier is ever more than one phase off.  (One barrier for the issuer to
+// wait on and one to commit to: with four a stage the issuer's own loop, 980
+// cycles, bound the pair kernel.)  A: the MMA's A operand (kByTile), B: its B operand.
 template <bool kNv, int RA, int RB, int kMost, int kTile, class RowsA, class RowsB>
 __device__ __forceinline__ void convert_scales(const ScaleEnv &v, const Staging &a, const Staging &b, uint32_t sf_tmem,
-                                               uint64_t *sf_full, uint64_t *sf_empty, RowsA rows_a, RowsB rows_b) {
+                                               uint32_t n_sf, uint64_t *full, uint64_t *empty, uint32_t n_stages,
+                                               RowsA rows_a, RowsB rows_b) {
     using C = ScaleCols<kNv>;
     constexpr int G = 4 / C::W, kACols = 4 * ((RA + 3) / 4) * C::W;
     static_assert(kACols + 4 * ((RB + 3) / 4) * C::W == C::kCols, "scale columns of a stage");
@@ -395,18 +398,39 @@ __device__ __forceinline__ void convert_scales(const ScaleEnv &v, const Staging 
     const int k_stages = (p.K + kStageK - 1) / kStageK;
     uint32_t bad = 0;
     bool ok = true;
-    const bool checks = (threadIdx.x >> 5) == kConvertWarp;    // the four read the same bytes
-    Ring sf, raw;
+    const int set = ((threadIdx.x >> 5) - kConvertWarp) >> 2;
+    const bool checks = ((threadIdx.x >> 5) & 3) == 0;    // the four of a set read the same bytes
+    Ring sf, raw, r;              // scale slot, staged group, stage
+    // Stage whose scale slot comes next: n_sf behind `r`.  Before the first one its
+    // phase is the one that counts as complete on a fresh barrier (that slot's first
+    // stage cannot be done before this warp's).
+    Ring used;
+    used.slot = n_stages - n_sf;
+    used.phase = 1;
+    if (n_sf == n_stages) used.slot = 0;
+    int turn = 0;
     for (int j = v.first; ok && j < v.total; j += v.step) {
-        const Item it = decode_item<kMost, kTile>(j, v.roff, v.ioff, p.E, p.n_tiles);
-        const int qa = rows_a(it), qb = rows_b(it);
-        for (int ks = 0; ok && ks < k_stages; ks += G) {
+        int qa = 0, qb = 0;
+        for (int ks = 0; ok && ks < k_stages; ks += G, turn = turn + 1 == kSets ? 0 : turn + 1) {
+            const int stages = min(G, k_stages - ks);
+            if (qa == 0) {        // the item's first group
+                const Item it = decode_item<kMost, kTile>(j, v.roff, v.ioff, p.E, p.n_tiles);
+                qa = rows_a(it) + 1;
+                qb = rows_b(it) + 1;
+            }
+            if (turn != set) {
+                raw.next(kDepth);
+                r.next(n_stages, stages);
+                used.next(n_stages, stages);
+                sf.next(n_sf, stages);
+                continue;
+            }
             ok = wait(&a.full[raw.slot], raw.phase, v.abort_flag, p.status, p.wait_limit_ns) &&
                  wait(&b.full[raw.slot], raw.phase, v.abort_flag, p.status, p.wait_limit_ns);
             if (!ok) break;
             uint32_t wa[RA][4], wb[RB][4];
-            read_group(a.bytes + raw.slot * (RA * 512), wa, [&](int q) { return q < qa; });
-            read_group(b.bytes + raw.slot * (RB * 512), wb, [&](int q) { return q < qb; });
+            read_group(a.bytes + raw.slot * (RA * 512), wa, [&](int q) { return q + 1 < qa; });
+            read_group(b.bytes + raw.slot * (RB * 512), wb, [&](int q) { return q + 1 < qb; });
             if (checks) bad |= bad_group<kNv>(wa) | bad_group<kNv>(wb);
             __syncwarp();
             if (lane == 0) {
@@ -416,8 +440,8 @@ __device__ __forceinline__ void convert_scales(const ScaleEnv &v, const Staging 
             raw.next(kDepth);
 #pragma unroll
             for (int s = 0; s < G; ++s) {
-                if (!ok || ks + s >= k_stages) break;
-                ok = wait(&sf_empty[sf.slot], sf.phase ^ 1u, v.abort_flag, p.status, p.wait_limit_ns);
+                if (s >= stages) break;
+                ok = wait(&empty[used.slot], used.phase, v.abort_flag, p.status, p.wait_limit_ns);
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t at = sf_tmem + sf.slot * C::kCols;
@@ -426,8 +450,10 @@ __device__ __forceinline__ void convert_scales(const ScaleEnv &v, const Staging 
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sf_full[sf.slot]);
-                sf.next(C::kSlots);
+                if (lane == 0) mbar_arrive(&full[r.slot]);
+                r.next(n_stages);
+                used.next(n_stages);
+                sf.next(n_sf);
             }
         }
     }
@@ -601,11 +627,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     int *roff = reinterpret_cast<int *>(smem + kOffRow);
     int *ioff = reinterpret_cast<int *>(smem + kOffItem);
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kOffBars);   // TMA -> issuer
-    uint64_t *empty = full + kMaxStages;                              // MMA commit -> TMA
-    uint64_t *sf_full = empty + kMaxStages;                           // scale converters -> issuer
-    uint64_t *sf_empty = sf_full + kMaxSfSlots;                       // MMA commit -> scale converters
-    uint64_t *acc_full = sf_empty + kMaxSfSlots;                        // MMA commit -> epilogue
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kOffBars);   // TMA, scale converters -> issuer
+    uint64_t *empty = full + kMaxStages;                              // MMA commit -> TMA, scale converters
+    uint64_t *acc_full = empty + kMaxStages;                          // MMA commit -> epilogue
     uint64_t *acc_empty = acc_full + 2;                               // epilogue -> issuer
     uint64_t *final_bar = acc_empty + 2;
     uint64_t *raw_bars = final_bar + 1;                               // scale copiers <-> converters
@@ -619,7 +643,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (tid == 0) *abort_flag = 0;
     if (!build_items<S::NT>(p, roff, ioff, bad_flag, nt_slot)) return;
-    const int total = ioff[E];
+    // redux: the compiler then knows the loops' bounds as warp-uniform
+    const int total = __reduce_max_sync(0xffffffffu, ioff[E]);
     if (static_cast<int>(blockIdx.x) >= total) return;
 
     // Stage layout: as many stages as fit with the widest chunk of this call.
@@ -628,15 +653,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t b_bytes = b_rows * kStageBytesRow;
     const uint32_t n_stages = min(static_cast<uint32_t>(kMaxStages), kRingBytes / (S::kABytes + b_bytes));
     uint8_t *b_ring = smem + n_stages * S::kABytes;
+    const uint32_t n_sf = min(static_cast<uint32_t>(C::kSlots), n_stages);
     const int k_stages = (p.K + kStageK - 1) / kStageK;
 
     if (warp == kProducerWarp) tmem_alloc(tmem_slot, kTmemCols);
     if (tid == 0) {
         for (uint32_t s = 0; s < n_stages; ++s) {
-            mbar_init(&full[s], 1);
+            mbar_init(&full[s], 1 + 4);
             mbar_init(&empty[s], 1);
         }
-        init_scale_bars(sf_full, sf_empty, raw_bars);
+        init_scale_bars(raw_bars);
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
             mbar_init(&acc_empty[b], 4);
@@ -712,8 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t d = tmem + buf * kAccCols;
             ok = wait(&acc_empty[buf], acc_phase, abort_flag, p.status, lim);
             for (int ks = 0; ok && ks < k_stages; ++ks) {
-                ok = wait(&full[r.slot], r.phase, abort_flag, p.status, lim) &&
-                     wait(&sf_full[sf.slot], sf.phase, abort_flag, p.status, lim);
+                ok = wait(&full[r.slot], r.phase, abort_flag, p.status, lim);
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t sfa = tmem + kSfCol0 + sf.slot * C::kCols;
@@ -734,12 +759,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                                          sfb + 4 * word * S::NA, (ks | t) != 0);
                     }
                     mma_commit(&empty[r.slot]);
-                    mma_commit(&sf_empty[sf.slot]);
                     if (ks == k_stages - 1) mma_commit(&acc_full[buf]);
                 }
                 __syncwarp();
                 r.next(n_stages);
-                sf.next(C::kSlots);
+                sf.next(n_sf);
             }
             buf ^= 1u;
             if (buf == 0) acc_phase ^= 1u;
@@ -772,7 +796,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 some);
         } else {
             convert_scales<kNv, 4 * S::MT, S::AR, S::NT, kTileN>(
-                v, gw, ga, tmem + kSfCol0 + (static_cast<uint32_t>((warp & 3) * 32) << 16), sf_full, sf_empty, all, some);
+                v, gw, ga, tmem + kSfCol0 + (static_cast<uint32_t>((warp & 3) * 32) << 16), n_sf, full, empty, n_stages, all,
+                some);
         }
     } else {
         const int quarter = warp & 3;
@@ -818,11 +843,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 //
 // The even CTA issues.  Token scales sit in the CTA of their rows, weight scales in
 // both (each SM scales its own half of D).  The odd CTA's issuer warp relays: once
-// its CTA's copies and scale atoms of a stage are there (it has waited for both: the
-// copies' transaction bytes, and the loaders' arrivals after their proxy fence) it
-// arrives on the even CTA's `ready` barrier; commits are multicast to both.  That
-// arrival is relaxed: what it reports is already in the odd SM's shared memory, and
-// a release at cluster scope took 1,650 cycles a stage.
+// its CTA's copies and scale columns of a stage are there (it has waited for both on
+// its own `full` barrier) it arrives on the even CTA's; commits are multicast to
+// both.  That arrival is relaxed: what it reports is already in the odd SM's shared
+// and tensor memory, and a release at cluster scope took 1,650 cycles a stage.
 
 constexpr int kPairM = 256;                    // token rows of an item
 constexpr int kPairN = 192;                    // weight rows of an item
@@ -837,7 +861,7 @@ constexpr int kPairOffPatch = kPairOffStaging + kPairStaging;
 constexpr int kPairOffRow = kPairOffPatch + 4 * 32 * kPatchRow * 4;
 constexpr int kPairOffItem = kPairOffRow + (kMaxE + 1) * 4;
 constexpr int kPairOffBars = (kPairOffItem + (kMaxE + 1) * 4 + 7) & ~7;
-constexpr int kPairOffMisc = kPairOffBars + (3 * kPairStages + 2 * kMaxSfSlots + 4 + 1 + 4 * kDepth) * 8;
+constexpr int kPairOffMisc = kPairOffBars + (2 * kPairStages + 4 + 1 + 4 * kDepth) * 8;
 constexpr int kPairSmem = kPairOffMisc + 64 + 1024;
 static_assert(kPairSmem <= 232448, "shared memory budget (pairs)");
 
@@ -860,36 +884,6 @@ __device__ __forceinline__ void mma_fp4_pair(uint32_t d, uint64_t a, uint64_t b,
             "[%5], [%6], p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sfa),
             "r"(sfb)
             : "memory");
-}
-
-__device__ __forceinline__ bool try_wait_cluster(uint64_t *bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
-// warp_wait_bounded with acquire at cluster scope.
-__device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *status,
-                                             uint64_t lim) {
-    if (__all_sync(0xffffffffu, try_wait_cluster(bar, parity))) return true;
-    const uint64_t t0 = globaltimer_ns();
-    for (;;) {
-        if (__all_sync(0xffffffffu, try_wait_cluster(bar, parity))) return true;
-        const bool late = globaltimer_ns() - t0 > lim;
-        if (__any_sync(0xffffffffu, late || *abort_flag)) {
-            if (late) {
-                *abort_flag = 1;
-                set_status(status, MOE_ERR_TIMEOUT);
-            }
-            return false;
-        }
-    }
 }
 
 // Token rows of CTA `rank` of an item: the chunk in two halves, the first a
@@ -976,11 +970,18 @@ __device__ __forceinline__ void pair_store_swiglu(const Params &p, uint32_t acc,
     const int lane = threadIdx.x & 31;
     const float g6 = 6.0f * h_scale;
     for (int b = 0; b < kPairN / 2; b += 32) {
-        uint32_t g[32], u[32];
-        __syncwarp();
-        tmem_ld32(acc + b, g);
-        tmem_ld32(acc + kPairN / 2 + b, u);
-        tmem_ld_wait();
+        float h[32];
+#pragma unroll
+        for (int k = 0; k < 32; k += 16) {
+            uint32_t g[16], u[16];
+            __syncwarp();
+            tmem_ld16(acc + b + k, g);
+            tmem_ld16(acc + kPairN / 2 + b + k, u);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                h[k + i] = silu_f32(__uint_as_float(g[i]) * scale) * (__uint_as_float(u[i]) * scale);
+        }
         if (b + 32 >= kPairN / 2) {
             tc_fence_before();
             __syncwarp();
@@ -988,10 +989,6 @@ __device__ __forceinline__ void pair_store_swiglu(const Params &p, uint32_t acc,
         }
         if (n0 + b >= p.I || lane >= valid) continue;      // I is a multiple of 32
         const size_t row = static_cast<size_t>(row0 + lane);
-        float h[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            h[i] = silu_f32(__uint_as_float(g[i]) * scale) * (__uint_as_float(u[i]) * scale);
         uint32_t w[4];
         constexpr int kBlock = kNv ? 16 : 32;
 #pragma unroll
@@ -1037,12 +1034,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     float *patch = reinterpret_cast<float *>(smem + kPairOffPatch);
     int *roff = reinterpret_cast<int *>(smem + kPairOffRow);
     int *ioff = reinterpret_cast<int *>(smem + kPairOffItem);
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kPairOffBars);   // TMA -> issuer / relay
-    uint64_t *ready = full + kPairStages;                                 // relay -> even CTA's issuer
-    uint64_t *empty = ready + kPairStages;                                // pair commit -> TMA of both
-    uint64_t *sf_full = empty + kPairStages;                              // scale converters -> issuer / relay
-    uint64_t *sf_empty = sf_full + kMaxSfSlots;                           // pair commit -> converters of both
-    uint64_t *acc_full = sf_empty + kMaxSfSlots;                           // pair commit -> epilogues of both
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kPairOffBars);   // TMA, scale converters (and relay) -> issuer (relay)
+    uint64_t *empty = full + kPairStages;                                 // pair commit -> TMA, converters of both
+    uint64_t *acc_full = empty + kPairStages;                             // pair commit -> epilogues of both
     uint64_t *acc_empty = acc_full + 2;                                   // epilogues of both -> issuer
     uint64_t *final_bar = acc_empty + 2;
     uint64_t *raw_bars = final_bar + 1;                               // scale copiers <-> converters
@@ -1059,20 +1053,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (tid == 0) *abort_flag = 0;
     // Both CTAs read the same sizes, so both return here or neither does.
     if (!build_items<kPairM>(p, roff, ioff, bad_flag, nt_slot)) return;
-    const int total = ioff[E];
+    // redux: the compiler then knows the loops' bounds as warp-uniform
+    const int total = __reduce_max_sync(0xffffffffu, ioff[E]);
     if (first >= total) return;
-    constexpr uint32_t n_stages = kPairStages;
+    constexpr uint32_t n_stages = kPairStages, n_sf = C::kSlots;
+    static_assert(n_sf <= n_stages, "scale slots");
     const int k_stages = (p.K + kStageK - 1) / kStageK;
     uint8_t *b_ring = smem + n_stages * kPairABytes;
 
     if (warp == kProducerWarp) tmem_alloc_pair(tmem_slot, kTmemCols);
     if (tid == 0) {
         for (uint32_t s = 0; s < n_stages; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&ready[s], 1);
+            mbar_init(&full[s], 1 + 4 + (rank == 0 ? 1 : 0));
             mbar_init(&empty[s], 1);
         }
-        init_scale_bars(sf_full, sf_empty, raw_bars);
+        init_scale_bars(raw_bars);
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
             mbar_init(&acc_empty[b], 8);
@@ -1133,17 +1128,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 wait_bounded(&full[i % n_stages], (i / n_stages) & 1u, nullptr, p.status, lim);
         }
     } else if (warp == kIssuerWarp && rank == 1) {
-        const uint32_t peer_ready = cluster_addr(ready, 0);
-        Ring r, sf;
+        const uint32_t peer_full = cluster_addr(full, 0);
+        Ring r;
         bool ok = true;
         for (int j = first; ok && j < total; j += step)
             for (int ks = 0; ok && ks < k_stages; ++ks) {
-                ok = wait(&full[r.slot], r.phase, abort_flag, p.status, lim) &&
-                     wait(&sf_full[sf.slot], sf.phase, abort_flag, p.status, lim);
-                if (ok && lane == 0) mbar_arrive_cluster(peer_ready + r.slot * 8);
+                ok = wait(&full[r.slot], r.phase, abort_flag, p.status, lim);
+                if (ok && lane == 0) mbar_arrive_cluster(peer_full + r.slot * 8);
                 __syncwarp();
                 r.next(n_stages);
-                sf.next(C::kSlots);
             }
     } else if (warp == kIssuerWarp) {
         const bool leader = elect_one();
@@ -1157,11 +1150,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         bool ok = true;
         for (int j = first; ok && j < total; j += step) {
             const uint32_t d = tmem + buf * kAccCols;
-            ok = wait_cluster(&acc_empty[buf], acc_phase, abort_flag, p.status, lim);
+            ok = wait(&acc_empty[buf], acc_phase, abort_flag, p.status, lim);
             for (int ks = 0; ok && ks < k_stages; ++ks) {
-                ok = wait(&full[r.slot], r.phase, abort_flag, p.status, lim) &&
-                     wait(&sf_full[sf.slot], sf.phase, abort_flag, p.status, lim) &&
-                     wait_cluster(&ready[r.slot], r.phase, abort_flag, p.status, lim);
+                ok = wait(&full[r.slot], r.phase, abort_flag, p.status, lim);
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t sfa = tmem + kSfCol0 + sf.slot * C::kCols;
@@ -1178,12 +1169,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                           sfb + 8 * word, (ks | t) != 0);
                     }
                     mma_commit_pair(&empty[r.slot], 3);
-                    mma_commit_pair(&sf_empty[sf.slot], 3);
                     if (ks == k_stages - 1) mma_commit_pair(&acc_full[buf], 3);
                 }
                 __syncwarp();
                 r.next(n_stages);
-                sf.next(C::kSlots);
+                sf.next(n_sf);
             }
             buf ^= 1u;
             if (buf == 0) acc_phase ^= 1u;
@@ -1223,7 +1213,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 some);
         } else {
             convert_scales<kNv, 4, kPairN / 32, kPairM, kTile>(
-                v, ga, gw, tmem + kSfCol0 + (static_cast<uint32_t>((warp & 3) * 32) << 16), sf_full, sf_empty, some, all);
+                v, ga, gw, tmem + kSfCol0 + (static_cast<uint32_t>((warp & 3) * 32) << 16), n_sf, full, empty, n_stages, some,
+                all);
         }
     } else {
         const int quarter = warp & 3;
