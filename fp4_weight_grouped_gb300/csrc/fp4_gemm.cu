@@ -50,14 +50,14 @@ namespace fp4 {
 
 constexpr int kProducerWarp = 0, kIssuerWarp = 1;
 constexpr int kWCopyWarp = 2, kACopyWarp = 3;          // scale bytes of weights, of tokens
-constexpr int kSets = 2;                               // converter sets, on scale groups in turn
+constexpr int kSets = 2;                               // converter sets: two of a group's four scale words each
 constexpr int kConvertWarp = 4, kEpilogueWarp = kConvertWarp + 4 * kSets;   // four warps a set: one a lane quarter
 constexpr int kThreads = 32 * (kEpilogueWarp + 4);
 constexpr int kMaxE = 1024;
 constexpr int kTileN = 128;                    // weight rows a tile (MMA M)
 constexpr int kStageBytesRow = 128;            // 256 k
 constexpr int kStageK = 256;
-constexpr int kMaxStages = 12;
+constexpr int kMaxStages = 5;                  // MXFP4 keeps as many stages of scales in tensor memory
 constexpr int kDepth = 4;                      // scale groups in the staging area
 constexpr int kAccCols = 192;                  // columns of one accumulator buffer
 constexpr int kSfCol0 = 2 * kAccCols;          // scale columns after the accumulators
@@ -69,18 +69,19 @@ constexpr int kStagingBytes = kDepth * 11 * 512;
 constexpr int kOffRow = kOffStaging + kStagingBytes;
 constexpr int kOffItem = kOffRow + (kMaxE + 1) * 4;
 constexpr int kOffBars = (kOffItem + (kMaxE + 1) * 4 + 7) & ~7;
-constexpr int kNumBars = 2 * kMaxStages + 4 + 1 + 4 * kDepth;
+constexpr int kNumBars = 2 * kMaxStages + 4 + 1 + 2 * kDepth;
 constexpr int kOffMisc = kOffBars + kNumBars * 8;
 constexpr int kSmemBytes = kOffMisc + 64 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 
 // Scale columns of a stage, and the stages they are kept for: every shape here has 12
-// columns a scale word (384 rows of 32-row columns over both operands).
+// columns a scale word (384 rows, 32 a column, over both operands).
 template <bool kNv>
 struct ScaleCols {
     static constexpr int W = kNv ? 4 : 2;                  // scale words a row and stage
     static constexpr int kCols = 12 * W;
-    static constexpr int kSlots = (kTmemCols - kSfCol0) / kCols;   // 5 or 2
+    static constexpr int kSlots = (kTmemCols - kSfCol0) / kCols;
+    static_assert(kSlots == (kNv ? 2 : kMaxStages), "see convert_scales");
 };
 
 struct Params {
@@ -195,11 +196,15 @@ __device__ __noinline__ Item decode_item(int j, const int *roff, const int *ioff
     return it;
 }
 
-// Position in the stage ring.
+// Position in a ring of n slots; by <= n.
 struct Ring {
     uint32_t slot = 0, phase = 0;
     __device__ __forceinline__ void next(uint32_t n, uint32_t by = 1) {
-        for (slot += by; slot >= n; slot -= n) phase ^= 1u;
+        slot += by;
+        if (slot >= n) {
+            slot -= n;
+            phase ^= 1u;
+        }
     }
 };
 
@@ -239,20 +244,23 @@ __device__ __noinline__ void copy_words(uint8_t *dst, const uint8_t *row, int at
     }
 }
 
-// A byte the format does not allow: E8M0 255; E4M3 NaN or a set sign bit (the
-// block-scaled MMA takes unsigned scales).
+// Bits 7 of the result's bytes: whether some byte of w is one the format does not
+// allow.  E8M0: 255, the only byte with bit 7 set that loses it by adding 1 (a carry
+// comes from a 255 alone).  E4M3: NaN (0x7F) or a set sign bit, as the block-scaled
+// MMA takes unsigned scales: bit 7 before or after adding 1.
 template <bool kNv>
 __device__ __forceinline__ uint32_t bad_bits(uint32_t w) {
-    const uint32_t x = kNv ? w ^ 0x7F7F7F7Fu : ~w;               // a byte 0 where w has the NaN byte
-    const uint32_t zero = (x - 0x01010101u) & ~x & 0x80808080u;  // nonzero if and only if there is one
-    return kNv ? zero | (w & 0x80808080u) : zero;
+    const uint32_t plus = w + 0x01010101u;
+    return kNv ? w | plus : w & ~plus;
 }
 
-// Staging of one operand's scale bytes: kDepth groups of 16 bytes a row (two stages
-// of MXFP4, one of NVFP4), R rows a lane (row lane + 32 q of the tile).
+// Staging of both operands' scale bytes: kDepth groups of 16 bytes a row (two stages
+// of MXFP4, one of NVFP4); R rows a lane and operand (row lane + 32 q of the tile),
+// 512 bytes from one q to the next, the weights' rows first.
 struct Staging {
-    uint8_t *bytes;                   // kDepth * R * 512
-    uint64_t *full, *empty;           // one a group: copier -> converters -> copier
+    uint8_t *bytes;
+    uint32_t group_bytes;
+    uint64_t *full, *empty;           // one a group: both copiers -> converters -> copiers
 };
 
 // What the scale warps need of their kernel.
@@ -267,37 +275,36 @@ struct ScaleEnv {
 // wait for or fence waits for copies of later stages.
 //
 // row(item, q): row of this lane, clamped to the tile's or the chunk's last row past
-// its end (those sums are never stored); groups of 32 rows from rows(item) on are
-// skipped.
-template <int R, int kMost, int kTile, class RowFn, class RowsFn>
-__device__ __forceinline__ void copy_scales(const ScaleEnv &v, const Staging &g, const uint8_t *base, int vec,
-                                            RowFn row, RowsFn rows) {
+// its end (those sums are never stored, and every staged byte is one of the tensor).
+template <int R, int kMost, int kTile, class RowFn>
+__device__ __forceinline__ void copy_scales(const ScaleEnv &v, const Staging &g, int first_row, const uint8_t *base,
+                                            int vec, RowFn row) {
     const Params &p = *v.p;
     const int lane = threadIdx.x & 31;
     const int pieces = (p.scale_row + 15) / 16;
+    uint8_t *mine = g.bytes + first_row * 512 + lane * 16;
     Ring r;
     bool ok = true;
     for (int j = v.first; ok && j < v.total; j += v.step) {
         const Item it = decode_item<kMost, kTile>(j, v.roff, v.ioff, p.E, p.n_tiles);
-        const int n = rows(it);
         const uint8_t *src[R];
 #pragma unroll
-        for (int q = 0; q < R; ++q) src[q] = base + (q < n ? row(it, q) : 0) * p.scale_row;
+        for (int q = 0; q < R; ++q) src[q] = base + row(it, q) * p.scale_row;
         for (int i = 0; i < pieces; ++i) {
             ok = wait(&g.empty[r.slot], r.phase ^ 1u, v.abort_flag, p.status, p.wait_limit_ns);
             if (!ok) break;
-            uint8_t *dst = g.bytes + r.slot * (R * 512) + lane * 16;
+            uint8_t *dst = mine + r.slot * g.group_bytes;
             if (vec == 16) {
                 const uint32_t sd = smem_u32(dst);
 #pragma unroll
-                for (int q = 0; q < R; ++q)
-                    if (q < n)
-                        asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(sd + q * 512),
-                                     "l"(src[q] + i * 16)
-                                     : "memory");
+                for (int q = 0; q < R; ++q) {
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(sd + q * 512), "l"(src[q])
+                                 : "memory");
+                    src[q] += 16;
+                }
             } else {
 #pragma unroll 1
-                for (int q = 0; q < n; ++q)
+                for (int q = 0; q < R; ++q)
                     copy_words(dst + q * 512, base + row(it, q) * p.scale_row, i * 16, p.scale_row, vec);
             }
             if (vec == 1)
@@ -326,138 +333,123 @@ __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&v)[C]) 
     }
 }
 
-// One staged group of an operand in registers: scale word i of row lane + 32 q in
-// w[q][i].  Rows nothing was copied for (q with used(q) false) read as zeros.
-template <int R, class Used>
-__device__ __forceinline__ void read_group(const uint8_t *group, uint32_t (&w)[R][4], Used used) {
-    const uint8_t *mine = group + (threadIdx.x & 31) * 16;
+// Two scale words of every row of one staged group.
+template <int R>
+__device__ __forceinline__ void read_words(const uint8_t *group, uint32_t (&w)[R][2]) {
 #pragma unroll
     for (int q = 0; q < R; ++q) {
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (used(q)) x = *reinterpret_cast<const uint4 *>(mine + q * 512);
-        w[q][0] = x.x; w[q][1] = x.y; w[q][2] = x.z; w[q][3] = x.w;
+        const uint2 x = *reinterpret_cast<const uint2 *>(group + q * 512);
+        w[q][0] = x.x;
+        w[q][1] = x.y;
     }
 }
 
-template <bool kNv, int R>
-__device__ __forceinline__ uint32_t bad_group(const uint32_t (&w)[R][4]) {
-    uint32_t bad = 0;
+// The columns of two scale words.  kByTile: (tile of 128 rows, word, column), a tile's
+// words kWords apart; else (word, tile, column).
+template <int R, bool kByTile, int kWords>
+__device__ __forceinline__ void store_words(uint32_t taddr, const uint32_t (&w)[R][2]) {
+    constexpr int T = (R + 3) / 4;
+    const auto at = [&](int q, int i) { return q < R ? w[q < R ? q : 0][i] : 0u; };
+    if constexpr (T == 1 || (kByTile && kWords != 2)) {
 #pragma unroll
-    for (int q = 0; q < R; ++q)
+        for (int t = 0; t < T; ++t) {
+            const uint32_t v[8] = {at(4 * t, 0), at(4 * t + 1, 0), at(4 * t + 2, 0), at(4 * t + 3, 0),
+                                   at(4 * t, 1), at(4 * t + 1, 1), at(4 * t + 2, 1), at(4 * t + 3, 1)};
+            tmem_st<8>(taddr + t * 4 * kWords, v);
+        }
+    } else {
+        uint32_t v[16];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) bad |= bad_bits<kNv>(w[q][i]);
-    return bad;
-}
-
-// Scale columns of stage s of a group.  kByTile: (tile of 128 rows, word, column),
-// else (word, tile, column).
-template <bool kNv, int R, bool kByTile>
-__device__ __forceinline__ void store_columns(uint32_t taddr, const uint32_t (&w)[R][4], int s) {
-    constexpr int W = kNv ? 4 : 2, T = (R + 3) / 4, C = 4 * T * W;
-    uint32_t v[C];
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int t = 0; t < T; ++t)
+            for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int i = 0; i < W; ++i)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const int q = 4 * t + c;
-                const uint32_t a = q < R ? w[q < R ? q : 0][i] : 0u;
-                const uint32_t b = !kNv && q < R ? w[q < R ? q : 0][!kNv ? 2 + i : i] : a;
-                v[(kByTile ? t * W + i : i * T + t) * 4 + c] = s ? b : a;
-            }
-    tmem_st<C>(taddr, v);
+                for (int c = 0; c < 4; ++c) v[(kByTile ? t * 2 + i : i * 2 + t) * 4 + c] = at(4 * t + c, i);
+        tmem_st<16>(taddr, v);
+    }
 }
 
 __device__ __forceinline__ void init_scale_bars(uint64_t *raw_bars) {
     for (int d = 0; d < kDepth; ++d) {
-        mbar_init(&raw_bars[d], 32);                  // weights: the copier's lanes
-        mbar_init(&raw_bars[kDepth + d], 4);          // the converter warps
-        mbar_init(&raw_bars[2 * kDepth + d], 32);     // tokens
-        mbar_init(&raw_bars[3 * kDepth + d], 4);
+        mbar_init(&raw_bars[d], 64);                  // the copiers' lanes
+        mbar_init(&raw_bars[kDepth + d], 4 * kSets);  // the converter warps
     }
 }
 
-// Converter warp: staged bytes of both operands -> scale columns in tensor memory,
-// a ring of n_sf <= n_stages stages.  The warp arrives on the stage's `full` barrier,
-// the TMA's; the scale slot of stage s is free once the MMAs of stage s - n_sf are
-// done, which that stage's `empty` barrier tells.  The sets take groups in turn (two,
-// since one set's reads and stores were slower than a stage's MMAs); with kDepth
-// even and n_stages >= 3 > G no barrier is ever more than one phase off.  (One barrier for the issuer to
-// wait on and one to commit to: with four a stage the issuer's own loop, 980
-// cycles, bound the pair kernel.)  A: the MMA's A operand (kByTile), B: its B operand.
-template <bool kNv, int RA, int RB, int kMost, int kTile, class RowsA, class RowsB>
-__device__ __forceinline__ void convert_scales(const ScaleEnv &v, const Staging &a, const Staging &b, uint32_t sf_tmem,
-                                               uint32_t n_sf, uint64_t *full, uint64_t *empty, uint32_t n_stages,
-                                               RowsA rows_a, RowsB rows_b) {
+// Arrivals a stage's `full` barrier takes from the converters.
+template <bool kNv>
+constexpr int kScaleArrivals = kNv ? 4 * kSets : 4;
+
+// Converter warp: staged bytes of both operands -> scale columns in tensor memory.  The
+// set's two words are a stage of MXFP4 (stage ks + set of the group), or half of one
+// of NVFP4.  The warp arrives on the stage's `full` barrier, the TMA's.  MXFP4 has as
+// many scale slots as stages, so a slot is free when its stage is; NVFP4 has two, so
+// the slot of stage s is free once the MMAs of stage s - 2 are done.
+//
+// What counts here is instructions: a warp takes 7 to 10 cycles for each, so a set
+// that handled whole groups with three rings to keep (280 instructions) needed 2,800
+// cycles for two stages and bound the kernel.
+//
+// A: the MMA's A operand (kByTile), B: its B operand; their first rows in the group.
+template <bool kNv, int RA, int RB>
+__device__ __forceinline__ void convert_scales(const ScaleEnv &v, const Staging &g, int first_a, int first_b,
+                                               uint32_t sf_tmem, uint64_t *full, uint64_t *empty, uint32_t n_stages) {
     using C = ScaleCols<kNv>;
-    constexpr int G = 4 / C::W, kACols = 4 * ((RA + 3) / 4) * C::W;
-    static_assert(kACols + 4 * ((RB + 3) / 4) * C::W == C::kCols, "scale columns of a stage");
+    constexpr int G = 4 / C::W, kACols = 4 * ((RA + 3) / 4) * C::W, TB = (RB + 3) / 4;
+    static_assert(kACols + 4 * TB * C::W == C::kCols, "scale columns of a stage");
+    static_assert(kSets == 2, "a set takes two of four words");
     const Params &p = *v.p;
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3;
     const int k_stages = (p.K + kStageK - 1) / kStageK;
+    const int set = ((threadIdx.x >> 5) - kConvertWarp) >> 2;
     uint32_t bad = 0;
     bool ok = true;
-    const int set = ((threadIdx.x >> 5) - kConvertWarp) >> 2;
-    const bool checks = ((threadIdx.x >> 5) & 3) == 0;    // the four of a set read the same bytes
-    Ring sf, raw, r;              // scale slot, staged group, stage
-    // Stage whose scale slot comes next: n_sf behind `r`.  Before the first one its
-    // phase is the one that counts as complete on a fresh barrier (that slot's first
-    // stage cannot be done before this warp's).
-    Ring used;
-    used.slot = n_stages - n_sf;
-    used.phase = 1;
-    if (n_sf == n_stages) used.slot = 0;
-    int turn = 0;
+    const uint8_t *mine = g.bytes + lane * 16 + set * 8;
+    // NV: the set's columns inside the stage's.
+    const uint32_t a_at = sf_tmem + (kNv ? set * 8 : 0), b_at = sf_tmem + kACols + (kNv ? set * 8 * TB : 0);
+    Ring raw, r;                  // staged group, this set's next stage
+    uint32_t sf = 0;              // NV: scale slot
+    if (!kNv && set) r.next(n_stages);
     for (int j = v.first; ok && j < v.total; j += v.step) {
-        int qa = 0, qb = 0;
-        for (int ks = 0; ok && ks < k_stages; ks += G, turn = turn + 1 == kSets ? 0 : turn + 1) {
-            const int stages = min(G, k_stages - ks);
-            if (qa == 0) {        // the item's first group
-                const Item it = decode_item<kMost, kTile>(j, v.roff, v.ioff, p.E, p.n_tiles);
-                qa = rows_a(it) + 1;
-                qb = rows_b(it) + 1;
-            }
-            if (turn != set) {
-                raw.next(kDepth);
-                r.next(n_stages, stages);
-                used.next(n_stages, stages);
-                sf.next(n_sf, stages);
-                continue;
-            }
-            ok = wait(&a.full[raw.slot], raw.phase, v.abort_flag, p.status, p.wait_limit_ns) &&
-                 wait(&b.full[raw.slot], raw.phase, v.abort_flag, p.status, p.wait_limit_ns);
+        for (int ks = 0; ks < k_stages; ks += G) {
+            ok = wait(&g.full[raw.slot], raw.phase, v.abort_flag, p.status, p.wait_limit_ns);
             if (!ok) break;
-            uint32_t wa[RA][4], wb[RB][4];
-            read_group(a.bytes + raw.slot * (RA * 512), wa, [&](int q) { return q + 1 < qa; });
-            read_group(b.bytes + raw.slot * (RB * 512), wb, [&](int q) { return q + 1 < qb; });
-            if (checks) bad |= bad_group<kNv>(wa) | bad_group<kNv>(wb);
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&a.empty[raw.slot]);
-                mbar_arrive(&b.empty[raw.slot]);
-            }
-            raw.next(kDepth);
+            const uint8_t *group = mine + raw.slot * g.group_bytes;
+            uint32_t wa[RA][2], wb[RB][2];
+            read_words(group + first_a * 512, wa);
+            read_words(group + first_b * 512, wb);
+            // The four warps of a set read the same bytes; each checks a quarter.
 #pragma unroll
-            for (int s = 0; s < G; ++s) {
-                if (s >= stages) break;
-                ok = wait(&empty[used.slot], used.phase, v.abort_flag, p.status, p.wait_limit_ns);
+            for (int i = 0; i < (RA + RB + 3) / 4; ++i)
+                if (4 * i + 3 < RA + RB || quarter + 4 * i < RA + RB) {
+                    const uint2 x = *reinterpret_cast<const uint2 *>(group + (quarter + 4 * i) * 512);
+                    bad |= bad_bits<kNv>(x.x) | bad_bits<kNv>(x.y);
+                }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&g.empty[raw.slot]);
+            raw.next(kDepth);
+            if (kNv || ks + set < k_stages) {     // an odd last stage is the first set's
+                const bool back = r.slot < 2;
+                if constexpr (kNv)
+                    ok = wait(&empty[back ? r.slot + n_stages - 2 : r.slot - 2], r.phase ^ back, v.abort_flag, p.status,
+                              p.wait_limit_ns);
+                else
+                    ok = wait(&empty[r.slot], r.phase ^ 1u, v.abort_flag, p.status, p.wait_limit_ns);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t at = sf_tmem + sf.slot * C::kCols;
-                store_columns<kNv, RA, true>(at, wa, s);
-                store_columns<kNv, RB, false>(at + kACols, wb, s);
+                const uint32_t at = (kNv ? sf : r.slot) * C::kCols;
+                store_words<RA, true, C::W>(a_at + at, wa);
+                store_words<RB, false, C::W>(b_at + at, wb);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&full[r.slot]);
-                r.next(n_stages);
-                used.next(n_stages);
-                sf.next(n_sf);
             }
+            sf ^= 1u;
+            r.next(n_stages, !kNv && ks + 2 <= k_stages ? 2 : 1);
         }
     }
-    if (bad) set_status(p.status, MOE_ERR_DATA);
+    if (bad & 0x80808080u) set_status(p.status, MOE_ERR_DATA);
 }
 
 // -------------------------------------------------------------- epilogues
@@ -653,13 +645,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t b_bytes = b_rows * kStageBytesRow;
     const uint32_t n_stages = min(static_cast<uint32_t>(kMaxStages), kRingBytes / (S::kABytes + b_bytes));
     uint8_t *b_ring = smem + n_stages * S::kABytes;
-    const uint32_t n_sf = min(static_cast<uint32_t>(C::kSlots), n_stages);
     const int k_stages = (p.K + kStageK - 1) / kStageK;
 
     if (warp == kProducerWarp) tmem_alloc(tmem_slot, kTmemCols);
     if (tid == 0) {
         for (uint32_t s = 0; s < n_stages; ++s) {
-            mbar_init(&full[s], 1 + 4);
+            mbar_init(&full[s], 1 + kScaleArrivals<kNv>);
             mbar_init(&empty[s], 1);
         }
         init_scale_bars(raw_bars);
@@ -729,8 +720,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool leader = elect_one();
         const uint32_t a_base = smem_u32(smem), b_base = smem_u32(b_ring);
         const int last_steps = (p.K - (k_stages - 1) * kStageK + 63) >> 6;
-        Ring r, sf;
-        uint32_t buf = 0, acc_phase = 1;
+        Ring r;
+        uint32_t sf = 0, buf = 0, acc_phase = 1;
         bool ok = true;
         for (int j = blockIdx.x; ok && j < total; j += gridDim.x) {
             const Item it = decode_item<S::NT, kTileN>(j, roff, ioff, E, p.n_tiles);
@@ -741,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = wait(&full[r.slot], r.phase, abort_flag, p.status, lim);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t sfa = tmem + kSfCol0 + sf.slot * C::kCols;
+                const uint32_t sfa = tmem + kSfCol0 + (kNv ? sf : r.slot) * C::kCols;
                 const uint32_t sfb = sfa + S::MT * S::W * 4;
                 const uint64_t a_desc = smem_desc_sw128(a_base + r.slot * S::kABytes);
                 const uint64_t b_desc = smem_desc_sw128(b_base + r.slot * b_bytes);
@@ -756,17 +747,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int m = 0; m < S::MT; ++m)
                             mma_fp4<kNv>(d + m * S::kAccStep, a_desc + 2 * t + m * (kTileN * kStageBytesRow >> 4),
                                          b_desc + 2 * t, t & 1 ? id2 : id0, sfa + 4 * (m * S::W + word),
-                                         sfb + 4 * word * S::NA, (ks | t) != 0);
+                                         sfb + 4 * word * S::NA, t > 0 || ks > 0);
                     }
                     mma_commit(&empty[r.slot]);
                     if (ks == k_stages - 1) mma_commit(&acc_full[buf]);
                 }
                 __syncwarp();
+                sf ^= 1u;
                 r.next(n_stages);
-                sf.next(n_sf);
             }
             buf ^= 1u;
-            if (buf == 0) acc_phase ^= 1u;
+            acc_phase ^= buf == 0;
         }
         // Every MMA and commit of the warp done before the CTA leaves.
         if (leader) mma_commit(final_bar);
@@ -774,30 +765,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait(final_bar, 0, nullptr, p.status, lim);
     } else if (warp < kEpilogueWarp) {
         const ScaleEnv v = {&p, roff, ioff, abort_flag, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), total};
-        const Staging gw = {smem + kOffStaging, raw_bars, raw_bars + kDepth};
-        const Staging ga = {smem + kOffStaging + kDepth * 4 * S::MT * 512, raw_bars + 2 * kDepth, raw_bars + 3 * kDepth};
-        const auto all = [](const Item &) { return 4 * S::MT; };
-        const auto some = [](const Item &it) { return (it.nvalid + 31) >> 5; };
+        const Staging g = {smem + kOffStaging, (4 * S::MT + S::AR) * 512, raw_bars, raw_bars + kDepth};
         if (warp == kWCopyWarp) {
             const int cols = kSwiglu ? p.I : p.N;
-            copy_scales<4 * S::MT, S::NT, kTileN>(
-                v, gw, p.w_scales, p.w_vec,
-                [&](const Item &it, int q) {
-                    return static_cast<int64_t>(it.e) * p.N + (q >= 4 ? p.I : 0) +
-                           min(it.n0 + lane + 32 * (q & 3), cols - 1);
-                },
-                all);
+            copy_scales<4 * S::MT, S::NT, kTileN>(v, g, 0, p.w_scales, p.w_vec, [&](const Item &it, int q) {
+                return static_cast<int64_t>(it.e) * p.N + (q >= 4 ? p.I : 0) +
+                       min(it.n0 + lane + 32 * (q & 3), cols - 1);
+            });
         } else if (warp == kACopyWarp) {
-            copy_scales<S::AR, S::NT, kTileN>(
-                v, ga, p.a_scales, p.a_vec,
-                [&](const Item &it, int q) {
-                    return static_cast<int64_t>(it.row0 + min(lane + 32 * q, it.nvalid - 1));
-                },
-                some);
+            copy_scales<S::AR, S::NT, kTileN>(v, g, 4 * S::MT, p.a_scales, p.a_vec, [&](const Item &it, int q) {
+                return static_cast<int64_t>(it.row0 + min(lane + 32 * q, it.nvalid - 1));
+            });
         } else {
-            convert_scales<kNv, 4 * S::MT, S::AR, S::NT, kTileN>(
-                v, gw, ga, tmem + kSfCol0 + (static_cast<uint32_t>((warp & 3) * 32) << 16), n_sf, full, empty, n_stages, all,
-                some);
+            convert_scales<kNv, 4 * S::MT, S::AR>(
+                v, g, 0, 4 * S::MT, tmem + kSfCol0 + (static_cast<uint32_t>((warp & 3) * 32) << 16), full, empty,
+                n_stages);
         }
     } else {
         const int quarter = warp & 3;
@@ -850,7 +832,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 constexpr int kPairM = 256;                    // token rows of an item
 constexpr int kPairN = 192;                    // weight rows of an item
-constexpr int kPairStages = 6;
+constexpr int kPairStages = 5;
 constexpr int kPairABytes = 128 * kStageBytesRow;
 constexpr int kPairBBytes = kPairN / 2 * kStageBytesRow;
 constexpr int kPairRing = kPairStages * (kPairABytes + kPairBBytes);
@@ -861,7 +843,7 @@ constexpr int kPairOffPatch = kPairOffStaging + kPairStaging;
 constexpr int kPairOffRow = kPairOffPatch + 4 * 32 * kPatchRow * 4;
 constexpr int kPairOffItem = kPairOffRow + (kMaxE + 1) * 4;
 constexpr int kPairOffBars = (kPairOffItem + (kMaxE + 1) * 4 + 7) & ~7;
-constexpr int kPairOffMisc = kPairOffBars + (2 * kPairStages + 4 + 1 + 4 * kDepth) * 8;
+constexpr int kPairOffMisc = kPairOffBars + (2 * kPairStages + 4 + 1 + 2 * kDepth) * 8;
 constexpr int kPairSmem = kPairOffMisc + 64 + 1024;
 static_assert(kPairSmem <= 232448, "shared memory budget (pairs)");
 
@@ -1056,15 +1038,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // redux: the compiler then knows the loops' bounds as warp-uniform
     const int total = __reduce_max_sync(0xffffffffu, ioff[E]);
     if (first >= total) return;
-    constexpr uint32_t n_stages = kPairStages, n_sf = C::kSlots;
-    static_assert(n_sf <= n_stages, "scale slots");
+    constexpr uint32_t n_stages = kPairStages;
+    static_assert(kPairStages == kMaxStages, "see convert_scales");
     const int k_stages = (p.K + kStageK - 1) / kStageK;
     uint8_t *b_ring = smem + n_stages * kPairABytes;
 
     if (warp == kProducerWarp) tmem_alloc_pair(tmem_slot, kTmemCols);
     if (tid == 0) {
         for (uint32_t s = 0; s < n_stages; ++s) {
-            mbar_init(&full[s], 1 + 4 + (rank == 0 ? 1 : 0));
+            mbar_init(&full[s], 1 + kScaleArrivals<kNv> + (rank == 0 ? 1 : 0));
             mbar_init(&empty[s], 1);
         }
         init_scale_bars(raw_bars);
@@ -1145,8 +1127,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // M = 256: the descriptor's M field (units of 16) is twice idesc_fp4's.
         const uint32_t m256 = (128u >> 4) << 24;
         const uint32_t id0 = idesc_fp4<kNv>(kPairN, 0) + m256, id2 = idesc_fp4<kNv>(kPairN, kNv ? 0 : 2) + m256;
-        Ring r, sf;
-        uint32_t buf = 0, acc_phase = 1;
+        Ring r;
+        uint32_t sf = 0, buf = 0, acc_phase = 1;
         bool ok = true;
         for (int j = first; ok && j < total; j += step) {
             const uint32_t d = tmem + buf * kAccCols;
@@ -1155,7 +1137,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 ok = wait(&full[r.slot], r.phase, abort_flag, p.status, lim);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t sfa = tmem + kSfCol0 + sf.slot * C::kCols;
+                const uint32_t sfa = tmem + kSfCol0 + (kNv ? sf : r.slot) * C::kCols;
                 const uint32_t sfb = sfa + C::W * 4;
                 const uint64_t a_desc = smem_desc_sw128(a_base + r.slot * kPairABytes);
                 const uint64_t b_desc = smem_desc_sw128(b_base + r.slot * kPairBBytes);
@@ -1166,55 +1148,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         if (t >= steps) break;
                         const int word = kNv ? t : t >> 1;
                         mma_fp4_pair<kNv>(d, a_desc + 2 * t, b_desc + 2 * t, t & 1 ? id2 : id0, sfa + 4 * word,
-                                          sfb + 8 * word, (ks | t) != 0);
+                                          sfb + 8 * word, t > 0 || ks > 0);
                     }
                     mma_commit_pair(&empty[r.slot], 3);
                     if (ks == k_stages - 1) mma_commit_pair(&acc_full[buf], 3);
                 }
                 __syncwarp();
+                sf ^= 1u;
                 r.next(n_stages);
-                sf.next(n_sf);
             }
             buf ^= 1u;
-            if (buf == 0) acc_phase ^= 1u;
+            acc_phase ^= buf == 0;
         }
         if (leader) mma_commit_pair(final_bar, 1);
         __syncwarp();
         wait(final_bar, 0, nullptr, p.status, lim);
     } else if (warp < kEpilogueWarp) {
         const ScaleEnv v = {&p, roff, ioff, abort_flag, first, step, total};
-        const Staging gw = {smem + kPairOffStaging, raw_bars, raw_bars + kDepth};
-        const Staging ga = {smem + kPairOffStaging + kDepth * 6 * 512, raw_bars + 2 * kDepth, raw_bars + 3 * kDepth};
-        const auto all = [](const Item &) { return kPairN / 32; };
-        const auto some = [&](const Item &it) {
-            int row0, valid;
-            pair_rows(it, rank, &row0, &valid);
-            return (valid + 31) >> 5;
-        };
+        const Staging g = {smem + kPairOffStaging, (6 + 4) * 512, raw_bars, raw_bars + kDepth};
         if (warp == kWCopyWarp) {
             // All 192 weight rows, in the order of the MMA's columns.
             const int cols = kSwiglu ? p.I : p.N;
-            copy_scales<kPairN / 32, kPairM, kTile>(
-                v, gw, p.w_scales, p.w_vec,
-                [&](const Item &it, int q) {
-                    const int n = kSwiglu ? (q >= 3 ? q - 3 : q) * 32 + lane : q * 32 + lane;
-                    return static_cast<int64_t>(it.e) * p.N + (kSwiglu && q >= 3 ? p.I : 0) +
-                           min(it.n0 + n, cols - 1);
-                },
-                all);
+            copy_scales<kPairN / 32, kPairM, kTile>(v, g, 0, p.w_scales, p.w_vec, [&](const Item &it, int q) {
+                const int n = kSwiglu ? (q >= 3 ? q - 3 : q) * 32 + lane : q * 32 + lane;
+                return static_cast<int64_t>(it.e) * p.N + (kSwiglu && q >= 3 ? p.I : 0) + min(it.n0 + n, cols - 1);
+            });
         } else if (warp == kACopyWarp) {
-            copy_scales<4, kPairM, kTile>(
-                v, ga, p.a_scales, p.a_vec,
-                [&](const Item &it, int q) {
-                    int row0, valid;
-                    pair_rows(it, rank, &row0, &valid);
-                    return static_cast<int64_t>(row0 + min(lane + 32 * q, valid - 1));
-                },
-                some);
+            copy_scales<4, kPairM, kTile>(v, g, 6, p.a_scales, p.a_vec, [&](const Item &it, int q) {
+                int row0, valid;
+                pair_rows(it, rank, &row0, &valid);
+                return static_cast<int64_t>(min(row0 + min(lane + 32 * q, max(valid - 1, 0)), p.rows - 1));
+            });
         } else {
-            convert_scales<kNv, 4, kPairN / 32, kPairM, kTile>(
-                v, ga, gw, tmem + kSfCol0 + (static_cast<uint32_t>((warp & 3) * 32) << 16), n_sf, full, empty, n_stages, some,
-                all);
+            convert_scales<kNv, 4, kPairN / 32>(
+                v, g, 6, 0, tmem + kSfCol0 + (static_cast<uint32_t>((warp & 3) * 32) << 16), full, empty, n_stages);
         }
     } else {
         const int quarter = warp & 3;
