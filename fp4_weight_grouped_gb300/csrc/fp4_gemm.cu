@@ -58,15 +58,15 @@ constexpr int kTileN = 128;                    // weight rows a tile (MMA M)
 constexpr int kStageBytesRow = 128;            // 256 k
 constexpr int kStageK = 256;
 constexpr int kMaxStages = 5;                  // MXFP4 keeps as many stages of scales in tensor memory
-constexpr int kDepth = 4;                      // scale groups in the staging area
+constexpr int kGroup = 4;                      // stages of a group of staged scale bytes
+constexpr int kDepth = 2;                      // groups in the staging area
 constexpr int kAccCols = 192;                  // columns of one accumulator buffer
 constexpr int kSfCol0 = 2 * kAccCols;          // scale columns after the accumulators
 constexpr int kTmemCols = 512;
 
-constexpr int kRingBytes = 192 * 1024;
-constexpr int kOffStaging = kRingBytes;        // scale bytes on their way to atoms
-constexpr int kStagingBytes = kDepth * 11 * 512;
-constexpr int kOffRow = kOffStaging + kStagingBytes;
+constexpr int kRingBytes = 172 * 1024;
+constexpr int kOffStaging = kRingBytes;        // scale bytes on their way to tensor memory
+constexpr int kOffRow = kOffStaging + kDepth * kGroup * 11 * 512;
 constexpr int kOffItem = kOffRow + (kMaxE + 1) * 4;
 constexpr int kOffBars = (kOffItem + (kMaxE + 1) * 4 + 7) & ~7;
 constexpr int kNumBars = 2 * kMaxStages + 4 + 1 + 2 * kDepth;
@@ -109,7 +109,7 @@ struct Shape {
     static constexpr int AR = NT / 32;                     // token rows a lane of the scale copier
     static constexpr int kABytes = MT * kTileN * kStageBytesRow;
     static constexpr int kAccStep = kSwiglu ? 96 : 0;      // columns from the gate to the up sums
-    static_assert(kDepth * (4 * MT + AR) * 512 <= kStagingBytes, "scale staging");
+    static_assert(4 * MT + AR <= 11, "scale staging");
 };
 
 // ------------------------------------------------------- block-scaled MMA
@@ -210,13 +210,15 @@ struct Ring {
 
 // ---------------------------------------------------------- scale loaders
 
-// Copy of 16 scale bytes [at, at + 16) of one row into shared memory where rows do
-// not load as 16-byte vectors; zeros past the row's end (2^-127 or 0: finite, and
-// they meet zero codes).  `vec`: bytes that load at once (8, 4 or 1; it divides the
-// row and the base address); 8 and 4 are asynchronous.
+// Copy of 16 scale bytes [at, at + 16) of one row into shared memory where a whole
+// group does not load as 16-byte vectors; zeros past the row's end (2^-127 or 0: finite, and
+// they meet zero codes).  `vec`: bytes that load at once (16, 8, 4 or 1; it divides the
+// row and the base address); all but 1 are asynchronous.
 __device__ __noinline__ void copy_words(uint8_t *dst, const uint8_t *row, int at, int scale_row, int vec) {
     const uint32_t sd = smem_u32(dst);
-    if (vec == 8) {
+    if (vec == 16) {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(sd), "l"(row + at) : "memory");
+    } else if (vec == 8) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const bool in = at + 8 * i < scale_row;
@@ -254,12 +256,12 @@ __device__ __forceinline__ uint32_t bad_bits(uint32_t w) {
     return kNv ? w | plus : w & ~plus;
 }
 
-// Staging of both operands' scale bytes: kDepth groups of 16 bytes a row (two stages
-// of MXFP4, one of NVFP4); R rows a lane and operand (row lane + 32 q of the tile),
-// 512 bytes from one q to the next, the weights' rows first.
+// Staging of both operands' scale bytes: kDepth groups of kGroup stages, which are 2
+// (MXFP4) or 4 (NVFP4) pieces of 16 bytes a row; R rows a lane and operand (row lane +
+// 32 q of the tile), 512 bytes from one q to the next, the weights' rows first.
 struct Staging {
     uint8_t *bytes;
-    uint32_t group_bytes;
+    uint32_t piece_bytes;             // all rows' pieces
     uint64_t *full, *empty;           // one a group: both copiers -> converters -> copiers
 };
 
@@ -274,9 +276,9 @@ struct ScaleEnv {
 // Copier warp.  The copies have a warp of their own so that nothing the converters
 // wait for or fence waits for copies of later stages.
 //
-// row(item, q): row of this lane, clamped to the tile's or the chunk's last row past
+// P: pieces of a group.  row(item, q): row of this lane, clamped to the tile's or the chunk's last row past
 // its end (those sums are never stored, and every staged byte is one of the tensor).
-template <int R, int kMost, int kTile, class RowFn>
+template <int P, int R, int kMost, int kTile, class RowFn>
 __device__ __forceinline__ void copy_scales(const ScaleEnv &v, const Staging &g, int first_row, const uint8_t *base,
                                             int vec, RowFn row) {
     const Params &p = *v.p;
@@ -290,22 +292,28 @@ __device__ __forceinline__ void copy_scales(const ScaleEnv &v, const Staging &g,
         const uint8_t *src[R];
 #pragma unroll
         for (int q = 0; q < R; ++q) src[q] = base + row(it, q) * p.scale_row;
-        for (int i = 0; i < pieces; ++i) {
+        for (int i = 0; i < pieces; i += P) {
             ok = wait(&g.empty[r.slot], r.phase ^ 1u, v.abort_flag, p.status, p.wait_limit_ns);
             if (!ok) break;
-            uint8_t *dst = mine + r.slot * g.group_bytes;
-            if (vec == 16) {
+            uint8_t *dst = mine + r.slot * P * g.piece_bytes;
+            if (vec == 16 && i + P <= pieces) {
                 const uint32_t sd = smem_u32(dst);
 #pragma unroll
                 for (int q = 0; q < R; ++q) {
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(sd + q * 512), "l"(src[q])
-                                 : "memory");
-                    src[q] += 16;
+#pragma unroll
+                    for (int k = 0; k < P; ++k)
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(sd + k * g.piece_bytes + q * 512),
+                                     "l"(src[q] + 16 * k)
+                                     : "memory");
+                    src[q] += 16 * P;
                 }
             } else {
 #pragma unroll 1
-                for (int q = 0; q < R; ++q)
-                    copy_words(dst + q * 512, base + row(it, q) * p.scale_row, i * 16, p.scale_row, vec);
+                for (int k = 0; k < P && i + k < pieces; ++k)
+#pragma unroll 1
+                    for (int q = 0; q < R; ++q)
+                        copy_words(dst + k * g.piece_bytes + q * 512, base + row(it, q) * p.scale_row, (i + k) * 16,
+                                   p.scale_row, vec);
             }
             if (vec == 1)
                 mbar_arrive(&g.full[r.slot]);
@@ -395,7 +403,7 @@ template <bool kNv, int RA, int RB>
 __device__ __forceinline__ void convert_scales(const ScaleEnv &v, const Staging &g, int first_a, int first_b,
                                                uint32_t sf_tmem, uint64_t *full, uint64_t *empty, uint32_t n_stages) {
     using C = ScaleCols<kNv>;
-    constexpr int G = 4 / C::W, kACols = 4 * ((RA + 3) / 4) * C::W, TB = (RB + 3) / 4;
+    constexpr int G = 4 / C::W, P = kGroup / G, kACols = 4 * ((RA + 3) / 4) * C::W, TB = (RB + 3) / 4;
     static_assert(kACols + 4 * TB * C::W == C::kCols, "scale columns of a stage");
     static_assert(kSets == 2, "a set takes two of four words");
     const Params &p = *v.p;
@@ -411,42 +419,45 @@ __device__ __forceinline__ void convert_scales(const ScaleEnv &v, const Staging 
     uint32_t sf = 0;              // NV: scale slot
     if (!kNv && set) r.next(n_stages);
     for (int j = v.first; ok && j < v.total; j += v.step) {
-        for (int ks = 0; ks < k_stages; ks += G) {
+        for (int k0 = 0; ok && k0 < k_stages; k0 += kGroup) {
             ok = wait(&g.full[raw.slot], raw.phase, v.abort_flag, p.status, p.wait_limit_ns);
-            if (!ok) break;
-            const uint8_t *group = mine + raw.slot * g.group_bytes;
-            uint32_t wa[RA][2], wb[RB][2];
-            read_words(group + first_a * 512, wa);
-            read_words(group + first_b * 512, wb);
-            // The four warps of a set read the same bytes; each checks a quarter.
+            const uint8_t *piece = mine + raw.slot * P * g.piece_bytes;
+            const int end = min(k0 + kGroup, k_stages);
+#pragma unroll 1
+            for (int ks = k0; ok && ks < end; ks += G, piece += g.piece_bytes) {
+                uint32_t wa[RA][2], wb[RB][2];
+                read_words(piece + first_a * 512, wa);
+                read_words(piece + first_b * 512, wb);
+                // The four warps of a set read the same bytes; each checks a quarter.
 #pragma unroll
-            for (int i = 0; i < (RA + RB + 3) / 4; ++i)
-                if (4 * i + 3 < RA + RB || quarter + 4 * i < RA + RB) {
-                    const uint2 x = *reinterpret_cast<const uint2 *>(group + (quarter + 4 * i) * 512);
-                    bad |= bad_bits<kNv>(x.x) | bad_bits<kNv>(x.y);
+                for (int i = 0; i < (RA + RB + 3) / 4; ++i)
+                    if (4 * i + 3 < RA + RB || quarter + 4 * i < RA + RB) {
+                        const uint2 x = *reinterpret_cast<const uint2 *>(piece + (quarter + 4 * i) * 512);
+                        bad |= bad_bits<kNv>(x.x) | bad_bits<kNv>(x.y);
+                    }
+                if (kNv || ks + set < k_stages) {     // an odd last stage is the first set's
+                    const bool back = r.slot < 2;
+                    if constexpr (kNv)
+                        ok = wait(&empty[back ? r.slot + n_stages - 2 : r.slot - 2], r.phase ^ back, v.abort_flag,
+                                  p.status, p.wait_limit_ns);
+                    else
+                        ok = wait(&empty[r.slot], r.phase ^ 1u, v.abort_flag, p.status, p.wait_limit_ns);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t at = (kNv ? sf : r.slot) * C::kCols;
+                    store_words<RA, true, C::W>(a_at + at, wa);
+                    store_words<RB, false, C::W>(b_at + at, wb);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&full[r.slot]);
                 }
+                sf ^= 1u;
+                r.next(n_stages, !kNv && ks + 2 <= k_stages ? 2 : 1);
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(&g.empty[raw.slot]);
             raw.next(kDepth);
-            if (kNv || ks + set < k_stages) {     // an odd last stage is the first set's
-                const bool back = r.slot < 2;
-                if constexpr (kNv)
-                    ok = wait(&empty[back ? r.slot + n_stages - 2 : r.slot - 2], r.phase ^ back, v.abort_flag, p.status,
-                              p.wait_limit_ns);
-                else
-                    ok = wait(&empty[r.slot], r.phase ^ 1u, v.abort_flag, p.status, p.wait_limit_ns);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t at = (kNv ? sf : r.slot) * C::kCols;
-                store_words<RA, true, C::W>(a_at + at, wa);
-                store_words<RB, false, C::W>(b_at + at, wb);
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&full[r.slot]);
-            }
-            sf ^= 1u;
-            r.next(n_stages, !kNv && ks + 2 <= k_stages ? 2 : 1);
         }
     }
     if (bad & 0x80808080u) set_status(p.status, MOE_ERR_DATA);
@@ -766,14 +777,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp < kEpilogueWarp) {
         const ScaleEnv v = {&p, roff, ioff, abort_flag, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), total};
         const Staging g = {smem + kOffStaging, (4 * S::MT + S::AR) * 512, raw_bars, raw_bars + kDepth};
+        constexpr int P = kGroup * C::W / 4;
         if (warp == kWCopyWarp) {
             const int cols = kSwiglu ? p.I : p.N;
-            copy_scales<4 * S::MT, S::NT, kTileN>(v, g, 0, p.w_scales, p.w_vec, [&](const Item &it, int q) {
+            copy_scales<P, 4 * S::MT, S::NT, kTileN>(v, g, 0, p.w_scales, p.w_vec, [&](const Item &it, int q) {
                 return static_cast<int64_t>(it.e) * p.N + (q >= 4 ? p.I : 0) +
                        min(it.n0 + lane + 32 * (q & 3), cols - 1);
             });
         } else if (warp == kACopyWarp) {
-            copy_scales<S::AR, S::NT, kTileN>(v, g, 4 * S::MT, p.a_scales, p.a_vec, [&](const Item &it, int q) {
+            copy_scales<P, S::AR, S::NT, kTileN>(v, g, 4 * S::MT, p.a_scales, p.a_vec, [&](const Item &it, int q) {
                 return static_cast<int64_t>(it.row0 + min(lane + 32 * q, it.nvalid - 1));
             });
         } else {
@@ -820,8 +832,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // With tokens as rows of D a thread holds one token's consecutive output columns:
 // an MX or NV block of h lies in one thread (no shuffles, no transpose), with the
 // gate sums in columns 0..95 and the up sums in 96..191 (CTA 0 loads the gate rows,
-// CTA 1 the up rows).  Plain outputs go through a 32 x 32 transpose in shared
-// memory to be stored in whole rows.
+// CTA 1 the up rows).
 //
 // The even CTA issues.  Token scales sit in the CTA of their rows, weight scales in
 // both (each SM scales its own half of D).  The odd CTA's issuer warp relays: once
@@ -836,7 +847,7 @@ constexpr int kPairStages = 5;
 constexpr int kPairABytes = 128 * kStageBytesRow;
 constexpr int kPairBBytes = kPairN / 2 * kStageBytesRow;
 constexpr int kPairRing = kPairStages * (kPairABytes + kPairBBytes);
-constexpr int kPairStaging = kDepth * (6 + 4) * 512;           // scale bytes on their way to atoms
+constexpr int kPairStaging = kDepth * kGroup * (6 + 4) * 512;  // scale bytes on their way to tensor memory
 constexpr int kPatchRow = 36;                  // floats a row of a warp's 32 x 32 transpose
 constexpr int kPairOffStaging = kPairRing;
 constexpr int kPairOffPatch = kPairOffStaging + kPairStaging;
@@ -888,8 +899,18 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
         : "r"(taddr));
 }
 
-// Plain outputs of one warp: 32 token rows x 192 columns, 32 columns at a time
-// through the warp's transpose patch.  `vec`: rows of 16-byte vectors.
+// 32 consecutive bytes, 32-byte aligned.
+__device__ __forceinline__ void store_sector(void *p, const uint32_t (&v)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
+// Plain outputs of one warp: lane = token row, 32 columns at a time.  `vec`: rows are
+// whole 32-byte sectors.  bf16: a lane stores its own columns, two sectors.  f32: a
+// transpose through shared memory, then eight rows of 128 bytes a store; lanes that
+// stored their own four sectors slowed the whole SM's loads (full layer w2 308 ->
+// 334 us).  Otherwise the transpose, a column a lane.
 __device__ __forceinline__ void pair_store_plain(const Params &p, uint32_t acc, int row0, int valid, int n0,
                                                  int cols, float scale, float *patch, int vec, uint32_t empty_bar) {
     const int lane = threadIdx.x & 31;
@@ -903,45 +924,47 @@ __device__ __forceinline__ void pair_store_plain(const Params &p, uint32_t acc, 
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(empty_bar);
         }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * scale);
+        const int left = p.N - n0 - c;
+        if (vec && p.out_bf16) {
+            __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.out) + static_cast<size_t>(row0 + lane) * p.N + n0 + c;
+            if (lane < valid) {
+#pragma unroll
+                for (int i = 0; i < 32; i += 16) {
+                    uint32_t w[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        w[k] = bf16_pair(__uint_as_float(v[i + 2 * k]), __uint_as_float(v[i + 2 * k + 1]));
+                    if (i < left) store_sector(o + i, w);
+                }
+            }
+            continue;
+        }
         if (valid <= 0) continue;      // warp-uniform
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<float4 *>(patch + lane * kPatchRow + 4 * i) =
-                make_float4(__uint_as_float(v[4 * i]) * scale, __uint_as_float(v[4 * i + 1]) * scale,
-                            __uint_as_float(v[4 * i + 2]) * scale, __uint_as_float(v[4 * i + 3]) * scale);
+        for (int i = 0; i < 32; i += 4)
+            *reinterpret_cast<uint4 *>(patch + lane * kPatchRow + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
         __syncwarp();
-        const size_t base = static_cast<size_t>(row0) * p.N + n0 + c;
-        const int left = p.N - n0 - c;
-        if (!vec) {
-            if (lane < left)
-#pragma unroll 1
-                for (int r = 0; r < min(32, valid); ++r) {
-                    const float f = patch[r * kPatchRow + lane];
-                    const size_t off = base + static_cast<size_t>(r) * p.N + lane;
-                    if (p.out_bf16) reinterpret_cast<__nv_bfloat16 *>(p.out)[off] = __float2bfloat16_rn(f);
-                    else reinterpret_cast<float *>(p.out)[off] = f;
-                }
-        } else if (p.out_bf16) {
+        if (vec) {
+            const int r0 = lane >> 2, k = (lane & 3) * 8;
+            float *o = static_cast<float *>(p.out) + static_cast<size_t>(row0 + r0) * p.N + n0 + c + k;
+            const float *from = patch + r0 * kPatchRow + k;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int r = i * 8 + (lane >> 2), k = (lane & 3) * 8;
-                const float4 a = *reinterpret_cast<const float4 *>(patch + r * kPatchRow + k);
-                const float4 b = *reinterpret_cast<const float4 *>(patch + r * kPatchRow + k + 4);
-                if (r < valid && k < left) {
-                    const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-                    store_row<8>(reinterpret_cast<__nv_bfloat16 *>(p.out) + base + static_cast<size_t>(r) * p.N + k, f);
-                }
+                const uint4 x = *reinterpret_cast<const uint4 *>(from + i * 8 * kPatchRow);
+                const uint4 y = *reinterpret_cast<const uint4 *>(from + i * 8 * kPatchRow + 4);
+                const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+                if (r0 + 8 * i < valid && k < left) store_sector(o + static_cast<size_t>(8 * i) * p.N, w);
             }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int r = i * 4 + (lane >> 3), k = (lane & 7) * 4;
-                const float4 a = *reinterpret_cast<const float4 *>(patch + r * kPatchRow + k);
-                if (r < valid && k < left)
-                    *reinterpret_cast<float4 *>(reinterpret_cast<float *>(p.out) + base +
-                                                static_cast<size_t>(r) * p.N + k) = a;
+        } else if (lane < left)
+#pragma unroll 1
+            for (int r = 0; r < min(32, valid); ++r) {
+                const float f = patch[r * kPatchRow + lane];
+                const size_t off = static_cast<size_t>(row0 + r) * p.N + n0 + c + lane;
+                if (p.out_bf16) static_cast<__nv_bfloat16 *>(p.out)[off] = __float2bfloat16_rn(f);
+                else static_cast<float *>(p.out)[off] = f;
             }
-        }
     }
 }
 
@@ -1166,15 +1189,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else if (warp < kEpilogueWarp) {
         const ScaleEnv v = {&p, roff, ioff, abort_flag, first, step, total};
         const Staging g = {smem + kPairOffStaging, (6 + 4) * 512, raw_bars, raw_bars + kDepth};
+        constexpr int P = kGroup * C::W / 4;
         if (warp == kWCopyWarp) {
             // All 192 weight rows, in the order of the MMA's columns.
             const int cols = kSwiglu ? p.I : p.N;
-            copy_scales<kPairN / 32, kPairM, kTile>(v, g, 0, p.w_scales, p.w_vec, [&](const Item &it, int q) {
+            copy_scales<P, kPairN / 32, kPairM, kTile>(v, g, 0, p.w_scales, p.w_vec, [&](const Item &it, int q) {
                 const int n = kSwiglu ? (q >= 3 ? q - 3 : q) * 32 + lane : q * 32 + lane;
                 return static_cast<int64_t>(it.e) * p.N + (kSwiglu && q >= 3 ? p.I : 0) + min(it.n0 + n, cols - 1);
             });
         } else if (warp == kACopyWarp) {
-            copy_scales<4, kPairM, kTile>(v, g, 6, p.a_scales, p.a_vec, [&](const Item &it, int q) {
+            copy_scales<P, 4, kPairM, kTile>(v, g, 6, p.a_scales, p.a_vec, [&](const Item &it, int q) {
                 int row0, valid;
                 pair_rows(it, rank, &row0, &valid);
                 return static_cast<int64_t>(min(row0 + min(lane + 32 * q, max(valid - 1, 0)), p.rows - 1));
@@ -1301,7 +1325,7 @@ moe_status launch(const Fp4Gemm &g, cudaStream_t stream, int num_sms) {
         static std::atomic<uint64_t> mask{0};
         const auto kernel = fp4_gemm_pair_kernel<kNv, kSwiglu>;
         if (!set_smem(reinterpret_cast<const void *>(kernel), kPairSmem, mask)) return MOE_ERR_CUDA;
-        const int out_vec = reinterpret_cast<uintptr_t>(g.out) % 16 == 0 && g.N % (g.out_bf16 ? 8 : 4) == 0;
+        const int out_vec = reinterpret_cast<uintptr_t>(g.out) % 32 == 0 && g.N % (g.out_bf16 ? 16 : 8) == 0;
         kernel<<<num_sms & ~1, kThreads, kPairSmem, stream>>>(tm_w, tm_a128, tm_a64, tm_a2, p, out_vec);
     } else {
         static std::atomic<uint64_t> mask{0};
