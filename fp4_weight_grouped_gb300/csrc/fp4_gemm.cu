@@ -50,7 +50,7 @@ namespace fp4 {
 
 constexpr int kProducerWarp = 0, kIssuerWarp = 1;
 constexpr int kWCopyWarp = 2, kACopyWarp = 3;          // scale bytes of weights, of tokens
-constexpr int kSets = 2;                               // converter sets: two of a group's four scale words each
+constexpr int kSets = 2;                               // converter sets, on stages in turn
 constexpr int kConvertWarp = 4, kEpilogueWarp = kConvertWarp + 4 * kSets;   // four warps a set: one a lane quarter
 constexpr int kThreads = 32 * (kEpilogueWarp + 4);
 constexpr int kMaxE = 1024;
@@ -341,40 +341,33 @@ __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&v)[C]) 
     }
 }
 
-// Two scale words of every row of one staged group.
-template <int R>
-__device__ __forceinline__ void read_words(const uint8_t *group, uint32_t (&w)[R][2]) {
+// W scale words of every row of one staged piece.
+template <int R, int W>
+__device__ __forceinline__ void read_words(const uint8_t *piece, uint32_t (&w)[R][W]) {
 #pragma unroll
     for (int q = 0; q < R; ++q) {
-        const uint2 x = *reinterpret_cast<const uint2 *>(group + q * 512);
-        w[q][0] = x.x;
-        w[q][1] = x.y;
+        if constexpr (W == 2) {
+            const uint2 x = *reinterpret_cast<const uint2 *>(piece + q * 512);
+            w[q][0] = x.x; w[q][1] = x.y;
+        } else {
+            const uint4 x = *reinterpret_cast<const uint4 *>(piece + q * 512);
+            w[q][0] = x.x; w[q][1] = x.y; w[q][2] = x.z; w[q][3] = x.w;
+        }
     }
 }
 
-// The columns of two scale words.  kByTile: (tile of 128 rows, word, column), a tile's
-// words kWords apart; else (word, tile, column).
-template <int R, bool kByTile, int kWords>
-__device__ __forceinline__ void store_words(uint32_t taddr, const uint32_t (&w)[R][2]) {
+// A stage's columns of one operand.  kByTile: (tile of 128 rows, word, column), else
+// (word, tile, column).
+template <int R, int W, bool kByTile>
+__device__ __forceinline__ void store_words(uint32_t taddr, const uint32_t (&w)[R][W]) {
     constexpr int T = (R + 3) / 4;
-    const auto at = [&](int q, int i) { return q < R ? w[q < R ? q : 0][i] : 0u; };
-    if constexpr (T == 1 || (kByTile && kWords != 2)) {
+    uint32_t v[4 * T * W];
 #pragma unroll
-        for (int t = 0; t < T; ++t) {
-            const uint32_t v[8] = {at(4 * t, 0), at(4 * t + 1, 0), at(4 * t + 2, 0), at(4 * t + 3, 0),
-                                   at(4 * t, 1), at(4 * t + 1, 1), at(4 * t + 2, 1), at(4 * t + 3, 1)};
-            tmem_st<8>(taddr + t * 4 * kWords, v);
-        }
-    } else {
-        uint32_t v[16];
+    for (int i = 0; i < W; ++i)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) v[(kByTile ? t * 2 + i : i * 2 + t) * 4 + c] = at(4 * t + c, i);
-        tmem_st<16>(taddr, v);
-    }
+        for (int q = 0; q < 4 * T; ++q)
+            v[(kByTile ? (q / 4) * W + i : i * T + q / 4) * 4 + (q & 3)] = q < R ? w[q < R ? q : 0][i] : 0u;
+    tmem_st<4 * T * W>(taddr, v);
 }
 
 __device__ __forceinline__ void init_scale_bars(uint64_t *raw_bars) {
@@ -384,15 +377,11 @@ __device__ __forceinline__ void init_scale_bars(uint64_t *raw_bars) {
     }
 }
 
-// Arrivals a stage's `full` barrier takes from the converters.
-template <bool kNv>
-constexpr int kScaleArrivals = kNv ? 4 * kSets : 4;
-
-// Converter warp: staged bytes of both operands -> scale columns in tensor memory.  The
-// set's two words are a stage of MXFP4 (stage ks + set of the group), or half of one
-// of NVFP4.  The warp arrives on the stage's `full` barrier, the TMA's.  MXFP4 has as
-// many scale slots as stages, so a slot is free when its stage is; NVFP4 has two, so
-// the slot of stage s is free once the MMAs of stage s - 2 are done.
+// Converter warp: staged bytes of both operands -> scale columns in tensor memory, of
+// stages set, set + 2, ... of each item.  The four warps of a set (one a lane quarter)
+// arrive on the stage's `full` barrier, the TMA's.  MXFP4 has as many scale slots as
+// stages, so a slot is free when its stage is; NVFP4 has two, so the slot of stage s
+// is free once the MMAs of stage s - 2 are done.
 //
 // What counts here is instructions: a warp takes 7 to 10 cycles for each, so a set
 // that handled whole groups with three rings to keep (280 instructions) needed 2,800
@@ -403,39 +392,41 @@ template <bool kNv, int RA, int RB>
 __device__ __forceinline__ void convert_scales(const ScaleEnv &v, const Staging &g, int first_a, int first_b,
                                                uint32_t sf_tmem, uint64_t *full, uint64_t *empty, uint32_t n_stages) {
     using C = ScaleCols<kNv>;
-    constexpr int G = 4 / C::W, P = kGroup / G, kACols = 4 * ((RA + 3) / 4) * C::W, TB = (RB + 3) / 4;
-    static_assert(kACols + 4 * TB * C::W == C::kCols, "scale columns of a stage");
-    static_assert(kSets == 2, "a set takes two of four words");
+    constexpr int W = C::W, kACols = 4 * ((RA + 3) / 4) * W, P = kGroup * W / 4;
+    static_assert(kACols + 4 * ((RB + 3) / 4) * W == C::kCols, "scale columns of a stage");
+    static_assert(kSets == 2 && kGroup % 2 == 0, "sets take stages in turn");
     const Params &p = *v.p;
     const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3;
     const int k_stages = (p.K + kStageK - 1) / kStageK;
     const int set = ((threadIdx.x >> 5) - kConvertWarp) >> 2;
     uint32_t bad = 0;
     bool ok = true;
-    const uint8_t *mine = g.bytes + lane * 16 + set * 8;
-    // NV: the set's columns inside the stage's.
-    const uint32_t a_at = sf_tmem + (kNv ? set * 8 : 0), b_at = sf_tmem + kACols + (kNv ? set * 8 * TB : 0);
+    // MXFP4: a piece is two stages, the set's the half it starts at; NVFP4: one.
+    const uint8_t *mine = g.bytes + lane * 16 + (kNv ? set * g.piece_bytes : set * 8);
     Ring raw, r;                  // staged group, this set's next stage
-    uint32_t sf = 0;              // NV: scale slot
-    if (!kNv && set) r.next(n_stages);
+    uint32_t sf = set;            // NVFP4: scale slot
+    if (set) r.next(n_stages);
     for (int j = v.first; ok && j < v.total; j += v.step) {
         for (int k0 = 0; ok && k0 < k_stages; k0 += kGroup) {
             ok = wait(&g.full[raw.slot], raw.phase, v.abort_flag, p.status, p.wait_limit_ns);
             const uint8_t *piece = mine + raw.slot * P * g.piece_bytes;
             const int end = min(k0 + kGroup, k_stages);
 #pragma unroll 1
-            for (int ks = k0; ok && ks < end; ks += G, piece += g.piece_bytes) {
-                uint32_t wa[RA][2], wb[RB][2];
-                read_words(piece + first_a * 512, wa);
-                read_words(piece + first_b * 512, wb);
-                // The four warps of a set read the same bytes; each checks a quarter.
+            for (int ks = k0; ok && ks < end; ks += 2, piece += (kNv ? 2 : 1) * g.piece_bytes) {
+                const int by = ks + 2 <= k_stages ? 2 : 1;
+                if (ks + set < k_stages) {     // an odd last stage is the first set's
+                    uint32_t wa[RA][W], wb[RB][W];
+                    read_words(piece + first_a * 512, wa);
+                    read_words(piece + first_b * 512, wb);
+                    // The four warps read the same bytes; each checks a quarter.
 #pragma unroll
-                for (int i = 0; i < (RA + RB + 3) / 4; ++i)
-                    if (4 * i + 3 < RA + RB || quarter + 4 * i < RA + RB) {
-                        const uint2 x = *reinterpret_cast<const uint2 *>(piece + (quarter + 4 * i) * 512);
-                        bad |= bad_bits<kNv>(x.x) | bad_bits<kNv>(x.y);
-                    }
-                if (kNv || ks + set < k_stages) {     // an odd last stage is the first set's
+                    for (int i = 0; i < (RA + RB + 3) / 4; ++i)
+                        if (4 * i + 3 < RA + RB || quarter + 4 * i < RA + RB) {
+                            uint32_t x[1][W];
+                            read_words(piece + (quarter + 4 * i) * 512, x);
+#pragma unroll
+                            for (int k = 0; k < W; ++k) bad |= bad_bits<kNv>(x[0][k]);
+                        }
                     const bool back = r.slot < 2;
                     if constexpr (kNv)
                         ok = wait(&empty[back ? r.slot + n_stages - 2 : r.slot - 2], r.phase ^ back, v.abort_flag,
@@ -444,16 +435,16 @@ __device__ __forceinline__ void convert_scales(const ScaleEnv &v, const Staging 
                         ok = wait(&empty[r.slot], r.phase ^ 1u, v.abort_flag, p.status, p.wait_limit_ns);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t at = (kNv ? sf : r.slot) * C::kCols;
-                    store_words<RA, true, C::W>(a_at + at, wa);
-                    store_words<RB, false, C::W>(b_at + at, wb);
+                    const uint32_t at = sf_tmem + (kNv ? sf : r.slot) * C::kCols;
+                    store_words<RA, W, true>(at, wa);
+                    store_words<RB, W, false>(at + kACols, wb);
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&full[r.slot]);
                 }
-                sf ^= 1u;
-                r.next(n_stages, !kNv && ks + 2 <= k_stages ? 2 : 1);
+                sf ^= by & 1;
+                r.next(n_stages, by);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&g.empty[raw.slot]);
@@ -661,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kProducerWarp) tmem_alloc(tmem_slot, kTmemCols);
     if (tid == 0) {
         for (uint32_t s = 0; s < n_stages; ++s) {
-            mbar_init(&full[s], 1 + kScaleArrivals<kNv>);
+            mbar_init(&full[s], 1 + 4);
             mbar_init(&empty[s], 1);
         }
         init_scale_bars(raw_bars);
@@ -1069,7 +1060,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == kProducerWarp) tmem_alloc_pair(tmem_slot, kTmemCols);
     if (tid == 0) {
         for (uint32_t s = 0; s < n_stages; ++s) {
-            mbar_init(&full[s], 1 + kScaleArrivals<kNv> + (rank == 0 ? 1 : 0));
+            mbar_init(&full[s], 1 + 4 + (rank == 0 ? 1 : 0));
             mbar_init(&empty[s], 1);
         }
         init_scale_bars(raw_bars);
