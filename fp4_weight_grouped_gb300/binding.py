@@ -49,6 +49,8 @@ def library_path() -> str:
 def load(path: str | None = None):
     """Load the shared library (it must have been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             p = path or build_lib.LIB
@@ -118,12 +120,20 @@ def status_string(status: int) -> str:
 
 
 def _ptr(t):
-    return None if t is None else C.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+# The current stream's handle without building a Stream object (4 us a call, as
+# long as a small kernel), where torch has the calls for it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
 def _stream(stream=None):
+    if stream is None and _raw_stream and _raw_device and torch.cuda.is_initialized():
+        return _raw_stream(_raw_device())
     s = stream if stream is not None else torch.cuda.current_stream()
-    return C.c_void_p(s.cuda_stream)
+    return s.cuda_stream
 
 
 def _check(rc: int, where: str):
@@ -465,14 +475,15 @@ def mxfp4_to_nvfp4(scales: torch.Tensor, out=None, workspace: torch.Tensor | Non
 
 def _need(name: str, t: torch.Tensor, shape, *dtypes):
     """The library takes raw pointers: a tensor it would misread is refused here."""
+    if t.dtype in dtypes and t.shape == shape and t.is_contiguous() and t.is_cuda:
+        return
     if t.dtype not in dtypes:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: not contiguous")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: not a CUDA tensor")
+    raise ValueError(f"{name}: not a CUDA tensor")
 
 
 def _rows_of(name: str, t: torch.Tensor) -> int:

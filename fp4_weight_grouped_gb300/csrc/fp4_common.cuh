@@ -79,4 +79,23 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
     return mag | (w & (mag + 0x77777777u) & 0x88888888u);
 }
 
+// Eight e2m1 codes (value j in nibble j) -> their values.
+__device__ __forceinline__ void e2m1x8_values(uint32_t w, float (&v)[8]) {
+    uint32_t h[4];
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+            "cvt.f32.f16 %0, lo;\n\tcvt.f32.f16 %1, hi;\n\t}"
+            : "=f"(v[2 * i]), "=f"(v[2 * i + 1])
+            : "r"(h[i]));
+}
+
 }  // namespace moe

@@ -1,10 +1,10 @@
 // Quantisation of activation rows to MXFP4 or NVFP4 (the rules are in
 // fp4_common.cuh), with the routing permutation in the load.
 //
-// A thread owns 8 consecutive elements; a block of 32 (16) elements is 4 (2)
-// lanes, whose maximum two (one) shuffles find.  A warp takes 256 elements of
-// one row at a time, so its loads, code words and values are contiguous.  Bound:
-// HBM; an element costs about ten instructions.
+// A lane owns 16 consecutive elements: an NV block, or half an MX block, whose other
+// half one shuffle reaches.  A warp takes 512 elements of one row at a time, so its
+// loads, code words and values are contiguous.  Magnitudes are compared as integers,
+// for bf16 two in a word.  Bound: HBM.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -18,14 +18,76 @@ namespace quant {
 
 constexpr int kThreads = 256;
 
+// Sixteen elements at p as f32, and the largest magnitude's f32 bits.
+__device__ __forceinline__ uint32_t load16(const float *p, int vec, float (&v)[16]) {
+    if (vec) {
+        float a[8], b[8];
+        load_row<8>(p, a);
+        load_row<8>(p + 8, b);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) { v[e] = a[e]; v[8 + e] = b[e]; }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = __ldg(p + e);
+    }
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) m = max(m, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+    return m;
+}
+
+__device__ __forceinline__ uint32_t load16(const __nv_bfloat16 *p, int vec, float (&v)[16]) {
+    uint32_t w[8];
+    if (vec) {
+        const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p)), b = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
+        w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+        w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+    } else {
+        const uint16_t *u = reinterpret_cast<const uint16_t *>(p);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = __ldg(u + 2 * i) | static_cast<uint32_t>(__ldg(u + 2 * i + 1)) << 16;
+    }
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+        v[2 * i] = bf16_low(w[i]);
+        v[2 * i + 1] = bf16_high(w[i]);
+    }
+    return max(m & 0xFFFF0000u, m << 16);
+}
+
+// Sixteen values, to be evicted first: they are not read again here, and x's rows,
+// which are (once for each choice of a token), stay in L2.
+__device__ __forceinline__ void store_stream(void *p, const uint32_t (&w)[8]) {
+    __stcs(static_cast<uint4 *>(p), make_uint4(w[0], w[1], w[2], w[3]));
+    __stcs(static_cast<uint4 *>(p) + 1, make_uint4(w[4], w[5], w[6], w[7]));
+}
+
+__device__ __forceinline__ void store16(float *p, const float (&v)[16]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint32_t w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(v[8 * h + e]);
+        store_stream(p + 8 * h, w);
+    }
+}
+
+__device__ __forceinline__ void store16(__nv_bfloat16 *p, const float (&v)[16]) {
+    uint32_t w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = bf16_pair(v[2 * e], v[2 * e + 1]);
+    store_stream(p, w);
+}
+
 template <typename T, bool kNv, typename V>
 __global__ void __launch_bounds__(kThreads)
     quantize_kernel(const T *x, int64_t x_rows, int64_t x_stride, int x_vec, int K, const int32_t *row_index,
                     int index_div, int64_t rows, const float *tensor_scale, uint8_t *codes, uint8_t *scales,
                     V *values, int *status) {
-    constexpr int kBlock = kNv ? 16 : 32;
     const int lane = threadIdx.x & 31;
-    const int segs = (K + 255) / 256;
+    const int segs = (K + 511) / 512;
     const int64_t total = rows * segs;
     const int64_t step = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
     float g = 1.0f;
@@ -35,8 +97,8 @@ __global__ void __launch_bounds__(kThreads)
     }
     const float g6 = 6.0f * g;
     for (int64_t i = blockIdx.x * static_cast<int64_t>(kThreads / 32) + (threadIdx.x >> 5); i < total; i += step) {
-        const int64_t r = i / segs;
-        const int k0 = static_cast<int>(i - r * segs) * 256 + lane * 8;
+        const int64_t r = total <= UINT32_MAX ? static_cast<uint32_t>(i) / static_cast<uint32_t>(segs) : i / segs;
+        const int k0 = static_cast<int>(i - r * segs) * 512 + lane * 16;
         int64_t src = r;
         bool have = true;
         if (row_index) {
@@ -45,60 +107,44 @@ __global__ void __launch_bounds__(kThreads)
             have = idx >= 0 && src < x_rows;
             if (!have && lane == 0) set_status(status, MOE_ERR_DATA);
         }
-        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (have && k0 < K) {
-            const T *p = x + src * x_stride + k0;
-            if (x_vec) {
-                load_row<8>(p, v);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    float one[1];
-                    load_row<1>(p + e, one);
-                    v[e] = one[0];
-                }
-            }
-        }
+        float v[16] = {};
         uint32_t m = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(v[e]) & 0x7FFFFFFFu);
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        if constexpr (!kNv) m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        if (have && k0 < K) m = load16(x + src * x_stride + k0, x_vec, v);
+        if constexpr (!kNv) m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        if (k0 >= K) continue;
         uint32_t byte;
         float inv, unit;
-        bool nan;
         if constexpr (kNv) {
             byte = nv_scale_byte(m, g6);
             inv = nv_inverse(byte, g);
             unit = e4m3_value(byte);
-            nan = byte == 0x7Fu;
         } else {
             byte = mx_scale_byte(m);
             inv = mx_inverse(byte);
             unit = mx_scale_value(byte);
-            nan = byte == 255u;
         }
+        uint32_t w[2];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = nan ? 0.0f : v[e] * inv;
-        const uint32_t w = e2m1x8(v);
-        if (k0 >= K) continue;
-        *reinterpret_cast<uint32_t *>(codes + r * (K / 2) + k0 / 2) = w;
-        if (k0 % kBlock == 0) scales[r * (K / kBlock) + k0 / kBlock] = static_cast<uint8_t>(byte);
+        for (int h = 0; h < 2; ++h) {
+            float q[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) q[e] = v[8 * h + e] * inv;
+            w[h] = byte == (kNv ? 0x7Fu : 255u) ? 0u : e2m1x8(q);
+        }
+        *reinterpret_cast<uint2 *>(codes + r * (K / 2) + k0 / 2) = make_uint2(w[0], w[1]);
+        if (kNv || (k0 & 16) == 0) scales[r * (K / (kNv ? 16 : 32)) + k0 / (kNv ? 16 : 32)] = static_cast<uint8_t>(byte);
         if (values) {
             // The values the codes stand for: exact in bf16 for MX; in f32 one
             // rounding (the product with g) for NV.
-            float o[8];
+            float o[16];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const uint32_t c = (w >> (4 * e)) & 15u, mag = c & 7u;
-                // e2m1 magnitude from its bits: (mag < 2) 0, 0.5; else 1.f * 2^(e - 1)
-                const float a = mag < 2u ? 0.5f * static_cast<float>(mag)
-                                         : __uint_as_float((mag << 22) + (126u << 23));
-                const float s = c & 8u ? -a : a;
-                o[e] = s * unit;
-                if constexpr (kNv) o[e] *= g;
+            for (int h = 0; h < 2; ++h) {
+                float e8[8];
+                e2m1x8_values(w[h], e8);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[8 * h + e] = kNv ? e8[e] * unit * g : e8[e] * unit;
             }
-            store_row<8>(values + r * K + k0, o);
+            store16(values + r * K + k0, o);
         }
     }
 }
@@ -109,7 +155,7 @@ namespace {
 
 template <typename T, bool kNv, typename V>
 void start(const Fp4Quant &q, V *values, cudaStream_t stream, int num_sms) {
-    const int64_t warps = q.rows * ((q.K + 255) / 256);
+    const int64_t warps = q.rows * ((q.K + 511) / 512);
     int64_t blocks = (warps + 7) / 8;
     const int64_t cap = static_cast<int64_t>(num_sms) * 8;
     if (blocks > cap) blocks = cap;

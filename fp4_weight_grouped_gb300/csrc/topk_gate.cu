@@ -93,13 +93,13 @@ __global__ void __launch_bounds__(kThreads)
         const uint32_t top = __reduce_max_sync(kAll, best);
         const uint32_t e = __reduce_min_sync(kAll, best == top ? lane + 32u * at : 0xFFFFFFFFu);
         if (static_cast<int>(e & 31u) == lane) {
-            float x = 0.0f;
+            // The value again from memory: a register picked by a run-time index would
+            // put the row into local memory.
+            const float x = exp_of(load_one(row + e), m);
 #pragma unroll
-            for (int i = 0; i < R; ++i)
-                if (i == static_cast<int>(e >> 5)) { x = v[i]; key[i] = 0u; }
+            for (int i = 0; i < R; ++i) key[i] = i == static_cast<int>(e >> 5) ? 0u : key[i];
             scan();
             out_id[j] = static_cast<int32_t>(e);
-            x = exp_of(x, m);
             if (renorm) { out_w[j] = x; total += x; }
             else out_w[j] = sum == 0.0f ? 0.0f : x / sum;
         }
@@ -136,9 +136,9 @@ __global__ void __launch_bounds__(kThreads)
         const int e = __ldg(id + j);
         const float dj = __ldg(d + j);
         if (static_cast<unsigned>(e) < static_cast<unsigned>(E) && (e & 31) == lane) {
+            chosen |= 1u << (e >> 5);
 #pragma unroll
-            for (int i = 0; i < R; ++i)
-                if (i == (e >> 5)) { grad[i] += dj; chosen |= 1u << i; }
+            for (int i = 0; i < R; ++i) grad[i] += i == (e >> 5) ? dj : 0.0f;
         }
     }
 #pragma unroll
