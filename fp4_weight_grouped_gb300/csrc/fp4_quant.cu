@@ -81,14 +81,16 @@ __device__ __forceinline__ void store16(__nv_bfloat16 *p, const float (&v)[16]) 
     store_stream(p, w);
 }
 
+// A warp's task is `span` consecutive 512-element segments of one row (so that the
+// index arithmetic, as long as a segment's, is paid once a task).
 template <typename T, bool kNv, typename V>
 __global__ void __launch_bounds__(kThreads)
-    quantize_kernel(const T *x, int64_t x_rows, int64_t x_stride, int x_vec, int K, const int32_t *row_index,
+    quantize_kernel(const T *x, int64_t x_rows, int64_t x_stride, int x_vec, int K, int span, const int32_t *row_index,
                     int index_div, int64_t rows, const float *tensor_scale, uint8_t *codes, uint8_t *scales,
                     V *values, int *status) {
     const int lane = threadIdx.x & 31;
-    const int segs = (K + 511) / 512;
-    const int64_t total = rows * segs;
+    const int tasks = (K + 512 * span - 1) / (512 * span);      // a row
+    const int64_t total = rows * tasks;
     const int64_t step = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
     float g = 1.0f;
     if constexpr (kNv) {
@@ -97,8 +99,8 @@ __global__ void __launch_bounds__(kThreads)
     }
     const float g6 = 6.0f * g;
     for (int64_t i = blockIdx.x * static_cast<int64_t>(kThreads / 32) + (threadIdx.x >> 5); i < total; i += step) {
-        const int64_t r = total <= UINT32_MAX ? static_cast<uint32_t>(i) / static_cast<uint32_t>(segs) : i / segs;
-        const int k0 = static_cast<int>(i - r * segs) * 512 + lane * 16;
+        const int64_t r = tasks == 1 ? i : i / tasks;
+        const int k_first = static_cast<int>(i - r * tasks) * span * 512, k_end = min(K, k_first + span * 512);
         int64_t src = r;
         bool have = true;
         if (row_index) {
@@ -107,44 +109,50 @@ __global__ void __launch_bounds__(kThreads)
             have = idx >= 0 && src < x_rows;
             if (!have && lane == 0) set_status(status, MOE_ERR_DATA);
         }
-        float v[16] = {};
-        uint32_t m = 0;
-        if (have && k0 < K) m = load16(x + src * x_stride + k0, x_vec, v);
-        if constexpr (!kNv) m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        if (k0 >= K) continue;
-        uint32_t byte;
-        float inv, unit;
-        if constexpr (kNv) {
-            byte = nv_scale_byte(m, g6);
-            inv = nv_inverse(byte, g);
-            unit = e4m3_value(byte);
-        } else {
-            byte = mx_scale_byte(m);
-            inv = mx_inverse(byte);
-            unit = mx_scale_value(byte);
-        }
-        uint32_t w[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            float q[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) q[e] = v[8 * h + e] * inv;
-            w[h] = byte == (kNv ? 0x7Fu : 255u) ? 0u : e2m1x8(q);
-        }
-        *reinterpret_cast<uint2 *>(codes + r * (K / 2) + k0 / 2) = make_uint2(w[0], w[1]);
-        if (kNv || (k0 & 16) == 0) scales[r * (K / (kNv ? 16 : 32)) + k0 / (kNv ? 16 : 32)] = static_cast<uint8_t>(byte);
-        if (values) {
-            // The values the codes stand for: exact in bf16 for MX; in f32 one
-            // rounding (the product with g) for NV.
-            float o[16];
+        const T *from = x + src * x_stride;
+        uint8_t *to = codes + r * (K / 2), *to_scale = scales + r * (K / (kNv ? 16 : 32));
+        V *to_value = values ? values + r * K : nullptr;
+        for (int k1 = k_first; k1 < k_end; k1 += 512) {
+            const int k0 = k1 + lane * 16;
+            float v[16] = {};
+            uint32_t m = 0;
+            if (have && k0 < K) m = load16(from + k0, x_vec, v);
+            if constexpr (!kNv) m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            if (k0 >= K) continue;
+            uint32_t byte;
+            float inv, unit;
+            if constexpr (kNv) {
+                byte = nv_scale_byte(m, g6);
+                inv = nv_inverse(byte, g);
+                unit = e4m3_value(byte);
+            } else {
+                byte = mx_scale_byte(m);
+                inv = mx_inverse(byte);
+                unit = mx_scale_value(byte);
+            }
+            uint32_t w[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                float e8[8];
-                e2m1x8_values(w[h], e8);
+                float q[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) o[8 * h + e] = kNv ? e8[e] * unit * g : e8[e] * unit;
+                for (int e = 0; e < 8; ++e) q[e] = v[8 * h + e] * inv;
+                w[h] = byte == (kNv ? 0x7Fu : 255u) ? 0u : e2m1x8(q);
             }
-            store16(values + r * K + k0, o);
+            *reinterpret_cast<uint2 *>(to + k0 / 2) = make_uint2(w[0], w[1]);
+            if (kNv || (k0 & 16) == 0) to_scale[k0 / (kNv ? 16 : 32)] = static_cast<uint8_t>(byte);
+            if (to_value) {
+                // The values the codes stand for: exact in bf16 for MX; in f32 one
+                // rounding (the product with g) for NV.
+                float o[16];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float e8[8];
+                    e2m1x8_values(w[h], e8);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) o[8 * h + e] = kNv ? e8[e] * unit * g : e8[e] * unit;
+                }
+                store16(to_value + k0, o);
+            }
         }
     }
 }
@@ -155,14 +163,17 @@ namespace {
 
 template <typename T, bool kNv, typename V>
 void start(const Fp4Quant &q, V *values, cudaStream_t stream, int num_sms) {
-    const int64_t warps = q.rows * ((q.K + 511) / 512);
+    // Whole rows a warp where that leaves two tasks a warp of the grid, else segments.
+    const int segs = (q.K + 511) / 512;
+    const int span = q.rows >= static_cast<int64_t>(num_sms) * 64 * 2 ? segs : 1;
+    const int64_t warps = q.rows * ((segs + span - 1) / span);
     int64_t blocks = (warps + 7) / 8;
     const int64_t cap = static_cast<int64_t>(num_sms) * 8;
     if (blocks > cap) blocks = cap;
     const T *x = static_cast<const T *>(q.x);
     const int x_vec = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && (q.x_stride * sizeof(T)) % 16 == 0;
     quant::quantize_kernel<T, kNv, V><<<static_cast<int>(blocks), quant::kThreads, 0, stream>>>(
-        x, q.x_rows, q.x_stride, x_vec, q.K, q.row_index, q.index_div, q.rows, q.tensor_scale, q.codes, q.scales,
+        x, q.x_rows, q.x_stride, x_vec, q.K, span, q.row_index, q.index_div, q.rows, q.tensor_scale, q.codes, q.scales,
         values, q.status);
 }
 

@@ -88,29 +88,100 @@ __global__ void __launch_bounds__(kThreads)
     }
     int32_t *out_id = ids + static_cast<int64_t>(t) * k;
     float *out_w = weights + static_cast<int64_t>(t) * k;
-    float total = 0.0f;
     for (int j = 0; j < k; ++j) {
         const uint32_t top = __reduce_max_sync(kAll, best);
         const uint32_t e = __reduce_min_sync(kAll, best == top ? lane + 32u * at : 0xFFFFFFFFu);
+        if (lane == 0) out_id[j] = static_cast<int32_t>(e);
         if (static_cast<int>(e & 31u) == lane) {
-            // The value again from memory: a register picked by a run-time index would
-            // put the row into local memory.
-            const float x = exp_of(load_one(row + e), m);
 #pragma unroll
             for (int i = 0; i < R; ++i) key[i] = i == static_cast<int>(e >> 5) ? 0u : key[i];
             scan();
-            out_id[j] = static_cast<int32_t>(e);
-            if (renorm) { out_w[j] = x; total += x; }
-            else out_w[j] = sum == 0.0f ? 0.0f : x / sum;
         }
+    }
+    // The weights, a chosen expert a lane: its logit comes from memory again (a
+    // register picked by a run-time index would put the row into local memory).
+    __syncwarp();
+    float total = 0.0f;
+    for (int j = lane; j < k; j += 32) {
+        const float x = exp_of(load_one(row + out_id[j]), m);
+        if (renorm) { out_w[j] = x; total += x; }
+        else out_w[j] = sum == 0.0f ? 0.0f : x / sum;
     }
     if (renorm) {
         total = warp_sum(total);
-        __syncwarp();
         for (int j = lane; j < k; j += 32) out_w[j] = total == 0.0f ? 0.0f : out_w[j] / total;
     }
 }
 
+// Gradient for k <= 32: chosen expert j and its dw in lane j.  An id that appears
+// more than once is the lowest such lane's, with the sum of their dw in lane order;
+// one outside [0, E) is nobody's.
+template <typename T, int R>
+__global__ void __launch_bounds__(kThreads)
+    gate_backward_small_kernel(const T *logits, int64_t stride, int n, int E, int k, int renorm, const int32_t *ids,
+                               const float *dw, T *dlogits) {
+    const int lane = threadIdx.x & 31;
+    const int t = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    if (t >= n) return;
+    const T *row = logits + t * stride;
+    T *out = dlogits + static_cast<int64_t>(t) * E;
+    int id = -1;
+    float d = 0.0f;
+    if (lane < k) {
+        id = __ldg(ids + static_cast<int64_t>(t) * k + lane);
+        d = __ldg(dw + static_cast<int64_t>(t) * k + lane);
+        if (static_cast<unsigned>(id) >= static_cast<unsigned>(E)) id = -1;
+    }
+    const uint32_t same = __match_any_sync(kAll, id);
+    const bool mine = id >= 0 && __ffs(same) - 1 == lane;
+    if (__any_sync(kAll, id >= 0 && (same & (same - 1)) != 0)) {
+        float sum = 0.0f;
+        for (int l = 0; l < 32; ++l) {
+            const float x = __shfl_sync(kAll, d, l);
+            if (same >> l & 1u) sum += x;
+        }
+        d = sum;
+    }
+    float l = mine ? load_one(row + id) : -CUDART_INF_F;
+    float v[R];
+    float m = l;                  // fmaxf skips NaN, as the forward's keys do
+    if (!renorm) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int e = lane + 32 * i;
+            v[i] = e < E ? load_one(row + e) : -CUDART_INF_F;
+            m = fmaxf(m, v[i]);
+        }
+    }
+    if (m != m) m = -CUDART_INF_F;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
+    l = exp_of(l, m);
+    float sum = renorm ? l : 0.0f;
+    if (!renorm) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            v[i] = exp_of(v[i], m);
+            sum += v[i];
+        }
+    }
+    sum = warp_sum(sum);
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    l *= inv;
+    const float dot = warp_sum(mine ? l * d : 0.0f);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int e = lane + 32 * i;
+        // (renorm: p is 0 here, and a NaN among the chosen reaches every expert)
+        const float g[1] = {0.0f - (renorm ? 0.0f : v[i]) * inv * dot};
+        if (e < E) store_row<1>(out + e, g);
+    }
+    __syncwarp();                 // the chosen experts' gradients replace what was just stored
+    const float g[1] = {l * (d - dot)};
+    if (mine) store_row<1>(out + id, g);
+}
+
+// Gradient for any k.
 template <typename T, int R>
 __global__ void __launch_bounds__(kThreads)
     gate_backward_kernel(const T *logits, int64_t stride, int n, int E, int k, int renorm, const int32_t *ids,
@@ -174,7 +245,10 @@ template <typename T, int R>
 void start(const Gate &g, bool backward, cudaStream_t stream) {
     const int blocks = (g.T + kThreads / 32 - 1) / (kThreads / 32);
     const T *l = static_cast<const T *>(g.logits);
-    if (backward)
+    if (backward && g.k <= 32)
+        gate_backward_small_kernel<T, R><<<blocks, kThreads, 0, stream>>>(l, g.stride, g.T, g.E, g.k, g.renorm, g.ids,
+                                                                         g.dw, static_cast<T *>(g.dlogits));
+    else if (backward)
         gate_backward_kernel<T, R><<<blocks, kThreads, 0, stream>>>(l, g.stride, g.T, g.E, g.k, g.renorm, g.ids, g.dw,
                                                                    static_cast<T *>(g.dlogits));
     else
