@@ -52,7 +52,8 @@ constexpr int kProducerWarp = 0, kIssuerWarp = 1;
 constexpr int kWCopyWarp = 2, kACopyWarp = 3;          // scale bytes of weights, of tokens
 constexpr int kSets = 2;                               // converter sets, on stages in turn
 constexpr int kConvertWarp = 4, kEpilogueWarp = kConvertWarp + 4 * kSets;   // four warps a set: one a lane quarter
-constexpr int kThreads = 32 * (kEpilogueWarp + 4);
+constexpr int kHalves = 2;                             // epilogue warps a lane quarter
+constexpr int kThreads = 32 * (kEpilogueWarp + 4 * kHalves);
 constexpr int kMaxE = 1024;
 constexpr int kTileN = 128;                    // weight rows a tile (MMA M)
 constexpr int kStageBytesRow = 128;            // 256 k
@@ -463,31 +464,34 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&v)[8]) {
                  : "r"(taddr));
 }
 
-// f32 / bf16 sums: lane = weight row, so a warp stores 32 consecutive columns
-// of one token row at a time.
-__device__ __forceinline__ void store_plain(const Params &p, const Item &it, uint32_t acc, int n, float scale,
-                                            uint64_t *acc_empty) {
-    const int lane = threadIdx.x & 31;
-    for (int c = 0; c < it.nvalid; c += 16) {
+// The sums of a buffer are in registers: release it.
+__device__ __forceinline__ void release_acc(uint64_t *acc_empty) {
+    tc_fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(acc_empty);
+}
+
+// f32 / bf16 sums: lane = weight row, so a warp stores 32 consecutive columns of one
+// token row at a time; the two warps of a lane quarter take 16 tokens in turn.
+__device__ __forceinline__ void store_plain(const Params &p, const Item &it, uint32_t acc, int n, int half,
+                                            float scale, uint64_t *acc_empty) {
+    if (half * 16 >= it.nvalid) release_acc(acc_empty);
+    for (int c = half * 16; c < it.nvalid; c += 16 * kHalves) {
         uint32_t v[16];
         __syncwarp();
         tmem_ld16(acc + c, v);
         tmem_ld_wait();
-        if (c + 16 >= it.nvalid) {      // the sums are in registers: release the buffer
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(acc_empty);
-        }
+        if (c + 16 * kHalves >= it.nvalid) release_acc(acc_empty);
         if (n < p.N) {
             const size_t off = static_cast<size_t>(it.row0 + c) * p.N + n;
             const int left = it.nvalid - c;
             if (p.out_bf16) {
-                __nv_bfloat16 *o = reinterpret_cast<__nv_bfloat16 *>(p.out) + off;
+                __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.out) + off;
 #pragma unroll
                 for (int t = 0; t < 16; ++t)
                     if (t < left) o[static_cast<size_t>(t) * p.N] = __float2bfloat16_rn(__uint_as_float(v[t]) * scale);
             } else {
-                float *o = reinterpret_cast<float *>(p.out) + off;
+                float *o = static_cast<float *>(p.out) + off;
 #pragma unroll
                 for (int t = 0; t < 16; ++t)
                     if (t < left) o[static_cast<size_t>(t) * p.N] = __uint_as_float(v[t]) * scale;
@@ -499,64 +503,76 @@ __device__ __forceinline__ void store_plain(const Params &p, const Item &it, uin
 // SwiGLU sums -> h = silu(g) * u in f32 -> 4-bit codes and block scales.  The
 // warp's lanes are 32 consecutive h columns; n0w is the first of them.
 template <bool kNv>
-__device__ __forceinline__ void store_swiglu(const Params &p, const Item &it, uint32_t acc, int n0w,
+__device__ __forceinline__ void store_swiglu(const Params &p, const Item &it, uint32_t acc, int n0w, int half,
                                              float scale, float h_scale, uint64_t *acc_empty) {
     const int lane = threadIdx.x & 31;
     const int t8 = lane & 7, q = lane >> 3;
     const float g6 = 6.0f * h_scale;
-    for (int c = 0; c < it.nvalid; c += 8) {
+    if (half * 8 >= it.nvalid) release_acc(acc_empty);
+    for (int c = half * 8; c < it.nvalid; c += 8 * kHalves) {
         uint32_t g[8], u[8];
         __syncwarp();
         tmem_ld8(acc + c, g);
         tmem_ld8(acc + Shape<kNv, true>::kAccStep + c, u);
         tmem_ld_wait();
-        if (c + 8 >= it.nvalid) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(acc_empty);
-        }
+        if (c + 8 * kHalves >= it.nvalid) release_acc(acc_empty);
         if (n0w >= p.I) continue;          // warp-uniform: I is a multiple of 32
         float h[8];
-        uint32_t my_byte = 0;
+        uint32_t m[8];
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
             h[t] = silu_f32(__uint_as_float(g[t]) * scale) * (__uint_as_float(u[t]) * scale);
-            const uint32_t mag = __float_as_uint(h[t]) & 0x7FFFFFFFu;
-            uint32_t byte;
-            float inv;
-            if constexpr (kNv) {
-                uint32_t m = mag;
+            m[t] = __float_as_uint(h[t]) & 0x7FFFFFFFu;
+        }
+        uint8_t *out_scale = p.out_scales + static_cast<size_t>(it.row0 + c) * (p.I / (kNv ? 16 : 32));
+        if constexpr (kNv) {
+            // Maxima of 8 tokens over the 16 lanes of a block by halving: each step
+            // sends half of the tokens a lane still has to its partner.  Lane l ends
+            // with the token of bits 3, 2, 1 of l, so the two divisions are done once,
+            // not once a token; the factors come back by a shuffle each.
+            uint32_t a[4], b[2], top;
+            const bool h8 = lane & 8, h4 = lane & 4, h2 = lane & 2;
 #pragma unroll
-                for (int d = 8; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-                byte = nv_scale_byte(m, g6);
-                inv = nv_inverse(byte, h_scale);
-                h[t] = byte == 0x7Fu ? 0.0f : h[t] * inv;
-            } else {
-                byte = mx_scale_byte(__reduce_max_sync(0xffffffffu, mag));
-                h[t] = byte == 255u ? 0.0f : h[t] * mx_inverse(byte);
+            for (int i = 0; i < 4; ++i)
+                a[i] = max(h8 ? m[4 + i] : m[i], __shfl_xor_sync(0xffffffffu, h8 ? m[i] : m[4 + i], 8));
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                b[i] = max(h4 ? a[2 + i] : a[i], __shfl_xor_sync(0xffffffffu, h4 ? a[i] : a[2 + i], 4));
+            top = max(h2 ? b[1] : b[0], __shfl_xor_sync(0xffffffffu, h2 ? b[0] : b[1], 2));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            const uint32_t byte = nv_scale_byte(top, g6);
+            const float inv = nv_inverse(byte, h_scale);
+            const int token = (lane >> 1) & 7, t = (token >> 2 & 1) << 2 | (token >> 1 & 1) << 1 | (token & 1);
+            if (!(lane & 1) && c + t < it.nvalid)
+                out_scale[static_cast<size_t>(t) * (p.I / 16) + n0w / 16 + (lane >> 4)] = static_cast<uint8_t>(byte);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float f = __shfl_sync(0xffffffffu, inv, (lane & 16) | k << 1);
+                h[k] = f == 0.0f ? 0.0f : h[k] * f;       // 0: zeros, or an infinity or NaN in the block
             }
-            if (t == t8) my_byte = byte;
+        } else {
+            uint32_t my_byte = 0;
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {
+                const uint32_t byte = mx_scale_byte(__reduce_max_sync(0xffffffffu, m[t]));
+                h[t] = byte == 255u ? 0.0f : h[t] * mx_inverse(byte);
+                if (t == t8) my_byte = byte;
+            }
+            if (q == 0 && c + t8 < it.nvalid)
+                out_scale[static_cast<size_t>(t8) * (p.I / 32) + n0w / 32] = static_cast<uint8_t>(my_byte);
         }
         // Nibble t of w: this lane's column at token c + t.  Transposed over the
         // eight lanes of a group: nibble i becomes column 8 q + i at token c + t8.
         uint32_t w = e2m1x8(h);
 #pragma unroll
-        for (int m = 4; m > 0; m >>= 1) {
-            const uint32_t low = m == 4 ? 0x0000FFFFu : m == 2 ? 0x00FF00FFu : 0x0F0F0F0Fu;
-            const uint32_t o = __shfl_xor_sync(0xffffffffu, w, m);
-            w = (lane & m) ? ((w & ~low) | ((o >> (4 * m)) & low)) : ((w & low) | ((o & low) << (4 * m)));
+        for (int k = 4; k > 0; k >>= 1) {
+            const uint32_t low = k == 4 ? 0x0000FFFFu : k == 2 ? 0x00FF00FFu : 0x0F0F0F0Fu;
+            const uint32_t o = __shfl_xor_sync(0xffffffffu, w, k);
+            w = (lane & k) ? ((w & ~low) | ((o >> (4 * k)) & low)) : ((w & low) | ((o & low) << (4 * k)));
         }
-        if (c + t8 < it.nvalid) {
-            const size_t row = static_cast<size_t>(it.row0 + c + t8);
-            uint8_t *codes = static_cast<uint8_t *>(p.out) + row * (p.I / 2) + n0w / 2;
-            *reinterpret_cast<uint32_t *>(codes + 4 * q) = w;
-            if constexpr (kNv) {
-                // lanes 0..15 have the first block's byte, 16..31 the second's
-                if ((q & 1) == 0) p.out_scales[row * (p.I / 16) + n0w / 16 + (q >> 1)] = my_byte;
-            } else {
-                if (q == 0) p.out_scales[row * (p.I / 32) + n0w / 32] = my_byte;
-            }
-        }
+        if (c + t8 < it.nvalid)
+            *reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(p.out) +
+                                          static_cast<size_t>(it.row0 + c + t8) * (p.I / 2) + n0w / 2 + 4 * q) = w;
     }
 }
 
@@ -658,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         init_scale_bars(raw_bars);
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], 4);
+            mbar_init(&acc_empty[b], 4 * kHalves);
         }
         mbar_init(final_bar, 1);
         mbar_fence_init();
@@ -785,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 n_stages);
         }
     } else {
-        const int quarter = warp & 3;
+        const int quarter = warp & 3, half = (warp - kEpilogueWarp) >> 2;
         const float a2 = kNv ? __ldg(p.a_scale_2) : 1.0f;
         const float h2 = kNv && kSwiglu ? __ldg(p.h_scale_2) : 1.0f;
         if (!(h2 > 0.0f && h2 < __uint_as_float(kF32Inf)) && tid == kThreads - 1) set_status(p.status, MOE_ERR_DATA);
@@ -797,9 +813,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t acc = tmem + buf * kAccCols + (static_cast<uint32_t>(quarter * 32) << 16);
             const float scale = kNv ? __ldg(p.w_scale_2 + it.e) * a2 : 1.0f;
             if constexpr (kSwiglu)
-                store_swiglu<kNv>(p, it, acc, it.n0 + 32 * quarter, scale, h2, &acc_empty[buf]);
+                store_swiglu<kNv>(p, it, acc, it.n0 + 32 * quarter, half, scale, h2, &acc_empty[buf]);
             else
-                store_plain(p, it, acc, it.n0 + 32 * quarter + lane, scale, &acc_empty[buf]);
+                store_plain(p, it, acc, it.n0 + 32 * quarter + lane, half, scale, &acc_empty[buf]);
             buf ^= 1u;
             if (buf == 0) phase ^= 1u;
         }
@@ -839,10 +855,8 @@ constexpr int kPairABytes = 128 * kStageBytesRow;
 constexpr int kPairBBytes = kPairN / 2 * kStageBytesRow;
 constexpr int kPairRing = kPairStages * (kPairABytes + kPairBBytes);
 constexpr int kPairStaging = kDepth * kGroup * (6 + 4) * 512;  // scale bytes on their way to tensor memory
-constexpr int kPatchRow = 36;                  // floats a row of a warp's 32 x 32 transpose
 constexpr int kPairOffStaging = kPairRing;
-constexpr int kPairOffPatch = kPairOffStaging + kPairStaging;
-constexpr int kPairOffRow = kPairOffPatch + 4 * 32 * kPatchRow * 4;
+constexpr int kPairOffRow = kPairOffStaging + kPairStaging;
 constexpr int kPairOffItem = kPairOffRow + (kMaxE + 1) * 4;
 constexpr int kPairOffBars = (kPairOffItem + (kMaxE + 1) * 4 + 7) & ~7;
 constexpr int kPairOffMisc = kPairOffBars + (2 * kPairStages + 4 + 1 + 2 * kDepth) * 8;
@@ -897,28 +911,42 @@ __device__ __forceinline__ void store_sector(void *p, const uint32_t (&v)[8]) {
                  : "memory");
 }
 
-// Plain outputs of one warp: lane = token row, 32 columns at a time.  `vec`: rows are
-// whole 32-byte sectors.  bf16: a lane stores its own columns, two sectors.  f32: a
-// transpose through shared memory, then eight rows of 128 bytes a store; lanes that
-// stored their own four sectors slowed the whole SM's loads (full layer w2 308 ->
-// 334 us).  Otherwise the transpose, a column a lane.
-__device__ __forceinline__ void pair_store_plain(const Params &p, uint32_t acc, int row0, int valid, int n0,
-                                                 int cols, float scale, float *patch, int vec, uint32_t empty_bar) {
+// 16 lanes x 32 columns: lane l holds columns 8 i + 2 (l % 4) + {0, 1} of rows l / 4
+// (v[4 i], v[4 i + 1]) and l / 4 + 8 (v[4 i + 2], v[4 i + 3]).
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr));
+}
+
+__device__ __forceinline__ void release_acc_pair(uint32_t empty_bar) {
+    tc_fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive_cluster(empty_bar);
+}
+
+// Plain outputs of one warp: 32 token rows, 32 columns at a time, the two warps of a
+// lane quarter in turn.  bf16 rows of whole sectors: lane = row, a lane stores its own
+// two sectors.  f32 (and any row alignment): the 16-lane load shape gives four lanes
+// eight consecutive columns of a row, one sector, so no transpose is needed.  (Through
+// shared memory the same blocks took 1,700 cycles each, more than their MMAs; lanes
+// that stored four f32 sectors of their own rows slowed the whole SM's loads.)
+__device__ __forceinline__ void pair_store_plain(const Params &p, uint32_t acc, int row0, int valid, int n0, int half,
+                                                 int cols, float scale, int vec, uint32_t empty_bar) {
     const int lane = threadIdx.x & 31;
-    for (int c = 0; c < cols; c += 32) {
-        uint32_t v[32];
-        __syncwarp();
-        tmem_ld32(acc + c, v);
-        tmem_ld_wait();
-        if (c + 32 >= cols) {          // the last sums are in registers: release the buffer
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(empty_bar);
-        }
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * scale);
+    if (half * 32 >= cols) release_acc_pair(empty_bar);
+    for (int c = half * 32; c < cols; c += 32 * kHalves) {
+        const bool last = c + 32 * kHalves >= cols;
         const int left = p.N - n0 - c;
-        if (vec && p.out_bf16) {
+        if (p.out_bf16 && vec) {
+            uint32_t v[32];
+            __syncwarp();
+            tmem_ld32(acc + c, v);
+            tmem_ld_wait();
+            if (last) release_acc_pair(empty_bar);
             __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.out) + static_cast<size_t>(row0 + lane) * p.N + n0 + c;
             if (lane < valid) {
 #pragma unroll
@@ -926,46 +954,52 @@ __device__ __forceinline__ void pair_store_plain(const Params &p, uint32_t acc, 
                     uint32_t w[8];
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        w[k] = bf16_pair(__uint_as_float(v[i + 2 * k]), __uint_as_float(v[i + 2 * k + 1]));
+                        w[k] = bf16_pair(__uint_as_float(v[i + 2 * k]) * scale, __uint_as_float(v[i + 2 * k + 1]) * scale);
                     if (i < left) store_sector(o + i, w);
                 }
             }
             continue;
         }
-        if (valid <= 0) continue;      // warp-uniform
-#pragma unroll
-        for (int i = 0; i < 32; i += 4)
-            *reinterpret_cast<uint4 *>(patch + lane * kPatchRow + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        uint32_t v[2][16];
         __syncwarp();
-        if (vec) {
-            const int r0 = lane >> 2, k = (lane & 3) * 8;
-            float *o = static_cast<float *>(p.out) + static_cast<size_t>(row0 + r0) * p.N + n0 + c + k;
-            const float *from = patch + r0 * kPatchRow + k;
+        tmem_ld_16x32(acc + c, v[0]);
+        tmem_ld_16x32(acc + c + (16u << 16), v[1]);
+        tmem_ld_wait();
+        if (last) release_acc_pair(empty_bar);
+        const int k = 2 * (lane & 3);
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const int r = 8 * g + (lane >> 2);
+            if (r >= valid) continue;
+            const size_t at = static_cast<size_t>(row0 + r) * p.N + n0 + c + k;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint4 x = *reinterpret_cast<const uint4 *>(from + i * 8 * kPatchRow);
-                const uint4 y = *reinterpret_cast<const uint4 *>(from + i * 8 * kPatchRow + 4);
-                const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-                if (r0 + 8 * i < valid && k < left) store_sector(o + static_cast<size_t>(8 * i) * p.N, w);
+                const float x = __uint_as_float(v[g >> 1][4 * i + 2 * (g & 1)]) * scale;
+                const float y = __uint_as_float(v[g >> 1][4 * i + 2 * (g & 1) + 1]) * scale;
+                if (!p.out_bf16 && vec) {
+                    if (8 * i < left)
+                        *reinterpret_cast<float2 *>(static_cast<float *>(p.out) + at + 8 * i) = make_float2(x, y);
+                } else if (p.out_bf16) {
+                    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.out) + at + 8 * i;
+                    if (8 * i + k < left) o[0] = __float2bfloat16_rn(x);
+                    if (8 * i + k + 1 < left) o[1] = __float2bfloat16_rn(y);
+                } else {
+                    float *o = static_cast<float *>(p.out) + at + 8 * i;
+                    if (8 * i + k < left) o[0] = x;
+                    if (8 * i + k + 1 < left) o[1] = y;
+                }
             }
-        } else if (lane < left)
-#pragma unroll 1
-            for (int r = 0; r < min(32, valid); ++r) {
-                const float f = patch[r * kPatchRow + lane];
-                const size_t off = static_cast<size_t>(row0 + r) * p.N + n0 + c + lane;
-                if (p.out_bf16) static_cast<__nv_bfloat16 *>(p.out)[off] = __float2bfloat16_rn(f);
-                else static_cast<float *>(p.out)[off] = f;
-            }
+        }
     }
 }
 
-// SwiGLU of one warp: lane = token row; blocks of 32 h columns.
+// SwiGLU of one warp: lane = token row; blocks of 32 h columns, from block `half` on.
 template <bool kNv>
 __device__ __forceinline__ void pair_store_swiglu(const Params &p, uint32_t acc, int row0, int valid, int n0,
-                                                  float scale, float h_scale, uint32_t empty_bar) {
+                                                  int half, float scale, float h_scale, uint32_t empty_bar) {
     const int lane = threadIdx.x & 31;
     const float g6 = 6.0f * h_scale;
-    for (int b = 0; b < kPairN / 2; b += 32) {
+    for (int b = 32 * half; b < kPairN / 2; b += 32 * kHalves) {
         float h[32];
 #pragma unroll
         for (int k = 0; k < 32; k += 16) {
@@ -978,11 +1012,7 @@ __device__ __forceinline__ void pair_store_swiglu(const Params &p, uint32_t acc,
             for (int i = 0; i < 16; ++i)
                 h[k + i] = silu_f32(__uint_as_float(g[i]) * scale) * (__uint_as_float(u[i]) * scale);
         }
-        if (b + 32 >= kPairN / 2) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(empty_bar);
-        }
+        if (b + 32 * kHalves >= kPairN / 2) release_acc_pair(empty_bar);
         if (n0 + b >= p.I || lane >= valid) continue;      // I is a multiple of 32
         const size_t row = static_cast<size_t>(row0 + lane);
         uint32_t w[4];
@@ -1027,7 +1057,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     constexpr int kTile = kSwiglu ? kPairN / 2 : kPairN;            // output columns of an item
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    float *patch = reinterpret_cast<float *>(smem + kPairOffPatch);
     int *roff = reinterpret_cast<int *>(smem + kPairOffRow);
     int *ioff = reinterpret_cast<int *>(smem + kPairOffItem);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + kPairOffBars);   // TMA, scale converters (and relay) -> issuer (relay)
@@ -1066,7 +1095,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         init_scale_bars(raw_bars);
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], 8);
+            mbar_init(&acc_empty[b], 2 * 4 * kHalves);
         }
         mbar_init(final_bar, 1);
         mbar_fence_init();
@@ -1199,11 +1228,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 v, g, 6, 0, tmem + kSfCol0 + (static_cast<uint32_t>((warp & 3) * 32) << 16), full, empty, n_stages);
         }
     } else {
-        const int quarter = warp & 3;
+        const int quarter = warp & 3, half = (warp - kEpilogueWarp) >> 2;
         const float a2 = kNv ? __ldg(p.a_scale_2) : 1.0f;
         const float h2 = kNv && kSwiglu ? __ldg(p.h_scale_2) : 1.0f;
         if (!(h2 > 0.0f && h2 < __uint_as_float(kF32Inf)) && tid == kThreads - 1) set_status(p.status, MOE_ERR_DATA);
+        // The three blocks of an item go two to one warp of a lane quarter and one to the
+        // other, the other way round for the next item.
         uint32_t buf = 0, phase = 0;
+        int turn = 0;
         for (int j = first; j < total; j += step) {
             const Item it = decode_item<kPairM, kTile>(j, roff, ioff, E, p.n_tiles);
             int row0, valid;
@@ -1214,12 +1246,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const float scale = kNv ? __ldg(p.w_scale_2 + it.e) * a2 : 1.0f;
             const uint32_t bar = cluster_addr(&acc_empty[buf], 0);
             if constexpr (kSwiglu)
-                pair_store_swiglu<kNv>(p, acc, row0 + quarter * 32, valid - quarter * 32, it.n0, scale, h2, bar);
+                pair_store_swiglu<kNv>(p, acc, row0 + quarter * 32, valid - quarter * 32, it.n0, half ^ turn, scale, h2, bar);
             else
-                pair_store_plain(p, acc, row0 + quarter * 32, valid - quarter * 32, it.n0,
-                                 min(kPairN, (p.N - it.n0 + 31) & ~31), scale, patch + quarter * 32 * kPatchRow,
-                                 out_vec, bar);
+                pair_store_plain(p, acc, row0 + quarter * 32, valid - quarter * 32, it.n0, half,
+                                 min(kPairN, (p.N - it.n0 + 31) & ~31), scale, out_vec, bar);
             buf ^= 1u;
+            turn ^= 1;
             if (buf == 0) phase ^= 1u;
         }
     }
