@@ -589,8 +589,9 @@ moe_status moe_fp4_grouped_gemm(const uint8_t *act_codes, const uint8_t *act_sca
                               group_sizes, E, N, workspace);
     g.out = out;
     g.out_bf16 = out_dtype == MOE_BF16;
-    st = moe::launch_fp4_gemm(g, format == MOE_FP4_NV, false, static_cast<cudaStream_t>(stream), sms);
-    g_last_launches = rows > 0 ? 1 : 0;
+    int launches = 0;
+    st = moe::launch_fp4_gemm(g, format == MOE_FP4_NV, false, static_cast<cudaStream_t>(stream), sms, &launches);
+    g_last_launches = launches;
     return st;
 }
 
@@ -615,8 +616,9 @@ moe_status moe_fp4_grouped_gemm_swiglu(const uint8_t *act_codes, const uint8_t *
     g.out = h_codes;
     g.out_scales = h_scales;
     g.h_scale_2 = h_scale_2;
-    st = moe::launch_fp4_gemm(g, format == MOE_FP4_NV, true, static_cast<cudaStream_t>(stream), sms);
-    g_last_launches = rows > 0 ? 1 : 0;
+    int launches = 0;
+    st = moe::launch_fp4_gemm(g, format == MOE_FP4_NV, true, static_cast<cudaStream_t>(stream), sms, &launches);
+    g_last_launches = launches;
     return st;
 }
 
@@ -662,8 +664,15 @@ moe_status moe_layer_forward_fp4(
                                    group_sizes, E, hidden, workspace);
         g2.out = y2;
         if ((st = moe::launch_fp4_quantize(q, s, sms)) == MOE_OK) ++launches;
-        if (st == MOE_OK && (st = moe::launch_fp4_gemm(g13, nv, true, s, sms)) == MOE_OK) ++launches;
-        if (st == MOE_OK && (st = moe::launch_fp4_gemm(g2, nv, false, s, sms)) == MOE_OK) ++launches;
+        int n = 0;
+        if (st == MOE_OK) {
+            st = moe::launch_fp4_gemm(g13, nv, true, s, sms, &n);
+            launches += n;
+        }
+        if (st == MOE_OK) {
+            st = moe::launch_fp4_gemm(g2, nv, false, s, sms, &n);
+            launches += n;
+        }
         if (st == MOE_OK && (st = moe::launch_combine(y2, slot_to_row, topk_w, T, k, hidden, out, 0, s, sms)) == MOE_OK)
             ++launches;
     }

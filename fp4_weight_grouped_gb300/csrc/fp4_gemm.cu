@@ -97,7 +97,8 @@ struct Params {
     int out_bf16;
     int n_tiles;
     int scale_row;           // scale bytes a row of K: K / 32 or K / 16
-    int w_vec, a_vec;        // scale bytes that load at once (see load_words)
+    int w_vec, a_vec;        // scale bytes that load at once (see copy_words)
+    int band_lo, band_hi;    // this launch's bands: those of band_lo to band_hi rows
     uint64_t wait_limit_ns;
 };
 
@@ -577,7 +578,8 @@ __device__ __forceinline__ void store_swiglu(const Params &p, const Item &it, ui
 }
 
 // Row and item offsets from the group sizes (64-bit sums: sizes that wrap 32 bits
-// are caught), and the widest chunk.  False (recorded): the sizes do not add up.
+// are caught), and the widest chunk.  Rows count every band, items those of this
+// launch.  False (recorded): the sizes do not add up.
 template <int kMost>
 __device__ __forceinline__ bool build_items(const Params &p, int *roff, int *ioff, int *bad_flag, int *nt_slot) {
     const int tid = threadIdx.x, lane = tid & 31, E = p.E;
@@ -592,7 +594,7 @@ __device__ __forceinline__ bool build_items(const Params &p, int *roff, int *iof
             const int n = e < E ? roff[e] : 0;
             neg |= n < 0;
             long long rows = n > 0 ? n : 0, items = 0;
-            if (rows > 0) {
+            if (rows > 0 && rows >= p.band_lo && rows <= p.band_hi) {
                 const int cr = chunk_rows(static_cast<int>(min(rows, static_cast<long long>(p.rows))), kMost);
                 most = max(most, min(cr, kMost));
                 items = ((rows + kMost - 1) / kMost) * p.n_tiles;
@@ -1308,17 +1310,24 @@ bool set_smem(const void *kernel, int bytes, std::atomic<uint64_t> &mask) {
     return true;
 }
 
+// Bands of at least this many rows run in CTA pairs.  Both kernels at 24 bands of K =
+// 4096 (w13 with SwiGLU) and K = 2048 (w2, f32), MXFP4, one CTA / pair, us:
+//   rows            64          128         192         256         512
+//   SwiGLU      43.3 / 49.4  53.7 / 50.7  60.2 / 50.9  74.3 / 52.3   130 / 86.9
+//   plain       28.8 / 32.0  32.3 / 34.6  37.7 / 38.1  46.5 / 41.5  72.7 / 66.2
+// (a chunk is 96 tokens with SwiGLU and 192 without, against 256 in a pair).
+constexpr int kPairBandSwiglu = 112, kPairBand = 193;
+// A call of fewer rows than this many times that is one launch, without pairs: the
+// empty launch of the other class costs about 4 us, as much as pairs would gain.  (The
+// second as a programmatic dependent launch saved that, but its clusters then start
+// out of order: full layer w13 with SwiGLU 451 -> 490 us.)
+constexpr int kPairCall = 8;
+
 template <bool kNv, bool kSwiglu>
-moe_status launch(const Fp4Gemm &g, cudaStream_t stream, int num_sms) {
-    // Long bands (64 rows an expert on average) in CTA pairs; see DESIGN.
-    const bool pair = static_cast<int64_t>(g.rows) >= 64 * static_cast<int64_t>(g.E);
-    CUtensorMap tm_w, tm_a64, tm_a2, tm_a128;
-    if (!encode_codes(&tm_w, g.w_codes, static_cast<int64_t>(g.E) * g.N, g.K, pair ? kPairN / 2 : kTileN) ||
-        !encode_codes(&tm_a64, g.a_codes, g.rows, g.K, 64) ||
-        !encode_codes(&tm_a2, g.a_codes, g.rows, g.K, pair ? 32 : 16) ||
-        (pair && !encode_codes(&tm_a128, g.a_codes, g.rows, g.K, 128)))
-        return MOE_ERR_CUDA;
-    const int tile = pair ? (kSwiglu ? kPairN / 2 : kPairN) : kTileN;
+moe_status launch(const Fp4Gemm &g, cudaStream_t stream, int num_sms, int *launches) {
+    constexpr int band = kSwiglu ? kPairBandSwiglu : kPairBand;
+    const bool pairs = g.rows >= (g.E == 1 ? band : kPairCall * band);
+    const bool singles = !pairs || g.E > 1;
     Params p;
     p.w_scales = g.w_scales;
     p.a_scales = g.a_scales;
@@ -1335,7 +1344,6 @@ moe_status launch(const Fp4Gemm &g, cudaStream_t stream, int num_sms) {
     p.E = g.E;
     p.I = kSwiglu ? g.N / 2 : 0;
     p.out_bf16 = g.out_bf16;
-    p.n_tiles = ((kSwiglu ? g.N / 2 : g.N) + tile - 1) / tile;
     p.scale_row = g.K / (kNv ? 16 : 32);
     const auto vec = [&](const uint8_t *scales) {
         const uintptr_t both = reinterpret_cast<uintptr_t>(scales) | static_cast<uintptr_t>(p.scale_row);
@@ -1344,27 +1352,53 @@ moe_status launch(const Fp4Gemm &g, cudaStream_t stream, int num_sms) {
     p.w_vec = vec(g.w_scales);
     p.a_vec = vec(g.a_scales);
     p.wait_limit_ns = g.wait_limit_ns;
-    if (pair) {
-        static std::atomic<uint64_t> mask{0};
-        const auto kernel = fp4_gemm_pair_kernel<kNv, kSwiglu>;
-        if (!set_smem(reinterpret_cast<const void *>(kernel), kPairSmem, mask)) return MOE_ERR_CUDA;
-        const int out_vec = reinterpret_cast<uintptr_t>(g.out) % 32 == 0 && g.N % (g.out_bf16 ? 16 : 8) == 0;
-        kernel<<<num_sms & ~1, kThreads, kPairSmem, stream>>>(tm_w, tm_a128, tm_a64, tm_a2, p, out_vec);
-    } else {
+    const int64_t w_rows = static_cast<int64_t>(g.E) * g.N;
+    const int columns = kSwiglu ? g.N / 2 : g.N;
+    CUtensorMap tm_w, tm_a64, tm_a2, tm_a128;
+    if (!encode_codes(&tm_a64, g.a_codes, g.rows, g.K, 64)) return MOE_ERR_CUDA;
+    *launches = 0;
+    if (singles) {
         static std::atomic<uint64_t> mask{0};
         const auto kernel = fp4_gemm_kernel<kNv, kSwiglu>;
-        if (!set_smem(reinterpret_cast<const void *>(kernel), kSmemBytes, mask)) return MOE_ERR_CUDA;
+        if (!set_smem(reinterpret_cast<const void *>(kernel), kSmemBytes, mask) ||
+            !encode_codes(&tm_w, g.w_codes, w_rows, g.K, kTileN) || !encode_codes(&tm_a2, g.a_codes, g.rows, g.K, 16))
+            return MOE_ERR_CUDA;
+        p.n_tiles = (columns + kTileN - 1) / kTileN;
+        p.band_lo = 1;
+        p.band_hi = pairs ? band - 1 : INT32_MAX;
         kernel<<<num_sms, kThreads, kSmemBytes, stream>>>(tm_w, tm_a64, tm_a2, p);
+        if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
+        ++*launches;
     }
-    return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    if (pairs) {
+        static std::atomic<uint64_t> mask{0};
+        const auto kernel = fp4_gemm_pair_kernel<kNv, kSwiglu>;
+        if (!set_smem(reinterpret_cast<const void *>(kernel), kPairSmem, mask) ||
+            !encode_codes(&tm_w, g.w_codes, w_rows, g.K, kPairN / 2) ||
+            !encode_codes(&tm_a2, g.a_codes, g.rows, g.K, 32) || !encode_codes(&tm_a128, g.a_codes, g.rows, g.K, 128))
+            return MOE_ERR_CUDA;
+        constexpr int tile = kSwiglu ? kPairN / 2 : kPairN;
+        p.n_tiles = (columns + tile - 1) / tile;
+        p.band_lo = band;
+        p.band_hi = INT32_MAX;
+        const int out_vec = reinterpret_cast<uintptr_t>(g.out) % 32 == 0 && g.N % (g.out_bf16 ? 16 : 8) == 0;
+        kernel<<<num_sms & ~1, kThreads, kPairSmem, stream>>>(tm_w, tm_a128, tm_a64, tm_a2, p, out_vec);
+        if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
+        ++*launches;
+    }
+    return MOE_OK;
 }
 
 }  // namespace fp4
 
-moe_status launch_fp4_gemm(const Fp4Gemm &g, bool nv, bool swiglu, cudaStream_t stream, int num_sms) {
+moe_status launch_fp4_gemm(const Fp4Gemm &g, bool nv, bool swiglu, cudaStream_t stream, int num_sms, int *launches) {
+    *launches = 0;
     if (g.rows == 0) return MOE_OK;
-    if (nv) return swiglu ? fp4::launch<true, true>(g, stream, num_sms) : fp4::launch<true, false>(g, stream, num_sms);
-    return swiglu ? fp4::launch<false, true>(g, stream, num_sms) : fp4::launch<false, false>(g, stream, num_sms);
+    if (nv)
+        return swiglu ? fp4::launch<true, true>(g, stream, num_sms, launches)
+                      : fp4::launch<true, false>(g, stream, num_sms, launches);
+    return swiglu ? fp4::launch<false, true>(g, stream, num_sms, launches)
+                  : fp4::launch<false, false>(g, stream, num_sms, launches);
 }
 
 }  // namespace moe

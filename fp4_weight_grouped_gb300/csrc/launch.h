@@ -108,7 +108,7 @@ struct Fp4Gemm {
     int *status;
     uint64_t wait_limit_ns;
 };
-moe_status launch_fp4_gemm(const Fp4Gemm &g, bool nv, bool swiglu, cudaStream_t stream, int num_sms);
+moe_status launch_fp4_gemm(const Fp4Gemm &g, bool nv, bool swiglu, cudaStream_t stream, int num_sms, int *launches);
 
 // Rows of x (row r, or row row_index[r] / index_div) to 4-bit codes and block
 // scales; `values` (optional) receives what they stand for.

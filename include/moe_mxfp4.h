@@ -626,7 +626,9 @@ MOE_API moe_status moe_fp4_quantize(const void *x, moe_dtype dtype, int64_t x_ro
  *  Other arguments as for moe_mxfp4_grouped_gemm.
  * A scale byte that stands for NaN (255; 0x7F), and for MOE_FP4_NV a negative
  * scale (the MMA's scales are unsigned), sets MOE_ERR_DATA; the outputs of its
- * row or column are then unspecified.  One kernel launch.
+ * row or column are then unspecified.
+ * One kernel launch, or (calls of about a thousand rows and more) two, for shorter and
+ * longer bands.
  */
 MOE_API moe_status moe_fp4_grouped_gemm(const uint8_t *act_codes, const uint8_t *act_scales,
                                         const float *act_scale_2, int64_t rows, int32_t K,

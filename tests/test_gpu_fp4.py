@@ -259,7 +259,8 @@ def check_product(B, rng, fmt, sizes, K, N, out_dtype=torch.float32, wide=False,
 SIZES = [
     ([1], 32, 1), ([5], 64, 130), ([0, 3, 0], 96, 128), ([17, 1, 0, 40], 256, 129),
     ([16, 33, 65], 512, 384), ([129, 0, 193, 385], 288, 200), ([192, 191, 1], 1056, 260),
-    ([700], 768, 136), ([192, 400], 4096, 128), ([2] * 40 + [0] * 5 + [90], 512, 256), ([1], 8192, 256),
+    ([200, 3, 0, 193, 192, 1, 600, 512], 288, 200), ([700, 1, 900, 16], 1056, 456), ([257, 1300, 0, 40], 2048, 192),
+    ([193], 96, 40), ([700], 768, 136), ([192, 400], 4096, 128), ([2] * 40 + [0] * 5 + [90], 512, 256), ([1], 8192, 256),
 ]
 
 
@@ -299,6 +300,21 @@ def test_product_repeats_bit_for_bit(B, fmt):
     first = B.fp4_grouped_gemm(*args, act_scale_2=a2, weight_scale_2=w2)
     for _ in range(20):
         assert torch.equal(first, B.fp4_grouped_gemm(*args, act_scale_2=a2, weight_scale_2=w2))
+
+
+@pytest.mark.parametrize("fmt", [MX, NV], ids=["mx", "nv"])
+def test_long_bands_repeat_bit_for_bit(B, fmt):
+    """Bands of every length class, forty times: a race in a ring shows as a difference."""
+    rng = np.random.default_rng(18)
+    sizes = rng.integers(0, 700, 12).tolist()
+    args, _ = check_product(B, rng, fmt, sizes, 1536, 448)
+    kw = dict(act_scale_2=scale1(0.75), weight_scale_2=torch.ones(12, device=DEV))
+    first = B.fp4_grouped_gemm(*args, **kw)
+    gated = B.fp4_grouped_gemm_swiglu(*args, h_scale_2=scale1(0.02), **kw)
+    for _ in range(40):
+        assert torch.equal(first, B.fp4_grouped_gemm(*args, **kw))
+        for a, b in zip(gated, B.fp4_grouped_gemm_swiglu(*args, h_scale_2=scale1(0.02), **kw)):
+            assert torch.equal(a, b)
 
 
 def test_product_no_rows_and_bad_sizes(B):
@@ -374,7 +390,9 @@ def swiglu_reference(a, w, I, s):
 
 @pytest.mark.parametrize("fmt", [MX, NV], ids=["mx", "nv"])
 @pytest.mark.parametrize("sizes,K,I", [([1], 32, 32), ([5, 0, 3], 96, 160), ([97, 16, 200], 512, 128),
-                                       ([33, 64], 1056, 416), ([2] * 30, 256, 256), ([96, 200], 4096, 64)])
+                                       ([33, 64], 1056, 416), ([2] * 30, 256, 256), ([96, 200], 4096, 64),
+                                       ([112, 111, 5, 0, 700, 256], 352, 224), ([300, 0, 1000, 31], 2048, 96),
+                                       ([129], 512, 32), ([600, 400], 96, 320)])
 def test_swiglu_product_quantises_h(B, fmt, sizes, K, I):
     rng = np.random.default_rng(K + I + fmt)
     E, rows, blk = len(sizes), sum(sizes), BLOCK[fmt]
