@@ -213,9 +213,9 @@ struct Ring {
 // ---------------------------------------------------------- scale loaders
 
 // Copy of 16 scale bytes [at, at + 16) of one row into shared memory where a whole
-// group does not load as 16-byte vectors; zeros past the row's end (2^-127 or 0: finite, and
-// they meet zero codes).  `vec`: bytes that load at once (16, 8, 4 or 1; it divides the
-// row and the base address); all but 1 are asynchronous.
+// group does not load as 16-byte vectors; zeros past the row's end (2^-127 or 0:
+// finite, and they meet zero codes).  `vec`: bytes that load at once (16, 8 or 4; it
+// divides the row and the base address).
 __device__ __noinline__ void copy_words(uint8_t *dst, const uint8_t *row, int at, int scale_row, int vec) {
     const uint32_t sd = smem_u32(dst);
     if (vec == 16) {
@@ -228,7 +228,7 @@ __device__ __noinline__ void copy_words(uint8_t *dst, const uint8_t *row, int at
                          "l"(in ? row + at + 8 * i : row), "r"(in ? 8 : 0)
                          : "memory");
         }
-    } else if (vec == 4) {
+    } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const bool in = at + 4 * i < scale_row;
@@ -236,14 +236,52 @@ __device__ __noinline__ void copy_words(uint8_t *dst, const uint8_t *row, int at
                          "l"(in ? row + at + 4 * i : row), "r"(in ? 4 : 0)
                          : "memory");
         }
-    } else {
-#pragma unroll 1
-        for (int i = 0; i < 4; ++i) {
-            uint32_t w = 0;
+    }
+}
+
+// The same for rows at any address: the aligned words that hold the bytes, up to
+// six rows' in flight together, shifted into place.  A word that reaches outside the tensor
+// [lo, hi) is put together from its bytes inside.
+template <int R>
+__device__ __forceinline__ void copy_unaligned(uint8_t *dst, const uint8_t *const (&src)[R], int at, int scale_row,
+                                               const uint8_t *lo, const uint8_t *hi) {
+    constexpr int kBatch = R <= 6 ? R : 4;
+    const int n = min(16, scale_row - at);
 #pragma unroll
-            for (int b = 0; b < 4; ++b)
-                if (at + 4 * i + b < scale_row) w |= static_cast<uint32_t>(__ldg(row + at + 4 * i + b)) << (8 * b);
-            *reinterpret_cast<uint32_t *>(dst + 4 * i) = w;
+    for (int q0 = 0; q0 < R; q0 += kBatch) {
+        uint32_t w[kBatch][5];
+#pragma unroll
+        for (int q = q0; q < q0 + kBatch && q < R; ++q) {
+            const uint8_t *from = src[q] + at;
+            const int off = static_cast<int>(reinterpret_cast<uintptr_t>(from) & 3);
+            from -= off;
+#pragma unroll
+            for (int i = 0; i < 5; ++i) {
+                const uint8_t *a = from + 4 * i;
+                uint32_t x = 0;
+                if (4 * i < n + off) {
+                    if (a >= lo && a + 4 <= hi) {
+                        x = __ldg(reinterpret_cast<const uint32_t *>(a));
+                    } else {
+#pragma unroll 1
+                        for (int b = 0; b < 4; ++b)
+                            if (a + b >= lo && a + b < hi) x |= static_cast<uint32_t>(__ldg(a + b)) << (8 * b);
+                    }
+                }
+                w[q - q0][i] = x;
+            }
+        }
+#pragma unroll
+        for (int q = q0; q < q0 + kBatch && q < R; ++q) {
+            const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(src[q] + at) & 3) * 8;
+            uint32_t o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int left = n - 4 * i;        // bytes of this word inside the row
+                o[i] = __funnelshift_r(w[q - q0][i], w[q - q0][i + 1], shift);
+                if (left < 4) o[i] = left <= 0 ? 0u : o[i] & ((1u << (8 * left)) - 1u);
+            }
+            *reinterpret_cast<uint4 *>(dst + q * 512) = make_uint4(o[0], o[1], o[2], o[3]);
         }
     }
 }
@@ -282,10 +320,11 @@ struct ScaleEnv {
 // its end (those sums are never stored, and every staged byte is one of the tensor).
 template <int P, int R, int kMost, int kTile, class RowFn>
 __device__ __forceinline__ void copy_scales(const ScaleEnv &v, const Staging &g, int first_row, const uint8_t *base,
-                                            int vec, RowFn row) {
+                                            int64_t rows, int vec, RowFn row) {
     const Params &p = *v.p;
     const int lane = threadIdx.x & 31;
     const int pieces = (p.scale_row + 15) / 16;
+    const int64_t bytes = rows * p.scale_row;
     uint8_t *mine = g.bytes + first_row * 512 + lane * 16;
     Ring r;
     bool ok = true;
@@ -309,6 +348,10 @@ __device__ __forceinline__ void copy_scales(const ScaleEnv &v, const Staging &g,
                                      : "memory");
                     src[q] += 16 * P;
                 }
+            } else if (vec == 1) {
+#pragma unroll 1
+                for (int k = 0; k < P && i + k < pieces; ++k)
+                    copy_unaligned<R>(dst + k * g.piece_bytes, src, (i + k) * 16, p.scale_row, base, base + bytes);
             } else {
 #pragma unroll 1
                 for (int k = 0; k < P && i + k < pieces; ++k)
@@ -579,52 +622,80 @@ __device__ __forceinline__ void store_swiglu(const Params &p, const Item &it, ui
 
 // Row and item offsets from the group sizes (64-bit sums: sizes that wrap 32 bits
 // are caught), and the widest chunk.  Rows count every band, items those of this
-// launch.  False (recorded): the sizes do not add up.
+// launch.  The experts go 32 to a warp, first for their totals, then for the offsets
+// on top of the totals before them (one warp over all of them took 2 us at 256
+// experts and 6 at 1,024).  False (recorded): the sizes do not add up.  `scratch`: 1 KB.
+struct Totals {
+    long long rows, items;
+    int most, bad;
+};
+
 template <int kMost>
-__device__ __forceinline__ bool build_items(const Params &p, int *roff, int *ioff, int *bad_flag, int *nt_slot) {
-    const int tid = threadIdx.x, lane = tid & 31, E = p.E;
-    for (int e = tid; e < E; e += blockDim.x) roff[e] = __ldg(p.group_sizes + e);
-    __syncthreads();
-    if (tid < 32) {
-        long long rsum = 0, isum = 0;
-        int most = 0;
-        bool neg = false;
-        for (int e0 = 0; e0 < E; e0 += 32) {
-            const int e = e0 + lane;
-            const int n = e < E ? roff[e] : 0;
-            neg |= n < 0;
-            long long rows = n > 0 ? n : 0, items = 0;
-            if (rows > 0 && rows >= p.band_lo && rows <= p.band_hi) {
-                const int cr = chunk_rows(static_cast<int>(min(rows, static_cast<long long>(p.rows))), kMost);
-                most = max(most, min(cr, kMost));
-                items = ((rows + kMost - 1) / kMost) * p.n_tiles;
-            }
-            long long r = rows, i = items;
+__device__ __forceinline__ bool build_items(const Params &p, int *roff, int *ioff, void *scratch, int *nt_slot) {
+    constexpr uint32_t kAll = 0xffffffffu;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = p.E, chunks = (E + 31) / 32;
+    Totals *totals = static_cast<Totals *>(scratch);
+    const auto rows_of = [&](int e, int *most) -> long long {    // items of expert e, its chunk's rows in *most
+        const int n = e < E ? __ldg(p.group_sizes + e) : 0;
+        *most = 0;
+        if (n <= 0 || n < p.band_lo || n > p.band_hi) return 0;
+        *most = chunk_rows(min(n, p.rows), kMost);
+        return (static_cast<long long>(n) + kMost - 1) / kMost * p.n_tiles;
+    };
+    for (int c = warp; c < chunks; c += kThreads / 32) {
+        const int e = c * 32 + lane, n = e < E ? __ldg(p.group_sizes + e) : 0;
+        int most;
+        long long items = rows_of(e, &most), rows = max(n, 0);
 #pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const long long ro = __shfl_up_sync(0xffffffffu, r, d), io = __shfl_up_sync(0xffffffffu, i, d);
-                if (lane >= d) { r += ro; i += io; }
-            }
-            if (e < E) {
-                // Stored as ints; used only when the totals check out below.
-                roff[e] = static_cast<int>(rsum + r - rows);
-                ioff[e] = static_cast<int>(isum + i - items);
-            }
-            rsum += __shfl_sync(0xffffffffu, r, 31);
-            isum += __shfl_sync(0xffffffffu, i, 31);
+        for (int d = 16; d > 0; d >>= 1) {
+            rows += __shfl_xor_sync(kAll, rows, d);
+            items += __shfl_xor_sync(kAll, items, d);
         }
-        most = __reduce_max_sync(0xffffffffu, most);
-        const bool bad = __any_sync(0xffffffffu, neg) || rsum != p.rows || isum > INT32_MAX;
-        if (lane == 0) {
-            roff[E] = static_cast<int>(rsum);
-            ioff[E] = static_cast<int>(isum);
-            *bad_flag = bad;
-            *nt_slot = most;
-            if (bad) set_status(p.status, MOE_ERR_DATA);
-        }
+        most = __reduce_max_sync(kAll, most);
+        const int bad = __any_sync(kAll, n < 0);
+        if (lane == 0) totals[c] = {rows, items, most, bad};
     }
     __syncthreads();
-    return !*bad_flag;
+    // Lane l holds the totals of chunk l; sums up to and of all chunks.
+    const Totals mine = lane < chunks ? totals[lane] : Totals{0, 0, 0, 0};
+    long long rsum = mine.rows, isum = mine.items;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long ro = __shfl_up_sync(kAll, rsum, d), io = __shfl_up_sync(kAll, isum, d);
+        if (lane >= d) { rsum += ro; isum += io; }
+    }
+    const long long all_rows = __shfl_sync(kAll, rsum, 31), all_items = __shfl_sync(kAll, isum, 31);
+    const bool bad = __any_sync(kAll, mine.bad) || all_rows != p.rows || all_items > INT32_MAX;
+    const int most = __reduce_max_sync(kAll, mine.most);
+    if (bad) {
+        if (threadIdx.x == 0) set_status(p.status, MOE_ERR_DATA);
+        return false;
+    }
+    for (int c = warp; c < chunks; c += kThreads / 32) {
+        const int e = c * 32 + lane, n = e < E ? __ldg(p.group_sizes + e) : 0;
+        int unused;
+        // The sums are below 2^31 here.
+        const int items = static_cast<int>(rows_of(e, &unused));
+        int r = n, i = items;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int ro = __shfl_up_sync(kAll, r, d), io = __shfl_up_sync(kAll, i, d);
+            if (lane >= d) { r += ro; i += io; }
+        }
+        const int r0 = static_cast<int>(__shfl_sync(kAll, rsum - mine.rows, c));
+        const int i0 = static_cast<int>(__shfl_sync(kAll, isum - mine.items, c));
+        if (e < E) {
+            roff[e] = r0 + r - n;
+            ioff[e] = i0 + i - items;
+        }
+    }
+    if (threadIdx.x == 0) {
+        roff[E] = static_cast<int>(all_rows);
+        ioff[E] = static_cast<int>(all_items);
+        *nt_slot = most;
+    }
+    __syncthreads();
+    return true;
 }
 
 // ------------------------------------------------------------------ kernel
@@ -647,14 +718,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *raw_bars = final_bar + 1;                               // scale copiers <-> converters
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kOffMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kOffMisc + 8);
-    int *bad_flag = reinterpret_cast<int *>(smem + kOffMisc + 16);
     int *nt_slot = reinterpret_cast<int *>(smem + kOffMisc + 24);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int E = p.E;
 
     if (tid == 0) *abort_flag = 0;
-    if (!build_items<S::NT>(p, roff, ioff, bad_flag, nt_slot)) return;
+    if (!build_items<S::NT>(p, roff, ioff, smem + kOffStaging, nt_slot)) return;
     // redux: the compiler then knows the loops' bounds as warp-uniform
     const int total = __reduce_max_sync(0xffffffffu, ioff[E]);
     if (static_cast<int>(blockIdx.x) >= total) return;
@@ -789,12 +859,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr int P = kGroup * C::W / 4;
         if (warp == kWCopyWarp) {
             const int cols = kSwiglu ? p.I : p.N;
-            copy_scales<P, 4 * S::MT, S::NT, kTileN>(v, g, 0, p.w_scales, p.w_vec, [&](const Item &it, int q) {
+            const int64_t w_rows = static_cast<int64_t>(E) * p.N;
+            copy_scales<P, 4 * S::MT, S::NT, kTileN>(v, g, 0, p.w_scales, w_rows, p.w_vec, [&](const Item &it, int q) {
                 return static_cast<int64_t>(it.e) * p.N + (q >= 4 ? p.I : 0) +
                        min(it.n0 + lane + 32 * (q & 3), cols - 1);
             });
         } else if (warp == kACopyWarp) {
-            copy_scales<P, S::AR, S::NT, kTileN>(v, g, 4 * S::MT, p.a_scales, p.a_vec, [&](const Item &it, int q) {
+            copy_scales<P, S::AR, S::NT, kTileN>(v, g, 4 * S::MT, p.a_scales, p.rows, p.a_vec, [&](const Item &it, int q) {
                 return static_cast<int64_t>(it.row0 + min(lane + 32 * q, it.nvalid - 1));
             });
         } else {
@@ -1069,7 +1140,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint64_t *raw_bars = final_bar + 1;                               // scale copiers <-> converters
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kPairOffMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kPairOffMisc + 8);
-    int *bad_flag = reinterpret_cast<int *>(smem + kPairOffMisc + 16);
     int *nt_slot = reinterpret_cast<int *>(smem + kPairOffMisc + 24);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -1079,7 +1149,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
     if (tid == 0) *abort_flag = 0;
     // Both CTAs read the same sizes, so both return here or neither does.
-    if (!build_items<kPairM>(p, roff, ioff, bad_flag, nt_slot)) return;
+    if (!build_items<kPairM>(p, roff, ioff, smem + kPairOffStaging, nt_slot)) return;
     // redux: the compiler then knows the loops' bounds as warp-uniform
     const int total = __reduce_max_sync(0xffffffffu, ioff[E]);
     if (first >= total) return;
@@ -1215,12 +1285,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (warp == kWCopyWarp) {
             // All 192 weight rows, in the order of the MMA's columns.
             const int cols = kSwiglu ? p.I : p.N;
-            copy_scales<P, kPairN / 32, kPairM, kTile>(v, g, 0, p.w_scales, p.w_vec, [&](const Item &it, int q) {
+            const int64_t w_rows = static_cast<int64_t>(E) * p.N;
+            copy_scales<P, kPairN / 32, kPairM, kTile>(v, g, 0, p.w_scales, w_rows, p.w_vec, [&](const Item &it, int q) {
                 const int n = kSwiglu ? (q >= 3 ? q - 3 : q) * 32 + lane : q * 32 + lane;
                 return static_cast<int64_t>(it.e) * p.N + (kSwiglu && q >= 3 ? p.I : 0) + min(it.n0 + n, cols - 1);
             });
         } else if (warp == kACopyWarp) {
-            copy_scales<P, 4, kPairM, kTile>(v, g, 6, p.a_scales, p.a_vec, [&](const Item &it, int q) {
+            copy_scales<P, 4, kPairM, kTile>(v, g, 6, p.a_scales, p.rows, p.a_vec, [&](const Item &it, int q) {
                 int row0, valid;
                 pair_rows(it, rank, &row0, &valid);
                 return static_cast<int64_t>(min(row0 + min(lane + 32 * q, max(valid - 1, 0)), p.rows - 1));
