@@ -372,6 +372,75 @@ __device__ __forceinline__ void copy_scales(const ScaleEnv &v, const Staging &g,
     asm volatile("cp.async.wait_all;" ::: "memory");   // none in flight when the CTA leaves
 }
 
+// Copier warp for rows that are not whole 16-byte pieces, of 16-byte aligned tensors:
+// the two aligned 16-byte windows that hold a piece go into the staging area as they
+// are, 1,024 bytes from one q to the next, and the converters shift.  (Loads that
+// were shifted here, before their store, waited for memory once a piece: 8 us of a
+// 16 us call at K = 1,056.)
+template <int P, int R, int kMost, int kTile, class RowFn>
+__device__ __forceinline__ void copy_scales_shift(const ScaleEnv &v, const Staging &g, int first_row,
+                                                  const uint8_t *base, int64_t rows, RowFn row) {
+    const Params &p = *v.p;
+    const int lane = threadIdx.x & 31;
+    const int pieces = (p.scale_row + 15) / 16;
+    const int64_t bytes = rows * p.scale_row;
+    const uint32_t mine = smem_u32(g.bytes + first_row * 1024 + lane * 16);
+    Ring r;
+    bool ok = true;
+    for (int j = v.first; ok && j < v.total; j += v.step) {
+        const Item it = decode_item<kMost, kTile>(j, v.roff, v.ioff, p.E, p.n_tiles);
+        for (int i = 0; i < pieces; i += P) {
+            ok = wait(&g.empty[r.slot], r.phase ^ 1u, v.abort_flag, p.status, p.wait_limit_ns);
+            if (!ok) break;
+#pragma unroll 1
+            for (int k = 0; k < P && i + k < pieces; ++k) {
+                const uint32_t dst = mine + (r.slot * P + k) * 2 * g.piece_bytes;
+                const int n = min(16, p.scale_row - (i + k) * 16);
+#pragma unroll
+                for (int q = 0; q < R; ++q) {
+                    const int64_t at = row(it, q) * p.scale_row + (i + k) * 16, window = at & ~int64_t(15);
+                    // Bytes of the windows inside the tensor; the second where it is needed.
+                    const int first = static_cast<int>(min(bytes - window, int64_t(16)));
+                    const int second = (at & 15) + n > 16 ? static_cast<int>(min(bytes - window - 16, int64_t(16))) : 0;
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(dst + q * 1024), "l"(base + window),
+                                 "r"(first)
+                                 : "memory");
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(dst + q * 1024 + 512),
+                                 "l"(base + window + (second > 0 ? 16 : 0)), "r"(max(second, 0))
+                                 : "memory");
+                }
+            }
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(&g.full[r.slot])) : "memory");
+            __syncwarp();
+            r.next(kDepth);
+        }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");   // none in flight when the CTA leaves
+}
+
+// Scale words of rows staged by copy_scales_shift: row q's piece starts at byte (offs >>
+// 4 q) & 15 of its windows, the words wanted `skip` bytes into it; `n` bytes from there
+// on are the row's, the rest reads as zeros.
+template <int R, int W>
+__device__ __forceinline__ void read_shifted(const uint8_t *piece, uint64_t offs, int skip, int n, uint32_t (&w)[R][W]) {
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+        const int b = (static_cast<int>(offs >> (4 * q)) & 15) + skip;
+        uint32_t raw[W + 1];
+#pragma unroll
+        for (int i = 0; i <= W; ++i) {
+            const int word = (b >> 2) + i;
+            raw[i] = *reinterpret_cast<const uint32_t *>(piece + q * 1024 + (word >> 2) * 512 + (word & 3) * 4);
+        }
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            const int left = n - 4 * i;
+            const uint32_t x = __funnelshift_r(raw[i], raw[i + 1], 8 * (b & 3));
+            w[q][i] = left >= 4 ? x : left <= 0 ? 0u : x & ((1u << (8 * left)) - 1u);
+        }
+    }
+}
+
 // 4, 8, 16 or 32 consecutive columns of each lane's own tensor-memory lane.
 template <int C>
 __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&v)[C]) {
@@ -433,11 +502,14 @@ __device__ __forceinline__ void init_scale_bars(uint64_t *raw_bars) {
 // cycles for two stages and bound the kernel.
 //
 // A: the MMA's A operand (kByTile), B: its B operand; their first rows in the group.
-template <bool kNv, int RA, int RB>
+template <bool kNv, bool kShift, int RA, int RB, int kMost, int kTile, class RowA, class RowB>
 __device__ __forceinline__ void convert_scales(const ScaleEnv &v, const Staging &g, int first_a, int first_b,
-                                               uint32_t sf_tmem, uint64_t *full, uint64_t *empty, uint32_t n_stages) {
+                                               uint32_t sf_tmem, uint64_t *full, uint64_t *empty, uint32_t n_stages,
+                                               RowA row_a, RowB row_b) {
     using C = ScaleCols<kNv>;
-    constexpr int W = C::W, kACols = 4 * ((RA + 3) / 4) * W, P = kGroup * W / 4;
+    constexpr int W = C::W, kACols = 4 * ((RA + 3) / 4) * W;
+    constexpr int kStages = kShift && kNv ? 2 : kGroup, P = kStages * W / 4;    // a group's
+    constexpr int kRow = kShift ? 1024 : 512;
     static_assert(kACols + 4 * ((RB + 3) / 4) * W == C::kCols, "scale columns of a stage");
     static_assert(kSets == 2 && kGroup % 2 == 0, "sets take stages in turn");
     const Params &p = *v.p;
@@ -446,32 +518,54 @@ __device__ __forceinline__ void convert_scales(const ScaleEnv &v, const Staging 
     const int set = ((threadIdx.x >> 5) - kConvertWarp) >> 2;
     uint32_t bad = 0;
     bool ok = true;
+    const uint32_t piece_bytes = g.piece_bytes * (kRow / 512);
     // MXFP4: a piece is two stages, the set's the half it starts at; NVFP4: one.
-    const uint8_t *mine = g.bytes + lane * 16 + (kNv ? set * g.piece_bytes : set * 8);
+    const uint8_t *mine = g.bytes + lane * 16 + (kNv ? set * piece_bytes : kShift ? 0 : set * 8);
     Ring raw, r;                  // staged group, this set's next stage
     uint32_t sf = set;            // NVFP4: scale slot
     if (set) r.next(n_stages);
     for (int j = v.first; ok && j < v.total; j += v.step) {
-        for (int k0 = 0; ok && k0 < k_stages; k0 += kGroup) {
+        uint64_t offs_a = 0, offs_b = 0;       // byte each row's pieces start at in their windows
+        if constexpr (kShift) {
+            const Item it = decode_item<kMost, kTile>(j, v.roff, v.ioff, p.E, p.n_tiles);
+#pragma unroll
+            for (int q = 0; q < RA; ++q) offs_a |= static_cast<uint64_t>(row_a(it, q) * p.scale_row & 15) << (4 * q);
+#pragma unroll
+            for (int q = 0; q < RB; ++q) offs_b |= static_cast<uint64_t>(row_b(it, q) * p.scale_row & 15) << (4 * q);
+        }
+        for (int k0 = 0; ok && k0 < k_stages; k0 += kStages) {
             ok = wait(&g.full[raw.slot], raw.phase, v.abort_flag, p.status, p.wait_limit_ns);
-            const uint8_t *piece = mine + raw.slot * P * g.piece_bytes;
-            const int end = min(k0 + kGroup, k_stages);
+            const uint8_t *piece = mine + raw.slot * P * piece_bytes;
+            const int end = min(k0 + kStages, k_stages);
 #pragma unroll 1
-            for (int ks = k0; ok && ks < end; ks += 2, piece += (kNv ? 2 : 1) * g.piece_bytes) {
+            for (int ks = k0; ok && ks < end; ks += 2, piece += (kNv ? 2 : 1) * piece_bytes) {
                 const int by = ks + 2 <= k_stages ? 2 : 1;
                 if (ks + set < k_stages) {     // an odd last stage is the first set's
                     uint32_t wa[RA][W], wb[RB][W];
-                    read_words(piece + first_a * 512, wa);
-                    read_words(piece + first_b * 512, wb);
-                    // The four warps read the same bytes; each checks a quarter.
+                    if constexpr (kShift) {
+                        const int skip = kNv ? 0 : set * 8, n = p.scale_row - (ks + set) * 4 * W;
+                        read_shifted(piece + first_a * kRow, offs_a, skip, n, wa);
+                        read_shifted(piece + first_b * kRow, offs_b, skip, n, wb);
 #pragma unroll
-                    for (int i = 0; i < (RA + RB + 3) / 4; ++i)
-                        if (4 * i + 3 < RA + RB || quarter + 4 * i < RA + RB) {
-                            uint32_t x[1][W];
-                            read_words(piece + (quarter + 4 * i) * 512, x);
+                        for (int k = 0; k < W; ++k) {
 #pragma unroll
-                            for (int k = 0; k < W; ++k) bad |= bad_bits<kNv>(x[0][k]);
+                            for (int q = 0; q < RA; ++q) bad |= bad_bits<kNv>(wa[q][k]);
+#pragma unroll
+                            for (int q = 0; q < RB; ++q) bad |= bad_bits<kNv>(wb[q][k]);
                         }
+                    } else {
+                        read_words(piece + first_a * 512, wa);
+                        read_words(piece + first_b * 512, wb);
+                        // The four warps read the same bytes; each checks a quarter.
+#pragma unroll
+                        for (int i = 0; i < (RA + RB + 3) / 4; ++i)
+                            if (4 * i + 3 < RA + RB || quarter + 4 * i < RA + RB) {
+                                uint32_t x[1][W];
+                                read_words(piece + (quarter + 4 * i) * 512, x);
+#pragma unroll
+                                for (int k = 0; k < W; ++k) bad |= bad_bits<kNv>(x[0][k]);
+                            }
+                    }
                     const bool back = r.slot < 2;
                     if constexpr (kNv)
                         ok = wait(&empty[back ? r.slot + n_stages - 2 : r.slot - 2], r.phase ^ back, v.abort_flag,
@@ -700,7 +794,9 @@ __device__ __forceinline__ bool build_items(const Params &p, int *roff, int *iof
 
 // ------------------------------------------------------------------ kernel
 
-template <bool kNv, bool kSwiglu>
+// kShift: scale rows that are not whole 16-byte pieces (see copy_scales_shift); an
+// instantiation of its own, so that the others' registers do not pay for it.
+template <bool kNv, bool kSwiglu, bool kShift>
 __global__ void __launch_bounds__(kThreads, 1)
     fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a64,
                     const __grid_constant__ CUtensorMap tm_a16, const Params p) {
@@ -857,21 +953,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         const ScaleEnv v = {&p, roff, ioff, abort_flag, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), total};
         const Staging g = {smem + kOffStaging, (4 * S::MT + S::AR) * 512, raw_bars, raw_bars + kDepth};
         constexpr int P = kGroup * C::W / 4;
+        const int cols = kSwiglu ? p.I : p.N;
+        const int64_t w_rows = static_cast<int64_t>(E) * p.N;
+        const auto w_row = [&](const Item &it, int q) {
+            return static_cast<int64_t>(it.e) * p.N + (q >= 4 ? p.I : 0) + min(it.n0 + lane + 32 * (q & 3), cols - 1);
+        };
+        const auto a_row = [&](const Item &it, int q) {
+            return static_cast<int64_t>(it.row0 + min(lane + 32 * q, it.nvalid - 1));
+        };
+        const uint32_t sf_tmem = tmem + kSfCol0 + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        constexpr int RW = 4 * S::MT, RA = S::AR;
         if (warp == kWCopyWarp) {
-            const int cols = kSwiglu ? p.I : p.N;
-            const int64_t w_rows = static_cast<int64_t>(E) * p.N;
-            copy_scales<P, 4 * S::MT, S::NT, kTileN>(v, g, 0, p.w_scales, w_rows, p.w_vec, [&](const Item &it, int q) {
-                return static_cast<int64_t>(it.e) * p.N + (q >= 4 ? p.I : 0) +
-                       min(it.n0 + lane + 32 * (q & 3), cols - 1);
-            });
+            if constexpr (kShift) copy_scales_shift<2, RW, S::NT, kTileN>(v, g, 0, p.w_scales, w_rows, w_row);
+            else copy_scales<P, RW, S::NT, kTileN>(v, g, 0, p.w_scales, w_rows, p.w_vec, w_row);
         } else if (warp == kACopyWarp) {
-            copy_scales<P, S::AR, S::NT, kTileN>(v, g, 4 * S::MT, p.a_scales, p.rows, p.a_vec, [&](const Item &it, int q) {
-                return static_cast<int64_t>(it.row0 + min(lane + 32 * q, it.nvalid - 1));
-            });
+            if constexpr (kShift) copy_scales_shift<2, RA, S::NT, kTileN>(v, g, RW, p.a_scales, p.rows, a_row);
+            else copy_scales<P, RA, S::NT, kTileN>(v, g, RW, p.a_scales, p.rows, p.a_vec, a_row);
         } else {
-            convert_scales<kNv, 4 * S::MT, S::AR>(
-                v, g, 0, 4 * S::MT, tmem + kSfCol0 + (static_cast<uint32_t>((warp & 3) * 32) << 16), full, empty,
-                n_stages);
+            convert_scales<kNv, kShift, RW, RA, S::NT, kTileN>(v, g, 0, RW, sf_tmem, full, empty, n_stages, w_row, a_row);
         }
     } else {
         const int quarter = warp & 3, half = (warp - kEpilogueWarp) >> 2;
@@ -1121,7 +1220,7 @@ __device__ __forceinline__ void pair_store_swiglu(const Params &p, uint32_t acc,
     }
 }
 
-template <bool kNv, bool kSwiglu>
+template <bool kNv, bool kSwiglu, bool kShift>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a128,
                          const __grid_constant__ CUtensorMap tm_a64, const __grid_constant__ CUtensorMap tm_a32,
@@ -1282,23 +1381,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const ScaleEnv v = {&p, roff, ioff, abort_flag, first, step, total};
         const Staging g = {smem + kPairOffStaging, (6 + 4) * 512, raw_bars, raw_bars + kDepth};
         constexpr int P = kGroup * C::W / 4;
+        const int cols = kSwiglu ? p.I : p.N;
+        const int64_t w_rows = static_cast<int64_t>(E) * p.N;
+        // All 192 weight rows, in the order of the MMA's columns.
+        const auto w_row = [&](const Item &it, int q) {
+            const int n = kSwiglu ? (q >= 3 ? q - 3 : q) * 32 + lane : q * 32 + lane;
+            return static_cast<int64_t>(it.e) * p.N + (kSwiglu && q >= 3 ? p.I : 0) + min(it.n0 + n, cols - 1);
+        };
+        const auto a_row = [&](const Item &it, int q) {
+            int row0, valid;
+            pair_rows(it, rank, &row0, &valid);
+            return static_cast<int64_t>(min(row0 + min(lane + 32 * q, max(valid - 1, 0)), p.rows - 1));
+        };
+        const uint32_t sf_tmem = tmem + kSfCol0 + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        constexpr int RW = kPairN / 32, RA = 4;
         if (warp == kWCopyWarp) {
-            // All 192 weight rows, in the order of the MMA's columns.
-            const int cols = kSwiglu ? p.I : p.N;
-            const int64_t w_rows = static_cast<int64_t>(E) * p.N;
-            copy_scales<P, kPairN / 32, kPairM, kTile>(v, g, 0, p.w_scales, w_rows, p.w_vec, [&](const Item &it, int q) {
-                const int n = kSwiglu ? (q >= 3 ? q - 3 : q) * 32 + lane : q * 32 + lane;
-                return static_cast<int64_t>(it.e) * p.N + (kSwiglu && q >= 3 ? p.I : 0) + min(it.n0 + n, cols - 1);
-            });
+            if constexpr (kShift) copy_scales_shift<2, RW, kPairM, kTile>(v, g, 0, p.w_scales, w_rows, w_row);
+            else copy_scales<P, RW, kPairM, kTile>(v, g, 0, p.w_scales, w_rows, p.w_vec, w_row);
         } else if (warp == kACopyWarp) {
-            copy_scales<P, 4, kPairM, kTile>(v, g, 6, p.a_scales, p.rows, p.a_vec, [&](const Item &it, int q) {
-                int row0, valid;
-                pair_rows(it, rank, &row0, &valid);
-                return static_cast<int64_t>(min(row0 + min(lane + 32 * q, max(valid - 1, 0)), p.rows - 1));
-            });
+            if constexpr (kShift) copy_scales_shift<2, RA, kPairM, kTile>(v, g, RW, p.a_scales, p.rows, a_row);
+            else copy_scales<P, RA, kPairM, kTile>(v, g, RW, p.a_scales, p.rows, p.a_vec, a_row);
         } else {
-            convert_scales<kNv, 4, kPairN / 32>(
-                v, g, 6, 0, tmem + kSfCol0 + (static_cast<uint32_t>((warp & 3) * 32) << 16), full, empty, n_stages);
+            convert_scales<kNv, kShift, RA, RW, kPairM, kTile>(v, g, RW, 0, sf_tmem, full, empty, n_stages, a_row, w_row);
         }
     } else {
         const int quarter = warp & 3, half = (warp - kEpilogueWarp) >> 2;
@@ -1394,7 +1498,7 @@ constexpr int kPairBandSwiglu = 112, kPairBand = 193;
 // out of order: full layer w13 with SwiGLU 451 -> 490 us.)
 constexpr int kPairCall = 8;
 
-template <bool kNv, bool kSwiglu>
+template <bool kNv, bool kSwiglu, bool kShift>
 moe_status launch(const Fp4Gemm &g, cudaStream_t stream, int num_sms, int *launches) {
     constexpr int band = kSwiglu ? kPairBandSwiglu : kPairBand;
     const bool pairs = g.rows >= (g.E == 1 ? band : kPairCall * band);
@@ -1430,7 +1534,7 @@ moe_status launch(const Fp4Gemm &g, cudaStream_t stream, int num_sms, int *launc
     *launches = 0;
     if (singles) {
         static std::atomic<uint64_t> mask{0};
-        const auto kernel = fp4_gemm_kernel<kNv, kSwiglu>;
+        const auto kernel = fp4_gemm_kernel<kNv, kSwiglu, kShift>;
         if (!set_smem(reinterpret_cast<const void *>(kernel), kSmemBytes, mask) ||
             !encode_codes(&tm_w, g.w_codes, w_rows, g.K, kTileN) || !encode_codes(&tm_a2, g.a_codes, g.rows, g.K, 16))
             return MOE_ERR_CUDA;
@@ -1443,7 +1547,7 @@ moe_status launch(const Fp4Gemm &g, cudaStream_t stream, int num_sms, int *launc
     }
     if (pairs) {
         static std::atomic<uint64_t> mask{0};
-        const auto kernel = fp4_gemm_pair_kernel<kNv, kSwiglu>;
+        const auto kernel = fp4_gemm_pair_kernel<kNv, kSwiglu, kShift>;
         if (!set_smem(reinterpret_cast<const void *>(kernel), kPairSmem, mask) ||
             !encode_codes(&tm_w, g.w_codes, w_rows, g.K, kPairN / 2) ||
             !encode_codes(&tm_a2, g.a_codes, g.rows, g.K, 32) || !encode_codes(&tm_a128, g.a_codes, g.rows, g.K, 128))
@@ -1465,11 +1569,17 @@ moe_status launch(const Fp4Gemm &g, cudaStream_t stream, int num_sms, int *launc
 moe_status launch_fp4_gemm(const Fp4Gemm &g, bool nv, bool swiglu, cudaStream_t stream, int num_sms, int *launches) {
     *launches = 0;
     if (g.rows == 0) return MOE_OK;
-    if (nv)
-        return swiglu ? fp4::launch<true, true>(g, stream, num_sms, launches)
-                      : fp4::launch<true, false>(g, stream, num_sms, launches);
-    return swiglu ? fp4::launch<false, true>(g, stream, num_sms, launches)
-                  : fp4::launch<false, false>(g, stream, num_sms, launches);
+    const uintptr_t scales = reinterpret_cast<uintptr_t>(g.w_scales) | reinterpret_cast<uintptr_t>(g.a_scales);
+    const bool shift = (g.K / (nv ? 16 : 32)) % 16 != 0 && scales % 16 == 0;
+    if (shift)
+        return nv ? swiglu ? fp4::launch<true, true, true>(g, stream, num_sms, launches)
+                           : fp4::launch<true, false, true>(g, stream, num_sms, launches)
+                  : swiglu ? fp4::launch<false, true, true>(g, stream, num_sms, launches)
+                           : fp4::launch<false, false, true>(g, stream, num_sms, launches);
+    return nv ? swiglu ? fp4::launch<true, true, false>(g, stream, num_sms, launches)
+                       : fp4::launch<true, false, false>(g, stream, num_sms, launches)
+              : swiglu ? fp4::launch<false, true, false>(g, stream, num_sms, launches)
+                       : fp4::launch<false, false, false>(g, stream, num_sms, launches);
 }
 
 }  // namespace moe
