@@ -470,6 +470,16 @@ __device__ __forceinline__ void read_words(const uint8_t *piece, uint32_t (&w)[R
     }
 }
 
+// bad_bits of words kQuarter, kQuarter + 4, ... of both operands'.
+template <bool kNv, int kQuarter, int RA, int RB, int W>
+__device__ __forceinline__ uint32_t bad_quarter(const uint32_t (&a)[RA][W], const uint32_t (&b)[RB][W]) {
+    uint32_t bad = 0;
+#pragma unroll
+    for (int i = kQuarter; i < (RA + RB) * W; i += 4)
+        bad |= bad_bits<kNv>(i < RA * W ? a[i < RA * W ? i / W : 0][i % W] : b[i < RA * W ? 0 : i / W - RA][i % W]);
+    return bad;
+}
+
 // A stage's columns of one operand.  kByTile: (tile of 128 rows, word, column), else
 // (word, tile, column).
 template <int R, int W, bool kByTile>
@@ -546,26 +556,15 @@ __device__ __forceinline__ void convert_scales(const ScaleEnv &v, const Staging 
                         const int skip = kNv ? 0 : set * 8, n = p.scale_row - (ks + set) * 4 * W;
                         read_shifted(piece + first_a * kRow, offs_a, skip, n, wa);
                         read_shifted(piece + first_b * kRow, offs_b, skip, n, wb);
-#pragma unroll
-                        for (int k = 0; k < W; ++k) {
-#pragma unroll
-                            for (int q = 0; q < RA; ++q) bad |= bad_bits<kNv>(wa[q][k]);
-#pragma unroll
-                            for (int q = 0; q < RB; ++q) bad |= bad_bits<kNv>(wb[q][k]);
-                        }
                     } else {
                         read_words(piece + first_a * 512, wa);
                         read_words(piece + first_b * 512, wb);
-                        // The four warps read the same bytes; each checks a quarter.
-#pragma unroll
-                        for (int i = 0; i < (RA + RB + 3) / 4; ++i)
-                            if (4 * i + 3 < RA + RB || quarter + 4 * i < RA + RB) {
-                                uint32_t x[1][W];
-                                read_words(piece + (quarter + 4 * i) * 512, x);
-#pragma unroll
-                                for (int k = 0; k < W; ++k) bad |= bad_bits<kNv>(x[0][k]);
-                            }
                     }
+                    // The four warps hold the same words; each checks a quarter.
+                    if (quarter == 0) bad |= bad_quarter<kNv, 0>(wa, wb);
+                    else if (quarter == 1) bad |= bad_quarter<kNv, 1>(wa, wb);
+                    else if (quarter == 2) bad |= bad_quarter<kNv, 2>(wa, wb);
+                    else bad |= bad_quarter<kNv, 3>(wa, wb);
                     const bool back = r.slot < 2;
                     if constexpr (kNv)
                         ok = wait(&empty[back ? r.slot + n_stages - 2 : r.slot - 2], r.phase ^ back, v.abort_flag,
