@@ -15,9 +15,9 @@
 //    the MMA reads; four MMAs of 64 k.
 //  * Block scales have to sit in tensor memory (word of row m at lane m % 32 of
 //    all four lane quarters, column m / 32; a word holds four consecutive
-//    scales).  Two warps copy the scale bytes row by row into a staging area
-//    (cp.async, several stages ahead), and four converter warps, one a lane
-//    quarter, read them back and write them with tcgen05.st.  So scales keep the
+//    scales).  TMA brings the scale bytes of four stages at a time into a staging
+//    area, and converter warps, one a lane quarter, read them back and write
+//    them with tcgen05.st.  So scales keep the
 //    layout the rest of the library uses, and tokens may start at any row.  The
 //    other way, atoms in shared memory and tcgen05.cp, cost the tensor pipe about
 //    66 cycles a copy: 600 (MXFP4) to 1,000 (NVFP4) cycles a stage, for 384 of MMA.
@@ -49,7 +49,7 @@ namespace moe {
 namespace fp4 {
 
 constexpr int kProducerWarp = 0, kIssuerWarp = 1;
-constexpr int kWCopyWarp = 2, kACopyWarp = 3;          // scale bytes of weights, of tokens
+constexpr int kCopyWarp = 2;                           // scale bytes (by threads: 2 weights, 3 tokens)
 constexpr int kSets = 2;                               // converter sets, on stages in turn
 constexpr int kConvertWarp = 4, kEpilogueWarp = kConvertWarp + 4 * kSets;   // four warps a set: one a lane quarter
 constexpr int kHalves = 2;                             // epilogue warps a lane quarter
@@ -97,7 +97,7 @@ struct Params {
     int out_bf16;
     int n_tiles;
     int scale_row;           // scale bytes a row of K: K / 32 or K / 16
-    int w_vec, a_vec;        // scale bytes that load at once (see copy_words)
+    int windows;             // scale tensors at 16-byte addresses (see copy_scales_shift)
     int band_lo, band_hi;    // this launch's bands: those of band_lo to band_hi rows
     uint64_t wait_limit_ns;
 };
@@ -212,35 +212,9 @@ struct Ring {
 
 // ---------------------------------------------------------- scale loaders
 
-// Copy of 16 scale bytes [at, at + 16) of one row into shared memory where a whole
-// group does not load as 16-byte vectors; zeros past the row's end (2^-127 or 0:
-// finite, and they meet zero codes).  `vec`: bytes that load at once (16, 8 or 4; it
-// divides the row and the base address).
-__device__ __noinline__ void copy_words(uint8_t *dst, const uint8_t *row, int at, int scale_row, int vec) {
-    const uint32_t sd = smem_u32(dst);
-    if (vec == 16) {
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(sd), "l"(row + at) : "memory");
-    } else if (vec == 8) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const bool in = at + 8 * i < scale_row;
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(sd + 8 * i),
-                         "l"(in ? row + at + 8 * i : row), "r"(in ? 8 : 0)
-                         : "memory");
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const bool in = at + 4 * i < scale_row;
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(sd + 4 * i),
-                         "l"(in ? row + at + 4 * i : row), "r"(in ? 4 : 0)
-                         : "memory");
-        }
-    }
-}
-
-// The same for rows at any address: the aligned words that hold the bytes, up to
-// six rows' in flight together, shifted into place.  A word that reaches outside the tensor
+// Scale bytes [at, at + 16) of R rows at any address into shared memory, zeros past a
+// row's end: the aligned words that hold the bytes, up to six rows' in flight
+// together, shifted into place.  A word that reaches outside the tensor
 // [lo, hi) is put together from its bytes inside.
 template <int R>
 __device__ __forceinline__ void copy_unaligned(uint8_t *dst, const uint8_t *const (&src)[R], int at, int scale_row,
@@ -281,7 +255,7 @@ __device__ __forceinline__ void copy_unaligned(uint8_t *dst, const uint8_t *cons
                 o[i] = __funnelshift_r(w[q - q0][i], w[q - q0][i + 1], shift);
                 if (left < 4) o[i] = left <= 0 ? 0u : o[i] & ((1u << (8 * left)) - 1u);
             }
-            *reinterpret_cast<uint4 *>(dst + q * 512) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4 *>(dst + q * 1024) = make_uint4(o[0], o[1], o[2], o[3]);
         }
     }
 }
@@ -296,13 +270,24 @@ __device__ __forceinline__ uint32_t bad_bits(uint32_t w) {
     return kNv ? w | plus : w & ~plus;
 }
 
-// Staging of both operands' scale bytes: kDepth groups of kGroup stages, which are 2
-// (MXFP4) or 4 (NVFP4) pieces of 16 bytes a row; R rows a lane and operand (row lane +
-// 32 q of the tile), 512 bytes from one q to the next, the weights' rows first.
+// Staging of both operands' scale bytes: kDepth groups, the weights' rows first; R rows
+// a lane and operand (row lane + 32 q of the tile).
+//
+// Rows of whole 16-byte pieces come by TMA, kGroup stages a group: 32 (MXFP4) or 64
+// (NVFP4) bytes a row in the swizzle of that width, which keeps the converters' reads
+// (a row a lane) free of bank conflicts, two-way at most for MXFP4.  (Copies by
+// threads, cp.async a row a lane, cost 32 shared-memory cycles each: the converters'
+// own reads then took 1,000 to 1,500 cycles a stage.)  Other rows: copy_scales_shift.
 struct Staging {
     uint8_t *bytes;
-    uint32_t piece_bytes;             // all rows' pieces
-    uint64_t *full, *empty;           // one a group: both copiers -> converters -> copiers
+    uint32_t group_bytes;
+    uint64_t *full, *empty;           // one a group: copiers -> converters -> copiers
+};
+
+// Staged bytes of a row and group, and of 32 rows (one q).
+template <bool kNv>
+struct GroupRow {
+    static constexpr int kBytes = kNv ? 64 : 32, kStep = 32 * kBytes;
 };
 
 // What the scale warps need of their kernel.
@@ -313,78 +298,55 @@ struct ScaleEnv {
     int first, step, total;           // the items: first, first + step, ... < total
 };
 
-// Copier warp.  The copies have a warp of their own so that nothing the converters
-// wait for or fence waits for copies of later stages.
-//
-// P: pieces of a group.  row(item, q): row of this lane, clamped to the tile's or the chunk's last row past
-// its end (those sums are never stored, and every staged byte is one of the tensor).
-template <int P, int R, int kMost, int kTile, class RowFn>
-__device__ __forceinline__ void copy_scales(const ScaleEnv &v, const Staging &g, int first_row, const uint8_t *base,
-                                            int64_t rows, int vec, RowFn row) {
+// Copier warp by TMA.  issue(item, group, dst, bar), by one lane, starts the copies of
+// a group; bytes(item): what they bring.
+template <int kMost, int kTile, class Issue, class Bytes>
+__device__ __forceinline__ void copy_scales(const ScaleEnv &v, const Staging &g, Issue issue, Bytes bytes) {
     const Params &p = *v.p;
-    const int lane = threadIdx.x & 31;
-    const int pieces = (p.scale_row + 15) / 16;
-    const int64_t bytes = rows * p.scale_row;
-    uint8_t *mine = g.bytes + first_row * 512 + lane * 16;
+    const bool leader = elect_one();
+    const int groups = (p.K + kGroup * kStageK - 1) / (kGroup * kStageK);
+    const uint32_t base = smem_u32(g.bytes);
     Ring r;
+    uint32_t issued = 0;
     bool ok = true;
     for (int j = v.first; ok && j < v.total; j += v.step) {
         const Item it = decode_item<kMost, kTile>(j, v.roff, v.ioff, p.E, p.n_tiles);
-        const uint8_t *src[R];
-#pragma unroll
-        for (int q = 0; q < R; ++q) src[q] = base + row(it, q) * p.scale_row;
-        for (int i = 0; i < pieces; i += P) {
+        const uint32_t n = bytes(it);
+        for (int i = 0; i < groups; ++i) {
             ok = wait(&g.empty[r.slot], r.phase ^ 1u, v.abort_flag, p.status, p.wait_limit_ns);
             if (!ok) break;
-            uint8_t *dst = mine + r.slot * P * g.piece_bytes;
-            if (vec == 16 && i + P <= pieces) {
-                const uint32_t sd = smem_u32(dst);
-#pragma unroll
-                for (int q = 0; q < R; ++q) {
-#pragma unroll
-                    for (int k = 0; k < P; ++k)
-                        asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(sd + k * g.piece_bytes + q * 512),
-                                     "l"(src[q] + 16 * k)
-                                     : "memory");
-                    src[q] += 16 * P;
-                }
-            } else if (vec == 1) {
-#pragma unroll 1
-                for (int k = 0; k < P && i + k < pieces; ++k)
-                    copy_unaligned<R>(dst + k * g.piece_bytes, src, (i + k) * 16, p.scale_row, base, base + bytes);
-            } else {
-#pragma unroll 1
-                for (int k = 0; k < P && i + k < pieces; ++k)
-#pragma unroll 1
-                    for (int q = 0; q < R; ++q)
-                        copy_words(dst + k * g.piece_bytes + q * 512, base + row(it, q) * p.scale_row, (i + k) * 16,
-                                   p.scale_row, vec);
+            if (leader) {
+                mbar_arrive_expect_tx(&g.full[r.slot], n);
+                issue(it, i, base + r.slot * g.group_bytes, &g.full[r.slot]);
             }
-            if (vec == 1)
-                mbar_arrive(&g.full[r.slot]);
-            else
-                asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(&g.full[r.slot]))
-                             : "memory");
             __syncwarp();
+            ++issued;
             r.next(kDepth);
         }
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");   // none in flight when the CTA leaves
+    if (!ok && (threadIdx.x & 31) == 0) {   // drain: every issued copy must land before the CTA exits
+        for (uint32_t i = issued > kDepth ? issued - kDepth : 0; i < issued; ++i)
+            wait_bounded(&g.full[i % kDepth], (i / kDepth) & 1u, nullptr, p.status, p.wait_limit_ns);
+    }
 }
 
-// Copier warp for rows that are not whole 16-byte pieces, of 16-byte aligned tensors:
-// the two aligned 16-byte windows that hold a piece go into the staging area as they
-// are, 1,024 bytes from one q to the next, and the converters shift.  (Loads that
+// Copier warp for rows that are not whole 16-byte pieces (one an operand).  Tensors
+// at 16-byte addresses: the two aligned 16-byte windows that hold a piece go into the
+// staging area as they are, 1,024 bytes from one q to the next, and the converters
+// shift.  Others are shifted here and take the first window.
+// P: pieces of a group.  row(item, q): row of this lane, clamped to the tile's or the
+// chunk's last row past its end (those sums are never stored, and every staged byte
+// is one of the tensor).  (Loads that
 // were shifted here, before their store, waited for memory once a piece: 8 us of a
 // 16 us call at K = 1,056.)
 template <int P, int R, int kMost, int kTile, class RowFn>
 __device__ __forceinline__ void copy_scales_shift(const ScaleEnv &v, const Staging &g, int first_row,
-                                                  const uint8_t *base, int64_t rows, RowFn row) {
+                                                  const uint8_t *base, int64_t rows, bool windows, RowFn row) {
     const Params &p = *v.p;
     const int lane = threadIdx.x & 31;
     const int pieces = (p.scale_row + 15) / 16;
     const int64_t bytes = rows * p.scale_row;
-    const uint32_t mine = smem_u32(g.bytes + first_row * 1024 + lane * 16);
+    uint8_t *mine = g.bytes + first_row * 1024 + lane * 16;
     Ring r;
     bool ok = true;
     for (int j = v.first; ok && j < v.total; j += v.step) {
@@ -394,7 +356,15 @@ __device__ __forceinline__ void copy_scales_shift(const ScaleEnv &v, const Stagi
             if (!ok) break;
 #pragma unroll 1
             for (int k = 0; k < P && i + k < pieces; ++k) {
-                const uint32_t dst = mine + (r.slot * P + k) * 2 * g.piece_bytes;
+                uint8_t *to = mine + r.slot * g.group_bytes + k * (g.group_bytes / P);
+                if (!windows) {
+                    const uint8_t *src[R];
+#pragma unroll
+                    for (int q = 0; q < R; ++q) src[q] = base + row(it, q) * p.scale_row;
+                    copy_unaligned<R>(to, src, (i + k) * 16, p.scale_row, base, base + bytes);
+                    continue;
+                }
+                const uint32_t dst = smem_u32(to);
                 const int n = min(16, p.scale_row - (i + k) * 16);
 #pragma unroll
                 for (int q = 0; q < R; ++q) {
@@ -409,6 +379,12 @@ __device__ __forceinline__ void copy_scales_shift(const ScaleEnv &v, const Stagi
                                  "l"(base + window + (second > 0 ? 16 : 0)), "r"(max(second, 0))
                                  : "memory");
                 }
+            }
+            if (!windows) {
+                mbar_arrive(&g.full[r.slot]);
+                __syncwarp();
+                r.next(kDepth);
+                continue;
             }
             asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(&g.full[r.slot])) : "memory");
             __syncwarp();
@@ -455,16 +431,16 @@ __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&v)[C]) 
     }
 }
 
-// W scale words of every row of one staged piece.
-template <int R, int W>
-__device__ __forceinline__ void read_words(const uint8_t *piece, uint32_t (&w)[R][W]) {
+// W scale words of every row of one staged group, kStep bytes from one q to the next.
+template <int kStep, int R, int W>
+__device__ __forceinline__ void read_words(const uint8_t *at, uint32_t (&w)[R][W]) {
 #pragma unroll
     for (int q = 0; q < R; ++q) {
         if constexpr (W == 2) {
-            const uint2 x = *reinterpret_cast<const uint2 *>(piece + q * 512);
+            const uint2 x = *reinterpret_cast<const uint2 *>(at + q * kStep);
             w[q][0] = x.x; w[q][1] = x.y;
         } else {
-            const uint4 x = *reinterpret_cast<const uint4 *>(piece + q * 512);
+            const uint4 x = *reinterpret_cast<const uint4 *>(at + q * kStep);
             w[q][0] = x.x; w[q][1] = x.y; w[q][2] = x.z; w[q][3] = x.w;
         }
     }
@@ -494,9 +470,9 @@ __device__ __forceinline__ void store_words(uint32_t taddr, const uint32_t (&w)[
     tmem_st<4 * T * W>(taddr, v);
 }
 
-__device__ __forceinline__ void init_scale_bars(uint64_t *raw_bars) {
+__device__ __forceinline__ void init_scale_bars(uint64_t *raw_bars, uint32_t copiers) {
     for (int d = 0; d < kDepth; ++d) {
-        mbar_init(&raw_bars[d], 64);                  // the copiers' lanes
+        mbar_init(&raw_bars[d], copiers);             // by TMA: 1; by threads: the two warps' lanes
         mbar_init(&raw_bars[kDepth + d], 4 * kSets);  // the converter warps
     }
 }
@@ -515,11 +491,11 @@ __device__ __forceinline__ void init_scale_bars(uint64_t *raw_bars) {
 template <bool kNv, bool kShift, int RA, int RB, int kMost, int kTile, class RowA, class RowB>
 __device__ __forceinline__ void convert_scales(const ScaleEnv &v, const Staging &g, int first_a, int first_b,
                                                uint32_t sf_tmem, uint64_t *full, uint64_t *empty, uint32_t n_stages,
-                                               RowA row_a, RowB row_b) {
+                                               bool windows, RowA row_a, RowB row_b) {
     using C = ScaleCols<kNv>;
     constexpr int W = C::W, kACols = 4 * ((RA + 3) / 4) * W;
-    constexpr int kStages = kShift && kNv ? 2 : kGroup, P = kStages * W / 4;    // a group's
-    constexpr int kRow = kShift ? 1024 : 512;
+    constexpr int kStages = kShift && kNv ? 2 : kGroup;       // of a group
+    constexpr int kStep = GroupRow<kNv>::kStep;
     static_assert(kACols + 4 * ((RB + 3) / 4) * W == C::kCols, "scale columns of a stage");
     static_assert(kSets == 2 && kGroup % 2 == 0, "sets take stages in turn");
     const Params &p = *v.p;
@@ -528,15 +504,16 @@ __device__ __forceinline__ void convert_scales(const ScaleEnv &v, const Staging 
     const int set = ((threadIdx.x >> 5) - kConvertWarp) >> 2;
     uint32_t bad = 0;
     bool ok = true;
-    const uint32_t piece_bytes = g.piece_bytes * (kRow / 512);
-    // MXFP4: a piece is two stages, the set's the half it starts at; NVFP4: one.
-    const uint8_t *mine = g.bytes + lane * 16 + (kNv ? set * piece_bytes : kShift ? 0 : set * 8);
+    // By TMA: this lane's rows, whose 16-byte chunk c lies at c ^ swizzle.  Shifted: a
+    // piece is half a group, of two MXFP4 stages or one of NVFP4.
+    const uint8_t *mine = g.bytes + lane * (kShift ? 16 : GroupRow<kNv>::kBytes);
+    const int swizzle = kNv ? lane >> 1 & 3 : lane >> 2 & 1;
     Ring raw, r;                  // staged group, this set's next stage
     uint32_t sf = set;            // NVFP4: scale slot
     if (set) r.next(n_stages);
     for (int j = v.first; ok && j < v.total; j += v.step) {
         uint64_t offs_a = 0, offs_b = 0;       // byte each row's pieces start at in their windows
-        if constexpr (kShift) {
+        if (kShift && windows) {
             const Item it = decode_item<kMost, kTile>(j, v.roff, v.ioff, p.E, p.n_tiles);
 #pragma unroll
             for (int q = 0; q < RA; ++q) offs_a |= static_cast<uint64_t>(row_a(it, q) * p.scale_row & 15) << (4 * q);
@@ -545,20 +522,23 @@ __device__ __forceinline__ void convert_scales(const ScaleEnv &v, const Staging 
         }
         for (int k0 = 0; ok && k0 < k_stages; k0 += kStages) {
             ok = wait(&g.full[raw.slot], raw.phase, v.abort_flag, p.status, p.wait_limit_ns);
-            const uint8_t *piece = mine + raw.slot * P * piece_bytes;
+            const uint8_t *group = mine + raw.slot * g.group_bytes;
             const int end = min(k0 + kStages, k_stages);
 #pragma unroll 1
-            for (int ks = k0; ok && ks < end; ks += 2, piece += (kNv ? 2 : 1) * piece_bytes) {
+            for (int ks = k0; ok && ks < end; ks += 2) {
                 const int by = ks + 2 <= k_stages ? 2 : 1;
                 if (ks + set < k_stages) {     // an odd last stage is the first set's
                     uint32_t wa[RA][W], wb[RB][W];
+                    const int i = (ks - k0) >> 1;
                     if constexpr (kShift) {
+                        const uint8_t *piece = group + (kNv ? set : i) * (g.group_bytes / 2);
                         const int skip = kNv ? 0 : set * 8, n = p.scale_row - (ks + set) * 4 * W;
-                        read_shifted(piece + first_a * kRow, offs_a, skip, n, wa);
-                        read_shifted(piece + first_b * kRow, offs_b, skip, n, wb);
+                        read_shifted(piece + first_a * 1024, offs_a, skip, n, wa);
+                        read_shifted(piece + first_b * 1024, offs_b, skip, n, wb);
                     } else {
-                        read_words(piece + first_a * 512, wa);
-                        read_words(piece + first_b * 512, wb);
+                        const uint8_t *at = group + (((kNv ? 2 * i + set : i) ^ swizzle) << 4) + (kNv ? 0 : set * 8);
+                        read_words<kStep>(at + first_a * kStep, wa);
+                        read_words<kStep>(at + first_b * kStep, wb);
                     }
                     // The four warps hold the same words; each checks a quarter.
                     if (quarter == 0) bad |= bad_quarter<kNv, 0>(wa, wb);
@@ -584,6 +564,8 @@ __device__ __forceinline__ void convert_scales(const ScaleEnv &v, const Staging 
                 sf ^= by & 1;
                 r.next(n_stages, by);
             }
+            // The group was read by loads; its next contents may come by TMA.
+            if constexpr (!kShift) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) mbar_arrive(&g.empty[raw.slot]);
             raw.next(kDepth);
@@ -713,6 +695,15 @@ __device__ __forceinline__ void store_swiglu(const Params &p, const Item &it, ui
     }
 }
 
+// Zeros in the staging area: the converters look at all of a group's bytes for ones
+// the format does not allow, also where the item has fewer token rows (later they
+// find an earlier item's).  Before the barrier that lets the copies start.
+__device__ __forceinline__ void clear_staging(uint8_t *staging, int bytes) {
+    for (int i = threadIdx.x * 16; i < bytes; i += kThreads * 16)
+        *reinterpret_cast<uint4 *>(staging + i) = make_uint4(0, 0, 0, 0);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
 // Row and item offsets from the group sizes (64-bit sums: sizes that wrap 32 bits
 // are caught), and the widest chunk.  Rows count every band, items those of this
 // launch.  The experts go 32 to a warp, first for their totals, then for the offsets
@@ -798,7 +789,8 @@ __device__ __forceinline__ bool build_items(const Params &p, int *roff, int *iof
 template <bool kNv, bool kSwiglu, bool kShift>
 __global__ void __launch_bounds__(kThreads, 1)
     fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a64,
-                    const __grid_constant__ CUtensorMap tm_a16, const Params p) {
+                    const __grid_constant__ CUtensorMap tm_a16, const __grid_constant__ CUtensorMap tm_ws,
+                    const __grid_constant__ CUtensorMap tm_as, const Params p) {
     using S = Shape<kNv, kSwiglu>;
     using C = ScaleCols<kNv>;
     extern __shared__ uint8_t smem_raw[];
@@ -824,6 +816,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int total = __reduce_max_sync(0xffffffffu, ioff[E]);
     if (static_cast<int>(blockIdx.x) >= total) return;
 
+    if constexpr (!kShift) clear_staging(smem + kOffStaging, kOffRow - kOffStaging);
     // Stage layout: as many stages as fit with the widest chunk of this call.
     const int nt_max = *nt_slot;
     const uint32_t b_rows = nt_max <= 32 ? nt_max : (nt_max + 63) & ~63;
@@ -838,7 +831,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&full[s], 1 + 4);
             mbar_init(&empty[s], 1);
         }
-        init_scale_bars(raw_bars);
+        init_scale_bars(raw_bars, kShift ? 64 : 1);
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
             mbar_init(&acc_empty[b], 4 * kHalves);
@@ -950,8 +943,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait(final_bar, 0, nullptr, p.status, lim);
     } else if (warp < kEpilogueWarp) {
         const ScaleEnv v = {&p, roff, ioff, abort_flag, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), total};
-        const Staging g = {smem + kOffStaging, (4 * S::MT + S::AR) * 512, raw_bars, raw_bars + kDepth};
-        constexpr int P = kGroup * C::W / 4;
+        constexpr int RW = 4 * S::MT, RA = S::AR, kStep = GroupRow<kNv>::kStep;
+        const Staging g = {smem + kOffStaging, (RW + RA) * (kShift ? 2048u : kStep), raw_bars, raw_bars + kDepth};
         const int cols = kSwiglu ? p.I : p.N;
         const int64_t w_rows = static_cast<int64_t>(E) * p.N;
         const auto w_row = [&](const Item &it, int q) {
@@ -961,15 +954,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             return static_cast<int64_t>(it.row0 + min(lane + 32 * q, it.nvalid - 1));
         };
         const uint32_t sf_tmem = tmem + kSfCol0 + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        constexpr int RW = 4 * S::MT, RA = S::AR;
-        if (warp == kWCopyWarp) {
-            if constexpr (kShift) copy_scales_shift<2, RW, S::NT, kTileN>(v, g, 0, p.w_scales, w_rows, w_row);
-            else copy_scales<P, RW, S::NT, kTileN>(v, g, 0, p.w_scales, w_rows, p.w_vec, w_row);
-        } else if (warp == kACopyWarp) {
-            if constexpr (kShift) copy_scales_shift<2, RA, S::NT, kTileN>(v, g, RW, p.a_scales, p.rows, a_row);
-            else copy_scales<P, RA, S::NT, kTileN>(v, g, RW, p.a_scales, p.rows, p.a_vec, a_row);
-        } else {
-            convert_scales<kNv, kShift, RW, RA, S::NT, kTileN>(v, g, 0, RW, sf_tmem, full, empty, n_stages, w_row, a_row);
+        if (warp >= kConvertWarp) {
+            convert_scales<kNv, kShift, RW, RA, S::NT, kTileN>(v, g, 0, RW, sf_tmem, full, empty, n_stages, p.windows,
+                                                               w_row, a_row);
+        } else if constexpr (kShift) {
+            if (warp == kCopyWarp)
+                copy_scales_shift<2, RW, S::NT, kTileN>(v, g, 0, p.w_scales, w_rows, p.windows, w_row);
+            else
+                copy_scales_shift<2, RA, S::NT, kTileN>(v, g, RW, p.a_scales, p.rows, p.windows, a_row);
+        } else if (warp == kCopyWarp) {
+            // 128-row boxes of weights, 32-row boxes of tokens.
+            copy_scales<S::NT, kTileN>(
+                v, g,
+                [&](const Item &it, int i, uint32_t dst, uint64_t *bar) {
+                    const int x = i * GroupRow<kNv>::kBytes;
+#pragma unroll
+                    for (int m = 0; m < S::MT; ++m) tma_load_3d(dst + 4 * m * kStep, &tm_ws, x, it.n0, it.e * S::MT + m, bar);
+                    for (int q = 0; 32 * q < it.nvalid; ++q)
+                        tma_load_2d(dst + (RW + q) * kStep, &tm_as, x, it.row0 + 32 * q, bar);
+                },
+                [&](const Item &it) { return (RW + (it.nvalid + 31) / 32) * kStep; });
         }
     } else {
         const int quarter = warp & 3, half = (warp - kEpilogueWarp) >> 2;
@@ -1223,6 +1227,7 @@ template <bool kNv, bool kSwiglu, bool kShift>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a128,
                          const __grid_constant__ CUtensorMap tm_a64, const __grid_constant__ CUtensorMap tm_a32,
+                         const __grid_constant__ CUtensorMap tm_ws, const __grid_constant__ CUtensorMap tm_as,
                          const Params p, int out_vec) {
     using C = ScaleCols<kNv>;
     constexpr int kTile = kSwiglu ? kPairN / 2 : kPairN;            // output columns of an item
@@ -1251,6 +1256,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // redux: the compiler then knows the loops' bounds as warp-uniform
     const int total = __reduce_max_sync(0xffffffffu, ioff[E]);
     if (first >= total) return;
+    if constexpr (!kShift) clear_staging(smem + kPairOffStaging, kPairStaging);
     constexpr uint32_t n_stages = kPairStages;
     static_assert(kPairStages == kMaxStages, "see convert_scales");
     const int k_stages = (p.K + kStageK - 1) / kStageK;
@@ -1262,7 +1268,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_init(&full[s], 1 + 4 + (rank == 0 ? 1 : 0));
             mbar_init(&empty[s], 1);
         }
-        init_scale_bars(raw_bars);
+        init_scale_bars(raw_bars, kShift ? 64 : 1);
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
             mbar_init(&acc_empty[b], 2 * 4 * kHalves);
@@ -1378,8 +1384,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         wait(final_bar, 0, nullptr, p.status, lim);
     } else if (warp < kEpilogueWarp) {
         const ScaleEnv v = {&p, roff, ioff, abort_flag, first, step, total};
-        const Staging g = {smem + kPairOffStaging, (6 + 4) * 512, raw_bars, raw_bars + kDepth};
-        constexpr int P = kGroup * C::W / 4;
+        constexpr int RW = kPairN / 32, RA = 4, kStep = GroupRow<kNv>::kStep;
+        const Staging g = {smem + kPairOffStaging, (RW + RA) * (kShift ? 2048u : kStep), raw_bars, raw_bars + kDepth};
         const int cols = kSwiglu ? p.I : p.N;
         const int64_t w_rows = static_cast<int64_t>(E) * p.N;
         // All 192 weight rows, in the order of the MMA's columns.
@@ -1393,15 +1399,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             return static_cast<int64_t>(min(row0 + min(lane + 32 * q, max(valid - 1, 0)), p.rows - 1));
         };
         const uint32_t sf_tmem = tmem + kSfCol0 + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        constexpr int RW = kPairN / 32, RA = 4;
-        if (warp == kWCopyWarp) {
-            if constexpr (kShift) copy_scales_shift<2, RW, kPairM, kTile>(v, g, 0, p.w_scales, w_rows, w_row);
-            else copy_scales<P, RW, kPairM, kTile>(v, g, 0, p.w_scales, w_rows, p.w_vec, w_row);
-        } else if (warp == kACopyWarp) {
-            if constexpr (kShift) copy_scales_shift<2, RA, kPairM, kTile>(v, g, RW, p.a_scales, p.rows, a_row);
-            else copy_scales<P, RA, kPairM, kTile>(v, g, RW, p.a_scales, p.rows, p.a_vec, a_row);
-        } else {
-            convert_scales<kNv, kShift, RA, RW, kPairM, kTile>(v, g, RW, 0, sf_tmem, full, empty, n_stages, a_row, w_row);
+        if (warp >= kConvertWarp) {
+            convert_scales<kNv, kShift, RA, RW, kPairM, kTile>(v, g, RW, 0, sf_tmem, full, empty, n_stages, p.windows,
+                                                               a_row, w_row);
+        } else if constexpr (kShift) {
+            if (warp == kCopyWarp)
+                copy_scales_shift<2, RW, kPairM, kTile>(v, g, 0, p.w_scales, w_rows, p.windows, w_row);
+            else
+                copy_scales_shift<2, RA, kPairM, kTile>(v, g, RW, p.a_scales, p.rows, p.windows, a_row);
+        } else if (warp == kCopyWarp) {
+            // Two 96-row boxes of weights (gate and up, or 192 rows), 64-row boxes of
+            // this CTA's tokens.
+            copy_scales<kPairM, kTile>(
+                v, g,
+                [&](const Item &it, int i, uint32_t dst, uint64_t *bar) {
+                    const int x = i * GroupRow<kNv>::kBytes;
+                    int row0, valid;
+                    pair_rows(it, rank, &row0, &valid);
+                    tma_load_3d(dst, &tm_ws, x, it.n0, kSwiglu ? 2 * it.e : it.e, bar);
+                    tma_load_3d(dst + 3 * kStep, &tm_ws, x, kSwiglu ? it.n0 : it.n0 + kPairN / 2,
+                                kSwiglu ? 2 * it.e + 1 : it.e, bar);
+                    for (int q = 0; 32 * q < valid; q += 2)
+                        tma_load_2d(dst + (RW + q) * kStep, &tm_as, x, row0 + 32 * q, bar);
+                },
+                [&](const Item &it) {
+                    int row0, valid;
+                    pair_rows(it, rank, &row0, &valid);
+                    return (RW + (valid + 63) / 64 * 2) * kStep;
+                });
         }
     } else {
         const int quarter = warp & 3, half = (warp - kEpilogueWarp) >> 2;
@@ -1472,6 +1497,22 @@ bool encode_codes(CUtensorMap *map, const void *base, int64_t rows, int K, uint3
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Scale bytes [outer][rows][scale_row] in boxes of one group's bytes a row by `box_rows`
+// rows; bytes past a row's end and rows past the last of an expert (half) read as zeros.
+bool encode_scales(CUtensorMap *map, const void *base, int scale_row, int64_t rows, int64_t outer, uint32_t box_rows,
+                   bool nv) {
+    PFN_cuTensorMapEncodeTiled_v12000 encode = encode_fn();
+    if (!encode) return false;
+    const cuuint64_t pitch = static_cast<cuuint64_t>(scale_row);
+    cuuint64_t dims[3] = {pitch, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(outer)};
+    cuuint64_t strides[2] = {pitch, pitch * static_cast<cuuint64_t>(rows)};
+    cuuint32_t box[3] = {nv ? 64u : 32u, box_rows, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, outer ? 3 : 2, const_cast<void *>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, nv ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Shared-memory attribute of a kernel, set once per device (the mask is the
 // caller's, one per kernel).
 bool set_smem(const void *kernel, int bytes, std::atomic<uint64_t> &mask) {
@@ -1519,28 +1560,30 @@ moe_status launch(const Fp4Gemm &g, cudaStream_t stream, int num_sms, int *launc
     p.I = kSwiglu ? g.N / 2 : 0;
     p.out_bf16 = g.out_bf16;
     p.scale_row = g.K / (kNv ? 16 : 32);
-    const auto vec = [&](const uint8_t *scales) {
-        const uintptr_t both = reinterpret_cast<uintptr_t>(scales) | static_cast<uintptr_t>(p.scale_row);
-        return both % 16 == 0 ? 16 : both % 8 == 0 ? 8 : both % 4 == 0 ? 4 : 1;
-    };
-    p.w_vec = vec(g.w_scales);
-    p.a_vec = vec(g.a_scales);
+    p.windows = (reinterpret_cast<uintptr_t>(g.w_scales) | reinterpret_cast<uintptr_t>(g.a_scales)) % 16 == 0;
     p.wait_limit_ns = g.wait_limit_ns;
     const int64_t w_rows = static_cast<int64_t>(g.E) * g.N;
     const int columns = kSwiglu ? g.N / 2 : g.N;
-    CUtensorMap tm_w, tm_a64, tm_a2, tm_a128;
+    CUtensorMap tm_w, tm_a64, tm_a2, tm_a128, tm_ws, tm_as;
     if (!encode_codes(&tm_a64, g.a_codes, g.rows, g.K, 64)) return MOE_ERR_CUDA;
+    tm_ws = tm_as = tm_a64;         // not used where threads copy the scales
+    const auto scale_maps = [&](uint32_t w_box, uint32_t a_box) {
+        return kShift || (encode_scales(&tm_ws, g.w_scales, p.scale_row, columns, static_cast<int64_t>(g.E) * (kSwiglu ? 2 : 1),
+                                        w_box, kNv) &&
+                          encode_scales(&tm_as, g.a_scales, p.scale_row, g.rows, 0, a_box, kNv));
+    };
     *launches = 0;
     if (singles) {
         static std::atomic<uint64_t> mask{0};
         const auto kernel = fp4_gemm_kernel<kNv, kSwiglu, kShift>;
         if (!set_smem(reinterpret_cast<const void *>(kernel), kSmemBytes, mask) ||
-            !encode_codes(&tm_w, g.w_codes, w_rows, g.K, kTileN) || !encode_codes(&tm_a2, g.a_codes, g.rows, g.K, 16))
+            !encode_codes(&tm_w, g.w_codes, w_rows, g.K, kTileN) || !encode_codes(&tm_a2, g.a_codes, g.rows, g.K, 16) ||
+            !scale_maps(kTileN, 32))
             return MOE_ERR_CUDA;
         p.n_tiles = (columns + kTileN - 1) / kTileN;
         p.band_lo = 1;
         p.band_hi = pairs ? band - 1 : INT32_MAX;
-        kernel<<<num_sms, kThreads, kSmemBytes, stream>>>(tm_w, tm_a64, tm_a2, p);
+        kernel<<<num_sms, kThreads, kSmemBytes, stream>>>(tm_w, tm_a64, tm_a2, tm_ws, tm_as, p);
         if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
         ++*launches;
     }
@@ -1549,14 +1592,15 @@ moe_status launch(const Fp4Gemm &g, cudaStream_t stream, int num_sms, int *launc
         const auto kernel = fp4_gemm_pair_kernel<kNv, kSwiglu, kShift>;
         if (!set_smem(reinterpret_cast<const void *>(kernel), kPairSmem, mask) ||
             !encode_codes(&tm_w, g.w_codes, w_rows, g.K, kPairN / 2) ||
-            !encode_codes(&tm_a2, g.a_codes, g.rows, g.K, 32) || !encode_codes(&tm_a128, g.a_codes, g.rows, g.K, 128))
+            !encode_codes(&tm_a2, g.a_codes, g.rows, g.K, 32) || !encode_codes(&tm_a128, g.a_codes, g.rows, g.K, 128) ||
+            !scale_maps(kPairN / 2, 64))
             return MOE_ERR_CUDA;
         constexpr int tile = kSwiglu ? kPairN / 2 : kPairN;
         p.n_tiles = (columns + tile - 1) / tile;
         p.band_lo = band;
         p.band_hi = INT32_MAX;
         const int out_vec = reinterpret_cast<uintptr_t>(g.out) % 32 == 0 && g.N % (g.out_bf16 ? 16 : 8) == 0;
-        kernel<<<num_sms & ~1, kThreads, kPairSmem, stream>>>(tm_w, tm_a128, tm_a64, tm_a2, p, out_vec);
+        kernel<<<num_sms & ~1, kThreads, kPairSmem, stream>>>(tm_w, tm_a128, tm_a64, tm_a2, tm_ws, tm_as, p, out_vec);
         if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
         ++*launches;
     }
@@ -1569,7 +1613,7 @@ moe_status launch_fp4_gemm(const Fp4Gemm &g, bool nv, bool swiglu, cudaStream_t 
     *launches = 0;
     if (g.rows == 0) return MOE_OK;
     const uintptr_t scales = reinterpret_cast<uintptr_t>(g.w_scales) | reinterpret_cast<uintptr_t>(g.a_scales);
-    const bool shift = (g.K / (nv ? 16 : 32)) % 16 != 0 && scales % 16 == 0;
+    const bool shift = (g.K / (nv ? 16 : 32)) % 16 != 0 || scales % 16 != 0;
     if (shift)
         return nv ? swiglu ? fp4::launch<true, true, true>(g, stream, num_sms, launches)
                            : fp4::launch<true, false, true>(g, stream, num_sms, launches)
