@@ -1527,11 +1527,12 @@ bool set_smem(const void *kernel, int bytes, std::atomic<uint64_t> &mask) {
 
 // Bands of at least this many rows run in CTA pairs.  Both kernels at 24 bands of K =
 // 4096 (w13 with SwiGLU) and K = 2048 (w2, f32), MXFP4, one CTA / pair, us:
-//   rows            64          128         192         256         512
-//   SwiGLU      43.3 / 49.4  53.7 / 50.7  60.2 / 50.9  74.3 / 52.3   130 / 86.9
-//   plain       28.8 / 32.0  32.3 / 34.6  37.7 / 38.1  46.5 / 41.5  72.7 / 66.2
-// (a chunk is 96 tokens with SwiGLU and 192 without, against 256 in a pair).
-constexpr int kPairBandSwiglu = 112, kPairBand = 193;
+//   rows            64          128         192         256         512        2048
+//   SwiGLU      41.9 / 48.4  52.3 / 50.2  59.2 / 50.5  71.8 / 51.2   125 / 82.7  419 / 282
+//   plain       28.7 / 31.3  33.1 / 34.3  38.4 / 37.6  46.5 / 41.0  73.4 / 64.5  247 / 216
+// (a chunk is 96 tokens with SwiGLU and 192 without, against 256 in a pair; NVFP4
+// crosses at the same sizes).
+constexpr int kPairBandSwiglu = 112, kPairBand = 160;
 // A call of fewer rows than this many times that is one launch, without pairs: the
 // empty launch of the other class costs about 4 us, as much as pairs would gain.  (The
 // second as a programmatic dependent launch saved that, but its clusters then start
