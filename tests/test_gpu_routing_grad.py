@@ -58,6 +58,31 @@ def test_combine_backward(B, T, E, k, N, types):
     assert bool(((dw.double() - ref).abs() <= (N / 32 + 8) * 2.0 ** -24 * mag).all())
 
 
+@pytest.mark.parametrize("types", [(F32, F32, F32), (BF16, BF16, BF16)], ids=["f32", "bf16"])
+@pytest.mark.parametrize("T,E,k,N", [(200, 8, 3, 72), (9, 8, 4, 12), (33, 8, 2, 3), (3, 4, 2, 1024), (16, 8, 8, 4096),
+                                     (64, 8, 6, 516), (5, 8, 2, 131)])
+def test_combine_backward_short_rows_and_few_slots(B, T, E, k, N, types):
+    """Fewer threads a slot than a warp, and a whole block, with slots that have no row.
+    dw: a lane adds up to max(8, N / 32) products and at most 8 + 5 joins follow."""
+    gen = torch.Generator(device=DEV).manual_seed(T + N)
+    ids = inputs.route_uniform(T, T, E, k)
+    ids.reshape(-1)[1::5] = -1
+    s2r = B.route_sort(torch.from_numpy(ids).to(DEV), E)[3]
+    w = torch.rand((T, k), generator=gen, device=DEV)
+    dout, y = rand(gen, (T, N), types[0]), rand(gen, (T * k, N), types[1])
+    out = torch.full((T * k, N), 7.0, dtype=types[2], device=DEV)
+    dw = torch.full((T, k), 7.0, device=DEV)
+    dy, _ = B.combine_backward(dout, y, s2r, w, out=(out, dw))
+    on, at = s2r >= 0, s2r.clamp_min(0).long()
+    want = torch.full_like(out, 7.0)
+    want[at[on]] = (w[:, :, None] * dout.float()[:, None, :]).view(T * k, N).to(types[2])[on]
+    assert torch.equal(dy, want)
+    prod = dout.double()[:, None, :] * y.double()[at].view(T, k, N) * on.view(T, k, 1)
+    ref, mag = prod.sum(-1), prod.abs().sum(-1)
+    assert bool(((dw.double() - ref).abs() <= (max(8, N / 32) + 13) * 2.0 ** -24 * mag).all())
+    assert torch.equal(dw, B.combine_backward(dout, y, s2r, w)[1])
+
+
 @pytest.mark.parametrize("src,dst", [(F32, F32), (BF16, BF16), (BF16, F32), (F32, BF16)])
 @pytest.mark.parametrize("T,E,k,N", SHAPES)
 def test_gather_backward(B, T, E, k, N, src, dst):
