@@ -172,6 +172,37 @@ def test_quantize_gather_strides_and_alignment(B, fmt):
 
 
 @pytest.mark.parametrize("fmt", [MX, NV], ids=["mx", "nv"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_quantize_many_rows_repeat_few(B, fmt, dtype):
+    """More rows than the GPU holds warps for, gathered from 130, some without a source, with
+    x and values 32-byte, 16-byte and element aligned: each row is its source's, bit for bit."""
+    rng = np.random.default_rng(11 + fmt)
+    T, rows, K = 130, 40001, 1056
+    x = dev(awkward_rows(rng, T, K)).to(dtype)
+    g = scale1(0.37)
+    one = torch.empty((T, K), dtype=dtype, device=DEV)
+    wc, wsc = B.fp4_quantize(x, fmt, tensor_scale=g, values=one)
+    pick = rng.integers(0, T, rows).astype(np.int32)
+    pick[::997] = T                                  # past the last row
+    at, there = dev(pick), dev(pick < T)
+    src = at.long().clamp_max(T - 1)
+    piece = 16 // x.element_size()
+    for off in (0, piece, 1):
+        big = torch.zeros((T, K + 2 * piece), dtype=dtype, device=DEV)
+        view = big[:, off:off + K]
+        view.copy_(x)
+        buf = torch.zeros(rows * K + 2 * piece, dtype=dtype, device=DEV)
+        v = buf[off if off != 1 else 0:][:rows * K].view(rows, K)
+        ws = status_ws()
+        c, sc = B.fp4_quantize(view, fmt, row_index=at, tensor_scale=g, values=v, workspace=ws)
+        assert B.read_status(ws) == B.MOE_ERR_DATA
+        assert torch.equal(c, wc[src] * there[:, None]) and torch.equal(sc, wsc[src] * there[:, None])
+        assert torch.equal(v[there], one[src][there]) and int(torch.count_nonzero(v[~there])) == 0
+        c, sc = B.fp4_quantize(view, fmt, row_index=at, tensor_scale=g)
+        assert torch.equal(c, wc[src] * there[:, None]) and torch.equal(sc, wsc[src] * there[:, None])
+
+
+@pytest.mark.parametrize("fmt", [MX, NV], ids=["mx", "nv"])
 def test_quantize_extremes_and_nonfinite(B, fmt):
     x = np.zeros((9, 64), np.float32)
     x[0] = np.finfo(np.float32).max
