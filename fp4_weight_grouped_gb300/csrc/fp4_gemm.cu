@@ -1030,7 +1030,9 @@ constexpr int kPairABytes = 128 * kStageBytesRow;
 constexpr int kPairBBytes = kPairN / 2 * kStageBytesRow;
 constexpr int kPairRing = kPairStages * (kPairABytes + kPairBBytes);
 constexpr int kPairStaging = kDepth * kGroup * (6 + 4) * 512;  // scale bytes on their way to tensor memory
-constexpr int kPairOffStaging = kPairRing;
+constexpr int kStoreBytes = 32 * 128;          // one epilogue warp's box of outputs: 32 rows of 128 bytes
+constexpr int kPairOffStore = kPairRing;
+constexpr int kPairOffStaging = kPairOffStore + 4 * kHalves * kStoreBytes;
 constexpr int kPairOffRow = kPairOffStaging + kPairStaging;
 constexpr int kPairOffItem = kPairOffRow + (kMaxE + 1) * 4;
 constexpr int kPairOffBars = (kPairOffItem + (kMaxE + 1) * 4 + 7) & ~7;
@@ -1168,6 +1170,52 @@ __device__ __forceinline__ void pair_store_plain(const Params &p, uint32_t acc, 
     }
 }
 
+// The same of 32 rows that are all there, by TMA: boxes of 128 bytes a row through this
+// warp's `box` (128-byte swizzle: a lane's 16-byte writes, a row a lane, are free of
+// bank conflicts).  Whole lines leave the SM in one request each; sectors stored by
+// lanes held up the loads (24,576 rows, N = 3,840, six bands, by lanes / by TMA, us:
+// MXFP4 bf16 K = 512 63.9 / 52.2, K = 2,048 91.7 / 87.1, K = 4,096 138 / 139; NVFP4 66.3 /
+// 53.8, 102 / 90, 158 / 146; MXFP4 f32 87.0 / 79.3, 110 / 107, 157 / 158).
+template <bool kBf16>
+__device__ __forceinline__ void pair_store_box(const CUtensorMap *map, uint32_t acc, int row0, int n0, int first,
+                                               int cols, float scale, uint8_t *box, uint32_t empty_bar) {
+    constexpr int kWidth = kBf16 ? 64 : 32;
+    const int lane = threadIdx.x & 31;
+    uint8_t *mine = box + lane * 128;
+    if (first * kWidth >= cols) release_acc_pair(empty_bar);
+    for (int c = first * kWidth; c < cols; c += kWidth * kHalves) {
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");   // the box was read
+        __syncwarp();
+#pragma unroll
+        for (int h = 0; h < kWidth; h += 32) {
+            uint32_t v[32];
+            tmem_ld32(acc + c + h, v);
+            tmem_ld_wait();
+            if (h + 32 == kWidth && c + kWidth * kHalves >= cols) release_acc_pair(empty_bar);
+            constexpr int kEach = kBf16 ? 8 : 4;                     // values of 16 bytes
+#pragma unroll
+            for (int i = 0; i < 32; i += kEach) {
+                uint32_t w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    w[k] = kBf16 ? bf16_pair(__uint_as_float(v[i + 2 * k]) * scale, __uint_as_float(v[i + 2 * k + 1]) * scale)
+                                 : __float_as_uint(__uint_as_float(v[i + k]) * scale);
+                const int chunk = (h + i) / kEach;
+                *reinterpret_cast<uint4 *>(mine + ((chunk ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+            asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                             reinterpret_cast<uint64_t>(map)),
+                         "r"(n0 + c), "r"(row0), "r"(smem_u32(box))
+                         : "memory");
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+    }
+}
+
 // SwiGLU of one warp: lane = token row; blocks of 32 h columns, from block `half` on.
 template <bool kNv>
 __device__ __forceinline__ void pair_store_swiglu(const Params &p, uint32_t acc, int row0, int valid, int n0,
@@ -1228,7 +1276,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a128,
                          const __grid_constant__ CUtensorMap tm_a64, const __grid_constant__ CUtensorMap tm_a32,
                          const __grid_constant__ CUtensorMap tm_ws, const __grid_constant__ CUtensorMap tm_as,
-                         const Params p, int out_vec) {
+                         const __grid_constant__ CUtensorMap tm_out, const Params p, int out_vec, int out_tma) {
     using C = ScaleCols<kNv>;
     constexpr int kTile = kSwiglu ? kPairN / 2 : kPairN;            // output columns of an item
     extern __shared__ uint8_t smem_raw[];
@@ -1437,6 +1485,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // other, the other way round for the next item.
         uint32_t buf = 0, phase = 0;
         int turn = 0;
+        uint8_t *box = smem + kPairOffStore + (warp - kEpilogueWarp) * kStoreBytes;
         for (int j = first; j < total; j += step) {
             const Item it = decode_item<kPairM, kTile>(j, roff, ioff, E, p.n_tiles);
             int row0, valid;
@@ -1448,13 +1497,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint32_t bar = cluster_addr(&acc_empty[buf], 0);
             if constexpr (kSwiglu)
                 pair_store_swiglu<kNv>(p, acc, row0 + quarter * 32, valid - quarter * 32, it.n0, half ^ turn, scale, h2, bar);
-            else
-                pair_store_plain(p, acc, row0 + quarter * 32, valid - quarter * 32, it.n0, half,
-                                 min(kPairN, (p.N - it.n0 + 31) & ~31), scale, out_vec, bar);
+            else {
+                const int row = row0 + quarter * 32, cols = min(kPairN, (p.N - it.n0 + 31) & ~31);
+                if (!out_tma || valid < quarter * 32 + 32)
+                    pair_store_plain(p, acc, row, valid - quarter * 32, it.n0, half, cols, scale, out_vec, bar);
+                else if (p.out_bf16)
+                    pair_store_box<true>(&tm_out, acc, row, it.n0, half ^ turn, cols, scale, box, bar);
+                else
+                    pair_store_box<false>(&tm_out, acc, row, it.n0, half, cols, scale, box, bar);
+            }
             buf ^= 1u;
             turn ^= 1;
             if (buf == 0) phase ^= 1u;
         }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
     // Neither CTA frees its tensor memory or leaves while the pair's MMAs, commits
     // or the peer's arrivals may still reach it.
@@ -1511,6 +1567,20 @@ bool encode_scales(CUtensorMap *map, const void *base, int scale_row, int64_t ro
     return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, outer ? 3 : 2, const_cast<void *>(base), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, nv ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Outputs [rows, N] in boxes of 128 bytes by 32 rows.
+bool encode_out(CUtensorMap *map, void *base, int64_t rows, int N, bool bf16) {
+    PFN_cuTensorMapEncodeTiled_v12000 encode = encode_fn();
+    if (!encode) return false;
+    const uint32_t size = bf16 ? 2 : 4;
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(rows)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(N) * size};
+    cuuint32_t box[2] = {128 / size, 32};
+    cuuint32_t estr[2] = {1, 1};
+    return encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, base, dims, strides,
+                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Shared-memory attribute of a kernel, set once per device (the mask is the
@@ -1601,7 +1671,11 @@ moe_status launch(const Fp4Gemm &g, cudaStream_t stream, int num_sms, int *launc
         p.band_lo = band;
         p.band_hi = INT32_MAX;
         const int out_vec = reinterpret_cast<uintptr_t>(g.out) % 32 == 0 && g.N % (g.out_bf16 ? 16 : 8) == 0;
-        kernel<<<num_sms & ~1, kThreads, kPairSmem, stream>>>(tm_w, tm_a128, tm_a64, tm_a2, tm_ws, tm_as, p, out_vec);
+        // TMA wants whole 16-byte pieces; smaller alignments store by threads.
+        const int out_tma = !kSwiglu && reinterpret_cast<uintptr_t>(g.out) % 16 == 0 && g.N % (g.out_bf16 ? 8 : 4) == 0;
+        CUtensorMap tm_out = tm_w;
+        if (out_tma && !encode_out(&tm_out, g.out, g.rows, g.N, g.out_bf16)) return MOE_ERR_CUDA;
+        kernel<<<num_sms & ~1, kThreads, kPairSmem, stream>>>(tm_w, tm_a128, tm_a64, tm_a2, tm_ws, tm_as, tm_out, p, out_vec, out_tma);
         if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
         ++*launches;
     }

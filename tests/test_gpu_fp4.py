@@ -309,6 +309,21 @@ def test_product_scale_alignment(B, fmt, offset):
     check_product(B, np.random.default_rng(offset), fmt, [30, 0, 70], 512, 140, offset=offset)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("N", [203, 204, 216])
+def test_product_output_alignment_of_long_bands(B, N, dtype):
+    """Rows and bases of every alignment give the same sums, and nothing outside the
+    output is written."""
+    rng = np.random.default_rng(N)
+    args, out = check_product(B, rng, MX, [300, 0, 40, 1000], 96, N, out_dtype=dtype)
+    for off in (1, 4, 8, 16):
+        flat = torch.full((out.numel() + 64,), 7.0, dtype=dtype, device=DEV)
+        got = flat[off:off + out.numel()].view(out.shape)
+        B.fp4_grouped_gemm(*args, out=got)
+        assert torch.equal(got, out)
+        assert bool((flat[:off] == 7.0).all()) and bool((flat[off + out.numel():] == 7.0).all())
+
+
 def test_product_wide_scale_range(B):
     check_product(B, np.random.default_rng(3), MX, [9, 50], 256, 128, wide=True)
 
