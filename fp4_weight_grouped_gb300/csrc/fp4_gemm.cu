@@ -583,6 +583,51 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&v)[8]) {
                  : "r"(taddr));
 }
 
+// Two f32 in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+// h = silu(g) u of two scaled pairs, silu(g) = g / (1 + 2^(-g log2 e)) with the hardware's
+// base-2 exponential and reciprocal (a few f32 ulps; h is rounded to 4 bits next).  Below
+// g = -88.7 the exponential is infinite and silu is -0, as f32 has it for this formula.
+template <bool kNv>
+__device__ __forceinline__ float2 gated2(uint32_t g0, uint32_t g1, uint32_t u0, uint32_t u1, float scale) {
+    float2 g = make_float2(__uint_as_float(g0), __uint_as_float(g1));
+    float2 u = make_float2(__uint_as_float(u0), __uint_as_float(u1));
+    if constexpr (kNv) {
+        g = mul2(g, make_float2(scale, scale));
+        u = mul2(u, make_float2(scale, scale));
+    }
+    const float2 x = mul2(g, make_float2(-1.4426950408889634f, -1.4426950408889634f));
+    float2 t, r;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(t.x) : "f"(x.x));
+    asm("ex2.approx.f32 %0, %1;" : "=f"(t.y) : "f"(x.y));
+    t = add2(t, make_float2(1.0f, 1.0f));
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r.x) : "f"(t.x));
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r.y) : "f"(t.y));
+    return mul2(mul2(g, r), u);
+}
+
+// max(m, |a|, |b|), NaN if one is.
+__device__ __forceinline__ float max_abs(float m, float a, float b) {
+    float d;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(m), "f"(a), "f"(b));
+    return d;
+}
+
 // The sums of a buffer are in registers: release it.
 __device__ __forceinline__ void release_acc(uint64_t *acc_empty) {
     tc_fence_before();
@@ -639,9 +684,12 @@ __device__ __forceinline__ void store_swiglu(const Params &p, const Item &it, ui
         float h[8];
         uint32_t m[8];
 #pragma unroll
-        for (int t = 0; t < 8; ++t) {
-            h[t] = silu_f32(__uint_as_float(g[t]) * scale) * (__uint_as_float(u[t]) * scale);
+        for (int t = 0; t < 8; t += 2) {
+            const float2 two = gated2<kNv>(g[t], g[t + 1], u[t], u[t + 1], scale);
+            h[t] = two.x;
+            h[t + 1] = two.y;
             m[t] = __float_as_uint(h[t]) & 0x7FFFFFFFu;
+            m[t + 1] = __float_as_uint(h[t + 1]) & 0x7FFFFFFFu;
         }
         uint8_t *out_scale = p.out_scales + static_cast<size_t>(it.row0 + c) * (p.I / (kNv ? 16 : 32));
         if constexpr (kNv) {
@@ -1232,8 +1280,11 @@ __device__ __forceinline__ void pair_store_swiglu(const Params &p, uint32_t acc,
             tmem_ld16(acc + kPairN / 2 + b + k, u);
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                h[k + i] = silu_f32(__uint_as_float(g[i]) * scale) * (__uint_as_float(u[i]) * scale);
+            for (int i = 0; i < 16; i += 2) {
+                const float2 two = gated2<kNv>(g[i], g[i + 1], u[i], u[i + 1], scale);
+                h[k + i] = two.x;
+                h[k + i + 1] = two.y;
+            }
         }
         if (b + 32 * kHalves >= kPairN / 2) release_acc_pair(empty_bar);
         if (n0 + b >= p.I || lane >= valid) continue;      // I is a multiple of 32
@@ -1242,9 +1293,10 @@ __device__ __forceinline__ void pair_store_swiglu(const Params &p, uint32_t acc,
         constexpr int kBlock = kNv ? 16 : 32;
 #pragma unroll
         for (int k = 0; k < 32; k += kBlock) {
-            uint32_t m = 0;
+            float most = 0.0f;
 #pragma unroll
-            for (int i = 0; i < kBlock; ++i) m = max(m, __float_as_uint(h[k + i]) & 0x7FFFFFFFu);
+            for (int i = 0; i < kBlock; i += 2) most = max_abs(most, h[k + i], h[k + i + 1]);
+            const uint32_t m = __float_as_uint(most);
             uint32_t byte;
             float inv;
             bool nan;
@@ -1261,8 +1313,12 @@ __device__ __forceinline__ void pair_store_swiglu(const Params &p, uint32_t acc,
             for (int i = 0; i < kBlock; i += 8) {
                 float q[8];
 #pragma unroll
-                for (int t = 0; t < 8; ++t) q[t] = nan ? 0.0f : h[k + i + t] * inv;
-                w[(k + i) / 8] = e2m1x8(q);
+                for (int t = 0; t < 8; t += 2) {
+                    const float2 two = mul2(make_float2(h[k + i + t], h[k + i + t + 1]), make_float2(inv, inv));
+                    q[t] = two.x;
+                    q[t + 1] = two.y;
+                }
+                w[(k + i) / 8] = nan ? 0u : e2m1x8(q);
             }
             p.out_scales[row * (p.I / kBlock) + (n0 + b + k) / kBlock] = static_cast<uint8_t>(byte);
         }
