@@ -756,7 +756,8 @@ __device__ __forceinline__ void clear_staging(uint8_t *staging, int bytes) {
 // are caught), and the widest chunk.  Rows count every band, items those of this
 // launch.  The experts go 32 to a warp, first for their totals, then for the offsets
 // on top of the totals before them (one warp over all of them took 2 us at 256
-// experts and 6 at 1,024).  False (recorded): the sizes do not add up.  `scratch`: 1 KB.
+// experts and 6 at 1,024).  False: no items, or (recorded) the sizes do not add up.
+// `scratch`: 1 KB.
 struct Totals {
     long long rows, items;
     int most, bad;
@@ -803,6 +804,7 @@ __device__ __forceinline__ bool build_items(const Params &p, int *roff, int *iof
         if (threadIdx.x == 0) set_status(p.status, MOE_ERR_DATA);
         return false;
     }
+    if (all_items == 0) return false;
     for (int c = warp; c < chunks; c += kThreads / 32) {
         const int e = c * 32 + lane, n = e < E ? __ldg(p.group_sizes + e) : 0;
         int unused;
@@ -832,6 +834,10 @@ __device__ __forceinline__ bool build_items(const Params &p, int *roff, int *iof
 
 // ------------------------------------------------------------------ kernel
 
+// The end of every CTA of a launch that may run beside the long bands' (see launch):
+// whoever waits for this launch then has waited for that one too.
+__device__ __forceinline__ void after_pairs() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // kShift: scale rows that are not whole 16-byte pieces (see copy_scales_shift); an
 // instantiation of its own, so that the others' registers do not pay for it.
 template <bool kNv, bool kSwiglu, bool kShift>
@@ -859,10 +865,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int E = p.E;
 
     if (tid == 0) *abort_flag = 0;
-    if (!build_items<S::NT>(p, roff, ioff, smem + kOffStaging, nt_slot)) return;
+    const bool any = build_items<S::NT>(p, roff, ioff, smem + kOffStaging, nt_slot);
     // redux: the compiler then knows the loops' bounds as warp-uniform
-    const int total = __reduce_max_sync(0xffffffffu, ioff[E]);
-    if (static_cast<int>(blockIdx.x) >= total) return;
+    const int total = any ? __reduce_max_sync(0xffffffffu, ioff[E]) : 0;
+    if (static_cast<int>(blockIdx.x) >= total) {
+        after_pairs();
+        return;
+    }
 
     if constexpr (!kShift) clear_staging(smem + kOffStaging, kOffRow - kOffStaging);
     // Stage layout: as many stages as fit with the widest chunk of this call.
@@ -1048,6 +1057,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     if (warp == kProducerWarp) tmem_dealloc(tmem, kTmemCols);
+    after_pairs();
 }
 
 // ------------------------------------------------- long bands: CTA pairs
@@ -1354,6 +1364,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t rank = cluster_rank();
     const int first = static_cast<int>(blockIdx.x >> 1), step = static_cast<int>(gridDim.x >> 1);
 
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (tid == 0) *abort_flag = 0;
     // Both CTAs read the same sizes, so both return here or neither does.
     if (!build_items<kPairM>(p, roff, ioff, smem + kPairOffStaging, nt_slot)) return;
@@ -1651,25 +1662,34 @@ bool set_smem(const void *kernel, int bytes, std::atomic<uint64_t> &mask) {
     return true;
 }
 
-// Bands of at least this many rows run in CTA pairs.  Both kernels at 24 bands of K =
-// 4096 (w13 with SwiGLU) and K = 2048 (w2, f32), MXFP4, one CTA / pair, us:
-//   rows            64          128         192         256         512        2048
-//   SwiGLU      41.9 / 48.4  52.3 / 50.2  59.2 / 50.5  71.8 / 51.2   125 / 82.7  419 / 282
-//   plain       28.7 / 31.3  33.1 / 34.3  38.4 / 37.6  46.5 / 41.0  73.4 / 64.5  247 / 216
-// (a chunk is 96 tokens with SwiGLU and 192 without, against 256 in a pair; NVFP4
-// crosses at the same sizes).
+// Bands of at least this many rows run in CTA pairs.  Calls of 24 bands at K = 4,096 (w13
+// with SwiGLU) and K = 2,048 (w2, f32), N = 4,096, one CTA / pair, us, the pairs' with 3 to 4
+// us for the other class's empty launch:
+//   rows a band           64         128         160         192         256         512        2,048
+//   MXFP4 SwiGLU  44.1 / 52.9 55.6 / 53.9 59.9 / 54.5 61.8 / 54.7 73.3 / 55.5 126 / 85.3 412 / 278
+//   MXFP4 plain   31.2 / 36.8 35.1 / 39.5 39.0 / 41.1 41.2 / 42.6 48.6 / 45.6 75.6 / 67.8 249 / 212
+//   NVFP4 SwiGLU  46.9 / 55.6 57.5 / 56.7 61.5 / 57.7 63.9 / 58.8 75.7 / 60.9 128 / 97.0 417 / 323
+//   NVFP4 plain   31.8 / 37.7 36.9 / 41.2 38.8 / 42.3 41.5 / 44.1 50.0 / 47.2 76.1 / 69.9 243 / 217
+// (a chunk is 96 tokens with SwiGLU and 192 without, against 256 in a pair).
 constexpr int kPairBandSwiglu = 112, kPairBand = 160;
-// A call of fewer rows than this many times that is one launch, without pairs: the
-// empty launch of the other class costs about 4 us, as much as pairs would gain.  (The
-// second as a programmatic dependent launch saved that, but its clusters then start
-// out of order: full layer w13 with SwiGLU 451 -> 490 us.)
-constexpr int kPairCall = 8;
+// Calls of fewer multiplications are one launch, without pairs: what pairs gain there is less
+// than the empty launch (MXFP4, bands x rows, one CTA / pair: SwiGLU 8 x 192 26.9 / 27.0, 8 x
+// 256 33.2 / 27.3, 4 x 512 31.2 / 26.9, 2 x 512 24.8 / 22.8; plain 8 x 256 20.8 / 22.7, 8 x
+// 512 33.1 / 32.9).
+constexpr double kPairMacsSwiglu = 3e10, kPairMacs = 4.5e10;
 
 template <bool kNv, bool kSwiglu, bool kShift>
 moe_status launch(const Fp4Gemm &g, cudaStream_t stream, int num_sms, int *launches) {
     constexpr int band = kSwiglu ? kPairBandSwiglu : kPairBand;
-    const bool pairs = g.rows >= (g.E == 1 ? band : kPairCall * band);
+    const double macs = static_cast<double>(g.rows) * g.N * g.K;
+    const int mode = gemm_pairing();
+    const bool pairs = mode != MOE_PAIRING_OFF && g.rows >= band &&
+                       (mode == MOE_PAIRING_ON || g.E == 1 || macs >= (kSwiglu ? kPairMacsSwiglu : kPairMacs));
     const bool singles = !pairs || g.E > 1;
+    // The pairs first, the short bands as a programmatic dependent launch: their CTAs take the
+    // SMs that the pairs leave (one launch after the other: Zipf prefill w13 407 us for 400,
+    // full layer w2 311 for 304).  The other way round, clusters start out of order as SMs
+    // come free one by one (full layer w13 with SwiGLU 451 -> 490 us).
     Params p;
     p.w_scales = g.w_scales;
     p.a_scales = g.a_scales;
@@ -1700,20 +1720,6 @@ moe_status launch(const Fp4Gemm &g, cudaStream_t stream, int num_sms, int *launc
                           encode_scales(&tm_as, g.a_scales, p.scale_row, g.rows, 0, a_box, kNv));
     };
     *launches = 0;
-    if (singles) {
-        static std::atomic<uint64_t> mask{0};
-        const auto kernel = fp4_gemm_kernel<kNv, kSwiglu, kShift>;
-        if (!set_smem(reinterpret_cast<const void *>(kernel), kSmemBytes, mask) ||
-            !encode_codes(&tm_w, g.w_codes, w_rows, g.K, kTileN) || !encode_codes(&tm_a2, g.a_codes, g.rows, g.K, 16) ||
-            !scale_maps(kTileN, 32))
-            return MOE_ERR_CUDA;
-        p.n_tiles = (columns + kTileN - 1) / kTileN;
-        p.band_lo = 1;
-        p.band_hi = pairs ? band - 1 : INT32_MAX;
-        kernel<<<num_sms, kThreads, kSmemBytes, stream>>>(tm_w, tm_a64, tm_a2, tm_ws, tm_as, p);
-        if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
-        ++*launches;
-    }
     if (pairs) {
         static std::atomic<uint64_t> mask{0};
         const auto kernel = fp4_gemm_pair_kernel<kNv, kSwiglu, kShift>;
@@ -1733,6 +1739,29 @@ moe_status launch(const Fp4Gemm &g, cudaStream_t stream, int num_sms, int *launc
         if (out_tma && !encode_out(&tm_out, g.out, g.rows, g.N, g.out_bf16)) return MOE_ERR_CUDA;
         kernel<<<num_sms & ~1, kThreads, kPairSmem, stream>>>(tm_w, tm_a128, tm_a64, tm_a2, tm_ws, tm_as, tm_out, p, out_vec, out_tma);
         if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
+        ++*launches;
+    }
+    if (singles) {
+        static std::atomic<uint64_t> mask{0};
+        const auto kernel = fp4_gemm_kernel<kNv, kSwiglu, kShift>;
+        if (!set_smem(reinterpret_cast<const void *>(kernel), kSmemBytes, mask) ||
+            !encode_codes(&tm_w, g.w_codes, w_rows, g.K, kTileN) || !encode_codes(&tm_a2, g.a_codes, g.rows, g.K, 16) ||
+            !scale_maps(kTileN, 32))
+            return MOE_ERR_CUDA;
+        p.n_tiles = (columns + kTileN - 1) / kTileN;
+        p.band_lo = 1;
+        p.band_hi = pairs ? band - 1 : INT32_MAX;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr.val.programmaticStreamSerializationAllowed = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(num_sms);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = kSmemBytes;
+        cfg.stream = stream;
+        cfg.attrs = &attr;
+        cfg.numAttrs = pairs ? 1 : 0;
+        if (cudaLaunchKernelEx(&cfg, kernel, tm_w, tm_a64, tm_a2, tm_ws, tm_as, p) != cudaSuccess) return MOE_ERR_CUDA;
         ++*launches;
     }
     return MOE_OK;

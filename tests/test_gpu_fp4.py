@@ -27,6 +27,15 @@ BLOCK = {0: 32, 1: 16}
 MX, NV = 0, 1
 
 
+@pytest.fixture(params=["auto", "on"])
+def pairing(B, request):
+    """Small calls run long bands in one launch with the short ones; "on" splits them as
+    large calls do."""
+    B.set_gemm_pairing(B.MOE_PAIRING_ON if request.param == "on" else B.MOE_PAIRING_AUTO)
+    yield
+    B.set_gemm_pairing(B.MOE_PAIRING_AUTO)
+
+
 @pytest.fixture(scope="module")
 def B():
     import __graft_entry__ as g
@@ -297,7 +306,7 @@ SIZES = [
 
 @pytest.mark.parametrize("fmt", [MX, NV], ids=["mx", "nv"])
 @pytest.mark.parametrize("sizes,K,N", SIZES, ids=[f"E{len(s)}_K{k}_N{n}" for s, k, n in SIZES])
-def test_product_matches_64_bits(B, fmt, sizes, K, N):
+def test_product_matches_64_bits(B, pairing, fmt, sizes, K, N):
     rng = np.random.default_rng(K + N + fmt)
     check_product(B, rng, fmt, sizes, K, N)
     check_product(B, rng, fmt, sizes, K, N, out_dtype=torch.bfloat16)
@@ -305,13 +314,13 @@ def test_product_matches_64_bits(B, fmt, sizes, K, N):
 
 @pytest.mark.parametrize("fmt", [MX, NV], ids=["mx", "nv"])
 @pytest.mark.parametrize("offset", [1, 4, 8])
-def test_product_scale_alignment(B, fmt, offset):
+def test_product_scale_alignment(B, pairing, fmt, offset):
     check_product(B, np.random.default_rng(offset), fmt, [30, 0, 70], 512, 140, offset=offset)
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
 @pytest.mark.parametrize("N", [203, 204, 216])
-def test_product_output_alignment_of_long_bands(B, N, dtype):
+def test_product_output_alignment_of_long_bands(B, pairing, N, dtype):
     """Rows and bases of every alignment give the same sums, and nothing outside the
     output is written."""
     rng = np.random.default_rng(N)
@@ -337,7 +346,7 @@ def test_product_many_experts_and_side_stream(B):
 
 
 @pytest.mark.parametrize("fmt", [MX, NV], ids=["mx", "nv"])
-def test_product_repeats_bit_for_bit(B, fmt):
+def test_product_repeats_bit_for_bit(B, pairing, fmt):
     rng = np.random.default_rng(8)
     args, out = check_product(B, rng, fmt, rng.integers(0, 300, 24).tolist(), 1024, 384)
     a2, w2 = scale1(0.75), None
@@ -349,7 +358,7 @@ def test_product_repeats_bit_for_bit(B, fmt):
 
 
 @pytest.mark.parametrize("fmt", [MX, NV], ids=["mx", "nv"])
-def test_long_bands_repeat_bit_for_bit(B, fmt):
+def test_long_bands_repeat_bit_for_bit(B, pairing, fmt):
     """Bands of every length class, forty times: a race in a ring shows as a difference."""
     rng = np.random.default_rng(18)
     sizes = rng.integers(0, 700, 12).tolist()
@@ -382,7 +391,7 @@ def test_product_no_rows_and_bad_sizes(B):
 
 @pytest.mark.parametrize("fmt,byte", [(MX, 255), (NV, 0x7F), (NV, 0xFF), (NV, 0x9A)])
 @pytest.mark.parametrize("side", ["act", "weight"])
-def test_product_reports_bad_scales(B, fmt, byte, side):
+def test_product_reports_bad_scales(B, pairing, fmt, byte, side):
     """Only the row (or column) of the bad scale may differ from a clean run."""
     rng = np.random.default_rng(10)
     wc, wsc = random_operand(rng, (2, 70), 160, fmt)
@@ -439,7 +448,7 @@ def swiglu_reference(a, w, I, s):
                                        ([33, 64], 1056, 416), ([2] * 30, 256, 256), ([96, 200], 4096, 64),
                                        ([112, 111, 5, 0, 700, 256], 352, 224), ([300, 0, 1000, 31], 2048, 96),
                                        ([129], 512, 32), ([600, 400], 96, 320)])
-def test_swiglu_product_quantises_h(B, fmt, sizes, K, I):
+def test_swiglu_product_quantises_h(B, pairing, fmt, sizes, K, I):
     rng = np.random.default_rng(K + I + fmt)
     E, rows, blk = len(sizes), sum(sizes), BLOCK[fmt]
     ac, asc = random_operand(rng, (rows,), K, fmt)
@@ -478,7 +487,7 @@ def quantise_byte(a, fmt, g):
     return nearest_e4m3(np.minimum(a / (6 * float(g)), 448).astype(np.float32))
 
 
-def test_swiglu_empty_and_nan(B):
+def test_swiglu_empty_and_nan(B, pairing):
     rng = np.random.default_rng(12)
     wc, wsc = random_operand(rng, (2, 128), 64, NV)
     ac, asc = random_operand(rng, (6,), 64, NV)
@@ -496,7 +505,7 @@ def test_swiglu_empty_and_nan(B):
 
 @pytest.mark.parametrize("fmt", [MX, NV], ids=["mx", "nv"])
 @pytest.mark.parametrize("T,k,E,H,I", [(1, 2, 4, 64, 32), (53, 3, 9, 288, 160)])
-def test_layer_equals_its_stages(B, fmt, T, k, E, H, I):
+def test_layer_equals_its_stages(B, pairing, fmt, T, k, E, H, I):
     rng = np.random.default_rng(T + fmt)
     x = torch.randn((T, H), device=DEV).to(torch.bfloat16)
     ids = dev(np.stack([rng.permutation(E)[:k] for _ in range(T)]).astype(np.int32))
