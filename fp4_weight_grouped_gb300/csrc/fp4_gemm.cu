@@ -8,9 +8,11 @@
 // block scaling, f32 accumulators), so there is no decode at all: the weights
 // go from global memory to shared memory by TMA and no thread touches them.
 //
-//  * Weights are the MMA's A operand (128 weight rows), the band's token rows
-//    its B operand (N = 16..192), as in the W4A16 product: a decode band of one
-//    row wastes no weight traffic.
+//  * Short bands (fp4_gemm_kernel): weights are the MMA's A operand (128 weight
+//    rows), the band's token rows its B operand (N = 16..192), as in the W4A16
+//    product: a decode band of one row wastes no weight traffic.  Long bands
+//    (fp4_gemm_pair_kernel) run in CTA pairs with tokens as A; see there, and
+//    launch() for which call takes which.
 //  * One K stage is 256 k: 128 bytes a row, the 128-byte swizzle TMA writes and
 //    the MMA reads; four MMAs of 64 k.
 //  * Block scales have to sit in tensor memory (word of row m at lane m % 32 of
@@ -21,6 +23,8 @@
 //    layout the rest of the library uses, and tokens may start at any row.  The
 //    other way, atoms in shared memory and tcgen05.cp, cost the tensor pipe about
 //    66 cycles a copy: 600 (MXFP4) to 1,000 (NVFP4) cycles a stage, for 384 of MMA.
+//    Two sets of four converter warps take the stages in turn; an arrival on the
+//    stage's own barrier, which the issuer waits for anyway, hands the scales over.
 //  * Accumulators are double-buffered (2 x 192 columns): the epilogue warps of
 //    one item run under the next item's MMAs.  A band's rows are cut into equal
 //    chunks of at most 192 (96 with SwiGLU) tokens, multiples of 16.
@@ -28,10 +32,18 @@
 //    MMAs into two column ranges, so a thread has g and u of one output column
 //    at the same token and no shuffle pairs them.  The 32 lanes of a warp hold
 //    32 consecutive h columns, one MX block: h is quantised in registers (block
-//    maximum by redux / half-warp redux, an 8 x 8 nibble transpose by three
-//    shuffles) and leaves the SM as 4-bit codes, never as bf16 or f32.
+//    maximum by redux, for NVFP4 by shuffles that halve the tokens, an 8 x 8 nibble
+//    transpose by three shuffles) and leaves the SM as 4-bit codes, never as bf16 or
+//    f32.  Sums, silu and the product are f32; the only rounding is that to 4 bits.
 //  * Persistent CTAs, one per SM, over a static list of (expert, chunk, tile).
 //  * Every wait is bounded; see wait_bounded.
+//
+// Bound: HBM for short bands, what TMA brings into an SM for long ones.  Measured, 256
+// experts, w13 K = 4,096, I = 2,048 and w2 K = 2,048, N = 4,096, of the bytes each has to
+// move at the measured copy rate: 64 tokens, top-6, w13 with SwiGLU MXFP4 276 us (100%),
+// NVFP4 295 (100%), w2 f32 150 (93%) and 157 (95%); 8,192 tokens (bands of 192 rows) w13
+// 441 us (81%) and 476 (80%), w2 304 (97%) and 312 (98%); bands of 8,192 rows, both
+// products 448 us, 5,520 TFLOP/s.
 #include <atomic>
 
 #include <cuda.h>
@@ -1074,6 +1086,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 // gate sums in columns 0..95 and the up sums in 96..191 (CTA 0 loads the gate rows,
 // CTA 1 the up rows).
 //
+// Measured, six bands of 4,096 rows, N = 3,840, MXFP4, bf16 out: K = 8,192 242 us (6,390
+// TFLOP/s), K = 2,048 87 us.  590 cycles a stage at 2,070 MHz; without the epilogue 550,
+// without the scales' conversion 557, without both 509: copies first, then what the
+// epilogue's and the converters' instructions take from one another.
+//
 // The even CTA issues.  Token scales sit in the CTA of their rows, weight scales in
 // both (each SM scales its own half of D).  The odd CTA's issuer warp relays: once
 // its CTA's copies and scale columns of a stage are there (it has waited for both on
@@ -1673,10 +1690,10 @@ bool set_smem(const void *kernel, int bytes, std::atomic<uint64_t> &mask) {
 // (a chunk is 96 tokens with SwiGLU and 192 without, against 256 in a pair).
 constexpr int kPairBandSwiglu = 112, kPairBand = 160;
 // Calls of fewer multiplications are one launch, without pairs: what pairs gain there is less
-// than the empty launch (MXFP4, bands x rows, one CTA / pair: SwiGLU 8 x 192 26.9 / 27.0, 8 x
-// 256 33.2 / 27.3, 4 x 512 31.2 / 26.9, 2 x 512 24.8 / 22.8; plain 8 x 256 20.8 / 22.7, 8 x
-// 512 33.1 / 32.9).
-constexpr double kPairMacsSwiglu = 3e10, kPairMacs = 4.5e10;
+// than the empty launch (MXFP4, bands x rows, one CTA / pair: SwiGLU 8 x 128 23.0 / 27.0, 8 x
+// 192 26.9 / 27.0, 8 x 256 33.2 / 27.3, 4 x 512 31.2 / 26.9; plain 8 x 256 20.8 / 22.7, 8 x
+// 512 33.1 / 32.9; 8 x 192 rows are 2.6e10 with SwiGLU and 1.3e10 without).
+constexpr double kPairMacsSwiglu = 2.5e10, kPairMacs = 4.5e10;
 
 template <bool kNv, bool kSwiglu, bool kShift>
 moe_status launch(const Fp4Gemm &g, cudaStream_t stream, int num_sms, int *launches) {

@@ -12,8 +12,11 @@
 //
 // One warp a token, the row in registers (expert lane + 32 i in register i), f32
 // throughout.  A selection step is one redux for the largest key and one for
-// the lowest expert that has it.  Bound: latency at decode sizes, HBM and issue
-// at thousands of tokens.
+// the lowest expert that has it.
+//
+// Bound: latency.  Measured, forward and gradient together: 64 tokens of 256 experts (f32,
+// k = 6) 5.3 us, the time of two launches; 8,192 tokens (bf16, renorm) 12.9 us for 12.9 MB:
+// every warp is resident at once, and the k selection steps are a chain of reductions.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>

@@ -464,6 +464,11 @@ MOE_API moe_status moe_layer_forward(const uint16_t *x, const int32_t *topk_ids,
  * loaded by each CTA; the even CTA issues M = 256 tensor-core MMAs over both.
  * Each SM thus loads half of every activation tile.  Results are identical
  * either way (same products, same accumulation order).
+ *
+ * The W4A4 products (moe_fp4_grouped_gemm and _swiglu) follow the mode too: their
+ * bands of 160 rows or more (112 with SwiGLU) run in CTA pairs, automatically in
+ * calls of one expert or of at least 4.5e10 (2.5e10) multiplications, with
+ * MOE_PAIRING_ON in every call.
  */
 typedef enum { MOE_PAIRING_AUTO = 0, MOE_PAIRING_OFF = 1, MOE_PAIRING_ON = 2 } moe_pairing;
 MOE_API moe_status moe_set_gemm_pairing(int32_t mode);
