@@ -224,6 +224,11 @@ struct Ring {
 
 // ---------------------------------------------------------- scale loaders
 
+// Staged bytes of a row that threads copy: the three 16-byte windows of two pieces (see
+// copy_scales_shift); of 32 rows (one q).  An odd number of 16-byte units keeps the copies
+// free of bank conflicts.
+constexpr int kShiftRow = 48, kShiftStep = 32 * kShiftRow, kShiftPieces = 2;
+
 // Scale bytes [at, at + 16) of R rows at any address into shared memory, zeros past a
 // row's end: the aligned words that hold the bytes, up to six rows' in flight
 // together, shifted into place.  A word that reaches outside the tensor
@@ -267,7 +272,7 @@ __device__ __forceinline__ void copy_unaligned(uint8_t *dst, const uint8_t *cons
                 o[i] = __funnelshift_r(w[q - q0][i], w[q - q0][i + 1], shift);
                 if (left < 4) o[i] = left <= 0 ? 0u : o[i] & ((1u << (8 * left)) - 1u);
             }
-            *reinterpret_cast<uint4 *>(dst + q * 1024) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4 *>(dst + q * kShiftStep) = make_uint4(o[0], o[1], o[2], o[3]);
         }
     }
 }
@@ -342,63 +347,78 @@ __device__ __forceinline__ void copy_scales(const ScaleEnv &v, const Staging &g,
     }
 }
 
-// Copier warp for rows that are not whole 16-byte pieces (one an operand).  Tensors
-// at 16-byte addresses: the two aligned 16-byte windows that hold a piece go into the
-// staging area as they are, 1,024 bytes from one q to the next, and the converters
-// shift.  Others are shifted here and take the first window.
-// P: pieces of a group.  row(item, q): row of this lane, clamped to the tile's or the
-// chunk's last row past its end (those sums are never stored, and every staged byte
-// is one of the tensor).  (Loads that
-// were shifted here, before their store, waited for memory once a piece: 8 us of a
-// 16 us call at K = 1,056.)
-template <int P, int R, int kMost, int kTile, class RowFn>
+// Copier warp for rows that are not whole 16-byte pieces (one an operand), two pieces a
+// group.  Tensors at 16-byte addresses: the three aligned 16-byte windows that hold the
+// pieces go into the staging area as they are, side by side, and the converters shift.
+// Others are shifted here.  row(item, q): row of this lane, clamped to the tile's or the
+// chunk's last row past its end (those sums are never stored, and every staged byte is one
+// of the tensor).
+//
+// One warp copies for the whole CTA, so its instructions count: row addresses are made once
+// an item, and only items whose windows reach past the tensor's end look at sizes.  (With
+// two windows a piece and sizes for each: K = 2,880, six bands of 4,096 rows, N = 3,840,
+// NVFP4 f32 384 us.  Loads shifted here, before their store, waited for memory once a piece:
+// 8 us of a 16 us call at K = 1,056.)
+template <int R, int kMost, int kTile, class RowFn>
 __device__ __forceinline__ void copy_scales_shift(const ScaleEnv &v, const Staging &g, int first_row,
                                                   const uint8_t *base, int64_t rows, bool windows, RowFn row) {
+    constexpr int P = kShiftPieces;
     const Params &p = *v.p;
     const int lane = threadIdx.x & 31;
-    const int pieces = (p.scale_row + 15) / 16;
+    const int pieces = (p.scale_row + 15) / 16, groups = (pieces + P - 1) / P;
     const int64_t bytes = rows * p.scale_row;
-    uint8_t *mine = g.bytes + first_row * 1024 + lane * 16;
+    uint8_t *mine = g.bytes + first_row * kShiftStep + lane * kShiftRow;
     Ring r;
     bool ok = true;
     for (int j = v.first; ok && j < v.total; j += v.step) {
         const Item it = decode_item<kMost, kTile>(j, v.roff, v.ioff, p.E, p.n_tiles);
-        for (int i = 0; i < pieces; i += P) {
+        const uint8_t *src[R];
+        bool inside = true;
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+            const int64_t at = row(it, q) * p.scale_row, first = windows ? at & ~int64_t(15) : at;
+            src[q] = base + first;
+            inside = inside && first + 16 * (P * groups + 1) <= bytes;
+        }
+        inside = __all_sync(0xffffffffu, inside);
+        for (int i = 0; i < groups; ++i) {
             ok = wait(&g.empty[r.slot], r.phase ^ 1u, v.abort_flag, p.status, p.wait_limit_ns);
             if (!ok) break;
-#pragma unroll 1
-            for (int k = 0; k < P && i + k < pieces; ++k) {
-                uint8_t *to = mine + r.slot * g.group_bytes + k * (g.group_bytes / P);
-                if (!windows) {
-                    const uint8_t *src[R];
-#pragma unroll
-                    for (int q = 0; q < R; ++q) src[q] = base + row(it, q) * p.scale_row;
-                    copy_unaligned<R>(to, src, (i + k) * 16, p.scale_row, base, base + bytes);
-                    continue;
-                }
-                const uint32_t dst = smem_u32(to);
-                const int n = min(16, p.scale_row - (i + k) * 16);
-#pragma unroll
-                for (int q = 0; q < R; ++q) {
-                    const int64_t at = row(it, q) * p.scale_row + (i + k) * 16, window = at & ~int64_t(15);
-                    // Bytes of the windows inside the tensor; the second where it is needed.
-                    const int first = static_cast<int>(min(bytes - window, int64_t(16)));
-                    const int second = (at & 15) + n > 16 ? static_cast<int>(min(bytes - window - 16, int64_t(16))) : 0;
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(dst + q * 1024), "l"(base + window),
-                                 "r"(first)
-                                 : "memory");
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(dst + q * 1024 + 512),
-                                 "l"(base + window + (second > 0 ? 16 : 0)), "r"(max(second, 0))
-                                 : "memory");
-                }
-            }
+            uint8_t *to = mine + r.slot * g.group_bytes;
             if (!windows) {
+#pragma unroll 1
+                for (int k = 0; k < P && i * P + k < pieces; ++k)
+                    copy_unaligned<R>(to + k * 16, src, (i * P + k) * 16, p.scale_row, base, base + bytes);
                 mbar_arrive(&g.full[r.slot]);
-                __syncwarp();
-                r.next(kDepth);
-                continue;
+            } else {
+                const uint32_t dst = smem_u32(to);
+                if (inside) {
+#pragma unroll
+                    for (int q = 0; q < R; ++q) {
+#pragma unroll
+                        for (int k = 0; k <= P; ++k)
+                            asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst + q * kShiftStep + k * 16),
+                                         "l"(src[q] + k * 16)
+                                         : "memory");
+                        src[q] += 16 * P;
+                    }
+                } else {
+#pragma unroll
+                    for (int q = 0; q < R; ++q) {
+#pragma unroll 1
+                        for (int k = 0; k <= P; ++k) {
+                            const int64_t left = bytes - (src[q] + k * 16 - base);     // zeros past the tensor
+                            asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                             dst + q * kShiftStep + k * 16),
+                                         "l"(left > 0 ? src[q] + k * 16 : base),
+                                         "r"(static_cast<int>(max(min(left, int64_t(16)), int64_t(0))))
+                                         : "memory");
+                        }
+                        src[q] += 16 * P;
+                    }
+                }
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(&g.full[r.slot])) : "memory");
             }
-            asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(&g.full[r.slot])) : "memory");
             __syncwarp();
             r.next(kDepth);
         }
@@ -406,25 +426,36 @@ __device__ __forceinline__ void copy_scales_shift(const ScaleEnv &v, const Stagi
     asm volatile("cp.async.wait_all;" ::: "memory");   // none in flight when the CTA leaves
 }
 
-// Scale words of rows staged by copy_scales_shift: row q's piece starts at byte (offs >>
-// 4 q) & 15 of its windows, the words wanted `skip` bytes into it; `n` bytes from there
-// on are the row's, the rest reads as zeros.
+// Where a row staged by copy_scales_shift starts: byte of the group, and the bits by which
+// its words are off the staged ones.
+template <int R>
+struct ShiftedRows {
+    uint32_t at[R], bits[R];
+};
+
+// Scale words of such rows; bits: some row's may not be 0.  `n` bytes from `group` on are
+// the row's, the rest reads as zeros.
 template <int R, int W>
-__device__ __forceinline__ void read_shifted(const uint8_t *piece, uint64_t offs, int skip, int n, uint32_t (&w)[R][W]) {
+__device__ __forceinline__ void read_shifted(const uint8_t *group, const ShiftedRows<R> &rows, bool bits, int n,
+                                             uint32_t (&w)[R][W]) {
 #pragma unroll
     for (int q = 0; q < R; ++q) {
-        const int b = (static_cast<int>(offs >> (4 * q)) & 15) + skip;
-        uint32_t raw[W + 1];
+        const uint32_t *from = reinterpret_cast<const uint32_t *>(group + rows.at[q]);
 #pragma unroll
-        for (int i = 0; i <= W; ++i) {
-            const int word = (b >> 2) + i;
-            raw[i] = *reinterpret_cast<const uint32_t *>(piece + q * 1024 + (word >> 2) * 512 + (word & 3) * 4);
+        for (int i = 0; i < W; ++i) w[q][i] = from[i];
+        if (bits) {
+            const uint32_t next = from[W];
+#pragma unroll
+            for (int i = 0; i < W; ++i) w[q][i] = __funnelshift_r(w[q][i], i + 1 < W ? w[q][i + 1] : next, rows.bits[q]);
         }
+    }
+    if (n < 4 * W) {
 #pragma unroll
         for (int i = 0; i < W; ++i) {
             const int left = n - 4 * i;
-            const uint32_t x = __funnelshift_r(raw[i], raw[i + 1], 8 * (b & 3));
-            w[q][i] = left >= 4 ? x : left <= 0 ? 0u : x & ((1u << (8 * left)) - 1u);
+            const uint32_t mask = left >= 4 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+#pragma unroll
+            for (int q = 0; q < R; ++q) w[q][i] &= mask;
         }
     }
 }
@@ -517,20 +548,30 @@ __device__ __forceinline__ void convert_scales(const ScaleEnv &v, const Staging 
     uint32_t bad = 0;
     bool ok = true;
     // By TMA: this lane's rows, whose 16-byte chunk c lies at c ^ swizzle.  Shifted: a
-    // piece is half a group, of two MXFP4 stages or one of NVFP4.
-    const uint8_t *mine = g.bytes + lane * (kShift ? 16 : GroupRow<kNv>::kBytes);
+    // group is two pieces, of two MXFP4 stages or one of NVFP4 each.
+    const uint8_t *mine = g.bytes + lane * (kShift ? kShiftRow : GroupRow<kNv>::kBytes);
+    const bool bits = windows && p.scale_row % 4 != 0;
     const int swizzle = kNv ? lane >> 1 & 3 : lane >> 2 & 1;
     Ring raw, r;                  // staged group, this set's next stage
     uint32_t sf = set;            // NVFP4: scale slot
     if (set) r.next(n_stages);
     for (int j = v.first; ok && j < v.total; j += v.step) {
-        uint64_t offs_a = 0, offs_b = 0;       // byte each row's pieces start at in their windows
-        if (kShift && windows) {
+        ShiftedRows<RA> rows_a;
+        ShiftedRows<RB> rows_b;
+        if constexpr (kShift) {
             const Item it = decode_item<kMost, kTile>(j, v.roff, v.ioff, p.E, p.n_tiles);
 #pragma unroll
-            for (int q = 0; q < RA; ++q) offs_a |= static_cast<uint64_t>(row_a(it, q) * p.scale_row & 15) << (4 * q);
+            for (int q = 0; q < RA; ++q) {
+                const uint32_t b = windows ? static_cast<uint32_t>(row_a(it, q) * p.scale_row) & 15u : 0u;
+                rows_a.at[q] = (first_a + q) * kShiftStep + (b & ~3u);
+                rows_a.bits[q] = 8 * (b & 3u);
+            }
 #pragma unroll
-            for (int q = 0; q < RB; ++q) offs_b |= static_cast<uint64_t>(row_b(it, q) * p.scale_row & 15) << (4 * q);
+            for (int q = 0; q < RB; ++q) {
+                const uint32_t b = windows ? static_cast<uint32_t>(row_b(it, q) * p.scale_row) & 15u : 0u;
+                rows_b.at[q] = (first_b + q) * kShiftStep + (b & ~3u);
+                rows_b.bits[q] = 8 * (b & 3u);
+            }
         }
         for (int k0 = 0; ok && k0 < k_stages; k0 += kStages) {
             ok = wait(&g.full[raw.slot], raw.phase, v.abort_flag, p.status, p.wait_limit_ns);
@@ -543,10 +584,10 @@ __device__ __forceinline__ void convert_scales(const ScaleEnv &v, const Staging 
                     uint32_t wa[RA][W], wb[RB][W];
                     const int i = (ks - k0) >> 1;
                     if constexpr (kShift) {
-                        const uint8_t *piece = group + (kNv ? set : i) * (g.group_bytes / 2);
-                        const int skip = kNv ? 0 : set * 8, n = p.scale_row - (ks + set) * 4 * W;
-                        read_shifted(piece + first_a * 1024, offs_a, skip, n, wa);
-                        read_shifted(piece + first_b * 1024, offs_b, skip, n, wb);
+                        const uint8_t *at = group + (2 * i + set) * 4 * W;
+                        const int n = p.scale_row - (ks + set) * 4 * W;
+                        read_shifted(at, rows_a, bits, n, wa);
+                        read_shifted(at, rows_b, bits, n, wb);
                     } else {
                         const uint8_t *at = group + (((kNv ? 2 * i + set : i) ^ swizzle) << 4) + (kNv ? 0 : set * 8);
                         read_words<kStep>(at + first_a * kStep, wa);
@@ -1013,7 +1054,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp < kEpilogueWarp) {
         const ScaleEnv v = {&p, roff, ioff, abort_flag, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), total};
         constexpr int RW = 4 * S::MT, RA = S::AR, kStep = GroupRow<kNv>::kStep;
-        const Staging g = {smem + kOffStaging, (RW + RA) * (kShift ? 2048u : kStep), raw_bars, raw_bars + kDepth};
+        const Staging g = {smem + kOffStaging, (RW + RA) * (kShift ? uint32_t(kShiftStep) : kStep), raw_bars, raw_bars + kDepth};
         const int cols = kSwiglu ? p.I : p.N;
         const int64_t w_rows = static_cast<int64_t>(E) * p.N;
         const auto w_row = [&](const Item &it, int q) {
@@ -1028,9 +1069,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                                w_row, a_row);
         } else if constexpr (kShift) {
             if (warp == kCopyWarp)
-                copy_scales_shift<2, RW, S::NT, kTileN>(v, g, 0, p.w_scales, w_rows, p.windows, w_row);
+                copy_scales_shift<RW, S::NT, kTileN>(v, g, 0, p.w_scales, w_rows, p.windows, w_row);
             else
-                copy_scales_shift<2, RA, S::NT, kTileN>(v, g, RW, p.a_scales, p.rows, p.windows, a_row);
+                copy_scales_shift<RA, S::NT, kTileN>(v, g, RW, p.a_scales, p.rows, p.windows, a_row);
         } else if (warp == kCopyWarp) {
             // 128-row boxes of weights, 32-row boxes of tokens.
             copy_scales<S::NT, kTileN>(
@@ -1517,7 +1558,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else if (warp < kEpilogueWarp) {
         const ScaleEnv v = {&p, roff, ioff, abort_flag, first, step, total};
         constexpr int RW = kPairN / 32, RA = 4, kStep = GroupRow<kNv>::kStep;
-        const Staging g = {smem + kPairOffStaging, (RW + RA) * (kShift ? 2048u : kStep), raw_bars, raw_bars + kDepth};
+        const Staging g = {smem + kPairOffStaging, (RW + RA) * (kShift ? uint32_t(kShiftStep) : kStep), raw_bars, raw_bars + kDepth};
         const int cols = kSwiglu ? p.I : p.N;
         const int64_t w_rows = static_cast<int64_t>(E) * p.N;
         // All 192 weight rows, in the order of the MMA's columns.
@@ -1536,9 +1577,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                                                a_row, w_row);
         } else if constexpr (kShift) {
             if (warp == kCopyWarp)
-                copy_scales_shift<2, RW, kPairM, kTile>(v, g, 0, p.w_scales, w_rows, p.windows, w_row);
+                copy_scales_shift<RW, kPairM, kTile>(v, g, 0, p.w_scales, w_rows, p.windows, w_row);
             else
-                copy_scales_shift<2, RA, kPairM, kTile>(v, g, RW, p.a_scales, p.rows, p.windows, a_row);
+                copy_scales_shift<RA, kPairM, kTile>(v, g, RW, p.a_scales, p.rows, p.windows, a_row);
         } else if (warp == kCopyWarp) {
             // Two 96-row boxes of weights (gate and up, or 192 rows), 64-row boxes of
             // this CTA's tokens.
