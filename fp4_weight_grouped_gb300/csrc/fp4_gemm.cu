@@ -82,7 +82,7 @@ constexpr int kOffStaging = kRingBytes;        // scale bytes on their way to te
 constexpr int kOffRow = kOffStaging + kDepth * kGroup * 11 * 512;
 constexpr int kOffItem = kOffRow + (kMaxE + 1) * 4;
 constexpr int kOffBars = (kOffItem + (kMaxE + 1) * 4 + 7) & ~7;
-constexpr int kNumBars = 2 * kMaxStages + 4 + 1 + 2 * kDepth;
+constexpr int kNumBars = 2 * kMaxStages + 4 + 1 + 2 * kDepth + 2 * kSets;
 constexpr int kOffMisc = kOffBars + kNumBars * 8;
 constexpr int kSmemBytes = kOffMisc + 64 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
@@ -299,6 +299,7 @@ struct Staging {
     uint8_t *bytes;
     uint32_t group_bytes;
     uint64_t *full, *empty;           // one a group: copiers -> converters -> copiers
+    uint64_t *sets;                   // two a converter set: its shifted words are there, were read
 };
 
 // Staged bytes of a row and group, and of 32 rows (one q).
@@ -426,36 +427,20 @@ __device__ __forceinline__ void copy_scales_shift(const ScaleEnv &v, const Stagi
     asm volatile("cp.async.wait_all;" ::: "memory");   // none in flight when the CTA leaves
 }
 
-// Where a row staged by copy_scales_shift starts: byte of the group, and the bits by which
-// its words are off the staged ones.
-template <int R>
-struct ShiftedRows {
-    uint32_t at[R], bits[R];
-};
-
-// Scale words of such rows; bits: some row's may not be 0.  `n` bytes from `group` on are
-// the row's, the rest reads as zeros.
-template <int R, int W>
-__device__ __forceinline__ void read_shifted(const uint8_t *group, const ShiftedRows<R> &rows, bool bits, int n,
-                                             uint32_t (&w)[R][W]) {
+// Scale words of one row staged by copy_scales_shift, `bits` bits after the staged word
+// `from`; `n` bytes of them are the row's, the rest reads as zeros.
+template <int W>
+__device__ __forceinline__ void read_shifted(const uint8_t *from, uint32_t bits, int n, uint32_t (&w)[W]) {
+    uint32_t raw[W + 1];
 #pragma unroll
-    for (int q = 0; q < R; ++q) {
-        const uint32_t *from = reinterpret_cast<const uint32_t *>(group + rows.at[q]);
+    for (int i = 0; i <= W; ++i) raw[i] = reinterpret_cast<const uint32_t *>(from)[i];
 #pragma unroll
-        for (int i = 0; i < W; ++i) w[q][i] = from[i];
-        if (bits) {
-            const uint32_t next = from[W];
-#pragma unroll
-            for (int i = 0; i < W; ++i) w[q][i] = __funnelshift_r(w[q][i], i + 1 < W ? w[q][i + 1] : next, rows.bits[q]);
-        }
-    }
+    for (int i = 0; i < W; ++i) w[i] = __funnelshift_r(raw[i], raw[i + 1], bits);
     if (n < 4 * W) {
 #pragma unroll
         for (int i = 0; i < W; ++i) {
             const int left = n - 4 * i;
-            const uint32_t mask = left >= 4 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
-#pragma unroll
-            for (int q = 0; q < R; ++q) w[q][i] &= mask;
+            w[i] &= left >= 4 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
         }
     }
 }
@@ -489,6 +474,12 @@ __device__ __forceinline__ void read_words(const uint8_t *at, uint32_t (&w)[R][W
     }
 }
 
+template <int W>
+__device__ __forceinline__ void put_words(uint8_t *at, const uint32_t (&w)[W]) {
+    if constexpr (W == 2) *reinterpret_cast<uint2 *>(at) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint4 *>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // bad_bits of words kQuarter, kQuarter + 4, ... of both operands'.
 template <bool kNv, int kQuarter, int RA, int RB, int W>
 __device__ __forceinline__ uint32_t bad_quarter(const uint32_t (&a)[RA][W], const uint32_t (&b)[RB][W]) {
@@ -518,6 +509,7 @@ __device__ __forceinline__ void init_scale_bars(uint64_t *raw_bars, uint32_t cop
         mbar_init(&raw_bars[d], copiers);             // by TMA: 1; by threads: the two warps' lanes
         mbar_init(&raw_bars[kDepth + d], 4 * kSets);  // the converter warps
     }
+    for (int i = 0; i < 2 * kSets; ++i) mbar_init(&raw_bars[2 * kDepth + i], 4);   // a set's warps
 }
 
 // Converter warp: staged bytes of both operands -> scale columns in tensor memory, of
@@ -548,29 +540,29 @@ __device__ __forceinline__ void convert_scales(const ScaleEnv &v, const Staging 
     uint32_t bad = 0;
     bool ok = true;
     // By TMA: this lane's rows, whose 16-byte chunk c lies at c ^ swizzle.  Shifted: a
-    // group is two pieces, of two MXFP4 stages or one of NVFP4 each.
+    // group is two pieces, of two MXFP4 stages or one of NVFP4 each.  The warps of a set
+    // then shift a quarter of the rows each into `words` (all four shifting all rows spent
+    // twice the shared-memory cycles: K = 2,880, NVFP4, 24 bands of 16 rows 70 us).
     const uint8_t *mine = g.bytes + lane * (kShift ? kShiftRow : GroupRow<kNv>::kBytes);
-    const bool bits = windows && p.scale_row % 4 != 0;
     const int swizzle = kNv ? lane >> 1 & 3 : lane >> 2 & 1;
+    constexpr int RT = RA + RB, kShare = (RT + 3) / 4, kWordStep = 32 * 4 * W;
+    uint8_t *words = g.bytes + kDepth * g.group_bytes + set * RT * kWordStep + lane * 4 * W;
+    uint64_t *ready = g.sets + 2 * set, *taken = ready + 1;
+    uint32_t turn = 0;
     Ring raw, r;                  // staged group, this set's next stage
     uint32_t sf = set;            // NVFP4: scale slot
     if (set) r.next(n_stages);
     for (int j = v.first; ok && j < v.total; j += v.step) {
-        ShiftedRows<RA> rows_a;
-        ShiftedRows<RB> rows_b;
+        uint32_t from[kShare], bits[kShare];   // this warp's rows quarter, quarter + 4, ...
         if constexpr (kShift) {
             const Item it = decode_item<kMost, kTile>(j, v.roff, v.ioff, p.E, p.n_tiles);
 #pragma unroll
-            for (int q = 0; q < RA; ++q) {
-                const uint32_t b = windows ? static_cast<uint32_t>(row_a(it, q) * p.scale_row) & 15u : 0u;
-                rows_a.at[q] = (first_a + q) * kShiftStep + (b & ~3u);
-                rows_a.bits[q] = 8 * (b & 3u);
-            }
-#pragma unroll
-            for (int q = 0; q < RB; ++q) {
-                const uint32_t b = windows ? static_cast<uint32_t>(row_b(it, q) * p.scale_row) & 15u : 0u;
-                rows_b.at[q] = (first_b + q) * kShiftStep + (b & ~3u);
-                rows_b.bits[q] = 8 * (b & 3u);
+            for (int t = 0; t < kShare; ++t) {
+                const int q = min(quarter + 4 * t, RT - 1);
+                const int64_t row = q < RA ? row_a(it, q) : row_b(it, q - RA);
+                const uint32_t b = windows ? static_cast<uint32_t>(row * p.scale_row) & 15u : 0u;
+                from[t] = (q < RA ? first_a + q : first_b + q - RA) * kShiftStep + (b & ~3u);
+                bits[t] = 8 * (b & 3u);
             }
         }
         for (int k0 = 0; ok && k0 < k_stages; k0 += kStages) {
@@ -586,15 +578,34 @@ __device__ __forceinline__ void convert_scales(const ScaleEnv &v, const Staging 
                     if constexpr (kShift) {
                         const uint8_t *at = group + (2 * i + set) * 4 * W;
                         const int n = p.scale_row - (ks + set) * 4 * W;
-                        read_shifted(at, rows_a, bits, n, wa);
-                        read_shifted(at, rows_b, bits, n, wb);
+                        ok = wait(taken, (turn & 1u) ^ 1u, v.abort_flag, p.status, p.wait_limit_ns);
+                        if (!ok) break;
+#pragma unroll
+                        for (int t = 0; t < kShare; ++t) {
+                            if (quarter + 4 * t >= RT) break;
+                            uint32_t w[W];
+                            read_shifted(at + from[t], bits[t], n, w);
+#pragma unroll
+                            for (int i = 0; i < W; ++i) bad |= bad_bits<kNv>(w[i]);
+                            put_words(words + (quarter + 4 * t) * kWordStep, w);
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(ready);
+                        ok = wait(ready, turn & 1u, v.abort_flag, p.status, p.wait_limit_ns);
+                        if (!ok) break;
+                        read_words<kWordStep>(words, wa);
+                        read_words<kWordStep>(words + RA * kWordStep, wb);
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(taken);
+                        ++turn;
                     } else {
                         const uint8_t *at = group + (((kNv ? 2 * i + set : i) ^ swizzle) << 4) + (kNv ? 0 : set * 8);
                         read_words<kStep>(at + first_a * kStep, wa);
                         read_words<kStep>(at + first_b * kStep, wb);
                     }
-                    // The four warps hold the same words; each checks a quarter.
-                    if (quarter == 0) bad |= bad_quarter<kNv, 0>(wa, wb);
+                    // The four warps hold the same words; each checks a quarter (shifted: did).
+                    if constexpr (kShift) {
+                    } else if (quarter == 0) bad |= bad_quarter<kNv, 0>(wa, wb);
                     else if (quarter == 1) bad |= bad_quarter<kNv, 1>(wa, wb);
                     else if (quarter == 2) bad |= bad_quarter<kNv, 2>(wa, wb);
                     else bad |= bad_quarter<kNv, 3>(wa, wb);
@@ -1054,7 +1065,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp < kEpilogueWarp) {
         const ScaleEnv v = {&p, roff, ioff, abort_flag, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), total};
         constexpr int RW = 4 * S::MT, RA = S::AR, kStep = GroupRow<kNv>::kStep;
-        const Staging g = {smem + kOffStaging, (RW + RA) * (kShift ? uint32_t(kShiftStep) : kStep), raw_bars, raw_bars + kDepth};
+        const Staging g = {smem + kOffStaging, (RW + RA) * (kShift ? uint32_t(kShiftStep) : kStep), raw_bars, raw_bars + kDepth, raw_bars + 2 * kDepth};
         const int cols = kSwiglu ? p.I : p.N;
         const int64_t w_rows = static_cast<int64_t>(E) * p.N;
         const auto w_row = [&](const Item &it, int q) {
@@ -1152,7 +1163,7 @@ constexpr int kPairOffStaging = kPairOffStore + 4 * kHalves * kStoreBytes;
 constexpr int kPairOffRow = kPairOffStaging + kPairStaging;
 constexpr int kPairOffItem = kPairOffRow + (kMaxE + 1) * 4;
 constexpr int kPairOffBars = (kPairOffItem + (kMaxE + 1) * 4 + 7) & ~7;
-constexpr int kPairOffMisc = kPairOffBars + (2 * kPairStages + 4 + 1 + 2 * kDepth) * 8;
+constexpr int kPairOffMisc = kPairOffBars + (2 * kPairStages + 4 + 1 + 2 * kDepth + 2 * kSets) * 8;
 constexpr int kPairSmem = kPairOffMisc + 64 + 1024;
 static_assert(kPairSmem <= 232448, "shared memory budget (pairs)");
 
@@ -1558,7 +1569,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else if (warp < kEpilogueWarp) {
         const ScaleEnv v = {&p, roff, ioff, abort_flag, first, step, total};
         constexpr int RW = kPairN / 32, RA = 4, kStep = GroupRow<kNv>::kStep;
-        const Staging g = {smem + kPairOffStaging, (RW + RA) * (kShift ? uint32_t(kShiftStep) : kStep), raw_bars, raw_bars + kDepth};
+        const Staging g = {smem + kPairOffStaging, (RW + RA) * (kShift ? uint32_t(kShiftStep) : kStep), raw_bars, raw_bars + kDepth, raw_bars + 2 * kDepth};
         const int cols = kSwiglu ? p.I : p.N;
         const int64_t w_rows = static_cast<int64_t>(E) * p.N;
         // All 192 weight rows, in the order of the MMA's columns.
