@@ -353,16 +353,17 @@ __device__ __forceinline__ void copy_scales(const ScaleEnv &v, const Staging &g,
 // pieces go into the staging area as they are, side by side, and the converters shift.
 // Others are shifted here.  row(item, q): row of this lane, clamped to the tile's or the
 // chunk's last row past its end (those sums are never stored, and every staged byte is one
-// of the tensor).
+// of the tensor).  used(item): how many q have rows at all.
 //
 // One warp copies for the whole CTA, so its instructions count: row addresses are made once
 // an item, and only items whose windows reach past the tensor's end look at sizes.  (With
 // two windows a piece and sizes for each: K = 2,880, six bands of 4,096 rows, N = 3,840,
 // NVFP4 f32 384 us.  Loads shifted here, before their store, waited for memory once a piece:
 // 8 us of a 16 us call at K = 1,056.)
-template <int R, int kMost, int kTile, class RowFn>
+template <int R, int kMost, int kTile, class RowFn, class UsedFn>
 __device__ __forceinline__ void copy_scales_shift(const ScaleEnv &v, const Staging &g, int first_row,
-                                                  const uint8_t *base, int64_t rows, bool windows, RowFn row) {
+                                                  const uint8_t *base, int64_t rows, bool windows, RowFn row,
+                                                  UsedFn used) {
     constexpr int P = kShiftPieces;
     const Params &p = *v.p;
     const int lane = threadIdx.x & 31;
@@ -374,6 +375,7 @@ __device__ __forceinline__ void copy_scales_shift(const ScaleEnv &v, const Stagi
     for (int j = v.first; ok && j < v.total; j += v.step) {
         const Item it = decode_item<kMost, kTile>(j, v.roff, v.ioff, p.E, p.n_tiles);
         const uint8_t *src[R];
+        const int n_used = used(it);
         bool inside = true;
 #pragma unroll
         for (int q = 0; q < R; ++q) {
@@ -396,6 +398,7 @@ __device__ __forceinline__ void copy_scales_shift(const ScaleEnv &v, const Stagi
                 if (inside) {
 #pragma unroll
                     for (int q = 0; q < R; ++q) {
+                        if (q >= n_used) break;
 #pragma unroll
                         for (int k = 0; k <= P; ++k)
                             asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst + q * kShiftStep + k * 16),
@@ -406,6 +409,7 @@ __device__ __forceinline__ void copy_scales_shift(const ScaleEnv &v, const Stagi
                 } else {
 #pragma unroll
                     for (int q = 0; q < R; ++q) {
+                        if (q >= n_used) break;
 #pragma unroll 1
                         for (int k = 0; k <= P; ++k) {
                             const int64_t left = bytes - (src[q] + k * 16 - base);     // zeros past the tensor
@@ -523,10 +527,10 @@ __device__ __forceinline__ void init_scale_bars(uint64_t *raw_bars, uint32_t cop
 // cycles for two stages and bound the kernel.
 //
 // A: the MMA's A operand (kByTile), B: its B operand; their first rows in the group.
-template <bool kNv, bool kShift, int RA, int RB, int kMost, int kTile, class RowA, class RowB>
+template <bool kNv, bool kShift, int RA, int RB, int kMost, int kTile, class RowA, class RowB, class UsedA, class UsedB>
 __device__ __forceinline__ void convert_scales(const ScaleEnv &v, const Staging &g, int first_a, int first_b,
                                                uint32_t sf_tmem, uint64_t *full, uint64_t *empty, uint32_t n_stages,
-                                               bool windows, RowA row_a, RowB row_b) {
+                                               bool windows, RowA row_a, RowB row_b, UsedA used_a, UsedB used_b) {
     using C = ScaleCols<kNv>;
     constexpr int W = C::W, kACols = 4 * ((RA + 3) / 4) * W;
     constexpr int kStages = kShift && kNv ? 2 : kGroup;       // of a group
@@ -554,6 +558,7 @@ __device__ __forceinline__ void convert_scales(const ScaleEnv &v, const Staging 
     if (set) r.next(n_stages);
     for (int j = v.first; ok && j < v.total; j += v.step) {
         uint32_t from[kShare], bits[kShare];   // this warp's rows quarter, quarter + 4, ...
+        bool has[kShare];
         if constexpr (kShift) {
             const Item it = decode_item<kMost, kTile>(j, v.roff, v.ioff, p.E, p.n_tiles);
 #pragma unroll
@@ -563,6 +568,7 @@ __device__ __forceinline__ void convert_scales(const ScaleEnv &v, const Staging 
                 const uint32_t b = windows ? static_cast<uint32_t>(row * p.scale_row) & 15u : 0u;
                 from[t] = (q < RA ? first_a + q : first_b + q - RA) * kShiftStep + (b & ~3u);
                 bits[t] = 8 * (b & 3u);
+                has[t] = quarter + 4 * t < RT && (q < RA ? q < used_a(it) : q - RA < used_b(it));
             }
         }
         for (int k0 = 0; ok && k0 < k_stages; k0 += kStages) {
@@ -582,7 +588,7 @@ __device__ __forceinline__ void convert_scales(const ScaleEnv &v, const Staging 
                         if (!ok) break;
 #pragma unroll
                         for (int t = 0; t < kShare; ++t) {
-                            if (quarter + 4 * t >= RT) break;
+                            if (!has[t]) continue;
                             uint32_t w[W];
                             read_shifted(at + from[t], bits[t], n, w);
 #pragma unroll
@@ -1074,15 +1080,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         const auto a_row = [&](const Item &it, int q) {
             return static_cast<int64_t>(it.row0 + min(lane + 32 * q, it.nvalid - 1));
         };
+        const auto w_used = [](const Item &) { return RW; };
+        const auto a_used = [](const Item &it) { return (it.nvalid + 31) / 32; };
         const uint32_t sf_tmem = tmem + kSfCol0 + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         if (warp >= kConvertWarp) {
             convert_scales<kNv, kShift, RW, RA, S::NT, kTileN>(v, g, 0, RW, sf_tmem, full, empty, n_stages, p.windows,
-                                                               w_row, a_row);
+                                                               w_row, a_row, w_used, a_used);
         } else if constexpr (kShift) {
             if (warp == kCopyWarp)
-                copy_scales_shift<RW, S::NT, kTileN>(v, g, 0, p.w_scales, w_rows, p.windows, w_row);
+                copy_scales_shift<RW, S::NT, kTileN>(v, g, 0, p.w_scales, w_rows, p.windows, w_row, w_used);
             else
-                copy_scales_shift<RA, S::NT, kTileN>(v, g, RW, p.a_scales, p.rows, p.windows, a_row);
+                copy_scales_shift<RA, S::NT, kTileN>(v, g, RW, p.a_scales, p.rows, p.windows, a_row, a_used);
         } else if (warp == kCopyWarp) {
             // 128-row boxes of weights, 32-row boxes of tokens.
             copy_scales<S::NT, kTileN>(
@@ -1582,15 +1590,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             pair_rows(it, rank, &row0, &valid);
             return static_cast<int64_t>(min(row0 + min(lane + 32 * q, max(valid - 1, 0)), p.rows - 1));
         };
+        const auto w_used = [](const Item &) { return RW; };
+        // Long bands nearly always use all; leaving some out cost 7% (NVFP4, 4,096 rows).
+        const auto a_used = [](const Item &) { return RA; };
         const uint32_t sf_tmem = tmem + kSfCol0 + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         if (warp >= kConvertWarp) {
             convert_scales<kNv, kShift, RA, RW, kPairM, kTile>(v, g, RW, 0, sf_tmem, full, empty, n_stages, p.windows,
-                                                               a_row, w_row);
+                                                               a_row, w_row, a_used, w_used);
         } else if constexpr (kShift) {
             if (warp == kCopyWarp)
-                copy_scales_shift<RW, kPairM, kTile>(v, g, 0, p.w_scales, w_rows, p.windows, w_row);
+                copy_scales_shift<RW, kPairM, kTile>(v, g, 0, p.w_scales, w_rows, p.windows, w_row, w_used);
             else
-                copy_scales_shift<RA, kPairM, kTile>(v, g, RW, p.a_scales, p.rows, p.windows, a_row);
+                copy_scales_shift<RA, kPairM, kTile>(v, g, RW, p.a_scales, p.rows, p.windows, a_row, a_used);
         } else if (warp == kCopyWarp) {
             // Two 96-row boxes of weights (gate and up, or 192 rows), 64-row boxes of
             // this CTA's tokens.
