@@ -401,7 +401,8 @@ __device__ __forceinline__ void copy_scales_shift(const ScaleEnv &v, const Stagi
                         if (q >= n_used) break;
 #pragma unroll
                         for (int k = 0; k <= P; ++k)
-                            asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst + q * kShiftStep + k * 16),
+                            asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(
+                                             dst + q * kShiftStep + k * 16),
                                          "l"(src[q] + k * 16)
                                          : "memory");
                         src[q] += 16 * P;
@@ -422,7 +423,8 @@ __device__ __forceinline__ void copy_scales_shift(const ScaleEnv &v, const Stagi
                         src[q] += 16 * P;
                     }
                 }
-                asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(&g.full[r.slot])) : "memory");
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(&g.full[r.slot]))
+                             : "memory");
             }
             __syncwarp();
             r.next(kDepth);
@@ -1069,9 +1071,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         wait(final_bar, 0, nullptr, p.status, lim);
     } else if (warp < kEpilogueWarp) {
-        const ScaleEnv v = {&p, roff, ioff, abort_flag, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), total};
+        const ScaleEnv v = {&p,    roff, ioff, abort_flag, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x),
+                            total};
         constexpr int RW = 4 * S::MT, RA = S::AR, kStep = GroupRow<kNv>::kStep;
-        const Staging g = {smem + kOffStaging, (RW + RA) * (kShift ? uint32_t(kShiftStep) : kStep), raw_bars, raw_bars + kDepth, raw_bars + 2 * kDepth};
+        const Staging g = {smem + kOffStaging, (RW + RA) * (kShift ? uint32_t(kShiftStep) : kStep), raw_bars,
+                           raw_bars + kDepth, raw_bars + 2 * kDepth};
         const int cols = kSwiglu ? p.I : p.N;
         const int64_t w_rows = static_cast<int64_t>(E) * p.N;
         const auto w_row = [&](const Item &it, int q) {
@@ -1098,7 +1102,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 [&](const Item &it, int i, uint32_t dst, uint64_t *bar) {
                     const int x = i * GroupRow<kNv>::kBytes;
 #pragma unroll
-                    for (int m = 0; m < S::MT; ++m) tma_load_3d(dst + 4 * m * kStep, &tm_ws, x, it.n0, it.e * S::MT + m, bar);
+                    for (int m = 0; m < S::MT; ++m)
+                        tma_load_3d(dst + 4 * m * kStep, &tm_ws, x, it.n0, it.e * S::MT + m, bar);
                     for (int q = 0; 32 * q < it.nvalid; ++q)
                         tma_load_2d(dst + (RW + q) * kStep, &tm_as, x, it.row0 + 32 * q, bar);
                 },
@@ -1266,7 +1271,8 @@ __device__ __forceinline__ void pair_store_plain(const Params &p, uint32_t acc, 
                     uint32_t w[8];
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        w[k] = bf16_pair(__uint_as_float(v[i + 2 * k]) * scale, __uint_as_float(v[i + 2 * k + 1]) * scale);
+                        w[k] = bf16_pair(__uint_as_float(v[i + 2 * k]) * scale,
+                                         __uint_as_float(v[i + 2 * k + 1]) * scale);
                     if (i < left) store_sector(o + i, w);
                 }
             }
@@ -1333,7 +1339,8 @@ __device__ __forceinline__ void pair_store_box(const CUtensorMap *map, uint32_t 
                 uint32_t w[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    w[k] = kBf16 ? bf16_pair(__uint_as_float(v[i + 2 * k]) * scale, __uint_as_float(v[i + 2 * k + 1]) * scale)
+                    w[k] = kBf16 ? bf16_pair(__uint_as_float(v[i + 2 * k]) * scale,
+                                             __uint_as_float(v[i + 2 * k + 1]) * scale)
                                  : __float_as_uint(__uint_as_float(v[i + k]) * scale);
                 const int chunk = (h + i) / kEach;
                 *reinterpret_cast<uint4 *>(mine + ((chunk ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -1426,7 +1433,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     int *roff = reinterpret_cast<int *>(smem + kPairOffRow);
     int *ioff = reinterpret_cast<int *>(smem + kPairOffItem);
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kPairOffBars);   // TMA, scale converters (and relay) -> issuer (relay)
+    // TMA, scale converters (and relay) -> issuer (relay)
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kPairOffBars);
     uint64_t *empty = full + kPairStages;                                 // pair commit -> TMA, converters of both
     uint64_t *acc_full = empty + kPairStages;                             // pair commit -> epilogues of both
     uint64_t *acc_empty = acc_full + 2;                                   // epilogues of both -> issuer
@@ -1577,7 +1585,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else if (warp < kEpilogueWarp) {
         const ScaleEnv v = {&p, roff, ioff, abort_flag, first, step, total};
         constexpr int RW = kPairN / 32, RA = 4, kStep = GroupRow<kNv>::kStep;
-        const Staging g = {smem + kPairOffStaging, (RW + RA) * (kShift ? uint32_t(kShiftStep) : kStep), raw_bars, raw_bars + kDepth, raw_bars + 2 * kDepth};
+        const Staging g = {smem + kPairOffStaging, (RW + RA) * (kShift ? uint32_t(kShiftStep) : kStep), raw_bars,
+                           raw_bars + kDepth, raw_bars + 2 * kDepth};
         const int cols = kSwiglu ? p.I : p.N;
         const int64_t w_rows = static_cast<int64_t>(E) * p.N;
         // All 192 weight rows, in the order of the MMA's columns.
@@ -1643,7 +1652,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const float scale = kNv ? __ldg(p.w_scale_2 + it.e) * a2 : 1.0f;
             const uint32_t bar = cluster_addr(&acc_empty[buf], 0);
             if constexpr (kSwiglu)
-                pair_store_swiglu<kNv>(p, acc, row0 + quarter * 32, valid - quarter * 32, it.n0, half ^ turn, scale, h2, bar);
+                pair_store_swiglu<kNv>(p, acc, row0 + quarter * 32, valid - quarter * 32, it.n0, half ^ turn, scale,
+                                       h2, bar);
             else {
                 const int row = row0 + quarter * 32, cols = min(kPairN, (p.N - it.n0 + 31) & ~31);
                 if (!out_tma || valid < quarter * 32 + 32)
@@ -1725,8 +1735,8 @@ bool encode_out(CUtensorMap *map, void *base, int64_t rows, int N, bool bf16) {
     cuuint64_t strides[1] = {static_cast<cuuint64_t>(N) * size};
     cuuint32_t box[2] = {128 / size, 32};
     cuuint32_t estr[2] = {1, 1};
-    return encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, base, dims, strides,
-                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+    return encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, base, dims,
+                  strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1795,8 +1805,8 @@ moe_status launch(const Fp4Gemm &g, cudaStream_t stream, int num_sms, int *launc
     if (!encode_codes(&tm_a64, g.a_codes, g.rows, g.K, 64)) return MOE_ERR_CUDA;
     tm_ws = tm_as = tm_a64;         // not used where threads copy the scales
     const auto scale_maps = [&](uint32_t w_box, uint32_t a_box) {
-        return kShift || (encode_scales(&tm_ws, g.w_scales, p.scale_row, columns, static_cast<int64_t>(g.E) * (kSwiglu ? 2 : 1),
-                                        w_box, kNv) &&
+        return kShift || (encode_scales(&tm_ws, g.w_scales, p.scale_row, columns,
+                                        static_cast<int64_t>(g.E) * (kSwiglu ? 2 : 1), w_box, kNv) &&
                           encode_scales(&tm_as, g.a_scales, p.scale_row, g.rows, 0, a_box, kNv));
     };
     *launches = 0;
@@ -1817,7 +1827,8 @@ moe_status launch(const Fp4Gemm &g, cudaStream_t stream, int num_sms, int *launc
         const int out_tma = !kSwiglu && reinterpret_cast<uintptr_t>(g.out) % 16 == 0 && g.N % (g.out_bf16 ? 8 : 4) == 0;
         CUtensorMap tm_out = tm_w;
         if (out_tma && !encode_out(&tm_out, g.out, g.rows, g.N, g.out_bf16)) return MOE_ERR_CUDA;
-        kernel<<<num_sms & ~1, kThreads, kPairSmem, stream>>>(tm_w, tm_a128, tm_a64, tm_a2, tm_ws, tm_as, tm_out, p, out_vec, out_tma);
+        kernel<<<num_sms & ~1, kThreads, kPairSmem, stream>>>(tm_w, tm_a128, tm_a64, tm_a2, tm_ws, tm_as, tm_out, p,
+                                                              out_vec, out_tma);
         if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
         ++*launches;
     }

@@ -139,8 +139,8 @@ __device__ __noinline__ void zero_row(int k_first, int k_end, uint8_t *to, uint8
 // branches by lane.  kValues: `values` is there.
 template <typename T, bool kNv, typename V, bool kValues>
 __global__ void __launch_bounds__(kThreads)
-    quantize_kernel(const T *x, int64_t x_rows, int64_t x_stride, int x_align, int K, int span, const int32_t *row_index,
-                    int index_div, int64_t rows, const float *tensor_scale, uint8_t *codes, uint8_t *scales,
+    quantize_kernel(const T *x, int64_t x_rows, int64_t x_stride, int x_align, int K, int span,
+                    const int32_t *row_index, int index_div, int64_t rows, const float *tensor_scale, uint8_t *codes, uint8_t *scales,
                     V *values, int values_wide, int *status) {
     const int lane = threadIdx.x & 31;
     const int tasks = (K + 512 * span - 1) / (512 * span);      // a row
@@ -243,8 +243,8 @@ void start(const Fp4Quant &q, V *values, cudaStream_t stream, int num_sms) {
     const int x_align = x_at % 32 == 0 ? 32 : x_at % 16 == 0 ? 16 : 0;
     const int wide = reinterpret_cast<uintptr_t>(values) % 32 == 0;   // K % 32 = 0: every row then
     quant::quantize_kernel<T, kNv, V, kValues><<<static_cast<int>(blocks), quant::kThreads, 0, stream>>>(
-        x, q.x_rows, q.x_stride, x_align, q.K, span, q.row_index, q.index_div, q.rows, q.tensor_scale, q.codes, q.scales,
-        values, wide, q.status);
+        x, q.x_rows, q.x_stride, x_align, q.K, span, q.row_index, q.index_div, q.rows, q.tensor_scale, q.codes,
+        q.scales, values, wide, q.status);
 }
 
 template <typename T, bool kNv>

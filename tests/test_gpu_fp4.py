@@ -372,6 +372,47 @@ def test_long_bands_repeat_bit_for_bit(B, pairing, fmt):
             assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("fmt", [MX, NV], ids=["mx", "nv"])
+@pytest.mark.parametrize("K", [96, 1056, 2048])
+def test_cta_pairs_and_graphs_give_the_same_bits(B, pairing, fmt, K):
+    """Bands of every length in CTA pairs or not, and replayed from a CUDA graph (whose
+    reader must wait for both launches), on outputs that are cleared before each replay."""
+    rng = np.random.default_rng(K)
+    sizes = [700, 3, 0, 161, 250, 31, 112, 1000]
+    E, N, rows = len(sizes), 448, sum(sizes)
+    ac, asc = random_operand(rng, (rows,), K, fmt)
+    wc, wsc = random_operand(rng, (E, N), K, fmt)
+    args = (dev(ac), dev(asc), dev(wc), dev(wsc), dev(np.array(sizes, np.int32)), fmt)
+    kw = dict(act_scale_2=scale1(0.5), weight_scale_2=torch.ones(E, device=DEV), workspace=status_ws())
+    h2 = scale1(0.02)
+    out = torch.empty((rows, N), device=DEV)
+    h = (torch.empty((rows, N // 4), dtype=torch.uint8, device=DEV),
+         torch.empty((rows, N // 2 // BLOCK[fmt]), dtype=torch.uint8, device=DEV))
+    sums = torch.empty((), dtype=torch.float64, device=DEV)
+
+    def run():
+        out.zero_()
+        B.fp4_grouped_gemm(*args, out=out, **kw)
+        sums.copy_(out.double().sum())
+        h[0].zero_()
+        B.fp4_grouped_gemm_swiglu(*args, h_scale_2=h2, out=h, **kw)
+
+    run()
+    want = [t.clone() for t in (out, sums, *h)]
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        run()
+    for _ in range(20):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, (out, sums, *h)))
+    B.set_gemm_pairing(B.MOE_PAIRING_OFF)
+    run()
+    assert all(torch.equal(a, b) for a, b in zip(want, (out, sums, *h)))
+
+
 def test_product_no_rows_and_bad_sizes(B):
     rng = np.random.default_rng(9)
     wc, wsc = random_operand(rng, (3, 64), 64, MX)
