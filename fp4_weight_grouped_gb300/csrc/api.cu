@@ -653,8 +653,8 @@ moe_status moe_layer_forward_fp4(
                                 nullptr, 0, static_cast<uint8_t *>(workspace) + kStatusBytes,
                                 status_word(workspace), s, &launches);
     if (st == MOE_OK && rows > 0) {
-        moe::Fp4Quant q = {x, 1, T, hidden, hidden, sorted_slot, k, rows, nv, x_scale_2, x_codes, x_scales,
-                           nullptr, 0, status_word(workspace)};
+        moe::Fp4Quant q = {x, 1, T, hidden, hidden, nullptr, 1, T, nv, x_scale_2, x_codes, x_scales,
+                           nullptr, 0, status_word(workspace), slot_to_row, k, rows};
         moe::Fp4Gemm g13 = fp4_gemm(x_codes, x_scales, x_scale_2, rows, hidden, w13_codes, w13_scales, w13_scale_2,
                                     group_sizes, E, 2 * inter, workspace);
         g13.out = h_codes;

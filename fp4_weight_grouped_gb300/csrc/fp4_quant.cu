@@ -8,7 +8,7 @@
 //
 // Bound: HBM writes where values are asked for, instruction issue where not.  Measured,
 // 49,152 rows of 4,096 bf16 gathered from 8,192 tokens: MXFP4 codes alone 64 us, NVFP4
-// 70 us (three quarters of all issue slots, 2.7 TB/s); with bf16 values 120 us (578 MB;
+// 70 us (three quarters of all issue slots, 2.7 TB/s; see kScatter for the layer's way); with bf16 values 120 us (578 MB;
 // filling as many bytes as it writes takes 112 us); without the gather 83 us (6.1 TB/s).
 // 3,001 rows of 2,080 f32 to NVFP4 with values: 9.4 us.
 #include <cuda_bf16.h>
@@ -137,11 +137,15 @@ __device__ __noinline__ void zero_row(int k_first, int k_end, uint8_t *to, uint8
 // issued before the one in front of it is worked on.  Lanes past the row's end work on
 // its last block again and store what its own lanes store, so nothing in the loop
 // branches by lane.  kValues: `values` is there.
-template <typename T, bool kNv, typename V, bool kValues>
+//
+// kScatter: the rows are tokens, and codes and scales go to the k rows of each token's
+// slots, so that a token is loaded and quantised once, not k times (a whole W4A4 layer of
+// 8,192 tokens, top-6: MXFP4 963 -> 937 us, NVFP4 1,010 -> 979 us).
+template <typename T, bool kNv, typename V, bool kValues, bool kScatter>
 __global__ void __launch_bounds__(kThreads)
     quantize_kernel(const T *x, int64_t x_rows, int64_t x_stride, int x_align, int K, int span,
                     const int32_t *row_index, int index_div, int64_t rows, const float *tensor_scale, uint8_t *codes, uint8_t *scales,
-                    V *values, int values_wide, int *status) {
+                    V *values, int values_wide, int *status, const int32_t *slot_to_row, int k, int64_t out_rows) {
     const int lane = threadIdx.x & 31;
     const int tasks = (K + 512 * span - 1) / (512 * span);      // a row
     const int64_t total = rows * tasks;
@@ -204,6 +208,18 @@ __global__ void __launch_bounds__(kThreads)
                 for (int e = 0; e < 8; ++e) q[e] = v[8 * h + e];
                 w[h] = byte == (kNv ? 0x7Fu : 255u) ? 0u : e2m1x8(q);
             }
+            if constexpr (kScatter) {
+#pragma unroll 4
+                for (int j = 0; j < k; ++j) {
+                    const int32_t d = __ldg(slot_to_row + r * k + j);
+                    if (d < 0 || d >= out_rows) continue;       // a slot without a row
+                    *reinterpret_cast<uint2 *>(codes + static_cast<int64_t>(d) * (K / 2) + at / 2) = make_uint2(w[0], w[1]);
+                    if (kNv || (lane & 1) == 0)
+                        scales[static_cast<int64_t>(d) * (K / (kNv ? 16 : 32)) + at / (kNv ? 16 : 32)] =
+                            static_cast<uint8_t>(byte);
+                }
+                continue;
+            }
             *reinterpret_cast<uint2 *>(to + at / 2) = make_uint2(w[0], w[1]);
             if (kNv || (lane & 1) == 0) to_scale[at / (kNv ? 16 : 32)] = static_cast<uint8_t>(byte);
             if constexpr (kValues) {
@@ -227,7 +243,7 @@ __global__ void __launch_bounds__(kThreads)
 
 namespace {
 
-template <typename T, bool kNv, typename V, bool kValues>
+template <typename T, bool kNv, typename V, bool kValues, bool kScatter>
 void start(const Fp4Quant &q, V *values, cudaStream_t stream, int num_sms) {
     // Whole rows a warp where there are two rows a warp that fits the SM, else segments.
     // 24 blocks an SM: 4 or 5 are resident, and the rest go to whichever is done first (the
@@ -242,19 +258,21 @@ void start(const Fp4Quant &q, V *values, cudaStream_t stream, int num_sms) {
     const uintptr_t x_at = reinterpret_cast<uintptr_t>(x) | static_cast<uintptr_t>(q.x_stride * sizeof(T));
     const int x_align = x_at % 32 == 0 ? 32 : x_at % 16 == 0 ? 16 : 0;
     const int wide = reinterpret_cast<uintptr_t>(values) % 32 == 0;   // K % 32 = 0: every row then
-    quant::quantize_kernel<T, kNv, V, kValues><<<static_cast<int>(blocks), quant::kThreads, 0, stream>>>(
+    quant::quantize_kernel<T, kNv, V, kValues, kScatter><<<static_cast<int>(blocks), quant::kThreads, 0, stream>>>(
         x, q.x_rows, q.x_stride, x_align, q.K, span, q.row_index, q.index_div, q.rows, q.tensor_scale, q.codes,
-        q.scales, values, wide, q.status);
+        q.scales, values, wide, q.status, q.slot_to_row, q.k, q.out_rows);
 }
 
 template <typename T, bool kNv>
 void start_values(const Fp4Quant &q, cudaStream_t stream, int num_sms) {
-    if (!q.values)
-        start<T, kNv, float, false>(q, nullptr, stream, num_sms);
+    if (q.slot_to_row)
+        start<T, kNv, float, false, true>(q, nullptr, stream, num_sms);
+    else if (!q.values)
+        start<T, kNv, float, false, false>(q, nullptr, stream, num_sms);
     else if (q.values_bf16)
-        start<T, kNv, __nv_bfloat16, true>(q, static_cast<__nv_bfloat16 *>(q.values), stream, num_sms);
+        start<T, kNv, __nv_bfloat16, true, false>(q, static_cast<__nv_bfloat16 *>(q.values), stream, num_sms);
     else
-        start<T, kNv, float, true>(q, static_cast<float *>(q.values), stream, num_sms);
+        start<T, kNv, float, true, false>(q, static_cast<float *>(q.values), stream, num_sms);
 }
 
 }  // namespace

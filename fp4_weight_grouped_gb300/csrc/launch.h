@@ -127,6 +127,10 @@ struct Fp4Quant {
     void *values;
     int values_bf16;
     int *status;
+    // Instead of row_index: row r (a token) goes to rows slot_to_row[r k + j] < out_rows, j < k.
+    const int32_t *slot_to_row;
+    int k;
+    int64_t out_rows;
 };
 moe_status launch_fp4_quantize(const Fp4Quant &q, cudaStream_t stream, int num_sms);
 

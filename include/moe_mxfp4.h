@@ -669,8 +669,8 @@ MOE_API moe_status moe_fp4_grouped_gemm_swiglu(const uint8_t *act_codes, const u
 
 /*
  * moe_layer_forward_fp4 — moe_layer_forward with 4-bit activations: route sort ->
- * moe_fp4_quantize (gathering) -> moe_fp4_grouped_gemm_swiglu ->
- * moe_fp4_grouped_gemm -> moe_combine, all on `stream`.
+ * quantisation as moe_fp4_quantize (a token once, stored to its k rows) ->
+ * moe_fp4_grouped_gemm_swiglu -> moe_fp4_grouped_gemm -> moe_combine, all on `stream`.
  *
  *  x_scale_2, h_scale_2, w13_scale_2, w2_scale_2   tensor scales (MOE_FP4_NV).
  *  Caller-owned intermediates: x_codes [T*k, hidden/2], x_scales, h_codes [T*k,

@@ -545,7 +545,7 @@ def test_swiglu_empty_and_nan(B, pairing):
 
 
 @pytest.mark.parametrize("fmt", [MX, NV], ids=["mx", "nv"])
-@pytest.mark.parametrize("T,k,E,H,I", [(1, 2, 4, 64, 32), (53, 3, 9, 288, 160)])
+@pytest.mark.parametrize("T,k,E,H,I", [(1, 2, 4, 64, 32), (53, 3, 9, 288, 160), (20011, 2, 5, 1056, 32)])
 def test_layer_equals_its_stages(B, pairing, fmt, T, k, E, H, I):
     rng = np.random.default_rng(T + fmt)
     x = torch.randn((T, H), device=DEV).to(torch.bfloat16)
