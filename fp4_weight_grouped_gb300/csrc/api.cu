@@ -475,6 +475,7 @@ moe_status moe_layer_forward(const uint16_t *x, const int32_t *topk_ids, const f
 moe_status moe_set_gemm_pairing(int32_t mode) {
     if (mode < MOE_PAIRING_AUTO || mode > MOE_PAIRING_ON) return MOE_ERR_INVALID_ARG;
     moe::set_gemm_pairing(mode);
+    moe::set_fp4_pairing(mode);
     return MOE_OK;
 }
 

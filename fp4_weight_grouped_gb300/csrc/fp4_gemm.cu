@@ -1768,11 +1768,13 @@ constexpr int kPairBandSwiglu = 112, kPairBand = 160;
 // 512 33.1 / 32.9; 8 x 192 rows are 2.6e10 with SwiGLU and 1.3e10 without).
 constexpr double kPairMacsSwiglu = 2.5e10, kPairMacs = 4.5e10;
 
+std::atomic<int> g_pairing{MOE_PAIRING_AUTO};      // process-wide
+
 template <bool kNv, bool kSwiglu, bool kShift>
 moe_status launch(const Fp4Gemm &g, cudaStream_t stream, int num_sms, int *launches) {
     constexpr int band = kSwiglu ? kPairBandSwiglu : kPairBand;
     const double macs = static_cast<double>(g.rows) * g.N * g.K;
-    const int mode = gemm_pairing();
+    const int mode = g_pairing.load(std::memory_order_relaxed);
     const bool pairs = mode != MOE_PAIRING_OFF && g.rows >= band &&
                        (mode == MOE_PAIRING_ON || g.E == 1 || macs >= (kSwiglu ? kPairMacsSwiglu : kPairMacs));
     const bool singles = !pairs || g.E > 1;
@@ -1859,6 +1861,8 @@ moe_status launch(const Fp4Gemm &g, cudaStream_t stream, int num_sms, int *launc
 }
 
 }  // namespace fp4
+
+void set_fp4_pairing(int mode) { fp4::g_pairing.store(mode, std::memory_order_relaxed); }
 
 moe_status launch_fp4_gemm(const Fp4Gemm &g, bool nv, bool swiglu, cudaStream_t stream, int num_sms, int *launches) {
     *launches = 0;

@@ -1434,7 +1434,6 @@ __global__ void bounded_wait_kernel(uint64_t limit_ns, int *status) {
 static std::atomic<int> g_pair_mode{0};
 
 void set_gemm_pairing(int mode) { g_pair_mode.store(mode, std::memory_order_relaxed); }
-int gemm_pairing() { return g_pair_mode.load(std::memory_order_relaxed); }
 
 // Clusters of two that the device can keep resident at once with the pair
 // kernel's shared memory (looked up once per device and weight format).

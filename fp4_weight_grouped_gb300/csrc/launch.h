@@ -72,7 +72,7 @@ moe_status launch_grouped_gemm_nvfp4(const uint16_t *act, int rows, int K, const
 // CTA-pair use for bands over 32 rows: 0 automatic, 1 never, 2 whenever the
 // shape allows (process-wide).
 void set_gemm_pairing(int mode);
-int gemm_pairing();
+void set_fp4_pairing(int mode);   // the W4A4 products' copy of it
 
 moe_status launch_decode_expert(const uint8_t *codes, const uint8_t *scales, int N, int K, int e,
                                 uint16_t *out, int *status, cudaStream_t stream);
