@@ -727,9 +727,17 @@ def layer_forward_fp4(x, topk_ids, topk_w, w13, w2, buffers: LayerBuffersFp4, x_
     _need("w13 scales", s13, (E, 2 * inter, hidden // block), torch.uint8)
     _need("w2 codes", c2, (E, hidden, inter // 2), torch.uint8)
     _need("w2 scales", s2, (E, hidden, inter // block), torch.uint8)
-    _need("buffers.x_codes", b.x_codes, (T * k, hidden // 2), torch.uint8)
-    _need("buffers.h_codes", b.h_codes, (T * k, inter // 2), torch.uint8)
+    rows = T * k
+    _need("buffers.x_codes", b.x_codes, (rows, hidden // 2), torch.uint8)
+    _need("buffers.x_scales", b.x_scales, (rows, hidden // block), torch.uint8)
+    _need("buffers.h_codes", b.h_codes, (rows, inter // 2), torch.uint8)
+    _need("buffers.h_scales", b.h_scales, (rows, inter // block), torch.uint8)
+    _need("buffers.y2", b.y2, (rows, hidden), torch.float32)
+    _need("buffers.out", b.out, (T, hidden), torch.float32)
     _need("buffers.group_sizes", b.group_sizes, (E,), torch.int32)
+    _need("buffers.group_offsets", b.group_offsets, (E + 1,), torch.int32)
+    _need("buffers.sorted_slot", b.sorted_slot, (rows,), torch.int32)
+    _need("buffers.slot_to_row", b.slot_to_row, (rows,), torch.int32)
     rc = load().moe_layer_forward_fp4(
         _ptr(x), _ptr(topk_ids), _ptr(topk_w), T, k, E, hidden, inter, fmt, _ptr(c13), _ptr(s13),
         _tensor_scale("w13 weight_scale_2", g13, E, fmt), _ptr(c2), _ptr(s2),
