@@ -486,6 +486,11 @@ def _need(name: str, t: torch.Tensor, shape, *dtypes):
     raise ValueError(f"{name}: not a CUDA tensor")
 
 
+def _at_least(name: str, t: torch.Tensor, shape, dtype):
+    """_need for a buffer that may have more rows than the call uses."""
+    _need(name, t, (max(t.shape[0], shape[0]) if t.dim() else 0, *shape[1:]), dtype)
+
+
 def _rows_of(name: str, t: torch.Tensor) -> int:
     """Row stride, in elements, of a 2-D tensor whose rows are contiguous."""
     if t.dim() != 2 or t.dtype not in (torch.float32, torch.bfloat16):
@@ -690,7 +695,8 @@ def gather_backward(dx_sorted: torch.Tensor, slot_to_row: torch.Tensor, k: int,
 
 
 class LayerBuffersFp4:
-    """Caller-owned intermediates of one 4-bit layer pass (allocated once, reused)."""
+    """Caller-owned intermediates of one 4-bit layer pass (allocated once, reused by every
+    call of at most T tokens and T * k rows)."""
 
     def __init__(self, T: int, k: int, E: int, hidden: int, inter: int, fmt: int, device="cuda"):
         rows, block = T * k, _fp4_block(fmt)
@@ -713,7 +719,8 @@ class LayerBuffersFp4:
 def layer_forward_fp4(x, topk_ids, topk_w, w13, w2, buffers: LayerBuffersFp4, x_scale_2=None,
                       h_scale_2=None, stream=None):
     """The routed-expert layer with 4-bit activations and weights.  w13 and w2 are (codes,
-    scales, weight_scale_2 or None); x bf16 [T, hidden]; -> buffers.out f32 [T, hidden]."""
+    scales, weight_scale_2 or None); x bf16 [T, hidden]; -> the first T rows of buffers.out, f32
+    [T, hidden]."""
     b, fmt = buffers, buffers.fmt
     block = _fp4_block(fmt)
     (c13, s13, g13), (c2, s2, g2) = w13, w2
@@ -728,16 +735,16 @@ def layer_forward_fp4(x, topk_ids, topk_w, w13, w2, buffers: LayerBuffersFp4, x_
     _need("w2 codes", c2, (E, hidden, inter // 2), torch.uint8)
     _need("w2 scales", s2, (E, hidden, inter // block), torch.uint8)
     rows = T * k
-    _need("buffers.x_codes", b.x_codes, (rows, hidden // 2), torch.uint8)
-    _need("buffers.x_scales", b.x_scales, (rows, hidden // block), torch.uint8)
-    _need("buffers.h_codes", b.h_codes, (rows, inter // 2), torch.uint8)
-    _need("buffers.h_scales", b.h_scales, (rows, inter // block), torch.uint8)
-    _need("buffers.y2", b.y2, (rows, hidden), torch.float32)
-    _need("buffers.out", b.out, (T, hidden), torch.float32)
-    _need("buffers.group_sizes", b.group_sizes, (E,), torch.int32)
-    _need("buffers.group_offsets", b.group_offsets, (E + 1,), torch.int32)
-    _need("buffers.sorted_slot", b.sorted_slot, (rows,), torch.int32)
-    _need("buffers.slot_to_row", b.slot_to_row, (rows,), torch.int32)
+    _at_least("buffers.x_codes", b.x_codes, (rows, hidden // 2), torch.uint8)
+    _at_least("buffers.x_scales", b.x_scales, (rows, hidden // block), torch.uint8)
+    _at_least("buffers.h_codes", b.h_codes, (rows, inter // 2), torch.uint8)
+    _at_least("buffers.h_scales", b.h_scales, (rows, inter // block), torch.uint8)
+    _at_least("buffers.y2", b.y2, (rows, hidden), torch.float32)
+    _at_least("buffers.out", b.out, (T, hidden), torch.float32)
+    _at_least("buffers.group_sizes", b.group_sizes, (E,), torch.int32)
+    _at_least("buffers.group_offsets", b.group_offsets, (E + 1,), torch.int32)
+    _at_least("buffers.sorted_slot", b.sorted_slot, (rows,), torch.int32)
+    _at_least("buffers.slot_to_row", b.slot_to_row, (rows,), torch.int32)
     rc = load().moe_layer_forward_fp4(
         _ptr(x), _ptr(topk_ids), _ptr(topk_w), T, k, E, hidden, inter, fmt, _ptr(c13), _ptr(s13),
         _tensor_scale("w13 weight_scale_2", g13, E, fmt), _ptr(c2), _ptr(s2),
@@ -747,7 +754,7 @@ def layer_forward_fp4(x, topk_ids, topk_w, w13, w2, buffers: LayerBuffersFp4, x_
         _ptr(b.x_scales), _ptr(b.h_codes), _ptr(b.h_scales), _ptr(b.y2), _ptr(b.workspace),
         b.workspace.numel(), _stream(stream))
     _check(rc, "moe_layer_forward_fp4")
-    return b.out
+    return b.out if b.out.shape[0] == T else b.out[:T]
 
 
 def debug_bounded_wait(limit_ns: int, workspace: torch.Tensor, stream=None):

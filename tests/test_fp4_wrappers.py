@@ -81,3 +81,18 @@ def test_layer_refuses_a_wrong_buffer(lib, name, fmt):
         with pytest.raises(ValueError, match=name):
             forward(layer(4, 2, fmt=fmt), b)
     assert "moe_layer_forward_fp4" not in lib.calls
+
+
+@pytest.mark.parametrize("fmt", [B.MOE_FP4_MX, B.MOE_FP4_NV], ids=["mx", "nv"])
+def test_layer_takes_larger_buffers(lib, fmt):
+    """One set of buffers serves every batch that fits: the first T rows of out are the result."""
+    b = buffers(8, 2, fmt=fmt)
+    for T, k in ((1, 2), (7, 2), (8, 1), (5, 3)):
+        out = forward(layer(T, k, fmt=fmt), b)
+        assert out.shape == (T, 64) and out.data_ptr() == b.out.data_ptr()
+        assert lib.calls[-1] == "moe_layer_forward_fp4"
+    lib.calls.clear()
+    for T, k in ((9, 1), (6, 3)):
+        with pytest.raises(ValueError):
+            forward(layer(T, k, fmt=fmt), b)
+    assert "moe_layer_forward_fp4" not in lib.calls
