@@ -136,6 +136,15 @@ def _stream(stream=None):
     return s.cuda_stream
 
 
+def _empty(shape, dtype, device, stream):
+    """torch.empty of the pool of the stream that the call runs on: given back, the memory
+    then goes to work that comes after the call's."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _check(rc: int, where: str):
     if rc != MOE_OK:
         raise MoeError(rc, where)
@@ -168,7 +177,7 @@ def workspace_bytes(T: int, k: int, E: int) -> int:
 
 
 def make_workspace(T: int, k: int, E: int, device="cuda", stream=None) -> torch.Tensor:
-    ws = torch.empty(workspace_bytes(T, k, E), dtype=torch.uint8, device=device)
+    ws = _empty(workspace_bytes(T, k, E), torch.uint8, device, stream)
     clear_status(ws, stream)
     return ws
 
@@ -462,8 +471,7 @@ def mxfp4_to_nvfp4(scales: torch.Tensor, out=None, workspace: torch.Tensor | Non
                torch.empty(E, dtype=torch.int64, device=dev))
     e4m3, ws2, oob = out
     if workspace is None:
-        workspace = torch.empty(int(load().moe_nvfp4_cast_workspace_bytes(E)), dtype=torch.uint8,
-                                device=dev)
+        workspace = _empty(int(load().moe_nvfp4_cast_workspace_bytes(E)), torch.uint8, dev, stream)
         clear_status(workspace, stream)
     rc = load().moe_mxfp4_to_nvfp4(_ptr(scales), E, N, 32 * Kb, _ptr(e4m3), _ptr(ws2), _ptr(oob),
                                    _ptr(workspace), workspace.numel(), _stream(stream))
@@ -509,8 +517,8 @@ def topk_gate(logits: torch.Tensor, k: int, renorm: bool = False, out=None, stre
     stride = _rows_of("logits", logits)
     T, E = logits.shape
     if out is None:
-        out = (torch.empty((T, k), dtype=torch.int32, device=logits.device),
-               torch.empty((T, k), dtype=torch.float32, device=logits.device))
+        out = (_empty((T, k), torch.int32, logits.device, stream),
+               _empty((T, k), torch.float32, logits.device, stream))
     ids, w = out
     _need("ids", ids, (T, k), torch.int32)
     _need("weights", w, (T, k), torch.float32)
@@ -529,7 +537,7 @@ def topk_gate_backward(logits: torch.Tensor, ids: torch.Tensor, dw: torch.Tensor
     _need("ids", ids, (T, k), torch.int32)
     _need("dw", dw, (T, k), torch.float32)
     if out is None:
-        out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+        out = _empty((T, E), logits.dtype, logits.device, stream)
     _need("dlogits", out, (T, E), logits.dtype)
     rc = load().moe_topk_gate_backward(_ptr(logits), _dtype_code(logits.dtype), stride, T, E, k,
                                        int(bool(renorm)), _ptr(ids), _ptr(dw), _ptr(out), _stream(stream))
@@ -558,7 +566,8 @@ def fp4_quantize(x: torch.Tensor, fmt: int, row_index: torch.Tensor | None = Non
     """x [x_rows, K] (f32 or bf16, any row stride) -> (codes uint8 [rows, K/2], scales uint8
     [rows, K/32 or K/16]).  With row_index int32 [rows] row r holds x[row_index[r] // index_div].
     tensor_scale f32 [1] (NVFP4).  values (f32 or bf16 [rows, K]) receives what the codes
-    stand for."""
+    stand for.  Bad indices and tensor scales are reported in the workspace (read_status):
+    without one the call makes its own, whose status nobody sees."""
     stride = _rows_of("x", x)
     block = _fp4_block(fmt)
     x_rows, K = x.shape
@@ -566,8 +575,8 @@ def fp4_quantize(x: torch.Tensor, fmt: int, row_index: torch.Tensor | None = Non
     if row_index is not None:
         _need("row_index", row_index, (rows,), torch.int32)
     if out is None:
-        out = (torch.empty((rows, K // 2), dtype=torch.uint8, device=x.device),
-               torch.empty((rows, K // block), dtype=torch.uint8, device=x.device))
+        out = (_empty((rows, K // 2), torch.uint8, x.device, stream),
+               _empty((rows, K // block), torch.uint8, x.device, stream))
     codes, scales = out
     _need("codes", codes, (rows, K // 2), torch.uint8)
     _need("scales", scales, (rows, K // block), torch.uint8)
@@ -606,10 +615,11 @@ def fp4_grouped_gemm(act_codes: torch.Tensor, act_scales: torch.Tensor, codes: t
                      out_dtype=torch.float32, workspace: torch.Tensor | None = None, stream=None):
     """4-bit activations (fp4_quantize) by 4-bit weights uint8 [E, N, K/2] with scales
     [E, N, K/32 or K/16] over row bands group_sizes int32 [E] -> out [rows, N] (f32 or bf16).
-    NVFP4: act_scale_2 f32 [1] and weight_scale_2 f32 [E]."""
+    NVFP4: act_scale_2 f32 [1] and weight_scale_2 f32 [E].  Bad scales and group sizes are
+    reported in the workspace (read_status), as for fp4_quantize."""
     rows, K, E, N, _ = _fp4_operands(act_codes, act_scales, codes, scales, group_sizes, fmt)
     if out is None:
-        out = torch.empty((rows, N), dtype=out_dtype, device=act_codes.device)
+        out = _empty((rows, N), out_dtype, act_codes.device, stream)
     _need("out", out, (rows, N), torch.float32, torch.bfloat16)
     if workspace is None:
         workspace = make_workspace(0, 1, 1, act_codes.device, stream)
@@ -631,14 +641,14 @@ def fp4_grouped_gemm_swiglu(act_codes: torch.Tensor, act_scales: torch.Tensor, c
                             workspace: torch.Tensor | None = None, stream=None):
     """The w13 product (codes [E, 2I, K/2], gate rows first) with SwiGLU and the
     quantisation of h in its epilogue -> (h_codes uint8 [rows, I/2], h_scales uint8
-    [rows, I/32 or I/16])."""
+    [rows, I/32 or I/16]).  Workspace as for fp4_grouped_gemm."""
     rows, K, E, N, block = _fp4_operands(act_codes, act_scales, codes, scales, group_sizes, fmt)
     if N % 2:
         raise ValueError("codes: an odd number of gate and up rows")
     I = N // 2
     if out is None:
-        out = (torch.empty((rows, I // 2), dtype=torch.uint8, device=act_codes.device),
-               torch.empty((rows, I // block), dtype=torch.uint8, device=act_codes.device))
+        out = (_empty((rows, I // 2), torch.uint8, act_codes.device, stream),
+               _empty((rows, I // block), torch.uint8, act_codes.device, stream))
     h_codes, h_scales = out
     _need("h_codes", h_codes, (rows, I // 2), torch.uint8)
     _need("h_scales", h_scales, (rows, I // block), torch.uint8)
@@ -664,8 +674,8 @@ def combine_backward(dout: torch.Tensor, y: torch.Tensor, slot_to_row: torch.Ten
     _need("slot_to_row", slot_to_row, (T * k,), torch.int32)
     _need("topk_w", topk_w, (T, k), torch.float32)
     if out is None:
-        out = (torch.empty((T * k, N), dtype=dy_dtype or dout.dtype, device=dout.device),
-               torch.empty((T, k), dtype=torch.float32, device=dout.device))
+        out = (_empty((T * k, N), dy_dtype or dout.dtype, dout.device, stream),
+               _empty((T, k), torch.float32, dout.device, stream))
     dy, dw = out
     _need("dy", dy, (T * k, N), torch.float32, torch.bfloat16)
     _need("dw", dw, (T, k), torch.float32)
@@ -686,7 +696,7 @@ def gather_backward(dx_sorted: torch.Tensor, slot_to_row: torch.Tensor, k: int,
     _need("dx_sorted", dx_sorted, (rows, hidden), torch.float32, torch.bfloat16)
     _need("slot_to_row", slot_to_row, (rows,), torch.int32)
     if out is None:
-        out = torch.empty((T, hidden), dtype=dx_sorted.dtype, device=dx_sorted.device)
+        out = _empty((T, hidden), dx_sorted.dtype, dx_sorted.device, stream)
     _need("dx", out, (T, hidden), torch.float32, torch.bfloat16)
     rc = load().moe_gather_backward(_ptr(dx_sorted), _dtype_code(dx_sorted.dtype), _ptr(slot_to_row), T,
                                     int(k), hidden, _ptr(out), _dtype_code(out.dtype), _stream(stream))

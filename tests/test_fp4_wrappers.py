@@ -96,3 +96,51 @@ def test_layer_takes_larger_buffers(lib, fmt):
         with pytest.raises(ValueError):
             forward(layer(T, k, fmt=fmt), b)
     assert "moe_layer_forward_fp4" not in lib.calls
+
+
+class Streams:
+    """In place of torch.cuda.stream: which stream is current where."""
+
+    def __init__(self, monkeypatch):
+        self.now, self.made = None, []
+        empty = torch.empty
+        monkeypatch.setattr(torch.cuda, "stream", self.enter)
+        monkeypatch.setattr(torch, "empty", lambda *a, **kw: (self.made.append(self.now), empty(*a, **kw))[1])
+
+    def enter(self, stream):
+        import contextlib
+
+        @contextlib.contextmanager
+        def on():
+            was, self.now = self.now, stream
+            yield
+            self.now = was
+        return on()
+
+
+def test_what_a_wrapper_makes_belongs_to_the_calls_stream(lib, monkeypatch):
+    """A workspace made on the current stream for a call on another one goes back to the
+    current stream's pool at return, while that call may still clear and write it; and memory
+    that the current stream still uses may become an output that the other one writes."""
+    x = gpu((4, 64), torch.float32)
+    codes, scales = gpu((4, 32), torch.uint8), gpu((4, 2), torch.uint8)
+    w, wsc, sizes = gpu((2, 64, 32), torch.uint8), gpu((2, 64, 2), torch.uint8), gpu((2,), torch.int32)
+    s2r, tw = gpu((8,), torch.int32), gpu((4, 2), torch.float32)
+    monkeypatch.setattr(B, "_need", lambda *a: None)      # what torch.empty gives here is a CPU tensor
+    side = object()
+    calls = {
+        "gate": lambda s: B.topk_gate(x, 2, stream=s),
+        "gate backward": lambda s: B.topk_gate_backward(x, gpu((4, 2), torch.int32), tw, stream=s),
+        "quantise": lambda s: B.fp4_quantize(x, B.MOE_FP4_MX, stream=s),
+        "product": lambda s: B.fp4_grouped_gemm(codes, scales, w, wsc, sizes, B.MOE_FP4_MX, stream=s),
+        "swiglu": lambda s: B.fp4_grouped_gemm_swiglu(codes, scales, w, wsc, sizes, B.MOE_FP4_MX, stream=s),
+        "combine": lambda s: B.combine_backward(x, gpu((8, 64), torch.float32), s2r, tw, stream=s),
+        "gather": lambda s: B.gather_backward(gpu((8, 64), torch.float32), s2r, 2, stream=s),
+        "workspace": lambda s: B.make_workspace(4, 2, 4, "cpu", s),
+    }
+    seen = Streams(monkeypatch)
+    for name, call in calls.items():
+        for stream in (side, None):
+            seen.made.clear()
+            call(stream)
+            assert seen.made and all(s is stream for s in seen.made), (name, seen.made)

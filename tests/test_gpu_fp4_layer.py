@@ -63,3 +63,22 @@ def test_larger_buffers_give_the_same_bits(B, fmt):
         assert B.read_status(big.workspace) == B.MOE_OK
         assert torch.equal(got, want)
         assert bool((big.out[T:] == 7.0).all()) and bool((big.y2[T * k:] == 7.0).all())
+
+
+def test_a_call_on_another_stream_leaves_later_memory_alone(B):
+    """The side stream is held up, so a workspace made for the call is cleared late: memory
+    that the current stream takes meanwhile keeps its contents."""
+    rng = np.random.default_rng(2)
+    codes, scales = operand(rng, (9,), 64, MX)
+    w, wsc = operand(rng, (2, 40), 64, MX)
+    sizes = dev(np.array([9, 0], np.int32))
+    want = B.fp4_grouped_gemm(codes, scales, w, wsc, sizes, MX)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+    got = B.fp4_grouped_gemm(codes, scales, w, wsc, sizes, MX, stream=side)
+    later = [torch.full((256,), 7, dtype=torch.uint8, device=DEV) for _ in range(64)]
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    assert all(bool((t == 7).all()) for t in later)
