@@ -499,6 +499,15 @@ def _at_least(name: str, t: torch.Tensor, shape, dtype):
     _need(name, t, (max(t.shape[0], shape[0]) if t.dim() else 0, *shape[1:]), dtype)
 
 
+def _workspace(ws, device, stream):
+    """The call's workspace: the caller's, if the kernels can write it, or a new one."""
+    if ws is None:
+        return make_workspace(0, 1, 1, device, stream)
+    if not (ws.is_cuda and ws.is_contiguous()):
+        raise ValueError("workspace: a contiguous CUDA tensor is needed")
+    return ws
+
+
 def _rows_of(name: str, t: torch.Tensor) -> int:
     """Row stride, in elements, of a 2-D tensor whose rows are contiguous."""
     if t.dim() != 2 or t.dtype not in (torch.float32, torch.bfloat16):
@@ -584,8 +593,7 @@ def fp4_quantize(x: torch.Tensor, fmt: int, row_index: torch.Tensor | None = Non
     if values is not None:
         _need("values", values, (rows, K), torch.float32, torch.bfloat16)
         vdt = _dtype_code(values.dtype)
-    if workspace is None:
-        workspace = make_workspace(0, 1, 1, x.device, stream)
+    workspace = _workspace(workspace, x.device, stream)
     rc = load().moe_fp4_quantize(_ptr(x), _dtype_code(x.dtype), x_rows, stride, K, _ptr(row_index),
                                  int(index_div), rows, fmt,
                                  _tensor_scale("tensor_scale", tensor_scale, 1, fmt), _ptr(codes),
@@ -621,8 +629,7 @@ def fp4_grouped_gemm(act_codes: torch.Tensor, act_scales: torch.Tensor, codes: t
     if out is None:
         out = _empty((rows, N), out_dtype, act_codes.device, stream)
     _need("out", out, (rows, N), torch.float32, torch.bfloat16)
-    if workspace is None:
-        workspace = make_workspace(0, 1, 1, act_codes.device, stream)
+    workspace = _workspace(workspace, act_codes.device, stream)
     rc = load().moe_fp4_grouped_gemm(_ptr(act_codes), _ptr(act_scales),
                                      _tensor_scale("act_scale_2", act_scale_2, 1, fmt), rows, K,
                                      _ptr(codes), _ptr(scales),
@@ -652,8 +659,7 @@ def fp4_grouped_gemm_swiglu(act_codes: torch.Tensor, act_scales: torch.Tensor, c
     h_codes, h_scales = out
     _need("h_codes", h_codes, (rows, I // 2), torch.uint8)
     _need("h_scales", h_scales, (rows, I // block), torch.uint8)
-    if workspace is None:
-        workspace = make_workspace(0, 1, 1, act_codes.device, stream)
+    workspace = _workspace(workspace, act_codes.device, stream)
     rc = load().moe_fp4_grouped_gemm_swiglu(
         _ptr(act_codes), _ptr(act_scales), _tensor_scale("act_scale_2", act_scale_2, 1, fmt), rows, K,
         _ptr(codes), _ptr(scales), _tensor_scale("weight_scale_2", weight_scale_2, E, fmt), fmt,
@@ -755,6 +761,7 @@ def layer_forward_fp4(x, topk_ids, topk_w, w13, w2, buffers: LayerBuffersFp4, x_
     _at_least("buffers.group_offsets", b.group_offsets, (E + 1,), torch.int32)
     _at_least("buffers.sorted_slot", b.sorted_slot, (rows,), torch.int32)
     _at_least("buffers.slot_to_row", b.slot_to_row, (rows,), torch.int32)
+    _workspace(b.workspace, x.device, stream)
     rc = load().moe_layer_forward_fp4(
         _ptr(x), _ptr(topk_ids), _ptr(topk_w), T, k, E, hidden, inter, fmt, _ptr(c13), _ptr(s13),
         _tensor_scale("w13 weight_scale_2", g13, E, fmt), _ptr(c2), _ptr(s2),

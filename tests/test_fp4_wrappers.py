@@ -144,3 +144,27 @@ def test_what_a_wrapper_makes_belongs_to_the_calls_stream(lib, monkeypatch):
             seen.made.clear()
             call(stream)
             assert seen.made and all(s is stream for s in seen.made), (name, seen.made)
+
+
+def test_a_workspace_the_kernels_cannot_write_is_refused(lib):
+    x, sizes = gpu((4, 64), torch.float32), gpu((2,), torch.int32)
+    codes, scales = gpu((4, 32), torch.uint8), gpu((4, 2), torch.uint8)
+    w, wsc = gpu((2, 64, 32), torch.uint8), gpu((2, 64, 2), torch.uint8)
+    ops = (codes, scales, w, wsc, sizes, B.MOE_FP4_MX)
+    b = buffers(4, 2)
+    good = gpu((256,), torch.uint8)
+    out = dict(gemm=gpu((4, 64), torch.float32), h=(gpu((4, 16), torch.uint8), gpu((4, 1), torch.uint8)))
+    calls = {
+        "moe_fp4_quantize": lambda ws: B.fp4_quantize(x, B.MOE_FP4_MX, out=(codes, scales), workspace=ws),
+        "moe_fp4_grouped_gemm": lambda ws: B.fp4_grouped_gemm(*ops, out=out["gemm"], workspace=ws),
+        "moe_fp4_grouped_gemm_swiglu": lambda ws: B.fp4_grouped_gemm_swiglu(*ops, out=out["h"], workspace=ws),
+        "moe_layer_forward_fp4": lambda ws: (setattr(b, "workspace", ws), forward(layer(4, 2), b)),
+    }
+    for name, call in calls.items():
+        call(good)
+        assert lib.calls[-1] == name
+        lib.calls.clear()
+        for bad in (torch.zeros(4096, dtype=torch.uint8), gpu((8192,), torch.uint8)[::2]):
+            with pytest.raises(ValueError, match="workspace"):
+                call(bad)
+        assert name not in lib.calls
