@@ -1160,8 +1160,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 // both (each SM scales its own half of D).  The odd CTA's issuer warp relays: once
 // its CTA's copies and scale columns of a stage are there (it has waited for both on
 // its own `full` barrier) it arrives on the even CTA's; commits are multicast to
-// both.  That arrival is relaxed: what it reports is already in the odd SM's shared
-// and tensor memory, and a release at cluster scope took 1,650 cycles a stage.
+// both.  Three agents then order a scale column before the MMA that reads it: the
+// converter that stored it (tcgen05.wait::st, fence before its arrival), the relay (a
+// fence after its wait and one before its arrival) and the issuer (a fence after its
+// wait).  The relay's arrival itself is relaxed: a release at cluster scope waits for
+// memory accesses that no MMA reads, and took 1,650 cycles a stage.
 
 constexpr int kPairM = 256;                    // token rows of an item
 constexpr int kPairN = 192;                    // weight rows of an item
@@ -1535,6 +1538,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int j = first; ok && j < total; j += step)
             for (int ks = 0; ok && ks < k_stages; ++ks) {
                 ok = wait(&full[r.slot], r.phase, abort_flag, p.status, lim);
+                tc_fence_after();           // this CTA's scale columns before the pair's MMAs
+                tc_fence_before();
                 if (ok && lane == 0) mbar_arrive_cluster(peer_full + r.slot * 8);
                 __syncwarp();
                 r.next(n_stages);
