@@ -55,6 +55,7 @@
 #include "device_common.cuh"
 #include "fp4_common.cuh"
 #include "launch.h"
+#include "ring_drain.h"
 #include "vec_io.cuh"
 
 namespace moe {
@@ -84,7 +85,8 @@ constexpr int kOffItem = kOffRow + (kMaxE + 1) * 4;
 constexpr int kOffBars = (kOffItem + (kMaxE + 1) * 4 + 7) & ~7;
 constexpr int kNumBars = 2 * kMaxStages + 4 + 1 + 2 * kDepth + 2 * kSets;
 constexpr int kOffMisc = kOffBars + kNumBars * 8;
-constexpr int kSmemBytes = kOffMisc + 64 + 1024;
+constexpr int kMiscBytes = 64;                 // see Misc
+constexpr int kSmemBytes = kOffMisc + kMiscBytes + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 
 // Scale columns of a stage, and the stages they are kept for: every shape here has 12
@@ -174,6 +176,58 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile in
                                      uint64_t lim) {
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     return wait_slow(bar, parity, abort_flag, status, lim);
+}
+
+// A word of shared memory of a CTA of the cluster (address from cluster_addr).
+__device__ __forceinline__ uint32_t load_cluster(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// A CTA's words that are no barriers.
+struct Misc {
+    uint32_t tmem;                 // tensor-memory address
+    int nt;                        // widest chunk of the call
+    int abort;                     // a wait of the CTA gave up
+    int bad;                       // a converter saw a scale that the format does not allow
+    uint32_t stages;               // of the ring,
+    uint32_t issued;               // and how many the producer issued
+    uint32_t relay;                // ring positions (slot + stages * phase) where the relay
+    uint32_t stops[kStopWarps];    // and the converter warps stopped
+};
+static_assert(sizeof(Misc) <= kMiscBytes && kStopWarps == 4 * kSets, "misc area");
+
+// The end of a CTA, by one thread once all warps (of a pair: of both CTAs) have stopped.
+//
+// Where a wait gave up, every copy that the producer issued has to land before the CTA
+// leaves.  The stages' barriers count the converters and the relay too, so their missing
+// arrivals are made up for; a stage that the producer issued has the phase before it
+// complete (it waited for that stage's MMAs), so they fall into the right one.  Bounded by
+// one limit: the first wait that gives up ends it.
+//
+// It takes nothing from the roles' registers but constants: with the barriers' address, the
+// flag and the bad scales' report passed on to the end, the NVFP4 pair kernel of shifted
+// scales spilled in its loops (K = 2,880, six bands of 4,096 rows 237 -> 251 us).
+__device__ __noinline__ void finish(uint32_t off_bars, uint32_t off_misc, int k_stages, bool pair, int *status,
+                                    uint64_t lim) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + off_bars);
+    const Misc &misc = *reinterpret_cast<const Misc *>(smem + off_misc);
+    if (misc.bad) set_status(status, MOE_ERR_DATA);
+    if (!misc.abort) return;
+    const uint32_t relay = pair ? load_cluster(cluster_addr(&misc.relay, 1)) : 0;
+    const uint32_t *relayed = pair && cluster_rank() == 0 ? &relay : nullptr;
+    const uint32_t issued = misc.issued, n_stages = misc.stages;
+    uint32_t from = issued > n_stages ? issued - n_stages : 0;
+    while (from < issued && mbar_try_wait(&full[from % n_stages], (from / n_stages) & 1u)) ++from;
+    for (uint32_t i = from; i < issued; ++i) {
+        uint64_t *bar = &full[i % n_stages];
+        for (uint32_t n = missing_arrivals(i, from, n_stages, k_stages, misc.stops, relayed); n > 0; --n)
+            mbar_arrive(bar);
+        if (!wait_bounded(bar, (i / n_stages) & 1u, nullptr, status, lim)) return;
+    }
 }
 
 // ------------------------------------------------------------------ items
@@ -342,10 +396,11 @@ __device__ __forceinline__ void copy_scales(const ScaleEnv &v, const Staging &g,
             r.next(kDepth);
         }
     }
-    if (!ok && (threadIdx.x & 31) == 0) {   // drain: every issued copy must land before the CTA exits
+    // Every issued copy lands before the CTA leaves, whoever else may have given up: these
+    // barriers count this warp alone.
+    if ((threadIdx.x & 31) == 0)
         for (uint32_t i = issued > kDepth ? issued - kDepth : 0; i < issued; ++i)
-            wait_bounded(&g.full[i % kDepth], (i / kDepth) & 1u, nullptr, p.status, p.wait_limit_ns);
-    }
+            if (!wait_bounded(&g.full[i % kDepth], (i / kDepth) & 1u, nullptr, p.status, p.wait_limit_ns)) break;
 }
 
 // Copier warp for rows that are not whole 16-byte pieces (one an operand), two pieces a
@@ -532,7 +587,8 @@ __device__ __forceinline__ void init_scale_bars(uint64_t *raw_bars, uint32_t cop
 template <bool kNv, bool kShift, int RA, int RB, int kMost, int kTile, class RowA, class RowB, class UsedA, class UsedB>
 __device__ __forceinline__ void convert_scales(const ScaleEnv &v, const Staging &g, int first_a, int first_b,
                                                uint32_t sf_tmem, uint64_t *full, uint64_t *empty, uint32_t n_stages,
-                                               bool windows, RowA row_a, RowB row_b, UsedA used_a, UsedB used_b) {
+                                               Misc *misc, bool windows, RowA row_a, RowB row_b, UsedA used_a,
+                                               UsedB used_b) {
     using C = ScaleCols<kNv>;
     constexpr int W = C::W, kACols = 4 * ((RA + 3) / 4) * W;
     constexpr int kStages = kShift && kNv ? 2 : kGroup;       // of a group
@@ -643,7 +699,8 @@ __device__ __forceinline__ void convert_scales(const ScaleEnv &v, const Staging 
             raw.next(kDepth);
         }
     }
-    if (bad & 0x80808080u) set_status(p.status, MOE_ERR_DATA);
+    if (bad & 0x80808080u) misc->bad = 1;
+    if (lane == 0) misc->stops[(threadIdx.x >> 5) - kConvertWarp] = r.phase * n_stages + r.slot;
 }
 
 // -------------------------------------------------------------- epilogues
@@ -929,15 +986,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *acc_empty = acc_full + 2;                               // epilogue -> issuer
     uint64_t *final_bar = acc_empty + 2;
     uint64_t *raw_bars = final_bar + 1;                               // scale copiers <-> converters
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kOffMisc);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kOffMisc + 8);
-    int *nt_slot = reinterpret_cast<int *>(smem + kOffMisc + 24);
+    Misc *misc = reinterpret_cast<Misc *>(smem + kOffMisc);
+    volatile int *abort_flag = &misc->abort;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int E = p.E;
 
-    if (tid == 0) *abort_flag = 0;
-    const bool any = build_items<S::NT>(p, roff, ioff, smem + kOffStaging, nt_slot);
+    if (tid == 0) misc->abort = misc->bad = 0;
+    const bool any = build_items<S::NT>(p, roff, ioff, smem + kOffStaging, &misc->nt);
     // redux: the compiler then knows the loops' bounds as warp-uniform
     const int total = any ? __reduce_max_sync(0xffffffffu, ioff[E]) : 0;
     if (static_cast<int>(blockIdx.x) >= total) {
@@ -947,14 +1003,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if constexpr (!kShift) clear_staging(smem + kOffStaging, kOffRow - kOffStaging);
     // Stage layout: as many stages as fit with the widest chunk of this call.
-    const int nt_max = *nt_slot;
+    const int nt_max = misc->nt;
     const uint32_t b_rows = nt_max <= 32 ? nt_max : (nt_max + 63) & ~63;
     const uint32_t b_bytes = b_rows * kStageBytesRow;
     const uint32_t n_stages = min(static_cast<uint32_t>(kMaxStages), kRingBytes / (S::kABytes + b_bytes));
+    static_assert(kRingBytes / (S::kABytes + ((S::NT + 63) & ~63) * kStageBytesRow) >= kMinDrainStages, "see finish");
     uint8_t *b_ring = smem + n_stages * S::kABytes;
     const int k_stages = (p.K + kStageK - 1) / kStageK;
 
-    if (warp == kProducerWarp) tmem_alloc(tmem_slot, kTmemCols);
+    if (warp == kProducerWarp) tmem_alloc(&misc->tmem, kTmemCols);
     if (tid == 0) {
         for (uint32_t s = 0; s < n_stages; ++s) {
             mbar_init(&full[s], 1 + 4);
@@ -971,7 +1028,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = misc->tmem;
     const uint64_t lim = p.wait_limit_ns;
 
     if (warp == kProducerWarp) {
@@ -1015,9 +1072,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 r.next(n_stages);
             }
         }
-        if (!ok && lane == 0) {   // drain: every issued copy must land before the CTA exits
-            for (uint32_t i = issued > n_stages ? issued - n_stages : 0; i < issued; ++i)
-                wait_bounded(&full[i % n_stages], (i / n_stages) & 1u, nullptr, p.status, lim);
+        if (lane == 0) {
+            misc->stages = n_stages;
+            misc->issued = issued;
         }
     } else if (warp == kIssuerWarp) {
         // The whole warp runs the loop, so that addresses and descriptors stay in
@@ -1088,8 +1145,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const auto a_used = [](const Item &it) { return (it.nvalid + 31) / 32; };
         const uint32_t sf_tmem = tmem + kSfCol0 + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         if (warp >= kConvertWarp) {
-            convert_scales<kNv, kShift, RW, RA, S::NT, kTileN>(v, g, 0, RW, sf_tmem, full, empty, n_stages, p.windows,
-                                                               w_row, a_row, w_used, a_used);
+            convert_scales<kNv, kShift, RW, RA, S::NT, kTileN>(v, g, 0, RW, sf_tmem, full, empty, n_stages,
+                                                               misc, p.windows, w_row, a_row, w_used, a_used);
         } else if constexpr (kShift) {
             if (warp == kCopyWarp)
                 copy_scales_shift<RW, S::NT, kTileN>(v, g, 0, p.w_scales, w_rows, p.windows, w_row, w_used);
@@ -1133,7 +1190,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == kProducerWarp) tmem_dealloc(tmem, kTmemCols);
+    if (warp == kProducerWarp) {
+        if (lane == 0) finish(kOffBars, kOffMisc, (p.K + kStageK - 1) / kStageK, false, p.status, p.wait_limit_ns);
+        __syncwarp();
+        tmem_dealloc(tmem, kTmemCols);
+    }
     after_pairs();
 }
 
@@ -1180,7 +1241,7 @@ constexpr int kPairOffRow = kPairOffStaging + kPairStaging;
 constexpr int kPairOffItem = kPairOffRow + (kMaxE + 1) * 4;
 constexpr int kPairOffBars = (kPairOffItem + (kMaxE + 1) * 4 + 7) & ~7;
 constexpr int kPairOffMisc = kPairOffBars + (2 * kPairStages + 4 + 1 + 2 * kDepth + 2 * kSets) * 8;
-constexpr int kPairSmem = kPairOffMisc + 64 + 1024;
+constexpr int kPairSmem = kPairOffMisc + kMiscBytes + 1024;
 static_assert(kPairSmem <= 232448, "shared memory budget (pairs)");
 
 template <bool kNv>
@@ -1443,9 +1504,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint64_t *acc_empty = acc_full + 2;                                   // epilogues of both -> issuer
     uint64_t *final_bar = acc_empty + 2;
     uint64_t *raw_bars = final_bar + 1;                               // scale copiers <-> converters
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kPairOffMisc);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kPairOffMisc + 8);
-    int *nt_slot = reinterpret_cast<int *>(smem + kPairOffMisc + 24);
+    Misc *misc = reinterpret_cast<Misc *>(smem + kPairOffMisc);
+    volatile int *abort_flag = &misc->abort;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int E = p.E;
@@ -1453,9 +1513,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int first = static_cast<int>(blockIdx.x >> 1), step = static_cast<int>(gridDim.x >> 1);
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (tid == 0) *abort_flag = 0;
+    if (tid == 0) misc->abort = misc->bad = 0;
     // Both CTAs read the same sizes, so both return here or neither does.
-    if (!build_items<kPairM>(p, roff, ioff, smem + kPairOffStaging, nt_slot)) return;
+    if (!build_items<kPairM>(p, roff, ioff, smem + kPairOffStaging, &misc->nt)) return;
     // redux: the compiler then knows the loops' bounds as warp-uniform
     const int total = __reduce_max_sync(0xffffffffu, ioff[E]);
     if (first >= total) return;
@@ -1465,7 +1525,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int k_stages = (p.K + kStageK - 1) / kStageK;
     uint8_t *b_ring = smem + n_stages * kPairABytes;
 
-    if (warp == kProducerWarp) tmem_alloc_pair(tmem_slot, kTmemCols);
+    if (warp == kProducerWarp) tmem_alloc_pair(&misc->tmem, kTmemCols);
     if (tid == 0) {
         for (uint32_t s = 0; s < n_stages; ++s) {
             mbar_init(&full[s], 1 + 4 + (rank == 0 ? 1 : 0));
@@ -1483,7 +1543,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncthreads();
     cluster_sync();        // the peer's barriers exist before any remote arrival
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = misc->tmem;
     const uint64_t lim = p.wait_limit_ns;
 
     if (warp == kProducerWarp) {
@@ -1527,9 +1587,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 r.next(n_stages);
             }
         }
-        if (!ok && lane == 0) {   // drain: every issued copy must land before the CTA exits
-            for (uint32_t i = issued > n_stages ? issued - n_stages : 0; i < issued; ++i)
-                wait_bounded(&full[i % n_stages], (i / n_stages) & 1u, nullptr, p.status, lim);
+        if (lane == 0) {
+            misc->stages = n_stages;
+            misc->issued = issued;
         }
     } else if (warp == kIssuerWarp && rank == 1) {
         const uint32_t peer_full = cluster_addr(full, 0);
@@ -1540,10 +1600,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 ok = wait(&full[r.slot], r.phase, abort_flag, p.status, lim);
                 tc_fence_after();           // this CTA's scale columns before the pair's MMAs
                 tc_fence_before();
-                if (ok && lane == 0) mbar_arrive_cluster(peer_full + r.slot * 8);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_cluster(peer_full + r.slot * 8);
                 __syncwarp();
                 r.next(n_stages);
             }
+        if (lane == 0) misc->relay = r.phase * n_stages + r.slot;
     } else if (warp == kIssuerWarp) {
         const bool leader = elect_one();
         const uint32_t a_base = smem_u32(smem), b_base = smem_u32(b_ring);
@@ -1609,8 +1671,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const auto a_used = [](const Item &) { return RA; };
         const uint32_t sf_tmem = tmem + kSfCol0 + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         if (warp >= kConvertWarp) {
-            convert_scales<kNv, kShift, RA, RW, kPairM, kTile>(v, g, RW, 0, sf_tmem, full, empty, n_stages, p.windows,
-                                                               a_row, w_row, a_used, w_used);
+            convert_scales<kNv, kShift, RA, RW, kPairM, kTile>(v, g, RW, 0, sf_tmem, full, empty, n_stages,
+                                                               misc, p.windows, a_row, w_row, a_used, w_used);
         } else if constexpr (kShift) {
             if (warp == kCopyWarp)
                 copy_scales_shift<RW, kPairM, kTile>(v, g, 0, p.w_scales, w_rows, p.windows, w_row, w_used);
@@ -1682,6 +1744,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     cluster_sync();
     tc_fence_after();
     if (warp == kProducerWarp) {
+        if (lane == 0)
+            finish(kPairOffBars, kPairOffMisc, (p.K + kStageK - 1) / kStageK, true, p.status, p.wait_limit_ns);
         __syncwarp();
         tmem_dealloc_pair(tmem, kTmemCols);
     }
