@@ -506,14 +506,15 @@ __device__ __forceinline__ void read_shifted(const uint8_t *from, uint32_t bits,
     }
 }
 
-// 4, 8, 16 or 32 consecutive columns of each lane's own tensor-memory lane.
+// 8, 16 or 32 consecutive columns of each lane's own tensor-memory lane.
 template <int C>
 __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&v)[C]) {
+    static_assert(C == 8 || C == 16 || C == 32, "a width without a store would store nothing");
     if constexpr (C == 32) {
         tmem_st32(taddr, v);
     } else if constexpr (C == 16) {
         tmem_st16(taddr, v);
-    } else if constexpr (C == 8) {
+    } else {
         asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
                      "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                      : "memory");
