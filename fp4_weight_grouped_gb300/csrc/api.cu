@@ -82,6 +82,9 @@ moe_status check_route_args(const int32_t *ids, int32_t T, int32_t k, int32_t E,
     return MOE_OK;
 }
 
+// Rows of 4-bit codes: the kernels count stages of up to 1,024 k, rounded up, in 32 bits.
+constexpr int32_t kMaxFp4K = INT32_MAX - 1023;
+
 bool known_dtype(int d) { return d == MOE_F32 || d == MOE_BF16; }
 
 moe_status check_fp4_gemm_args(const uint8_t *act_codes, const uint8_t *act_scales, const float *act_scale_2,
@@ -92,7 +95,7 @@ moe_status check_fp4_gemm_args(const uint8_t *act_codes, const uint8_t *act_scal
     // A tile may start its loads up to 256 rows past the last row (they read as
     // zeros): its coordinates stay 32-bit.
     constexpr int64_t kMaxRows = INT32_MAX - 512;
-    if (rows < 0 || rows > kMaxRows || K <= 0 || K % 32 != 0 || N <= 0 || E <= 0 || E > kMaxE)
+    if (rows < 0 || rows > kMaxRows || K <= 0 || K > kMaxFp4K || K % 32 != 0 || N <= 0 || E <= 0 || E > kMaxE)
         return MOE_ERR_INVALID_ARG;
     if (static_cast<int64_t>(E) * N > kMaxRows) return MOE_ERR_INVALID_ARG;
     if (!codes || !scales || !group_sizes || !workspace || workspace_bytes < kStatusBytes)
@@ -553,7 +556,7 @@ moe_status moe_fp4_quantize(const void *x, moe_dtype dtype, int64_t x_rows, int6
                             moe_fp4_format format, const float *tensor_scale, uint8_t *codes,
                             uint8_t *scales, void *values, moe_dtype values_dtype, void *workspace,
                             size_t workspace_bytes, void *stream) {
-    if (!known_dtype(dtype) || (format != MOE_FP4_MX && format != MOE_FP4_NV) || K <= 0 || K % 32 != 0 ||
+    if (!known_dtype(dtype) || (format != MOE_FP4_MX && format != MOE_FP4_NV) || K <= 0 || K > kMaxFp4K || K % 32 != 0 ||
         x_rows < 0 || x_rows > INT32_MAX || x_stride < 0 || rows < 0 || rows > INT32_MAX || index_div < 1)
         return MOE_ERR_INVALID_ARG;
     if (!workspace || workspace_bytes < kStatusBytes || !aligned(workspace, 16)) return MOE_ERR_INVALID_ARG;

@@ -591,7 +591,7 @@ MOE_API moe_status moe_topk_gate_backward(const void *logits, moe_dtype dtype, i
  *  x            device f32 or bf16, x_rows rows of K elements, row i at x + i *
  *               x_stride elements (x_stride >= 0).  16-byte aligned rows load as
  *               vectors; any other alignment of the element type is taken.
- *  K            row length, a multiple of 32.
+ *  K            row length, a multiple of 32 up to 2^31 - 1024.
  *  row_index    device int32 [rows], or NULL; index_div >= 1.  With sorted_slot
  *               and index_div = top_k, the gather of moe_route_sort.  An entry
  *               whose row lies outside [0, x_rows) sets MOE_ERR_DATA and its row
@@ -625,7 +625,7 @@ MOE_API moe_status moe_fp4_quantize(const void *x, moe_dtype dtype, int64_t x_ro
  *               (moe_fp4_quantize).
  *  codes        device uint8 [E, N, K/2], scales [E, N, K/32] or [E, N, K/16]: the
  *               weights of moe_mxfp4_grouped_gemm / moe_nvfp4_grouped_gemm.
- *  K            a multiple of 32.  Both code buffers 16-byte aligned.
+ *  K            a multiple of 32 up to 2^31 - 1024.  Both code buffers 16-byte aligned.
  *  act_scale_2, weight_scale_2   device f32 [1] and [E] (MOE_FP4_NV; ignored for
  *               MOE_FP4_MX).
  *  Other arguments as for moe_mxfp4_grouped_gemm.
