@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kThreads)
 
 template <typename T, int R>
 void start(const Gate &g, bool backward, cudaStream_t stream) {
-    const int blocks = (g.T + kThreads / 32 - 1) / (kThreads / 32);
+    const int blocks = static_cast<int>((static_cast<int64_t>(g.T) + kThreads / 32 - 1) / (kThreads / 32));
     const T *l = static_cast<const T *>(g.logits);
     if (backward && g.k <= 32)
         gate_backward_small_kernel<T, R><<<blocks, kThreads, 0, stream>>>(l, g.stride, g.T, g.E, g.k, g.renorm, g.ids,
