@@ -38,12 +38,12 @@
 //  * Persistent CTAs, one per SM, over a static list of (expert, chunk, tile).
 //  * Every wait is bounded; see wait_bounded.
 //
-// Bound: HBM for short bands, what TMA brings into an SM for long ones.  Measured, 256
-// experts, w13 K = 4,096, I = 2,048 and w2 K = 2,048, N = 4,096, of the bytes each has to
-// move at the measured copy rate: 64 tokens, top-6, w13 with SwiGLU MXFP4 276 us (100%),
-// NVFP4 295 (100%), w2 f32 150 (93%) and 157 (95%); 8,192 tokens (bands of 192 rows) w13
-// 441 us (81%) and 476 (80%), w2 304 (97%) and 312 (98%); bands of 8,192 rows, both
-// products 448 us, 5,520 TFLOP/s.
+// Bound: HBM for short bands, what TMA brings into an SM for long ones.  Measured
+// (perf/routed_bands.py), 256 experts, top-6, w13 K = 4,096, I = 2,048 and w2 K = 2,048,
+// N = 4,096, of the bytes each has to move at the measured copy rate: 64 tokens (199 experts)
+// w13 with SwiGLU MXFP4 262 us (100%), NVFP4 280 (99%), w2 f32 141 (93%) and 147 (94%);
+// 8,192 tokens (bands of 192 rows) w13 436 us (82%) and 472 (81%), w2 307 (96%) and 313
+// (97%); six bands of 8,192 rows, both products 447 us, 5,535 TFLOP/s.
 #include <atomic>
 
 #include <cuda.h>
@@ -731,8 +731,10 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 }
 
 // h = silu(g) u of two scaled pairs, silu(g) = g / (1 + 2^(-g log2 e)) with the hardware's
-// base-2 exponential and reciprocal (a few f32 ulps; h is rounded to 4 bits next).  Below
-// g = -88.7 the exponential is infinite and silu is -0, as f32 has it for this formula.
+// base-2 exponential and reciprocal.  The exponent is rounded to f32 once, so the relative
+// error grows with |g| where g < 0: about (1.25 |g| + 10) 2^-24, a few ulps near 0 and 7e-6
+// at g = -88.  (h is rounded to 4 bits next.)  Below g = -88.7 the exponential is infinite
+// and silu is -0, as f32 has it for this formula.
 template <bool kNv>
 __device__ __forceinline__ float2 gated2(uint32_t g0, uint32_t g1, uint32_t u0, uint32_t u1, float scale) {
     float2 g = make_float2(__uint_as_float(g0), __uint_as_float(g1));
@@ -1213,10 +1215,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 // gate sums in columns 0..95 and the up sums in 96..191 (CTA 0 loads the gate rows,
 // CTA 1 the up rows).
 //
-// Measured, six bands of 4,096 rows, N = 3,840, MXFP4, bf16 out: K = 8,192 242 us (6,390
-// TFLOP/s), K = 2,048 87 us.  590 cycles a stage at 2,070 MHz; without the epilogue 550,
-// without the scales' conversion 557, without both 509: copies first, then what the
-// epilogue's and the converters' instructions take from one another.
+// Measured (perf/routed_bands.py slope), six bands of 4,096 rows, N = 3,840, MXFP4, bf16
+// out: K = 8,192 237 us (6,510 TFLOP/s), K = 2,048 82 us.  A stage more costs about 520
+// cycles at 2,070 MHz (NVFP4 560), the copies' 541 within the clock's doubt.  What does not
+// grow with K is 31 us with bf16 outputs, 52 with f32 ones and 28 with SwiGLU (NVFP4 30, 52
+// and 38), several times the start-up.  With plain outputs that is about their write time at
+// the copy rate (28 and 55 us); with SwiGLU's 26 MB it is not, and no cause has been shown:
+// the epilogue's instructions are too few for it.  (Over whole calls at 590 cycles a stage,
+// no epilogue left 550, no scale conversion 557, neither 509.)
 //
 // The even CTA issues.  Token scales sit in the CTA of their rows, weight scales in
 // both (each SM scales its own half of D).  The odd CTA's issuer warp relays: once
@@ -1835,7 +1841,10 @@ constexpr int kPairBandSwiglu = 112, kPairBand = 160;
 // Calls of fewer multiplications are one launch, without pairs: what pairs gain there is less
 // than the empty launch (MXFP4, bands x rows, one CTA / pair: SwiGLU 8 x 128 23.0 / 27.0, 8 x
 // 192 26.9 / 27.0, 8 x 256 33.2 / 27.3, 4 x 512 31.2 / 26.9; plain 8 x 256 20.8 / 22.7, 8 x
-// 512 33.1 / 32.9; 8 x 192 rows are 2.6e10 with SwiGLU and 1.3e10 without).
+// 512 33.1 / 32.9; 8 x 192 rows are 2.6e10 with SwiGLU and 1.3e10 without).  The rule does not
+// see the bands: a large call of short ones alone pays an empty launch of pairs, most of it
+// beside the other (2,048 tokens, top-6 of 256 experts, bands of up to 63 rows, pairs / none:
+// w13 MXFP4 338 / 338, NVFP4 364 / 362, w2 204 / 202 and 211 / 209).
 constexpr double kPairMacsSwiglu = 2.5e10, kPairMacs = 4.5e10;
 
 std::atomic<int> g_pairing{MOE_PAIRING_AUTO};      // process-wide

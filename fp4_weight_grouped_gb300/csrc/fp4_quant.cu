@@ -8,7 +8,7 @@
 //
 // Bound: HBM writes where values are asked for, instruction issue where not.  Measured,
 // 49,152 rows of 4,096 bf16 gathered from 8,192 tokens: MXFP4 codes alone 64 us, NVFP4
-// 70 us (three quarters of all issue slots, 2.7 TB/s; see kScatter for the layer's way); with bf16 values 120 us (578 MB;
+// 70 us (three quarters of all issue slots, 2.7 TB/s; see kScatter for the layer's way); with bf16 values 124 us (578 MB;
 // filling as many bytes as it writes takes 112 us); without the gather 83 us (6.1 TB/s).
 // 3,001 rows of 2,080 f32 to NVFP4 with values: 9.4 us.
 #include <cuda_bf16.h>

@@ -4,7 +4,8 @@ the experts, and at bands of one length.
     python perf/routed_bands.py [routings] [bands] [k2880] [slope] [layer]     (default: all)
 
 Each figure is the median of several replays of a CUDA graph of calls one after another, so
-without the host; the weights of one call are larger than L2 or are read from it as in use.
+without the host.  Calls follow one another without a flush of L2: weights of hundreds of MB pass
+through it, those of few experts partly stay there, as they do in use.
 "share" is of the bytes that the call has to move (touched experts' weights, rows in and out)
 at the copy rate of MEASURED_PEAKS.json.
 """
@@ -86,7 +87,7 @@ class Products:
         if B.read_status(self.ws) != B.MOE_OK:
             raise SystemExit(f"{what}: status {B.read_status(self.ws)}")
         flops = 2.0 * self.rows * self.K * self.N
-        print(f"{what:44s} {us:9.2f} us  share {self.bytes(out_row) / us * 1e6 / HBM * 100:5.1f}%  "
+        print(f"{what:52s} {us:9.2f} us  share {self.bytes(out_row) / us * 1e6 / HBM * 100:5.1f}%  "
               f"{flops / us / 1e6:8.1f} TFLOP/s", flush=True)
 
     def plain(self, what, dtype=torch.float32):
@@ -117,8 +118,9 @@ def routings():
             gen = generator()
             ids = route(T, TOP_K, E, zipf, gen)
             sizes = torch.bincount(ids.flatten().long(), minlength=E).to(torch.int32)
-            Products(sizes, HIDDEN, 2 * INTER, f, fmt, gen).swiglu(f"{name} {f} w13")
-            Products(sizes, INTER, HIDDEN, f, fmt, gen).plain(f"{name} {f} w2")
+            label = f"{name} ({int((sizes > 0).sum())} of {E} experts)"
+            Products(sizes, HIDDEN, 2 * INTER, f, fmt, gen).swiglu(f"{label} {f} w13")
+            Products(sizes, INTER, HIDDEN, f, fmt, gen).plain(f"{label} {f} w2")
 
 
 def bands():
