@@ -223,8 +223,8 @@ __global__ void __launch_bounds__(kThreads)
             *reinterpret_cast<uint2 *>(to + at / 2) = make_uint2(w[0], w[1]);
             if (kNv || (lane & 1) == 0) to_scale[at / (kNv ? 16 : 32)] = static_cast<uint8_t>(byte);
             if constexpr (kValues) {
-                // The values the codes stand for: exact in bf16 for MX; in f32 one
-                // rounding (the product with g) for NV.
+                // The values the codes stand for: exact in bf16 for MX; for NV one
+                // rounding to f32 (the product with g), and one more where V is bf16.
                 float o[16];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {

@@ -601,7 +601,8 @@ MOE_API moe_status moe_topk_gate_backward(const void *logits, moe_dtype dtype, i
  *  codes        device uint8 [rows, K/2] out, 16-byte aligned.
  *  scales       device uint8 [rows, K/32] or [rows, K/16] out.
  *  values       device [rows, K] out or NULL, 16-byte aligned: the numbers the
- *               codes stand for (bf16 holds them exactly for MOE_FP4_MX).
+ *               codes stand for (bf16 holds them exactly for MOE_FP4_MX; for MOE_FP4_NV
+ *               they are rounded to f32 by the product with g, then to bf16).
  *  workspace    device, >= 256 bytes, 16-byte aligned (status word).
  */
 MOE_API moe_status moe_fp4_quantize(const void *x, moe_dtype dtype, int64_t x_rows, int64_t x_stride,
