@@ -494,9 +494,10 @@ def _need(name: str, t: torch.Tensor, shape, *dtypes):
     raise ValueError(f"{name}: not a CUDA tensor")
 
 
-def _at_least(name: str, t: torch.Tensor, shape, dtype):
-    """_need for a buffer that may have more rows than the call uses."""
-    _need(name, t, (max(t.shape[0], shape[0]) if t.dim() else 0, *shape[1:]), dtype)
+def _room(name: str, t: torch.Tensor, n: int, dtype):
+    """A buffer with room for n elements, which the call lays out itself."""
+    if not (t.numel() >= n and t.dtype == dtype and t.is_contiguous() and t.is_cuda):
+        raise ValueError(f"{name}: {t.numel()} elements of {t.dtype}, {n} of {dtype} in contiguous CUDA memory are needed")
 
 
 def _workspace(ws, device, stream):
@@ -751,16 +752,18 @@ def layer_forward_fp4(x, topk_ids, topk_w, w13, w2, buffers: LayerBuffersFp4, x_
     _need("w2 codes", c2, (E, hidden, inter // 2), torch.uint8)
     _need("w2 scales", s2, (E, hidden, inter // block), torch.uint8)
     rows = T * k
-    _at_least("buffers.x_codes", b.x_codes, (rows, hidden // 2), torch.uint8)
-    _at_least("buffers.x_scales", b.x_scales, (rows, hidden // block), torch.uint8)
-    _at_least("buffers.h_codes", b.h_codes, (rows, inter // 2), torch.uint8)
-    _at_least("buffers.h_scales", b.h_scales, (rows, inter // block), torch.uint8)
-    _at_least("buffers.y2", b.y2, (rows, hidden), torch.float32)
-    _at_least("buffers.out", b.out, (T, hidden), torch.float32)
-    _at_least("buffers.group_sizes", b.group_sizes, (E,), torch.int32)
-    _at_least("buffers.group_offsets", b.group_offsets, (E + 1,), torch.int32)
-    _at_least("buffers.sorted_slot", b.sorted_slot, (rows,), torch.int32)
-    _at_least("buffers.slot_to_row", b.slot_to_row, (rows,), torch.int32)
+    _room("buffers.x_codes", b.x_codes, rows * hidden // 2, torch.uint8)
+    _room("buffers.x_scales", b.x_scales, rows * hidden // block, torch.uint8)
+    _room("buffers.h_codes", b.h_codes, rows * inter // 2, torch.uint8)
+    _room("buffers.h_scales", b.h_scales, rows * inter // block, torch.uint8)
+    _room("buffers.y2", b.y2, rows * hidden, torch.float32)
+    _room("buffers.out", b.out, T * hidden, torch.float32)
+    _room("buffers.group_sizes", b.group_sizes, E, torch.int32)
+    _room("buffers.group_offsets", b.group_offsets, E + 1, torch.int32)
+    _room("buffers.sorted_slot", b.sorted_slot, rows, torch.int32)
+    _room("buffers.slot_to_row", b.slot_to_row, rows, torch.int32)
+    if b.out.shape[1:] != (hidden,):
+        raise ValueError(f"buffers.out: shape {tuple(b.out.shape)}, expected [T, {hidden}]")
     _workspace(b.workspace, x.device, stream)
     rc = load().moe_layer_forward_fp4(
         _ptr(x), _ptr(topk_ids), _ptr(topk_w), T, k, E, hidden, inter, fmt, _ptr(c13), _ptr(s13),

@@ -168,3 +168,13 @@ def test_a_workspace_the_kernels_cannot_write_is_refused(lib):
             with pytest.raises(ValueError, match="workspace"):
                 call(bad)
         assert name not in lib.calls
+
+
+def test_layer_refuses_results_of_another_width(lib):
+    """out may have more rows than the call, not other ones."""
+    for shape in ((8, 32), (4, 128), (256,), (4, 1, 64)):
+        b = buffers(4, 2)
+        b.out = gpu(shape, torch.float32)
+        with pytest.raises(ValueError, match="out"):
+            forward(layer(4, 2), b)
+    assert "moe_layer_forward_fp4" not in lib.calls
