@@ -141,6 +141,8 @@ def _empty(shape, dtype, device, stream):
     then goes to work that comes after the call's."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):       # anything with the handle, as _stream takes it
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
 

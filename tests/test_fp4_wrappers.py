@@ -98,12 +98,29 @@ def test_layer_takes_larger_buffers(lib, fmt):
     assert "moe_layer_forward_fp4" not in lib.calls
 
 
+class Side:
+    """In place of torch.cuda.Stream."""
+
+    def __init__(self, handle=4096):
+        self.cuda_stream = handle
+
+    def __eq__(self, other):
+        return isinstance(other, Side) and self.cuda_stream == other.cuda_stream
+
+
+class Foreign:
+    """Another library's stream: a handle alone."""
+    cuda_stream = 4096
+
+
 class Streams:
     """In place of torch.cuda.stream: which stream is current where."""
 
     def __init__(self, monkeypatch):
         self.now, self.made = None, []
         empty = torch.empty
+        monkeypatch.setattr(torch.cuda, "Stream", Side)
+        monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: Side(handle))
         monkeypatch.setattr(torch.cuda, "stream", self.enter)
         monkeypatch.setattr(torch, "empty", lambda *a, **kw: (self.made.append(self.now), empty(*a, **kw))[1])
 
@@ -127,7 +144,7 @@ def test_what_a_wrapper_makes_belongs_to_the_calls_stream(lib, monkeypatch):
     w, wsc, sizes = gpu((2, 64, 32), torch.uint8), gpu((2, 64, 2), torch.uint8), gpu((2,), torch.int32)
     s2r, tw = gpu((8,), torch.int32), gpu((4, 2), torch.float32)
     monkeypatch.setattr(B, "_need", lambda *a: None)      # what torch.empty gives here is a CPU tensor
-    side = object()
+    side = Side()
     calls = {
         "gate": lambda s: B.topk_gate(x, 2, stream=s),
         "gate backward": lambda s: B.topk_gate_backward(x, gpu((4, 2), torch.int32), tw, stream=s),
@@ -140,10 +157,10 @@ def test_what_a_wrapper_makes_belongs_to_the_calls_stream(lib, monkeypatch):
     }
     seen = Streams(monkeypatch)
     for name, call in calls.items():
-        for stream in (side, None):
+        for stream, want in ((side, side), (Foreign(), side), (None, None)):
             seen.made.clear()
             call(stream)
-            assert seen.made and all(s is stream for s in seen.made), (name, seen.made)
+            assert seen.made and all(s == want for s in seen.made), (name, seen.made)
 
 
 def test_a_workspace_the_kernels_cannot_write_is_refused(lib):

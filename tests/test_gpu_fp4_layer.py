@@ -82,3 +82,17 @@ def test_a_call_on_another_stream_leaves_later_memory_alone(B):
     torch.cuda.synchronize()
     assert torch.equal(got, want)
     assert all(bool((t == 7).all()) for t in later)
+
+
+def test_a_stream_given_by_its_handle(B):
+    class Handle:
+        def __init__(self, stream):
+            self.cuda_stream = stream.cuda_stream
+
+    x = torch.randn((5, 64), device=DEV)
+    want = B.fp4_quantize(x, MX)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = B.fp4_quantize(x, MX, stream=Handle(side))
+    side.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
