@@ -19,6 +19,8 @@ MOE_ROUTE_SORT_NOALLOC_SCRATCH_BYTES = 512 * 1024
 MOE_F32, MOE_BF16 = 0, 1
 MOE_ACT_ROW_MAJOR, MOE_ACT_K8_INTERLEAVED, MOE_ACT_K8_TOKEN_ORDER = 0, 1, 2
 MOE_FP4_MX, MOE_FP4_NV = 0, 1
+MOE_MATVEC_MAX_ROWS, MOE_MATVEC_MAX_K = 512, 32768
+MOE_GRAD_WORKSPACE_BYTES = 32 * 1024
 
 SYMBOLS = (
     "moe_status_string", "moe_workspace_bytes", "moe_clear_status", "moe_read_status",
@@ -29,7 +31,8 @@ SYMBOLS = (
     "moe_mxfp4_grouped_gemm_swiglu_gather", "moe_mxfp4_grouped_gemm_scatter", "moe_combine_slots",
     "moe_act_interleave_k8", "moe_set_gemm_pairing", "moe_topk_gate", "moe_topk_gate_backward",
     "moe_fp4_quantize", "moe_fp4_grouped_gemm", "moe_fp4_grouped_gemm_swiglu",
-    "moe_layer_forward_fp4", "moe_combine_backward", "moe_gather_backward",
+    "moe_layer_forward_fp4", "moe_combine_backward", "moe_gather_backward", "moe_fp4_matvec",
+    "moe_fp4_matvec_swiglu", "moe_layer_decode", "moe_grad_norm", "moe_grad_clip",
 )
 
 _lock = threading.Lock()
@@ -103,6 +106,14 @@ def load(path: str | None = None):
                 "moe_combine_backward": ([P, C.c_int, P, C.c_int, P, P, I32, I32, I32, P, C.c_int, P, P],
                                          C.c_int),
                 "moe_gather_backward": ([P, C.c_int, P, I32, I32, I32, P, C.c_int, P], C.c_int),
+                "moe_fp4_matvec": ([P, I64, I32, P, I32, I32, P, P, P, C.c_int, I32, I32, P, C.c_int, P, SZ,
+                                    P], C.c_int),
+                "moe_fp4_matvec_swiglu": ([P, I64, I32, P, I32, I32, P, P, P, C.c_int, I32, I32, P, P, SZ,
+                                           P], C.c_int),
+                "moe_layer_decode": ([P, P, P, I32, I32, I32, I32, I32, C.c_int] + [P] * 9 +
+                                     [C.c_int, P, SZ, P], C.c_int),
+                "moe_grad_norm": ([P, P, P, I32, P, P, SZ, P], C.c_int),
+                "moe_grad_clip": ([P, P, P, I32, C.c_float, C.c_float, P, P, P, SZ, P], C.c_int),
             }
             for name, (args, res) in sig.items():
                 f = getattr(lib, name)
@@ -777,6 +788,160 @@ def layer_forward_fp4(x, topk_ids, topk_w, w13, w2, buffers: LayerBuffersFp4, x_
         b.workspace.numel(), _stream(stream))
     _check(rc, "moe_layer_forward_fp4")
     return b.out if b.out.shape[0] == T else b.out[:T]
+
+
+# ------------------------------------------------------- a few tokens in 4 bits
+
+def _matvec_operands(x, codes, scales, fmt, row_expert, index_div):
+    stride = _rows_of("x", x)
+    if x.dtype != torch.bfloat16:
+        raise ValueError(f"x: dtype {x.dtype}, expected torch.bfloat16")
+    if index_div < 1:
+        raise ValueError("index_div: at least 1 is needed")
+    K = x.shape[1]
+    E, N, _ = codes.shape
+    if row_expert is None:
+        rows = x.shape[0] * index_div
+    else:
+        rows = row_expert.numel()
+        _need("row_expert", row_expert, (rows,), torch.int32)
+        if rows > x.shape[0] * index_div:
+            raise ValueError(f"x: {x.shape[0]} rows, {-(-rows // index_div)} are needed")
+    _need("codes", codes, (E, N, K // 2), torch.uint8)
+    _need("scales", scales, (E, N, K // _fp4_block(fmt)), torch.uint8)
+    return stride, rows, K, E, N
+
+
+def fp4_matvec(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, fmt: int,
+               row_expert: torch.Tensor | None = None, index_div: int = 1,
+               weight_scale_2: torch.Tensor | None = None, out: torch.Tensor | None = None,
+               out_dtype=torch.float32, workspace: torch.Tensor | None = None, stream=None):
+    """Products of a few rows with 4-bit weights: row r of the result is x[r // index_div]
+    (bf16, any row stride) times the weights of expert row_expert[r] (int32 [rows]; None: expert
+    0).  codes uint8 [E, N, K/2], scales [E, N, K/32 or K/16], weight_scale_2 f32 [E] (NVFP4) ->
+    out [rows, N] (f32 or bf16).  Bad experts and scales are reported in the workspace."""
+    stride, rows, K, E, N = _matvec_operands(x, codes, scales, fmt, row_expert, index_div)
+    if out is None:
+        out = _empty((rows, N), out_dtype, x.device, stream)
+    _need("out", out, (rows, N), torch.float32, torch.bfloat16)
+    workspace = _workspace(workspace, x.device, stream)
+    rc = load().moe_fp4_matvec(_ptr(x), stride, index_div, _ptr(row_expert), rows, K, _ptr(codes), _ptr(scales),
+                               _tensor_scale("weight_scale_2", weight_scale_2, E, fmt), fmt, E, N, _ptr(out),
+                               _dtype_code(out.dtype), _ptr(workspace), workspace.numel(), _stream(stream))
+    _check(rc, "moe_fp4_matvec")
+    return out
+
+
+def fp4_matvec_swiglu(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, fmt: int,
+                      row_expert: torch.Tensor | None = None, index_div: int = 1,
+                      weight_scale_2: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                      workspace: torch.Tensor | None = None, stream=None):
+    """fp4_matvec with w13 weights (codes [E, 2I, K/2], gate rows first) and SwiGLU behind it
+    -> h bf16 [rows, I]."""
+    stride, rows, K, E, N = _matvec_operands(x, codes, scales, fmt, row_expert, index_div)
+    if N % 2:
+        raise ValueError("codes: an odd number of gate and up rows")
+    I = N // 2
+    if out is None:
+        out = _empty((rows, I), torch.bfloat16, x.device, stream)
+    _need("out", out, (rows, I), torch.bfloat16)
+    workspace = _workspace(workspace, x.device, stream)
+    rc = load().moe_fp4_matvec_swiglu(_ptr(x), stride, index_div, _ptr(row_expert), rows, K, _ptr(codes),
+                                      _ptr(scales), _tensor_scale("weight_scale_2", weight_scale_2, E, fmt), fmt,
+                                      E, I, _ptr(out), _ptr(workspace), workspace.numel(), _stream(stream))
+    _check(rc, "moe_fp4_matvec_swiglu")
+    return out
+
+
+def layer_decode(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor, w13, w2, fmt: int,
+                 h: torch.Tensor | None = None, y2: torch.Tensor | None = None,
+                 out: torch.Tensor | None = None, out_dtype=torch.float32,
+                 workspace: torch.Tensor | None = None, stream=None):
+    """The routed-expert layer for a few tokens (T * k up to MOE_MATVEC_MAX_ROWS): x bf16 [T,
+    hidden], w13 and w2 (codes, scales, weight_scale_2 or None) -> out [T, hidden] (f32 or
+    bf16).  h bf16 [T*k, inter] and y2 f32 [T*k, hidden] are intermediates, made when not given."""
+    block = _fp4_block(fmt)
+    (c13, s13, g13), (c2, s2, g2) = w13, w2
+    T, k = topk_ids.shape
+    E, two_i, half = c13.shape
+    hidden, inter = 2 * half, two_i // 2
+    _need("x", x, (T, hidden), torch.bfloat16)
+    _need("topk_ids", topk_ids, (T, k), torch.int32)
+    _need("topk_w", topk_w, (T, k), torch.float32)
+    _need("w13 codes", c13, (E, 2 * inter, hidden // 2), torch.uint8)
+    _need("w13 scales", s13, (E, 2 * inter, hidden // block), torch.uint8)
+    _need("w2 codes", c2, (E, hidden, inter // 2), torch.uint8)
+    _need("w2 scales", s2, (E, hidden, inter // block), torch.uint8)
+    if h is None:
+        h = _empty((T * k, inter), torch.bfloat16, x.device, stream)
+    if y2 is None:
+        y2 = _empty((T * k, hidden), torch.float32, x.device, stream)
+    if out is None:
+        out = _empty((T, hidden), out_dtype, x.device, stream)
+    _room("h", h, T * k * inter, torch.bfloat16)
+    _room("y2", y2, T * k * hidden, torch.float32)
+    _need("out", out, (T, hidden), torch.float32, torch.bfloat16)
+    workspace = _workspace(workspace, x.device, stream)
+    rc = load().moe_layer_decode(
+        _ptr(x), _ptr(topk_ids), _ptr(topk_w), T, k, E, hidden, inter, fmt, _ptr(c13), _ptr(s13),
+        _tensor_scale("w13 weight_scale_2", g13, E, fmt), _ptr(c2), _ptr(s2),
+        _tensor_scale("w2 weight_scale_2", g2, E, fmt), _ptr(h), _ptr(y2), _ptr(out), _dtype_code(out.dtype),
+        _ptr(workspace), workspace.numel(), _stream(stream))
+    _check(rc, "moe_layer_decode")
+    return out
+
+
+# ------------------------------------------------------- gradient norm and clipping
+
+_GRAD_DTYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+
+
+def _grad_arrays(grads, name="grads"):
+    """Pointers, sizes and types of a list of gradients, as the library takes them."""
+    n = len(grads)
+    for i, t in enumerate(grads):
+        if not (t.dtype in _GRAD_DTYPES and t.is_contiguous() and t.is_cuda):
+            raise ValueError(f"{name}[{i}]: a contiguous float32 or bfloat16 CUDA tensor is needed")
+    return ((C.c_void_p * n)(*[t.data_ptr() for t in grads]), (C.c_int64 * n)(*[t.numel() for t in grads]),
+            (C.c_int32 * n)(*[_GRAD_DTYPES[t.dtype] for t in grads]))
+
+
+def _grad_call(grads, norm, workspace, stream):
+    device = grads[0].device if grads else "cuda"
+    if norm is None:
+        norm = _empty((1,), torch.float32, device, stream)
+    _need("norm", norm, (1,), torch.float32)
+    if workspace is None:
+        workspace = _empty((MOE_GRAD_WORKSPACE_BYTES,), torch.uint8, device, stream)
+    return norm, _workspace(workspace, device, stream)
+
+
+def grad_norm(grads, norm: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """Global norm f32 [1] of a list of contiguous gradients (f32 or bf16 each)."""
+    ptrs, sizes, dtypes = _grad_arrays(grads)
+    norm, workspace = _grad_call(grads, norm, workspace, stream)
+    rc = load().moe_grad_norm(ptrs, sizes, dtypes, len(grads), _ptr(norm), _ptr(workspace), workspace.numel(),
+                              _stream(stream))
+    _check(rc, "moe_grad_norm")
+    return norm
+
+
+def clip_grads(grads, max_norm: float, eps: float = 1e-6, out=None, norm: torch.Tensor | None = None,
+               workspace: torch.Tensor | None = None, stream=None):
+    """Scale a list of gradients (f32 or bf16 each, contiguous) by min(1, max_norm / (norm +
+    eps)), in place or into the tensors of `out`; returns their global norm, f32 [1].  A norm
+    that is not finite scales nothing.  Workspace: MOE_GRAD_WORKSPACE_BYTES."""
+    ptrs, sizes, dtypes = _grad_arrays(grads)
+    outs = None
+    if out is not None:
+        outs, osizes, odtypes = _grad_arrays(out, "out")
+        if len(out) != len(grads) or list(osizes) != list(sizes) or list(odtypes) != list(dtypes):
+            raise ValueError("out: not of the gradients' sizes and types")
+    norm, workspace = _grad_call(grads, norm, workspace, stream)
+    rc = load().moe_grad_clip(ptrs, sizes, dtypes, len(grads), float(max_norm), float(eps), outs, _ptr(norm),
+                              _ptr(workspace), workspace.numel(), _stream(stream))
+    _check(rc, "moe_grad_clip")
+    return norm
 
 
 def debug_bounded_wait(limit_ns: int, workspace: torch.Tensor, stream=None):

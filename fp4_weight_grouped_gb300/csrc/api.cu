@@ -136,6 +136,55 @@ moe_status check_gate_args(const void *logits, int dtype, int64_t stride, int32_
     return MOE_OK;
 }
 
+moe_status check_matvec_args(const uint16_t *x, int64_t x_stride, int32_t index_div, int32_t rows, int32_t K,
+                             const uint8_t *codes, const uint8_t *scales, const float *weight_scale_2, int format,
+                             int32_t E, int64_t N, int64_t columns, const void *out, const void *workspace,
+                             size_t workspace_bytes) {
+    if (rows < 0 || K <= 0 || K % 32 != 0 || E <= 0 || E > kMaxE || N <= 0 || index_div < 1 || x_stride < 0)
+        return MOE_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(E) * N > INT32_MAX || static_cast<int64_t>(rows) * columns > INT32_MAX)
+        return MOE_ERR_INVALID_ARG;
+    if (format != MOE_FP4_MX && format != MOE_FP4_NV) return MOE_ERR_INVALID_ARG;
+    if (!codes || !scales || !workspace || workspace_bytes < kStatusBytes || !aligned(codes, 16) || !aligned(workspace, 16))
+        return MOE_ERR_INVALID_ARG;
+    if (format == MOE_FP4_NV && (!weight_scale_2 || !aligned(weight_scale_2, 4))) return MOE_ERR_INVALID_ARG;
+    if (rows > 0 && (!x || !out || !aligned(x, 2))) return MOE_ERR_INVALID_ARG;
+    if (rows > MOE_MATVEC_MAX_ROWS || K > MOE_MATVEC_MAX_K) return MOE_ERR_CAPACITY;
+    return MOE_OK;
+}
+
+moe::Matvec matvec(const uint16_t *x, int64_t x_stride, int32_t index_div, const int32_t *row_expert, int32_t rows,
+                   int32_t K, const uint8_t *codes, const uint8_t *scales, const float *weight_scale_2, int format,
+                   int32_t E, int32_t N, bool swiglu, void *out, int out_bf16, void *workspace) {
+    return {x, x_stride, index_div, row_expert, rows, K, E, N, codes, scales, weight_scale_2,
+            format == MOE_FP4_NV ? moe::Matvec::kNv : moe::Matvec::kMx, swiglu, out, out_bf16, status_word(workspace)};
+}
+
+moe_status grad_call(const void *const *grads, const int64_t *sizes, const int32_t *dtypes, int32_t n, float max_norm,
+                     float eps, void *const *outs, float *norm, void *workspace, size_t workspace_bytes,
+                     void *stream) {
+    if (n < 0 || (n > 0 && (!grads || !sizes || !dtypes)) || !norm || !aligned(norm, 4)) return MOE_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < MOE_GRAD_WORKSPACE_BYTES || !aligned(workspace, 16)) return MOE_ERR_INVALID_ARG;
+    if (!(max_norm >= 0.0f) || !(eps >= 0.0f) || eps > 3.402823466e38f) return MOE_ERR_INVALID_ARG;
+    for (int32_t i = 0; i < n; ++i) {
+        if (sizes[i] < 0 || sizes[i] > (INT64_MAX >> 4) || !known_dtype(dtypes[i])) return MOE_ERR_INVALID_ARG;
+        const uintptr_t a = dtypes[i] == MOE_F32 ? 4 : 2;
+        if (sizes[i] > 0 && (!grads[i] || !aligned(grads[i], a) || (outs && (!outs[i] || !aligned(outs[i], a)))))
+            return MOE_ERR_INVALID_ARG;
+    }
+    moe::GradList g = {grads, outs, sizes, dtypes, n, max_norm, eps, norm,
+                       static_cast<uint8_t *>(workspace) + kStatusBytes};
+    moe_status st = moe::check_grad_spans(g);
+    if (st != MOE_OK) return st;
+    int sms = 0;
+    if ((st = current_device(&sms)) != MOE_OK) return st;
+    if (moe::grad_partial_bytes(sms) + kStatusBytes > MOE_GRAD_WORKSPACE_BYTES) return MOE_ERR_UNSUPPORTED;
+    int launches = 0;
+    st = moe::launch_grad_clip(g, static_cast<cudaStream_t>(stream), sms, &launches);
+    g_last_launches = launches;
+    return st;
+}
+
 }  // namespace
 
 extern "C" {
@@ -716,6 +765,89 @@ moe_status moe_gather_backward(const void *dx_sorted, moe_dtype in_dtype, const 
                                      out_dtype == MOE_BF16, static_cast<cudaStream_t>(stream), sms);
     g_last_launches = T > 0 ? 1 : 0;
     return st;
+}
+
+moe_status moe_fp4_matvec(const uint16_t *x, int64_t x_stride, int32_t index_div, const int32_t *row_expert,
+                          int32_t rows, int32_t K, const uint8_t *codes, const uint8_t *scales,
+                          const float *weight_scale_2, moe_fp4_format format, int32_t E, int32_t N, void *out,
+                          moe_dtype out_dtype, void *workspace, size_t workspace_bytes, void *stream) {
+    if (!known_dtype(out_dtype) || !aligned(out, out_dtype == MOE_F32 ? 4 : 2)) return MOE_ERR_INVALID_ARG;
+    moe_status st = check_matvec_args(x, x_stride, index_div, rows, K, codes, scales, weight_scale_2, format, E, N, N,
+                                      out, workspace, workspace_bytes);
+    if (st != MOE_OK) return st;
+    int sms = 0;
+    if ((st = current_device(&sms)) != MOE_OK) return st;
+    st = moe::launch_matvec(matvec(x, x_stride, index_div, row_expert, rows, K, codes, scales, weight_scale_2, format, E,
+                                   N, false, out, out_dtype == MOE_BF16, workspace),
+                            static_cast<cudaStream_t>(stream), sms);
+    g_last_launches = rows > 0 ? 1 : 0;
+    return st;
+}
+
+moe_status moe_fp4_matvec_swiglu(const uint16_t *x, int64_t x_stride, int32_t index_div, const int32_t *row_expert,
+                                 int32_t rows, int32_t K, const uint8_t *codes, const uint8_t *scales,
+                                 const float *weight_scale_2, moe_fp4_format format, int32_t E, int32_t I,
+                                 uint16_t *h, void *workspace, size_t workspace_bytes, void *stream) {
+    if (!aligned(h, 2)) return MOE_ERR_INVALID_ARG;
+    moe_status st = check_matvec_args(x, x_stride, index_div, rows, K, codes, scales, weight_scale_2, format, E,
+                                      2 * static_cast<int64_t>(I), I, h, workspace, workspace_bytes);
+    if (st != MOE_OK) return st;
+    int sms = 0;
+    if ((st = current_device(&sms)) != MOE_OK) return st;
+    st = moe::launch_matvec(matvec(x, x_stride, index_div, row_expert, rows, K, codes, scales, weight_scale_2, format, E,
+                                   I, true, h, 1, workspace),
+                            static_cast<cudaStream_t>(stream), sms);
+    g_last_launches = rows > 0 ? 1 : 0;
+    return st;
+}
+
+moe_status moe_layer_decode(const uint16_t *x, const int32_t *topk_ids, const float *topk_w, int32_t T, int32_t k,
+                            int32_t E, int32_t hidden, int32_t inter, moe_fp4_format format, const uint8_t *w13_codes,
+                            const uint8_t *w13_scales, const float *w13_scale_2, const uint8_t *w2_codes,
+                            const uint8_t *w2_scales, const float *w2_scale_2, uint16_t *h, float *y2, void *out,
+                            moe_dtype out_dtype, void *workspace, size_t workspace_bytes, void *stream) {
+    if (T < 0 || k <= 0 || !known_dtype(out_dtype) || !aligned(out, out_dtype == MOE_F32 ? 4 : 2) || !aligned(h, 2) ||
+        !aligned(y2, 4))
+        return MOE_ERR_INVALID_ARG;
+    if (T > 0 && (!topk_ids || !topk_w || !out)) return MOE_ERR_INVALID_ARG;
+    const int64_t slots = static_cast<int64_t>(T) * k;
+    const int32_t rows = static_cast<int32_t>(slots < INT32_MAX ? slots : INT32_MAX);
+    moe_status st = check_matvec_args(x, hidden, k, rows, hidden, w13_codes, w13_scales, w13_scale_2, format, E,
+                                      2 * static_cast<int64_t>(inter), inter, h, workspace, workspace_bytes);
+    if (st == MOE_OK || st == MOE_ERR_CAPACITY) {
+        const moe_status s2 = check_matvec_args(h, inter, 1, rows, inter, w2_codes, w2_scales, w2_scale_2, format, E,
+                                                hidden, hidden, y2, workspace, workspace_bytes);
+        if (s2 != MOE_OK && (st == MOE_OK || s2 == MOE_ERR_INVALID_ARG)) st = s2;
+    }
+    if (st != MOE_OK) return st;
+    int sms = 0;
+    if ((st = current_device(&sms)) != MOE_OK) return st;
+    g_last_launches = 0;
+    if (rows == 0) return MOE_OK;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    st = moe::launch_matvec(matvec(x, hidden, k, topk_ids, rows, hidden, w13_codes, w13_scales, w13_scale_2, format, E,
+                                   inter, true, h, 1, workspace),
+                            s, sms);
+    if (st == MOE_OK)
+        st = moe::launch_matvec(matvec(h, inter, 1, topk_ids, rows, inter, w2_codes, w2_scales, w2_scale_2, format, E,
+                                       hidden, false, y2, 0, workspace),
+                                s, sms);
+    if (st == MOE_OK) st = moe::launch_weigh(y2, topk_ids, topk_w, T, k, hidden, E, out, out_dtype == MOE_BF16, s);
+    g_last_launches = 3;
+    return st;
+}
+
+moe_status moe_grad_norm(const void *const *grads, const int64_t *sizes, const int32_t *dtypes, int32_t n, float *norm,
+                         void *workspace, size_t workspace_bytes, void *stream) {
+    return grad_call(grads, sizes, dtypes, n, 0.0f, 0.0f, nullptr, norm, workspace, workspace_bytes, stream);
+}
+
+moe_status moe_grad_clip(const void *const *grads, const int64_t *sizes, const int32_t *dtypes, int32_t n,
+                         float max_norm, float eps, void *const *outs, float *norm, void *workspace,
+                         size_t workspace_bytes, void *stream) {
+    void *const *in_place = const_cast<void *const *>(grads);
+    return grad_call(grads, sizes, dtypes, n, max_norm, eps, outs ? outs : in_place, norm, workspace, workspace_bytes,
+                     stream);
 }
 
 moe_status moe_debug_bounded_wait(uint64_t limit_ns, void *workspace, size_t workspace_bytes,

@@ -162,4 +162,43 @@ struct Gate {
 };
 moe_status launch_topk_gate(const Gate &g, bool backward, cudaStream_t stream);
 
+// Products of a few rows with weights that each row chooses: 4-bit or bf16, plain or SwiGLU
+// (N = I columns of h, weights of 2 I rows an expert).
+struct Matvec {
+    enum Format { kMx, kNv, kBf16 };
+    const uint16_t *x;
+    int64_t x_stride;
+    int index_div;
+    const int32_t *row_expert;
+    int rows, K, E, N;
+    const void *weights;
+    const uint8_t *scales;
+    const float *weight_scale_2;
+    Format format;
+    bool swiglu;
+    void *out;
+    int out_bf16;
+    int *status;
+};
+moe_status launch_matvec(const Matvec &m, cudaStream_t stream, int num_sms);
+
+// out[t] = sum_j w[t, j] y[t k + j] over the slots whose id is in [0, E).
+moe_status launch_weigh(const float *y, const int32_t *ids, const float *w, int T, int k, int N, int E, void *out,
+                        int out_bf16, cudaStream_t stream);
+
+// Global norm of n tensors and, with `out`, clipping by it.
+struct GradList {
+    const void *const *in;
+    void *const *out;             // null: the norm alone
+    const int64_t *sizes;
+    const int32_t *dtypes;
+    int n;
+    double max_norm, eps;
+    float *norm;
+    void *partial;                // grad_partial_bytes
+};
+size_t grad_partial_bytes(int num_sms);
+moe_status check_grad_spans(const GradList &g);
+moe_status launch_grad_clip(const GradList &g, cudaStream_t stream, int num_sms, int *launches);
+
 }  // namespace moe

@@ -724,6 +724,122 @@ MOE_API moe_status moe_gather_backward(const void *dx_sorted, moe_dtype in_dtype
                                        int32_t hidden, void *dx, moe_dtype out_dtype, void *stream);
 
 /*
+ * moe_fp4_matvec — products of a few activation rows with 4-bit expert weights
+ * that each row names (W4A16), without a sort:
+ *
+ *   out[r, n] = sum_k x[r / index_div, k] * w[row_expert[r], n, k]
+ *
+ * with w as in moe_mxfp4_grouped_gemm (MOE_FP4_MX: e2m1 * 2^(scale - 127) per 32 k) or
+ * moe_nvfp4_grouped_gemm (MOE_FP4_NV: e2m1 * e4m3 per 16 k * weight_scale_2[e]).  Made
+ * for decode steps: rows of one expert share one pass over its weights, 8 at a time,
+ * and weights of experts that no row names are not read.  Many rows an expert belong
+ * to the grouped GEMMs.
+ *
+ *  x            device bf16, row i at x + i * x_stride elements (x_stride >= 0),
+ *               2-byte aligned (16-byte aligned rows load as vectors).
+ *  index_div    rows of the result that share a row of x: top_k, or 1.
+ *  row_expert   device int32 [rows], or NULL: expert 0.  A row whose entry lies
+ *               outside [0, E) sets MOE_ERR_DATA and becomes zeros.
+ *  rows         0..MOE_MATVEC_MAX_ROWS (more: MOE_ERR_CAPACITY).
+ *  K            a multiple of 32 up to MOE_MATVEC_MAX_K (more: MOE_ERR_CAPACITY).
+ *  codes        device uint8 [E, N, K/2], 16-byte aligned; scales [E, N, K/32] or
+ *               [E, N, K/16]; weight_scale_2 device f32 [E] (MOE_FP4_NV; ignored for
+ *               MOE_FP4_MX).
+ *  E, N         1..1024 experts; N >= 1 columns; E * N and rows * N below 2^31.
+ *  out          device [rows, N], f32 or bf16.
+ *  workspace    device, >= 256 bytes, 16-byte aligned (status word).
+ * Products are exact and sums are f32, but for elements of x below 2^-28 of their row's
+ * largest: they are rounded to 2^-38 of it.  MOE_FP4_MX blocks whose scale is below
+ * 2^-118 count as zero.  A scale byte that the format does not allow (E8M0 above 252,
+ * an E4M3 NaN) sets MOE_ERR_DATA and makes its column NaN.  Results repeat bit for bit.
+ */
+#define MOE_MATVEC_MAX_ROWS 512
+#define MOE_MATVEC_MAX_K 32768
+MOE_API moe_status moe_fp4_matvec(const uint16_t *x, int64_t x_stride, int32_t index_div,
+                                  const int32_t *row_expert, int32_t rows, int32_t K,
+                                  const uint8_t *codes, const uint8_t *scales,
+                                  const float *weight_scale_2, moe_fp4_format format, int32_t E,
+                                  int32_t N, void *out, moe_dtype out_dtype, void *workspace,
+                                  size_t workspace_bytes, void *stream);
+
+/*
+ * moe_fp4_matvec_swiglu — the w13 product of moe_fp4_matvec with SwiGLU behind it:
+ *
+ *   h[r, i] = silu(y[r, i]) * y[r, I + i],  y = moe_fp4_matvec over 2 I weight rows
+ *
+ * in f32, rounded once to bf16.
+ *  codes / scales   [E, 2*I, K/2] / [E, 2*I, K/32 or K/16]: rows [0, I) gate, [I, 2I) up.
+ *  h            device bf16 [rows, I] out.  E * 2 I and rows * I below 2^31.
+ *  Other arguments as for moe_fp4_matvec.
+ */
+MOE_API moe_status moe_fp4_matvec_swiglu(const uint16_t *x, int64_t x_stride, int32_t index_div,
+                                         const int32_t *row_expert, int32_t rows, int32_t K,
+                                         const uint8_t *codes, const uint8_t *scales,
+                                         const float *weight_scale_2, moe_fp4_format format,
+                                         int32_t E, int32_t I, uint16_t *h, void *workspace,
+                                         size_t workspace_bytes, void *stream);
+
+/*
+ * moe_layer_decode — moe_layer_forward for a few tokens, without route sort:
+ * moe_fp4_matvec_swiglu over the T * k slots -> moe_fp4_matvec -> weighted sum of a
+ * token's slots in ascending j, all on `stream`.
+ *
+ *  x            device bf16 [T, hidden]; topk_ids int32 [T, k]; topk_w f32 [T, k].  A slot
+ *               whose id lies outside [0, E) sets MOE_ERR_DATA and adds nothing.
+ *  T * k        up to MOE_MATVEC_MAX_ROWS; hidden and inter multiples of 32 up to
+ *               MOE_MATVEC_MAX_K (more: MOE_ERR_CAPACITY).
+ *  w13_scale_2, w2_scale_2   device f32 [E] (MOE_FP4_NV).
+ *  h, y2        caller-owned intermediates: bf16 [T*k, inter], f32 [T*k, hidden].
+ *  out          device [T, hidden], f32 or bf16.
+ */
+MOE_API moe_status moe_layer_decode(const uint16_t *x, const int32_t *topk_ids, const float *topk_w,
+                                    int32_t T, int32_t k, int32_t E, int32_t hidden, int32_t inter,
+                                    moe_fp4_format format, const uint8_t *w13_codes,
+                                    const uint8_t *w13_scales, const float *w13_scale_2,
+                                    const uint8_t *w2_codes, const uint8_t *w2_scales,
+                                    const float *w2_scale_2, uint16_t *h, float *y2, void *out,
+                                    moe_dtype out_dtype, void *workspace, size_t workspace_bytes,
+                                    void *stream);
+
+/*
+ * moe_grad_norm — global norm of a list of gradient tensors: the square root of the sum
+ * of all squares.
+ *
+ *  grads, sizes, dtypes   host arrays of n device pointers, element counts (>= 0) and
+ *               types (moe_dtype); read during the call only.  A tensor is contiguous
+ *               and aligned to its elements.
+ *  norm         device f32 [1] out (infinity where the norm passes f32's range).
+ *  workspace    device, >= MOE_GRAD_WORKSPACE_BYTES, 16-byte aligned.  Calls that may run
+ *               at the same time need one each.
+ * Sums are f64 but for a thread's few elements, and right over the whole range of the
+ * types.  Results repeat bit for bit.
+ */
+#define MOE_GRAD_WORKSPACE_BYTES (32u * 1024u)
+MOE_API moe_status moe_grad_norm(const void *const *grads, const int64_t *sizes,
+                                 const int32_t *dtypes, int32_t n, float *norm, void *workspace,
+                                 size_t workspace_bytes, void *stream);
+
+/*
+ * moe_grad_clip — gradients scaled so that their global norm is at most max_norm:
+ *
+ *   out = g * min(1, max_norm / (norm + eps)),  norm as moe_grad_norm has it
+ *
+ * each product formed in f32 and rounded to the tensor's type.  Where the norm is an
+ * infinity or a NaN nothing is scaled: out = g, and `norm` tells the caller.
+ *
+ *  outs         host array of n device pointers, each its gradient itself (in place) or
+ *               memory of the same size and type that overlaps no gradient; NULL: in
+ *               place throughout.  No two outputs overlap (MOE_ERR_INVALID_ARG).  A scale
+ *               of 1 in place writes nothing.
+ *  max_norm     >= 0 (infinity clips nothing); eps >= 0 and finite.
+ *  Other arguments as for moe_grad_norm.
+ */
+MOE_API moe_status moe_grad_clip(const void *const *grads, const int64_t *sizes,
+                                 const int32_t *dtypes, int32_t n, float max_norm, float eps,
+                                 void *const *outs, float *norm, void *workspace,
+                                 size_t workspace_bytes, void *stream);
+
+/*
  * moe_debug_bounded_wait — failure-detection self-test.  Launches one block
  * that waits on a shared-memory barrier nothing will ever complete, using the
  * same bounded wait as the GEMM pipeline with a limit of `limit_ns`
