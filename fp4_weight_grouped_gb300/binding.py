@@ -32,7 +32,8 @@ SYMBOLS = (
     "moe_act_interleave_k8", "moe_set_gemm_pairing", "moe_topk_gate", "moe_topk_gate_backward",
     "moe_fp4_quantize", "moe_fp4_grouped_gemm", "moe_fp4_grouped_gemm_swiglu",
     "moe_layer_forward_fp4", "moe_combine_backward", "moe_gather_backward", "moe_fp4_matvec",
-    "moe_fp4_matvec_swiglu", "moe_layer_decode", "moe_grad_norm", "moe_grad_clip",
+    "moe_fp4_matvec_swiglu", "moe_layer_decode", "moe_grad_norm", "moe_grad_clip", "moe_ffn_forward",
+    "moe_ffn_backward",
 )
 
 _lock = threading.Lock()
@@ -112,6 +113,8 @@ def load(path: str | None = None):
                                            P], C.c_int),
                 "moe_layer_decode": ([P, P, P, I32, I32, I32, I32, I32, C.c_int] + [P] * 9 +
                                      [C.c_int, P, SZ, P], C.c_int),
+                "moe_ffn_forward": ([P, I64, I32, I32, I32, P, P, P, P, P, C.c_int, P, SZ, P], C.c_int),
+                "moe_ffn_backward": ([P, P, I64, I32, I32, I32] + [P] * 8 + [C.c_int, P, SZ, P], C.c_int),
                 "moe_grad_norm": ([P, P, P, I32, P, P, SZ, P], C.c_int),
                 "moe_grad_clip": ([P, P, P, I32, C.c_float, C.c_float, P, P, P, SZ, P], C.c_int),
             }
@@ -888,6 +891,78 @@ def layer_decode(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor, 
         _tensor_scale("w2 weight_scale_2", g2, E, fmt), _ptr(h), _ptr(y2), _ptr(out), _dtype_code(out.dtype),
         _ptr(workspace), workspace.numel(), _stream(stream))
     _check(rc, "moe_layer_decode")
+    return out
+
+
+# ------------------------------------------------------- dense gated feed-forward block
+
+def _ffn_operands(x, w13, w2):
+    stride = _rows_of("x", x)
+    if x.dtype != torch.bfloat16:
+        raise ValueError(f"x: dtype {x.dtype}, expected torch.bfloat16")
+    T, hidden = x.shape
+    inter = w13.shape[0] // 2
+    _need("w13", w13, (2 * inter, hidden), torch.bfloat16)
+    _need("w2", w2, (hidden, inter), torch.bfloat16)
+    return stride, T, hidden, inter
+
+
+def ffn_forward(x: torch.Tensor, w13: torch.Tensor, w2: torch.Tensor, h: torch.Tensor | None = None,
+                gu: torch.Tensor | None = None, out: torch.Tensor | None = None, out_dtype=torch.bfloat16,
+                workspace: torch.Tensor | None = None, stream=None):
+    """Dense gated block: x bf16 [T, hidden] (row stride a multiple of 8), w13 bf16 [2*inter,
+    hidden] (gate rows first), w2 bf16 [hidden, inter] -> out [T, hidden] (bf16 or f32).  h bf16
+    [T, inter] is made when not given; gu bf16 [T, 2*inter] is written when given.  The backward
+    takes both."""
+    stride, T, hidden, inter = _ffn_operands(x, w13, w2)
+    if h is None:
+        h = _empty((T, inter), torch.bfloat16, x.device, stream)
+    _need("h", h, (T, inter), torch.bfloat16)
+    if gu is not None:
+        _need("gu", gu, (T, 2 * inter), torch.bfloat16)
+    if out is None:
+        out = _empty((T, hidden), out_dtype, x.device, stream)
+    _need("out", out, (T, hidden), torch.float32, torch.bfloat16)
+    workspace = _workspace(workspace, x.device, stream)
+    rc = load().moe_ffn_forward(_ptr(x), stride, T, hidden, inter, _ptr(w13), _ptr(w2), _ptr(gu), _ptr(h), _ptr(out),
+                                _dtype_code(out.dtype), _ptr(workspace), workspace.numel(), _stream(stream))
+    _check(rc, "moe_ffn_forward")
+    return out
+
+
+def ffn_backward(dout: torch.Tensor, x: torch.Tensor, w13: torch.Tensor, w2: torch.Tensor, h: torch.Tensor,
+                 gu: torch.Tensor, dgu: torch.Tensor | None = None, out=None, dw_dtype=torch.bfloat16,
+                 workspace: torch.Tensor | None = None, stream=None):
+    """Gradients of ffn_forward: dout bf16 [T, hidden], and x, the weights, h and gu of the
+    forward -> (dx bf16 [T, hidden], dw13 [2*inter, hidden], dw2 [hidden, inter]; bf16 or f32).
+    An entry of `out` that is None is not computed.  dgu bf16 [T, 2*inter] is scratch."""
+    stride, T, hidden, inter = _ffn_operands(x, w13, w2)
+    _need("dout", dout, (T, hidden), torch.bfloat16)
+    _need("h", h, (T, inter), torch.bfloat16)
+    _need("gu", gu, (T, 2 * inter), torch.bfloat16)
+    if dgu is None:
+        dgu = _empty((T, 2 * inter), torch.bfloat16, x.device, stream)
+    _need("dgu", dgu, (T, 2 * inter), torch.bfloat16)
+    if out is None:
+        out = (_empty((T, hidden), torch.bfloat16, x.device, stream),
+               _empty((2 * inter, hidden), dw_dtype, x.device, stream),
+               _empty((hidden, inter), dw_dtype, x.device, stream))
+    dx, dw13, dw2 = out
+    if dx is not None:
+        _need("dx", dx, (T, hidden), torch.bfloat16)
+    if dw13 is not None:
+        _need("dw13", dw13, (2 * inter, hidden), torch.float32, torch.bfloat16)
+    if dw2 is not None:
+        _need("dw2", dw2, (hidden, inter), torch.float32, torch.bfloat16)
+        if dw13 is not None and dw13.dtype != dw2.dtype:
+            raise ValueError("dw13 and dw2: one type is needed")
+    dw = dw13 if dw13 is not None else dw2
+    workspace = _workspace(workspace, x.device, stream)
+    rc = load().moe_ffn_backward(_ptr(dout), _ptr(x), stride, T, hidden, inter, _ptr(w13), _ptr(w2), _ptr(h),
+                                 _ptr(gu), _ptr(dgu), _ptr(dx), _ptr(dw13), _ptr(dw2),
+                                 MOE_BF16 if dw is None else _dtype_code(dw.dtype), _ptr(workspace),
+                                 workspace.numel(), _stream(stream))
+    _check(rc, "moe_ffn_backward")
     return out
 
 

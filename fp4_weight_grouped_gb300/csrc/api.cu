@@ -160,6 +160,19 @@ moe::Matvec matvec(const uint16_t *x, int64_t x_stride, int32_t index_div, const
             format == MOE_FP4_NV ? moe::Matvec::kNv : moe::Matvec::kMx, swiglu, out, out_bf16, status_word(workspace)};
 }
 
+moe_status check_ffn_args(const uint16_t *x, int64_t x_stride, int32_t T, int32_t hidden, int32_t inter,
+                          const uint16_t *w13, const uint16_t *w2, const void *workspace, size_t workspace_bytes) {
+    constexpr int32_t kMost = 1 << 30;
+    if (T < 0 || T >= kMost || hidden <= 0 || hidden >= kMost || hidden % 8 || inter <= 0 || inter >= kMost / 2 || inter % 8)
+        return MOE_ERR_INVALID_ARG;
+    if (T > 1 && (x_stride < hidden || x_stride % 8)) return MOE_ERR_INVALID_ARG;
+    if (!w13 || !w2 || !aligned(w13, 16) || !aligned(w2, 16) || !workspace || workspace_bytes < kStatusBytes ||
+        !aligned(workspace, 16))
+        return MOE_ERR_INVALID_ARG;
+    if (T > 0 && (!x || !aligned(x, 16))) return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
 moe_status grad_call(const void *const *grads, const int64_t *sizes, const int32_t *dtypes, int32_t n, float max_norm,
                      float eps, void *const *outs, float *norm, void *workspace, size_t workspace_bytes,
                      void *stream) {
@@ -834,6 +847,45 @@ moe_status moe_layer_decode(const uint16_t *x, const int32_t *topk_ids, const fl
                                 s, sms);
     if (st == MOE_OK) st = moe::launch_weigh(y2, topk_ids, topk_w, T, k, hidden, E, out, out_dtype == MOE_BF16, s);
     g_last_launches = 3;
+    return st;
+}
+
+moe_status moe_ffn_forward(const uint16_t *x, int64_t x_stride, int32_t T, int32_t hidden, int32_t inter,
+                           const uint16_t *w13, const uint16_t *w2, uint16_t *gu, uint16_t *h, void *out,
+                           moe_dtype out_dtype, void *workspace, size_t workspace_bytes, void *stream) {
+    moe_status st = check_ffn_args(x, x_stride, T, hidden, inter, w13, w2, workspace, workspace_bytes);
+    if (st != MOE_OK) return st;
+    if (!known_dtype(out_dtype) || (T > 0 && (!h || !out)) || !aligned(gu, 16) || !aligned(h, 16) || !aligned(out, 16))
+        return MOE_ERR_INVALID_ARG;
+    int sms = 0;
+    if ((st = current_device(&sms)) != MOE_OK) return st;
+    const moe::Ffn f = {x, T > 1 ? x_stride : hidden, T, hidden, inter, w13, w2, gu, h, out, out_dtype == MOE_BF16,
+                        status_word(workspace), kWaitLimitNs};
+    int launches = 0;
+    st = moe::launch_ffn_forward(f, static_cast<cudaStream_t>(stream), sms, &launches);
+    g_last_launches = launches;
+    return st;
+}
+
+moe_status moe_ffn_backward(const uint16_t *dout, const uint16_t *x, int64_t x_stride, int32_t T, int32_t hidden,
+                            int32_t inter, const uint16_t *w13, const uint16_t *w2, const uint16_t *h,
+                            const uint16_t *gu, uint16_t *dgu, uint16_t *dx, void *dw13, void *dw2,
+                            moe_dtype dw_dtype, void *workspace, size_t workspace_bytes, void *stream) {
+    moe_status st = check_ffn_args(x, x_stride, T, hidden, inter, w13, w2, workspace, workspace_bytes);
+    if (st != MOE_OK) return st;
+    if (!known_dtype(dw_dtype)) return MOE_ERR_INVALID_ARG;
+    if (T > 0 && (!dout || (dw2 && !h) || ((dx || dw13) && (!gu || !dgu)))) return MOE_ERR_INVALID_ARG;
+    if (!aligned(dout, 16) || !aligned(h, 16) || !aligned(gu, 16) || !aligned(dgu, 16) || !aligned(dx, 16) ||
+        !aligned(dw13, 16) || !aligned(dw2, 16))
+        return MOE_ERR_INVALID_ARG;
+    int sms = 0;
+    if ((st = current_device(&sms)) != MOE_OK) return st;
+    const moe::Ffn f = {x, T > 1 ? x_stride : hidden, T, hidden, inter, w13, w2, const_cast<uint16_t *>(gu),
+                        const_cast<uint16_t *>(h), nullptr, 0, status_word(workspace), kWaitLimitNs};
+    const moe::FfnGrad d = {dout, dgu, dx, dw13, dw2, dw_dtype == MOE_F32};
+    int launches = 0;
+    st = moe::launch_ffn_backward(f, d, static_cast<cudaStream_t>(stream), sms, &launches);
+    g_last_launches = launches;
     return st;
 }
 

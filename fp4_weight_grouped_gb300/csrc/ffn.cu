@@ -1,0 +1,560 @@
+// Dense gated feed-forward block in bf16, forward and backward:
+//
+//   [g | u] = x W13^T          h = silu(g) u         out = h W2^T
+//   dh = dout W2               dg = dh u s (1 + g (1 - s))      du = dh g s,   s = 1 / (1 + e^-g)
+//   dx = [dg | du] W13         dW13 = [dg | du]^T x             dW2 = dout^T h
+//
+// Every product is D[m, n] = sum_k A(m, k) B(n, k) with each operand stored along k (rows
+// of k) or along m / n (rows of m or n, for the products whose k is an outer dimension):
+// the tensor core reads either from shared memory as TMA leaves it, so nothing is
+// transposed in memory.
+//
+//  * CTA pairs (tcgen05.mma cta_group::2): 256 rows by kN columns an item, the rows split
+//    over the pair's tensor memory, either CTA fetching half of A and half of B.  A stage
+//    is 64 k: 128-byte rows in the 128-byte swizzle.
+//  * Accumulators are double-buffered: four epilogue warps empty one while the other fills.
+//  * SwiGLU: the even CTA fetches gate rows of W13 and the odd CTA the matching up rows, so
+//    a thread finds g and u of one output in two column ranges of its own lane.
+//  * The gradient's elementwise part is the epilogue of dh: dh is never stored.
+//  * Sums are f32; h, g, u, dg and du are rounded to bf16 once, where they are stored for
+//    the next product (which takes bf16).
+//  * Persistent pairs over a list of jobs; a job is one product.
+//  * Every wait is bounded (see wait_bounded and pair_drain.h).
+#include <atomic>
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+#include <stdint.h>
+
+#include "device_common.cuh"
+#include "launch.h"
+#include "pair_drain.h"
+#include "vec_io.cuh"
+
+namespace moe {
+namespace ffn {
+
+constexpr int kProducerWarp = 0, kIssuerWarp = 1, kEpilogueWarp = 2;
+constexpr int kThreads = 32 * (kEpilogueWarp + 4);
+constexpr int kStageK = 64;
+constexpr int kRows = 128;                         // of A a CTA
+constexpr int kABytes = kRows * 128;
+constexpr int kMaxJobs = 2;
+constexpr int kFewRows = 8;                        // tokens up to which matvec.cu streams the weights
+
+template <int kN>
+struct Tile {
+    static constexpr int kBRows = kN / 2;          // of B a CTA
+    static constexpr int kBBytes = kBRows * 128;
+    static constexpr int kStageBytes = kABytes + kBBytes;
+    static constexpr int kStages = (232448 - 2048) / kStageBytes;
+    static constexpr int kCols = 2 * kN;           // of tensor memory
+    static constexpr int kOffBars = kStages * kStageBytes;
+    static constexpr int kNumBars = 2 * kStages + 5;
+    static constexpr int kOffMisc = kOffBars + kNumBars * 8;
+    static constexpr int kSmem = kOffMisc + 32 + 1024;
+    static_assert(kSmem <= 232448, "shared memory budget");
+};
+
+enum Epilogue { kStore, kGate, kGateBack };
+
+struct Job {
+    int m, n, k;                 // n: columns of the output (gate: of h)
+    int tiles_m, tiles_n, k_stages;
+    int first;                   // item
+    int a_mn, b_mn;              // operand stored along m (n) instead of k
+    int tile_cols, b_step;       // output columns an item; the odd CTA's first row of B
+    int epilogue;
+    int out_f32;
+    void *out;                   // [m, n]; gate: h; gate back: dgu [m, 2 n]
+    uint16_t *gu;                // [m, 2 n]: gate: written if given; gate back: read
+};
+
+struct Args {
+    CUtensorMap a[kMaxJobs], b[kMaxJobs];
+    Job job[kMaxJobs];
+    int jobs, items;
+    int *status;
+    uint64_t wait_limit_ns;
+};
+
+struct Misc {
+    uint32_t tmem;
+    int abort;
+    uint32_t issued;
+};
+
+// One box into this CTA's shared memory, its bytes counted on a barrier of either CTA of the pair.
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap *map, int32_t x, int32_t y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// An operand in rows of m or n: boxes of 64 elements (128 bytes) by 64 k, one behind another.
+// Eight k are 1,024 bytes apart, 64 elements a box.
+__device__ __forceinline__ uint64_t smem_desc_mn(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(8192u >> 4) << 16;          // next 64 elements
+    d |= static_cast<uint64_t>(1024u >> 4) << 32;          // next 8 k
+    d |= 1ull << 46;
+    d |= 2ull << 61;
+    return d;
+}
+
+__device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *status,
+                                       uint64_t lim) {
+    return warp_wait_bounded(bar, parity, abort_flag, status, lim);
+}
+
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *status,
+                                     uint64_t lim) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    return wait_slow(bar, parity, abort_flag, status, lim);
+}
+
+struct Item {
+    int job, m0, n0;
+};
+
+__device__ __forceinline__ Item item_of(const Args &p, int i) {
+    int j = 0;
+    while (j + 1 < p.jobs && i >= p.job[j + 1].first) ++j;
+    const Job &w = p.job[j];
+    const int at = i - w.first;
+    return {j, at / w.tiles_n * 2 * kRows, at % w.tiles_n * w.tile_cols};
+}
+
+// 16 consecutive outputs of a row at column n: n columns are a multiple of 8.
+__device__ __forceinline__ void store16(void *row, int n, int cols, bool f32, bool sector, const float (&v)[16]) {
+    if (f32) {
+        float *o = static_cast<float *>(row) + n;
+#pragma unroll
+        for (int i = 0; i < 16; i += 4)
+            if (n + i < cols) *reinterpret_cast<float4 *>(o + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        return;
+    }
+    uint16_t *o = static_cast<uint16_t *>(row) + n;
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = bf16_pair(v[2 * i], v[2 * i + 1]);
+    if (sector && n + 16 <= cols) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(o), "r"(w[0]), "r"(w[1]),
+                     "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+        return;
+    }
+    if (n < cols) *reinterpret_cast<uint4 *>(o) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (n + 8 < cols) *reinterpret_cast<uint4 *>(o + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+__device__ __forceinline__ void load16(const uint16_t *row, int n, int cols, float (&v)[16]) {
+#pragma unroll
+    for (int h = 0; h < 16; h += 8) {
+        float t[8] = {};
+        if (n + h < cols) load_row<8>(reinterpret_cast<const __nv_bfloat16 *>(row + n + h), t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[h + i] = t[i];
+    }
+}
+
+// dg and du of one element; s and 1 - s both without cancellation.
+__device__ __forceinline__ void gate_back(float dh, float g, float u, float &dg, float &du) {
+    float t, r;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(t) : "f"(-1.4426950408889634f * fabsf(g)));
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.0f + t));
+    const float s = g >= 0.0f ? r : t * r, c = g >= 0.0f ? t * r : r;
+    dg = dh * u * (s * fmaf(g, c, 1.0f));
+    du = dh * (g * s);
+}
+
+template <int kN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ffn_kernel(const __grid_constant__ Args p) {
+    using T = Tile<kN>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + T::kOffBars);      // the even CTA's count
+    uint64_t *empty = full + T::kStages;
+    uint64_t *acc_full = empty + T::kStages, *acc_empty = acc_full + 2, *final_bar = acc_empty + 2;
+    Misc *misc = reinterpret_cast<Misc *>(smem + T::kOffMisc);
+    volatile int *abort_flag = &misc->abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+    const uint64_t lim = p.wait_limit_ns;
+
+    if (threadIdx.x == 0) {
+        misc->abort = 0;
+        misc->issued = 0;
+        for (int i = 0; i < T::kStages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_empty[i], 8);           // four warps of either CTA
+        }
+        mbar_init(final_bar, 1);
+        mbar_fence_init();
+    }
+    if (warp == kIssuerWarp) tmem_alloc_pair(&misc->tmem, T::kCols);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = misc->tmem;
+
+    if (warp == kProducerWarp) {
+        const bool leader = elect_one();
+        const uint32_t base = smem_u32(smem), bar0 = cluster_addr(full, 0);
+        uint32_t slot = 0, phase = 1, issued = 0;
+        bool ok = true;
+        for (int i = first; ok && i < p.items; i += step) {
+            const Item it = item_of(p, i);
+            const Job &w = p.job[it.job];
+            const CUtensorMap *ma = &p.a[it.job], *mb = &p.b[it.job];
+            const int row_a = it.m0 + rank * kRows, row_b = it.n0 + rank * w.b_step;
+            for (int ks = 0; ks < w.k_stages; ++ks) {
+                ok = wait(&empty[slot], phase, abort_flag, p.status, lim);
+                if (!ok) break;
+                const uint32_t a = base + slot * T::kStageBytes, b = a + kABytes, bar = bar0 + slot * 8;
+                const int k = ks * kStageK;
+                if (leader) {
+                    if (rank == 0) mbar_arrive_expect_tx(&full[slot], 2 * T::kStageBytes);
+                    if (w.a_mn) {
+                        tma_load_pair(a, ma, row_a, k, bar);
+                        tma_load_pair(a + 8192, ma, row_a + 64, k, bar);
+                    } else {
+                        tma_load_pair(a, ma, k, row_a, bar);
+                    }
+                    if (w.b_mn) {
+#pragma unroll
+                        for (int q = 0; q < T::kBRows; q += 64) tma_load_pair(b + q * 128, mb, row_b + q, k, bar);
+                    } else {
+                        tma_load_pair(b, mb, k, row_b, bar);
+                    }
+                }
+                __syncwarp();
+                ++issued;
+                slot = slot + 1 == T::kStages ? 0 : slot + 1;
+                phase ^= slot == 0;
+            }
+        }
+        if (lane == 0) misc->issued = issued;
+    } else if (warp == kIssuerWarp && rank == 0) {
+        const bool leader = elect_one();
+        const uint32_t base = smem_u32(smem);
+        uint32_t slot = 0, phase = 0, buf = 0, acc_phase = 1;
+        bool ok = true;
+        for (int i = first; ok && i < p.items; i += step) {
+            const Item it = item_of(p, i);
+            const Job &w = p.job[it.job];
+            const uint32_t idesc = idesc_bf16_f32(2 * kRows, kN) | (w.a_mn ? 1u << 15 : 0) | (w.b_mn ? 1u << 16 : 0);
+            // 16 k further: 32 bytes along a row, or 16 rows of 128 bytes.
+            const uint32_t a_step = w.a_mn ? 128 : 2, b_step = w.b_mn ? 128 : 2;
+            const uint32_t d = tmem + buf * kN;
+            ok = wait(&acc_empty[buf], acc_phase, abort_flag, p.status, lim);
+            tc_fence_after();
+            for (int ks = 0; ok && ks < w.k_stages; ++ks) {
+                ok = wait(&full[slot], phase, abort_flag, p.status, lim);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t a = base + slot * T::kStageBytes, b = a + kABytes;
+                const uint64_t da = w.a_mn ? smem_desc_mn(a) : smem_desc_sw128(a);
+                const uint64_t db = w.b_mn ? smem_desc_mn(b) : smem_desc_sw128(b);
+                if (leader) {
+#pragma unroll
+                    for (int t = 0; t < kStageK / 16; ++t)
+                        mma_pair(d, da + t * a_step, db + t * b_step, idesc, t > 0 || ks > 0);
+                    mma_commit_pair(&empty[slot], 3);
+                    if (ks == w.k_stages - 1) mma_commit_pair(&acc_full[buf], 3);
+                }
+                __syncwarp();
+                slot = slot + 1 == T::kStages ? 0 : slot + 1;
+                phase ^= slot == 0;
+            }
+            buf ^= 1u;
+            acc_phase ^= buf == 0;
+        }
+        if (leader) mma_commit_pair(final_bar, 1);
+        __syncwarp();
+        wait(final_bar, 0, nullptr, p.status, lim);
+    } else if (warp >= kEpilogueWarp) {
+        const int quarter = warp & 3;
+        uint32_t buf = 0, phase = 0;
+        for (int i = first; i < p.items; i += step) {
+            const Item it = item_of(p, i);
+            const Job &w = p.job[it.job];
+            if (!wait(&acc_full[buf], phase, abort_flag, p.status, lim)) break;
+            tc_fence_after();
+            const uint32_t acc = tmem + buf * kN + (static_cast<uint32_t>(quarter * 32) << 16);
+            const int64_t row = it.m0 + static_cast<int64_t>(rank) * kRows + quarter * 32 + lane;
+            const bool real = row < w.m;
+            const int width = w.epilogue == kGateBack ? 2 * w.n : w.n;
+            uint8_t *out = static_cast<uint8_t *>(w.out) + (real ? row : 0) * width * (w.out_f32 ? 4 : 2);
+            const bool sector = (reinterpret_cast<uintptr_t>(w.out) & 31) == 0 && width % 16 == 0;
+            if (w.epilogue == kGate) {
+                uint16_t *gu = w.gu ? w.gu + (real ? row : 0) * 2 * w.n : nullptr;
+                const bool gu_sector = (reinterpret_cast<uintptr_t>(w.gu) & 31) == 0 && w.n % 16 == 0;
+#pragma unroll 1
+                for (int c = 0; c < kN / 2; c += 16) {
+                    const int n = it.n0 + c;
+                    if (n >= w.n) break;
+                    uint32_t rg[16], ru[16];
+                    tmem_ld16(acc + c, rg);
+                    tmem_ld16(acc + kN / 2 + c, ru);
+                    tmem_ld_wait();
+                    float g[16], u[16], h[16];
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) {
+                        g[q] = __uint_as_float(rg[q]);
+                        u[q] = __uint_as_float(ru[q]);
+                        h[q] = silu_f32(g[q]) * u[q];
+                    }
+                    if (real) {
+                        store16(out, n, w.n, false, sector, h);
+                        if (gu) {
+                            store16(gu, n, w.n, false, gu_sector, g);
+                            store16(gu + w.n, n, w.n, false, gu_sector, u);
+                        }
+                    }
+                    __syncwarp();
+                }
+            } else {
+                const uint16_t *gu = w.gu + (real ? row : 0) * 2 * w.n;
+                uint16_t *up = reinterpret_cast<uint16_t *>(out) + w.n;
+#pragma unroll 1
+                for (int c = 0; c < kN; c += 16) {
+                    const int n = it.n0 + c;
+                    if (n >= w.n) break;
+                    uint32_t r[16];
+                    tmem_ld16(acc + c, r);
+                    float v[16];
+                    if (w.epilogue == kGateBack) {
+                        float g[16], u[16], du[16];
+                        load16(gu, n, w.n, g);
+                        load16(gu + w.n, n, w.n, u);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) gate_back(__uint_as_float(r[q]), g[q], u[q], v[q], du[q]);
+                        if (real) store16(up, n, w.n, false, sector && w.n % 16 == 0, du);
+                    } else {
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) v[q] = __uint_as_float(r[q]);
+                    }
+                    if (real) store16(out, n, w.n, w.out_f32, sector, v);
+                    __syncwarp();
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(cluster_addr(&acc_empty[buf], 0));
+            buf ^= 1u;
+            phase ^= buf == 0;
+        }
+    }
+    // Neither CTA frees its tensor memory or leaves while the pair's MMAs, copies, commits or
+    // the peer's arrivals may still reach it.
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    if (rank == 0 && threadIdx.x == 0) {
+        uint32_t n1, aborted;
+        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(n1) : "r"(cluster_addr(&misc->issued, 1)) : "memory");
+        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(aborted) : "r"(cluster_addr(&misc->abort, 1)) : "memory");
+        if (aborted || misc->abort) {       // every copy that was issued lands before the pair leaves
+            const uint32_t n0 = misc->issued, n = n0 > n1 ? n0 : n1;
+            for (uint32_t i = pair_first(n0, n1, T::kStages); i < n; ++i) {
+                uint64_t *bar = &full[i % T::kStages];
+                const uint32_t parity = (i / T::kStages) & 1u;
+                if (mbar_try_wait(bar, parity)) continue;
+                const PairFix f = pair_fix(i, n0, n1, T::kStageBytes);
+                if (f.arrive) mbar_arrive_expect_tx(bar, f.expect);
+                if (f.complete)
+                    asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+                                 "r"(f.complete)
+                                 : "memory");
+                if (!wait_bounded(bar, parity, nullptr, p.status, lim)) break;
+            }
+        }
+    }
+    __syncthreads();
+    if (warp == kIssuerWarp) tmem_dealloc_pair(tmem, T::kCols);
+    cluster_sync();
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) !=
+                cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return static_cast<PFN_cuTensorMapEncodeTiled_v12000>(nullptr);
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    }();
+    return fn;
+}
+
+// A bf16 matrix [rows, cols] with rows `pitch` elements apart, in boxes of 64 columns by
+// box_rows rows; what lies past its edges reads as zeros.
+bool encode(CUtensorMap *map, const void *base, int64_t rows, int64_t cols, int64_t pitch, uint32_t box_rows) {
+    PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch) * 2};
+    cuuint32_t box[2] = {64, box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// An operand (i, k): [rows of i, k], or with mn [rows of k, i].
+struct Operand {
+    const void *p;
+    int64_t pitch;
+    bool mn;
+};
+
+struct Product {
+    Operand a, b;
+    int64_t m, n, k;             // n: rows of B; gate: output columns
+    int epilogue;
+    void *out;
+    int out_f32;
+    uint16_t *gu;
+};
+
+template <int kN>
+moe_status launch(const Product *w, int jobs, int *status, uint64_t limit, cudaStream_t stream, int num_sms) {
+    using T = Tile<kN>;
+    Args p = {};
+    p.jobs = jobs;
+    p.status = status;
+    p.wait_limit_ns = limit;
+    int64_t items = 0;
+    for (int j = 0; j < jobs; ++j) {
+        Job &o = p.job[j];
+        const bool gate = w[j].epilogue == kGate;
+        o.m = static_cast<int>(w[j].m);
+        o.n = static_cast<int>(w[j].n);
+        o.k = static_cast<int>(w[j].k);
+        o.a_mn = w[j].a.mn;
+        o.b_mn = w[j].b.mn;
+        o.tile_cols = gate ? kN / 2 : kN;
+        o.b_step = gate ? o.n : kN / 2;
+        o.tiles_m = (o.m + 2 * kRows - 1) / (2 * kRows);
+        o.tiles_n = (o.n + o.tile_cols - 1) / o.tile_cols;
+        o.k_stages = (o.k + kStageK - 1) / kStageK;
+        o.first = static_cast<int>(items);
+        o.epilogue = w[j].epilogue;
+        o.out = w[j].out;
+        o.out_f32 = w[j].out_f32;
+        o.gu = w[j].gu;
+        items += static_cast<int64_t>(o.tiles_m) * o.tiles_n;
+        if (items > INT32_MAX / 2) return MOE_ERR_CAPACITY;
+        const int64_t n_rows = gate ? 2 * w[j].n : w[j].n;
+        const Operand &a = w[j].a, &b = w[j].b;
+        if (!(a.mn ? encode(&p.a[j], a.p, w[j].k, w[j].m, a.pitch, kStageK)
+                   : encode(&p.a[j], a.p, w[j].m, w[j].k, a.pitch, kRows)) ||
+            !(b.mn ? encode(&p.b[j], b.p, w[j].k, n_rows, b.pitch, kStageK)
+                   : encode(&p.b[j], b.p, n_rows, w[j].k, b.pitch, T::kBRows)))
+            return MOE_ERR_CUDA;
+    }
+    p.items = static_cast<int>(items);
+    static std::atomic<uint64_t> mask{0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
+    const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+    if (!bit || !(mask.load(std::memory_order_acquire) & bit)) {
+        if (cudaFuncSetAttribute(ffn_kernel<kN>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmem) != cudaSuccess)
+            return MOE_ERR_CUDA;
+        mask.fetch_or(bit, std::memory_order_release);
+    }
+    const int pairs = static_cast<int>(items < num_sms / 2 ? items : num_sms / 2);
+    ffn_kernel<kN><<<2 * pairs, kThreads, T::kSmem, stream>>>(p);
+    return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+moe_status run(const Product *w, int jobs, int *status, uint64_t limit, cudaStream_t stream, int num_sms) {
+    return launch<256>(w, jobs, status, limit, stream, num_sms);
+}
+
+}  // namespace ffn
+
+moe_status launch_ffn_forward(const Ffn &f, cudaStream_t stream, int num_sms, int *launches) {
+    *launches = 0;
+    if (f.T == 0) return MOE_OK;
+    const int64_t T = f.T, H = f.hidden, I = f.inter;
+    if (T <= ffn::kFewRows && !f.gu && H <= MOE_MATVEC_MAX_K && I <= MOE_MATVEC_MAX_K) {
+        Matvec m = {f.x, f.x_stride, 1, nullptr, f.T, f.hidden, 1, f.inter, f.w13, nullptr, nullptr,
+                    Matvec::kBf16, true, f.h, 1, f.status};
+        moe_status st = launch_matvec(m, stream, num_sms);
+        if (st != MOE_OK) return st;
+        m = {f.h, I, 1, nullptr, f.T, f.inter, 1, f.hidden, f.w2, nullptr, nullptr,
+             Matvec::kBf16, false, f.out, f.out_bf16, f.status};
+        *launches = 2;
+        return launch_matvec(m, stream, num_sms);
+    }
+    const ffn::Product up = {{f.x, f.x_stride, false}, {f.w13, H, false}, T, I, H, ffn::kGate, f.h, 0, f.gu};
+    moe_status st = ffn::run(&up, 1, f.status, f.wait_limit_ns, stream, num_sms);
+    if (st != MOE_OK) return st;
+    ++*launches;
+    const ffn::Product down = {{f.h, I, false}, {f.w2, I, false}, T, H, I, ffn::kStore, f.out, !f.out_bf16, nullptr};
+    st = ffn::run(&down, 1, f.status, f.wait_limit_ns, stream, num_sms);
+    if (st == MOE_OK) ++*launches;
+    return st;
+}
+
+moe_status launch_ffn_backward(const Ffn &f, const FfnGrad &d, cudaStream_t stream, int num_sms, int *launches) {
+    *launches = 0;
+    const int64_t T = f.T, H = f.hidden, I = f.inter;
+    const size_t size = d.dw_f32 ? 4 : 2;
+    if (T == 0) {                      // sums of nothing
+        if (d.dw13 && cudaMemsetAsync(d.dw13, 0, 2 * I * H * size, stream) != cudaSuccess) return MOE_ERR_CUDA;
+        if (d.dw2 && cudaMemsetAsync(d.dw2, 0, H * I * size, stream) != cudaSuccess) return MOE_ERR_CUDA;
+        return MOE_OK;
+    }
+    ffn::Product w[2];
+    int n = 0;
+    if (d.dx || d.dw13)
+        w[n++] = {{d.dout, H, false}, {f.w2, I, true}, T, I, H, ffn::kGateBack, d.dgu, 0, f.gu};
+    if (d.dw2)
+        w[n++] = {{d.dout, H, true}, {f.h, I, true}, H, I, T, ffn::kStore, d.dw2, d.dw_f32, nullptr};
+    if (n > 0) {
+        const moe_status st = ffn::run(w, n, f.status, f.wait_limit_ns, stream, num_sms);
+        if (st != MOE_OK) return st;
+        ++*launches;
+    }
+    n = 0;
+    if (d.dw13)
+        w[n++] = {{d.dgu, 2 * I, true}, {f.x, f.x_stride, true}, 2 * I, H, T, ffn::kStore, d.dw13, d.dw_f32, nullptr};
+    if (d.dx)
+        w[n++] = {{d.dgu, 2 * I, false}, {f.w13, H, true}, T, H, 2 * I, ffn::kStore, d.dx, 0, nullptr};
+    if (n > 0) {
+        const moe_status st = ffn::run(w, n, f.status, f.wait_limit_ns, stream, num_sms);
+        if (st != MOE_OK) return st;
+        ++*launches;
+    }
+    return MOE_OK;
+}
+
+}  // namespace moe

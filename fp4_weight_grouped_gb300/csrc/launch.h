@@ -201,4 +201,26 @@ size_t grad_partial_bytes(int num_sms);
 moe_status check_grad_spans(const GradList &g);
 moe_status launch_grad_clip(const GradList &g, cudaStream_t stream, int num_sms, int *launches);
 
+// Dense gated feed-forward block: forward (h, gu if given, out written) and what the backward reads of it.
+struct Ffn {
+    const uint16_t *x;
+    int64_t x_stride;
+    int T, hidden, inter;
+    const uint16_t *w13, *w2;
+    uint16_t *gu, *h;
+    void *out;
+    int out_bf16;
+    int *status;
+    uint64_t wait_limit_ns;
+};
+// Gradients; dx, dw13 and dw2 may each be null.
+struct FfnGrad {
+    const uint16_t *dout;
+    uint16_t *dgu, *dx;
+    void *dw13, *dw2;
+    int dw_f32;
+};
+moe_status launch_ffn_forward(const Ffn &f, cudaStream_t stream, int num_sms, int *launches);
+moe_status launch_ffn_backward(const Ffn &f, const FfnGrad &d, cudaStream_t stream, int num_sms, int *launches);
+
 }  // namespace moe

@@ -802,6 +802,53 @@ MOE_API moe_status moe_layer_decode(const uint16_t *x, const int32_t *topk_ids, 
                                     void *stream);
 
 /*
+ * moe_ffn_forward — dense gated feed-forward block in bf16 (a shared expert beside the
+ * routed ones):
+ *
+ *   [g | u] = x w13^T,   h = silu(g) * u,   out = h w2^T
+ *
+ * with f32 sums; h (and gu) are rounded to bf16 once, out to its type.
+ *
+ *  x            device bf16 [T, hidden], row t at x + t * x_stride elements; x_stride a
+ *               multiple of 8 and at least hidden (any value for T <= 1).
+ *  hidden, inter   positive multiples of 8.  2 * inter and T below 2^30.
+ *  w13          device bf16 [2*inter, hidden]: rows [0, inter) gate, [inter, 2*inter) up.
+ *  w2           device bf16 [hidden, inter].
+ *  gu           device bf16 [T, 2*inter] out ([g | u]), or NULL: what the backward reads.
+ *  h            device bf16 [T, inter] out.
+ *  out          device [T, hidden] out, f32 or bf16.
+ *  workspace    device, >= 256 bytes (status word).
+ * All buffers 16-byte aligned.  Two launches; results repeat bit for bit.
+ */
+MOE_API moe_status moe_ffn_forward(const uint16_t *x, int64_t x_stride, int32_t T, int32_t hidden,
+                                   int32_t inter, const uint16_t *w13, const uint16_t *w2,
+                                   uint16_t *gu, uint16_t *h, void *out, moe_dtype out_dtype,
+                                   void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * moe_ffn_backward — gradients of moe_ffn_forward.  With s = 1 / (1 + e^-g):
+ *
+ *   dh = dout w2,  dg = dh * u * s (1 + g (1 - s)),  du = dh * g s
+ *   dx = [dg | du] w13,   dw13 = [dg | du]^T x,   dw2 = dout^T h
+ *
+ * with f32 sums; dg and du are rounded to bf16 once, results to their types.
+ *
+ *  dout         device bf16 [T, hidden].
+ *  x, w13, w2, h, gu   as the forward had and left them.
+ *  dgu          device bf16 [T, 2*inter] out: [dg | du] (not written, and may be NULL, where
+ *               dx and dw13 are both NULL; gu likewise).
+ *  dx           device bf16 [T, hidden] out; dw13 [2*inter, hidden] and dw2 [hidden, inter]
+ *               out, of dw_dtype.  Each may be NULL (not computed).
+ * All buffers 16-byte aligned.  Up to two launches; results repeat bit for bit.
+ */
+MOE_API moe_status moe_ffn_backward(const uint16_t *dout, const uint16_t *x, int64_t x_stride,
+                                    int32_t T, int32_t hidden, int32_t inter, const uint16_t *w13,
+                                    const uint16_t *w2, const uint16_t *h, const uint16_t *gu,
+                                    uint16_t *dgu, uint16_t *dx, void *dw13, void *dw2,
+                                    moe_dtype dw_dtype, void *workspace, size_t workspace_bytes,
+                                    void *stream);
+
+/*
  * moe_grad_norm — global norm of a list of gradient tensors: the square root of the sum
  * of all squares.
  *
