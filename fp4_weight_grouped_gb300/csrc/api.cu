@@ -155,9 +155,10 @@ moe_status check_matvec_args(const uint16_t *x, int64_t x_stride, int32_t index_
 
 moe::Matvec matvec(const uint16_t *x, int64_t x_stride, int32_t index_div, const int32_t *row_expert, int32_t rows,
                    int32_t K, const uint8_t *codes, const uint8_t *scales, const float *weight_scale_2, int format,
-                   int32_t E, int32_t N, bool swiglu, void *out, int out_bf16, void *workspace) {
+                   int32_t E, int32_t N, bool swiglu, void *out, int out_bf16, void *workspace, bool chained = false) {
     return {x, x_stride, index_div, row_expert, rows, K, E, N, codes, scales, weight_scale_2,
-            format == MOE_FP4_NV ? moe::Matvec::kNv : moe::Matvec::kMx, swiglu, out, out_bf16, status_word(workspace)};
+            format == MOE_FP4_NV ? moe::Matvec::kNv : moe::Matvec::kMx, swiglu, out, out_bf16, status_word(workspace),
+            chained};
 }
 
 moe_status check_ffn_args(const uint16_t *x, int64_t x_stride, int32_t T, int32_t hidden, int32_t inter,
@@ -843,7 +844,7 @@ moe_status moe_layer_decode(const uint16_t *x, const int32_t *topk_ids, const fl
                             s, sms);
     if (st == MOE_OK)
         st = moe::launch_matvec(matvec(h, inter, 1, topk_ids, rows, inter, w2_codes, w2_scales, w2_scale_2, format, E,
-                                       hidden, false, y2, 0, workspace),
+                                       hidden, false, y2, 0, workspace, true),
                                 s, sms);
     if (st == MOE_OK) st = moe::launch_weigh(y2, topk_ids, topk_w, T, k, hidden, E, out, out_dtype == MOE_BF16, s);
     g_last_launches = 3;

@@ -506,11 +506,11 @@ moe_status launch_ffn_forward(const Ffn &f, cudaStream_t stream, int num_sms, in
     const int64_t T = f.T, H = f.hidden, I = f.inter;
     if (T <= ffn::kFewRows && !f.gu && H <= MOE_MATVEC_MAX_K && I <= MOE_MATVEC_MAX_K) {
         Matvec m = {f.x, f.x_stride, 1, nullptr, f.T, f.hidden, 1, f.inter, f.w13, nullptr, nullptr,
-                    Matvec::kBf16, true, f.h, 1, f.status};
+                    Matvec::kBf16, true, f.h, 1, f.status, false};
         moe_status st = launch_matvec(m, stream, num_sms);
         if (st != MOE_OK) return st;
         m = {f.h, I, 1, nullptr, f.T, f.inter, 1, f.hidden, f.w2, nullptr, nullptr,
-             Matvec::kBf16, false, f.out, f.out_bf16, f.status};
+             Matvec::kBf16, false, f.out, f.out_bf16, f.status, true};
         *launches = 2;
         return launch_matvec(m, stream, num_sms);
     }
