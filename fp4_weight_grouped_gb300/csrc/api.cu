@@ -158,7 +158,7 @@ moe::Matvec matvec(const uint16_t *x, int64_t x_stride, int32_t index_div, const
                    int32_t E, int32_t N, bool swiglu, void *out, int out_bf16, void *workspace, bool chained = false) {
     return {x, x_stride, index_div, row_expert, rows, K, E, N, codes, scales, weight_scale_2,
             format == MOE_FP4_NV ? moe::Matvec::kNv : moe::Matvec::kMx, swiglu, out, out_bf16, status_word(workspace),
-            chained};
+            kWaitLimitNs, chained};
 }
 
 moe_status check_ffn_args(const uint16_t *x, int64_t x_stride, int32_t T, int32_t hidden, int32_t inter,

@@ -31,6 +31,7 @@
 #include "device_common.cuh"
 #include "launch.h"
 #include "pair_drain.h"
+#include "tensor_map.h"
 #include "vec_io.cuh"
 
 namespace moe {
@@ -400,23 +401,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ffn_ker
     cluster_sync();
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-        void *ptr = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) !=
-                cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            return static_cast<PFN_cuTensorMapEncodeTiled_v12000>(nullptr);
-        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-    }();
-    return fn;
-}
-
 // A bf16 matrix [rows, cols] with rows `pitch` elements apart, in boxes of 64 columns by
 // box_rows rows; what lies past its edges reads as zeros.
 bool encode(CUtensorMap *map, const void *base, int64_t rows, int64_t cols, int64_t pitch, uint32_t box_rows) {
-    PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+    PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encode();
     if (!fn) return false;
     cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
     cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch) * 2};
@@ -506,11 +494,11 @@ moe_status launch_ffn_forward(const Ffn &f, cudaStream_t stream, int num_sms, in
     const int64_t T = f.T, H = f.hidden, I = f.inter;
     if (T <= ffn::kFewRows && !f.gu && H <= MOE_MATVEC_MAX_K && I <= MOE_MATVEC_MAX_K) {
         Matvec m = {f.x, f.x_stride, 1, nullptr, f.T, f.hidden, 1, f.inter, f.w13, nullptr, nullptr,
-                    Matvec::kBf16, true, f.h, 1, f.status, false};
+                    Matvec::kBf16, true, f.h, 1, f.status, f.wait_limit_ns, false};
         moe_status st = launch_matvec(m, stream, num_sms);
         if (st != MOE_OK) return st;
         m = {f.h, I, 1, nullptr, f.T, f.inter, 1, f.hidden, f.w2, nullptr, nullptr,
-             Matvec::kBf16, false, f.out, f.out_bf16, f.status, true};
+             Matvec::kBf16, false, f.out, f.out_bf16, f.status, f.wait_limit_ns, true};
         *launches = 2;
         return launch_matvec(m, stream, num_sms);
     }

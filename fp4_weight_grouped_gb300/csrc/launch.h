@@ -179,6 +179,7 @@ struct Matvec {
     void *out;
     int out_bf16;
     int *status;
+    uint64_t wait_limit_ns;
     bool chained;                 // x comes from the launch before: may start under its end
 };
 moe_status launch_matvec(const Matvec &m, cudaStream_t stream, int num_sms);

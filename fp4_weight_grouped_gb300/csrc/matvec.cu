@@ -22,16 +22,21 @@
 //    2^15 * 6 * 32 a block, 1,024 blocks) below 2^127 for every scale that the format has;
 //    scales below 2^-118 underflow to 0 for it.
 //    NVFP4: e2m1 * e4m3 has 6 bits and fits f16, so the scale goes into the weight.
-//  * Each warp fetches its own stages with cp.async, kDepth ahead, across tiles: no
-//    barriers to wait for and nothing to hang on.
+//  * Each warp fetches its own stages by TMA into its own ring, a few ahead and across
+//    tiles.  (By cp.async the copies took half of the shared-memory pipe: they write a
+//    sector at a time.)  A wait that gives up records it, and the warp goes on without.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
 #include <atomic>
 
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include "device_common.cuh"
 #include "launch.h"
+#include "tensor_map.h"
 
 namespace moe {
 namespace mv {
@@ -40,17 +45,18 @@ enum Format { kMx, kNv, kBf16 };
 
 constexpr int kWarps = 16, kThreads = 32 * kWarps;
 constexpr int kTok = 8;                       // rows a chunk at most (the MMA's n)
+constexpr int kTileRows = 32;                 // weight rows a tile: two MMAs' share one load of x
 constexpr int kRowBytes = 64;                 // of a weight row in a stage
-constexpr int kTileFloats = 16 * kTok;        // sums of a tile
+constexpr int kTileFloats = kTileRows * kTok; // sums of a tile
 
 template <int F>
 struct Fmt {
     static constexpr int kUnit = F == kBf16 ? 32 : 128;             // k of a stage
-    // A row in a stage: MXFP4 is read by words, the others by 16 bytes; both free of conflicts.
-    static constexpr int kPitch = F == kMx ? 80 : 64;
-    static constexpr int kScaleWords = F == kMx ? 2 : F == kNv ? 3 : 0;   // a row, any alignment
-    static constexpr int kStage = 16 * kPitch + 64 * kScaleWords;
-    static constexpr int kDepth = F == kBf16 ? 8 : 6;
+    // Scales come 16 bytes a row, the stage's and its neighbours'.
+    static constexpr int kScaleBytes = F == kMx ? 4 : F == kNv ? 8 : 0;   // of a row in a stage
+    static constexpr int kScales = F == kBf16 ? 0 : 16 * kTileRows;
+    static constexpr int kStage = kTileRows * kRowBytes + kScales;
+    static constexpr int kDepth = F == kBf16 ? 5 : 3, kDeep = F == kBf16 ? 6 : 4;   // stages (see launch)
 };
 
 struct Params {
@@ -65,20 +71,11 @@ struct Params {
     int out_bf16;
     int *status;
     int tok;                      // rows a chunk, 1..kTok
+    int depth;                    // stages of a warp's ring
     int k_pad;                    // K up to a stage
     int x_vec;                    // x rows at 16-byte addresses
+    uint64_t wait_limit_ns;
 };
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool real) {
-    const int n = real ? 16 : 0;
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
     uint32_t v;
@@ -88,11 +85,6 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
 __device__ __forceinline__ uint32_t lds16(uint32_t a) {
     uint16_t v;
     asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ uint32_t lds8(uint32_t a) {
-    uint32_t v;
-    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
     return v;
 }
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
@@ -233,79 +225,96 @@ __device__ __forceinline__ void build_chunks(const Params &p, const Chunks &c) {
     __syncthreads();
 }
 
-// The chunk's rows of x into shared memory (f16, scaled by 2^-e; bf16 as they are), zeros up
-// to k_pad.  exps[t] receives e.  Everyone is past its last use of x when this is called.
-// NVFP4: within 128 k, 16 bytes q go to place 4 (q % 4) + q / 4, where the lanes that hold
-// 32 k each find theirs side by side.
-template <int F>
-__device__ __forceinline__ void stage_x(const Params &p, const int *slots, int n, uint8_t *xs, int pitch, int *exps) {
-    const int tid = threadIdx.x, vecs = p.k_pad / 8;
-    const auto load = [&](const uint16_t *row, int v) {
-        uint4 a = make_uint4(0, 0, 0, 0);
-        if (8 * v < p.K) {            // K is a multiple of 8
-            if (p.x_vec) {
-                a = __ldg(reinterpret_cast<const uint4 *>(row) + v);
-            } else {
-                const uint16_t *q = row + 8 * v;
-                a.x = __ldg(q) | static_cast<uint32_t>(__ldg(q + 1)) << 16;
-                a.y = __ldg(q + 2) | static_cast<uint32_t>(__ldg(q + 3)) << 16;
-                a.z = __ldg(q + 4) | static_cast<uint32_t>(__ldg(q + 5)) << 16;
-                a.w = __ldg(q + 6) | static_cast<uint32_t>(__ldg(q + 7)) << 16;
-            }
+// Power of two that a row of x is scaled by, from the exponent field of its largest magnitude.
+__device__ __forceinline__ int row_exponent(int top) { return max(top - 127 - 14, -126); }
+
+// Eight elements of a row of x; zeros past its end.
+__device__ __forceinline__ uint4 load_x(const Params &p, int slot, int v) {
+    uint4 a = make_uint4(0, 0, 0, 0);
+    if (8 * v < p.K) {                // K is a multiple of 8
+        const uint16_t *q = p.x + (slot / p.div) * p.x_stride + 8 * v;
+        if (p.x_vec) {
+            a = __ldg(reinterpret_cast<const uint4 *>(q));
+        } else {
+            a.x = __ldg(q) | static_cast<uint32_t>(__ldg(q + 1)) << 16;
+            a.y = __ldg(q + 2) | static_cast<uint32_t>(__ldg(q + 3)) << 16;
+            a.z = __ldg(q + 4) | static_cast<uint32_t>(__ldg(q + 5)) << 16;
+            a.w = __ldg(q + 6) | static_cast<uint32_t>(__ldg(q + 7)) << 16;
         }
-        return a;
-    };
-    if constexpr (F == kBf16) {
-        for (int t = 0; t < n; ++t) {
-            const uint16_t *row = p.x + (slots[t] / p.div) * p.x_stride;
-            for (int v = tid; v < vecs; v += kThreads)
-                *reinterpret_cast<uint4 *>(xs + t * pitch + 16 * v) = load(row, v);
-        }
-        __syncthreads();
-        return;
-    } else {
-        if (tid < kTok) exps[tid] = 0;
-        __syncthreads();
-        // Largest finite magnitude of every row, by its exponent field.
-        for (int t = 0; t < n; ++t) {
-            const uint16_t *row = p.x + (slots[t] / p.div) * p.x_stride;
-            uint32_t top = 0;
-            for (int v = tid; v < vecs; v += kThreads) {
-                const uint4 a = load(row, v);
-                const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t lo = w[i] & 0x7F80u, hi = w[i] >> 16 & 0x7F80u;
-                    top = max(top, lo == 0x7F80u ? 0u : lo);
-                    top = max(top, hi == 0x7F80u ? 0u : hi);
-                }
-            }
-            top = __reduce_max_sync(0xffffffffu, top);
-            if ((tid & 31) == 0) atomicMax(&exps[t], static_cast<int>(top >> 7));
-        }
-        __syncthreads();
-        for (int t = 0; t < n; ++t) {
-            const uint16_t *row = p.x + (slots[t] / p.div) * p.x_stride;
-            const int e = max(exps[t] - 127 - 14, -126);
-            const float f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-            for (int v = tid; v < vecs; v += kThreads) {
-                const uint4 a = load(row, v);
-                const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-                uint32_t o[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    asm("cvt.rn.f16x2.f32 %0, %1, %2;"
-                        : "=r"(o[i])
-                        : "f"(__uint_as_float(w[i] & 0xFFFF0000u) * f), "f"(__uint_as_float(w[i] << 16) * f));
-                const int at = F == kNv ? (v & ~15) | (v & 3) << 2 | (v >> 2 & 3) : v;
-                *reinterpret_cast<uint4 *>(xs + t * pitch + 16 * at) = make_uint4(o[0], o[1], o[2], o[3]);
-            }
-        }
-        __syncthreads();
-        // Only now: every thread has read the field above.
-        if (tid < n) exps[tid] = max(exps[tid] - 127 - 14, -126);
-        __syncthreads();
     }
+    return a;
+}
+
+// Largest exponent field among the finite ones of eight elements.
+__device__ __forceinline__ uint32_t top_of(const uint4 &a) {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = w[i] & 0x7F80u, hi = w[i] >> 16 & 0x7F80u;
+        top = max(top, lo == 0x7F80u ? 0u : lo);
+        top = max(top, hi == 0x7F80u ? 0u : hi);
+    }
+    return top >> 7;
+}
+
+template <int F>
+__device__ __forceinline__ void store_x(uint8_t *row, int v, const uint4 &a, int top) {
+    if constexpr (F == kBf16) {
+        *reinterpret_cast<uint4 *>(row + 16 * v) = a;
+    } else {
+        const float f = __uint_as_float(static_cast<uint32_t>(127 - row_exponent(top)) << 23);
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            asm("cvt.rn.f16x2.f32 %0, %1, %2;"
+                : "=r"(o[i])
+                : "f"(__uint_as_float(w[i] & 0xFFFF0000u) * f), "f"(__uint_as_float(w[i] << 16) * f));
+        const int at = F == kNv ? (v & ~15) | (v & 3) << 2 | (v >> 2 & 3) : v;
+        *reinterpret_cast<uint4 *>(row + 16 * at) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+}
+
+// The chunk's rows of x into shared memory (4-bit weights: f16, scaled by 2^-row_exponent;
+// bf16 as they are), zeros up to k_pad.  tops[t] (zero before) receives row t's largest
+// exponent field.  NVFP4: within 128 k, 16 bytes q go to place 4 (q % 4) + q / 4, where the
+// lanes that hold 32 k each find theirs side by side.
+template <int F>
+__device__ __forceinline__ void stage_x(const Params &p, const int *slots, int n, uint8_t *xs, int pitch, int *tops) {
+    const int tid = threadIdx.x, vecs = p.k_pad / 8;
+    if (vecs <= kThreads) {           // one load a row and thread
+        uint4 a[kTok];
+#pragma unroll
+        for (int t = 0; t < kTok; ++t)
+            if (t < n && tid < vecs) a[t] = load_x(p, slots[t], tid);
+        if constexpr (F != kBf16) {
+#pragma unroll
+            for (int t = 0; t < kTok; ++t) {
+                if (t >= n) break;
+                const uint32_t top = __reduce_max_sync(0xffffffffu, tid < vecs ? top_of(a[t]) : 0u);
+                if ((tid & 31) == 0) atomicMax(&tops[t], static_cast<int>(top));
+            }
+            __syncthreads();
+        }
+#pragma unroll
+        for (int t = 0; t < kTok; ++t)
+            if (t < n && tid < vecs) store_x<F>(xs + t * pitch, tid, a[t], F == kBf16 ? 0 : tops[t]);
+    } else {
+        if constexpr (F != kBf16) {
+            for (int t = 0; t < n; ++t) {
+                uint32_t top = 0;
+                for (int v = tid; v < vecs; v += kThreads) top = max(top, top_of(load_x(p, slots[t], v)));
+                top = __reduce_max_sync(0xffffffffu, top);
+                if ((tid & 31) == 0) atomicMax(&tops[t], static_cast<int>(top));
+            }
+            __syncthreads();
+        }
+        for (int t = 0; t < n; ++t)
+            for (int v = tid; v < vecs; v += kThreads)
+                store_x<F>(xs + t * pitch, v, load_x(p, slots[t], v), F == kBf16 ? 0 : tops[t]);
+    }
+    __syncthreads();
 }
 
 // How many warps share a tile's K: a tile's sums are joined across them behind a barrier, so
@@ -324,100 +333,139 @@ __device__ __forceinline__ int choose_kw(uint32_t tiles, uint32_t units) {
     return best;
 }
 
-// One stage (128 k; bf16: 32) of 16 weight rows: acc += w x.
-template <int F, bool kShift>
-__device__ __forceinline__ void multiply(uint32_t at, uint32_t xa, bool has_x, int blocks, int g, int t4,
-                                         const uint32_t (&off)[2], float (&acc)[4], uint32_t (&bad)[2]) {
-    using C = Fmt<F>;
-    const uint4 zero = make_uint4(0, 0, 0, 0);
+// 16 bytes where `real`, else what v holds already.
+__device__ __forceinline__ void lds128_if(uint4 &v, uint32_t a, bool real) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+                 "@p ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+                 : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
+                 : "r"(a), "r"(static_cast<int>(real)));
+}
+
+// Scale bytes of a stage, of the four rows that a lane multiplies: MXFP4 one word a row,
+// NVFP4 the two bytes of the lane's 32 k.
+using Scales = uint32_t[2][2];
+
+// Rows of scales that TMA does not take (not a multiple of 16 bytes, or elsewhere aligned):
+// byte by byte from global memory, zeros past the row's end.
+template <int F>
+__device__ __forceinline__ void load_scales(const uint8_t *const (&rows)[2][2], int unit, int t4, int row_bytes, Scales &v) {
+    constexpr int n = F == kMx ? 4 : 2;
+    const int at = F == kMx ? 4 * unit : 8 * unit + 2 * t4;
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            v[s][r] = 0;
+#pragma unroll
+            for (int i = 0; i < n; ++i)
+                if (at + i < row_bytes) v[s][r] |= static_cast<uint32_t>(__ldg(rows[s][r] + at + i)) << (8 * i);
+        }
+}
+
+// One stage (128 k; bf16: 32) of 32 weight rows: acc += w x.  A row's 16-byte pieces lie in
+// the 64-byte swizzle; `at` is row g's piece 0 with it.  `step`: bytes from row g of an MMA
+// to row g + 8, `next` to the second MMA's.  x: this lane's share of the chunk's rows, zeros
+// in lanes without one.
+template <int F>
+__device__ __forceinline__ void multiply(uint32_t at, int step, int next, uint32_t xa, bool has_x, int t4,
+                                         const Scales &sw, uint4 (&x)[4], float (&acc)[2][4], Scales &bad) {
     if constexpr (F == kBf16) {
-        const uint4 a = lds128(at + g * C::kPitch + t4 * 16), c = lds128(at + (g + 8) * C::kPitch + t4 * 16);
-        const uint4 v = has_x ? lds128(xa) : zero;
-        mma16816<false>(acc, a.x, c.x, a.y, c.y, v.x, v.y);
-        mma16816<false>(acc, a.z, c.z, a.w, c.w, v.z, v.w);
+        lds128_if(x[0], xa, has_x);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const uint32_t row = (at ^ (16 * t4)) + s * next;
+            const uint4 a = lds128(row), c = lds128(row + step);
+            mma16816<false>(acc[s], a.x, c.x, a.y, c.y, x[0].x, x[0].y);
+            mma16816<false>(acc[s], a.z, c.z, a.w, c.w, x[0].z, x[0].w);
+        }
     } else if constexpr (F == kNv) {
         // Lane t4 holds the 32 k of block t4, two scales a row.
-        const uint4 ra = lds128(at + g * C::kPitch + 16 * t4), rc = lds128(at + (g + 8) * C::kPitch + 16 * t4);
-        uint4 v[4];
+        uint4 ra[2], rc[2];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = has_x ? lds128(xa + 64 * j) : zero;
-        uint32_t b[2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const uint32_t sa = at + 16 * C::kPitch + (g + 8 * r) * 4 * C::kScaleWords + 2 * t4;
-            b[r] = kShift ? lds8(sa + off[r]) | lds8(sa + off[r] + 1) << 8 : lds16(sa);
-            if (t4 >= blocks) b[r] = 0;               // past the row's end
+        for (int s = 0; s < 2; ++s) {
+            const uint32_t row = (at ^ (16 * t4)) + s * next;
+            ra[s] = lds128(row);
+            rc[s] = lds128(row + step);
         }
-        bad[0] |= (((b[0] | b[1] << 16) & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;     // NaN
-        uint32_t s[2][2];
-        e4m3_pairs(b[0], s[0][0], s[0][1]);
-        e4m3_pairs(b[1], s[1][0], s[1][1]);
-        const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wc[4] = {rc.x, rc.y, rc.z, rc.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            uint32_t a[4], c[4];
-            decode8(wa[j], a);
-            decode8(wc[j], c);
+        for (int j = 0; j < 4; ++j) lds128_if(x[j], xa + 64 * j, has_x);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                a[i] = hmul2(a[i], s[0][j >> 1]);
-                c[i] = hmul2(c[i], s[1][j >> 1]);
+        for (int s = 0; s < 2; ++s) {
+            bad[0][0] |= (((sw[s][0] | sw[s][1] << 16) & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;     // NaN
+            uint32_t f[2][2];
+            e4m3_pairs(sw[s][0], f[0][0], f[0][1]);
+            e4m3_pairs(sw[s][1], f[1][0], f[1][1]);
+            const uint32_t wa[4] = {ra[s].x, ra[s].y, ra[s].z, ra[s].w}, wc[4] = {rc[s].x, rc[s].y, rc[s].z, rc[s].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t a[4], c[4];
+                decode8(wa[j], a);
+                decode8(wc[j], c);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    a[i] = hmul2(a[i], f[0][j >> 1]);
+                    c[i] = hmul2(c[i], f[1][j >> 1]);
+                }
+                mma16816<true>(acc[s], a[0], c[0], a[1], c[1], x[j].x, x[j].y);
+                mma16816<true>(acc[s], a[2], c[2], a[3], c[3], x[j].z, x[j].w);
             }
-            mma16816<true>(acc, a[0], c[0], a[1], c[1], v[j].x, v[j].y);
-            mma16816<true>(acc, a[2], c[2], a[3], c[3], v[j].z, v[j].w);
         }
     } else {
-        uint32_t wa[4], wc[4], sw[2];
-        uint4 v[4];
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            wa[b] = lds32(at + g * C::kPitch + 16 * b + 4 * t4);
-            wc[b] = lds32(at + (g + 8) * C::kPitch + 16 * b + 4 * t4);
-            v[b] = has_x ? lds128(xa + 64 * b) : zero;
-        }
+        for (int s = 0; s < 2; ++s)
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const uint32_t sa = at + 16 * C::kPitch + (g + 8 * r) * 4 * C::kScaleWords;
-            sw[r] = kShift ? __funnelshift_r(lds32(sa), lds32(sa + 4), 8 * off[r]) : lds32(sa);
-            if (blocks < 4) sw[r] &= (1u << (8 * blocks)) - 1;                            // past the row's end
-            bad[r] |= ((sw[r] & 0x7F7F7F7Fu) + 0x03030303u) & sw[r] & 0x80808080u;        // 253 and more
-        }
+            for (int r = 0; r < 2; ++r)
+                bad[s][r] |= ((sw[s][r] & 0x7F7F7F7Fu) + 0x03030303u) & sw[s][r] & 0x80808080u;         // 253 and more
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            uint32_t a[4], c[4];
-            decode8(wa[b], a);
-            decode8(wc[b], c);
-            float d[4] = {0.f, 0.f, 0.f, 0.f};
-            mma16816<true>(d, a[0], c[0], a[1], c[1], v[b].x, v[b].y);
-            mma16816<true>(d, a[2], c[2], a[3], c[3], v[b].z, v[b].w);
-            const float s0 = __uint_as_float((sw[0] >> (8 * b) & 0xFFu) << 23) * 0x1p-31f;
-            const float s1 = __uint_as_float((sw[1] >> (8 * b) & 0xFFu) << 23) * 0x1p-31f;
-            acc[0] = fmaf(s0, d[0], acc[0]);
-            acc[1] = fmaf(s0, d[1], acc[1]);
-            acc[2] = fmaf(s1, d[2], acc[2]);
-            acc[3] = fmaf(s1, d[3], acc[3]);
-        }
+        for (int b = 0; b < 4; ++b) lds128_if(x[b], xa + 64 * b, has_x);
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const uint32_t row = (at ^ (16 * b)) + 4 * t4 + s * next;
+                uint32_t a[4], c[4];
+                decode8(lds32(row), a);
+                decode8(lds32(row + step), c);
+                float d[4] = {0.f, 0.f, 0.f, 0.f};
+                mma16816<true>(d, a[0], c[0], a[1], c[1], x[b].x, x[b].y);
+                mma16816<true>(d, a[2], c[2], a[3], c[3], x[b].z, x[b].w);
+                const float s0 = __uint_as_float((sw[s][0] >> (8 * b) & 0xFFu) << 23) * 0x1p-31f;
+                const float s1 = __uint_as_float((sw[s][1] >> (8 * b) & 0xFFu) << 23) * 0x1p-31f;
+                acc[s][0] = fmaf(s0, d[0], acc[s][0]);
+                acc[s][1] = fmaf(s0, d[1], acc[s][1]);
+                acc[s][2] = fmaf(s1, d[2], acc[s][2]);
+                acc[s][3] = fmaf(s1, d[3], acc[s][3]);
+            }
     }
 }
 
-template <int F, bool kSwiglu, bool kShift>
-__global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const Params p) {
+template <int F, bool kSwiglu, bool kTmaScales>
+__global__ void __launch_bounds__(kThreads, 1)
+    matvec_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_s, const Params p) {
     using C = Fmt<F>;
-    extern __shared__ __align__(16) uint8_t smem[];
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t4 = lane & 3;
-    const int pitch = p.k_pad * 2 + 64;
-    // ring | sums | x | chunk tables
-    uint8_t *ring = smem + warp * C::kDepth * C::kStage;
-    float *sums = reinterpret_cast<float *>(smem + kWarps * C::kDepth * C::kStage);
-    uint8_t *xs = reinterpret_cast<uint8_t *>(sums + 2 * kWarps * kTileFloats);
-    int *tab = reinterpret_cast<int *>(xs + p.tok * pitch);
-    const Chunks ch = {tab + kTok + 1, tab + kTok + 1 + p.rows, tab + kTok + 2 + 2 * p.rows,
-                       tab + kTok + 2 + 3 * p.rows, tab + kTok};
-    int *exps = tab;
+    const int pitch = p.k_pad * 2 + 64, depth = p.depth;
+    // ring | sums | x | barriers | chunk tables
+    float *sums = reinterpret_cast<float *>(smem + kWarps * depth * C::kStage);
+    uint8_t *xs = reinterpret_cast<uint8_t *>(sums + kWarps * kTileFloats);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(xs + p.tok * pitch) + warp * C::kDeep;
+    int *tab = reinterpret_cast<int *>(xs + p.tok * pitch + kWarps * C::kDeep * sizeof(uint64_t));
+    int *tops = tab;                              // [2][kTok], in turn
+    tab += 2 * kTok;
+    const Chunks ch = {tab + 1, tab + 1 + p.rows, tab + 2 + 2 * p.rows, tab + 2 + 3 * p.rows, tab};
+    if (lane == 0) {
+        for (int i = 0; i < depth; ++i) mbar_init(&bars[i], 1);
+        mbar_fence_init();
+        tma_prefetch_map(&tm_w);
+        if (kTmaScales) tma_prefetch_map(&tm_s);
+    }
+    if (tid < 2 * kTok) tops[tid] = 0;
     build_chunks(p, ch);
 
-    constexpr int kTileCols = kSwiglu ? 8 : 16;
+    constexpr int kTileCols = kSwiglu ? kTileRows / 2 : kTileRows;
     const int tiles = (p.N + kTileCols - 1) / kTileCols;
     const int units = (p.K + C::kUnit - 1) / C::kUnit;
     const int n_chunks = *ch.count;
@@ -429,48 +477,29 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const Params p) {
     const int count = total / grid + (blk < total % grid);
     const int wk = warp % kw, wt = warp / kw;
     const int u0 = units * wk / kw, u1 = units * (wk + 1) / kw;
-    const int64_t w_pitch = F == kBf16 ? 2ll * p.K : p.K / 2;
-    const int64_t s_pitch = F == kMx ? p.K / 32 : p.K / 16;
-    const int64_t w_rows = kSwiglu ? 2ll * p.N : p.N;
-    const int row_bytes = static_cast<int>(w_pitch), scale_bytes = static_cast<int>(s_pitch);
 
-    // Weight row r of this warp's tile; columns past the last read the last one's.
-    const auto weight_row = [&](int chunk, int grp, int r) {
-        const int tile = grp * group + wt;
-        const int n = kSwiglu ? min(tile * 8 + (r & 7), p.N - 1) + (r >= 8 ? p.N : 0) : min(tile * 16 + r, p.N - 1);
-        return ch.expert[chunk] * w_rows + n;
-    };
-    // A stage: lane copies 32 bytes of row lane / 2; lanes 0..15 the scale words of row lane.
-    const uint32_t ring_a = smem_u32(ring);
-    const uint32_t dst0 = ring_a + (lane >> 1) * C::kPitch + (lane & 1) * 32;
-    const uint32_t sdst0 = ring_a + 16 * C::kPitch + (lane & 15) * 4 * C::kScaleWords;
-    constexpr int kScaleBytes = F == kMx ? 4 : 8;
-    const uint8_t *wp = nullptr, *sp = nullptr;
-    int f_left = u0 < u1 ? count : 0, f_unit = u0, f_chunk = n_chunks ? first / groups : 0;
-    int f_grp = n_chunks ? first % groups : 0;
-    const auto fetch_next = [&](int slot) {
+    // A stage: 16 rows and 16 rows more (SwiGLU: 16 gate rows, the 16 up rows of the same
+    // columns), and their scales.  What lies past an expert's rows or a row's end reads as zeros.
+    const uint32_t ring = smem_u32(smem) + warp * depth * C::kStage;
+    int f_left = u0 < u1 ? count : 0, f_unit = u0, f_slot = 0;
+    int f_chunk = count > 0 ? first / groups : 0, f_grp = count > 0 ? first % groups : 0;
+    const auto fetch_next = [&]() {
         if (f_left > 0) {
-            if (f_unit == u0) {
-                wp = p.w + weight_row(f_chunk, f_grp, lane >> 1) * w_pitch + (lane & 1) * 32;
-                if constexpr (F != kBf16) sp = p.scales + weight_row(f_chunk, f_grp, lane & 15) * s_pitch;
-            }
-            const int at = f_unit * kRowBytes;
-            const uint32_t d = dst0 + slot * C::kStage;
-            // A piece past the row's end becomes zeros; its address is not read.
-            const int have = row_bytes - at - (lane & 1) * 32;
-            cp_async16(d, wp + (have > 0 ? at : 0), have > 0);
-            cp_async16(d + 16, wp + (have > 16 ? at + 16 : 0), have > 16);
-            if constexpr (F != kBf16) {
-                if (lane < 16) {
-                    const uint32_t sd = sdst0 + slot * C::kStage;
-                    const uint8_t *src = sp + f_unit * kScaleBytes;
-                    const int bytes = min(scale_bytes - f_unit * kScaleBytes, kScaleBytes);     // of the row here
-                    const int off = kShift ? static_cast<int>(reinterpret_cast<uintptr_t>(src) & 3) : 0;
-#pragma unroll
-                    for (int i = 0; i < (kShift ? C::kScaleWords : C::kScaleWords - 1); ++i)
-                        if (4 * i < off + bytes) cp_async4(sd + 4 * i, src - off + 4 * i);      // words that hold one
+            if (lane == 0) {
+                const int e = ch.expert[f_chunk], n = (f_grp * group + wt) * kTileCols;
+                const uint32_t dst = ring + f_slot * C::kStage;
+                uint64_t *bar = &bars[f_slot];
+                const int z0 = kSwiglu ? 2 * e : e, z1 = kSwiglu ? 2 * e + 1 : e, n1 = kSwiglu ? n : n + 16;
+                mbar_arrive_expect_tx(bar, kTileRows * kRowBytes + (kTmaScales ? C::kScales : 0));
+                tma_load_3d(dst, &tm_w, f_unit * kRowBytes, n, z0, bar);
+                tma_load_3d(dst + 16 * kRowBytes, &tm_w, f_unit * kRowBytes, n1, z1, bar);
+                if constexpr (kTmaScales) {
+                    const int x = f_unit * C::kScaleBytes & ~15;
+                    tma_load_3d(dst + 32 * kRowBytes, &tm_s, x, n, z0, bar);
+                    tma_load_3d(dst + 32 * kRowBytes + 256, &tm_s, x, n1, z1, bar);
                 }
             }
+            f_slot = f_slot + 1 == depth ? 0 : f_slot + 1;
             if (++f_unit == u1) {
                 f_unit = u0;
                 --f_left;
@@ -480,10 +509,9 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const Params p) {
                 }
             }
         }
-        cp_commit();
     };
 #pragma unroll 1
-    for (int i = 0; i < C::kDepth - 1; ++i) fetch_next(i);
+    for (int i = 0; i < depth - 1; ++i) fetch_next();
 
     // Weights and ids do not depend on the launch before (a chain of products); x does, and
     // so do the outputs' readers.
@@ -500,61 +528,98 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const Params p) {
         }
     }
 
-    int slot = 0, slot_in = C::kDepth - 1, buf = 0, n_tok = 0, start = 0;
+    // Rows g and g + 8 of the two MMAs: plain 0..15 and 16..31, SwiGLU gate and up of eight columns.
+    constexpr int kStep = (kSwiglu ? 16 : 8) * kRowBytes, kNext = (kSwiglu ? 8 : 16) * kRowBytes;
+    const uint32_t row0 = ring + g * kRowBytes + (g >> 1 & 3) * 16;
+    const uint32_t scale0 = ring + 32 * kRowBytes + g * 16 + (F == kNv ? 2 * t4 : 0);
+    uint32_t slot = 0, phase = 0;
+    int n_tok = 0, start = 0, turn = 0;
     int chunk = count > 0 ? first / groups : 0, grp = count > 0 ? first % groups : 0;
-    bool fresh = true;
+    bool fresh = true, ok = true;
     uint32_t any_bad = 0;
+    uint4 x[4];
     for (int left = count; left > 0; --left) {
         if (fresh) {
             fresh = false;
             start = ch.first[chunk];
             n_tok = ch.first[chunk + 1] - start;
-            __syncthreads();                      // sums of the last item are read with the old exponents
-            stage_x<F>(p, ch.order + start, n_tok, xs, pitch, exps);
-        }
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
-        uint32_t bad[2] = {0, 0}, off[2] = {0, 0};
-        if constexpr (kShift) {
+            turn ^= kTok;
+            __syncthreads();                      // everyone is past the last x, its sums and exponents
+            stage_x<F>(p, ch.order + start, n_tok, xs, pitch, tops + turn);
+            if (tid < kTok) tops[(turn ^ kTok) + tid] = 0;
 #pragma unroll
-            for (int r = 0; r < 2; ++r)           // a stage's scale bytes are a multiple of 4
-                off[r] = reinterpret_cast<uintptr_t>(p.scales + weight_row(chunk, grp, g + 8 * r) * s_pitch) & 3;
+            for (int i = 0; i < 4; ++i) x[i] = make_uint4(0, 0, 0, 0);
+        }
+        float acc[2][4] = {};
+        Scales bad = {};
+        const uint8_t *srow[2][2] = {};
+        if constexpr (F != kBf16 && !kTmaScales) {
+            const int n = (grp * group + wt) * kTileCols;
+            const int64_t at = static_cast<int64_t>(ch.expert[chunk]) * (kSwiglu ? 2 : 1) * p.N;
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {     // columns past the last: the last one's
+                    const int c = kSwiglu ? min(n + 8 * s + g, p.N - 1) + r * p.N : min(n + 16 * s + 8 * r + g, p.N - 1);
+                    srow[s][r] = p.scales + (at + c) * (p.K / (F == kMx ? 32 : 16));
+                }
         }
         uint32_t xa = smem_u32(xs) + min(g, n_tok - 1) * pitch + t4 * 16 + u0 * (F == kBf16 ? 64 : 256);
 #pragma unroll 1
-        for (int unit = u0; unit < u1; ++unit) {
-            cp_wait<C::kDepth - 2>();
-            __syncwarp();                         // all lanes' copies; and the slot to fill is read
-            fetch_next(slot_in);
-            multiply<F, kShift>(ring_a + slot * C::kStage, xa, g < n_tok, F == kBf16 ? 1 : (p.K - unit * 128) >> 5, g, t4,
-                                off, acc, bad);
+        for (int unit = u0; ok && unit < u1; ++unit) {
+            Scales sw = {};
+            if constexpr (F != kBf16 && !kTmaScales) load_scales<F>(srow, unit, t4, p.K / (F == kMx ? 32 : 16), sw);
+            __syncwarp();                         // the slot to fill is read by all
+            fetch_next();
+            ok = warp_wait_bounded(&bars[slot], phase, nullptr, p.status, p.wait_limit_ns);
+            if (!ok) break;
+            if constexpr (F != kBf16 && kTmaScales) {
+                const uint32_t sa = scale0 + slot * C::kStage + (unit * C::kScaleBytes & 15);
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const uint32_t a = sa + (kSwiglu ? 8 * s + 16 * r : 16 * s + 8 * r) * 16;
+                        sw[s][r] = F == kMx ? lds32(a) : lds16(a);
+                    }
+            }
+            multiply<F>(row0 + slot * C::kStage, kStep, kNext, xa, g < n_tok, t4, sw, x, acc, bad);
             xa += F == kBf16 ? 64 : 256;
-            slot = slot + 1 == C::kDepth ? 0 : slot + 1;
-            slot_in = slot_in + 1 == C::kDepth ? 0 : slot_in + 1;
+            slot = slot + 1 == depth ? 0 : slot + 1;
+            phase ^= slot == 0;
         }
         if constexpr (F == kMx) {
             const float nan = __uint_as_float(0x7FC00000u);
-            if (bad[0]) acc[0] = acc[1] = nan;
-            if (bad[1]) acc[2] = acc[3] = nan;
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                if (bad[s][0]) acc[s][0] = acc[s][1] = nan;
+                if (bad[s][1]) acc[s][2] = acc[s][3] = nan;
+            }
         }
-        any_bad |= bad[0] | bad[1];
-        float *mine = sums + (buf * kWarps + warp) * kTileFloats;
-        *reinterpret_cast<float2 *>(mine + g * kTok + 2 * t4) = make_float2(acc[0], acc[1]);
-        *reinterpret_cast<float2 *>(mine + (g + 8) * kTok + 2 * t4) = make_float2(acc[2], acc[3]);
+        any_bad |= bad[0][0] | bad[0][1] | bad[1][0] | bad[1][1];
+        __syncthreads();                          // the last item's sums are read
+        float *mine = sums + warp * kTileFloats;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            *reinterpret_cast<float2 *>(mine + (16 * s + g) * kTok + 2 * t4) = make_float2(acc[s][0], acc[s][1]);
+            *reinterpret_cast<float2 *>(mine + (16 * s + g + 8) * kTok + 2 * t4) = make_float2(acc[s][2], acc[s][3]);
+        }
         __syncthreads();
         // Everyone adds up its outputs over the warps that shared the tile, in order.
         constexpr int kOuts = kTileCols * kTok;
         for (int i = tid; i < group * kOuts; i += kThreads) {
-            const int tile = i / kOuts, r = i % kOuts / kTok, t = i % kTok;
-            const int n = (grp * group + tile) * kTileCols + r;
+            const int tile = i / kOuts, c = i % kOuts / kTok, t = i % kTok;
+            const int n = (grp * group + tile) * kTileCols + c;
             if (t >= n_tok || n >= p.N) continue;
-            const float *q = sums + (buf * kWarps + tile * kw) * kTileFloats + r * kTok + t;
+            const int r = kSwiglu ? (c & 8) * 2 + (c & 7) : c;
+            const float *q = sums + tile * kw * kTileFloats + r * kTok + t;
             float v = 0.f, u = 0.f;
             for (int j = 0; j < kw; ++j) {
                 v += q[j * kTileFloats];
                 if (kSwiglu) u += q[j * kTileFloats + 8 * kTok];
             }
             if constexpr (F != kBf16) {
-                const int e = exps[t] + (F == kMx ? 31 : 0);
+                const int e = row_exponent(tops[turn + t]) + (F == kMx ? 31 : 0);
                 const float s2 = F == kNv ? __ldg(p.ws2 + ch.expert[chunk]) : 1.0f;
                 const auto whole = [&](float a) {
                     return e > 0 ? ldexpf(a * s2, e) : ldexpf(a, e) * s2;
@@ -567,14 +632,20 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const Params p) {
             if (kSwiglu || p.out_bf16) static_cast<__nv_bfloat16 *>(p.out)[o] = __float2bfloat16_rn(v);
             else static_cast<float *>(p.out)[o] = v;
         }
-        buf ^= 1;
         if (++grp == groups) {
             grp = 0;
             ++chunk;
             fresh = true;
         }
     }
-    cp_wait<0>();
+    // After a wait that gave up: what was issued, from that stage on, lands before the CTA leaves.
+    if (!ok) {
+        do {
+            if (!warp_wait_bounded(&bars[slot], phase, nullptr, p.status, p.wait_limit_ns)) break;
+            slot = slot + 1 == static_cast<uint32_t>(depth) ? 0 : slot + 1;
+            phase ^= slot == 0;
+        } while (slot != static_cast<uint32_t>(f_slot));
+    }
     if constexpr (F != kBf16)
         if (__any_sync(0xffffffffu, any_bad != 0) && lane == 0) set_status(p.status, MOE_ERR_DATA);
 }
@@ -597,22 +668,42 @@ __global__ void weigh_kernel(const float *y, const int32_t *ids, const float *w,
 
 constexpr int kMaxSmem = 232448;
 
-template <int F, bool kSwiglu, bool kShift>
+// Rows [outer][rows][bytes] in boxes of box_bytes by 16 rows; what lies past an end reads as zeros.
+bool encode(CUtensorMap *map, const void *base, int64_t bytes, int64_t rows, int64_t outer, uint32_t box_bytes, bool swizzle) {
+    PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encode();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(bytes), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(outer)};
+    cuuint64_t strides[2] = {dims[0], dims[0] * dims[1]};
+    cuuint32_t box[3] = {box_bytes, 16, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int F, bool kSwiglu, bool kTmaScales>
 moe_status launch(Params p, bool chained, cudaStream_t stream, int num_sms) {
     using C = Fmt<F>;
     p.k_pad = (p.K + C::kUnit - 1) / C::kUnit * C::kUnit;
-    const size_t fixed = kWarps * C::kDepth * C::kStage + 2 * kWarps * kTileFloats * sizeof(float) +
-                         (kTok + 2 + 4 * static_cast<size_t>(p.rows)) * sizeof(int);
     const size_t pitch = static_cast<size_t>(p.k_pad) * 2 + 64;
+    const size_t rest = 1024 + kWarps * kTileFloats * sizeof(float) + kWarps * C::kDeep * sizeof(uint64_t) +
+                        (2 * kTok + 2 + 4 * static_cast<size_t>(p.rows)) * sizeof(int);
+    const auto smem = [&](int depth, int tok) { return static_cast<size_t>(kWarps * depth * C::kStage) + rest + tok * pitch; };
     p.tok = p.rows < kTok ? p.rows : kTok;
-    while (p.tok > 1 && fixed + p.tok * pitch > kMaxSmem) p.tok = (p.tok + 1) / 2;
-    const size_t bytes = fixed + p.tok * pitch;
+    p.depth = smem(C::kDeep, p.tok) <= kMaxSmem ? C::kDeep : C::kDepth;
+    while (p.tok > 1 && smem(p.depth, p.tok) > kMaxSmem) p.tok = (p.tok + 1) / 2;
+    const size_t bytes = smem(p.depth, p.tok);
     if (bytes > kMaxSmem) return MOE_ERR_CAPACITY;
+    CUtensorMap tm_w, tm_s;
+    const int64_t outer = static_cast<int64_t>(p.E) * (kSwiglu ? 2 : 1);
+    if (!encode(&tm_w, p.w, F == kBf16 ? 2ll * p.K : p.K / 2, p.N, outer, kRowBytes, true)) return MOE_ERR_CUDA;
+    tm_s = tm_w;
+    if (kTmaScales && !encode(&tm_s, p.scales, p.K / (F == kMx ? 32 : 16), p.N, outer, 16, false)) return MOE_ERR_CUDA;
     static std::atomic<uint64_t> mask{0};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
     const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
-    const auto kernel = matvec_kernel<F, kSwiglu, kShift>;
+    const auto kernel = matvec_kernel<F, kSwiglu, kTmaScales>;
     if (!bit || !(mask.load(std::memory_order_acquire) & bit)) {
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) != cudaSuccess)
             return MOE_ERR_CUDA;
@@ -628,7 +719,7 @@ moe_status launch(Params p, bool chained, cudaStream_t stream, int num_sms) {
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = chained ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, kernel, tm_w, tm_s, p) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // namespace mv
@@ -650,14 +741,14 @@ moe_status launch_matvec(const Matvec &m, cudaStream_t stream, int num_sms) {
     p.out = m.out;
     p.out_bf16 = m.out_bf16;
     p.status = m.status;
+    p.wait_limit_ns = m.wait_limit_ns;
     p.x_vec = reinterpret_cast<uintptr_t>(m.x) % 16 == 0 && (m.x_stride % 8 == 0 || m.rows <= m.index_div);
     if (m.format == Matvec::kBf16)
         return m.swiglu ? mv::launch<mv::kBf16, true, false>(p, m.chained, stream, num_sms)
                         : mv::launch<mv::kBf16, false, false>(p, m.chained, stream, num_sms);
     const bool nv = m.format == Matvec::kNv;
-    // Scale rows at 4-byte addresses are copied as they are; others as the words around them.
-    const bool shift = (m.K / (nv ? 16 : 32)) % 4 != 0 || reinterpret_cast<uintptr_t>(m.scales) % 4 != 0;
-    if (shift)
+    // Rows of scales that TMA takes: a multiple of 16 bytes, at 16-byte addresses.
+    if (m.K / (nv ? 16 : 32) % 16 == 0 && reinterpret_cast<uintptr_t>(m.scales) % 16 == 0)
         return nv ? m.swiglu ? mv::launch<mv::kNv, true, true>(p, m.chained, stream, num_sms)
                              : mv::launch<mv::kNv, false, true>(p, m.chained, stream, num_sms)
                   : m.swiglu ? mv::launch<mv::kMx, true, true>(p, m.chained, stream, num_sms)
