@@ -7,9 +7,9 @@
 //
 //  * Rows of the same expert are taken together, up to 8 at a time (a chunk), so a
 //    weight is read once for them.  Every CTA works the chunks out from the ids itself.
-//  * A tile is 16 weight rows (SwiGLU: 8 gate and the 8 matching up rows, so that one
-//    thread finds both).  The warps of a CTA share the tile's K, 128 k (bf16: 32) a
-//    stage, and add up their sums in shared memory in a fixed order.
+//  * A tile is 32 weight rows (SwiGLU: 16 gate rows and the 16 matching up rows, so that one
+//    thread finds both).  kw warps of a CTA share a tile's K, 256 k (bf16: 64) a stage, and
+//    add up their sums in shared memory in a fixed order.
 //  * mma.sync m16n8k16 with the weights as A and the chunk's rows as B columns: eight
 //    rows cost what one costs, and a thread's four sums are f32.  Tensor memory has
 //    nothing to offer here: no operand is used twice.
@@ -22,9 +22,10 @@
 //    2^15 * 6 * 32 a block, 1,024 blocks) below 2^127 for every scale that the format has;
 //    scales below 2^-118 underflow to 0 for it.
 //    NVFP4: e2m1 * e4m3 has 6 bits and fits f16, so the scale goes into the weight.
-//  * Each warp fetches its own stages by TMA into its own ring, a few ahead and across
-//    tiles.  (By cp.async the copies took half of the shared-memory pipe: they write a
-//    sector at a time.)  A wait that gives up records it, and the warp goes on without.
+//  * Each warp fetches its own stages by TMA into its own ring, across tiles: 128 bytes of 32
+//    rows a box (a box costs an SM at least 33 ns: boxes of 64 bytes by 16 rows, and scales
+//    in boxes of their own beside them, held the kernel at 4.4 TB/s; by cp.async the copies'
+//    writes took half of the shared-memory pipe).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -32,7 +33,6 @@
 #include <atomic>
 
 #include <cuda.h>
-#include <cudaTypedefs.h>
 
 #include "device_common.cuh"
 #include "launch.h"
@@ -46,17 +46,15 @@ enum Format { kMx, kNv, kBf16 };
 constexpr int kWarps = 16, kThreads = 32 * kWarps;
 constexpr int kTok = 8;                       // rows a chunk at most (the MMA's n)
 constexpr int kTileRows = 32;                 // weight rows a tile: two MMAs' share one load of x
-constexpr int kRowBytes = 64;                 // of a weight row in a stage
-constexpr int kTileFloats = kTileRows * kTok; // sums of a tile
+constexpr int kMaxDepth = 4;
+constexpr int kSumPitch = 36;                 // floats of a token's 32 sums, free of bank conflicts
 
 template <int F>
 struct Fmt {
-    static constexpr int kUnit = F == kBf16 ? 32 : 128;             // k of a stage
-    // Scales come 16 bytes a row, the stage's and its neighbours'.
-    static constexpr int kScaleBytes = F == kMx ? 4 : F == kNv ? 8 : 0;   // of a row in a stage
-    static constexpr int kScales = F == kBf16 ? 0 : 16 * kTileRows;
-    static constexpr int kStage = kTileRows * kRowBytes + kScales;
-    static constexpr int kDepth = F == kBf16 ? 5 : 3, kDeep = F == kBf16 ? 6 : 4;   // stages (see launch)
+    static constexpr int kUnit = F == kBf16 ? 64 : 256;             // k of a stage: 128 bytes a row
+    // Scales come 16 bytes a row: NVFP4's of a stage, MXFP4's of two.
+    static constexpr int kScaleBytes = F == kMx ? 8 : F == kNv ? 16 : 0;
+    static constexpr int kStage = kTileRows * 128 + (F == kBf16 ? 0 : 16 * kTileRows);
 };
 
 struct Params {
@@ -71,6 +69,7 @@ struct Params {
     int out_bf16;
     int *status;
     int tok;                      // rows a chunk, 1..kTok
+    int kw;                       // warps that share a tile, a power of two
     int depth;                    // stages of a warp's ring
     int k_pad;                    // K up to a stage
     int x_vec;                    // x rows at 16-byte addresses
@@ -317,22 +316,6 @@ __device__ __forceinline__ void stage_x(const Params &p, const int *slots, int n
     __syncthreads();
 }
 
-// How many warps share a tile's K: a tile's sums are joined across them behind a barrier, so
-// few is better, but the CTAs' shares come in items of kWarps / kw tiles.  In units of a
-// stage's time; an item's end costs about two.
-__device__ __forceinline__ int choose_kw(uint32_t tiles, uint32_t units) {
-    uint32_t best = 1, cost = UINT32_MAX;
-    for (uint32_t kw = 1; kw <= kWarps; kw *= 2) {
-        const uint32_t items = (tiles * kw + kWarps - 1) / kWarps;
-        const uint32_t c = (items + gridDim.x - 1) / gridDim.x * ((units + kw - 1) / kw + 2);
-        if (c < cost) {
-            cost = c;
-            best = kw;
-        }
-    }
-    return best;
-}
-
 // 16 bytes where `real`, else what v holds already.
 __device__ __forceinline__ void lds128_if(uint4 &v, uint32_t a, bool real) {
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
@@ -341,16 +324,16 @@ __device__ __forceinline__ void lds128_if(uint4 &v, uint32_t a, bool real) {
                  : "r"(a), "r"(static_cast<int>(real)));
 }
 
-// Scale bytes of a stage, of the four rows that a lane multiplies: MXFP4 one word a row,
-// NVFP4 the two bytes of the lane's 32 k.
+// Scale bytes of half a stage, of the four rows that a lane multiplies: MXFP4 one word a
+// row, NVFP4 the two bytes of the lane's 32 k.
 using Scales = uint32_t[2][2];
 
 // Rows of scales that TMA does not take (not a multiple of 16 bytes, or elsewhere aligned):
 // byte by byte from global memory, zeros past the row's end.
 template <int F>
-__device__ __forceinline__ void load_scales(const uint8_t *const (&rows)[2][2], int unit, int t4, int row_bytes, Scales &v) {
+__device__ __forceinline__ void load_scales(const uint8_t *const (&rows)[2][2], int half, int t4, int row_bytes, Scales &v) {
     constexpr int n = F == kMx ? 4 : 2;
-    const int at = F == kMx ? 4 * unit : 8 * unit + 2 * t4;
+    const int at = F == kMx ? 4 * half : 8 * half + 2 * t4;
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
@@ -362,18 +345,19 @@ __device__ __forceinline__ void load_scales(const uint8_t *const (&rows)[2][2], 
         }
 }
 
-// One stage (128 k; bf16: 32) of 32 weight rows: acc += w x.  A row's 16-byte pieces lie in
-// the 64-byte swizzle; `at` is row g's piece 0 with it.  `step`: bytes from row g of an MMA
-// to row g + 8, `next` to the second MMA's.  x: this lane's share of the chunk's rows, zeros
-// in lanes without one.
-template <int F>
-__device__ __forceinline__ void multiply(uint32_t at, int step, int next, uint32_t xa, bool has_x, int t4,
-                                         const Scales &sw, uint4 (&x)[4], float (&acc)[2][4], Scales &bad) {
+// Half a stage (128 k; bf16: 32) of 32 weight rows: acc += w x.  The rows' 16-byte pieces lie
+// in the 128-byte swizzle (piece ^ row % 8): `at` is, with the swizzle in it, the lane's
+// piece t4 of its first row, or for MXFP4 (read by words of eight rows) word t4 of piece 0.
+// step: bytes from row g of an MMA to row g + 8, next: to the second MMA's.  x: this lane's
+// share of the chunk's rows, zeros in lanes without one.
+template <int F, int kHalf>
+__device__ __forceinline__ void multiply(uint32_t at, int step, int next, uint32_t xa, bool has_x, const Scales &sw,
+                                         uint4 (&x)[4], float (&acc)[2][4], Scales &bad) {
     if constexpr (F == kBf16) {
         lds128_if(x[0], xa, has_x);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            const uint32_t row = (at ^ (16 * t4)) + s * next;
+            const uint32_t row = (at ^ (64 * kHalf)) + s * next;
             const uint4 a = lds128(row), c = lds128(row + step);
             mma16816<false>(acc[s], a.x, c.x, a.y, c.y, x[0].x, x[0].y);
             mma16816<false>(acc[s], a.z, c.z, a.w, c.w, x[0].z, x[0].w);
@@ -383,7 +367,7 @@ __device__ __forceinline__ void multiply(uint32_t at, int step, int next, uint32
         uint4 ra[2], rc[2];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            const uint32_t row = (at ^ (16 * t4)) + s * next;
+            const uint32_t row = (at ^ (64 * kHalf)) + s * next;
             ra[s] = lds128(row);
             rc[s] = lds128(row + step);
         }
@@ -422,7 +406,7 @@ __device__ __forceinline__ void multiply(uint32_t at, int step, int next, uint32
         for (int b = 0; b < 4; ++b)
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                const uint32_t row = (at ^ (16 * b)) + 4 * t4 + s * next;
+                const uint32_t row = (at ^ (64 * kHalf + 16 * b)) + s * next;
                 uint32_t a[4], c[4];
                 decode8(lds32(row), a);
                 decode8(lds32(row + step), c);
@@ -447,57 +431,52 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t4 = lane & 3;
-    const int pitch = p.k_pad * 2 + 64, depth = p.depth;
-    // ring | sums | x | barriers | chunk tables
-    float *sums = reinterpret_cast<float *>(smem + kWarps * depth * C::kStage);
-    uint8_t *xs = reinterpret_cast<uint8_t *>(sums + kWarps * kTileFloats);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(xs + p.tok * pitch) + warp * C::kDeep;
-    int *tab = reinterpret_cast<int *>(xs + p.tok * pitch + kWarps * C::kDeep * sizeof(uint64_t));
+    const int kw = p.kw, group = kWarps / kw, depth = p.depth;          // group: tiles an item
+    const int pitch = p.k_pad * 2 + 64, sum_floats = p.tok * kSumPitch;
+    // ring: stages, all warps' scales behind them | x | sums | barriers | chunk tables
+    uint8_t *xs = smem + kWarps * depth * C::kStage;
+    float *sums = reinterpret_cast<float *>(xs + p.tok * pitch);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sums + kWarps * sum_floats) + warp * kMaxDepth;
+    int *tab = reinterpret_cast<int *>(bars + (kWarps - warp) * kMaxDepth);
     int *tops = tab;                              // [2][kTok], in turn
     tab += 2 * kTok;
     const Chunks ch = {tab + 1, tab + 1 + p.rows, tab + 2 + 2 * p.rows, tab + 2 + 3 * p.rows, tab};
     if (lane == 0) {
         for (int i = 0; i < depth; ++i) mbar_init(&bars[i], 1);
         mbar_fence_init();
-        tma_prefetch_map(&tm_w);
-        if (kTmaScales) tma_prefetch_map(&tm_s);
+        if (warp == 0) {
+            tma_prefetch_map(&tm_w);
+            if (kTmaScales) tma_prefetch_map(&tm_s);
+        }
     }
     if (tid < 2 * kTok) tops[tid] = 0;
     build_chunks(p, ch);
 
     constexpr int kTileCols = kSwiglu ? kTileRows / 2 : kTileRows;
     const int tiles = (p.N + kTileCols - 1) / kTileCols;
-    const int units = (p.K + C::kUnit - 1) / C::kUnit;
-    const int n_chunks = *ch.count;
-    const int kw = choose_kw(n_chunks * tiles, units), group = kWarps / kw;
     const int groups = (tiles + group - 1) / group;          // items a chunk
     // The CTA's share of the items, one after another.  (rows * N < 2^31, so counts fit.)
-    const int total = n_chunks * groups, grid = gridDim.x, blk = blockIdx.x;
+    const int total = *ch.count * groups, grid = gridDim.x, blk = blockIdx.x;
     const int first = total / grid * blk + min(blk, total % grid);
     const int count = total / grid + (blk < total % grid);
-    const int wk = warp % kw, wt = warp / kw;
-    const int u0 = units * wk / kw, u1 = units * (wk + 1) / kw;
+    const int chunk0 = count > 0 ? first / groups : 0, grp0 = count > 0 ? first % groups : 0;
+    const int wk = warp & (kw - 1), wt = warp / kw;
+    const int units = (p.K + C::kUnit - 1) / C::kUnit, u0 = units * wk / kw, u1 = units * (wk + 1) / kw;
 
-    // A stage: 16 rows and 16 rows more (SwiGLU: 16 gate rows, the 16 up rows of the same
-    // columns), and their scales.  What lies past an expert's rows or a row's end reads as zeros.
-    const uint32_t ring = smem_u32(smem) + warp * depth * C::kStage;
-    int f_left = u0 < u1 ? count : 0, f_unit = u0, f_slot = 0;
-    int f_chunk = count > 0 ? first / groups : 0, f_grp = count > 0 ? first % groups : 0;
+    // A stage: 32 rows (SwiGLU: 16 gate rows, the 16 up rows of the same columns) and their
+    // scales.  What lies past an expert's rows or a row's end reads as zeros.
+    const uint32_t ring = smem_u32(smem) + warp * depth * (kTileRows * 128);
+    const uint32_t scale_ring = smem_u32(smem) + kWarps * depth * (kTileRows * 128) + warp * depth * (16 * kTileRows);
+    int f_left = u0 < u1 ? count : 0, f_unit = u0, f_slot = 0, f_chunk = chunk0, f_grp = grp0;
     const auto fetch_next = [&]() {
         if (f_left > 0) {
             if (lane == 0) {
-                const int e = ch.expert[f_chunk], n = (f_grp * group + wt) * kTileCols;
-                const uint32_t dst = ring + f_slot * C::kStage;
+                const int z = ch.expert[f_chunk] * (kSwiglu ? 2 : 1), n = (f_grp * group + wt) * kTileCols;
                 uint64_t *bar = &bars[f_slot];
-                const int z0 = kSwiglu ? 2 * e : e, z1 = kSwiglu ? 2 * e + 1 : e, n1 = kSwiglu ? n : n + 16;
-                mbar_arrive_expect_tx(bar, kTileRows * kRowBytes + (kTmaScales ? C::kScales : 0));
-                tma_load_3d(dst, &tm_w, f_unit * kRowBytes, n, z0, bar);
-                tma_load_3d(dst + 16 * kRowBytes, &tm_w, f_unit * kRowBytes, n1, z1, bar);
-                if constexpr (kTmaScales) {
-                    const int x = f_unit * C::kScaleBytes & ~15;
-                    tma_load_3d(dst + 32 * kRowBytes, &tm_s, x, n, z0, bar);
-                    tma_load_3d(dst + 32 * kRowBytes + 256, &tm_s, x, n1, z1, bar);
-                }
+                mbar_arrive_expect_tx(bar, kTileRows * (kTmaScales ? 128 + 16 : 128));
+                tma_load_3d(ring + f_slot * (kTileRows * 128), &tm_w, f_unit * 128, n, z, bar);
+                if constexpr (kTmaScales)
+                    tma_load_3d(scale_ring + f_slot * (16 * kTileRows), &tm_s, f_unit * C::kScaleBytes & ~15, n, z, bar);
             }
             f_slot = f_slot + 1 == depth ? 0 : f_slot + 1;
             if (++f_unit == u1) {
@@ -511,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     };
 #pragma unroll 1
-    for (int i = 0; i < depth - 1; ++i) fetch_next();
+    for (int i = 0; i < depth; ++i) fetch_next();
 
     // Weights and ids do not depend on the launch before (a chain of products); x does, and
     // so do the outputs' readers.
@@ -528,23 +507,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
 
-    // Rows g and g + 8 of the two MMAs: plain 0..15 and 16..31, SwiGLU gate and up of eight columns.
-    constexpr int kStep = (kSwiglu ? 16 : 8) * kRowBytes, kNext = (kSwiglu ? 8 : 16) * kRowBytes;
-    const uint32_t row0 = ring + g * kRowBytes + (g >> 1 & 3) * 16;
-    const uint32_t scale0 = ring + 32 * kRowBytes + g * 16 + (F == kNv ? 2 * t4 : 0);
-    uint32_t slot = 0, phase = 0;
-    int n_tok = 0, start = 0, turn = 0;
-    int chunk = count > 0 ? first / groups : 0, grp = count > 0 ? first % groups : 0;
+    // MMA rows g and g + 8 are stage rows q and q + 8 of 16 (SwiGLU: gate and up of eight
+    // columns).  Neighbours in g are four rows apart: the eight lanes that read 16 bytes
+    // together then meet eight different pieces of the swizzle.
+    const int q = g >> 1 | (g & 1) << 2;
+    constexpr int kStep = (kSwiglu ? 16 : 8), kNext = (kSwiglu ? 8 : 16);
+    const uint32_t row0 = ring + q * 128 + (F == kMx ? q * 16 + 4 * t4 : (t4 ^ q) * 16);
+    const uint32_t scale0 = scale_ring + q * 16 + (F == kNv ? 2 * t4 : 0);
+    constexpr int kUnitX = 2 * C::kUnit;
+    uint32_t slot = 0, phase = 0, any_bad = 0;
+    int n_tok = 0, start = 0, turn = 0, chunk = chunk0, grp = grp0;
     bool fresh = true, ok = true;
-    uint32_t any_bad = 0;
     uint4 x[4];
     for (int left = count; left > 0; --left) {
-        if (fresh) {
+        if (fresh) {                              // everyone is past the last x
             fresh = false;
             start = ch.first[chunk];
             n_tok = ch.first[chunk + 1] - start;
+            if (left != count) __syncthreads();   // and past its exponents
             turn ^= kTok;
-            __syncthreads();                      // everyone is past the last x, its sums and exponents
             stage_x<F>(p, ch.order + start, n_tok, xs, pitch, tops + turn);
             if (tid < kTok) tops[(turn ^ kTok) + tid] = 0;
 #pragma unroll
@@ -560,32 +541,39 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int s = 0; s < 2; ++s)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {     // columns past the last: the last one's
-                    const int c = kSwiglu ? min(n + 8 * s + g, p.N - 1) + r * p.N : min(n + 16 * s + 8 * r + g, p.N - 1);
+                    const int c = kSwiglu ? min(n + 8 * s + q, p.N - 1) + r * p.N : min(n + 16 * s + 8 * r + q, p.N - 1);
                     srow[s][r] = p.scales + (at + c) * (p.K / (F == kMx ? 32 : 16));
                 }
         }
-        uint32_t xa = smem_u32(xs) + min(g, n_tok - 1) * pitch + t4 * 16 + u0 * (F == kBf16 ? 64 : 256);
+        uint32_t xa = smem_u32(xs) + min(g, n_tok - 1) * pitch + t4 * 16 + u0 * kUnitX;
 #pragma unroll 1
         for (int unit = u0; ok && unit < u1; ++unit) {
-            Scales sw = {};
-            if constexpr (F != kBf16 && !kTmaScales) load_scales<F>(srow, unit, t4, p.K / (F == kMx ? 32 : 16), sw);
-            __syncwarp();                         // the slot to fill is read by all
-            fetch_next();
+            Scales sw[2] = {};
+            if constexpr (F != kBf16 && !kTmaScales) {
+                load_scales<F>(srow, 2 * unit, t4, p.K / (F == kMx ? 32 : 16), sw[0]);
+                load_scales<F>(srow, 2 * unit + 1, t4, p.K / (F == kMx ? 32 : 16), sw[1]);
+            }
             ok = warp_wait_bounded(&bars[slot], phase, nullptr, p.status, p.wait_limit_ns);
             if (!ok) break;
             if constexpr (F != kBf16 && kTmaScales) {
-                const uint32_t sa = scale0 + slot * C::kStage + (unit * C::kScaleBytes & 15);
+                const uint32_t sa = scale0 + slot * (16 * kTileRows) + (unit * C::kScaleBytes & 15);
 #pragma unroll
                 for (int s = 0; s < 2; ++s)
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const uint32_t a = sa + (kSwiglu ? 8 * s + 16 * r : 16 * s + 8 * r) * 16;
-                        sw[s][r] = F == kMx ? lds32(a) : lds16(a);
-                    }
+                    for (int r = 0; r < 2; ++r)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t a = sa + (s * kNext + r * kStep) * 16 + h * C::kScaleBytes / 2;
+                            sw[h][s][r] = F == kMx ? lds32(a) : lds16(a);
+                        }
             }
-            multiply<F>(row0 + slot * C::kStage, kStep, kNext, xa, g < n_tok, t4, sw, x, acc, bad);
-            xa += F == kBf16 ? 64 : 256;
-            slot = slot + 1 == depth ? 0 : slot + 1;
+            const uint32_t at = row0 + slot * (kTileRows * 128);
+            multiply<F, 0>(at, kStep * 128, kNext * 128, xa, g < n_tok, sw[0], x, acc, bad);
+            multiply<F, 1>(at, kStep * 128, kNext * 128, xa + kUnitX / 2, g < n_tok, sw[1], x, acc, bad);
+            xa += kUnitX;
+            __syncwarp();                         // the slot is read by all
+            fetch_next();
+            slot = slot + 1 == static_cast<uint32_t>(depth) ? 0 : slot + 1;
             phase ^= slot == 0;
         }
         if constexpr (F == kMx) {
@@ -598,25 +586,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         any_bad |= bad[0][0] | bad[0][1] | bad[1][0] | bad[1][1];
         __syncthreads();                          // the last item's sums are read
-        float *mine = sums + warp * kTileFloats;
+        float *mine = sums + warp * sum_floats;   // [token][stage row]
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            *reinterpret_cast<float2 *>(mine + (16 * s + g) * kTok + 2 * t4) = make_float2(acc[s][0], acc[s][1]);
-            *reinterpret_cast<float2 *>(mine + (16 * s + g + 8) * kTok + 2 * t4) = make_float2(acc[s][2], acc[s][3]);
-        }
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int t = 2 * t4 + (i & 1);
+                if (t < n_tok) mine[t * kSumPitch + s * kNext + (i >> 1) * kStep + q] = acc[s][i];
+            }
         __syncthreads();
         // Everyone adds up its outputs over the warps that shared the tile, in order.
-        constexpr int kOuts = kTileCols * kTok;
-        for (int i = tid; i < group * kOuts; i += kThreads) {
-            const int tile = i / kOuts, c = i % kOuts / kTok, t = i % kTok;
+        for (int i = tid; i < group * kTileCols * n_tok; i += kThreads) {
+            const int c = i % kTileCols, tile = i / kTileCols % group, t = i / kTileCols / group;
             const int n = (grp * group + tile) * kTileCols + c;
-            if (t >= n_tok || n >= p.N) continue;
-            const int r = kSwiglu ? (c & 8) * 2 + (c & 7) : c;
-            const float *q = sums + tile * kw * kTileFloats + r * kTok + t;
+            if (n >= p.N) continue;
+            const float *from = sums + tile * kw * sum_floats + t * kSumPitch + c;
             float v = 0.f, u = 0.f;
             for (int j = 0; j < kw; ++j) {
-                v += q[j * kTileFloats];
-                if (kSwiglu) u += q[j * kTileFloats + 8 * kTok];
+                v += from[j * sum_floats];
+                if (kSwiglu) u += from[j * sum_floats + 16];
             }
             if constexpr (F != kBf16) {
                 const int e = row_exponent(tops[turn + t]) + (F == kMx ? 31 : 0);
@@ -668,37 +656,52 @@ __global__ void weigh_kernel(const float *y, const int32_t *ids, const float *w,
 
 constexpr int kMaxSmem = 232448;
 
-// Rows [outer][rows][bytes] in boxes of box_bytes by 16 rows; what lies past an end reads as zeros.
-bool encode(CUtensorMap *map, const void *base, int64_t bytes, int64_t rows, int64_t outer, uint32_t box_bytes, bool swizzle) {
+// Rows [outer][rows][bytes] in boxes of box_bytes by 32 rows, or by 16 rows of two neighbours
+// in `outer`; what lies past an end reads as zeros.
+bool encode(CUtensorMap *map, const void *base, int64_t bytes, int64_t rows, int64_t outer, uint32_t box_bytes, bool two) {
     PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encode();
     if (!fn) return false;
     cuuint64_t dims[3] = {static_cast<cuuint64_t>(bytes), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(outer)};
     cuuint64_t strides[2] = {dims[0], dims[0] * dims[1]};
-    cuuint32_t box[3] = {box_bytes, 16, 1};
+    cuuint32_t box[3] = {box_bytes, two ? 16u : 32u, two ? 2u : 1u};
     cuuint32_t estr[3] = {1, 1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+              CU_TENSOR_MAP_INTERLEAVE_NONE, box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int F, bool kSwiglu, bool kTmaScales>
 moe_status launch(Params p, bool chained, cudaStream_t stream, int num_sms) {
     using C = Fmt<F>;
     p.k_pad = (p.K + C::kUnit - 1) / C::kUnit * C::kUnit;
-    const size_t pitch = static_cast<size_t>(p.k_pad) * 2 + 64;
-    const size_t rest = 1024 + kWarps * kTileFloats * sizeof(float) + kWarps * C::kDeep * sizeof(uint64_t) +
-                        (2 * kTok + 2 + 4 * static_cast<size_t>(p.rows)) * sizeof(int);
-    const auto smem = [&](int depth, int tok) { return static_cast<size_t>(kWarps * depth * C::kStage) + rest + tok * pitch; };
+    // Rows a chunk and stages of a ring, as many as there is room for; two stages at least.
+    const size_t rest = 1024 + kWarps * kMaxDepth * sizeof(uint64_t) + (2 * kTok + 2 + 4 * static_cast<size_t>(p.rows)) * sizeof(int);
+    const size_t x_row = static_cast<size_t>(p.k_pad) * 2 + 64 + kWarps * kSumPitch * sizeof(float);
     p.tok = p.rows < kTok ? p.rows : kTok;
-    p.depth = smem(C::kDeep, p.tok) <= kMaxSmem ? C::kDeep : C::kDepth;
-    while (p.tok > 1 && smem(p.depth, p.tok) > kMaxSmem) p.tok = (p.tok + 1) / 2;
-    const size_t bytes = smem(p.depth, p.tok);
-    if (bytes > kMaxSmem) return MOE_ERR_CAPACITY;
+    while (p.tok > 1 && rest + p.tok * x_row + 2 * kWarps * C::kStage > kMaxSmem) p.tok = (p.tok + 1) / 2;
+    const size_t fixed = rest + p.tok * x_row;
+    if (fixed + 2 * kWarps * C::kStage > kMaxSmem) return MOE_ERR_CAPACITY;
+    const size_t stages = (kMaxSmem - fixed) / (kWarps * C::kStage);
+    p.depth = static_cast<int>(stages < kMaxDepth ? stages : kMaxDepth);
+    const size_t bytes = fixed + p.depth * kWarps * C::kStage;
+    // Warps a tile: few mean few sums to join, many that the CTAs' shares of the items come out
+    // even.  In units of a stage's time; an item's end costs about one.
+    constexpr int kTileCols = kSwiglu ? kTileRows / 2 : kTileRows;
+    const int64_t chunks = p.row_expert ? (p.rows < p.E ? p.rows : p.E) : (p.rows + p.tok - 1) / p.tok;
+    const int64_t tiles = (p.N + kTileCols - 1) / kTileCols, units = p.k_pad / C::kUnit;
+    int64_t best = INT64_MAX;
+    for (int kw = kWarps; kw >= 1; kw /= 2) {
+        const int64_t items = chunks * ((tiles * kw + kWarps - 1) / kWarps);
+        const int64_t cost = (items + num_sms - 1) / num_sms * ((units + kw - 1) / kw + 1);
+        if (cost >= best) continue;
+        best = cost;
+        p.kw = kw;
+    }
     CUtensorMap tm_w, tm_s;
     const int64_t outer = static_cast<int64_t>(p.E) * (kSwiglu ? 2 : 1);
-    if (!encode(&tm_w, p.w, F == kBf16 ? 2ll * p.K : p.K / 2, p.N, outer, kRowBytes, true)) return MOE_ERR_CUDA;
+    if (!encode(&tm_w, p.w, F == kBf16 ? 2ll * p.K : p.K / 2, p.N, outer, 128, kSwiglu)) return MOE_ERR_CUDA;
     tm_s = tm_w;
-    if (kTmaScales && !encode(&tm_s, p.scales, p.K / (F == kMx ? 32 : 16), p.N, outer, 16, false)) return MOE_ERR_CUDA;
+    if (kTmaScales && !encode(&tm_s, p.scales, p.K / (F == kMx ? 32 : 16), p.N, outer, 16, kSwiglu)) return MOE_ERR_CUDA;
     static std::atomic<uint64_t> mask{0};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
