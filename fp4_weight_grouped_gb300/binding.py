@@ -8,6 +8,7 @@ from __future__ import annotations
 import ctypes as C
 import os
 import threading
+from array import array
 
 import torch
 
@@ -972,13 +973,20 @@ _GRAD_DTYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 
 
 def _grad_arrays(grads, name="grads"):
-    """Pointers, sizes and types of a list of gradients, as the library takes them."""
-    n = len(grads)
-    for i, t in enumerate(grads):
-        if not (t.dtype in _GRAD_DTYPES and t.is_contiguous() and t.is_cuda):
-            raise ValueError(f"{name}[{i}]: a contiguous float32 or bfloat16 CUDA tensor is needed")
-    return ((C.c_void_p * n)(*[t.data_ptr() for t in grads]), (C.c_int64 * n)(*[t.numel() for t in grads]),
-            (C.c_int32 * n)(*[_GRAD_DTYPES[t.dtype] for t in grads]))
+    """Pointers, sizes and types of a list of gradients, as arrays that the library reads."""
+    ptrs, sizes, dtypes = array("Q"), array("q"), array("i")
+    for t in grads:
+        dtype = _GRAD_DTYPES.get(t.dtype)
+        if dtype is None or not (t.is_contiguous() and t.is_cuda):
+            raise ValueError(f"{name}[{len(ptrs)}]: a contiguous float32 or bfloat16 CUDA tensor is needed")
+        ptrs.append(t.data_ptr())
+        sizes.append(t.numel())
+        dtypes.append(dtype)
+    return ptrs, sizes, dtypes
+
+
+def _address(a):
+    return a.buffer_info()[0]
 
 
 def _grad_call(grads, norm, workspace, stream):
@@ -995,7 +1003,7 @@ def grad_norm(grads, norm: torch.Tensor | None = None, workspace: torch.Tensor |
     """Global norm f32 [1] of a list of contiguous gradients (f32 or bf16 each)."""
     ptrs, sizes, dtypes = _grad_arrays(grads)
     norm, workspace = _grad_call(grads, norm, workspace, stream)
-    rc = load().moe_grad_norm(ptrs, sizes, dtypes, len(grads), _ptr(norm), _ptr(workspace), workspace.numel(),
+    rc = load().moe_grad_norm(_address(ptrs), _address(sizes), _address(dtypes), len(ptrs), _ptr(norm), _ptr(workspace), workspace.numel(),
                               _stream(stream))
     _check(rc, "moe_grad_norm")
     return norm
@@ -1010,11 +1018,11 @@ def clip_grads(grads, max_norm: float, eps: float = 1e-6, out=None, norm: torch.
     outs = None
     if out is not None:
         outs, osizes, odtypes = _grad_arrays(out, "out")
-        if len(out) != len(grads) or list(osizes) != list(sizes) or list(odtypes) != list(dtypes):
+        if osizes != sizes or odtypes != dtypes:
             raise ValueError("out: not of the gradients' sizes and types")
     norm, workspace = _grad_call(grads, norm, workspace, stream)
-    rc = load().moe_grad_clip(ptrs, sizes, dtypes, len(grads), float(max_norm), float(eps), outs, _ptr(norm),
-                              _ptr(workspace), workspace.numel(), _stream(stream))
+    rc = load().moe_grad_clip(_address(ptrs), _address(sizes), _address(dtypes), len(ptrs), float(max_norm),
+                              float(eps), None if outs is None else _address(outs), _ptr(norm), _ptr(workspace), workspace.numel(), _stream(stream))
     _check(rc, "moe_grad_clip")
     return norm
 

@@ -7,10 +7,12 @@
 //    to be cleared between calls.
 //  * The tensors' addresses travel in the kernel's parameters, kCap a launch (longer lists
 //    take several launches); a chunk of work finds its tensor by bisection.
-//  * Squares are summed in f32 over the elements that a thread loads together and in f64
-//    from there on.  Where such a sum is too small or large for f32 (elements under about
-//    2^-50 or over 2^60) its squares are formed again in f64: the norm is right over the
-//    whole range of the types.
+//  * f64 additions are slow here (about two a cycle and SM): a thread adds the squares of the
+//    elements that it loads together in f32, and those sums in an f32 pair (the sum and what
+//    its roundings left out, by Knuth's two-sum); the block joins its pairs and only the
+//    block's sum is f64.  A group of squares outside 2^-90 .. 2^80, where f32 would lose some
+//    of them or the sums overflow, is formed again in f64 and travels beside the pairs: the
+//    norm is right over the whole range of the types.
 //  * Bound by HBM: one read for the norm and a read and a write for the clipping.  The
 //    second kernel goes through the chunks backwards, so what the first read last (the L2's
 //    share) is not fetched again.
@@ -28,9 +30,10 @@
 namespace moe {
 namespace clip {
 
-constexpr int kThreads = 256;
-constexpr int kBlocksPerSm = 8;
+constexpr int kThreads = 512;
+constexpr int kBlocksPerSm = 3;           // few: every block of the second kernel adds up all sums
 constexpr int kVecs = 4;                  // 16-byte loads a thread has in flight
+constexpr int kMinChunk = 4096, kMaxChunk = 32768;
 
 struct Tensor {
     const void *in;
@@ -64,25 +67,49 @@ __device__ __forceinline__ float as_f32(T v) {
     else return v;
 }
 
-// f32 sums in this range hold their squares to f32 accuracy: what underflows (under 2^-126
-// each) is below 2^-30 of it.
-__device__ __forceinline__ bool sum_holds(float s) { return s > 0x1p-90f && s < 0x1p120f; }
+// A sum and what its roundings left out.
+struct Pair {
+    float hi, lo;
+};
+
+__device__ __forceinline__ void add(Pair &a, float b) {
+    const float s = a.hi + b, t = s - a.hi;
+    a.lo += (a.hi - (s - t)) + (b - t);
+    a.hi = s;
+}
+
+// f32 sums in this range hold their squares to f32 accuracy (what underflows, under 2^-126
+// each, is below 2^-30 of it), and 2^40 of them fit f32.
+__device__ __forceinline__ bool sum_holds(float s) { return s > 0x1p-90f && s < 0x1p80f; }
 
 template <int V>
-__device__ __forceinline__ double squares(const float (&v)[V]) {
-    float s = 0.f;
+__device__ __forceinline__ float squares(const float (&v)[V]) {
+    float a = 0.f, b = 0.f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) s = fmaf(v[i], v[i], s);
-    if (sum_holds(s)) return s;
-    uint32_t any = 0;
-#pragma unroll
-    for (int i = 0; i < V; ++i) any |= __float_as_uint(v[i]) << 1;
-    if (any == 0) return 0.0;
+    for (int i = 0; i < V; i += 2) {
+        a = fmaf(v[i], v[i], a);
+        b = fmaf(v[i + 1], v[i + 1], b);
+    }
+    return a + b;
+}
+
+// The squares of n vectors, `stride` vectors apart, in f64.
+template <typename T>
+__device__ __noinline__ double squares64(const T *p, int n, int64_t stride) {
+    constexpr int V = 16 / sizeof(T);
     double d = 0.0;
-#pragma unroll 1
-    for (int i = 0; i < V; ++i) d = fma(static_cast<double>(v[i]), static_cast<double>(v[i]), d);
+    for (int i = 0; i < n; ++i)
+        for (int j = 0; j < V; ++j) {
+            const double x = as_f32(p[i * stride * V + j]);
+            d = fma(x, x, d);
+        }
     return d;
 }
+
+struct Sums {
+    Pair near;
+    double far;
+};
 
 // Elements of [p, p + n) before the first 16-byte address.
 template <typename T>
@@ -91,65 +118,88 @@ __device__ __forceinline__ int head_of(const T *p, int n) {
 }
 
 template <typename T>
-__device__ __forceinline__ double chunk_squares(const T *p, int n) {
+__device__ __forceinline__ void chunk_squares(const T *p, int n, Sums &sums) {
     constexpr int V = 16 / sizeof(T);
     const int tid = threadIdx.x;
-    double d = 0.0;
     const int head = head_of(p, n), vecs = (n - head) / V, tail = head + vecs * V;
     const T *q = p + head;
+    const auto take = [&](float s, int v, int count) {
+        if (sum_holds(s)) add(sums.near, s);
+        else sums.far += squares64(q + static_cast<int64_t>(v) * V, count, kThreads);
+    };
     int v = tid;
     for (; v + (kVecs - 1) * kThreads < vecs; v += kVecs * kThreads) {
         float x[kVecs][V];
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) load_row<V>(q + static_cast<int64_t>(v + i * kThreads) * V, x[i]);
+        float s = 0.f;
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) d += squares(x[i]);
+        for (int i = 0; i < kVecs; i += 2) s += squares(x[i]) + squares(x[i + 1]);
+        take(s, v, kVecs);
     }
     for (; v < vecs; v += kThreads) {
         float x[V];
         load_row<V>(q + static_cast<int64_t>(v) * V, x);
-        d += squares(x);
+        take(squares(x), v, 1);
     }
     // Up to V - 1 elements before and behind the vectors.
     const int at = tid < head ? tid : tail + tid - head;
-    if (at < n && (tid < head || at >= tail)) {
-        const double x = as_f32(p[at]);
-        d = fma(x, x, d);
+    if (at < n) {
+        const float x = as_f32(p[at]), s = x * x;
+        if (sum_holds(s)) add(sums.near, s);
+        else sums.far = fma(static_cast<double>(x), static_cast<double>(x), sums.far);
     }
-    return d;
 }
 
-__device__ __forceinline__ double block_sum(double d, double *shared) {
+// The sum of n doubles, in lane 0 of the warp that asks: the same in every block.
+__device__ __forceinline__ double total_of(const double *partial, int n) {
+    double d = 0.0;
+    for (int i = threadIdx.x & 31; i < n; i += 32) d += __ldcg(partial + i);
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) d += __shfl_xor_sync(0xffffffffu, d, m);
-    if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = d;
-    __syncthreads();
-    d = 0.0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) d += shared[w];
     return d;
 }
 
 template <int kCap>
-__global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ List<kCap> l, double *partial, int add) {
-    __shared__ double shared[kThreads / 32];
-    double d = 0.0;
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
+    norm_kernel(const __grid_constant__ List<kCap> l, double *partial, int add_to) {
+    __shared__ Pair pairs[kThreads / 32];
+    __shared__ double far[kThreads / 32];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    Sums sums = {};
     for (int c = blockIdx.x; c < l.chunks; c += gridDim.x) {
         const Tensor &t = l.t[tensor_of(l, c)];
         const int64_t at = static_cast<int64_t>(c - t.chunk0) * l.chunk;
         const int n = static_cast<int>(min(static_cast<int64_t>(l.chunk), t.n - at));
-        if (t.bf16) d += chunk_squares(static_cast<const __nv_bfloat16 *>(t.in) + at, n);
-        else d += chunk_squares(static_cast<const float *>(t.in) + at, n);
+        if (t.bf16) chunk_squares(static_cast<const __nv_bfloat16 *>(t.in) + at, n, sums);
+        else chunk_squares(static_cast<const float *>(t.in) + at, n, sums);
     }
-    d = block_sum(d, shared);
-    if (threadIdx.x == 0) partial[blockIdx.x] = add ? partial[blockIdx.x] + d : d;
-}
-
-// The sum of all partial sums, the same in every block.
-__device__ __forceinline__ double total_of(const double *partial, int n, double *shared) {
-    double d = 0.0;
-    for (int i = threadIdx.x; i < n; i += kThreads) d += __ldcg(partial + i);
-    return block_sum(d, shared);
+    const auto join = [](Pair &a, int m) {
+        const float hi = __shfl_xor_sync(0xffffffffu, a.hi, m), lo = __shfl_xor_sync(0xffffffffu, a.lo, m);
+        add(a, hi);
+        a.lo += lo;
+    };
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) join(sums.near, m);
+    const int warp = threadIdx.x >> 5;
+    if ((threadIdx.x & 31) == 0) pairs[warp] = sums.near;
+    const bool any_far = __syncthreads_or(sums.far != 0.0);       // a NaN is not 0
+    if (any_far) {
+#pragma unroll
+        for (int m = 16; m > 0; m >>= 1) sums.far += __shfl_xor_sync(0xffffffffu, sums.far, m);
+        if ((threadIdx.x & 31) == 0) far[warp] = sums.far;
+        __syncthreads();
+    }
+    if (threadIdx.x < 32) {
+        Pair a = threadIdx.x < kThreads / 32 ? pairs[threadIdx.x] : Pair{0.f, 0.f};
+#pragma unroll
+        for (int m = 16; m > 0; m >>= 1) join(a, m);
+        if (threadIdx.x == 0) {
+            double d = static_cast<double>(a.hi) + a.lo;
+            for (int w = 0; any_far && w < kThreads / 32; ++w) d += far[w];
+            partial[blockIdx.x] = add_to ? partial[blockIdx.x] + d : d;
+        }
+    }
 }
 
 template <typename T>
@@ -203,18 +253,31 @@ __device__ __forceinline__ void copy_chunk(const T *p, T *o, int n) {
 }
 
 template <int kCap>
-__global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__ List<kCap> l, const double *partial,
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) scale_kernel(const __grid_constant__ List<kCap> l, const double *partial,
                                                          int n_partial, double max_norm, double eps, float *norm) {
-    __shared__ double shared[kThreads / 32];
-    const double total = sqrt(total_of(partial, n_partial, shared));
-    if (blockIdx.x == 0 && threadIdx.x == 0 && norm) *norm = static_cast<float>(total);
-    // A norm that is not finite clips nothing: the gradients are left (or copied) as they are.
-    const bool clips = total < __longlong_as_double(0x7FF0000000000000ll) && max_norm < total + eps;
-    // A scale near or below f32's smallest normal number (a norm past 2^100) would lose bits:
-    // part of it is applied ahead, as a power of two.
-    const double whole = clips ? max_norm / (total + eps) : 1.0;
-    const float pre = whole < 0x1p-100 ? 0x1p-100f : 1.0f;
-    const float s = static_cast<float>(whole < 0x1p-100 ? whole * 0x1p100 : whole);
+    __shared__ struct {
+        int clips;
+        float pre, s;
+    } shared;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (threadIdx.x < 32) {
+        const double sum = total_of(partial, n_partial);
+        if (threadIdx.x == 0) {       // one thread: a root and a quotient in f64 by all took 20 us
+            const double total = sqrt(sum);
+            if (blockIdx.x == 0 && norm) *norm = static_cast<float>(total);
+            // A norm that is not finite clips nothing: the gradients are left (or copied) as they are.
+            const bool clips = total < __longlong_as_double(0x7FF0000000000000ll) && max_norm < total + eps;
+            // A scale near or below f32's smallest normal number (a norm past 2^100) would lose
+            // bits: part of it is applied ahead, as a power of two.
+            const double whole = clips ? max_norm / (total + eps) : 1.0;
+            shared.clips = clips;
+            shared.pre = whole < 0x1p-100 ? 0x1p-100f : 1.0f;
+            shared.s = static_cast<float>(whole < 0x1p-100 ? whole * 0x1p100 : whole);
+        }
+    }
+    __syncthreads();
+    const bool clips = shared.clips;
+    const float pre = shared.pre, s = shared.s;
     for (int i = blockIdx.x; i < l.chunks; i += gridDim.x) {
         const int c = l.chunks - 1 - i;
         const Tensor &t = l.t[tensor_of(l, c)];
@@ -231,9 +294,9 @@ __global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__
     }
 }
 
-__global__ void __launch_bounds__(kThreads) finish_kernel(const double *partial, int n_partial, float *norm) {
-    __shared__ double shared[kThreads / 32];
-    const double total = total_of(partial, n_partial, shared);
+__global__ void __launch_bounds__(32) finish_kernel(const double *partial, int n_partial, float *norm) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const double total = total_of(partial, n_partial);
     if (threadIdx.x == 0) *norm = static_cast<float>(sqrt(total));
 }
 
@@ -243,8 +306,8 @@ moe_status for_lists(const GradList &g, int blocks, const Body &body) {
     int64_t all = 0;
     for (int i = 0; i < g.n; ++i) all += g.sizes[i];
     // Chunks small enough to spread over the blocks, large enough to stream.
-    int chunk = 2048;
-    while (chunk < 16384 && all / chunk > 4ll * blocks) chunk *= 2;
+    int chunk = kMinChunk;
+    while (chunk < kMaxChunk && all / chunk > 4ll * blocks) chunk *= 2;
     List<kCap> l;
     for (int i = 0; i < g.n;) {
         const int first = i;
@@ -269,25 +332,41 @@ moe_status for_lists(const GradList &g, int blocks, const Body &body) {
     return MOE_OK;
 }
 
+// A launch that may start under the end of the one before.
+template <class... Args>
+moe_status launch_after(void (*kernel)(Args...), int blocks, int threads, bool chained, cudaStream_t stream, const Args &...args) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(threads);
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = chained ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
 template <int kCap>
 moe_status run(const GradList &g, cudaStream_t stream, int num_sms, int *launches) {
     const int blocks = num_sms * kBlocksPerSm;
     double *partial = static_cast<double *>(g.partial);
     moe_status st = for_lists<kCap>(g, blocks, [&](const List<kCap> &l, bool first) {
-        norm_kernel<kCap><<<blocks, kThreads, 0, stream>>>(l, partial, !first);
         ++*launches;
-        return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+        return launch_after(norm_kernel<kCap>, blocks, kThreads, false, stream, l, partial, static_cast<int>(!first));
     });
     if (st != MOE_OK) return st;
+    const double *sums = partial;
     if (!g.out) {
-        finish_kernel<<<1, kThreads, 0, stream>>>(partial, blocks, g.norm);
         ++*launches;
-        return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+        return launch_after(finish_kernel, 1, 32, true, stream, sums, blocks, g.norm);
     }
+    // The first scaling launch follows a norm launch and may start under its end; in place it
+    // writes what that read, but only behind its wait.
     return for_lists<kCap>(g, blocks, [&](const List<kCap> &l, bool first) {
-        scale_kernel<kCap><<<blocks, kThreads, 0, stream>>>(l, partial, blocks, g.max_norm, g.eps, first ? g.norm : nullptr);
         ++*launches;
-        return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+        return launch_after(scale_kernel<kCap>, blocks, kThreads, first, stream, l, sums, blocks, g.max_norm, g.eps,
+                            first ? g.norm : static_cast<float *>(nullptr));
     });
 }
 

@@ -1,8 +1,8 @@
 """Global gradient norm and clipping against the formulas in 64 bits.
 
-The norm: squares of a thread's 4 or 8 elements are summed in f32 (a relative error of at
-most 8 2^-24 each, of either sign), the rest in f64, and the root halves it: 4 2^-24 is a
-bound, rounding to f32 adds 2^-24.  A clipped element: the scale rounded to f32, one f32
+The norm: squares of a thread's elements are summed in f32, four in a row and three sums
+deep (a relative error of at most 7 2^-24, of either sign), the rest in f32 pairs and f64,
+and the root halves it: 4 2^-24 is a bound, rounding to f32 adds 2^-24.  A clipped element: the scale rounded to f32, one f32
 product, one rounding to the type."""
 import math
 
