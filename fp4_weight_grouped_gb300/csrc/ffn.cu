@@ -66,6 +66,7 @@ struct Job {
     int tiles_m, tiles_n, k_stages;
     int first;                   // item
     int a_mn, b_mn;              // operand stored along m (n) instead of k
+    int a_rows, odd_a;           // rows of A in a box (along k), whether the odd CTA has any
     int tile_cols, b_step;       // output columns an item; the odd CTA's first row of B
     int epilogue;
     int out_f32;
@@ -85,6 +86,7 @@ struct Misc {
     uint32_t tmem;
     int abort;
     uint32_t issued;
+    uint32_t odd_issued, odd_abort;     // the odd CTA's, left with the even one at the end
 };
 
 // One box into this CTA's shared memory, its bytes counted on a barrier of either CTA of the pair.
@@ -138,6 +140,19 @@ __device__ __forceinline__ Item item_of(const Args &p, int i) {
     const Job &w = p.job[j];
     const int at = i - w.first;
     return {j, at / w.tiles_n * 2 * kRows, at % w.tiles_n * w.tile_cols};
+}
+
+// What the odd CTA copies in stage i of a pair's stream.
+template <int kN>
+__device__ __noinline__ uint32_t odd_bytes(const Args &p, int first, int step, uint32_t i) {
+    int item = first;
+    for (; item + step < p.items; item += step) {
+        const uint32_t n = p.job[item_of(p, item).job].k_stages;
+        if (i < n) break;
+        i -= n;
+    }
+    const Job &w = p.job[item_of(p, item).job];
+    return w.odd_a * w.a_rows * 128 + Tile<kN>::kBBytes;
 }
 
 // 16 consecutive outputs of a row at column n: n columns are a multiple of 8.
@@ -218,7 +233,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ffn_ker
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem = misc->tmem;
+    // A launch in a chain starts under the end of the one before, whose outputs it reads.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
+    // The two loops that feed the tensor core run in one warp each, an instruction after the
+    // other: what they need of a job is in registers ahead of them (read from the parameters
+    // stage by stage it made a stage 240 ns at least, whatever its work).
     if (warp == kProducerWarp) {
         const bool leader = elect_one();
         const uint32_t base = smem_u32(smem), bar0 = cluster_addr(full, 0);
@@ -229,22 +250,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ffn_ker
             const Job &w = p.job[it.job];
             const CUtensorMap *ma = &p.a[it.job], *mb = &p.b[it.job];
             const int row_a = it.m0 + rank * kRows, row_b = it.n0 + rank * w.b_step;
-            for (int ks = 0; ks < w.k_stages; ++ks) {
+            const uint32_t bytes = w.a_rows * 128 * (1 + w.odd_a) + 2 * T::kBBytes;
+            const bool a_mn = w.a_mn, b_mn = w.b_mn, has_a = rank == 0 || w.odd_a;
+            const int k_end = w.k_stages * kStageK;
+            for (int k = 0; k < k_end; k += kStageK) {
                 ok = wait(&empty[slot], phase, abort_flag, p.status, lim);
                 if (!ok) break;
-                const uint32_t a = base + slot * T::kStageBytes, b = a + kABytes, bar = bar0 + slot * 8;
-                const int k = ks * kStageK;
                 if (leader) {
-                    if (rank == 0) mbar_arrive_expect_tx(&full[slot], 2 * T::kStageBytes);
-                    if (w.a_mn) {
+                    const uint32_t a = base + slot * T::kStageBytes, b = a + kABytes, bar = bar0 + slot * 8;
+                    if (rank == 0) mbar_arrive_expect_tx(&full[slot], bytes);
+                    if (a_mn) {
                         tma_load_pair(a, ma, row_a, k, bar);
                         tma_load_pair(a + 8192, ma, row_a + 64, k, bar);
-                    } else {
+                    } else if (has_a) {
                         tma_load_pair(a, ma, k, row_a, bar);
                     }
-                    if (w.b_mn) {
+                    if (b_mn) {
 #pragma unroll
-                        for (int q = 0; q < T::kBRows; q += 64) tma_load_pair(b + q * 128, mb, row_b + q, k, bar);
+                        for (int q = 0; q < T::kBRows / 64 * 64; q += 64) tma_load_pair(b + q * 128, mb, row_b + q, k, bar);
                     } else {
                         tma_load_pair(b, mb, k, row_b, bar);
                     }
@@ -267,22 +290,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ffn_ker
             const uint32_t idesc = idesc_bf16_f32(2 * kRows, kN) | (w.a_mn ? 1u << 15 : 0) | (w.b_mn ? 1u << 16 : 0);
             // 16 k further: 32 bytes along a row, or 16 rows of 128 bytes.
             const uint32_t a_step = w.a_mn ? 128 : 2, b_step = w.b_mn ? 128 : 2;
+            const uint64_t da0 = w.a_mn ? smem_desc_mn(base) : smem_desc_sw128(base);
+            const uint64_t db0 = w.b_mn ? smem_desc_mn(base + kABytes) : smem_desc_sw128(base + kABytes);
             const uint32_t d = tmem + buf * kN;
+            const int k_stages = w.k_stages;
             ok = wait(&acc_empty[buf], acc_phase, abort_flag, p.status, lim);
             tc_fence_after();
-            for (int ks = 0; ok && ks < w.k_stages; ++ks) {
+            for (int ks = 0; ok && ks < k_stages; ++ks) {
                 ok = wait(&full[slot], phase, abort_flag, p.status, lim);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t a = base + slot * T::kStageBytes, b = a + kABytes;
-                const uint64_t da = w.a_mn ? smem_desc_mn(a) : smem_desc_sw128(a);
-                const uint64_t db = w.b_mn ? smem_desc_mn(b) : smem_desc_sw128(b);
                 if (leader) {
+                    const uint64_t da = da0 + slot * (T::kStageBytes / 16), db = db0 + slot * (T::kStageBytes / 16);
 #pragma unroll
                     for (int t = 0; t < kStageK / 16; ++t)
                         mma_pair(d, da + t * a_step, db + t * b_step, idesc, t > 0 || ks > 0);
                     mma_commit_pair(&empty[slot], 3);
-                    if (ks == w.k_stages - 1) mma_commit_pair(&acc_full[buf], 3);
+                    if (ks == k_stages - 1) mma_commit_pair(&acc_full[buf], 3);
                 }
                 __syncwarp();
                 slot = slot + 1 == T::kStages ? 0 : slot + 1;
@@ -374,19 +398,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ffn_ker
     __syncwarp();
     tc_fence_before();
     __syncthreads();
+    if (rank == 1 && threadIdx.x == 0) {
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr(&misc->odd_issued, 0)), "r"(misc->issued) : "memory");
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr(&misc->odd_abort, 0)), "r"(misc->abort) : "memory");
+    }
     cluster_sync();
     tc_fence_after();
     if (rank == 0 && threadIdx.x == 0) {
-        uint32_t n1, aborted;
-        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(n1) : "r"(cluster_addr(&misc->issued, 1)) : "memory");
-        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(aborted) : "r"(cluster_addr(&misc->abort, 1)) : "memory");
-        if (aborted || misc->abort) {       // every copy that was issued lands before the pair leaves
+        if (misc->odd_abort || misc->abort) {       // every copy that was issued lands before the pair leaves
+            const uint32_t n1 = misc->odd_issued;
             const uint32_t n0 = misc->issued, n = n0 > n1 ? n0 : n1;
             for (uint32_t i = pair_first(n0, n1, T::kStages); i < n; ++i) {
                 uint64_t *bar = &full[i % T::kStages];
                 const uint32_t parity = (i / T::kStages) & 1u;
                 if (mbar_try_wait(bar, parity)) continue;
-                const PairFix f = pair_fix(i, n0, n1, T::kStageBytes);
+                const PairFix f = pair_fix(i, n0, n1, odd_bytes<kN>(p, first, step, i));
                 if (f.arrive) mbar_arrive_expect_tx(bar, f.expect);
                 if (f.complete)
                     asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)),
@@ -396,7 +422,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ffn_ker
             }
         }
     }
-    __syncthreads();
     if (warp == kIssuerWarp) tmem_dealloc_pair(tmem, T::kCols);
     cluster_sync();
 }
@@ -431,8 +456,18 @@ struct Product {
     uint16_t *gu;
 };
 
+// Items of a list of products at kN columns an item.
+int64_t count_items(const Product *w, int jobs, int kN) {
+    int64_t items = 0;
+    for (int j = 0; j < jobs; ++j) {
+        const int cols = w[j].epilogue == kGate ? kN / 2 : kN;
+        items += (w[j].m + 2 * kRows - 1) / (2 * kRows) * ((w[j].n + cols - 1) / cols);
+    }
+    return items;
+}
+
 template <int kN>
-moe_status launch(const Product *w, int jobs, int *status, uint64_t limit, cudaStream_t stream, int num_sms) {
+moe_status launch(const Product *w, int jobs, bool chained, int *status, uint64_t limit, cudaStream_t stream, int num_sms) {
     using T = Tile<kN>;
     Args p = {};
     p.jobs = jobs;
@@ -452,6 +487,11 @@ moe_status launch(const Product *w, int jobs, int *status, uint64_t limit, cudaS
         o.tiles_m = (o.m + 2 * kRows - 1) / (2 * kRows);
         o.tiles_n = (o.n + o.tile_cols - 1) / o.tile_cols;
         o.k_stages = (o.k + kStageK - 1) / kStageK;
+        // Up to 128 rows, the box holds no more of them and the odd CTA copies none: its half of
+        // the products, of what is left in its memory, goes nowhere (their boxes would cost what full ones do).
+        const bool few = !w[j].a.mn && o.m <= kRows;
+        o.a_rows = few ? (o.m + 7) & ~7 : kRows;
+        o.odd_a = !few;
         o.first = static_cast<int>(items);
         o.epilogue = w[j].epilogue;
         o.out = w[j].out;
@@ -462,7 +502,7 @@ moe_status launch(const Product *w, int jobs, int *status, uint64_t limit, cudaS
         const int64_t n_rows = gate ? 2 * w[j].n : w[j].n;
         const Operand &a = w[j].a, &b = w[j].b;
         if (!(a.mn ? encode(&p.a[j], a.p, w[j].k, w[j].m, a.pitch, kStageK)
-                   : encode(&p.a[j], a.p, w[j].m, w[j].k, a.pitch, kRows)) ||
+                   : encode(&p.a[j], a.p, w[j].m, w[j].k, a.pitch, o.a_rows)) ||
             !(b.mn ? encode(&p.b[j], b.p, w[j].k, n_rows, b.pitch, kStageK)
                    : encode(&p.b[j], b.p, n_rows, w[j].k, b.pitch, T::kBRows)))
             return MOE_ERR_CUDA;
@@ -478,12 +518,28 @@ moe_status launch(const Product *w, int jobs, int *status, uint64_t limit, cudaS
         mask.fetch_or(bit, std::memory_order_release);
     }
     const int pairs = static_cast<int>(items < num_sms / 2 ? items : num_sms / 2);
-    ffn_kernel<kN><<<2 * pairs, kThreads, T::kSmem, stream>>>(p);
-    return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * pairs);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = T::kSmem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = chained ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, ffn_kernel<kN>, p) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
-moe_status run(const Product *w, int jobs, int *status, uint64_t limit, cudaStream_t stream, int num_sms) {
-    return launch<256>(w, jobs, status, limit, stream, num_sms);
+// The widest items that still give every pair of SMs one: wide items read A less often, few
+// items leave SMs idle.  B along n comes in boxes of 64, two CTAs' make 128.
+moe_status run(const Product *w, int jobs, bool chained, int *status, uint64_t limit, cudaStream_t stream, int num_sms) {
+    bool b_mn = false;
+    for (int j = 0; j < jobs; ++j) b_mn = b_mn || w[j].b.mn;
+    const int pairs = num_sms / 2;
+    if (count_items(w, jobs, 256) >= pairs) return launch<256>(w, jobs, chained, status, limit, stream, num_sms);
+    if (b_mn || count_items(w, jobs, 128) >= pairs) return launch<128>(w, jobs, chained, status, limit, stream, num_sms);
+    return launch<64>(w, jobs, chained, status, limit, stream, num_sms);
 }
 
 }  // namespace ffn
@@ -503,11 +559,11 @@ moe_status launch_ffn_forward(const Ffn &f, cudaStream_t stream, int num_sms, in
         return launch_matvec(m, stream, num_sms);
     }
     const ffn::Product up = {{f.x, f.x_stride, false}, {f.w13, H, false}, T, I, H, ffn::kGate, f.h, 0, f.gu};
-    moe_status st = ffn::run(&up, 1, f.status, f.wait_limit_ns, stream, num_sms);
+    moe_status st = ffn::run(&up, 1, false, f.status, f.wait_limit_ns, stream, num_sms);
     if (st != MOE_OK) return st;
     ++*launches;
     const ffn::Product down = {{f.h, I, false}, {f.w2, I, false}, T, H, I, ffn::kStore, f.out, !f.out_bf16, nullptr};
-    st = ffn::run(&down, 1, f.status, f.wait_limit_ns, stream, num_sms);
+    st = ffn::run(&down, 1, true, f.status, f.wait_limit_ns, stream, num_sms);
     if (st == MOE_OK) ++*launches;
     return st;
 }
@@ -528,7 +584,7 @@ moe_status launch_ffn_backward(const Ffn &f, const FfnGrad &d, cudaStream_t stre
     if (d.dw2)
         w[n++] = {{d.dout, H, true}, {f.h, I, true}, H, I, T, ffn::kStore, d.dw2, d.dw_f32, nullptr};
     if (n > 0) {
-        const moe_status st = ffn::run(w, n, f.status, f.wait_limit_ns, stream, num_sms);
+        const moe_status st = ffn::run(w, n, false, f.status, f.wait_limit_ns, stream, num_sms);
         if (st != MOE_OK) return st;
         ++*launches;
     }
@@ -538,7 +594,7 @@ moe_status launch_ffn_backward(const Ffn &f, const FfnGrad &d, cudaStream_t stre
     if (d.dx)
         w[n++] = {{d.dgu, 2 * I, false}, {f.w13, H, true}, T, H, 2 * I, ffn::kStore, d.dx, 0, nullptr};
     if (n > 0) {
-        const moe_status st = ffn::run(w, n, f.status, f.wait_limit_ns, stream, num_sms);
+        const moe_status st = ffn::run(w, n, true, f.status, f.wait_limit_ns, stream, num_sms);
         if (st != MOE_OK) return st;
         ++*launches;
     }

@@ -3,9 +3,9 @@
 //
 // The barrier of a stage, in the even CTA, counts one arrival (the even producer's, which
 // expects the bytes of both CTAs) and the bytes that either CTA copies.  The producers have
-// issued n0 and n1 stages; a barrier completes, and all copies on it have landed, once what
-// never came has been made up for: the arrival and the even CTA's bytes of a stage that only
-// the odd CTA issued, the odd CTA's bytes of one that only the even CTA issued.
+// issued n0 (even) and n1 (odd) stages.  A barrier completes, and all copies on it have
+// landed, once what never came has been made up for: the odd CTA's bytes of a stage that only
+// the even CTA issued, and of one that only the odd CTA issued the arrival, expecting them.
 #pragma once
 
 #include <stdint.h>
@@ -24,10 +24,10 @@ struct PairFix {
     uint32_t complete;   // bytes to count as landed
 };
 
-// Stage `i` of copies of `bytes` a CTA, i < max(n0, n1).
-MOE_PAIR_FN PairFix pair_fix(uint32_t i, uint32_t n0, uint32_t n1, uint32_t bytes) {
-    if (i >= n0) return {true, bytes, 0};
-    if (i >= n1) return {false, 0, bytes};
+// Stage i < max(n0, n1), of which the odd CTA copies odd_bytes.
+MOE_PAIR_FN PairFix pair_fix(uint32_t i, uint32_t n0, uint32_t n1, uint32_t odd_bytes) {
+    if (i >= n0) return {true, odd_bytes, 0};
+    if (i >= n1) return {false, 0, odd_bytes};
     return {false, 0, 0};
 }
 
