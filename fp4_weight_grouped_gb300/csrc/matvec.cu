@@ -73,6 +73,7 @@ struct Params {
     int depth;                    // stages of a warp's ring
     int k_pad;                    // K up to a stage
     int x_vec;                    // x rows at 16-byte addresses
+    int chained;                  // x comes from the launch before
     uint64_t wait_limit_ns;
 };
 
@@ -279,14 +280,19 @@ __device__ __forceinline__ void store_x(uint8_t *row, int v, const uint4 &a, int
 // bf16 as they are), zeros up to k_pad.  tops[t] (zero before) receives row t's largest
 // exponent field.  NVFP4: within 128 k, 16 bytes q go to place 4 (q % 4) + q / 4, where the
 // lanes that hold 32 k each find theirs side by side.
-template <int F>
-__device__ __forceinline__ void stage_x(const Params &p, const int *slots, int n, uint8_t *xs, int pitch, int *tops) {
-    const int tid = threadIdx.x, vecs = p.k_pad / 8;
-    if (vecs <= kThreads) {           // one load a row and thread
-        uint4 a[kTok];
+// Rows of x in registers, where a thread has one load of each (vecs <= kThreads).
+__device__ __forceinline__ void fetch_x(const Params &p, const int *slots, int n, uint4 (&a)[kTok]) {
 #pragma unroll
-        for (int t = 0; t < kTok; ++t)
-            if (t < n && tid < vecs) a[t] = load_x(p, slots[t], tid);
+    for (int t = 0; t < kTok; ++t)
+        if (t < n && static_cast<int>(threadIdx.x) < p.k_pad / 8) a[t] = load_x(p, slots[t], threadIdx.x);
+}
+
+template <int F>
+__device__ __forceinline__ void stage_x(const Params &p, const int *slots, int n, uint8_t *xs, int pitch, int *tops,
+                                        bool fetched, uint4 (&a)[kTok]) {
+    const int tid = threadIdx.x, vecs = p.k_pad / 8;
+    if (vecs <= kThreads) {
+        if (!fetched) fetch_x(p, slots, n, a);
         if constexpr (F != kBf16) {
 #pragma unroll
             for (int t = 0; t < kTok; ++t) {
@@ -489,11 +495,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     };
+    // The first rows of x ahead of the weights, behind which they would queue, unless they
+    // come from the launch before (a chain of products): weights and ids do not.
+    uint4 xr[kTok];
+    const bool ahead = !p.chained && count > 0 && p.k_pad / 8 <= kThreads;
+    if (ahead) fetch_x(p, ch.order + ch.first[chunk0], ch.first[chunk0 + 1] - ch.first[chunk0], xr);
 #pragma unroll 1
     for (int i = 0; i < depth; ++i) fetch_next();
-
-    // Weights and ids do not depend on the launch before (a chain of products); x does, and
-    // so do the outputs' readers.
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (blockIdx.x == 0 && p.row_expert) {        // rows without an expert: zeros
@@ -526,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             n_tok = ch.first[chunk + 1] - start;
             if (left != count) __syncthreads();   // and past its exponents
             turn ^= kTok;
-            stage_x<F>(p, ch.order + start, n_tok, xs, pitch, tops + turn);
+            stage_x<F>(p, ch.order + start, n_tok, xs, pitch, tops + turn, ahead && left == count, xr);
             if (tid < kTok) tops[(turn ^ kTok) + tid] = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[i] = make_uint4(0, 0, 0, 0);
@@ -671,7 +679,7 @@ bool encode(CUtensorMap *map, const void *base, int64_t bytes, int64_t rows, int
 }
 
 template <int F, bool kSwiglu, bool kTmaScales>
-moe_status launch(Params p, bool chained, cudaStream_t stream, int num_sms) {
+moe_status launch(Params p, cudaStream_t stream, int num_sms) {
     using C = Fmt<F>;
     p.k_pad = (p.K + C::kUnit - 1) / C::kUnit * C::kUnit;
     // Rows a chunk and stages of a ring, as many as there is room for; two stages at least.
@@ -721,7 +729,7 @@ moe_status launch(Params p, bool chained, cudaStream_t stream, int num_sms) {
     cfg.dynamicSmemBytes = bytes;
     cfg.stream = stream;
     cfg.attrs = &attr;
-    cfg.numAttrs = chained ? 1 : 0;
+    cfg.numAttrs = p.chained ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kernel, tm_w, tm_s, p) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -745,21 +753,22 @@ moe_status launch_matvec(const Matvec &m, cudaStream_t stream, int num_sms) {
     p.out_bf16 = m.out_bf16;
     p.status = m.status;
     p.wait_limit_ns = m.wait_limit_ns;
+    p.chained = m.chained;
     p.x_vec = reinterpret_cast<uintptr_t>(m.x) % 16 == 0 && (m.x_stride % 8 == 0 || m.rows <= m.index_div);
     if (m.format == Matvec::kBf16)
-        return m.swiglu ? mv::launch<mv::kBf16, true, false>(p, m.chained, stream, num_sms)
-                        : mv::launch<mv::kBf16, false, false>(p, m.chained, stream, num_sms);
+        return m.swiglu ? mv::launch<mv::kBf16, true, false>(p, stream, num_sms)
+                        : mv::launch<mv::kBf16, false, false>(p, stream, num_sms);
     const bool nv = m.format == Matvec::kNv;
     // Rows of scales that TMA takes: a multiple of 16 bytes, at 16-byte addresses.
     if (m.K / (nv ? 16 : 32) % 16 == 0 && reinterpret_cast<uintptr_t>(m.scales) % 16 == 0)
-        return nv ? m.swiglu ? mv::launch<mv::kNv, true, true>(p, m.chained, stream, num_sms)
-                             : mv::launch<mv::kNv, false, true>(p, m.chained, stream, num_sms)
-                  : m.swiglu ? mv::launch<mv::kMx, true, true>(p, m.chained, stream, num_sms)
-                             : mv::launch<mv::kMx, false, true>(p, m.chained, stream, num_sms);
-    return nv ? m.swiglu ? mv::launch<mv::kNv, true, false>(p, m.chained, stream, num_sms)
-                         : mv::launch<mv::kNv, false, false>(p, m.chained, stream, num_sms)
-              : m.swiglu ? mv::launch<mv::kMx, true, false>(p, m.chained, stream, num_sms)
-                         : mv::launch<mv::kMx, false, false>(p, m.chained, stream, num_sms);
+        return nv ? m.swiglu ? mv::launch<mv::kNv, true, true>(p, stream, num_sms)
+                             : mv::launch<mv::kNv, false, true>(p, stream, num_sms)
+                  : m.swiglu ? mv::launch<mv::kMx, true, true>(p, stream, num_sms)
+                             : mv::launch<mv::kMx, false, true>(p, stream, num_sms);
+    return nv ? m.swiglu ? mv::launch<mv::kNv, true, false>(p, stream, num_sms)
+                         : mv::launch<mv::kNv, false, false>(p, stream, num_sms)
+              : m.swiglu ? mv::launch<mv::kMx, true, false>(p, stream, num_sms)
+                         : mv::launch<mv::kMx, false, false>(p, stream, num_sms);
 }
 
 moe_status launch_weigh(const float *y, const int32_t *ids, const float *w, int T, int k, int N, int E, void *out,
