@@ -64,10 +64,10 @@ enum Epilogue { kStore, kGate, kGateBack };
 struct Job {
     int m, n, k;                 // n: columns of the output (gate: of h)
     int tiles_m, tiles_n, k_stages;
-    int first;                   // item
+    int first, full;             // first item; items of all kN columns, the others have half
     int a_mn, b_mn;              // operand stored along m (n) instead of k
     int a_rows, odd_a;           // rows of A in a box (along k), whether the odd CTA has any
-    int tile_cols, b_step;       // output columns an item; the odd CTA's first row of B
+    int tile_cols, b_step;       // output columns an item; gate: the odd CTA's first row of B
     int epilogue;
     int out_f32;
     void *out;                   // [m, n]; gate: h; gate back: dgu [m, 2 n]
@@ -75,7 +75,7 @@ struct Job {
 };
 
 struct Args {
-    CUtensorMap a[kMaxJobs], b[kMaxJobs];
+    CUtensorMap a[kMaxJobs], b[kMaxJobs], b_half[kMaxJobs];      // b_half: boxes of half the rows
     Job job[kMaxJobs];
     int jobs, items;
     int *status;
@@ -132,14 +132,17 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile in
 
 struct Item {
     int job, m0, n0;
+    int half;                    // half as many columns
 };
 
 __device__ __forceinline__ Item item_of(const Args &p, int i) {
     int j = 0;
     while (j + 1 < p.jobs && i >= p.job[j + 1].first) ++j;
     const Job &w = p.job[j];
-    const int at = i - w.first;
-    return {j, at / w.tiles_n * 2 * kRows, at % w.tiles_n * w.tile_cols};
+    const int at = i - w.first, over = at - w.full;
+    const int tile = over < 0 ? at : w.full + (over >> 1);
+    return {j, tile / w.tiles_n * 2 * kRows, tile % w.tiles_n * w.tile_cols + (over >= 0 && (over & 1) ? w.tile_cols / 2 : 0),
+            over >= 0};
 }
 
 // What the odd CTA copies in stage i of a pair's stream.
@@ -151,8 +154,9 @@ __device__ __noinline__ uint32_t odd_bytes(const Args &p, int first, int step, u
         if (i < n) break;
         i -= n;
     }
-    const Job &w = p.job[item_of(p, item).job];
-    return w.odd_a * w.a_rows * 128 + Tile<kN>::kBBytes;
+    const Item it = item_of(p, item);
+    const Job &w = p.job[it.job];
+    return w.odd_a * w.a_rows * 128 + (Tile<kN>::kBBytes >> it.half);
 }
 
 // 16 consecutive outputs of a row at column n: n columns are a multiple of 8.
@@ -248,9 +252,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ffn_ker
         for (int i = first; ok && i < p.items; i += step) {
             const Item it = item_of(p, i);
             const Job &w = p.job[it.job];
-            const CUtensorMap *ma = &p.a[it.job], *mb = &p.b[it.job];
-            const int row_a = it.m0 + rank * kRows, row_b = it.n0 + rank * w.b_step;
-            const uint32_t bytes = w.a_rows * 128 * (1 + w.odd_a) + 2 * T::kBBytes;
+            const CUtensorMap *ma = &p.a[it.job], *mb = it.half ? &p.b_half[it.job] : &p.b[it.job];
+            const int b_rows = T::kBRows >> it.half;
+            const int row_a = it.m0 + rank * kRows;
+            const int row_b = it.n0 + rank * (w.epilogue == kGate ? w.b_step : b_rows);
+            const uint32_t bytes = w.a_rows * 128 * (1 + w.odd_a) + 2 * (T::kBBytes >> it.half);
             const bool a_mn = w.a_mn, b_mn = w.b_mn, has_a = rank == 0 || w.odd_a;
             const int k_end = w.k_stages * kStageK;
             for (int k = 0; k < k_end; k += kStageK) {
@@ -267,7 +273,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ffn_ker
                     }
                     if (b_mn) {
 #pragma unroll
-                        for (int q = 0; q < T::kBRows / 64 * 64; q += 64) tma_load_pair(b + q * 128, mb, row_b + q, k, bar);
+                        for (int q = 0; q < T::kBRows / 64 * 64; q += 64)
+                            if (q < b_rows) tma_load_pair(b + q * 128, mb, row_b + q, k, bar);
                     } else {
                         tma_load_pair(b, mb, k, row_b, bar);
                     }
@@ -287,7 +294,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ffn_ker
         for (int i = first; ok && i < p.items; i += step) {
             const Item it = item_of(p, i);
             const Job &w = p.job[it.job];
-            const uint32_t idesc = idesc_bf16_f32(2 * kRows, kN) | (w.a_mn ? 1u << 15 : 0) | (w.b_mn ? 1u << 16 : 0);
+            const uint32_t idesc = idesc_bf16_f32(2 * kRows, kN >> it.half) | (w.a_mn ? 1u << 15 : 0) | (w.b_mn ? 1u << 16 : 0);
             // 16 k further: 32 bytes along a row, or 16 rows of 128 bytes.
             const uint32_t a_step = w.a_mn ? 128 : 2, b_step = w.b_mn ? 128 : 2;
             const uint64_t da0 = w.a_mn ? smem_desc_mn(base) : smem_desc_sw128(base);
@@ -329,6 +336,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ffn_ker
             const uint32_t acc = tmem + buf * kN + (static_cast<uint32_t>(quarter * 32) << 16);
             const int64_t row = it.m0 + static_cast<int64_t>(rank) * kRows + quarter * 32 + lane;
             const bool real = row < w.m;
+            const int cols = kN >> it.half;
             const int width = w.epilogue == kGateBack ? 2 * w.n : w.n;
             uint8_t *out = static_cast<uint8_t *>(w.out) + (real ? row : 0) * width * (w.out_f32 ? 4 : 2);
             const bool sector = (reinterpret_cast<uintptr_t>(w.out) & 31) == 0 && width % 16 == 0;
@@ -336,12 +344,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ffn_ker
                 uint16_t *gu = w.gu ? w.gu + (real ? row : 0) * 2 * w.n : nullptr;
                 const bool gu_sector = (reinterpret_cast<uintptr_t>(w.gu) & 31) == 0 && w.n % 16 == 0;
 #pragma unroll 1
-                for (int c = 0; c < kN / 2; c += 16) {
+                for (int c = 0; c < cols / 2; c += 16) {
                     const int n = it.n0 + c;
                     if (n >= w.n) break;
                     uint32_t rg[16], ru[16];
                     tmem_ld16(acc + c, rg);
-                    tmem_ld16(acc + kN / 2 + c, ru);
+                    tmem_ld16(acc + cols / 2 + c, ru);
                     tmem_ld_wait();
                     float g[16], u[16], h[16];
 #pragma unroll
@@ -363,7 +371,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ffn_ker
                 const uint16_t *gu = w.gu + (real ? row : 0) * 2 * w.n;
                 uint16_t *up = reinterpret_cast<uint16_t *>(out) + w.n;
 #pragma unroll 1
-                for (int c = 0; c < kN; c += 16) {
+                for (int c = 0; c < cols; c += 16) {
                     const int n = it.n0 + c;
                     if (n >= w.n) break;
                     uint32_t r[16];
@@ -474,6 +482,7 @@ moe_status launch(const Product *w, int jobs, bool chained, int *status, uint64_
     p.status = status;
     p.wait_limit_ns = limit;
     int64_t items = 0;
+    const int pairs_most = num_sms / 2;
     for (int j = 0; j < jobs; ++j) {
         Job &o = p.job[j];
         const bool gate = w[j].epilogue == kGate;
@@ -483,7 +492,7 @@ moe_status launch(const Product *w, int jobs, bool chained, int *status, uint64_
         o.a_mn = w[j].a.mn;
         o.b_mn = w[j].b.mn;
         o.tile_cols = gate ? kN / 2 : kN;
-        o.b_step = gate ? o.n : kN / 2;
+        o.b_step = gate ? o.n : 0;
         o.tiles_m = (o.m + 2 * kRows - 1) / (2 * kRows);
         o.tiles_n = (o.n + o.tile_cols - 1) / o.tile_cols;
         o.k_stages = (o.k + kStageK - 1) / kStageK;
@@ -497,14 +506,23 @@ moe_status launch(const Product *w, int jobs, bool chained, int *status, uint64_
         o.out = w[j].out;
         o.out_f32 = w[j].out_f32;
         o.gu = w[j].gu;
-        items += static_cast<int64_t>(o.tiles_m) * o.tiles_n;
-        if (items > INT32_MAX / 2) return MOE_ERR_CAPACITY;
+        // Where a last round of items would give less than half of the pairs one, its items are
+        // cut in two (4,096 tokens, 256 items on 76 pairs: 123 -> 116 us).
+        const int64_t tiles = static_cast<int64_t>(o.tiles_m) * o.tiles_n;
+        if (items + 2 * tiles > INT32_MAX / 2) return MOE_ERR_CAPACITY;
+        const int64_t rest = (items + tiles) % pairs_most;
+        const bool cut = kN == 256 && j == jobs - 1 && items + tiles > pairs_most && 2 * rest <= pairs_most && rest <= tiles;
+        o.full = static_cast<int>(cut ? tiles - rest : tiles);
+        items += tiles + (cut ? rest : 0);
         const int64_t n_rows = gate ? 2 * w[j].n : w[j].n;
         const Operand &a = w[j].a, &b = w[j].b;
         if (!(a.mn ? encode(&p.a[j], a.p, w[j].k, w[j].m, a.pitch, kStageK)
                    : encode(&p.a[j], a.p, w[j].m, w[j].k, a.pitch, o.a_rows)) ||
             !(b.mn ? encode(&p.b[j], b.p, w[j].k, n_rows, b.pitch, kStageK)
                    : encode(&p.b[j], b.p, n_rows, w[j].k, b.pitch, T::kBRows)))
+            return MOE_ERR_CUDA;
+        p.b_half[j] = p.b[j];
+        if (o.full < tiles && !b.mn && !encode(&p.b_half[j], b.p, n_rows, w[j].k, b.pitch, T::kBRows / 2))
             return MOE_ERR_CUDA;
     }
     p.items = static_cast<int>(items);
@@ -517,7 +535,7 @@ moe_status launch(const Product *w, int jobs, bool chained, int *status, uint64_
             return MOE_ERR_CUDA;
         mask.fetch_or(bit, std::memory_order_release);
     }
-    const int pairs = static_cast<int>(items < num_sms / 2 ? items : num_sms / 2);
+    const int pairs = static_cast<int>(items < pairs_most ? items : pairs_most);
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
@@ -531,14 +549,18 @@ moe_status launch(const Product *w, int jobs, bool chained, int *status, uint64_
     return cudaLaunchKernelEx(&cfg, ffn_kernel<kN>, p) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
-// The widest items that still give every pair of SMs one: wide items read A less often, few
-// items leave SMs idle.  B along n comes in boxes of 64, two CTAs' make 128.
+// The width of items: rounds over the pairs times what a stage takes (about 0.17, 0.23 and
+// 0.33 us: TMA's rows of A and B).  Wide items read A less often, narrow ones leave fewer SMs
+// idle.  hidden 4,096, inter 2,048, forward: 64 tokens 41 us with 256 columns and 26 with 64,
+// 512 tokens 42 us with 64 and 29 with 128, 1,024 tokens 45 us with 128 and 41 with 256.  B
+// along n comes in boxes of 64, the two CTAs' make 128.
 moe_status run(const Product *w, int jobs, bool chained, int *status, uint64_t limit, cudaStream_t stream, int num_sms) {
     bool b_mn = false;
     for (int j = 0; j < jobs; ++j) b_mn = b_mn || w[j].b.mn;
-    const int pairs = num_sms / 2;
-    if (count_items(w, jobs, 256) >= pairs) return launch<256>(w, jobs, chained, status, limit, stream, num_sms);
-    if (b_mn || count_items(w, jobs, 128) >= pairs) return launch<128>(w, jobs, chained, status, limit, stream, num_sms);
+    const auto cost = [&](int kN, int stage) { return (count_items(w, jobs, kN) + num_sms / 2 - 1) / (num_sms / 2) * stage; };
+    const int64_t c256 = cost(256, 33), c128 = cost(128, 23), c64 = b_mn ? INT64_MAX : cost(64, 17);
+    if (c256 <= c128 && c256 <= c64) return launch<256>(w, jobs, chained, status, limit, stream, num_sms);
+    if (c128 <= c64) return launch<128>(w, jobs, chained, status, limit, stream, num_sms);
     return launch<64>(w, jobs, chained, status, limit, stream, num_sms);
 }
 
