@@ -45,18 +45,26 @@ constexpr int kABytes = kRows * 128;
 constexpr int kMaxJobs = 2;
 constexpr int kFewRows = 8;                        // tokens up to which matvec.cu streams the weights
 
+constexpr int kRingBytes = 230400;                 // of shared memory, for the stages
+constexpr int kMaxStages = 16;
+constexpr int kNumBars = 2 * kMaxStages + 5;
+constexpr int kOffMisc = kRingBytes + kNumBars * 8;
+constexpr int kSmem = kRingBytes + 1024 + 1024;
+static_assert(kSmem <= 232448 && kOffMisc + 32 <= kRingBytes + 1024, "shared memory budget");
+
 template <int kN>
 struct Tile {
     static constexpr int kBRows = kN / 2;          // of B a CTA
     static constexpr int kBBytes = kBRows * 128;
-    static constexpr int kStageBytes = kABytes + kBBytes;
-    static constexpr int kStages = (232448 - 2048) / kStageBytes;
+    // Of 64 k a stage: the short stages of narrow items take two (64 tokens 26.8 us with one,
+    // 23.4 with two, 26.3 with three, whose ring has three stages).
+    static constexpr int kAtoms = kN == 64 ? 2 : 1;
     static constexpr int kCols = 2 * kN;           // of tensor memory
-    static constexpr int kOffBars = kStages * kStageBytes;
-    static constexpr int kNumBars = 2 * kStages + 5;
-    static constexpr int kOffMisc = kOffBars + kNumBars * 8;
-    static constexpr int kSmem = kOffMisc + 32 + 1024;
-    static_assert(kSmem <= 232448, "shared memory budget");
+    // Narrow items, those of few tokens, have stages that hold no more rows of A than the jobs do.
+    static constexpr bool kSized = kN == 64;
+    static constexpr int kStageBytes = kAtoms * (kABytes + kBBytes);
+    static constexpr int kStages = kRingBytes / kStageBytes;
+    static_assert(kStages <= kMaxStages);
 };
 
 enum Epilogue { kStore, kGate, kGateBack };
@@ -78,6 +86,7 @@ struct Args {
     CUtensorMap a[kMaxJobs], b[kMaxJobs], b_half[kMaxJobs];      // b_half: boxes of half the rows
     Job job[kMaxJobs];
     int jobs, items;
+    int stages, stage_bytes, a_bytes;        // of the ring: atoms of A, then those of B
     int *status;
     uint64_t wait_limit_ns;
 };
@@ -98,12 +107,15 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap *m
         : "memory");
 }
 
-__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// Descriptors by halves: a stage moves their addresses, all in the lower one.
+__device__ __forceinline__ void mma_pair(uint32_t d, uint32_t a, uint32_t a_hi, uint32_t b, uint32_t b_hi, uint32_t idesc,
+                                         uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "mov.b64 da, {%1, %2};\n\tmov.b64 db, {%3, %4};\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %5, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(a_hi), "r"(b), "r"(b_hi), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 
@@ -121,12 +133,13 @@ __device__ __forceinline__ uint64_t smem_desc_mn(uint32_t saddr) {
 
 __device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *status,
                                        uint64_t lim) {
-    return warp_wait_bounded(bar, parity, abort_flag, status, lim);
+    return wait_bounded(bar, parity, abort_flag, status, lim);
 }
 
+// By one thread.
 __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *status,
                                      uint64_t lim) {
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if (mbar_try_wait(bar, parity)) return true;
     return wait_slow(bar, parity, abort_flag, status, lim);
 }
 
@@ -156,7 +169,7 @@ __device__ __noinline__ uint32_t odd_bytes(const Args &p, int first, int step, u
     }
     const Item it = item_of(p, item);
     const Job &w = p.job[it.job];
-    return w.odd_a * w.a_rows * 128 + (Tile<kN>::kBBytes >> it.half);
+    return Tile<kN>::kAtoms * (w.odd_a * w.a_rows * 128 + (Tile<kN>::kBBytes >> it.half));
 }
 
 // 16 consecutive outputs of a row at column n: n columns are a multiple of 8.
@@ -207,10 +220,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ffn_ker
     using T = Tile<kN>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + T::kOffBars);      // the even CTA's count
-    uint64_t *empty = full + T::kStages;
-    uint64_t *acc_full = empty + T::kStages, *acc_empty = acc_full + 2, *final_bar = acc_empty + 2;
-    Misc *misc = reinterpret_cast<Misc *>(smem + T::kOffMisc);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kRingBytes);       // the even CTA's count
+    uint64_t *empty = full + kMaxStages;
+    uint64_t *acc_full = empty + kMaxStages, *acc_empty = acc_full + 2, *final_bar = acc_empty + 2;
+    Misc *misc = reinterpret_cast<Misc *>(smem + kOffMisc);
+    const uint32_t n_stages = T::kSized ? p.stages : T::kStages;
+    const uint32_t stage_bytes = T::kSized ? p.stage_bytes : T::kStageBytes, a_bytes = T::kSized ? p.a_bytes : kABytes;
     volatile int *abort_flag = &misc->abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
@@ -220,7 +235,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ffn_ker
     if (threadIdx.x == 0) {
         misc->abort = 0;
         misc->issued = 0;
-        for (int i = 0; i < T::kStages; ++i) {
+        for (uint32_t i = 0; i < n_stages; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
         }
@@ -241,97 +256,101 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ffn_ker
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    // The two loops that feed the tensor core run in one warp each, an instruction after the
-    // other: what they need of a job is in registers ahead of them (read from the parameters
-    // stage by stage it made a stage 240 ns at least, whatever its work).
+    // The two loops that feed the tensor core are one thread each, an instruction after the
+    // other: no votes or reconvergence of a warp, and what they need of a job in registers
+    // ahead of them (64 tokens: read from the parameters stage by stage 265 ns a stage whatever
+    // its work, from registers 172).
     if (warp == kProducerWarp) {
-        const bool leader = elect_one();
-        const uint32_t base = smem_u32(smem), bar0 = cluster_addr(full, 0);
-        uint32_t slot = 0, phase = 1, issued = 0;
-        bool ok = true;
-        for (int i = first; ok && i < p.items; i += step) {
-            const Item it = item_of(p, i);
-            const Job &w = p.job[it.job];
-            const CUtensorMap *ma = &p.a[it.job], *mb = it.half ? &p.b_half[it.job] : &p.b[it.job];
-            const int b_rows = T::kBRows >> it.half;
-            const int row_a = it.m0 + rank * kRows;
-            const int row_b = it.n0 + rank * (w.epilogue == kGate ? w.b_step : b_rows);
-            const uint32_t bytes = w.a_rows * 128 * (1 + w.odd_a) + 2 * (T::kBBytes >> it.half);
-            const bool a_mn = w.a_mn, b_mn = w.b_mn, has_a = rank == 0 || w.odd_a;
-            const int k_end = w.k_stages * kStageK;
-            for (int k = 0; k < k_end; k += kStageK) {
-                ok = wait(&empty[slot], phase, abort_flag, p.status, lim);
-                if (!ok) break;
-                if (leader) {
-                    const uint32_t a = base + slot * T::kStageBytes, b = a + kABytes, bar = bar0 + slot * 8;
+        if (elect_one()) {
+            const uint32_t base = smem_u32(smem), bar0 = cluster_addr(full, 0);
+            uint32_t slot = 0, phase = 1, issued = 0;
+            bool ok = true;
+            for (int i = first; ok && i < p.items; i += step) {
+                const Item it = item_of(p, i);
+                const Job &w = p.job[it.job];
+                const CUtensorMap *ma = &p.a[it.job], *mb = it.half ? &p.b_half[it.job] : &p.b[it.job];
+                const int b_rows = T::kBRows >> it.half;
+                const int row_a = it.m0 + rank * kRows;
+                const int row_b = it.n0 + rank * (w.epilogue == kGate ? w.b_step : b_rows);
+                const uint32_t bytes = T::kAtoms * (w.a_rows * 128 * (1 + w.odd_a) + 2 * (T::kBBytes >> it.half));
+                const bool a_mn = w.a_mn, b_mn = w.b_mn, has_a = rank == 0 || w.odd_a;
+                const int k_end = w.k_stages * T::kAtoms * kStageK;
+                for (int k = 0; k < k_end; k += T::kAtoms * kStageK) {
+                    ok = wait(&empty[slot], phase, abort_flag, p.status, lim);
+                    if (!ok) break;
+                    const uint32_t bar = bar0 + slot * 8;
                     if (rank == 0) mbar_arrive_expect_tx(&full[slot], bytes);
-                    if (a_mn) {
-                        tma_load_pair(a, ma, row_a, k, bar);
-                        tma_load_pair(a + 8192, ma, row_a + 64, k, bar);
-                    } else if (has_a) {
-                        tma_load_pair(a, ma, k, row_a, bar);
-                    }
-                    if (b_mn) {
 #pragma unroll
-                        for (int q = 0; q < T::kBRows / 64 * 64; q += 64)
-                            if (q < b_rows) tma_load_pair(b + q * 128, mb, row_b + q, k, bar);
-                    } else {
-                        tma_load_pair(b, mb, k, row_b, bar);
+                    for (int h = 0; h < T::kAtoms; ++h) {
+                        const uint32_t a = base + slot * stage_bytes + h * a_bytes;
+                        const uint32_t b = base + slot * stage_bytes + T::kAtoms * a_bytes + h * T::kBBytes;
+                        const int at = k + h * kStageK;
+                        if (a_mn) {
+                            tma_load_pair(a, ma, row_a, at, bar);
+                            tma_load_pair(a + 8192, ma, row_a + 64, at, bar);
+                        } else if (has_a) {
+                            tma_load_pair(a, ma, at, row_a, bar);
+                        }
+                        if (b_mn) {
+#pragma unroll
+                            for (int q = 0; q < T::kBRows / 64 * 64; q += 64)
+                                if (q < b_rows) tma_load_pair(b + q * 128, mb, row_b + q, at, bar);
+                        } else {
+                            tma_load_pair(b, mb, at, row_b, bar);
+                        }
                     }
+                    ++issued;
+                    slot = slot + 1 == n_stages ? 0 : slot + 1;
+                    phase ^= slot == 0;
                 }
-                __syncwarp();
-                ++issued;
-                slot = slot + 1 == T::kStages ? 0 : slot + 1;
-                phase ^= slot == 0;
             }
+            misc->issued = issued;
         }
-        if (lane == 0) misc->issued = issued;
     } else if (warp == kIssuerWarp && rank == 0) {
-        const bool leader = elect_one();
-        const uint32_t base = smem_u32(smem);
-        uint32_t slot = 0, phase = 0, buf = 0, acc_phase = 1;
-        bool ok = true;
-        for (int i = first; ok && i < p.items; i += step) {
-            const Item it = item_of(p, i);
-            const Job &w = p.job[it.job];
-            const uint32_t idesc = idesc_bf16_f32(2 * kRows, kN >> it.half) | (w.a_mn ? 1u << 15 : 0) | (w.b_mn ? 1u << 16 : 0);
-            // 16 k further: 32 bytes along a row, or 16 rows of 128 bytes.
-            const uint32_t a_step = w.a_mn ? 128 : 2, b_step = w.b_mn ? 128 : 2;
-            const uint64_t da0 = w.a_mn ? smem_desc_mn(base) : smem_desc_sw128(base);
-            const uint64_t db0 = w.b_mn ? smem_desc_mn(base + kABytes) : smem_desc_sw128(base + kABytes);
-            const uint32_t d = tmem + buf * kN;
-            const int k_stages = w.k_stages;
-            ok = wait(&acc_empty[buf], acc_phase, abort_flag, p.status, lim);
-            tc_fence_after();
-            for (int ks = 0; ok && ks < k_stages; ++ks) {
-                ok = wait(&full[slot], phase, abort_flag, p.status, lim);
-                if (!ok) break;
+        if (elect_one()) {
+            const uint32_t base = smem_u32(smem);
+            uint32_t slot = 0, phase = 0, buf = 0, acc_phase = 1;
+            bool ok = true;
+            for (int i = first; ok && i < p.items; i += step) {
+                const Item it = item_of(p, i);
+                const Job &w = p.job[it.job];
+                const uint32_t idesc = idesc_bf16_f32(2 * kRows, kN >> it.half) | (w.a_mn ? 1u << 15 : 0) | (w.b_mn ? 1u << 16 : 0);
+                // 16 k further: 32 bytes along a row, or 16 rows of 128 bytes.
+                const uint32_t a_step = w.a_mn ? 128 : 2, b_step = w.b_mn ? 128 : 2;
+                const uint64_t da0 = w.a_mn ? smem_desc_mn(base) : smem_desc_sw128(base);
+                const uint64_t db0 = w.b_mn ? smem_desc_mn(base + T::kAtoms * a_bytes) : smem_desc_sw128(base + T::kAtoms * a_bytes);
+                const uint32_t d = tmem + buf * kN;
+                const int k_stages = w.k_stages;
+                ok = wait(&acc_empty[buf], acc_phase, abort_flag, p.status, lim);
                 tc_fence_after();
-                if (leader) {
-                    const uint64_t da = da0 + slot * (T::kStageBytes / 16), db = db0 + slot * (T::kStageBytes / 16);
+                for (int ks = 0; ok && ks < k_stages; ++ks) {
+                    ok = wait(&full[slot], phase, abort_flag, p.status, lim);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t at = slot * (stage_bytes >> 4), da = static_cast<uint32_t>(da0) + at,
+                                   db = static_cast<uint32_t>(db0) + at;
 #pragma unroll
-                    for (int t = 0; t < kStageK / 16; ++t)
-                        mma_pair(d, da + t * a_step, db + t * b_step, idesc, t > 0 || ks > 0);
+                    for (int t = 0; t < T::kAtoms * kStageK / 16; ++t)
+                        mma_pair(d, da + (t & 3) * a_step + (t >> 2) * (a_bytes >> 4), da0 >> 32,
+                                 db + (t & 3) * b_step + (t >> 2) * (T::kBBytes >> 4), db0 >> 32, idesc, t > 0 || ks > 0);
                     mma_commit_pair(&empty[slot], 3);
                     if (ks == k_stages - 1) mma_commit_pair(&acc_full[buf], 3);
+                    slot = slot + 1 == n_stages ? 0 : slot + 1;
+                    phase ^= slot == 0;
                 }
-                __syncwarp();
-                slot = slot + 1 == T::kStages ? 0 : slot + 1;
-                phase ^= slot == 0;
+                buf ^= 1u;
+                acc_phase ^= buf == 0;
             }
-            buf ^= 1u;
-            acc_phase ^= buf == 0;
+            mma_commit_pair(final_bar, 1);
+            wait(final_bar, 0, nullptr, p.status, lim);
         }
-        if (leader) mma_commit_pair(final_bar, 1);
-        __syncwarp();
-        wait(final_bar, 0, nullptr, p.status, lim);
     } else if (warp >= kEpilogueWarp) {
         const int quarter = warp & 3;
         uint32_t buf = 0, phase = 0;
         for (int i = first; i < p.items; i += step) {
             const Item it = item_of(p, i);
             const Job &w = p.job[it.job];
-            if (!wait(&acc_full[buf], phase, abort_flag, p.status, lim)) break;
+            if (!warp_wait_bounded(&acc_full[buf], phase, abort_flag, p.status, lim)) break;
             tc_fence_after();
             const uint32_t acc = tmem + buf * kN + (static_cast<uint32_t>(quarter * 32) << 16);
             const int64_t row = it.m0 + static_cast<int64_t>(rank) * kRows + quarter * 32 + lane;
@@ -416,9 +435,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ffn_ker
         if (misc->odd_abort || misc->abort) {       // every copy that was issued lands before the pair leaves
             const uint32_t n1 = misc->odd_issued;
             const uint32_t n0 = misc->issued, n = n0 > n1 ? n0 : n1;
-            for (uint32_t i = pair_first(n0, n1, T::kStages); i < n; ++i) {
-                uint64_t *bar = &full[i % T::kStages];
-                const uint32_t parity = (i / T::kStages) & 1u;
+            for (uint32_t i = pair_first(n0, n1, n_stages); i < n; ++i) {
+                uint64_t *bar = &full[i % n_stages];
+                const uint32_t parity = (i / n_stages) & 1u;
                 if (mbar_try_wait(bar, parity)) continue;
                 const PairFix f = pair_fix(i, n0, n1, odd_bytes<kN>(p, first, step, i));
                 if (f.arrive) mbar_arrive_expect_tx(bar, f.expect);
@@ -495,7 +514,7 @@ moe_status launch(const Product *w, int jobs, bool chained, int *status, uint64_
         o.b_step = gate ? o.n : 0;
         o.tiles_m = (o.m + 2 * kRows - 1) / (2 * kRows);
         o.tiles_n = (o.n + o.tile_cols - 1) / o.tile_cols;
-        o.k_stages = (o.k + kStageK - 1) / kStageK;
+        o.k_stages = (o.k + T::kAtoms * kStageK - 1) / (T::kAtoms * kStageK);
         // Up to 128 rows, the box holds no more of them and the odd CTA copies none: its half of
         // the products, of what is left in its memory, goes nowhere (their boxes would cost what full ones do).
         const bool few = !w[j].a.mn && o.m <= kRows;
@@ -526,12 +545,21 @@ moe_status launch(const Product *w, int jobs, bool chained, int *status, uint64_
             return MOE_ERR_CUDA;
     }
     p.items = static_cast<int>(items);
+    // With few rows of A more stages are on their way (64 tokens 23.4 -> 21.3 us).  The MMAs read
+    // 128 rows all the same, what lies behind A among them, whose products nobody reads; the
+    // last stage's lie within the ring.
+    int a_rows = 0;
+    for (int j = 0; j < jobs; ++j) a_rows = p.job[j].a_rows > a_rows ? p.job[j].a_rows : a_rows;
+    p.a_bytes = a_rows * 128;              // a multiple of 1,024
+    p.stage_bytes = T::kAtoms * (p.a_bytes + T::kBBytes);
+    p.stages = (kRingBytes - T::kStageBytes) / p.stage_bytes + 1;
+    if (p.stages > kMaxStages) p.stages = kMaxStages;
     static std::atomic<uint64_t> mask{0};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
     const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
     if (!bit || !(mask.load(std::memory_order_acquire) & bit)) {
-        if (cudaFuncSetAttribute(ffn_kernel<kN>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmem) != cudaSuccess)
+        if (cudaFuncSetAttribute(ffn_kernel<kN>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
             return MOE_ERR_CUDA;
         mask.fetch_or(bit, std::memory_order_release);
     }
@@ -542,7 +570,7 @@ moe_status launch(const Product *w, int jobs, bool chained, int *status, uint64_
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * pairs);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = T::kSmem;
+    cfg.dynamicSmemBytes = kSmem;
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = chained ? 1 : 0;
@@ -550,8 +578,8 @@ moe_status launch(const Product *w, int jobs, bool chained, int *status, uint64_
 }
 
 // The width of items: rounds over the pairs times what a stage takes (about 0.17, 0.23 and
-// 0.33 us: TMA's rows of A and B).  Wide items read A less often, narrow ones leave fewer SMs
-// idle.  hidden 4,096, inter 2,048, forward: 64 tokens 41 us with 256 columns and 26 with 64,
+// 0.33 us for 64 k: TMA's rows of A and B, and what a stage costs by itself).  Wide items read A less often, narrow ones leave fewer SMs
+// idle.  hidden 4,096, inter 2,048, forward: 64 tokens 41 us with 256 columns and 21 with 64,
 // 512 tokens 42 us with 64 and 29 with 128, 1,024 tokens 45 us with 128 and 41 with 256.  B
 // along n comes in boxes of 64, the two CTAs' make 128.
 moe_status run(const Product *w, int jobs, bool chained, int *status, uint64_t limit, cudaStream_t stream, int num_sms) {
