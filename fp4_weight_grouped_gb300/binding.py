@@ -526,6 +526,17 @@ def _workspace(ws, device, stream):
     return ws
 
 
+_current_device = _raw_device or torch.cuda.current_device
+
+
+def _here(*tensors):
+    """The library works on the current device: tensors of another one are refused."""
+    device = _current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"a tensor on {t.device}, the current device is cuda:{device}")
+
+
 def _rows_of(name: str, t: torch.Tensor) -> int:
     """Row stride, in elements, of a 2-D tensor whose rows are contiguous."""
     if t.dim() != 2 or t.dtype not in (torch.float32, torch.bfloat16):
@@ -829,6 +840,7 @@ def fp4_matvec(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, fmt: 
         out = _empty((rows, N), out_dtype, x.device, stream)
     _need("out", out, (rows, N), torch.float32, torch.bfloat16)
     workspace = _workspace(workspace, x.device, stream)
+    _here(x, codes, scales, row_expert, weight_scale_2, out, workspace)
     rc = load().moe_fp4_matvec(_ptr(x), stride, index_div, _ptr(row_expert), rows, K, _ptr(codes), _ptr(scales),
                                _tensor_scale("weight_scale_2", weight_scale_2, E, fmt), fmt, E, N, _ptr(out),
                                _dtype_code(out.dtype), _ptr(workspace), workspace.numel(), _stream(stream))
@@ -850,6 +862,7 @@ def fp4_matvec_swiglu(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor
         out = _empty((rows, I), torch.bfloat16, x.device, stream)
     _need("out", out, (rows, I), torch.bfloat16)
     workspace = _workspace(workspace, x.device, stream)
+    _here(x, codes, scales, row_expert, weight_scale_2, out, workspace)
     rc = load().moe_fp4_matvec_swiglu(_ptr(x), stride, index_div, _ptr(row_expert), rows, K, _ptr(codes),
                                       _ptr(scales), _tensor_scale("weight_scale_2", weight_scale_2, E, fmt), fmt,
                                       E, I, _ptr(out), _ptr(workspace), workspace.numel(), _stream(stream))
@@ -886,6 +899,7 @@ def layer_decode(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor, 
     _room("y2", y2, T * k * hidden, torch.float32)
     _need("out", out, (T, hidden), torch.float32, torch.bfloat16)
     workspace = _workspace(workspace, x.device, stream)
+    _here(x, topk_ids, topk_w, c13, s13, g13, c2, s2, g2, h, y2, out, workspace)
     rc = load().moe_layer_decode(
         _ptr(x), _ptr(topk_ids), _ptr(topk_w), T, k, E, hidden, inter, fmt, _ptr(c13), _ptr(s13),
         _tensor_scale("w13 weight_scale_2", g13, E, fmt), _ptr(c2), _ptr(s2),
@@ -925,6 +939,7 @@ def ffn_forward(x: torch.Tensor, w13: torch.Tensor, w2: torch.Tensor, h: torch.T
         out = _empty((T, hidden), out_dtype, x.device, stream)
     _need("out", out, (T, hidden), torch.float32, torch.bfloat16)
     workspace = _workspace(workspace, x.device, stream)
+    _here(x, w13, w2, h, gu, out, workspace)
     rc = load().moe_ffn_forward(_ptr(x), stride, T, hidden, inter, _ptr(w13), _ptr(w2), _ptr(gu), _ptr(h), _ptr(out),
                                 _dtype_code(out.dtype), _ptr(workspace), workspace.numel(), _stream(stream))
     _check(rc, "moe_ffn_forward")
@@ -959,6 +974,7 @@ def ffn_backward(dout: torch.Tensor, x: torch.Tensor, w13: torch.Tensor, w2: tor
             raise ValueError("dw13 and dw2: one type is needed")
     dw = dw13 if dw13 is not None else dw2
     workspace = _workspace(workspace, x.device, stream)
+    _here(dout, x, w13, w2, h, gu, dgu, dx, dw13, dw2, workspace)
     rc = load().moe_ffn_backward(_ptr(dout), _ptr(x), stride, T, hidden, inter, _ptr(w13), _ptr(w2), _ptr(h),
                                  _ptr(gu), _ptr(dgu), _ptr(dx), _ptr(dw13), _ptr(dw2),
                                  MOE_BF16 if dw is None else _dtype_code(dw.dtype), _ptr(workspace),
@@ -975,10 +991,11 @@ _GRAD_DTYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 def _grad_arrays(grads, name="grads"):
     """Pointers, sizes and types of a list of gradients, as arrays that the library reads."""
     ptrs, sizes, dtypes = array("Q"), array("q"), array("i")
+    device = _current_device()
     for t in grads:
         dtype = _GRAD_DTYPES.get(t.dtype)
-        if dtype is None or not (t.is_contiguous() and t.is_cuda):
-            raise ValueError(f"{name}[{len(ptrs)}]: a contiguous float32 or bfloat16 CUDA tensor is needed")
+        if dtype is None or not t.is_contiguous() or t.get_device() != device:
+            raise ValueError(f"{name}[{len(ptrs)}]: a contiguous float32 or bfloat16 tensor on the current device is needed")
         ptrs.append(t.data_ptr())
         sizes.append(t.numel())
         dtypes.append(dtype)
@@ -996,6 +1013,7 @@ def _grad_call(grads, norm, workspace, stream):
     _need("norm", norm, (1,), torch.float32)
     if workspace is None:
         workspace = _empty((MOE_GRAD_WORKSPACE_BYTES,), torch.uint8, device, stream)
+    _here(norm, workspace)
     return norm, _workspace(workspace, device, stream)
 
 
