@@ -529,12 +529,45 @@ def _workspace(ws, device, stream):
 _current_device = _raw_device or torch.cuda.current_device
 
 
-def _here(*tensors):
-    """The library works on the current device: tensors of another one are refused."""
-    device = _current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != device:
-            raise ValueError(f"a tensor on {t.device}, the current device is cuda:{device}")
+def _take(name: str, t: torch.Tensor, shape, dtypes, device: int) -> int:
+    """Address of a tensor that the library reads or writes as raw memory of the current
+    device: refused where it is not what the call takes for it."""
+    if t.dtype in dtypes and t.shape == shape and t.is_contiguous() and t.get_device() == device:
+        return t.data_ptr()
+    _need(name, t, shape, *dtypes)
+    raise ValueError(f"{name}: on {t.device}, the current device is cuda:{device}")
+
+
+def _take_room(name: str, t: torch.Tensor, n: int, dtype, device: int) -> int:
+    """Address of a buffer with room for n elements, which the call lays out itself."""
+    if t.numel() >= n and t.dtype == dtype and t.is_contiguous() and t.get_device() == device:
+        return t.data_ptr()
+    _room(name, t, n, dtype)
+    raise ValueError(f"{name}: on {t.device}, the current device is cuda:{device}")
+
+
+def _take_rows(name: str, t: torch.Tensor, device: int):
+    """Address and row stride, in elements, of a bf16 matrix whose rows are contiguous."""
+    stride = _rows_of(name, t)
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected torch.bfloat16")
+    if t.get_device() != device:
+        raise ValueError(f"{name}: on {t.device}, the current device is cuda:{device}")
+    return t.data_ptr(), stride
+
+
+def _take_workspace(ws, like: torch.Tensor, stream, device: int):
+    """Address and size of the call's workspace, and the tensor itself where the call made it."""
+    if ws is None:
+        ws = make_workspace(0, 1, 1, like.device, stream)
+    elif not (ws.is_contiguous() and ws.get_device() == device):
+        _workspace(ws, like.device, stream)
+        raise ValueError(f"workspace: on {ws.device}, the current device is cuda:{device}")
+    return ws.data_ptr(), ws.numel() * ws.element_size(), ws
+
+
+_BF16, _U8, _I32, _F32, _FLOATS = ((torch.bfloat16,), (torch.uint8,), (torch.int32,), (torch.float32,),
+                                   (torch.float32, torch.bfloat16))
 
 
 def _rows_of(name: str, t: torch.Tensor) -> int:
@@ -807,24 +840,29 @@ def layer_forward_fp4(x, topk_ids, topk_w, w13, w2, buffers: LayerBuffersFp4, x_
 
 # ------------------------------------------------------- a few tokens in 4 bits
 
-def _matvec_operands(x, codes, scales, fmt, row_expert, index_div):
-    stride = _rows_of("x", x)
-    if x.dtype != torch.bfloat16:
-        raise ValueError(f"x: dtype {x.dtype}, expected torch.bfloat16")
+def _scale_2(name, t, n, fmt, device):
+    if fmt != MOE_FP4_NV:
+        return None
+    if t is None:
+        raise ValueError(f"{name} is needed for NVFP4")
+    return _take(name, t, (n,), _F32, device)
+
+
+def _matvec_operands(x, codes, scales, fmt, row_expert, index_div, weight_scale_2, device):
+    px, stride = _take_rows("x", x, device)
     if index_div < 1:
         raise ValueError("index_div: at least 1 is needed")
-    K = x.shape[1]
+    x_rows, K = x.shape
     E, N, _ = codes.shape
-    if row_expert is None:
-        rows = x.shape[0] * index_div
-    else:
+    rows, ids = x_rows * index_div, None
+    if row_expert is not None:
         rows = row_expert.numel()
-        _need("row_expert", row_expert, (rows,), torch.int32)
-        if rows > x.shape[0] * index_div:
-            raise ValueError(f"x: {x.shape[0]} rows, {-(-rows // index_div)} are needed")
-    _need("codes", codes, (E, N, K // 2), torch.uint8)
-    _need("scales", scales, (E, N, K // _fp4_block(fmt)), torch.uint8)
-    return stride, rows, K, E, N
+        ids = _take("row_expert", row_expert, (rows,), _I32, device)
+        if rows > x_rows * index_div:
+            raise ValueError(f"x: {x_rows} rows, {-(-rows // index_div)} are needed")
+    return (px, stride, index_div, ids, rows, K, _take("codes", codes, (E, N, K // 2), _U8, device),
+            _take("scales", scales, (E, N, K // _fp4_block(fmt)), _U8, device),
+            _scale_2("weight_scale_2", weight_scale_2, E, fmt, device), fmt, E), rows, N
 
 
 def fp4_matvec(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, fmt: int,
@@ -835,15 +873,13 @@ def fp4_matvec(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, fmt: 
     (bf16, any row stride) times the weights of expert row_expert[r] (int32 [rows]; None: expert
     0).  codes uint8 [E, N, K/2], scales [E, N, K/32 or K/16], weight_scale_2 f32 [E] (NVFP4) ->
     out [rows, N] (f32 or bf16).  Bad experts and scales are reported in the workspace."""
-    stride, rows, K, E, N = _matvec_operands(x, codes, scales, fmt, row_expert, index_div)
+    device = _current_device()
+    args, rows, N = _matvec_operands(x, codes, scales, fmt, row_expert, index_div, weight_scale_2, device)
     if out is None:
         out = _empty((rows, N), out_dtype, x.device, stream)
-    _need("out", out, (rows, N), torch.float32, torch.bfloat16)
-    workspace = _workspace(workspace, x.device, stream)
-    _here(x, codes, scales, row_expert, weight_scale_2, out, workspace)
-    rc = load().moe_fp4_matvec(_ptr(x), stride, index_div, _ptr(row_expert), rows, K, _ptr(codes), _ptr(scales),
-                               _tensor_scale("weight_scale_2", weight_scale_2, E, fmt), fmt, E, N, _ptr(out),
-                               _dtype_code(out.dtype), _ptr(workspace), workspace.numel(), _stream(stream))
+    po = _take("out", out, (rows, N), _FLOATS, device)
+    ws, n, made = _take_workspace(workspace, x, stream, device)
+    rc = load().moe_fp4_matvec(*args, N, po, _dtype_code(out.dtype), ws, n, _stream(stream))
     _check(rc, "moe_fp4_matvec")
     return out
 
@@ -854,18 +890,16 @@ def fp4_matvec_swiglu(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor
                       workspace: torch.Tensor | None = None, stream=None):
     """fp4_matvec with w13 weights (codes [E, 2I, K/2], gate rows first) and SwiGLU behind it
     -> h bf16 [rows, I]."""
-    stride, rows, K, E, N = _matvec_operands(x, codes, scales, fmt, row_expert, index_div)
+    device = _current_device()
+    args, rows, N = _matvec_operands(x, codes, scales, fmt, row_expert, index_div, weight_scale_2, device)
     if N % 2:
         raise ValueError("codes: an odd number of gate and up rows")
     I = N // 2
     if out is None:
         out = _empty((rows, I), torch.bfloat16, x.device, stream)
-    _need("out", out, (rows, I), torch.bfloat16)
-    workspace = _workspace(workspace, x.device, stream)
-    _here(x, codes, scales, row_expert, weight_scale_2, out, workspace)
-    rc = load().moe_fp4_matvec_swiglu(_ptr(x), stride, index_div, _ptr(row_expert), rows, K, _ptr(codes),
-                                      _ptr(scales), _tensor_scale("weight_scale_2", weight_scale_2, E, fmt), fmt,
-                                      E, I, _ptr(out), _ptr(workspace), workspace.numel(), _stream(stream))
+    po = _take("out", out, (rows, I), _BF16, device)
+    ws, n, made = _take_workspace(workspace, x, stream, device)
+    rc = load().moe_fp4_matvec_swiglu(*args, I, po, ws, n, _stream(stream))
     _check(rc, "moe_fp4_matvec_swiglu")
     return out
 
@@ -876,50 +910,43 @@ def layer_decode(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor, 
                  workspace: torch.Tensor | None = None, stream=None):
     """The routed-expert layer for a few tokens (T * k up to MOE_MATVEC_MAX_ROWS): x bf16 [T,
     hidden], w13 and w2 (codes, scales, weight_scale_2 or None) -> out [T, hidden] (f32 or
-    bf16).  h bf16 [T*k, inter] and y2 f32 [T*k, hidden] are intermediates, made when not given."""
-    block = _fp4_block(fmt)
+    bf16).  h bf16 [T*k, inter] and y2 f32 [T*k, hidden] are intermediates, made when not given;
+    buffers of a larger call serve a smaller one."""
+    device, block = _current_device(), _fp4_block(fmt)
     (c13, s13, g13), (c2, s2, g2) = w13, w2
     T, k = topk_ids.shape
     E, two_i, half = c13.shape
     hidden, inter = 2 * half, two_i // 2
-    _need("x", x, (T, hidden), torch.bfloat16)
-    _need("topk_ids", topk_ids, (T, k), torch.int32)
-    _need("topk_w", topk_w, (T, k), torch.float32)
-    _need("w13 codes", c13, (E, 2 * inter, hidden // 2), torch.uint8)
-    _need("w13 scales", s13, (E, 2 * inter, hidden // block), torch.uint8)
-    _need("w2 codes", c2, (E, hidden, inter // 2), torch.uint8)
-    _need("w2 scales", s2, (E, hidden, inter // block), torch.uint8)
     if h is None:
         h = _empty((T * k, inter), torch.bfloat16, x.device, stream)
     if y2 is None:
         y2 = _empty((T * k, hidden), torch.float32, x.device, stream)
     if out is None:
         out = _empty((T, hidden), out_dtype, x.device, stream)
-    _room("h", h, T * k * inter, torch.bfloat16)
-    _room("y2", y2, T * k * hidden, torch.float32)
-    _need("out", out, (T, hidden), torch.float32, torch.bfloat16)
-    workspace = _workspace(workspace, x.device, stream)
-    _here(x, topk_ids, topk_w, c13, s13, g13, c2, s2, g2, h, y2, out, workspace)
+    ws, n, made = _take_workspace(workspace, x, stream, device)
     rc = load().moe_layer_decode(
-        _ptr(x), _ptr(topk_ids), _ptr(topk_w), T, k, E, hidden, inter, fmt, _ptr(c13), _ptr(s13),
-        _tensor_scale("w13 weight_scale_2", g13, E, fmt), _ptr(c2), _ptr(s2),
-        _tensor_scale("w2 weight_scale_2", g2, E, fmt), _ptr(h), _ptr(y2), _ptr(out), _dtype_code(out.dtype),
-        _ptr(workspace), workspace.numel(), _stream(stream))
+        _take("x", x, (T, hidden), _BF16, device), _take("topk_ids", topk_ids, (T, k), _I32, device),
+        _take("topk_w", topk_w, (T, k), _F32, device), T, k, E, hidden, inter, fmt,
+        _take("w13 codes", c13, (E, 2 * inter, hidden // 2), _U8, device),
+        _take("w13 scales", s13, (E, 2 * inter, hidden // block), _U8, device),
+        _scale_2("w13 weight_scale_2", g13, E, fmt, device),
+        _take("w2 codes", c2, (E, hidden, inter // 2), _U8, device),
+        _take("w2 scales", s2, (E, hidden, inter // block), _U8, device),
+        _scale_2("w2 weight_scale_2", g2, E, fmt, device), _take_room("h", h, T * k * inter, torch.bfloat16, device),
+        _take_room("y2", y2, T * k * hidden, torch.float32, device), _take("out", out, (T, hidden), _FLOATS, device),
+        _dtype_code(out.dtype), ws, n, _stream(stream))
     _check(rc, "moe_layer_decode")
     return out
 
 
 # ------------------------------------------------------- dense gated feed-forward block
 
-def _ffn_operands(x, w13, w2):
-    stride = _rows_of("x", x)
-    if x.dtype != torch.bfloat16:
-        raise ValueError(f"x: dtype {x.dtype}, expected torch.bfloat16")
+def _ffn_operands(x, w13, w2, device):
+    px, stride = _take_rows("x", x, device)
     T, hidden = x.shape
     inter = w13.shape[0] // 2
-    _need("w13", w13, (2 * inter, hidden), torch.bfloat16)
-    _need("w2", w2, (hidden, inter), torch.bfloat16)
-    return stride, T, hidden, inter
+    return (px, stride, T, hidden, inter, _take("w13", w13, (2 * inter, hidden), _BF16, device),
+            _take("w2", w2, (hidden, inter), _BF16, device)), T, hidden, inter
 
 
 def ffn_forward(x: torch.Tensor, w13: torch.Tensor, w2: torch.Tensor, h: torch.Tensor | None = None,
@@ -929,19 +956,16 @@ def ffn_forward(x: torch.Tensor, w13: torch.Tensor, w2: torch.Tensor, h: torch.T
     hidden] (gate rows first), w2 bf16 [hidden, inter] -> out [T, hidden] (bf16 or f32).  h bf16
     [T, inter] is made when not given; gu bf16 [T, 2*inter] is written when given.  The backward
     takes both."""
-    stride, T, hidden, inter = _ffn_operands(x, w13, w2)
+    device = _current_device()
+    args, T, hidden, inter = _ffn_operands(x, w13, w2, device)
     if h is None:
         h = _empty((T, inter), torch.bfloat16, x.device, stream)
-    _need("h", h, (T, inter), torch.bfloat16)
-    if gu is not None:
-        _need("gu", gu, (T, 2 * inter), torch.bfloat16)
     if out is None:
         out = _empty((T, hidden), out_dtype, x.device, stream)
-    _need("out", out, (T, hidden), torch.float32, torch.bfloat16)
-    workspace = _workspace(workspace, x.device, stream)
-    _here(x, w13, w2, h, gu, out, workspace)
-    rc = load().moe_ffn_forward(_ptr(x), stride, T, hidden, inter, _ptr(w13), _ptr(w2), _ptr(gu), _ptr(h), _ptr(out),
-                                _dtype_code(out.dtype), _ptr(workspace), workspace.numel(), _stream(stream))
+    ws, n, made = _take_workspace(workspace, x, stream, device)
+    rc = load().moe_ffn_forward(*args, None if gu is None else _take("gu", gu, (T, 2 * inter), _BF16, device),
+                                _take("h", h, (T, inter), _BF16, device), _take("out", out, (T, hidden), _FLOATS, device),
+                                _dtype_code(out.dtype), ws, n, _stream(stream))
     _check(rc, "moe_ffn_forward")
     return out
 
@@ -952,33 +976,26 @@ def ffn_backward(dout: torch.Tensor, x: torch.Tensor, w13: torch.Tensor, w2: tor
     """Gradients of ffn_forward: dout bf16 [T, hidden], and x, the weights, h and gu of the
     forward -> (dx bf16 [T, hidden], dw13 [2*inter, hidden], dw2 [hidden, inter]; bf16 or f32).
     An entry of `out` that is None is not computed.  dgu bf16 [T, 2*inter] is scratch."""
-    stride, T, hidden, inter = _ffn_operands(x, w13, w2)
-    _need("dout", dout, (T, hidden), torch.bfloat16)
-    _need("h", h, (T, inter), torch.bfloat16)
-    _need("gu", gu, (T, 2 * inter), torch.bfloat16)
+    device = _current_device()
+    args, T, hidden, inter = _ffn_operands(x, w13, w2, device)
     if dgu is None:
         dgu = _empty((T, 2 * inter), torch.bfloat16, x.device, stream)
-    _need("dgu", dgu, (T, 2 * inter), torch.bfloat16)
     if out is None:
         out = (_empty((T, hidden), torch.bfloat16, x.device, stream),
                _empty((2 * inter, hidden), dw_dtype, x.device, stream),
                _empty((hidden, inter), dw_dtype, x.device, stream))
     dx, dw13, dw2 = out
-    if dx is not None:
-        _need("dx", dx, (T, hidden), torch.bfloat16)
-    if dw13 is not None:
-        _need("dw13", dw13, (2 * inter, hidden), torch.float32, torch.bfloat16)
-    if dw2 is not None:
-        _need("dw2", dw2, (hidden, inter), torch.float32, torch.bfloat16)
-        if dw13 is not None and dw13.dtype != dw2.dtype:
-            raise ValueError("dw13 and dw2: one type is needed")
     dw = dw13 if dw13 is not None else dw2
-    workspace = _workspace(workspace, x.device, stream)
-    _here(dout, x, w13, w2, h, gu, dgu, dx, dw13, dw2, workspace)
-    rc = load().moe_ffn_backward(_ptr(dout), _ptr(x), stride, T, hidden, inter, _ptr(w13), _ptr(w2), _ptr(h),
-                                 _ptr(gu), _ptr(dgu), _ptr(dx), _ptr(dw13), _ptr(dw2),
-                                 MOE_BF16 if dw is None else _dtype_code(dw.dtype), _ptr(workspace),
-                                 workspace.numel(), _stream(stream))
+    if dw is not None and dw2 is not None and dw.dtype != dw2.dtype:
+        raise ValueError("dw13 and dw2: one type is needed")
+    ws, n, made = _take_workspace(workspace, x, stream, device)
+    rc = load().moe_ffn_backward(
+        _take("dout", dout, (T, hidden), _BF16, device), *args, _take("h", h, (T, inter), _BF16, device),
+        _take("gu", gu, (T, 2 * inter), _BF16, device), _take("dgu", dgu, (T, 2 * inter), _BF16, device),
+        None if dx is None else _take("dx", dx, (T, hidden), _BF16, device),
+        None if dw13 is None else _take("dw13", dw13, (2 * inter, hidden), _FLOATS, device),
+        None if dw2 is None else _take("dw2", dw2, (hidden, inter), _FLOATS, device),
+        MOE_BF16 if dw is None else _dtype_code(dw.dtype), ws, n, _stream(stream))
     _check(rc, "moe_ffn_backward")
     return out
 
@@ -1007,22 +1024,20 @@ def _address(a):
 
 
 def _grad_call(grads, norm, workspace, stream):
-    device = grads[0].device if grads else "cuda"
+    """The norm's tensor, its address, the workspace's address and size, and the workspace."""
+    device = _current_device()
     if norm is None:
-        norm = _empty((1,), torch.float32, device, stream)
-    _need("norm", norm, (1,), torch.float32)
+        norm = _empty((1,), torch.float32, grads[0].device if grads else "cuda", stream)
     if workspace is None:
-        workspace = _empty((MOE_GRAD_WORKSPACE_BYTES,), torch.uint8, device, stream)
-    _here(norm, workspace)
-    return norm, _workspace(workspace, device, stream)
+        workspace = _empty((MOE_GRAD_WORKSPACE_BYTES,), torch.uint8, norm.device, stream)
+    return norm, _take("norm", norm, (1,), _F32, device), *_take_workspace(workspace, norm, stream, device)
 
 
 def grad_norm(grads, norm: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
     """Global norm f32 [1] of a list of contiguous gradients (f32 or bf16 each)."""
     ptrs, sizes, dtypes = _grad_arrays(grads)
-    norm, workspace = _grad_call(grads, norm, workspace, stream)
-    rc = load().moe_grad_norm(_address(ptrs), _address(sizes), _address(dtypes), len(ptrs), _ptr(norm), _ptr(workspace), workspace.numel(),
-                              _stream(stream))
+    norm, pn, ws, n, made = _grad_call(grads, norm, workspace, stream)
+    rc = load().moe_grad_norm(_address(ptrs), _address(sizes), _address(dtypes), len(ptrs), pn, ws, n, _stream(stream))
     _check(rc, "moe_grad_norm")
     return norm
 
@@ -1038,9 +1053,9 @@ def clip_grads(grads, max_norm: float, eps: float = 1e-6, out=None, norm: torch.
         outs, osizes, odtypes = _grad_arrays(out, "out")
         if osizes != sizes or odtypes != dtypes:
             raise ValueError("out: not of the gradients' sizes and types")
-    norm, workspace = _grad_call(grads, norm, workspace, stream)
+    norm, pn, ws, n, made = _grad_call(grads, norm, workspace, stream)
     rc = load().moe_grad_clip(_address(ptrs), _address(sizes), _address(dtypes), len(ptrs), float(max_norm),
-                              float(eps), None if outs is None else _address(outs), _ptr(norm), _ptr(workspace), workspace.numel(), _stream(stream))
+                              float(eps), None if outs is None else _address(outs), pn, ws, n, _stream(stream))
     _check(rc, "moe_grad_clip")
     return norm
 

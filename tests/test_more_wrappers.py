@@ -181,3 +181,9 @@ def test_clipping(lib):
         with pytest.raises(ValueError):
             B.clip_grads(g, 1.0, norm=n, workspace=WS)
     assert not lib.calls
+
+
+def test_decode_takes_larger_intermediates(lib):
+    a = decode()
+    B.layer_decode(**{**a, "h": gpu((64, 32), BF), "y2": gpu((64, 64), F32)})
+    assert lib.calls[-1][0] == "moe_layer_decode"
