@@ -228,18 +228,19 @@ __device__ __forceinline__ void build_chunks(const Params &p, const Chunks &c) {
 // Power of two that a row of x is scaled by, from the exponent field of its largest magnitude.
 __device__ __forceinline__ int row_exponent(int top) { return max(top - 127 - 14, -126); }
 
-// Eight elements of a row of x; zeros past its end.
+// Eight elements of a row of x; zeros past its end.  Not through the read-only path: x may come
+// from a launch that ended after this one began.
 __device__ __forceinline__ uint4 load_x(const Params &p, int slot, int v) {
     uint4 a = make_uint4(0, 0, 0, 0);
     if (8 * v < p.K) {                // K is a multiple of 8
         const uint16_t *q = p.x + (slot / p.div) * p.x_stride + 8 * v;
         if (p.x_vec) {
-            a = __ldg(reinterpret_cast<const uint4 *>(q));
+            a = __ldcg(reinterpret_cast<const uint4 *>(q));
         } else {
-            a.x = __ldg(q) | static_cast<uint32_t>(__ldg(q + 1)) << 16;
-            a.y = __ldg(q + 2) | static_cast<uint32_t>(__ldg(q + 3)) << 16;
-            a.z = __ldg(q + 4) | static_cast<uint32_t>(__ldg(q + 5)) << 16;
-            a.w = __ldg(q + 6) | static_cast<uint32_t>(__ldg(q + 7)) << 16;
+            a.x = __ldcg(q) | static_cast<uint32_t>(__ldcg(q + 1)) << 16;
+            a.y = __ldcg(q + 2) | static_cast<uint32_t>(__ldcg(q + 3)) << 16;
+            a.z = __ldcg(q + 4) | static_cast<uint32_t>(__ldcg(q + 5)) << 16;
+            a.w = __ldcg(q + 6) | static_cast<uint32_t>(__ldcg(q + 7)) << 16;
         }
     }
     return a;
@@ -433,8 +434,7 @@ template <int F, bool kSwiglu, bool kTmaScales>
 __global__ void __launch_bounds__(kThreads, 1)
     matvec_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_s, const Params p) {
     using C = Fmt<F>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    extern __shared__ __align__(1024) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t4 = lane & 3;
     const int kw = p.kw, group = kWarps / kw, depth = p.depth;          // group: tiles an item
@@ -683,9 +683,11 @@ moe_status launch(Params p, cudaStream_t stream, int num_sms) {
     using C = Fmt<F>;
     p.k_pad = (p.K + C::kUnit - 1) / C::kUnit * C::kUnit;
     // Rows a chunk and stages of a ring, as many as there is room for; two stages at least.
-    const size_t rest = 1024 + kWarps * kMaxDepth * sizeof(uint64_t) + (2 * kTok + 2 + 4 * static_cast<size_t>(p.rows)) * sizeof(int);
+    const size_t rest = kWarps * kMaxDepth * sizeof(uint64_t) + (2 * kTok + 2 + 4 * static_cast<size_t>(p.rows)) * sizeof(int);
     const size_t x_row = static_cast<size_t>(p.k_pad) * 2 + 64 + kWarps * kSumPitch * sizeof(float);
-    p.tok = p.rows < kTok ? p.rows : kTok;
+    // Rows that share an expert, twice the average at most: room for x is taken from the rings.
+    const int64_t share = p.row_expert ? (2ll * p.rows + p.E - 1) / p.E : p.rows;
+    p.tok = static_cast<int>(share < kTok ? share : kTok);
     while (p.tok > 1 && rest + p.tok * x_row + 2 * kWarps * C::kStage > kMaxSmem) p.tok = (p.tok + 1) / 2;
     const size_t fixed = rest + p.tok * x_row;
     if (fixed + 2 * kWarps * C::kStage > kMaxSmem) return MOE_ERR_CAPACITY;
