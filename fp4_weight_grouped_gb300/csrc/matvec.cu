@@ -225,6 +225,8 @@ __device__ __forceinline__ void build_chunks(const Params &p, const Chunks &c) {
     __syncthreads();
 }
 
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
 // Power of two that a row of x is scaled by, from the exponent field of its largest magnitude.
 __device__ __forceinline__ int row_exponent(int top) { return max(top - 127 - 14, -126); }
 
@@ -357,14 +359,14 @@ __device__ __forceinline__ void load_scales(const uint8_t *const (&rows)[2][2], 
 // piece t4 of its first row, or for MXFP4 (read by words of eight rows) word t4 of piece 0.
 // step: bytes from row g of an MMA to row g + 8, next: to the second MMA's.  x: this lane's
 // share of the chunk's rows, zeros in lanes without one.
-template <int F, int kHalf>
+template <int F>
 __device__ __forceinline__ void multiply(uint32_t at, int step, int next, uint32_t xa, bool has_x, const Scales &sw,
                                          uint4 (&x)[4], float (&acc)[2][4], Scales &bad) {
     if constexpr (F == kBf16) {
         lds128_if(x[0], xa, has_x);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            const uint32_t row = (at ^ (64 * kHalf)) + s * next;
+            const uint32_t row = at + s * next;
             const uint4 a = lds128(row), c = lds128(row + step);
             mma16816<false>(acc[s], a.x, c.x, a.y, c.y, x[0].x, x[0].y);
             mma16816<false>(acc[s], a.z, c.z, a.w, c.w, x[0].z, x[0].w);
@@ -374,7 +376,7 @@ __device__ __forceinline__ void multiply(uint32_t at, int step, int next, uint32
         uint4 ra[2], rc[2];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            const uint32_t row = (at ^ (64 * kHalf)) + s * next;
+            const uint32_t row = at + s * next;
             ra[s] = lds128(row);
             rc[s] = lds128(row + step);
         }
@@ -413,7 +415,7 @@ __device__ __forceinline__ void multiply(uint32_t at, int step, int next, uint32
         for (int b = 0; b < 4; ++b)
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                const uint32_t row = (at ^ (64 * kHalf + 16 * b)) + s * next;
+                const uint32_t row = (at ^ (16 * b)) + s * next;
                 uint32_t a[4], c[4];
                 decode8(lds32(row), a);
                 decode8(lds32(row + step), c);
@@ -437,7 +439,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(1024) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t4 = lane & 3;
-    const int kw = p.kw, group = kWarps / kw, depth = p.depth;          // group: tiles an item
+    const int kw = p.kw, depth = p.depth;
+    const int group = kWarps / kw, group_log2 = 31 - __clz(group);      // tiles an item, a power of two
     const int pitch = p.k_pad * 2 + 64, sum_floats = p.tok * kSumPitch;
     // ring: stages, all warps' scales behind them | x | sums | barriers | chunk tables
     uint8_t *xs = smem + kWarps * depth * C::kStage;
@@ -556,28 +559,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t xa = smem_u32(xs) + min(g, n_tok - 1) * pitch + t4 * 16 + u0 * kUnitX;
 #pragma unroll 1
         for (int unit = u0; ok && unit < u1; ++unit) {
-            Scales sw[2] = {};
-            if constexpr (F != kBf16 && !kTmaScales) {
-                load_scales<F>(srow, 2 * unit, t4, p.K / (F == kMx ? 32 : 16), sw[0]);
-                load_scales<F>(srow, 2 * unit + 1, t4, p.K / (F == kMx ? 32 : 16), sw[1]);
-            }
             ok = warp_wait_bounded(&bars[slot], phase, nullptr, p.status, p.wait_limit_ns);
             if (!ok) break;
-            if constexpr (F != kBf16 && kTmaScales) {
-                const uint32_t sa = scale0 + slot * (16 * kTileRows) + (unit * C::kScaleBytes & 15);
+            // One half after the other, not unrolled: in a short launch (one token's w2) waiting
+            // for instructions is the first of all stalls.
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+                Scales sw = {};
+                if constexpr (F != kBf16 && !kTmaScales) {
+                    load_scales<F>(srow, 2 * unit + h, t4, p.K / (F == kMx ? 32 : 16), sw);
+                } else if constexpr (F != kBf16) {
+                    const uint32_t sa = scale0 + slot * (16 * kTileRows) + (unit * C::kScaleBytes & 15) + h * (C::kScaleBytes / 2);
 #pragma unroll
-                for (int s = 0; s < 2; ++s)
+                    for (int s = 0; s < 2; ++s)
 #pragma unroll
-                    for (int r = 0; r < 2; ++r)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const uint32_t a = sa + (s * kNext + r * kStep) * 16 + h * C::kScaleBytes / 2;
-                            sw[h][s][r] = F == kMx ? lds32(a) : lds16(a);
+                        for (int r = 0; r < 2; ++r) {
+                            const uint32_t a = sa + (s * kNext + r * kStep) * 16;
+                            sw[s][r] = F == kMx ? lds32(a) : lds16(a);
                         }
+                }
+                multiply<F>((row0 + slot * (kTileRows * 128)) ^ (64 * h), kStep * 128, kNext * 128, xa + h * (kUnitX / 2),
+                            g < n_tok, sw, x, acc, bad);
             }
-            const uint32_t at = row0 + slot * (kTileRows * 128);
-            multiply<F, 0>(at, kStep * 128, kNext * 128, xa, g < n_tok, sw[0], x, acc, bad);
-            multiply<F, 1>(at, kStep * 128, kNext * 128, xa + kUnitX / 2, g < n_tok, sw[1], x, acc, bad);
             xa += kUnitX;
             __syncwarp();                         // the slot is read by all
             fetch_next();
@@ -605,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncthreads();
         // Everyone adds up its outputs over the warps that shared the tile, in order.
         for (int i = tid; i < group * kTileCols * n_tok; i += kThreads) {
-            const int c = i % kTileCols, tile = i / kTileCols % group, t = i / kTileCols / group;
+            const int c = i % kTileCols, tile = i / kTileCols & (group - 1), t = i / kTileCols >> group_log2;
             const int n = (grp * group + tile) * kTileCols + c;
             if (n >= p.N) continue;
             const float *from = sums + tile * kw * sum_floats + t * kSumPitch + c;
@@ -617,9 +620,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if constexpr (F != kBf16) {
                 const int e = row_exponent(tops[turn + t]) + (F == kMx ? 31 : 0);
                 const float s2 = F == kNv ? __ldg(p.ws2 + ch.expert[chunk]) : 1.0f;
-                const auto whole = [&](float a) {
-                    return e > 0 ? ldexpf(a * s2, e) : ldexpf(a, e) * s2;
-                };
+                // 2^e by two factors, each of them a normal number.
+                const float f = power_of_two(e / 2), f2 = power_of_two(e - e / 2);
+                const auto whole = [&](float a) { return e > 0 ? a * s2 * f * f2 : a * f * f2 * s2; };
                 v = whole(v);
                 if (kSwiglu) u = whole(u);
             }
