@@ -45,7 +45,9 @@ def gate(g, u):
 # T, hidden, inter: one token to many, sizes off every tile and stage, one column group.
 SHAPES = [(1, 8, 8), (2, 64, 24), (7, 712, 1056), (8, 4096, 128), (9, 264, 136), (33, 72, 520), (64, 4096, 2048),
           (128, 128, 128), (129, 136, 8), (250, 1032, 520), (256, 256, 256), (301, 712, 1056), (513, 520, 264),
-          (1024, 64, 1024), (2500, 512, 96)]
+          (1024, 64, 1024), (2500, 512, 96),
+          # a last round of few items, which are cut in two: outputs, gate, gradients
+          (2048, 2560, 64), (2048, 64, 1280), (64, 2560, 1024)]
 
 
 @pytest.mark.parametrize("T,H,I", SHAPES)
@@ -227,3 +229,52 @@ def test_graphs_and_streams(B):
     step(stream=side)
     side.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(first, (out, *grads)))
+
+
+def test_two_streams_at_once(B):
+    args = [inputs(n, 256, 192, seed=n) for n in (130, 260)]
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+
+    def step(i, s, b):
+        x, w13, w2, dout = args[i]
+        B.ffn_forward(x, w13, w2, h=b["h"], gu=b["gu"], out=b["out"], workspace=b["ws"], stream=s)
+        B.ffn_backward(dout, x, w13, w2, b["h"], b["gu"], dgu=b["dgu"], out=b["grads"], workspace=b["ws"], stream=s)
+
+    def buffers(i):
+        x, w13, w2, _ = args[i]
+        T = x.shape[0]
+        return dict(h=torch.empty((T, 192), **bf), gu=torch.empty((T, 384), **bf), dgu=torch.empty((T, 384), **bf),
+                    out=torch.empty_like(x), grads=tuple(torch.empty_like(t) for t in (x, w13, w2)), ws=B.make_workspace(0, 1, 1))
+
+    want = [buffers(i) for i in range(2)]
+    for i in range(2):
+        step(i, None, want[i])
+    torch.cuda.synchronize()
+    many = [[buffers(i) for _ in range(6)] for i in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for j in range(6):
+        for i in range(2):
+            step(i, streams[i], many[i][j])
+    torch.cuda.synchronize()
+    for i in range(2):
+        for b in many[i]:
+            assert all(torch.equal(p, q) for p, q in zip((b["out"], *b["grads"]), (want[i]["out"], *want[i]["grads"])))
+
+
+@pytest.mark.parametrize("T", [4, 200])
+def test_inputs_that_a_kernel_ahead_still_writes(B, T):
+    """Both products in a chain: the second starts under the first's end, the first waits for
+    what is ahead of it."""
+    x, w13, w2, _ = inputs(T, 512, 384)
+    xs = [x * (0.5 + 0.1 * i) for i in range(12)]
+    want = []
+    for a in xs:
+        want.append(B.ffn_forward(a, w13, w2))
+        torch.cuda.synchronize()
+    now, h, got = torch.empty_like(x), torch.empty((T, 384), device="cuda").bfloat16(), []
+    for a in xs:
+        now.copy_(a)
+        got.append(B.ffn_forward(now, w13, w2, h=h))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))

@@ -174,3 +174,34 @@ def test_graphs_and_streams(B):
         n = norm64(grads)
         assert abs(float(norm) - n) <= NORM * n
         check(out, grads, 3.0 / (n + 1e-6))
+
+
+def test_two_streams_at_once(B):
+    """A workspace each."""
+    g = torch.Generator(device="cuda").manual_seed(8)
+    grads = [make(g, [50000, 333, 7], "mixed", std) for std in (1.0, 30.0)]
+    outs = [[[torch.empty_like(t) for t in grads[i]] for _ in range(8)] for i in range(2)]
+    ws = [torch.zeros(B.MOE_GRAD_WORKSPACE_BYTES, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    norms = [torch.empty(8, device="cuda") for _ in range(2)]
+    want = [[torch.empty_like(t) for t in grads[i]] for i in range(2)]
+    for i in range(2):
+        B.clip_grads(grads[i], 2.0, out=want[i])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for j in range(8):
+        for i in range(2):
+            B.clip_grads(grads[i], 2.0, out=outs[i][j], norm=norms[i][j:j + 1], workspace=ws[i], stream=streams[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert bool((norms[i] == norms[i][0]).all())
+        assert all(torch.equal(a, b) for o in outs[i] for a, b in zip(o, want[i]))
+
+
+def test_gradients_that_a_kernel_ahead_still_writes(B):
+    """Norm and scale in place, over and over: each call sees what the one ahead of it left."""
+    x = torch.full((300001,), 8.0, device="cuda")
+    for i in range(6):
+        n = 8.0 * math.sqrt(300001) * 0.5 ** i
+        norm = B.clip_grads([x], 0.5 * n, eps=0.0)
+        assert abs(float(norm) - n) <= (i + 1) * NORM * n
+    assert bool(((x - 8.0 * 0.5 ** 6).abs() <= 6 * (NORM + 2.0 ** -23) * 8.0 * 0.5 ** 6).all())

@@ -303,3 +303,57 @@ def test_graphs_and_streams(B):
     got = B.fp4_matvec(x, w[0], w[1], 0, row_expert=ids, stream=side)
     side.synchronize()
     assert torch.equal(got, out)
+
+
+@pytest.mark.parametrize("fmt", [0, 1], ids=["mx", "nv"])
+@pytest.mark.parametrize("rows", [9, 20, 33, 100])
+def test_many_rows_of_one_expert(B, rows, fmt):
+    """More rows of an expert than are taken together, the others' in between."""
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    w = weights(g, 40, 36, 288, fmt)
+    x = torch.randn((rows, 288), generator=g, device="cuda").bfloat16()
+    ids = torch.full((rows,), 7, dtype=torch.int32, device="cuda")
+    ids[3], ids[rows - 2] = 39, 0
+    got = B.fp4_matvec(x, w[0], w[1], fmt, row_expert=ids, weight_scale_2=w[2])
+    check(got, x, w, ids.tolist(), 1, fmt)
+    same = B.fp4_matvec(x[:1].expand(rows, -1), w[0], w[1], fmt, row_expert=torch.full_like(ids, 7), weight_scale_2=w[2])
+    assert torch.equal(same, got[:1].expand(rows, -1))
+
+
+def test_two_streams_at_once(B):
+    g = torch.Generator(device="cuda").manual_seed(13)
+    w = weights(g, 16, 512, 1024, 0)
+    x = torch.randn((2, 8, 1024), generator=g, device="cuda").bfloat16()
+    ids = torch.randint(0, 16, (2, 8), generator=g, device="cuda", dtype=torch.int32)
+    want = [B.fp4_matvec(x[i], w[0], w[1], 0, row_expert=ids[i]) for i in range(2)]
+    out = [[torch.empty_like(want[0]) for _ in range(10)] for _ in range(2)]
+    ws = [B.make_workspace(0, 1, 1) for _ in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for j in range(10):
+        for i in range(2):
+            B.fp4_matvec(x[i], w[0], w[1], 0, row_expert=ids[i], out=out[i][j], workspace=ws[i], stream=streams[i])
+    torch.cuda.synchronize()
+    assert all(torch.equal(t, want[i]) for i in range(2) for t in out[i])
+
+
+def test_inputs_that_a_kernel_ahead_still_writes(B):
+    """x and the ids of a call are whatever the stream's work ahead of it leaves."""
+    g = torch.Generator(device="cuda").manual_seed(14)
+    E, H, I, k = 8, 512, 256, 2
+    w13, w2 = weights(g, E, 2 * I, H, 0, 116, 122), weights(g, E, H, I, 0, 116, 122)
+    xs = torch.randn((20, 3, H), generator=g, device="cuda").bfloat16()
+    idss = torch.rand((20, 3, E), generator=g, device="cuda").topk(k, dim=2).indices.to(torch.int32)
+    tw = torch.rand((3, k), generator=g, device="cuda")
+    want = []
+    for x, ids in zip(xs, idss):
+        want.append(B.layer_decode(x.contiguous(), ids.contiguous(), tw, w13, w2, 0))
+        torch.cuda.synchronize()
+    x, ids = torch.empty_like(xs[0]), torch.empty_like(idss[0])
+    h, y2, got = torch.empty((6, I), device="cuda").bfloat16(), torch.empty((6, H), device="cuda"), []
+    for a, b in zip(xs, idss):
+        x.copy_(a)
+        ids.copy_(b)
+        got.append(B.layer_decode(x, ids, tw, w13, w2, 0, h=h, y2=y2))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
