@@ -49,6 +49,11 @@ constexpr int kTileRows = 32;                 // weight rows a tile: two MMAs' s
 constexpr int kMaxDepth = 4;
 constexpr int kSumPitch = 36;                 // floats of a token's 32 sums, free of bank conflicts
 
+template <int v>
+struct Int {
+    static constexpr int value = v;
+};
+
 template <int F>
 struct Fmt {
     static constexpr int kUnit = F == kBf16 ? 64 : 256;             // k of a stage: 128 bytes a row
@@ -85,6 +90,11 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
 __device__ __forceinline__ uint32_t lds16(uint32_t a) {
     uint16_t v;
     asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
     return v;
 }
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
@@ -124,6 +134,12 @@ __device__ __forceinline__ void e4m3_pairs(uint32_t b, uint32_t &first, uint32_t
     asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(h) : "r"(b));
     first = prmt(h, h, 0x1010u);
     second = prmt(h, h, 0x3232u);
+}
+__device__ __forceinline__ void e4m3_floats(uint32_t b, float &first, float &second) {
+    asm("{\n\t.reg .b16 t, lo, hi;\n\t.reg .b32 h;\n\tcvt.u16.u32 t, %2;\n\tcvt.rn.f16x2.e4m3x2 h, t;\n\t"
+        "mov.b32 {lo, hi}, h;\n\tcvt.f32.f16 %0, lo;\n\tcvt.f32.f16 %1, hi;\n\t}"
+        : "=f"(first), "=f"(second)
+        : "r"(b));
 }
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
     uint32_t d;
@@ -262,7 +278,7 @@ __device__ __forceinline__ uint32_t top_of(const uint4 &a) {
 }
 
 template <int F>
-__device__ __forceinline__ void store_x(uint8_t *row, int v, const uint4 &a, int top) {
+__device__ __forceinline__ void store_x(uint8_t *row, int v, const uint4 &a, int top, bool by_blocks) {
     if constexpr (F == kBf16) {
         *reinterpret_cast<uint4 *>(row + 16 * v) = a;
     } else {
@@ -274,15 +290,11 @@ __device__ __forceinline__ void store_x(uint8_t *row, int v, const uint4 &a, int
             asm("cvt.rn.f16x2.f32 %0, %1, %2;"
                 : "=r"(o[i])
                 : "f"(__uint_as_float(w[i] & 0xFFFF0000u) * f), "f"(__uint_as_float(w[i] << 16) * f));
-        const int at = F == kNv ? (v & ~15) | (v & 3) << 2 | (v >> 2 & 3) : v;
+        const int at = F == kNv || by_blocks ? (v & ~15) | (v & 3) << 2 | (v >> 2 & 3) : v;
         *reinterpret_cast<uint4 *>(row + 16 * at) = make_uint4(o[0], o[1], o[2], o[3]);
     }
 }
 
-// The chunk's rows of x into shared memory (4-bit weights: f16, scaled by 2^-row_exponent;
-// bf16 as they are), zeros up to k_pad.  tops[t] (zero before) receives row t's largest
-// exponent field.  NVFP4: within 128 k, 16 bytes q go to place 4 (q % 4) + q / 4, where the
-// lanes that hold 32 k each find theirs side by side.
 // Rows of x in registers, where a thread has one load of each (vecs <= kThreads).
 __device__ __forceinline__ void fetch_x(const Params &p, const int *slots, int n, uint4 (&a)[kTok]) {
 #pragma unroll
@@ -290,9 +302,13 @@ __device__ __forceinline__ void fetch_x(const Params &p, const int *slots, int n
         if (t < n && static_cast<int>(threadIdx.x) < p.k_pad / 8) a[t] = load_x(p, slots[t], threadIdx.x);
 }
 
+// The chunk's rows of x into shared memory (4-bit weights: f16, scaled by 2^-row_exponent;
+// bf16 as they are), zeros up to k_pad.  tops[t] (zero before) receives row t's largest
+// exponent field.  Where a lane holds 32 k of its own (NVFP4, and MXFP4 for few rows), 16 bytes
+// q of 128 k go to place 4 (q % 4) + q / 4: the lanes find theirs side by side.
 template <int F>
 __device__ __forceinline__ void stage_x(const Params &p, const int *slots, int n, uint8_t *xs, int pitch, int *tops,
-                                        bool fetched, uint4 (&a)[kTok]) {
+                                        bool fetched, bool by_blocks, uint4 (&a)[kTok]) {
     const int tid = threadIdx.x, vecs = p.k_pad / 8;
     if (vecs <= kThreads) {
         if (!fetched) fetch_x(p, slots, n, a);
@@ -307,7 +323,7 @@ __device__ __forceinline__ void stage_x(const Params &p, const int *slots, int n
         }
 #pragma unroll
         for (int t = 0; t < kTok; ++t)
-            if (t < n && tid < vecs) store_x<F>(xs + t * pitch, tid, a[t], F == kBf16 ? 0 : tops[t]);
+            if (t < n && tid < vecs) store_x<F>(xs + t * pitch, tid, a[t], F == kBf16 ? 0 : tops[t], by_blocks);
     } else {
         if constexpr (F != kBf16) {
             for (int t = 0; t < n; ++t) {
@@ -320,7 +336,7 @@ __device__ __forceinline__ void stage_x(const Params &p, const int *slots, int n
         }
         for (int t = 0; t < n; ++t)
             for (int v = tid; v < vecs; v += kThreads)
-                store_x<F>(xs + t * pitch, v, load_x(p, slots[t], v), F == kBf16 ? 0 : tops[t]);
+                store_x<F>(xs + t * pitch, v, load_x(p, slots[t], v), F == kBf16 ? 0 : tops[t], by_blocks);
     }
     __syncthreads();
 }
@@ -333,16 +349,14 @@ __device__ __forceinline__ void lds128_if(uint4 &v, uint32_t a, bool real) {
                  : "r"(a), "r"(static_cast<int>(real)));
 }
 
-// Scale bytes of half a stage, of the four rows that a lane multiplies: MXFP4 one word a
-// row, NVFP4 the two bytes of the lane's 32 k.
+// Scale bytes, half a stage's, of the four rows that a lane multiplies: MXFP4 a word a row, NVFP4
+// the two bytes of the lane's 32 k, MXFP4 for few rows of x the one byte of its 32 k.
 using Scales = uint32_t[2][2];
 
 // Rows of scales that TMA does not take (not a multiple of 16 bytes, or elsewhere aligned):
 // byte by byte from global memory, zeros past the row's end.
-template <int F>
-__device__ __forceinline__ void load_scales(const uint8_t *const (&rows)[2][2], int half, int t4, int row_bytes, Scales &v) {
-    constexpr int n = F == kMx ? 4 : 2;
-    const int at = F == kMx ? 4 * half : 8 * half + 2 * t4;
+template <int n>
+__device__ __forceinline__ void load_scales(const uint8_t *const (&rows)[2][2], int at, int row_bytes, Scales &v) {
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
@@ -432,7 +446,64 @@ __device__ __forceinline__ void multiply(uint32_t at, int step, int next, uint32
     }
 }
 
-template <int F, bool kSwiglu, bool kTmaScales>
+// The same for one or two rows of x.  A lane's 16 bytes are 32 k of their own, and a column of the
+// MMAs holds a row of x where k is in one scale block and zeros elsewhere: the sums keep the
+// blocks apart, and a block's scale multiplies once behind them (half of the instructions of the
+// form above: one token's w13 20.0 -> 18.1 us, w2 13.5 -> 11.6).  Column j: row j % 2, block j / 2
+// of four (MXFP4: a half's; NVFP4: those of two words after those of the other two), or for one
+// row of NVFP4 (kRows 1) block j of eight.  has: whether this lane's words 0 and 1, and 2 and 3,
+// belong to its column; x stays zero where they do not.  What acc holds is a quarter of a sum.
+template <int F, int kRows>
+__device__ __forceinline__ void multiply_few(uint32_t at, int step, int next, uint32_t xa, const bool (&has)[2],
+                                             const Scales &sw, uint4 (&x)[4], float (&acc)[2][4], Scales &bad) {
+    uint4 ra[2], rc[2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        const uint32_t row = at + s * next;
+        ra[s] = lds128(row);
+        rc[s] = lds128(row + step);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) lds128_if(x[j], xa + 64 * j, has[j >> 1]);
+    float scale[2][2][2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        if constexpr (F == kNv)
+            bad[0][0] |= (((sw[s][0] | sw[s][1] << 16) & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;         // NaN
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            if constexpr (F == kMx) {
+                bad[s][r] |= (sw[s][r] + 3u) & 0x100u;                                                   // 253 and more
+                scale[s][r][0] = __uint_as_float(sw[s][r] << 23) * 0x1p-31f;
+            } else {
+                e4m3_floats(sw[s][r], scale[s][r][0], scale[s][r][1]);
+            }
+        }
+    }
+    constexpr int kWords = F == kNv && kRows == 2 ? 2 : 4;      // that one set of sums takes
+#pragma unroll
+    for (int b = 0; b < 4; b += kWords) {
+        float d[2][4] = {};
+#pragma unroll
+        for (int j = b; j < b + kWords; ++j)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const uint32_t wa[4] = {ra[s].x, ra[s].y, ra[s].z, ra[s].w}, wc[4] = {rc[s].x, rc[s].y, rc[s].z, rc[s].w};
+                uint32_t a[4], c[4];
+                decode8(wa[j], a);
+                decode8(wc[j], c);
+                mma16816<true>(d[s], a[0], c[0], a[1], c[1], x[j].x, x[j].y);
+                mma16816<true>(d[s], a[2], c[2], a[3], c[3], x[j].z, x[j].w);
+            }
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)       // either column the same block and its own row, or the same row
+                acc[s][kRows == 2 ? i : i & 2] = fmaf(scale[s][i >> 1][kRows == 2 ? b >> 1 : i & 1], d[s][i], acc[s][kRows == 2 ? i : i & 2]);
+    }
+}
+
+template <int F, bool kSwiglu, bool kTmaScales, bool kFew>
 __global__ void __launch_bounds__(kThreads, 1)
     matvec_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_s, const Params p) {
     using C = Fmt<F>;
@@ -523,12 +594,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     // together then meet eight different pieces of the swizzle.
     const int q = g >> 1 | (g & 1) << 2;
     constexpr int kStep = (kSwiglu ? 16 : 8), kNext = (kSwiglu ? 8 : 16);
-    const uint32_t row0 = ring + q * 128 + (F == kMx ? q * 16 + 4 * t4 : (t4 ^ q) * 16);
-    const uint32_t scale0 = scale_ring + q * 16 + (F == kNv ? 2 * t4 : 0);
+    const uint32_t piece0 = ring + q * 128 + (t4 ^ q) * 16, row0 = F == kMx ? ring + q * 128 + q * 16 + 4 * t4 : piece0;
+    const uint32_t scale0 = scale_ring + q * 16;
     constexpr int kUnitX = 2 * C::kUnit;
     uint32_t slot = 0, phase = 0, any_bad = 0;
     int n_tok = 0, start = 0, turn = 0, chunk = chunk0, grp = grp0;
-    bool fresh = true, ok = true;
+    bool fresh = true, ok = true, few = false;
     uint4 x[4];
     for (int left = count; left > 0; --left) {
         if (fresh) {                              // everyone is past the last x
@@ -537,7 +608,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             n_tok = ch.first[chunk + 1] - start;
             if (left != count) __syncthreads();   // and past its exponents
             turn ^= kTok;
-            stage_x<F>(p, ch.order + start, n_tok, xs, pitch, tops + turn, ahead && left == count, xr);
+            // Only where it is the expert's only chunk: rows that share an expert take one way, so that
+            // equal ones have equal results.
+            few = kFew && n_tok <= 2 && (chunk == 0 || ch.expert[chunk - 1] != ch.expert[chunk]) &&
+                  (chunk + 1 == *ch.count || ch.expert[chunk + 1] != ch.expert[chunk]);
+            stage_x<F>(p, ch.order + start, n_tok, xs, pitch, tops + turn, ahead && left == count, few, xr);
             if (tid < kTok) tops[(turn ^ kTok) + tid] = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[i] = make_uint4(0, 0, 0, 0);
@@ -556,36 +631,60 @@ __global__ void __launch_bounds__(kThreads, 1)
                     srow[s][r] = p.scales + (at + c) * (p.K / (F == kMx ? 32 : 16));
                 }
         }
-        uint32_t xa = smem_u32(xs) + min(g, n_tok - 1) * pitch + t4 * 16 + u0 * kUnitX;
-#pragma unroll 1
-        for (int unit = u0; ok && unit < u1; ++unit) {
-            ok = warp_wait_bounded(&bars[slot], phase, nullptr, p.status, p.wait_limit_ns);
-            if (!ok) break;
-            // One half after the other, not unrolled: in a short launch (one token's w2) waiting
-            // for instructions is the first of all stalls.
-#pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
-                Scales sw = {};
-                if constexpr (F != kBf16 && !kTmaScales) {
-                    load_scales<F>(srow, 2 * unit + h, t4, p.K / (F == kMx ? 32 : 16), sw);
-                } else if constexpr (F != kBf16) {
-                    const uint32_t sa = scale0 + slot * (16 * kTileRows) + (unit * C::kScaleBytes & 15) + h * (C::kScaleBytes / 2);
+        uint32_t xa = smem_u32(xs) + min(few ? g & 1 : g, n_tok - 1) * pitch + t4 * 16 + u0 * kUnitX;
+        // The scale bytes that a lane wants: n of a row, from byte `at` of a row's stage on.
+        const auto scales_of = [&](auto n, int unit, int at, Scales &sw) {
+            if constexpr (!kTmaScales) {
+                load_scales<n.value>(srow, unit * C::kScaleBytes + at, p.K / (F == kMx ? 32 : 16), sw);
+            } else {
+                const uint32_t sa = scale0 + slot * (16 * kTileRows) + (unit * C::kScaleBytes & 15) + at;
 #pragma unroll
-                    for (int s = 0; s < 2; ++s)
+                for (int s = 0; s < 2; ++s)
 #pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            const uint32_t a = sa + (s * kNext + r * kStep) * 16;
-                            sw[s][r] = F == kMx ? lds32(a) : lds16(a);
-                        }
-                }
-                multiply<F>((row0 + slot * (kTileRows * 128)) ^ (64 * h), kStep * 128, kNext * 128, xa + h * (kUnitX / 2),
-                            g < n_tok, sw, x, acc, bad);
+                    for (int r = 0; r < 2; ++r) {
+                        const uint32_t a = sa + (s * kNext + r * kStep) * 16;
+                        sw[s][r] = n.value == 4 ? lds32(a) : n.value == 2 ? lds16(a) : lds8(a);
+                    }
             }
-            xa += kUnitX;
-            __syncwarp();                         // the slot is read by all
-            fetch_next();
-            slot = slot + 1 == static_cast<uint32_t>(depth) ? 0 : slot + 1;
-            phase ^= slot == 0;
+        };
+        const auto stages = [&](auto few_rows) {
+            constexpr int kScales = F == kNv ? 2 : few_rows.value ? 1 : 4;
+            const uint32_t rows = (F == kMx && !few_rows.value ? row0 : piece0);
+            bool has[2] = {g < n_tok};
+            if (few_rows.value > 0) has[0] = has[1] = t4 == g >> 1 && (g & 1) < n_tok;
+            if (F == kNv && few_rows.value == 1) {
+                has[0] = t4 == g >> 1 && (g & 1) == 0;
+                has[1] = t4 == g >> 1 && (g & 1) == 1;
+            }
+#pragma unroll 1
+            for (int unit = u0; ok && unit < u1; ++unit) {
+                ok = warp_wait_bounded(&bars[slot], phase, nullptr, p.status, p.wait_limit_ns);
+                if (!ok) break;
+                // One half after the other, not unrolled: in a short launch (one token's w2) waiting
+                // for instructions is the first of all stalls.
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    Scales sw = {};
+                    if constexpr (F != kBf16) scales_of(Int<kScales>{}, unit, h * (C::kScaleBytes / 2) + (kScales < 4 ? kScales * t4 : 0), sw);
+                    const uint32_t at = (rows + slot * (kTileRows * 128)) ^ (64 * h), x_at = xa + h * (kUnitX / 2);
+                    if constexpr (few_rows.value > 0)
+                        multiply_few<F, few_rows.value>(at, kStep * 128, kNext * 128, x_at, has, sw, x, acc, bad);
+                    else
+                        multiply<F>(at, kStep * 128, kNext * 128, x_at, has[0], sw, x, acc, bad);
+                }
+                xa += kUnitX;
+                __syncwarp();                     // the slot is read by all
+                fetch_next();
+                slot = slot + 1 == static_cast<uint32_t>(depth) ? 0 : slot + 1;
+                phase ^= slot == 0;
+            }
+        };
+        if constexpr (kFew) {
+            if (F == kNv && few && n_tok == 1) stages(Int<1>{});
+            else if (few) stages(Int<2>{});
+            else stages(Int<0>{});
+        } else {
+            stages(Int<0>{});
         }
         if constexpr (F == kMx) {
             const float nan = __uint_as_float(0x7FC00000u);
@@ -596,6 +695,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         any_bad |= bad[0][0] | bad[0][1] | bad[1][0] | bad[1][1];
+        if (kFew && few) {                        // the quarters of a sum lie in four lanes
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    acc[s][i] += __shfl_xor_sync(0xffffffffu, acc[s][i], 1);
+                    acc[s][i] += __shfl_xor_sync(0xffffffffu, acc[s][i], 2);
+                }
+        }
         __syncthreads();                          // the last item's sums are read
         float *mine = sums + warp * sum_floats;   // [token][stage row]
 #pragma unroll
@@ -681,7 +789,7 @@ bool encode(CUtensorMap *map, const void *base, int64_t bytes, int64_t rows, int
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int F, bool kSwiglu, bool kTmaScales>
+template <int F, bool kSwiglu, bool kTmaScales, bool kFew>
 moe_status launch(Params p, cudaStream_t stream, int num_sms) {
     using C = Fmt<F>;
     p.k_pad = (p.K + C::kUnit - 1) / C::kUnit * C::kUnit;
@@ -718,7 +826,7 @@ moe_status launch(Params p, cudaStream_t stream, int num_sms) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
     const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
-    const auto kernel = matvec_kernel<F, kSwiglu, kTmaScales>;
+    const auto kernel = matvec_kernel<F, kSwiglu, kTmaScales, kFew>;
     if (!bit || !(mask.load(std::memory_order_acquire) & bit)) {
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) != cudaSuccess)
             return MOE_ERR_CUDA;
@@ -735,6 +843,15 @@ moe_status launch(Params p, cudaStream_t stream, int num_sms) {
     cfg.attrs = &attr;
     cfg.numAttrs = p.chained ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kernel, tm_w, tm_s, p) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+template <int F>
+moe_status launch_format(const Params &p, bool swiglu, bool tma, bool few, cudaStream_t stream, int num_sms) {
+    if (few)
+        return swiglu ? tma ? launch<F, true, true, true>(p, stream, num_sms) : launch<F, true, false, true>(p, stream, num_sms)
+                      : tma ? launch<F, false, true, true>(p, stream, num_sms) : launch<F, false, false, true>(p, stream, num_sms);
+    return swiglu ? tma ? launch<F, true, true, false>(p, stream, num_sms) : launch<F, true, false, false>(p, stream, num_sms)
+                  : tma ? launch<F, false, true, false>(p, stream, num_sms) : launch<F, false, false, false>(p, stream, num_sms);
 }
 
 }  // namespace mv
@@ -760,19 +877,19 @@ moe_status launch_matvec(const Matvec &m, cudaStream_t stream, int num_sms) {
     p.chained = m.chained;
     p.x_vec = reinterpret_cast<uintptr_t>(m.x) % 16 == 0 && (m.x_stride % 8 == 0 || m.rows <= m.index_div);
     if (m.format == Matvec::kBf16)
-        return m.swiglu ? mv::launch<mv::kBf16, true, false>(p, stream, num_sms)
-                        : mv::launch<mv::kBf16, false, false>(p, stream, num_sms);
+        return m.swiglu ? mv::launch<mv::kBf16, true, false, false>(p, stream, num_sms)
+                        : mv::launch<mv::kBf16, false, false, false>(p, stream, num_sms);
     const bool nv = m.format == Matvec::kNv;
+    // Whether experts with one or two rows have their own form in the kernel: not where they are
+    // the exception, which would then only wait for the others (256 experts, six a token,
+    // layer_decode with and without it, MXFP4 / NVFP4: 6 rows 29.4, 31.3 / 30.7, 31.3 us; 48 rows
+    // 124, 136 / 129.5, 136; 96 rows 200, 205 / 209.6, 206; 384 rows 484, 484 / 510, 490), nor
+    // where a call surely has more (4 rows of one matrix: 8.7, 8.4).
+    const bool few = m.row_expert && m.E > 1 ? m.rows <= 2 * m.E && m.rows <= (nv ? 64 : 128) : m.rows <= 2;
     // Rows of scales that TMA takes: a multiple of 16 bytes, at 16-byte addresses.
-    if (m.K / (nv ? 16 : 32) % 16 == 0 && reinterpret_cast<uintptr_t>(m.scales) % 16 == 0)
-        return nv ? m.swiglu ? mv::launch<mv::kNv, true, true>(p, stream, num_sms)
-                             : mv::launch<mv::kNv, false, true>(p, stream, num_sms)
-                  : m.swiglu ? mv::launch<mv::kMx, true, true>(p, stream, num_sms)
-                             : mv::launch<mv::kMx, false, true>(p, stream, num_sms);
-    return nv ? m.swiglu ? mv::launch<mv::kNv, true, false>(p, stream, num_sms)
-                         : mv::launch<mv::kNv, false, false>(p, stream, num_sms)
-              : m.swiglu ? mv::launch<mv::kMx, true, false>(p, stream, num_sms)
-                         : mv::launch<mv::kMx, false, false>(p, stream, num_sms);
+    const bool tma = m.K / (nv ? 16 : 32) % 16 == 0 && reinterpret_cast<uintptr_t>(m.scales) % 16 == 0;
+    return nv ? mv::launch_format<mv::kNv>(p, m.swiglu, tma, few, stream, num_sms)
+              : mv::launch_format<mv::kMx>(p, m.swiglu, tma, few, stream, num_sms);
 }
 
 moe_status launch_weigh(const float *y, const int32_t *ids, const float *w, int T, int k, int N, int E, void *out,
