@@ -8,8 +8,9 @@
 //  * Rows of the same expert are taken together, up to 8 at a time (a chunk), so a
 //    weight is read once for them.  Every CTA works the chunks out from the ids itself.
 //  * A tile is 32 weight rows (SwiGLU: 16 gate rows and the 16 matching up rows, so that one
-//    thread finds both).  kw warps of a CTA share a tile's K, 256 k (bf16: 64) a stage, and
-//    add up their sums in shared memory in a fixed order.
+//    thread finds both).  kw warps of a CTA share a tile's K, 256 k (bf16: 64) a stage, every
+//    kw-th stage each (that neighbours along a row are read together: one token through six
+//    experts 29.4 -> 27.3 us), and add up their sums in shared memory in a fixed order.
 //  * mma.sync m16n8k16 with the weights as A and the chunk's rows as B columns: eight
 //    rows cost what one costs, and a thread's four sums are f32.  Tensor memory has
 //    nothing to offer here: no operand is used twice.
@@ -541,13 +542,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int count = total / grid + (blk < total % grid);
     const int chunk0 = count > 0 ? first / groups : 0, grp0 = count > 0 ? first % groups : 0;
     const int wk = warp & (kw - 1), wt = warp / kw;
-    const int units = (p.K + C::kUnit - 1) / C::kUnit, u0 = units * wk / kw, u1 = units * (wk + 1) / kw;
+    const int units = (p.K + C::kUnit - 1) / C::kUnit;
 
     // A stage: 32 rows (SwiGLU: 16 gate rows, the 16 up rows of the same columns) and their
     // scales.  What lies past an expert's rows or a row's end reads as zeros.
     const uint32_t ring = smem_u32(smem) + warp * depth * (kTileRows * 128);
     const uint32_t scale_ring = smem_u32(smem) + kWarps * depth * (kTileRows * 128) + warp * depth * (16 * kTileRows);
-    int f_left = u0 < u1 ? count : 0, f_unit = u0, f_slot = 0, f_chunk = chunk0, f_grp = grp0;
+    int f_left = wk < units ? count : 0, f_unit = wk, f_slot = 0, f_chunk = chunk0, f_grp = grp0;
     const auto fetch_next = [&]() {
         if (f_left > 0) {
             if (lane == 0) {
@@ -559,8 +560,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tma_load_3d(scale_ring + f_slot * (16 * kTileRows), &tm_s, f_unit * C::kScaleBytes & ~15, n, z, bar);
             }
             f_slot = f_slot + 1 == depth ? 0 : f_slot + 1;
-            if (++f_unit == u1) {
-                f_unit = u0;
+            f_unit += kw;
+            if (f_unit >= units) {
+                f_unit = wk;
                 --f_left;
                 if (++f_grp == groups) {
                     f_grp = 0;
@@ -631,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     srow[s][r] = p.scales + (at + c) * (p.K / (F == kMx ? 32 : 16));
                 }
         }
-        uint32_t xa = smem_u32(xs) + min(few ? g & 1 : g, n_tok - 1) * pitch + t4 * 16 + u0 * kUnitX;
+        uint32_t xa = smem_u32(xs) + min(few ? g & 1 : g, n_tok - 1) * pitch + t4 * 16 + wk * kUnitX;
         // The scale bytes that a lane wants: n of a row, from byte `at` of a row's stage on.
         const auto scales_of = [&](auto n, int unit, int at, Scales &sw) {
             if constexpr (!kTmaScales) {
@@ -657,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 has[1] = t4 == g >> 1 && (g & 1) == 1;
             }
 #pragma unroll 1
-            for (int unit = u0; ok && unit < u1; ++unit) {
+            for (int unit = wk; ok && unit < units; unit += kw) {
                 ok = warp_wait_bounded(&bars[slot], phase, nullptr, p.status, p.wait_limit_ns);
                 if (!ok) break;
                 // One half after the other, not unrolled: in a short launch (one token's w2) waiting
@@ -672,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     else
                         multiply<F>(at, kStep * 128, kNext * 128, x_at, has[0], sw, x, acc, bad);
                 }
-                xa += kUnitX;
+                xa += kUnitX * kw;
                 __syncwarp();                     // the slot is read by all
                 fetch_next();
                 slot = slot + 1 == static_cast<uint32_t>(depth) ? 0 : slot + 1;
