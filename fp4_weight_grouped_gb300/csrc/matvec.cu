@@ -806,15 +806,19 @@ moe_status launch(Params p, cudaStream_t stream, int num_sms) {
     const size_t stages = (kMaxSmem - fixed) / (kWarps * C::kStage);
     p.depth = static_cast<int>(stages < kMaxDepth ? stages : kMaxDepth);
     const size_t bytes = fixed + p.depth * kWarps * C::kStage;
-    // Warps a tile: few mean few sums to join, many that the CTAs' shares of the items come out
-    // even.  In units of a stage's time; an item's end costs about one.
+    // Warps a tile: the fewest rounds of items, in fifths of a stage's time.  An item's end costs
+    // about one of them, but a whole stage where a warp has one stage an item and waits for the
+    // next one's (K = 4,096, w13 by 1, 2, 4, 8 and 16 warps a tile, us: 6 rows 26.0, 16.5, 17.7,
+    // 17.0, 18.4; 48 rows 79.7, 78.9, 75.3, 74.5, 88.1; w2, K = 2,048: 6 rows 15.8, 11.2, 12.0,
+    // 12.5, 13.6; 48 rows 45.7, 44.7, 43.6, 49.5, 65.1).
     constexpr int kTileCols = kSwiglu ? kTileRows / 2 : kTileRows;
     const int64_t chunks = p.row_expert ? (p.rows < p.E ? p.rows : p.E) : (p.rows + p.tok - 1) / p.tok;
     const int64_t tiles = (p.N + kTileCols - 1) / kTileCols, units = p.k_pad / C::kUnit;
     int64_t best = INT64_MAX;
     for (int kw = kWarps; kw >= 1; kw /= 2) {
         const int64_t items = chunks * ((tiles * kw + kWarps - 1) / kWarps);
-        const int64_t cost = (items + num_sms - 1) / num_sms * ((units + kw - 1) / kw + 1);
+        const int64_t stages = (units + kw - 1) / kw;
+        const int64_t cost = (items + num_sms - 1) / num_sms * (stages > 1 ? 5 * stages + 1 : 10);
         if (cost >= best) continue;
         best = cost;
         p.kw = kw;
