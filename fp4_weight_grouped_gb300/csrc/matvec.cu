@@ -44,7 +44,6 @@ namespace mv {
 
 enum Format { kMx, kNv, kBf16 };
 
-constexpr int kWarps = 16, kThreads = 32 * kWarps;
 constexpr int kTok = 8;                       // rows a chunk at most (the MMA's n)
 constexpr int kTileRows = 32;                 // weight rows a tile: two MMAs' share one load of x
 constexpr int kMaxDepth = 4;
@@ -53,6 +52,18 @@ constexpr int kSumPitch = 36;                 // floats of a token's 32 sums, fr
 template <int v>
 struct Int {
     static constexpr int value = v;
+};
+
+// A CTA with an SM to itself, or (kFew, chunks of up to four rows) two CTAs an SM: one works
+// while the other starts, ends an item or waits (one token 27.3 -> 26.5 us, eight in NVFP4
+// 115.5 -> 111.0; bf16 within 4% either way, so it has none).
+template <bool kFew>
+struct Shape {
+    static constexpr int kWarps = kFew ? 8 : 16, kThreads = 32 * kWarps;
+    static constexpr int kTok = kFew ? 4 : 8;
+    static constexpr int kVecs = kFew ? 2 : 1;     // loads of a row of x that a thread keeps in registers
+    static constexpr int kCtas = kFew ? 2 : 1;
+    static constexpr int kMaxSmem = kFew ? 115712 : 232448;
 };
 
 template <int F>
@@ -74,10 +85,11 @@ struct Params {
     void *out;
     int out_bf16;
     int *status;
-    int tok;                      // rows a chunk, 1..kTok
+    int tok;                      // rows a chunk, 1..Shape::kTok
     int kw;                       // warps that share a tile, a power of two
     int depth;                    // stages of a warp's ring
     int k_pad;                    // K up to a stage
+    int smem;                     // bytes a CTA
     int x_vec;                    // x rows at 16-byte addresses
     int chained;                  // x comes from the launch before
     uint64_t wait_limit_ns;
@@ -156,6 +168,7 @@ struct Chunks {
     int *count;
 };
 
+template <int kThreads>
 __device__ __forceinline__ void build_chunks(const Params &p, const Chunks &c) {
     const int tid = threadIdx.x;
     if (!p.row_expert) {
@@ -296,35 +309,45 @@ __device__ __forceinline__ void store_x(uint8_t *row, int v, const uint4 &a, int
     }
 }
 
-// Rows of x in registers, where a thread has one load of each (vecs <= kThreads).
+// Rows of x in registers, where a thread has kVecs loads of each at most.
+template <class S>
 __device__ __forceinline__ void fetch_x(const Params &p, const int *slots, int n, uint4 (&a)[kTok]) {
 #pragma unroll
-    for (int t = 0; t < kTok; ++t)
-        if (t < n && static_cast<int>(threadIdx.x) < p.k_pad / 8) a[t] = load_x(p, slots[t], threadIdx.x);
+    for (int i = 0; i < kTok; ++i) {
+        const int t = i / S::kVecs, v = threadIdx.x + i % S::kVecs * S::kThreads;
+        if (t < n && v < p.k_pad / 8) a[i] = load_x(p, slots[t], v);
+    }
 }
 
 // The chunk's rows of x into shared memory (4-bit weights: f16, scaled by 2^-row_exponent;
 // bf16 as they are), zeros up to k_pad.  tops[t] (zero before) receives row t's largest
 // exponent field.  Where a lane holds 32 k of its own (NVFP4, and MXFP4 for few rows), 16 bytes
 // q of 128 k go to place 4 (q % 4) + q / 4: the lanes find theirs side by side.
-template <int F>
+template <int F, class S>
 __device__ __forceinline__ void stage_x(const Params &p, const int *slots, int n, uint8_t *xs, int pitch, int *tops,
                                         bool fetched, bool by_blocks, uint4 (&a)[kTok]) {
+    constexpr int kThreads = S::kThreads, kVecs = S::kVecs;
     const int tid = threadIdx.x, vecs = p.k_pad / 8;
-    if (vecs <= kThreads) {
-        if (!fetched) fetch_x(p, slots, n, a);
+    if (vecs <= kThreads * kVecs) {
+        if (!fetched) fetch_x<S>(p, slots, n, a);
         if constexpr (F != kBf16) {
 #pragma unroll
-            for (int t = 0; t < kTok; ++t) {
+            for (int t = 0; t < S::kTok; ++t) {
                 if (t >= n) break;
-                const uint32_t top = __reduce_max_sync(0xffffffffu, tid < vecs ? top_of(a[t]) : 0u);
+                uint32_t top = 0;
+#pragma unroll
+                for (int i = 0; i < kVecs; ++i)
+                    if (tid + i * kThreads < vecs) top = max(top, top_of(a[t * kVecs + i]));
+                top = __reduce_max_sync(0xffffffffu, top);
                 if ((tid & 31) == 0) atomicMax(&tops[t], static_cast<int>(top));
             }
             __syncthreads();
         }
 #pragma unroll
-        for (int t = 0; t < kTok; ++t)
-            if (t < n && tid < vecs) store_x<F>(xs + t * pitch, tid, a[t], F == kBf16 ? 0 : tops[t], by_blocks);
+        for (int i = 0; i < kTok; ++i) {
+            const int t = i / kVecs, v = tid + i % kVecs * kThreads;
+            if (t < n && v < vecs) store_x<F>(xs + t * pitch, v, a[i], F == kBf16 ? 0 : tops[t], by_blocks);
+        }
     } else {
         if constexpr (F != kBf16) {
             for (int t = 0; t < n; ++t) {
@@ -505,9 +528,11 @@ __device__ __forceinline__ void multiply_few(uint32_t at, int step, int next, ui
 }
 
 template <int F, bool kSwiglu, bool kTmaScales, bool kFew>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Shape<kFew>::kThreads, Shape<kFew>::kCtas)
     matvec_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_s, const Params p) {
     using C = Fmt<F>;
+    using S = Shape<kFew>;
+    constexpr int kWarps = S::kWarps, kThreads = S::kThreads;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t4 = lane & 3;
@@ -531,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     if (tid < 2 * kTok) tops[tid] = 0;
-    build_chunks(p, ch);
+    build_chunks<kThreads>(p, ch);
 
     constexpr int kTileCols = kSwiglu ? kTileRows / 2 : kTileRows;
     const int tiles = (p.N + kTileCols - 1) / kTileCols;
@@ -574,8 +599,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The first rows of x ahead of the weights, behind which they would queue, unless they
     // come from the launch before (a chain of products): weights and ids do not.
     uint4 xr[kTok];
-    const bool ahead = !p.chained && count > 0 && p.k_pad / 8 <= kThreads;
-    if (ahead) fetch_x(p, ch.order + ch.first[chunk0], ch.first[chunk0 + 1] - ch.first[chunk0], xr);
+    const bool ahead = !p.chained && count > 0 && p.k_pad / 8 <= kThreads * S::kVecs;
+    if (ahead) fetch_x<S>(p, ch.order + ch.first[chunk0], ch.first[chunk0 + 1] - ch.first[chunk0], xr);
 #pragma unroll 1
     for (int i = 0; i < depth; ++i) fetch_next();
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -614,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // equal ones have equal results.
             few = kFew && n_tok <= 2 && (chunk == 0 || ch.expert[chunk - 1] != ch.expert[chunk]) &&
                   (chunk + 1 == *ch.count || ch.expert[chunk + 1] != ch.expert[chunk]);
-            stage_x<F>(p, ch.order + start, n_tok, xs, pitch, tops + turn, ahead && left == count, few, xr);
+            stage_x<F, S>(p, ch.order + start, n_tok, xs, pitch, tops + turn, ahead && left == count, few, xr);
             if (tid < kTok) tops[(turn ^ kTok) + tid] = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[i] = make_uint4(0, 0, 0, 0);
@@ -697,7 +722,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         any_bad |= bad[0][0] | bad[0][1] | bad[1][0] | bad[1][1];
-        if (kFew && few) {                        // the quarters of a sum lie in four lanes
+        if (few) {                                // the quarters of a sum lie in four lanes
 #pragma unroll
             for (int s = 0; s < 2; ++s)
 #pragma unroll
@@ -775,8 +800,6 @@ __global__ void weigh_kernel(const float *y, const int32_t *ids, const float *w,
     else out[static_cast<int64_t>(t) * N + n] = acc;
 }
 
-constexpr int kMaxSmem = 232448;
-
 // Rows [outer][rows][bytes] in boxes of box_bytes by 32 rows, or by 16 rows of two neighbours
 // in `outer`; what lies past an end reads as zeros.
 bool encode(CUtensorMap *map, const void *base, int64_t bytes, int64_t rows, int64_t outer, uint32_t box_bytes, bool two) {
@@ -791,38 +814,49 @@ bool encode(CUtensorMap *map, const void *base, int64_t bytes, int64_t rows, int
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int F, bool kSwiglu, bool kTmaScales, bool kFew>
-moe_status launch(Params p, cudaStream_t stream, int num_sms) {
+// Rows a chunk, stages of a ring and warps a tile; the time that they will take in fifths of a
+// stage's (INT64_MAX: no room).
+template <int F, class S>
+int64_t plan(Params &p, bool swiglu, int num_sms) {
     using C = Fmt<F>;
     p.k_pad = (p.K + C::kUnit - 1) / C::kUnit * C::kUnit;
-    // Rows a chunk and stages of a ring, as many as there is room for; two stages at least (three
-    // measured no faster: 256 experts, 6 and 48 rows, K = 4,096).
-    const size_t rest = kWarps * kMaxDepth * sizeof(uint64_t) + (2 * kTok + 2 + 4 * static_cast<size_t>(p.rows)) * sizeof(int);
-    const size_t x_row = static_cast<size_t>(p.k_pad) * 2 + 64 + kWarps * kSumPitch * sizeof(float);
-    p.tok = p.rows < kTok ? p.rows : kTok;
-    while (p.tok > 1 && rest + p.tok * x_row + 2 * kWarps * C::kStage > kMaxSmem) p.tok = (p.tok + 1) / 2;
+    // As many rows and stages as there is room for; two stages at least (three measured no
+    // faster: 256 experts, 6 and 48 rows, K = 4,096).
+    const size_t rest = S::kWarps * kMaxDepth * sizeof(uint64_t) + (2 * kTok + 2 + 4 * static_cast<size_t>(p.rows)) * sizeof(int);
+    const size_t x_row = static_cast<size_t>(p.k_pad) * 2 + 64 + S::kWarps * kSumPitch * sizeof(float);
+    const size_t ring = S::kWarps * C::kStage;
+    p.tok = p.rows < S::kTok ? p.rows : S::kTok;
+    while (p.tok > 1 && rest + p.tok * x_row + 2 * ring > S::kMaxSmem) p.tok = (p.tok + 1) / 2;
     const size_t fixed = rest + p.tok * x_row;
-    if (fixed + 2 * kWarps * C::kStage > kMaxSmem) return MOE_ERR_CAPACITY;
-    const size_t stages = (kMaxSmem - fixed) / (kWarps * C::kStage);
+    if (fixed + 2 * ring > S::kMaxSmem) return INT64_MAX;
+    const size_t stages = (S::kMaxSmem - fixed) / ring;
     p.depth = static_cast<int>(stages < kMaxDepth ? stages : kMaxDepth);
-    const size_t bytes = fixed + p.depth * kWarps * C::kStage;
+    p.smem = static_cast<int>(fixed + p.depth * ring);
     // Warps a tile: the fewest rounds of items, in fifths of a stage's time.  An item's end costs
     // about one of them, but a whole stage where a warp has one stage an item and waits for the
     // next one's (K = 4,096, w13 by 1, 2, 4, 8 and 16 warps a tile, us: 6 rows 26.0, 16.5, 17.7,
     // 17.0, 18.4; 48 rows 79.7, 78.9, 75.3, 74.5, 88.1; w2, K = 2,048: 6 rows 15.8, 11.2, 12.0,
     // 12.5, 13.6; 48 rows 45.7, 44.7, 43.6, 49.5, 65.1).
-    constexpr int kTileCols = kSwiglu ? kTileRows / 2 : kTileRows;
+    const int cols = swiglu ? kTileRows / 2 : kTileRows, ctas = S::kCtas * num_sms;
     const int64_t chunks = p.row_expert ? (p.rows < p.E ? p.rows : p.E) : (p.rows + p.tok - 1) / p.tok;
-    const int64_t tiles = (p.N + kTileCols - 1) / kTileCols, units = p.k_pad / C::kUnit;
+    const int64_t tiles = (p.N + cols - 1) / cols, units = p.k_pad / C::kUnit;
     int64_t best = INT64_MAX;
-    for (int kw = kWarps; kw >= 1; kw /= 2) {
-        const int64_t items = chunks * ((tiles * kw + kWarps - 1) / kWarps);
+    for (int kw = S::kWarps; kw >= 1; kw /= 2) {
+        const int64_t items = chunks * ((tiles * kw + S::kWarps - 1) / S::kWarps);
         const int64_t stages = (units + kw - 1) / kw;
-        const int64_t cost = (items + num_sms - 1) / num_sms * (stages > 1 ? 5 * stages + 1 : 10);
+        const int64_t cost = (items + ctas - 1) / ctas * (stages > 1 ? 5 * stages + 1 : 10);
         if (cost >= best) continue;
         best = cost;
         p.kw = kw;
     }
+    return best;
+}
+
+template <int F, bool kSwiglu, bool kTmaScales, bool kFew>
+moe_status launch(Params p, cudaStream_t stream, int num_sms) {
+    using C = Fmt<F>;
+    using S = Shape<kFew>;
+    if (plan<F, S>(p, kSwiglu, num_sms) == INT64_MAX) return MOE_ERR_CAPACITY;
     CUtensorMap tm_w, tm_s;
     const int64_t outer = static_cast<int64_t>(p.E) * (kSwiglu ? 2 : 1);
     if (!encode(&tm_w, p.w, F == kBf16 ? 2ll * p.K : p.K / 2, p.N, outer, 128, kSwiglu)) return MOE_ERR_CUDA;
@@ -834,7 +868,7 @@ moe_status launch(Params p, cudaStream_t stream, int num_sms) {
     const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
     const auto kernel = matvec_kernel<F, kSwiglu, kTmaScales, kFew>;
     if (!bit || !(mask.load(std::memory_order_acquire) & bit)) {
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) != cudaSuccess)
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kMaxSmem) != cudaSuccess)
             return MOE_ERR_CUDA;
         mask.fetch_or(bit, std::memory_order_release);
     }
@@ -842,9 +876,9 @@ moe_status launch(Params p, cudaStream_t stream, int num_sms) {
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(num_sms);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = bytes;
+    cfg.gridDim = dim3(S::kCtas * num_sms);
+    cfg.blockDim = dim3(S::kThreads);
+    cfg.dynamicSmemBytes = p.smem;
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = p.chained ? 1 : 0;
@@ -853,6 +887,13 @@ moe_status launch(Params p, cudaStream_t stream, int num_sms) {
 
 template <int F>
 moe_status launch_format(const Params &p, bool swiglu, bool tma, bool few, cudaStream_t stream, int num_sms) {
+    // Two CTAs an SM where chunks of two rows fit and there are items for them (one row of one
+    // matrix, K = N = 4,096: 8.3 us by them, 7.0 by one).
+    if (few) {
+        Params q = p;
+        const int64_t one = plan<F, Shape<false>>(q, swiglu, num_sms);
+        few = plan<F, Shape<true>>(q, swiglu, num_sms) <= one && (q.tok > 1 || q.rows == 1);
+    }
     if (few)
         return swiglu ? tma ? launch<F, true, true, true>(p, stream, num_sms) : launch<F, true, false, true>(p, stream, num_sms)
                       : tma ? launch<F, false, true, true>(p, stream, num_sms) : launch<F, false, false, true>(p, stream, num_sms);
@@ -886,12 +927,12 @@ moe_status launch_matvec(const Matvec &m, cudaStream_t stream, int num_sms) {
         return m.swiglu ? mv::launch<mv::kBf16, true, false, false>(p, stream, num_sms)
                         : mv::launch<mv::kBf16, false, false, false>(p, stream, num_sms);
     const bool nv = m.format == Matvec::kNv;
-    // Whether experts with one or two rows have their own form in the kernel: not where they are
-    // the exception, which would then only wait for the others (256 experts, six a token,
-    // layer_decode with and without it, MXFP4 / NVFP4: 6 rows 29.4, 31.3 / 30.7, 31.3 us; 48 rows
-    // 124, 136 / 129.5, 136; 96 rows 200, 205 / 209.6, 206; 384 rows 484, 484 / 510, 490), nor
-    // where a call surely has more (4 rows of one matrix: 8.7, 8.4).
-    const bool few = m.row_expert && m.E > 1 ? m.rows <= 2 * m.E && m.rows <= (nv ? 64 : 128) : m.rows <= 2;
+    // Whether experts with one or two rows have their own form in the kernel (and chunks up to four
+    // rows, so that two CTAs fit an SM): not where a call has so many rows that these are the
+    // exception (256 experts, w13 + w2 with and without it, MXFP4 / NVFP4, us: 24 rows 64, 73 / 65,
+    // 73; 48 rows 106, 123 / 110, 123; 96 rows 184, 197 / 191, 196; 192 rows 312, 328 / 326, 326;
+    // 384 rows 567, 492 / 579, 492), nor where it has one matrix (4 rows: 8.7, 8.4).
+    const bool few = m.row_expert && m.E > 1 ? m.rows <= m.E : m.rows <= 2;
     // Rows of scales that TMA takes: a multiple of 16 bytes, at 16-byte addresses.
     const bool tma = m.K / (nv ? 16 : 32) % 16 == 0 && reinterpret_cast<uintptr_t>(m.scales) % 16 == 0;
     return nv ? mv::launch_format<mv::kNv>(p, m.swiglu, tma, few, stream, num_sms)
