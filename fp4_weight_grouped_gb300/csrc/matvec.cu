@@ -785,16 +785,28 @@ __global__ void __launch_bounds__(Shape<kFew>::kThreads, Shape<kFew>::kCtas)
 }
 
 // out[t, n] = sum_j w[t, j] * y[t k + j, n] over the slots with a valid expert, in ascending j.
+// ids and weights come ahead of the wait for y, and the loads of eight rows go out together.
 template <typename T>
 __global__ void weigh_kernel(const float *y, const int32_t *ids, const float *w, int k, int N, int E, T *out) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    __shared__ float weight[MOE_MATVEC_MAX_ROWS];
+    __shared__ bool real[MOE_MATVEC_MAX_ROWS];
     const int n = blockIdx.x * blockDim.x + threadIdx.x, t = blockIdx.y;
+    for (int j = threadIdx.x; j < k; j += blockDim.x) {        // k: up to MOE_MATVEC_MAX_ROWS
+        weight[j] = __ldg(w + t * k + j);
+        real[j] = static_cast<unsigned>(__ldg(ids + t * k + j)) < static_cast<unsigned>(E);
+    }
+    __syncthreads();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (n >= N) return;
+    const float *row = y + static_cast<int64_t>(t) * k * N + n;
     float acc = 0.f;
-    for (int j = 0; j < k; ++j) {
-        const int s = t * k + j;
-        if (static_cast<unsigned>(__ldg(ids + s)) >= static_cast<unsigned>(E)) continue;
-        acc = fmaf(__ldg(w + s), __ldcg(y + static_cast<int64_t>(s) * N + n), acc);
+    for (int j = 0; j < k; j += 8) {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = j + i < k && real[j + i] ? __ldcg(row + static_cast<int64_t>(j + i) * N) : 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (j + i < k && real[j + i]) acc = fmaf(weight[j + i], v[i], acc);
     }
     if constexpr (sizeof(T) == 2) out[static_cast<int64_t>(t) * N + n] = __float2bfloat16_rn(acc);
     else out[static_cast<int64_t>(t) * N + n] = acc;
