@@ -300,14 +300,21 @@ __global__ void __launch_bounds__(32) finish_kernel(const double *partial, int n
     if (threadIdx.x == 0) *norm = static_cast<float>(sqrt(total));
 }
 
+// Elements a chunk: small enough to spread over the blocks, large enough to stream.  And no more
+// blocks than chunks: each leaves a sum that every block of the second kernel reads.
+int chunk_size(const GradList &g, int *blocks) {
+    int64_t all = 0, chunks = 0;
+    for (int i = 0; i < g.n; ++i) all += g.sizes[i];
+    int chunk = kMinChunk;
+    while (chunk < kMaxChunk && all / chunk > 4ll * *blocks) chunk *= 2;
+    for (int i = 0; i < g.n && chunks < *blocks; ++i) chunks += (g.sizes[i] + chunk - 1) / chunk;
+    if (chunks < *blocks) *blocks = static_cast<int>(chunks);
+    return chunk;
+}
+
 // Calls body(list, first) for every launch's worth of tensors.
 template <int kCap, class Body>
-moe_status for_lists(const GradList &g, int blocks, const Body &body) {
-    int64_t all = 0;
-    for (int i = 0; i < g.n; ++i) all += g.sizes[i];
-    // Chunks small enough to spread over the blocks, large enough to stream.
-    int chunk = kMinChunk;
-    while (chunk < kMaxChunk && all / chunk > 4ll * blocks) chunk *= 2;
+moe_status for_lists(const GradList &g, int chunk, const Body &body) {
     List<kCap> l;
     for (int i = 0; i < g.n;) {
         const int first = i;
@@ -349,9 +356,10 @@ moe_status launch_after(void (*kernel)(Args...), int blocks, int threads, bool c
 
 template <int kCap>
 moe_status run(const GradList &g, cudaStream_t stream, int num_sms, int *launches) {
-    const int blocks = num_sms * kBlocksPerSm;
+    int blocks = num_sms * kBlocksPerSm;
+    const int chunk = chunk_size(g, &blocks);
     double *partial = static_cast<double *>(g.partial);
-    moe_status st = for_lists<kCap>(g, blocks, [&](const List<kCap> &l, bool first) {
+    moe_status st = for_lists<kCap>(g, chunk, [&](const List<kCap> &l, bool first) {
         ++*launches;
         return launch_after(norm_kernel<kCap>, blocks, kThreads, false, stream, l, partial, static_cast<int>(!first));
     });
@@ -363,7 +371,7 @@ moe_status run(const GradList &g, cudaStream_t stream, int num_sms, int *launche
     }
     // The first scaling launch follows a norm launch and may start under its end; in place it
     // writes what that read, but only behind its wait.
-    return for_lists<kCap>(g, blocks, [&](const List<kCap> &l, bool first) {
+    return for_lists<kCap>(g, chunk, [&](const List<kCap> &l, bool first) {
         ++*launches;
         return launch_after(scale_kernel<kCap>, blocks, kThreads, first, stream, l, sums, blocks, g.max_norm, g.eps,
                             first ? g.norm : static_cast<float *>(nullptr));
