@@ -320,6 +320,66 @@ def test_many_rows_of_one_expert(B, rows, fmt):
     assert torch.equal(same, got[:1].expand(rows, -1))
 
 
+@pytest.mark.parametrize("fmt", [0, 1], ids=["mx", "nv"])
+@pytest.mark.parametrize("K", [32, 256, 1056, 2048, 4608, 12288, 20480])
+def test_experts_with_one_to_nine_rows_in_one_call(B, K, fmt):
+    """No more rows than experts: experts with one or two rows go their own way, beside others."""
+    g = torch.Generator(device="cuda").manual_seed(K)
+    w = weights(g, 48, 70, K, fmt)
+    counts = {3: 1, 4: 2, 5: 1, 11: 3, 12: 2, 20: 4, 21: 5, 30: 1, 40: 9, 47: 2}
+    experts = [e for e, n in counts.items() for _ in range(n)]
+    order = torch.randperm(len(experts), generator=g, device="cuda").tolist()
+    experts = [experts[i] for i in order]
+    x = torch.randn((len(experts), K), generator=g, device="cuda").bfloat16()
+    ids = torch.tensor(experts, dtype=torch.int32, device="cuda")
+    got = B.fp4_matvec(x, w[0], w[1], fmt, row_expert=ids, weight_scale_2=w[2])
+    check(got, x, w, experts, 1, fmt)
+    same = x[:1].expand(len(experts), K).contiguous()
+    got = B.fp4_matvec(same, w[0], w[1], fmt, row_expert=ids, weight_scale_2=w[2])
+    for e in counts:
+        rows = [r for r, f in enumerate(experts) if f == e]
+        assert all(torch.equal(got[r], got[rows[0]]) for r in rows), e
+
+
+@pytest.mark.parametrize("fmt", [0, 1], ids=["mx", "nv"])
+@pytest.mark.parametrize("rows", [1, 2, 3])
+def test_a_row_that_is_not_finite_beside_others_of_its_expert(B, rows, fmt):
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    w = weights(g, 9, 40, 512, fmt)
+    ids = torch.tensor([4] * rows, dtype=torch.int32, device="cuda")
+    x = torch.randn((rows, 512), generator=g, device="cuda").bfloat16()
+    clean = B.fp4_matvec(x, w[0], w[1], fmt, row_expert=ids, weight_scale_2=w[2])
+    x[0, 77] = float("inf")
+    got = B.fp4_matvec(x, w[0], w[1], fmt, row_expert=ids, weight_scale_2=w[2])
+    assert torch.equal(got[1:], clean[1:])
+    at = dense(w, 4, fmt)[:, 77]
+    # An infinity times a weight keeps its sign; times 0 it is NaN.
+    want = torch.where(at == 0, torch.full_like(at, float("nan")), at.sign() * float("inf"))
+    assert torch.equal(got[0].isnan(), want.isnan()) and torch.equal(got[0][at != 0].double(), want[at != 0])
+
+
+@pytest.mark.parametrize("rows", [1, 2, 3])
+@pytest.mark.parametrize("fmt,byte", [(0, 253), (0, 255), (1, 0x7F), (1, 0xFF)])
+def test_bad_scales_of_experts_with_few_rows(B, rows, fmt, byte):
+    """In each block of a row, the first, the last and one within: its column is NaN, no other."""
+    g = torch.Generator(device="cuda").manual_seed(byte)
+    K, N = 512, 40
+    w = weights(g, 9, N, K, fmt)
+    x = torch.randn((rows, K), generator=g, device="cuda").bfloat16()
+    ids = torch.tensor([4] * rows, dtype=torch.int32, device="cuda")
+    clean = B.fp4_matvec(x, w[0], w[1], fmt, row_expert=ids, weight_scale_2=w[2])
+    blocks = w[1].shape[-1]
+    cols = {0: 0, 7: blocks - 1, 13: blocks // 2, 22: 5, 39: 10}
+    for n, b in cols.items():
+        w[1][4, n, b] = byte
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    got = B.fp4_matvec(x, w[0], w[1], fmt, row_expert=ids, weight_scale_2=w[2], workspace=ws)
+    bad = torch.zeros(N, dtype=torch.bool, device="cuda")
+    bad[list(cols)] = True
+    assert bool(got[:, bad].isnan().all()) and torch.equal(got[:, ~bad], clean[:, ~bad])
+    assert B.read_status(ws) == B.MOE_ERR_DATA
+
+
 def test_two_streams_at_once(B):
     g = torch.Generator(device="cuda").manual_seed(13)
     w = weights(g, 16, 512, 1024, 0)
