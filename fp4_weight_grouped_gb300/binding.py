@@ -9,6 +9,7 @@ import ctypes as C
 import os
 import threading
 from array import array
+from operator import attrgetter
 
 import torch
 
@@ -1003,20 +1004,20 @@ def ffn_backward(dout: torch.Tensor, x: torch.Tensor, w13: torch.Tensor, w2: tor
 # ------------------------------------------------------- gradient norm and clipping
 
 _GRAD_DTYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+_DTYPE = attrgetter("dtype")
 
 
 def _grad_arrays(grads, name="grads"):
-    """Pointers, sizes and types of a list of gradients, as arrays that the library reads."""
-    ptrs, sizes, dtypes = array("Q"), array("q"), array("i")
-    device = _current_device()
-    for t in grads:
-        dtype = _GRAD_DTYPES.get(t.dtype)
-        if dtype is None or not t.is_contiguous() or t.get_device() != device:
-            raise ValueError(f"{name}[{len(ptrs)}]: a contiguous float32 or bfloat16 tensor on the current device is needed")
-        ptrs.append(t.data_ptr())
-        sizes.append(t.numel())
-        dtypes.append(dtype)
-    return ptrs, sizes, dtypes
+    """Pointers, sizes and types of a list of gradients, as arrays that the library reads.  By
+    maps over the list: a model's few hundred tensors cost the host more than a small model's
+    clipping takes."""
+    grads, device = list(grads), _current_device()
+    dtypes = list(map(_GRAD_DTYPES.get, map(_DTYPE, grads)))
+    if None in dtypes or not all(map(torch.Tensor.is_contiguous, grads)) or {t.get_device() for t in grads} - {device}:
+        bad = next(i for i, t in enumerate(grads)
+                   if dtypes[i] is None or not t.is_contiguous() or t.get_device() != device)
+        raise ValueError(f"{name}[{bad}]: a contiguous float32 or bfloat16 tensor on the current device is needed")
+    return (array("Q", map(torch.Tensor.data_ptr, grads)), array("q", map(torch.Tensor.numel, grads)), array("i", dtypes))
 
 
 def _address(a):
