@@ -785,7 +785,8 @@ moe_status moe_fp4_matvec(const uint16_t *x, int64_t x_stride, int32_t index_div
                           int32_t rows, int32_t K, const uint8_t *codes, const uint8_t *scales,
                           const float *weight_scale_2, moe_fp4_format format, int32_t E, int32_t N, void *out,
                           moe_dtype out_dtype, void *workspace, size_t workspace_bytes, void *stream) {
-    if (!known_dtype(out_dtype) || !aligned(out, out_dtype == MOE_F32 ? 4 : 2)) return MOE_ERR_INVALID_ARG;
+    if (!known_dtype(out_dtype) || !aligned(out, out_dtype == MOE_F32 ? 4 : 2) || !aligned(row_expert, 4))
+        return MOE_ERR_INVALID_ARG;
     moe_status st = check_matvec_args(x, x_stride, index_div, rows, K, codes, scales, weight_scale_2, format, E, N, N,
                                       out, workspace, workspace_bytes);
     if (st != MOE_OK) return st;
@@ -802,7 +803,7 @@ moe_status moe_fp4_matvec_swiglu(const uint16_t *x, int64_t x_stride, int32_t in
                                  int32_t rows, int32_t K, const uint8_t *codes, const uint8_t *scales,
                                  const float *weight_scale_2, moe_fp4_format format, int32_t E, int32_t I,
                                  uint16_t *h, void *workspace, size_t workspace_bytes, void *stream) {
-    if (!aligned(h, 2)) return MOE_ERR_INVALID_ARG;
+    if (!aligned(h, 2) || !aligned(row_expert, 4)) return MOE_ERR_INVALID_ARG;
     moe_status st = check_matvec_args(x, x_stride, index_div, rows, K, codes, scales, weight_scale_2, format, E,
                                       2 * static_cast<int64_t>(I), I, h, workspace, workspace_bytes);
     if (st != MOE_OK) return st;
@@ -821,7 +822,7 @@ moe_status moe_layer_decode(const uint16_t *x, const int32_t *topk_ids, const fl
                             const uint8_t *w2_scales, const float *w2_scale_2, uint16_t *h, float *y2, void *out,
                             moe_dtype out_dtype, void *workspace, size_t workspace_bytes, void *stream) {
     if (T < 0 || k <= 0 || !known_dtype(out_dtype) || !aligned(out, out_dtype == MOE_F32 ? 4 : 2) || !aligned(h, 2) ||
-        !aligned(y2, 4))
+        !aligned(y2, 4) || !aligned(topk_ids, 4) || !aligned(topk_w, 4))
         return MOE_ERR_INVALID_ARG;
     if (T > 0 && (!topk_ids || !topk_w || !out)) return MOE_ERR_INVALID_ARG;
     const int64_t slots = static_cast<int64_t>(T) * k;

@@ -731,7 +731,7 @@ MOE_API moe_status moe_gather_backward(const void *dx_sorted, moe_dtype in_dtype
  *
  * with w as in moe_mxfp4_grouped_gemm (MOE_FP4_MX: e2m1 * 2^(scale - 127) per 32 k) or
  * moe_nvfp4_grouped_gemm (MOE_FP4_NV: e2m1 * e4m3 per 16 k * weight_scale_2[e]).  Made
- * for decode steps: rows of one expert share one pass over its weights, 8 at a time,
+ * for decode steps: rows of one expert share one pass over its weights, 4 or 8 at a time,
  * and weights of experts that no row names are not read.  Many rows an expert belong
  * to the grouped GEMMs.
  *
@@ -751,7 +751,9 @@ MOE_API moe_status moe_gather_backward(const void *dx_sorted, moe_dtype in_dtype
  * Products are exact and sums are f32, but for elements of x below 2^-28 of their row's
  * largest: they are rounded to 2^-38 of it.  MOE_FP4_MX blocks whose scale is below
  * 2^-118 count as zero.  A scale byte that the format does not allow (E8M0 above 252,
- * an E4M3 NaN) sets MOE_ERR_DATA and makes its column NaN.  Results repeat bit for bit.
+ * an E4M3 NaN) sets MOE_ERR_DATA and makes its column NaN.  Results repeat bit for bit, and
+ * equal rows of a call that name the same expert have equal results; between calls of
+ * other row counts sums may be formed in another order.  The output overlaps no input.
  */
 #define MOE_MATVEC_MAX_ROWS 512
 #define MOE_MATVEC_MAX_K 32768
@@ -791,6 +793,7 @@ MOE_API moe_status moe_fp4_matvec_swiglu(const uint16_t *x, int64_t x_stride, in
  *  w13_scale_2, w2_scale_2   device f32 [E] (MOE_FP4_NV).
  *  h, y2        caller-owned intermediates: bf16 [T*k, inter], f32 [T*k, hidden].
  *  out          device [T, hidden], f32 or bf16.
+ * The outputs overlap no input and not each other.
  */
 MOE_API moe_status moe_layer_decode(const uint16_t *x, const int32_t *topk_ids, const float *topk_w,
                                     int32_t T, int32_t k, int32_t E, int32_t hidden, int32_t inter,
@@ -818,7 +821,8 @@ MOE_API moe_status moe_layer_decode(const uint16_t *x, const int32_t *topk_ids, 
  *  h            device bf16 [T, inter] out.
  *  out          device [T, hidden] out, f32 or bf16.
  *  workspace    device, >= 256 bytes (status word).
- * All buffers 16-byte aligned.  Two launches; results repeat bit for bit.
+ * All buffers 16-byte aligned; outputs overlap no input and not each other.  Two launches;
+ * results repeat bit for bit.
  */
 MOE_API moe_status moe_ffn_forward(const uint16_t *x, int64_t x_stride, int32_t T, int32_t hidden,
                                    int32_t inter, const uint16_t *w13, const uint16_t *w2,
@@ -839,7 +843,8 @@ MOE_API moe_status moe_ffn_forward(const uint16_t *x, int64_t x_stride, int32_t 
  *               dx and dw13 are both NULL; gu likewise).
  *  dx           device bf16 [T, hidden] out; dw13 [2*inter, hidden] and dw2 [hidden, inter]
  *               out, of dw_dtype.  Each may be NULL (not computed).
- * All buffers 16-byte aligned.  Up to two launches; results repeat bit for bit.
+ * All buffers 16-byte aligned; outputs overlap no input and not each other.  Up to two
+ * launches; results repeat bit for bit.
  */
 MOE_API moe_status moe_ffn_backward(const uint16_t *dout, const uint16_t *x, int64_t x_stride,
                                     int32_t T, int32_t hidden, int32_t inter, const uint16_t *w13,
@@ -858,8 +863,9 @@ MOE_API moe_status moe_ffn_backward(const uint16_t *dout, const uint16_t *x, int
  *  norm         device f32 [1] out (infinity where the norm passes f32's range).
  *  workspace    device, >= MOE_GRAD_WORKSPACE_BYTES, 16-byte aligned.  Calls that may run
  *               at the same time need one each.
- * Sums are f64 but for a thread's few elements, and right over the whole range of the
- * types.  Results repeat bit for bit.
+ * Sums are pairs of f32 (a sum and what its roundings left out) within a block and f64
+ * across blocks; the norm is right over the whole range of the types.  Results repeat bit
+ * for bit.
  */
 #define MOE_GRAD_WORKSPACE_BYTES (32u * 1024u)
 MOE_API moe_status moe_grad_norm(const void *const *grads, const int64_t *sizes,

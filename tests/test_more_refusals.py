@@ -58,6 +58,18 @@ def test_layer_decode(lib):
     check(lib.moe_layer_decode, good, [dict(T=300, c2=None), dict(hidden=65536, inter=40)])
 
 
+def test_ids_and_weights_off_their_alignment(lib):
+    """A load of four bytes at another address would end the process's use of the GPU."""
+    good = {**{n: v for n, v in MATVEC.items() if n not in ("N", "out", "dt", "ws", "wsb", "stream")}, "I": 24, "h": FAKE,
+            "ws": FAKE, "wsb": 256, "stream": None}
+    for ids in (4097, 4098):
+        check(lib.moe_fp4_matvec, {**MATVEC, "rows": 513}, [dict(ids=ids)])
+        check(lib.moe_fp4_matvec_swiglu, {**good, "rows": 513}, [dict(ids=ids)])
+    good = dict(x=FAKE, ids=FAKE, w=FAKE, T=300, k=2, E=4, hidden=64, inter=32, fmt=0, c13=FAKE, s13=FAKE, g13=None, c2=FAKE,
+                s2=FAKE, g2=None, h=FAKE, y2=FAKE, out=FAKE, dt=0, ws=FAKE, wsb=256, stream=None)
+    check(lib.moe_layer_decode, good, [dict(ids=4098), dict(w=4097), dict(w=4098)])
+
+
 FFN = dict(x=FAKE, x_stride=72, T=5, hidden=64, inter=32, w13=FAKE, w2=FAKE, gu=FAKE, h=FAKE, out=FAKE, dt=1, ws=FAKE,
            wsb=256, stream=None)
 FFN_BAD = [dict(x=None), dict(x=FAKE + 8), dict(x_stride=56), dict(x_stride=68), dict(x_stride=-8), dict(T=-1),
