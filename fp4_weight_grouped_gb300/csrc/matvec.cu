@@ -5,7 +5,12 @@
 // w in 4 bits (MXFP4: e2m1 * 2^(s - 127) per 32 k; NVFP4: e2m1 * e4m3 per 16 k, times
 // an f32 an expert) or bf16.  For one to a few dozen rows: no sort, no row bands.
 //
-//  * Rows of the same expert are taken together, up to 8 at a time (a chunk), so a
+// Bound by HBM where there are weights enough: 6.6 TB/s for every further token's six experts
+// in MXFP4 (hidden 4,096, inter 2,048, w13; 6.3 for w2), on top of 7 to 8 us that a launch
+// takes before and behind them (5.5 for a tiny product).  One token: w13 16 us, w2 11; eight
+// in NVFP4: 75 us (6.0 TB/s) and 43 (5.3).
+//
+//  * Rows of the same expert are taken together, up to 8 or 4 at a time (a chunk), so a
 //    weight is read once for them.  Every CTA works the chunks out from the ids itself.
 //  * A tile is 32 weight rows (SwiGLU: 16 gate rows and the 16 matching up rows, so that one
 //    thread finds both).  kw warps of a CTA share a tile's K, 256 k (bf16: 64) a stage, every
@@ -23,10 +28,13 @@
 //    2^15 * 6 * 32 a block, 1,024 blocks) below 2^127 for every scale that the format has;
 //    scales below 2^-118 underflow to 0 for it.
 //    NVFP4: e2m1 * e4m3 has 6 bits and fits f16, so the scale goes into the weight.
+//    Experts with one or two rows: the columns that are left over keep the scale blocks apart
+//    (multiply_few), for either format.
 //  * Each warp fetches its own stages by TMA into its own ring, across tiles: 128 bytes of 32
 //    rows a box (a box costs an SM at least 33 ns: boxes of 64 bytes by 16 rows, and scales
 //    in boxes of their own beside them, held the kernel at 4.4 TB/s; by cp.async the copies'
-//    writes took half of the shared-memory pipe).
+//    writes took half of the shared-memory pipe).  HBM gives rows of 128 bytes 6.0 to 6.2
+//    TB/s when they come alone, rows of 256 and more 6.8 to 7.0.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
