@@ -17,7 +17,8 @@
 //  * CTA pairs (tcgen05.mma cta_group::2): 256 rows by kN columns an item, the rows split
 //    over the pair's tensor memory, either CTA fetching half of A and half of B.  64 k are
 //    128-byte rows in the 128-byte swizzle, an atom; a stage is one of them or two.
-//  * Accumulators are double-buffered: four epilogue warps empty one while the other fills.
+//  * Accumulators are double-buffered: eight epilogue warps empty one while the other fills (four took
+//    longer than the MMAs for the gradient's part: 64 tokens' backward 45 -> 39 us).
 //  * SwiGLU: the even CTA fetches gate rows of W13 and the odd CTA the matching up rows, so
 //    a thread finds g and u of one output in two column ranges of its own lane.
 //  * The gradient's elementwise part is the epilogue of dh: dh is never stored.
@@ -37,6 +38,7 @@
 #include "device_common.cuh"
 #include "launch.h"
 #include "pair_drain.h"
+#include "pair_schedule.h"
 #include "tensor_map.h"
 #include "vec_io.cuh"
 
@@ -44,7 +46,8 @@ namespace moe {
 namespace ffn {
 
 constexpr int kProducerWarp = 0, kIssuerWarp = 1, kEpilogueWarp = 2;
-constexpr int kThreads = 32 * (kEpilogueWarp + 4);
+constexpr int kEpilogueWarps = 8;                  // two a quarter of the tensor memory, half of the columns each
+constexpr int kThreads = 32 * (kEpilogueWarp + kEpilogueWarps);
 constexpr int kStageK = 64;
 constexpr int kRows = 128;                         // of A a CTA
 constexpr int kABytes = kRows * 128;
@@ -96,6 +99,7 @@ struct Args {
     CUtensorMap a[kMaxJobs], b[kMaxJobs], b_half[kMaxJobs];      // b_half: boxes of half the rows
     Job job[kMaxJobs];
     int jobs, items;
+    PairSchedule schedule;
     int stages, stage_bytes, a_bytes;        // of the ring: atoms of A, then those of B
     int chained;                             // A comes from the launch before
     int *status;
@@ -171,9 +175,9 @@ __device__ __forceinline__ Item item_of(const Args &p, int i) {
 
 // What the odd CTA copies in stage i of a pair's stream.
 template <int kN>
-__device__ __noinline__ uint32_t odd_bytes(const Args &p, int first, int step, uint32_t i) {
-    int item = first;
-    for (; item + step < p.items; item += step) {
+__device__ __noinline__ uint32_t odd_bytes(const Args &p, int pair, uint32_t i) {
+    int item = pair;
+    for (; p.schedule.next(pair, item) < p.items; item = p.schedule.next(pair, item)) {
         const uint32_t n = p.job[item_of(p, item).job].k_stages;
         if (i < n) break;
         i -= n;
@@ -206,14 +210,17 @@ __device__ __forceinline__ void store16(void *row, int n, int cols, bool f32, bo
     if (n + 8 < cols) *reinterpret_cast<uint4 *>(o + 8) = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
-__device__ __forceinline__ void load16(const uint16_t *row, int n, int cols, float (&v)[16]) {
+// 16 consecutive elements of a row at column n, as they are; zeros past the last column.
+__device__ __forceinline__ void load16(const uint16_t *row, int n, int cols, uint4 (&v)[2]) {
 #pragma unroll
-    for (int h = 0; h < 16; h += 8) {
-        float t[8] = {};
-        if (n + h < cols) load_row<8>(reinterpret_cast<const __nv_bfloat16 *>(row + n + h), t);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[h + i] = t[i];
-    }
+    for (int h = 0; h < 2; ++h)
+        v[h] = n + 8 * h < cols ? __ldg(reinterpret_cast<const uint4 *>(row + n + 8 * h)) : make_uint4(0, 0, 0, 0);
+}
+
+__device__ __forceinline__ float bf16_of(const uint4 (&v)[2], int i) {
+    const uint4 &q = v[i >> 3];
+    const uint32_t w = (i & 7) < 2 ? q.x : (i & 7) < 4 ? q.y : (i & 7) < 6 ? q.z : q.w;
+    return __uint_as_float(i & 1 ? w & 0xFFFF0000u : w << 16);
 }
 
 // dg and du of one element; s and 1 - s both without cancellation.
@@ -240,7 +247,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ffn_ker
     volatile int *abort_flag = &misc->abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
-    const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+    const int pair = blockIdx.x >> 1;
     const uint64_t lim = p.wait_limit_ns;
 
     if (threadIdx.x == 0) {
@@ -252,7 +259,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ffn_ker
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&acc_full[i], 1);
-            mbar_init(&acc_empty[i], 8);           // four warps of either CTA
+            mbar_init(&acc_empty[i], 2 * kEpilogueWarps);
         }
         mbar_init(final_bar, 1);
         mbar_fence_init();
@@ -279,7 +286,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ffn_ker
             uint32_t slot = 0, phase = 1, issued = 0, ahead = 0;
             bool ok = true;
             if (!T::kAhead) asm volatile("griddepcontrol.wait;" ::: "memory");
-            for (int i = first; ok && i < p.items; i += step) {
+            for (int i = pair; ok && i < p.items; i = p.schedule.next(pair, i)) {
                 const Item it = item_of(p, i);
                 const Job &w = p.job[it.job];
                 const CUtensorMap *ma = &p.a[it.job], *mb = it.half ? &p.b_half[it.job] : &p.b[it.job];
@@ -317,7 +324,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ffn_ker
                     }
                 };
                 constexpr int kStep = T::kAtoms * kStageK;
-                if (T::kAhead && p.chained && i == first) {      // B, which the launch before does not write
+                if (T::kAhead && p.chained && i == pair) {      // B, which the launch before does not write
                     ahead = min(min(n_stages, 4u), static_cast<uint32_t>(w.k_stages));
                     for (uint32_t q = 0; q < ahead; ++q) load_b(q, q * kStep);
                     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -340,7 +347,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ffn_ker
             const uint32_t base = smem_u32(smem);
             uint32_t slot = 0, phase = 0, buf = 0, acc_phase = 1;
             bool ok = true;
-            for (int i = first; ok && i < p.items; i += step) {
+            for (int i = pair; ok && i < p.items; i = p.schedule.next(pair, i)) {
                 const Item it = item_of(p, i);
                 const Job &w = p.job[it.job];
                 const uint32_t idesc = idesc_bf16_f32(2 * kRows, kN >> it.half) | (w.a_mn ? 1u << 15 : 0) | (w.b_mn ? 1u << 16 : 0);
@@ -374,9 +381,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ffn_ker
             wait(final_bar, 0, nullptr, p.status, lim);
         }
     } else if (warp >= kEpilogueWarp) {
-        const int quarter = warp & 3;
+        const int quarter = warp & 3, side = (warp - kEpilogueWarp) >> 2;
         uint32_t buf = 0, phase = 0;
-        for (int i = first; i < p.items; i += step) {
+        for (int i = pair; i < p.items; i = p.schedule.next(pair, i)) {
             const Item it = item_of(p, i);
             const Job &w = p.job[it.job];
             if (!warp_wait_bounded(&acc_full[buf], phase, abort_flag, p.status, lim)) break;
@@ -392,7 +399,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ffn_ker
                 uint16_t *gu = w.gu ? w.gu + (real ? row : 0) * 2 * w.n : nullptr;
                 const bool gu_sector = (reinterpret_cast<uintptr_t>(w.gu) & 31) == 0 && w.n % 16 == 0;
 #pragma unroll 1
-                for (int c = 0; c < cols / 2; c += 16) {
+                for (int c = side * cols / 4; c < (side + 1) * cols / 4; c += 16) {
                     const int n = it.n0 + c;
                     if (n >= w.n) break;
                     uint32_t rg[16], ru[16];
@@ -418,20 +425,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ffn_ker
             } else {
                 const uint16_t *gu = w.gu + (real ? row : 0) * 2 * w.n;
                 uint16_t *up = reinterpret_cast<uint16_t *>(out) + w.n;
+                // g and u of the next columns are asked for ahead of the work on these.
+                uint4 g[2], u[2];
+                if (w.epilogue == kGateBack) {
+                    load16(gu, it.n0 + side * cols / 2, w.n, g);
+                    load16(gu + w.n, it.n0 + side * cols / 2, w.n, u);
+                }
 #pragma unroll 1
-                for (int c = 0; c < cols; c += 16) {
+                for (int c = side * cols / 2; c < (side + 1) * cols / 2; c += 16) {
                     const int n = it.n0 + c;
                     if (n >= w.n) break;
                     uint32_t r[16];
                     tmem_ld16(acc + c, r);
                     float v[16];
                     if (w.epilogue == kGateBack) {
-                        float g[16], u[16], du[16];
-                        load16(gu, n, w.n, g);
-                        load16(gu + w.n, n, w.n, u);
+                        float du[16];
+                        uint4 next_g[2], next_u[2];
+                        const int next = c + 16 < (side + 1) * cols / 2 ? n + 16 : w.n;
+                        load16(gu, next, w.n, next_g);
+                        load16(gu + w.n, next, w.n, next_u);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int q = 0; q < 16; ++q) gate_back(__uint_as_float(r[q]), g[q], u[q], v[q], du[q]);
+                        for (int q = 0; q < 16; ++q) gate_back(__uint_as_float(r[q]), bf16_of(g, q), bf16_of(u, q), v[q], du[q]);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            g[h] = next_g[h];
+                            u[h] = next_u[h];
+                        }
                         if (real) store16(up, n, w.n, false, sector && w.n % 16 == 0, du);
                     } else {
                         tmem_ld_wait();
@@ -468,7 +488,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ffn_ker
                 uint64_t *bar = &full[i % n_stages];
                 const uint32_t parity = (i / n_stages) & 1u;
                 if (mbar_try_wait(bar, parity)) continue;
-                const PairFix f = pair_fix(i, n0, n1, odd_bytes<kN>(p, first, step, i));
+                const PairFix f = pair_fix(i, n0, n1, odd_bytes<kN>(p, pair, i));
                 if (f.arrive) mbar_arrive_expect_tx(bar, f.expect);
                 if (f.complete)
                     asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)),
@@ -512,14 +532,48 @@ struct Product {
     uint16_t *gu;
 };
 
-// Items of a list of products at kN columns an item.
-int64_t count_items(const Product *w, int jobs, int kN) {
-    int64_t items = 0;
-    for (int j = 0; j < jobs; ++j) {
-        const int cols = w[j].epilogue == kGate ? kN / 2 : kN;
-        items += (w[j].m + 2 * kRows - 1) / (2 * kRows) * ((w[j].n + cols - 1) / cols);
+int64_t count_items(const Product &w, int kN) {
+    const int cols = w.epilogue == kGate ? kN / 2 : kN;
+    return (w.m + 2 * kRows - 1) / (2 * kRows) * ((w.n + cols - 1) / cols);
+}
+
+// An item's time in stages of 64 k, or its epilogue's, which runs beside the next item's stages:
+// about four, and where it reads g and u and works out their gradients (256 columns 14 us) 44.
+int64_t item_stages(const Product &w, int kN) {
+    const int64_t k = (w.k + kStageK - 1) / kStageK, end = w.epilogue == kGateBack ? kN * 11 / 64 : 4;
+    return k > end ? k : end;
+}
+
+// How a launch's items are shared out: job `first` first, `ahead` rounds (0: none) of the other
+// job's items by the pairs without one of its; the stages of the pair that takes longest.
+struct Plan {
+    int first, ahead;
+    int64_t stages;
+};
+
+// Either one round after another in the order given, or, where a job's items are few and long (the
+// gradients of weights over many tokens, of x over a wide block), those first, one a pair, and
+// about as many of the others meanwhile on the other pairs as they take (8,179 tokens, hidden
+// 2,360, inter 192, forward and backward 135 -> 113 us; 512 tokens, 4,096 by 2,048, 102 -> 78).  What is
+// less than a tenth better by this count is not by the clock (6,000 tokens, 2,048 by 1,024).
+Plan plan(const Product *w, int jobs, int kN, int64_t pairs) {
+    const int64_t n = count_items(w[0], kN), a = item_stages(w[0], kN), rest = n % pairs;
+    Plan best = {0, 0, (n + pairs - 1) / pairs * a};
+    if (jobs == 1) return best;
+    const int64_t more = count_items(w[1], kN), b = item_stages(w[1], kN), over = more % pairs, rounds = n / pairs * a + more / pairs * b;
+    best.stages = rounds + (rest + over > pairs ? a + b : rest > 0 && (over == 0 || a > b) ? a : over > 0 ? b : 0);
+    for (int j = 0; j < 2; ++j) {
+        const int64_t few = count_items(w[j], kN), many = count_items(w[1 - j], kN);
+        const int64_t long_k = item_stages(w[j], kN), short_k = item_stages(w[1 - j], kN), others = pairs - few;
+        if (others <= 0 || long_k < 2 * short_k) continue;
+        for (int64_t r = long_k / short_k; r <= long_k / short_k + 1; ++r) {
+            const int64_t meanwhile = (many < r * others ? (many + others - 1) / others : r) * short_k;
+            const int64_t left = many > r * others ? many - r * others : 0;
+            const int64_t stages = (long_k > meanwhile ? long_k : meanwhile) + (left + pairs - 1) / pairs * short_k;
+            if (stages * 10 < best.stages * 9) best = {j, static_cast<int>(r), stages};
+        }
     }
-    return items;
+    return best;
 }
 
 template <int kN>
@@ -532,6 +586,9 @@ moe_status launch(const Product *w, int jobs, bool chained, int *status, uint64_
     p.wait_limit_ns = limit;
     int64_t items = 0;
     const int pairs_most = num_sms / 2;
+    const Plan how = plan(w, jobs, kN, pairs_most);
+    const Product in_order[kMaxJobs] = {w[how.first], w[jobs - 1 - how.first]};
+    w = in_order;
     for (int j = 0; j < jobs; ++j) {
         Job &o = p.job[j];
         const bool gate = w[j].epilogue == kGate;
@@ -560,7 +617,7 @@ moe_status launch(const Product *w, int jobs, bool chained, int *status, uint64_
         const int64_t tiles = static_cast<int64_t>(o.tiles_m) * o.tiles_n;
         if (items + 2 * tiles > INT32_MAX / 2) return MOE_ERR_CAPACITY;
         const int64_t rest = (items + tiles) % pairs_most;
-        const bool cut = kN == 256 && j == jobs - 1 && items + tiles > pairs_most && 2 * rest <= pairs_most && rest <= tiles;
+        const bool cut = kN == 256 && j == jobs - 1 && how.ahead == 0 && items + tiles > pairs_most && 2 * rest <= pairs_most && rest <= tiles;
         o.full = static_cast<int>(cut ? tiles - rest : tiles);
         items += tiles + (cut ? rest : 0);
         const int64_t n_rows = gate ? 2 * w[j].n : w[j].n;
@@ -575,6 +632,8 @@ moe_status launch(const Product *w, int jobs, bool chained, int *status, uint64_
             return MOE_ERR_CUDA;
     }
     p.items = static_cast<int>(items);
+    const int pairs = static_cast<int>(items < pairs_most ? items : pairs_most);
+    p.schedule = PairSchedule(pairs, how.ahead > 0 ? p.job[1].first : 0, how.ahead);
     // With few rows of A more stages are on their way (64 tokens 23.4 -> 21.3 us).  The MMAs read
     // 128 rows all the same, what lies behind A among them, whose products nobody reads; the
     // last stage's lie within the ring.
@@ -593,7 +652,6 @@ moe_status launch(const Product *w, int jobs, bool chained, int *status, uint64_
             return MOE_ERR_CUDA;
         mask.fetch_or(bit, std::memory_order_release);
     }
-    const int pairs = static_cast<int>(items < pairs_most ? items : pairs_most);
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
@@ -615,7 +673,7 @@ moe_status launch(const Product *w, int jobs, bool chained, int *status, uint64_
 moe_status run(const Product *w, int jobs, bool chained, int *status, uint64_t limit, cudaStream_t stream, int num_sms) {
     bool b_mn = false;
     for (int j = 0; j < jobs; ++j) b_mn = b_mn || w[j].b.mn;
-    const auto cost = [&](int kN, int stage) { return (count_items(w, jobs, kN) + num_sms / 2 - 1) / (num_sms / 2) * stage; };
+    const auto cost = [&](int kN, int stage) { return plan(w, jobs, kN, num_sms / 2).stages * stage; };
     const int64_t c256 = cost(256, 33), c128 = cost(128, 23), c64 = b_mn ? INT64_MAX : cost(64, 17);
     if (c256 <= c128 && c256 <= c64) return launch<256>(w, jobs, chained, status, limit, stream, num_sms);
     if (c128 <= c64) return launch<128>(w, jobs, chained, status, limit, stream, num_sms);
