@@ -101,6 +101,13 @@ def test_backward(B, T, H, I, dw):
         assert torch.equal(one[i], whole)
 
 
+@pytest.mark.parametrize("T,H,I", [(4096, 264, 136), (8179, 600, 192), (700, 4104, 2056), (108, 2760, 1832), (1, 1928, 1808)])
+def test_long_items_beside_short_ones(B, T, H, I):
+    """Launches whose two products have items of very different lengths: few long ones, which go
+    first, and the others beside them, with and without a rest that goes round all pairs."""
+    test_backward(B, T, H, I, torch.bfloat16)
+
+
 def test_gradient_is_the_functions(B):
     """Autograd in 64 bits through the whole block: 2^-8 a rounding, three of them in a row
     (gu, dgu, the result), on independent elements: 2^-7 of the norm covers them."""
