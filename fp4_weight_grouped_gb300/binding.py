@@ -549,6 +549,8 @@ def _take_room(name: str, t: torch.Tensor, n: int, dtype, device: int) -> int:
 
 def _take_rows(name: str, t: torch.Tensor, device: int):
     """Address and row stride, in elements, of a bf16 matrix whose rows are contiguous."""
+    if t.dtype == torch.bfloat16 and t.is_contiguous() and t.get_device() == device and t.dim() == 2:
+        return t.data_ptr(), t.shape[1]
     stride = _rows_of(name, t)
     if t.dtype != torch.bfloat16:
         raise ValueError(f"{name}: dtype {t.dtype}, expected torch.bfloat16")
