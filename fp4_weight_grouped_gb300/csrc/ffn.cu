@@ -12,7 +12,7 @@
 // Bound by the tensor pipe for many tokens (hidden 4,096, inter 2,048: 8,192 tokens forward
 // 212 us, 1,950 TFLOP/s, forward and backward 660 us, 1,870), below some 512 by start-up, about
 // 6 us a launch (64 tokens 20.7 us, of which the MMAs of 256 rows take 8; 250 tokens of hidden
-// 1,032, inter 520, forward and backward 37.8 us in four launches).
+// 1,032, inter 520, forward and backward 36.6 us in four launches).
 //
 //  * CTA pairs (tcgen05.mma cta_group::2): 256 rows by kN columns an item, the rows split
 //    over the pair's tensor memory, either CTA fetching half of A and half of B.  64 k are
