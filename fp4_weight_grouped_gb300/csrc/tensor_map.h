@@ -1,4 +1,4 @@
-// The driver's tensor-map encoder, looked up once.
+// The CUDA driver's tensor-map encoder, looked up once.
 #pragma once
 
 #include <cuda.h>
