@@ -380,6 +380,28 @@ def test_bad_scales_of_experts_with_few_rows(B, rows, fmt, byte):
     assert B.read_status(ws) == B.MOE_ERR_DATA
 
 
+@pytest.mark.parametrize("fmt", [0, 1], ids=["mx", "nv"])
+@pytest.mark.parametrize("E", [8, 40])
+def test_layer_of_tokens_that_name_an_expert_twice(B, E, fmt):
+    """The same expert for both slots of a token, for several tokens, and apart."""
+    g = torch.Generator(device="cuda").manual_seed(E)
+    H, I, k = 512, 288, 3
+    w13, w2 = weights(g, E, 2 * I, H, fmt, 114, 122), weights(g, E, H, I, fmt, 114, 122)
+    ids = torch.tensor([[3, 3, 3], [3, 5, 5], [7, 0, 3], [1, 2, 1]], dtype=torch.int32, device="cuda")
+    x = torch.randn((4, H), generator=g, device="cuda").bfloat16()
+    x[3] = x[0]
+    w = torch.randn((4, k), generator=g, device="cuda")
+    h, y2 = torch.empty((4 * k, I), device="cuda").bfloat16(), torch.empty((4 * k, H), device="cuda")
+    out = B.layer_decode(x, ids, w, w13, w2, fmt, h=h, y2=y2)
+    flat = ids.view(-1).tolist()
+    check(y2, h, w2, flat, 1, fmt)
+    same = B.fp4_matvec_swiglu(x, w13[0], w13[1], fmt, row_expert=ids.view(-1), index_div=k, weight_scale_2=w13[2])
+    assert torch.equal(same, h) and torch.equal(h[0], h[1]) and torch.equal(h[4], h[5]) and torch.equal(y2[0], y2[2])
+    terms = w.double().view(4, k, 1) * y2.double().view(4, k, H)
+    # k products and sums in f32, each off by half a step of what has been summed so far
+    assert bool(((out.double() - terms.sum(1)).abs() <= k * 2.0 ** -24 * terms.abs().sum(1) + 1e-30).all())
+
+
 def test_two_streams_at_once(B):
     g = torch.Generator(device="cuda").manual_seed(13)
     w = weights(g, 16, 512, 1024, 0)
