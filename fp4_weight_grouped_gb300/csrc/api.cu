@@ -144,6 +144,7 @@ moe_status check_matvec_args(const uint16_t *x, int64_t x_stride, int32_t index_
         return MOE_ERR_INVALID_ARG;
     if (static_cast<int64_t>(E) * N > INT32_MAX || static_cast<int64_t>(rows) * columns > INT32_MAX)
         return MOE_ERR_INVALID_ARG;
+    if (columns > MOE_MATVEC_MAX_COLUMNS) return MOE_ERR_INVALID_ARG;      // the last item's columns lie up to 510 past them
     if (format != MOE_FP4_MX && format != MOE_FP4_NV) return MOE_ERR_INVALID_ARG;
     if (!codes || !scales || !workspace || workspace_bytes < kStatusBytes || !aligned(codes, 16) || !aligned(workspace, 16))
         return MOE_ERR_INVALID_ARG;

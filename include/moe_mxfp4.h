@@ -745,7 +745,8 @@ MOE_API moe_status moe_gather_backward(const void *dx_sorted, moe_dtype in_dtype
  *  codes        device uint8 [E, N, K/2], 16-byte aligned; scales [E, N, K/32] or
  *               [E, N, K/16]; weight_scale_2 device f32 [E] (MOE_FP4_NV; ignored for
  *               MOE_FP4_MX).
- *  E, N         1..1024 experts; N >= 1 columns; E * N and rows * N below 2^31.
+ *  E, N         1..1024 experts; 1..MOE_MATVEC_MAX_COLUMNS columns; E * N and rows * N
+ *               below 2^31.
  *  out          device [rows, N], f32 or bf16.
  *  workspace    device, >= 256 bytes, 16-byte aligned (status word).
  * Products are exact and sums are f32, but for elements of x below 2^-28 of their row's
@@ -757,6 +758,7 @@ MOE_API moe_status moe_gather_backward(const void *dx_sorted, moe_dtype in_dtype
  */
 #define MOE_MATVEC_MAX_ROWS 512
 #define MOE_MATVEC_MAX_K 32768
+#define MOE_MATVEC_MAX_COLUMNS (INT32_MAX - 512)
 MOE_API moe_status moe_fp4_matvec(const uint16_t *x, int64_t x_stride, int32_t index_div,
                                   const int32_t *row_expert, int32_t rows, int32_t K,
                                   const uint8_t *codes, const uint8_t *scales,
