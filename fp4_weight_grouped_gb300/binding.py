@@ -547,6 +547,12 @@ def _take_room(name: str, t: torch.Tensor, n: int, dtype, device: int) -> int:
     raise ValueError(f"{name}: on {t.device}, the current device is cuda:{device}")
 
 
+def _fit32(*sizes: int):
+    """Sizes that the library takes in 32 bits: ctypes would hand on a larger one by its lower half."""
+    if max(sizes) > 0x7FFFFFFF:
+        raise ValueError(f"sizes {sizes}: one does not fit 32 bits")
+
+
 def _take_rows(name: str, t: torch.Tensor, device: int):
     """Address and row stride, in elements, of a bf16 matrix whose rows are contiguous."""
     if t.dtype == torch.bfloat16 and t.is_contiguous() and t.get_device() == device and t.dim() == 2:
@@ -863,6 +869,7 @@ def _matvec_operands(x, codes, scales, fmt, row_expert, index_div, weight_scale_
         ids = _take("row_expert", row_expert, (rows,), _I32, device)
         if rows > x_rows * index_div:
             raise ValueError(f"x: {x_rows} rows, {-(-rows // index_div)} are needed")
+    _fit32(rows, index_div, K, E, N)
     return (px, stride, index_div, ids, rows, K, _take("codes", codes, (E, N, K // 2), _U8, device),
             _take("scales", scales, (E, N, K // _fp4_block(fmt)), _U8, device),
             _scale_2("weight_scale_2", weight_scale_2, E, fmt, device), fmt, E), rows, N
@@ -920,6 +927,7 @@ def layer_decode(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor, 
     T, k = topk_ids.shape
     E, two_i, half = c13.shape
     hidden, inter = 2 * half, two_i // 2
+    _fit32(T, k, E, hidden, inter)
     if h is None:
         h = _empty((T * k, inter), torch.bfloat16, x.device, stream)
     if y2 is None:
@@ -948,6 +956,7 @@ def _ffn_operands(x, w13, w2, device):
     px, stride = _take_rows("x", x, device)
     T, hidden = x.shape
     inter = w13.shape[0] // 2
+    _fit32(T, hidden, inter)
     return (px, stride, T, hidden, inter, _take("w13", w13, (2 * inter, hidden), _BF16, device),
             _take("w2", w2, (hidden, inter), _BF16, device)), T, hidden, inter
 
