@@ -386,7 +386,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) ffn_ker
         for (int i = pair; i < p.items; i = p.schedule.next(pair, i)) {
             const Item it = item_of(p, i);
             const Job &w = p.job[it.job];
-            if (!warp_wait_bounded(&acc_full[buf], phase, abort_flag, p.status, accumulator_limit(lim, w.k_stages))) break;
+            if (!warp_wait_bounded(&acc_full[buf], phase, abort_flag, p.status, lim)) break;
             tc_fence_after();
             const uint32_t acc = tmem + buf * kN + (static_cast<uint32_t>(quarter * 32) << 16);
             const int64_t row = it.m0 + static_cast<int64_t>(rank) * kRows + quarter * 32 + lane;

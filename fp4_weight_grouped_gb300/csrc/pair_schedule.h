@@ -1,8 +1,6 @@
-// Which items of a launch a CTA pair takes, one after another, and how long an epilogue waits for
-// one.  Host code as well, so that both can be tested without a GPU.
+// Which items of a launch a CTA pair takes, one after another.  Host code as well, so that the
+// order can be tested without a GPU.
 #pragma once
-
-#include <stdint.h>
 
 #ifdef __CUDACC__
 #define MOE_SCHEDULE_FN __host__ __device__ __forceinline__
@@ -26,11 +24,5 @@ struct PairSchedule {
         return item < long_items || after >= from ? from + pair : after;
     }
 };
-
-// Nanoseconds after which the wait for an item's accumulator gives up: the feeding threads wait for
-// one stage at a time, this for all of them.  2 us a stage; it takes 0.17 to 0.33.
-MOE_SCHEDULE_FN uint64_t accumulator_limit(uint64_t limit_ns, int k_stages) {
-    return limit_ns + 2000ull * static_cast<uint64_t>(k_stages);
-}
 
 }  // namespace moe
