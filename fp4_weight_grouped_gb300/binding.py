@@ -22,6 +22,7 @@ MOE_F32, MOE_BF16 = 0, 1
 MOE_ACT_ROW_MAJOR, MOE_ACT_K8_INTERLEAVED, MOE_ACT_K8_TOKEN_ORDER = 0, 1, 2
 MOE_FP4_MX, MOE_FP4_NV = 0, 1
 MOE_MATVEC_MAX_ROWS, MOE_MATVEC_MAX_K = 512, 32768
+MOE_FFN_MAX_SUM = 1 << 19
 MOE_GRAD_WORKSPACE_BYTES = 32 * 1024
 
 SYMBOLS = (
@@ -987,7 +988,8 @@ def ffn_backward(dout: torch.Tensor, x: torch.Tensor, w13: torch.Tensor, w2: tor
                  workspace: torch.Tensor | None = None, stream=None):
     """Gradients of ffn_forward: dout bf16 [T, hidden], and x, the weights, h and gu of the
     forward -> (dx bf16 [T, hidden], dw13 [2*inter, hidden], dw2 [hidden, inter]; bf16 or f32).
-    An entry of `out` that is None is not computed.  dgu bf16 [T, 2*inter] is scratch."""
+    An entry of `out` that is None is not computed.  Up to MOE_FFN_MAX_SUM tokens where dw13 or dw2
+    is.  dgu bf16 [T, 2*inter] is scratch."""
     device = _current_device()
     args, T, hidden, inter = _ffn_operands(x, w13, w2, device)
     if dgu is None:

@@ -175,6 +175,11 @@ moe_status check_ffn_args(const uint16_t *x, int64_t x_stride, int32_t T, int32_
     return MOE_OK;
 }
 
+// Whether the sums' lengths are ones that the tensor cores' f32 is good for; behind the other checks.
+moe_status check_ffn_sums(int32_t hidden, int32_t inter, int32_t tokens) {
+    return hidden > MOE_FFN_MAX_SUM || inter > MOE_FFN_MAX_SUM / 2 || tokens > MOE_FFN_MAX_SUM ? MOE_ERR_CAPACITY : MOE_OK;
+}
+
 moe_status grad_call(const void *const *grads, const int64_t *sizes, const int32_t *dtypes, int32_t n, float max_norm,
                      float eps, void *const *outs, float *norm, void *workspace, size_t workspace_bytes,
                      void *stream) {
@@ -860,6 +865,7 @@ moe_status moe_ffn_forward(const uint16_t *x, int64_t x_stride, int32_t T, int32
     if (st != MOE_OK) return st;
     if (!known_dtype(out_dtype) || (T > 0 && (!h || !out)) || !aligned(gu, 16) || !aligned(h, 16) || !aligned(out, 16))
         return MOE_ERR_INVALID_ARG;
+    if ((st = check_ffn_sums(hidden, inter, 0)) != MOE_OK) return st;
     int sms = 0;
     if ((st = current_device(&sms)) != MOE_OK) return st;
     const moe::Ffn f = {x, T > 1 ? x_stride : hidden, T, hidden, inter, w13, w2, gu, h, out, out_dtype == MOE_BF16,
@@ -881,6 +887,7 @@ moe_status moe_ffn_backward(const uint16_t *dout, const uint16_t *x, int64_t x_s
     if (!aligned(dout, 16) || !aligned(h, 16) || !aligned(gu, 16) || !aligned(dgu, 16) || !aligned(dx, 16) ||
         !aligned(dw13, 16) || !aligned(dw2, 16))
         return MOE_ERR_INVALID_ARG;
+    if ((st = check_ffn_sums(hidden, inter, dw13 || dw2 ? T : 0)) != MOE_OK) return st;
     int sms = 0;
     if ((st = current_device(&sms)) != MOE_OK) return st;
     const moe::Ffn f = {x, T > 1 ? x_stride : hidden, T, hidden, inter, w13, w2, const_cast<uint16_t *>(gu),

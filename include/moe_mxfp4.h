@@ -812,11 +812,14 @@ MOE_API moe_status moe_layer_decode(const uint16_t *x, const int32_t *topk_ids, 
  *
  *   [g | u] = x w13^T,   h = silu(g) * u,   out = h w2^T
  *
- * with f32 sums; h (and gu) are rounded to bf16 once, out to its type.
+ * with f32 sums; h (and gu) are rounded to bf16 once, out to its type.  The tensor cores
+ * cut off what a sum's f32 does not hold, up to a step in eight products: at most K 2^-27
+ * of the sum of K magnitudes.
  *
  *  x            device bf16 [T, hidden], row t at x + t * x_stride elements; x_stride a
  *               multiple of 8 and at least hidden (any value for T <= 1).
- *  hidden, inter   positive multiples of 8.  2 * inter and T below 2^30.
+ *  hidden, inter   positive multiples of 8; hidden and 2 * inter up to MOE_FFN_MAX_SUM
+ *               (more: MOE_ERR_CAPACITY).  T below 2^30.
  *  w13          device bf16 [2*inter, hidden]: rows [0, inter) gate, [inter, 2*inter) up.
  *  w2           device bf16 [hidden, inter].
  *  gu           device bf16 [T, 2*inter] out ([g | u]), or NULL: what the backward reads.
@@ -826,6 +829,7 @@ MOE_API moe_status moe_layer_decode(const uint16_t *x, const int32_t *topk_ids, 
  * All buffers 16-byte aligned; outputs overlap no input and not each other.  Two launches;
  * results repeat bit for bit.
  */
+#define MOE_FFN_MAX_SUM (1 << 19)
 MOE_API moe_status moe_ffn_forward(const uint16_t *x, int64_t x_stride, int32_t T, int32_t hidden,
                                    int32_t inter, const uint16_t *w13, const uint16_t *w2,
                                    uint16_t *gu, uint16_t *h, void *out, moe_dtype out_dtype,
@@ -845,6 +849,8 @@ MOE_API moe_status moe_ffn_forward(const uint16_t *x, int64_t x_stride, int32_t 
  *               dx and dw13 are both NULL; gu likewise).
  *  dx           device bf16 [T, hidden] out; dw13 [2*inter, hidden] and dw2 [hidden, inter]
  *               out, of dw_dtype.  Each may be NULL (not computed).
+ *  T            up to MOE_FFN_MAX_SUM where dw13 or dw2 is computed, a sum over the tokens
+ *               (more: MOE_ERR_CAPACITY; the gradients of parts of the tokens add up).
  * All buffers 16-byte aligned; outputs overlap no input and not each other.  Up to two
  * launches; results repeat bit for bit.
  */
