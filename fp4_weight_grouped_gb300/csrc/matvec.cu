@@ -24,9 +24,8 @@
 //    has 8 bits, f16 spans 2^-24 .. 2^15: elements down to 2^-28 of the row's largest are
 //    exact, smaller ones are off by at most 2^-39 of it.
 //  * MXFP4: the scale is the same for the 32 k of two MMAs, whose sums it multiplies in
-//    f32.  It is kept 2^-31 low until the end, which keeps the sums of scaled rows (up to
-//    2^15 * 6 * 32 a block, 1,024 blocks) below 2^127 for every scale that the format has;
-//    scales below 2^-118 underflow to 0 for it.
+//    f32, beside as much of the power of two that x was scaled by as f32 holds (row_bias):
+//    every scale of the format counts, and sums have the range of the result.
 //    NVFP4: e2m1 * e4m3 has 6 bits and fits f16, so the scale goes into the weight.
 //    Experts with one or two rows: the columns that are left over keep the scale blocks apart
 //    (multiply_few), for either format.
@@ -135,6 +134,15 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
         asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// a += s f d for the two columns of a lane's row, two numbers an instruction.
+__device__ __forceinline__ void add_scaled(float &a0, float &a1, float s, const float (&f)[2], float d0, float d1) {
+    asm("{\n\t.reg .b64 a, d, s, f;\n\t"
+        "mov.b64 a, {%0, %1};\n\tmov.b64 d, {%5, %6};\n\tmov.b64 s, {%2, %2};\n\tmov.b64 f, {%3, %4};\n\t"
+        "mul.rn.f32x2 d, d, f;\n\tfma.rn.f32x2 a, s, d, a;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "+f"(a0), "+f"(a1)
+        : "f"(s), "f"(f[0]), "f"(f[1]), "f"(d0), "f"(d1));
 }
 
 // Eight e2m1 codes to f16 pairs: (0, 1), (2, 3), (4, 5), (6, 7).
@@ -267,6 +275,21 @@ __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(st
 
 // Power of two that a row of x is scaled by, from the exponent field of its largest magnitude.
 __device__ __forceinline__ int row_exponent(int top) { return max(top - 127 - 14, -126); }
+
+// MXFP4: what a row's sums are multiplied by at the end is 2^(row_exponent - row_bias).  For x of
+// ordinary size (largest magnitude 2^-17 to 2^16) the bias is the exponent: the sums are in the
+// result's own units, and overflow or lose bits where the result does.  For smaller x they stay
+// 2^-31 low, which holds 1,024 blocks' sums of up to 2^15 * 6 * 32 below 2^127 for every scale; for
+// larger x they are lower than the result, but a step of theirs (2^-149) is no more than what the
+// smallest weight, 2^-128, makes of x's own rounding to 2^-38 of its row's largest.
+__device__ __forceinline__ int row_bias(int exponent) { return min(max(exponent, -31), 2); }
+
+// A block's sum (2^-25 to 2^23) times half of 2^row_bias is exact, and twice the scale of any byte,
+// 2^(s + 1 - 127), a normal number: the only rounding is the sum's.
+__device__ __forceinline__ float bias_factor(int top) {
+    return power_of_two(min(max(top - 127 - 14, -31), 2) - 1);             // row_bias(row_exponent(top)) - 1
+}
+__device__ __forceinline__ float twice_e8m0(uint32_t s) { return __uint_as_float(s * 0x800000u + 0x800000u); }
 
 // Eight elements of a row of x; zeros past its end.  Not through the read-only path: x may come
 // from a launch that ended after this one began.
@@ -404,10 +427,11 @@ __device__ __forceinline__ void load_scales(const uint8_t *const (&rows)[2][2], 
 // in the 128-byte swizzle (piece ^ row % 8): `at` is, with the swizzle in it, the lane's
 // piece t4 of its first row, or for MXFP4 (read by words of eight rows) word t4 of piece 0.
 // step: bytes from row g of an MMA to row g + 8, next: to the second MMA's.  x: this lane's
-// share of the chunk's rows, zeros in lanes without one.
+// share of the chunk's rows, zeros in lanes without one.  factor: MXFP4: bias_factor of the rows in
+// the lane's two columns.
 template <int F>
 __device__ __forceinline__ void multiply(uint32_t at, int step, int next, uint32_t xa, bool has_x, const Scales &sw,
-                                         uint4 (&x)[4], float (&acc)[2][4], Scales &bad) {
+                                         const float (&factor)[2], uint4 (&x)[4], float (&acc)[2][4], Scales &bad) {
     if constexpr (F == kBf16) {
         lds128_if(x[0], xa, has_x);
 #pragma unroll
@@ -468,12 +492,9 @@ __device__ __forceinline__ void multiply(uint32_t at, int step, int next, uint32
                 float d[4] = {0.f, 0.f, 0.f, 0.f};
                 mma16816<true>(d, a[0], c[0], a[1], c[1], x[b].x, x[b].y);
                 mma16816<true>(d, a[2], c[2], a[3], c[3], x[b].z, x[b].w);
-                const float s0 = __uint_as_float((sw[s][0] >> (8 * b) & 0xFFu) << 23) * 0x1p-31f;
-                const float s1 = __uint_as_float((sw[s][1] >> (8 * b) & 0xFFu) << 23) * 0x1p-31f;
-                acc[s][0] = fmaf(s0, d[0], acc[s][0]);
-                acc[s][1] = fmaf(s0, d[1], acc[s][1]);
-                acc[s][2] = fmaf(s1, d[2], acc[s][2]);
-                acc[s][3] = fmaf(s1, d[3], acc[s][3]);
+                const float s0 = twice_e8m0(sw[s][0] >> (8 * b) & 0xFFu), s1 = twice_e8m0(sw[s][1] >> (8 * b) & 0xFFu);
+                add_scaled(acc[s][0], acc[s][1], s0, factor, d[0], d[1]);
+                add_scaled(acc[s][2], acc[s][3], s1, factor, d[2], d[3]);
             }
     }
 }
@@ -483,11 +504,13 @@ __device__ __forceinline__ void multiply(uint32_t at, int step, int next, uint32
 // blocks apart, and a block's scale multiplies once behind them (half of the instructions of the
 // form above: one token's w13 20.0 -> 18.1 us, w2 13.5 -> 11.6).  Column j: row j % 2, block j / 2
 // of four (MXFP4: a half's; NVFP4: those of two words after those of the other two), or for one
-// row of NVFP4 (kRows 1) block j of eight.  has: whether this lane's words 0 and 1, and 2 and 3,
-// belong to its column; x stays zero where they do not.  What acc holds is a quarter of a sum.
+// row of NVFP4 (kRows 1) block j of eight; of one row of MXFP4 every second column is empty.  has:
+// whether this lane's words 0 and 1, and 2 and 3, belong to its column; x stays zero where they do
+// not.  factor: as above.  What acc holds is a quarter of a sum.
 template <int F, int kRows>
 __device__ __forceinline__ void multiply_few(uint32_t at, int step, int next, uint32_t xa, const bool (&has)[2],
-                                             const Scales &sw, uint4 (&x)[4], float (&acc)[2][4], Scales &bad) {
+                                             const Scales &sw, const float (&factor)[2], uint4 (&x)[4],
+                                             float (&acc)[2][4], Scales &bad) {
     uint4 ra[2], rc[2];
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
@@ -506,7 +529,7 @@ __device__ __forceinline__ void multiply_few(uint32_t at, int step, int next, ui
         for (int r = 0; r < 2; ++r) {
             if constexpr (F == kMx) {
                 bad[s][r] |= (sw[s][r] + 3u) & 0x100u;                                                   // 253 and more
-                scale[s][r][0] = __uint_as_float(sw[s][r] << 23) * 0x1p-31f;
+                scale[s][r][0] = twice_e8m0(sw[s][r]);
             } else {
                 e4m3_floats(sw[s][r], scale[s][r][0], scale[s][r][1]);
             }
@@ -528,10 +551,19 @@ __device__ __forceinline__ void multiply_few(uint32_t at, int step, int next, ui
                 mma16816<true>(d[s], a[2], c[2], a[3], c[3], x[j].z, x[j].w);
             }
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
+        for (int s = 0; s < 2; ++s) {
+            if constexpr (F == kMx && kRows == 1) {        // the second column of a lane has no row
+                acc[s][0] = fmaf(scale[s][0][0], d[s][0] * factor[0], acc[s][0]);
+                acc[s][2] = fmaf(scale[s][1][0], d[s][2] * factor[0], acc[s][2]);
+            } else if constexpr (F == kMx) {
+                add_scaled(acc[s][0], acc[s][1], scale[s][0][0], factor, d[s][0], d[s][1]);
+                add_scaled(acc[s][2], acc[s][3], scale[s][1][0], factor, d[s][2], d[s][3]);
+            } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)       // either column the same block and its own row, or the same row
-                acc[s][kRows == 2 ? i : i & 2] = fmaf(scale[s][i >> 1][kRows == 2 ? b >> 1 : i & 1], d[s][i], acc[s][kRows == 2 ? i : i & 2]);
+                for (int i = 0; i < 4; ++i)   // either column the same block and its own row, or the same row
+                    acc[s][kRows == 2 ? i : i & 2] = fmaf(scale[s][i >> 1][kRows == 2 ? b >> 1 : i & 1], d[s][i], acc[s][kRows == 2 ? i : i & 2]);
+            }
+        }
     }
 }
 
@@ -636,6 +668,7 @@ __global__ void __launch_bounds__(Shape<kFew>::kThreads, Shape<kFew>::kCtas)
     int n_tok = 0, start = 0, turn = 0, chunk = chunk0, grp = grp0;
     bool fresh = true, ok = true, few = false;
     uint4 x[4];
+    float factor[2] = {};
     for (int left = count; left > 0; --left) {
         if (fresh) {                              // everyone is past the last x
             fresh = false;
@@ -649,6 +682,10 @@ __global__ void __launch_bounds__(Shape<kFew>::kThreads, Shape<kFew>::kCtas)
                   (chunk + 1 == *ch.count || ch.expert[chunk + 1] != ch.expert[chunk]);
             stage_x<F, S>(p, ch.order + start, n_tok, xs, pitch, tops + turn, ahead && left == count, few, xr);
             if (tid < kTok) tops[(turn ^ kTok) + tid] = 0;
+            if constexpr (F == kMx) {             // of the rows in this lane's columns
+#pragma unroll
+                for (int i = 0; i < 2; ++i) factor[i] = bias_factor(tops[turn + (few ? i : (2 * t4 + i) % kTok)]);
+            }
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[i] = make_uint4(0, 0, 0, 0);
         }
@@ -703,9 +740,9 @@ __global__ void __launch_bounds__(Shape<kFew>::kThreads, Shape<kFew>::kCtas)
                     if constexpr (F != kBf16) scales_of(Int<kScales>{}, unit, h * (C::kScaleBytes / 2) + (kScales < 4 ? kScales * t4 : 0), sw);
                     const uint32_t at = (rows + slot * (kTileRows * 128)) ^ (64 * h), x_at = xa + h * (kUnitX / 2);
                     if constexpr (few_rows.value > 0)
-                        multiply_few<F, few_rows.value>(at, kStep * 128, kNext * 128, x_at, has, sw, x, acc, bad);
+                        multiply_few<F, few_rows.value>(at, kStep * 128, kNext * 128, x_at, has, sw, factor, x, acc, bad);
                     else
-                        multiply<F>(at, kStep * 128, kNext * 128, x_at, has[0], sw, x, acc, bad);
+                        multiply<F>(at, kStep * 128, kNext * 128, x_at, has[0], sw, factor, x, acc, bad);
                 }
                 xa += kUnitX * kw;
                 __syncwarp();                     // the slot is read by all
@@ -715,7 +752,7 @@ __global__ void __launch_bounds__(Shape<kFew>::kThreads, Shape<kFew>::kCtas)
             }
         };
         if constexpr (kFew) {
-            if (F == kNv && few && n_tok == 1) stages(Int<1>{});
+            if (few && n_tok == 1) stages(Int<1>{});
             else if (few) stages(Int<2>{});
             else stages(Int<0>{});
         } else {
@@ -761,7 +798,7 @@ __global__ void __launch_bounds__(Shape<kFew>::kThreads, Shape<kFew>::kCtas)
                 if (kSwiglu) u += from[j * sum_floats + 16];
             }
             if constexpr (F != kBf16) {
-                const int e = row_exponent(tops[turn + t]) + (F == kMx ? 31 : 0);
+                const int exponent = row_exponent(tops[turn + t]), e = exponent - (F == kMx ? row_bias(exponent) : 0);
                 const float s2 = F == kNv ? __ldg(p.ws2 + ch.expert[chunk]) : 1.0f;
                 // 2^e by two factors, each of them a normal number.
                 const float f = power_of_two(e / 2), f2 = power_of_two(e - e / 2);

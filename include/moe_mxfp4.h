@@ -750,11 +750,11 @@ MOE_API moe_status moe_gather_backward(const void *dx_sorted, moe_dtype in_dtype
  *  out          device [rows, N], f32 or bf16.
  *  workspace    device, >= 256 bytes, 16-byte aligned (status word).
  * Products are exact and sums are f32, but for elements of x below 2^-28 of their row's
- * largest: they are rounded to 2^-38 of it.  MOE_FP4_MX blocks whose scale is below
- * 2^-118 count as zero.  A scale byte that the format does not allow (E8M0 above 252,
- * an E4M3 NaN) sets MOE_ERR_DATA and makes its column NaN.  Results repeat bit for bit, and
- * equal rows of a call that name the same expert have equal results; between calls of
- * other row counts sums may be formed in another order.  The output overlaps no input.
+ * largest: they are rounded to 2^-38 of it.  A scale byte that the format does not allow
+ * (E8M0 above 252, an E4M3 NaN) sets MOE_ERR_DATA and makes its column NaN.  Results
+ * repeat bit for bit, and equal rows of a call that name the same expert have equal results;
+ * between calls of other row counts sums may be formed in another order.  The output
+ * overlaps no input.
  */
 #define MOE_MATVEC_MAX_ROWS 512
 #define MOE_MATVEC_MAX_K 32768
