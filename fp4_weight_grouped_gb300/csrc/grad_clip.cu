@@ -11,8 +11,8 @@
 //    elements that it loads together in f32, and those sums in an f32 pair (the sum and what
 //    its roundings left out, by Knuth's two-sum); the block joins its pairs and only the
 //    block's sum is f64.  A group of squares outside 2^-90 .. 2^80, where f32 would lose some
-//    of them or the sums overflow, is formed again in f64 and travels beside the pairs: the
-//    norm is right over the whole range of the types.
+//    of them or the sums overflow, is formed again from scaled elements and travels beside the
+//    pairs, in f64: the norm is right over the whole range of the types.
 //  * Bound by HBM: one read for the norm and a read and a write for the clipping.  The
 //    second kernel goes through the chunks backwards, so what the first read last (the L2's
 //    share) is not fetched again.  1.3 GB in 120 tensors: 619 us, 6.3 TB/s of the three passes
@@ -94,17 +94,54 @@ __device__ __forceinline__ float squares(const float (&v)[V]) {
     return a + b;
 }
 
-// The squares of n vectors, `stride` vectors apart, in f64.
+// The squares of n vectors, kThreads vectors apart, whatever their magnitude: of the elements
+// times a power of two that brings the largest to 1 (or 4), in f32 as above, and back in the
+// exponent of a double, by integers.
 template <typename T>
-__device__ __noinline__ double squares64(const T *p, int n, int64_t stride) {
+__device__ __forceinline__ double scaled_squares(const T *p, int n) {
     constexpr int V = 16 / sizeof(T);
-    double d = 0.0;
-    for (int i = 0; i < n; ++i)
-        for (int j = 0; j < V; ++j) {
-            const double x = as_f32(p[i * stride * V + j]);
-            d = fma(x, x, d);
+    uint32_t most = 0;
+    for (int i = 0; i < n; ++i) {
+        float x[V];
+        load_row<V>(p + i * kThreads * V, x);
+#pragma unroll
+        for (int j = 0; j < V; ++j) most = max(most, __float_as_uint(x[j]) & 0x7FFFFFFFu);
+    }
+    if (most == 0) return 0.0;
+    if (most >= 0x7F800000u) return __uint_as_float(most);           // an infinity or a NaN
+    const int e = min(max(static_cast<int>(most >> 23), 1), 253);
+    const float f = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+    float s = 0.f;
+    for (int i = 0; i < n; ++i) {
+        float x[V];
+        load_row<V>(p + i * kThreads * V, x);
+#pragma unroll
+        for (int j = 0; j < V; ++j) x[j] *= f;
+        s += squares(x);
+    }
+    // s is in 2^-46 .. 2^9 (the largest element may be subnormal): a normal number
+    const uint64_t b = __float_as_uint(s);
+    return __longlong_as_double(static_cast<int64_t>((b << 29) + (static_cast<uint64_t>(1023 - 127 + 2 * (e - 127)) << 52)));
+}
+
+// A thread's groups of a chunk that f32 does not hold, a bit each.  Read again behind the chunk
+// rather than kept in registers or worked out on the spot, either of which spills in the loop that
+// every gradient goes through (1 GB in bf16 150 -> 197 us, in f32 150 -> 170).  Zeros and small
+// elements are ordinary in gradients; element by element in f64 they took 13 times as long as
+// others in bf16 and 7 times in f32.
+template <typename T>
+__device__ __noinline__ double far_squares(const T *q, int vecs, uint32_t groups) {
+    constexpr int V = 16 / sizeof(T);
+    double far = 0.0;
+    for (int v = threadIdx.x; groups; groups >>= 1) {
+        const int count = v + (kVecs - 1) * kThreads < vecs ? kVecs : 1;
+        if (groups & 1) {
+            const double d = scaled_squares(q + static_cast<int64_t>(v) * V, count);
+            if (__double_as_longlong(d) != 0) far += d;
         }
-    return d;
+        v += count * kThreads;
+    }
+    return far;
 }
 
 struct Sums {
@@ -124,9 +161,11 @@ __device__ __forceinline__ void chunk_squares(const T *p, int n, Sums &sums) {
     const int tid = threadIdx.x;
     const int head = head_of(p, n), vecs = (n - head) / V, tail = head + vecs * V;
     const T *q = p + head;
-    const auto take = [&](float s, int v, int count) {
+    uint32_t far = 0, bit = 1;                // at most kMaxChunk / (4 kThreads kVecs) + kVecs - 1 groups
+    const auto take = [&](float s) {
         if (sum_holds(s)) add(sums.near, s);
-        else sums.far += squares64(q + static_cast<int64_t>(v) * V, count, kThreads);
+        else far |= bit;
+        bit <<= 1;
     };
     int v = tid;
     for (; v + (kVecs - 1) * kThreads < vecs; v += kVecs * kThreads) {
@@ -136,13 +175,14 @@ __device__ __forceinline__ void chunk_squares(const T *p, int n, Sums &sums) {
         float s = 0.f;
 #pragma unroll
         for (int i = 0; i < kVecs; i += 2) s += squares(x[i]) + squares(x[i + 1]);
-        take(s, v, kVecs);
+        take(s);
     }
     for (; v < vecs; v += kThreads) {
         float x[V];
         load_row<V>(q + static_cast<int64_t>(v) * V, x);
-        take(squares(x), v, 1);
+        take(squares(x));
     }
+    if (far) sums.far += far_squares(q, vecs, far);
     // Up to V - 1 elements before and behind the vectors.
     const int at = tid < head ? tid : tail + tid - head;
     if (at < n) {
