@@ -602,7 +602,9 @@ __global__ void __launch_bounds__(Shape<kFew>::kThreads, Shape<kFew>::kCtas)
     const int tiles = (p.N + kTileCols - 1) / kTileCols;
     const int groups = (tiles + group - 1) / group;          // items a chunk
     // The CTA's share of the items, one after another.  (rows * N < 2^31, so counts fit.)
-    const int total = *ch.count * groups, grid = gridDim.x, blk = blockIdx.x;
+    const int chunks = *ch.count;
+    const bool unnamed = ch.first[chunks] < p.rows;
+    const int total = chunks * groups, grid = gridDim.x, blk = blockIdx.x;
     const int first = total / grid * blk + min(blk, total % grid);
     const int count = total / grid + (blk < total % grid);
     const int chunk0 = count > 0 ? first / groups : 0, grp0 = count > 0 ? first % groups : 0;
@@ -645,11 +647,15 @@ __global__ void __launch_bounds__(Shape<kFew>::kThreads, Shape<kFew>::kCtas)
     for (int i = 0; i < depth; ++i) fetch_next();
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (blockIdx.x == 0 && p.row_expert) {        // rows without an expert: zeros
-        for (int s = warp; s < p.rows; s += kWarps) {
+    if (unnamed) {                                // rows without an expert: zeros, by all CTAs
+        constexpr int kPiece = 1024;              // columns a warp
+        if (blk == 0 && tid == 0) set_status(p.status, MOE_ERR_DATA);
+        const int pieces = (p.N - 1) / kPiece + 1;
+        for (int i = blk * kWarps + warp; i < p.rows * pieces; i += grid * kWarps) {
+            const int s = i / pieces, from = i % pieces * kPiece;
             if (ch.scratch[s] != INT32_MAX) continue;
-            if (lane == 0) set_status(p.status, MOE_ERR_DATA);
-            for (int n = lane; n < p.N; n += 32) {
+            const int end = p.N - from < kPiece ? p.N : from + kPiece;
+            for (int n = from + lane; n < end; n += 32) {
                 if (p.out_bf16) static_cast<uint16_t *>(p.out)[static_cast<int64_t>(s) * p.N + n] = 0;
                 else static_cast<float *>(p.out)[static_cast<int64_t>(s) * p.N + n] = 0.0f;
             }
