@@ -1024,7 +1024,7 @@ def _grad_arrays(grads, name="grads"):
     """Pointers, sizes and types of a list of gradients, as arrays that the library reads.  By
     maps over the list: a model's few hundred tensors cost the host more than a small model's
     clipping takes."""
-    grads, device = list(grads), _current_device()
+    device = _current_device()
     dtypes = list(map(_GRAD_DTYPES.get, map(_DTYPE, grads)))
     if None in dtypes or not all(map(torch.Tensor.is_contiguous, grads)) or {t.get_device() for t in grads} - {device}:
         bad = next(i for i, t in enumerate(grads)
@@ -1049,6 +1049,7 @@ def _grad_call(grads, norm, workspace, stream):
 
 def grad_norm(grads, norm: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
     """Global norm f32 [1] of a list of contiguous gradients (f32 or bf16 each)."""
+    grads = list(grads)
     ptrs, sizes, dtypes = _grad_arrays(grads)
     norm, pn, ws, n, made = _grad_call(grads, norm, workspace, stream)
     rc = load().moe_grad_norm(_address(ptrs), _address(sizes), _address(dtypes), len(ptrs), pn, ws, n, _stream(stream))
@@ -1061,10 +1062,11 @@ def clip_grads(grads, max_norm: float, eps: float = 1e-6, out=None, norm: torch.
     """Scale a list of gradients (f32 or bf16 each, contiguous) by min(1, max_norm / (norm +
     eps)), in place or into the tensors of `out`; returns their global norm, f32 [1].  A norm
     that is not finite scales nothing.  Workspace: MOE_GRAD_WORKSPACE_BYTES."""
+    grads = list(grads)
     ptrs, sizes, dtypes = _grad_arrays(grads)
     outs = None
     if out is not None:
-        outs, osizes, odtypes = _grad_arrays(out, "out")
+        outs, osizes, odtypes = _grad_arrays(list(out), "out")
         if osizes != sizes or odtypes != dtypes:
             raise ValueError("out: not of the gradients' sizes and types")
     norm, pn, ws, n, made = _grad_call(grads, norm, workspace, stream)
