@@ -1048,7 +1048,7 @@ def _grad_call(grads, norm, workspace, stream):
 
 
 def grad_norm(grads, norm: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
-    """Global norm f32 [1] of a list of contiguous gradients (f32 or bf16 each)."""
+    """Global norm f32 [1] of contiguous gradients (f32 or bf16 each; any iterable of tensors)."""
     grads = list(grads)
     ptrs, sizes, dtypes = _grad_arrays(grads)
     norm, pn, ws, n, made = _grad_call(grads, norm, workspace, stream)
@@ -1059,9 +1059,10 @@ def grad_norm(grads, norm: torch.Tensor | None = None, workspace: torch.Tensor |
 
 def clip_grads(grads, max_norm: float, eps: float = 1e-6, out=None, norm: torch.Tensor | None = None,
                workspace: torch.Tensor | None = None, stream=None):
-    """Scale a list of gradients (f32 or bf16 each, contiguous) by min(1, max_norm / (norm +
-    eps)), in place or into the tensors of `out`; returns their global norm, f32 [1].  A norm
-    that is not finite scales nothing.  Workspace: MOE_GRAD_WORKSPACE_BYTES."""
+    """Scale gradients (any iterable of contiguous f32 or bf16 tensors) by min(1, max_norm / (norm +
+    eps)), in place or into the tensors of `out`; returns their global norm, f32 [1].  Gradients
+    that hold an infinity or a NaN are not scaled (the norm of finite ones past f32's range is
+    returned as infinity, and clips).  Workspace: MOE_GRAD_WORKSPACE_BYTES."""
     grads = list(grads)
     ptrs, sizes, dtypes = _grad_arrays(grads)
     outs = None

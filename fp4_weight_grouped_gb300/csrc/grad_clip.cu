@@ -306,7 +306,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) scale_kernel(const __g
         if (threadIdx.x == 0) {       // one thread: a root and a quotient in f64 by all took 20 us
             const double total = sqrt(sum);
             if (blockIdx.x == 0 && norm) *norm = static_cast<float>(total);
-            // A norm that is not finite clips nothing: the gradients are left (or copied) as they are.
+            // An infinite or NaN sum clips nothing: the gradients are left (or copied) as they are.  A sum of
+            // finite ones is finite in f64, past f32's range too.
             const bool clips = total < __longlong_as_double(0x7FF0000000000000ll) && max_norm < total + eps;
             // A scale near or below f32's smallest normal number (a norm past 2^100) would lose
             // bits: part of it is applied ahead, as a power of two.

@@ -873,7 +873,7 @@ MOE_API moe_status moe_ffn_backward(const uint16_t *dout, const uint16_t *x, int
  *               at the same time need one each.
  * Sums are pairs of f32 (a sum and what its roundings left out) within a block and f64
  * across blocks; the norm is right over the whole range of the types.  Results repeat bit
- * for bit.
+ * for bit.  `norm` and `workspace` overlap no tensor and not each other (not checked).
  */
 #define MOE_GRAD_WORKSPACE_BYTES (32u * 1024u)
 MOE_API moe_status moe_grad_norm(const void *const *grads, const int64_t *sizes,
@@ -885,8 +885,10 @@ MOE_API moe_status moe_grad_norm(const void *const *grads, const int64_t *sizes,
  *
  *   out = g * min(1, max_norm / (norm + eps)),  norm as moe_grad_norm has it
  *
- * each product formed in f32 and rounded to the tensor's type.  Where the norm is an
- * infinity or a NaN nothing is scaled: out = g, and `norm` tells the caller.
+ * each product formed in f32 and rounded to the tensor's type.  Where a gradient holds an
+ * infinity or a NaN nothing is scaled: out = g, and `norm`, infinite or NaN, tells the
+ * caller.  A norm of finite gradients past f32's range clips like any other (it is held in
+ * f64), though `norm` is an infinity then too.
  *
  *  outs         host array of n device pointers, each its gradient itself (in place) or
  *               memory of the same size and type that overlaps no gradient; NULL: in
