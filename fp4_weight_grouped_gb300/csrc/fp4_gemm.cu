@@ -49,13 +49,13 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
-#include <cudaTypedefs.h>
 #include <stdint.h>
 
 #include "device_common.cuh"
 #include "fp4_common.cuh"
 #include "launch.h"
 #include "ring_drain.h"
+#include "tensor_map.h"
 #include "vec_io.cuh"
 
 namespace moe {
@@ -1759,23 +1759,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     cluster_sync();
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-        void *ptr = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) !=
-                cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            return static_cast<PFN_cuTensorMapEncodeTiled_v12000>(nullptr);
-        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-    }();
-    return fn;
-}
-
 // Codes [rows, K / 2] in boxes of 128 bytes (256 k) by `box_rows` rows; bytes
 // past a row's end and rows past the last read as zero codes.
 bool encode_codes(CUtensorMap *map, const void *base, int64_t rows, int K, uint32_t box_rows) {
-    PFN_cuTensorMapEncodeTiled_v12000 encode = encode_fn();
+    PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encode();
     if (!encode) return false;
     cuuint64_t dims[2] = {static_cast<cuuint64_t>(K / 2), static_cast<cuuint64_t>(rows)};
     cuuint64_t strides[1] = {static_cast<cuuint64_t>(K / 2)};
@@ -1790,7 +1777,7 @@ bool encode_codes(CUtensorMap *map, const void *base, int64_t rows, int K, uint3
 // rows; bytes past a row's end and rows past the last of an expert (half) read as zeros.
 bool encode_scales(CUtensorMap *map, const void *base, int scale_row, int64_t rows, int64_t outer, uint32_t box_rows,
                    bool nv) {
-    PFN_cuTensorMapEncodeTiled_v12000 encode = encode_fn();
+    PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encode();
     if (!encode) return false;
     const cuuint64_t pitch = static_cast<cuuint64_t>(scale_row);
     cuuint64_t dims[3] = {pitch, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(outer)};
@@ -1804,7 +1791,7 @@ bool encode_scales(CUtensorMap *map, const void *base, int scale_row, int64_t ro
 
 // Outputs [rows, N] in boxes of 128 bytes by 32 rows.
 bool encode_out(CUtensorMap *map, void *base, int64_t rows, int N, bool bf16) {
-    PFN_cuTensorMapEncodeTiled_v12000 encode = encode_fn();
+    PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encode();
     if (!encode) return false;
     const uint32_t size = bf16 ? 2 : 4;
     cuuint64_t dims[2] = {static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(rows)};

@@ -51,12 +51,12 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
-#include <cudaTypedefs.h>
 #include <stdint.h>
 
 #include "device_common.cuh"
 #include "launch.h"
 #include "mxfp4_decode.cuh"
+#include "tensor_map.h"
 
 namespace moe {
 namespace gemm {
@@ -1460,21 +1460,6 @@ static int pair_clusters(int num_sms, int smem_bytes) {
     return n > 0 ? n : 0;
 }
 
-// The driver's tensor-map encoder, looked up once per process (a function-local
-// static is initialised once even when host threads race on the first call).
-static PFN_cuTensorMapEncodeTiled_v12000 get_encode_fn() {
-    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-        void *ptr = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000,
-                                             cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            return static_cast<PFN_cuTensorMapEncodeTiled_v12000>(nullptr);
-        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-    }();
-    return fn;
-}
-
 // Both weight formats.  kNv = false: `scales` are per-32 E8M0 bytes [E, N, K/32].
 // kNv = true: `scales` are per-16 E4M3 bytes [E, N, K/16] and ws2 the per-expert
 // f32 weight_scale_2.
@@ -1496,7 +1481,7 @@ static moe_status launch_gemm(const uint16_t *act, int rows, int K, const uint8_
     using namespace gemm;
     if (rows == 0) return MOE_OK;
     const int I = N / 2;   // fused SwiGLU: gate rows [0, I), up rows [I, 2I); I % 16 == 0
-    PFN_cuTensorMapEncodeTiled_v12000 encode = get_encode_fn();
+    PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encode();
     if (!encode) return MOE_ERR_CUDA;
 
     CUtensorMap tm_codes, tm_act, tm_act3, tm_scales, tm_act64;

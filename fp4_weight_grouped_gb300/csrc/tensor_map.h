@@ -1,4 +1,5 @@
-// The CUDA driver's tensor-map encoder, looked up once.
+// The CUDA driver's tensor-map encoder, looked up once (a function-local static is initialised
+// once even when host threads race on the first call).
 #pragma once
 
 #include <cuda.h>
