@@ -10,7 +10,8 @@
 // transposed in memory.
 //
 // Bound by the tensor pipe for many tokens (hidden 4,096, inter 2,048: 8,192 tokens forward
-// 212 us, 1,950 TFLOP/s, forward and backward 660 us, 1,870), below some 512 by start-up, about
+// 212 us, 1,950 TFLOP/s, forward and backward 660, 1,870, in a short burst; one call after another
+// the power cap makes the latter 770, 1,600), below some 512 by start-up, about
 // 6 us a launch (64 tokens 20.7 us, of which the MMAs of 256 rows take 8; 250 tokens of hidden
 // 1,032, inter 520, forward and backward 36.6 us in four launches).
 //
@@ -22,9 +23,14 @@
 //  * SwiGLU: the even CTA fetches gate rows of W13 and the odd CTA the matching up rows, so
 //    a thread finds g and u of one output in two column ranges of its own lane.
 //  * The gradient's elementwise part is the epilogue of dh: dh is never stored.
-//  * Sums are f32; h, g, u, dg and du are rounded to bf16 once, where they are stored for
-//    the next product, whose operands are bf16 (f32 ones would be tf32, at half of the rate and
-//    twice the bytes).  dW13 and dx carry the roundings of g and u, of dg and du and their own.
+//  * Sums are f32, as the tensor core has it: what does not fit is cut off, up to a step in eight
+//    products (2^14 tokens of one sign: 8e-5 of the sum; 2^19, the most that is taken: 0.0034).
+//  * h, dg and du are rounded to bf16 once, where they are stored for the next product, whose
+//    operands are bf16 (f32 ones would be tf32, at half of the rate and twice the bytes).  g and u
+//    are read back by the gradient's elementwise part alone and could be f32; bf16 halves the memory
+//    that a training step holds for them between forward and backward, and saves their bytes (134 MB
+//    for 8,192 tokens of inter 2,048: some 20 us).  dW13 and dx carry g and u's rounding, dg and du's
+//    and their own: 0.0030 of the norm, against 0.0017 for their own alone.
 //  * Persistent pairs over a list of jobs; a job is one product.
 //  * Every wait is bounded (see wait_bounded and pair_drain.h).
 #include <atomic>

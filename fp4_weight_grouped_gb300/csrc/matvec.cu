@@ -8,7 +8,7 @@
 // Bound by HBM where there are weights enough: 6.6 TB/s for every further token's six experts
 // in MXFP4 (hidden 4,096, inter 2,048, w13; 6.3 for w2), on top of 7 to 8 us that a launch
 // takes before and behind them (5.5 for a tiny product).  One token: w13 16 us, w2 11; eight
-// in NVFP4: 75 us (6.0 TB/s) and 43 (5.3).
+// in NVFP4: 75 us (6.0 TB/s) and 43 (5.3), in MXFP4 73 and 41.
 //
 //  * Rows of the same expert are taken together, up to 8 or 4 at a time (a chunk), so a
 //    weight is read once for them.  Every CTA works the chunks out from the ids itself.
@@ -23,6 +23,9 @@
 //    scaled by a power of two that brings its largest magnitude to [2^14, 2^15).  A bf16
 //    has 8 bits, f16 spans 2^-24 .. 2^15: elements down to 2^-28 of the row's largest are
 //    exact, smaller ones are off by at most 2^-39 of it.
+//  * h is rounded to bf16 between a decode step's products, as in the layer that sorts its rows,
+//    so that either gives the same step: the output's error is 0.0023 of its norm, with h in f32
+//    it would be the output's own rounding, 0.0016.
 //  * MXFP4: the scale is the same for the 32 k of two MMAs, whose sums it multiplies in
 //    f32, beside as much of the power of two that x was scaled by as f32 holds (row_bias):
 //    every scale of the format counts, and sums have the range of the result.
