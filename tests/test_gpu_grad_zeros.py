@@ -47,7 +47,7 @@ def test_zeros_are_as_fast_as_other_gradients(B, dtype):
     few = x.clone()
     few.view(-1, 64)[:, :32] = 0
     for y in (torch.zeros_like(x), some, few, x * 2.0 ** -60):
-        assert micros(lambda: B.grad_norm([y], norm=norm, workspace=ws)) < 2 * ordinary
+        assert micros(lambda: B.grad_norm([y], norm=norm, workspace=ws)) < 3 * ordinary
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
